@@ -1,7 +1,7 @@
 """GB300 ring attention -- forward, backward and the context-parallel variants:
 the Python binding of libra.so (include/ra.h).
 
-The functions keep the C names (``ra_plan``, ``ra_plan_tile_counts``, ``ra_fwd``,
+The functions keep the C names (``ra_plan``, ``ra_plan_window``, ``ra_plan_tile_counts``, ``ra_fwd``,
 ``ra_fwd_static``, ``ra_fwd_static_status``, ``ra_merge_partials``, ``ra_layout_perm``, ``ra_layout_index``,
 ``ra_fwd_step``, ``ra_ring_rotate``, ``ra_ring_fwd``, ``ra_bwd``,
 ``ra_bwd_scratch_size``, ``ra_allgather_kv``, ``ra_fwd_gathered``,
@@ -28,7 +28,7 @@ import numpy as np
 
 __all__ = [
     "RaError", "Plan", "LAYOUTS",
-    "ra_plan", "ra_plan_destroy", "ra_plan_tile_counts", "ra_fwd", "ra_merge_partials",
+    "ra_plan", "ra_plan_window", "ra_plan_destroy", "ra_plan_tile_counts", "ra_fwd", "ra_merge_partials",
     "ra_layout_perm", "ra_layout_index", "ra_sync_status", "ra_last_error", "ra_fwd_static",
     "ra_fwd_static_status", "ra_fwd_step", "ra_ring_rotate", "ra_ring_fwd", "ra_bwd", "ra_bwd_scratch_size",
     "ra_allgather_kv", "ra_fwd_gathered", "ra_ulysses_a2a", "ra_wait_selftest",
@@ -39,7 +39,7 @@ LAYOUTS = {"contiguous": 0, "striped": 1, "zigzag": 2}
 DTYPES = {"f32": 0, "bf16": 1}
 _STATUS = {0: "RA_OK", 1: "RA_ERR_INVALID_ARG", 2: "RA_ERR_UNSUPPORTED", 3: "RA_ERR_CUDA",
            4: "RA_ERR_TIMEOUT", 5: "RA_ERR_NO_DEVICE", 6: "RA_ERR_BOUNDS"}
-EXPORTED = ("ra_plan", "ra_plan_destroy", "ra_plan_tile_counts", "ra_fwd", "ra_merge_partials",
+EXPORTED = ("ra_plan", "ra_plan_window", "ra_plan_destroy", "ra_plan_tile_counts", "ra_fwd", "ra_merge_partials",
             "ra_layout_perm", "ra_layout_index", "ra_sync_status", "ra_last_error", "ra_fwd_static",
             "ra_fwd_static_status", "ra_fwd_step", "ra_ring_rotate", "ra_ring_fwd", "ra_bwd", "ra_bwd_scratch_size",
             "ra_allgather_kv", "ra_fwd_gathered", "ra_ulysses_a2a", "ra_wait_selftest")
@@ -81,6 +81,7 @@ def load_library():
     P, I32, I64, VP = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
     sig = {
         "ra_plan": ([ctypes.POINTER(_Problem), ctypes.POINTER(P)], I32),
+        "ra_plan_window": ([ctypes.POINTER(_Problem), I64, I64, ctypes.POINTER(P)], I32),
         "ra_plan_destroy": ([P], I32),
         "ra_plan_tile_counts": ([P, VP, VP, VP], I32),
         "ra_fwd": ([P, VP, VP, VP, VP, VP, VP, VP, VP], I32),
@@ -173,19 +174,39 @@ class Plan:
             pass
 
 
-def ra_plan(batch, seq, heads_q, heads_kv, head_dim, n_shards, layout="contiguous",
-            causal=False, dtype="bf16", scale=0.0):
-    """Validate a problem and build its ring schedule (see include/ra.h)."""
-    lib = load_library()
+def _make_plan(batch, seq, heads_q, heads_kv, head_dim, n_shards, layout, causal, dtype, scale, create):
     dt = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
     prob = _Problem(int(batch), int(seq), int(heads_q), int(heads_kv), int(head_dim), int(n_shards),
                     _layout(layout), int(bool(causal)), dt, float(scale or 0.0))
     h = ctypes.c_void_p()
-    _check(lib.ra_plan(ctypes.byref(prob), ctypes.byref(h)))
+    _check(create(prob, h))
     info = dict(batch=int(batch), seq=int(seq), heads_q=int(heads_q), heads_kv=int(heads_kv),
                 head_dim=int(head_dim), n_shards=int(n_shards), layout=_layout(layout),
                 causal=bool(causal), dtype=dt, scale=float(scale or 0.0))
     return Plan(h, info)
+
+
+def ra_plan(batch, seq, heads_q, heads_kv, head_dim, n_shards, layout="contiguous",
+            causal=False, dtype="bf16", scale=0.0):
+    """Validate a problem and build its ring schedule (see include/ra.h)."""
+    lib = load_library()
+    return _make_plan(batch, seq, heads_q, heads_kv, head_dim, n_shards, layout, causal, dtype, scale,
+                      lambda prob, h: lib.ra_plan(ctypes.byref(prob), ctypes.byref(h)))
+
+
+def ra_plan_window(batch, seq, heads_q, heads_kv, head_dim, n_shards, window, sinks=0, layout="contiguous",
+                   dtype="bf16", scale=0.0):
+    """A causal plan in which a query sees its last ``window`` keys and the first ``sinks`` keys.
+
+    Key j is visible to query i (natural positions) when j <= i and (j > i - window or
+    j < sinks).  The plan works with every call that takes one: ``ra_fwd``,
+    ``ra_fwd_step``, ``ra_ring_fwd``, ``ra_fwd_gathered`` and ``ra_bwd``.
+    """
+    lib = load_library()
+    plan = _make_plan(batch, seq, heads_q, heads_kv, head_dim, n_shards, layout, True, dtype, scale,
+                      lambda prob, h: lib.ra_plan_window(ctypes.byref(prob), int(window), int(sinks), ctypes.byref(h)))
+    plan.problem.update(window=int(window), sinks=int(sinks))
+    return plan
 
 
 def ra_plan_destroy(plan):

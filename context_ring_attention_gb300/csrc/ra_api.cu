@@ -22,6 +22,7 @@
 
 #include "ra_internal.h"
 #include "bwd_internal.h"
+#include "win_internal.h"
 
 struct ra_plan_s {
   ra_problem prob;
@@ -49,6 +50,17 @@ struct ra_plan_s {
   cudaEvent_t ev_entry = nullptr, ev_rot = nullptr, ev_step = nullptr;  // ra_ring_fwd ordering
   bool round_sync = false;  // forward kernel schedule (ra::use_round_sync)
   int sm_count = 0;
+  // Windowed plans (ra_plan_window): window 0 is the whole causal prefix.  The forward's
+  // groups come twice, over the ring's key blocks and over gathered (natural-order)
+  // keys: group g of the gathered forward is win_groups[n_win_groups + g].
+  int32_t window = 0, sinks = 0;
+  std::vector<ra::WinItem> win_items;
+  std::vector<ra::WinGroup> win_groups;
+  std::vector<ra::WinRange> win_ranges;
+  int64_t n_win_groups = 0;
+  ra::WinItem* d_win_items = nullptr;
+  ra::WinGroup* d_win_groups = nullptr;
+  ra::WinRange* d_win_ranges = nullptr;
   // One event per stream the plan's kernels were queued on, recorded after the
   // latest of them: ra_plan_destroy queues the frees of the device tables behind
   // exactly this work.  A slot whose event has completed is reused for a new stream.
@@ -313,6 +325,187 @@ void build_schedule(ra_plan_s* pl) {
   }
 }
 
+// The planner of a windowed plan (ra_plan_window).
+int32_t win_pos(const ra_problem& pb, int64_t s_n, int p, int64_t row) {
+  return (int32_t)ra::pos_of(pb.layout, pb.n_shards, s_n, p, row);
+}
+
+// Key ranges of a group over the ring (gathered: over the natural-order keys), appended
+// to the plan's list; returns the number of key tiles.
+int32_t add_ranges(ra_plan_s* pl, ra::WinGroup* gr, bool gathered) {
+  const ra_problem& pb = pl->prob;
+  const int N = pb.n_shards;
+  int32_t tiles = 0;
+  gr->range0 = (int32_t)pl->win_ranges.size();
+  auto add = [&](int step, int r, int32_t from, int32_t to) {
+    if (to <= from) return;
+    pl->win_ranges.push_back({step, r, from, to});
+    tiles += ra::range_tiles(pl->win_ranges.back());
+  };
+  for (int t = 0; t < (gathered ? 1 : N); ++t) {
+    const int r = gathered ? 0 : (gr->shard - t + N) % N;
+    const ra::WinSpan sp =
+        ra::win_span(gathered ? (int)RA_LAYOUT_CONTIGUOUS : pb.layout, gathered ? 1 : N,
+                     (int32_t)(gathered ? pb.seq : pl->s_n), pl->window, pl->sinks, r, gr->minpos, gr->maxpos);
+    add(t, r, 0, sp.first);
+    add(t, r, sp.lo, sp.hi);
+  }
+  gr->n_ranges = (int32_t)pl->win_ranges.size() - gr->range0;
+  return tiles;
+}
+
+// FULL / PARTIAL / SKIP counts of a windowed plan: a 128-row key tile is visited when
+// it holds a row of the span of the query tile, and FULL when every query of the tile
+// sees every key of it.
+void win_tile_counts(ra_plan_s* pl) {
+  const ra_problem& pb = pl->prob;
+  const int N = pb.n_shards;
+  const int32_t s_n = (int32_t)pl->s_n, T = ra::kTileRows;
+  pl->full.assign(N, 0);
+  pl->partial.assign(N, 0);
+  pl->skip.assign(N, 0);
+  for (int p = 0; p < N; ++p)
+    for (int qt = 0; qt < pl->n_qtiles; ++qt) {
+      const int32_t qmin = win_pos(pb, s_n, p, (int64_t)qt * T);
+      const int32_t qmax = (int32_t)last_row_pos(pb, s_n, p, (int64_t)qt * T);
+      for (int t = 0; t < N; ++t) {
+        const int r = (p - t + N) % N;
+        const ra::WinSpan sp = ra::win_span(pb.layout, N, s_n, pl->window, pl->sinks, r, qmin, qmax);
+        const int32_t a = (sp.first + T - 1) / T, b = sp.hi > sp.lo ? (sp.hi + T - 1) / T : 0;
+        const int32_t from = sp.hi > sp.lo ? std::max(a, sp.lo / T) : 0;
+        const int32_t visited = a + std::max(0, b - from);
+        // rows every query of the tile sees: below `all` and from `win` on or below `sink`
+        const int32_t all = ra::rows_le(pb.layout, N, s_n, r, qmin);
+        const int32_t win = ra::rows_le(pb.layout, N, s_n, r, qmax - pl->window);
+        const int32_t sink = std::min(all, ra::rows_le(pb.layout, N, s_n, r, pl->sinks - 1));
+        // tiles [0, x) end at or below row x*T (the last tile at s_n)
+        auto ended = [&](int32_t row) { return row >= s_n ? pl->n_ktiles : row / T; };
+        int32_t full;
+        if (sink >= win) {
+          full = ended(all);
+        } else {
+          const int32_t lo = (win + T - 1) / T;
+          full = ended(sink) + std::max(0, ended(all) - std::max(lo, ended(sink)));
+        }
+        pl->full[p] += full;
+        pl->partial[p] += visited - full;
+        pl->skip[p] += pl->n_ktiles - visited;
+      }
+    }
+}
+
+// Backward work lists of a windowed plan, as build_bwd_schedule: an item's own tile
+// stops at run_end, and WorkItem::pad holds the position at its other end.
+void build_win_bwd(ra_plan_s* pl) {
+  const ra_problem& pb = pl->prob;
+  const int N = pb.n_shards;
+  const int32_t s_n = (int32_t)pl->s_n;
+  const int G = pb.heads_q / pb.heads_kv;
+  std::vector<Keyed> kv, qs;
+  int64_t seqno = 0;
+  for (int p = 0; p < N; ++p)
+    for (int32_t row = 0; row < s_n;) {
+      const int32_t end = std::min(row + 128, ra::run_end(pb.layout, s_n, row));
+      const int32_t first = win_pos(pb, s_n, p, row), last = win_pos(pb, s_n, p, end - 1);
+      // the tile as keys: 64-row query tiles of every shard that see it
+      const int64_t far = (int64_t)last + pl->window - 1;
+      const int32_t upto = (int32_t)(first < pl->sinks ? pb.seq - 1 : std::min<int64_t>(far, pb.seq - 1));
+      int32_t as_kv = 0, as_q = 0;
+      for (int t = 0; t < N; ++t) {
+        const int32_t lo = ra::rows_le(pb.layout, N, s_n, (p + t) % N, first - 1);
+        const int32_t hi = ra::rows_le(pb.layout, N, s_n, (p + t) % N, upto);
+        if (hi > lo) as_kv += ((hi + 63) / 64 - lo / 64) * G;
+        // and as queries: 64-row key tiles it meets
+        const ra::WinSpan sp = ra::win_span(pb.layout, N, s_n, pl->window, pl->sinks, (p - t + N) % N, first, last);
+        as_q += (sp.first + 63) / 64 + (sp.hi > sp.lo ? (sp.hi + 63) / 64 - sp.lo / 64 : 0);
+      }
+      for (int64_t b = 0; b < pb.batch; ++b)
+        for (int h = 0; h < pb.heads_q; ++h) {
+          ra::WorkItem w{};
+          w.bh0 = (int32_t)(b * pb.heads_q + h);
+          w.bh1 = -1;
+          w.shard = p;
+          w.row0 = row;
+          w.maxq = last;
+          w.pad = first;
+          w.cost = as_q;
+          qs.push_back({w, seqno++});
+          if (h % G) continue;
+          w.maxq = first;
+          w.pad = last;
+          w.cost = as_kv;
+          kv.push_back({w, seqno++});
+        }
+      row = end;
+    }
+  // (schedule groups by the query head bh0: the key tiles' is the first of their group)
+  pl->bwd_items = schedule(kv, pb.heads_q, G);
+  for (ra::WorkItem& w : pl->bwd_items)
+    w.bh0 = (int32_t)(w.bh0 / pb.heads_q * pb.heads_kv + w.bh0 % pb.heads_q / G);
+  pl->n_bwd_kv = (int64_t)pl->bwd_items.size();
+  const std::vector<ra::WorkItem> q_sorted = schedule(qs, pb.heads_q, G);
+  pl->bwd_items.insert(pl->bwd_items.end(), q_sorted.begin(), q_sorted.end());
+}
+
+void build_win_schedule(ra_plan_s* pl) {
+  const ra_problem& pb = pl->prob;
+  const int N = pb.n_shards;
+  const int32_t s_n = (int32_t)pl->s_n;
+  pl->n_qtiles = (int)((s_n + ra::kTileRows - 1) / ra::kTileRows);
+  pl->n_ktiles = pl->n_qtiles;
+  win_tile_counts(pl);
+  if (pb.dtype != RA_DTYPE_BF16) return;  // the SIMT kernels walk rows, not items
+  const int G = pb.heads_q / pb.heads_kv;
+  const bool head_pairs = G % 2 == 0;
+
+  // Query groups: one 128-row tile for two heads of a key/value head's group, or (odd
+  // group) two consecutive tiles of one head.
+  std::vector<int32_t> tiles;
+  for (int p = 0; p < N; ++p)
+    for (int32_t row = 0; row < s_n;) {
+      ra::WinGroup gr{};
+      gr.shard = p;
+      gr.row0 = row;
+      gr.row_end = ra::run_end(pb.layout, s_n, row);
+      gr.row1 = head_pairs ? row : (row + ra::kTileRows < gr.row_end ? row + ra::kTileRows : -1);
+      const int32_t end = std::min((gr.row1 < 0 ? row : gr.row1) + ra::kTileRows, gr.row_end);
+      gr.minpos = win_pos(pb, s_n, p, row);
+      gr.maxpos = win_pos(pb, s_n, p, end - 1);
+      pl->win_groups.push_back(gr);
+      row = end;
+    }
+  pl->n_win_groups = (int64_t)pl->win_groups.size();
+  for (int64_t g = 0; g < pl->n_win_groups; ++g) tiles.push_back(add_ranges(pl, &pl->win_groups[g], false));
+  std::vector<int32_t> gathered_tiles;
+  for (int64_t g = 0; g < pl->n_win_groups; ++g) {
+    ra::WinGroup gr = pl->win_groups[g];
+    gathered_tiles.push_back(add_ranges(pl, &gr, true));
+    pl->win_groups.push_back(gr);
+  }
+
+  // Items, longest first with key/value heads grouped (the order of ra::schedule_before).
+  std::vector<Keyed> list;
+  int64_t seqno = 0;
+  for (int64_t g = 0; g < pl->n_win_groups; ++g)
+    for (int64_t b = 0; b < pb.batch; ++b)
+      for (int h = 0; h < pb.heads_q; h += head_pairs ? 2 : 1) {
+        ra::WorkItem w{};
+        w.bh0 = (int32_t)(b * pb.heads_q + h);
+        w.bh1 = head_pairs ? w.bh0 + 1 : (pl->win_groups[g].row1 >= 0 ? w.bh0 : -1);
+        w.shard = (int32_t)g;
+        w.cost = tiles[g];
+        w.pad = gathered_tiles[g];
+        list.push_back({w, seqno++});
+      }
+  const std::vector<ra::WorkItem> order = schedule(list, pb.heads_q, G);
+  // the gathered forward's items: the same order, its own groups and counts
+  for (int gathered = 0; gathered < 2; ++gathered)
+    for (const ra::WorkItem& w : order)
+      pl->win_items.push_back({w.shard + (gathered ? (int32_t)pl->n_win_groups : 0), w.bh0, w.bh1,
+                               gathered ? w.pad : w.cost});
+  build_win_bwd(pl);
+}
+
 ra_status upload(ra_plan_s* pl) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -336,9 +529,9 @@ ra_status upload(ra_plan_s* pl) {
   cudaStream_t ms = pl->mem_stream;
   e = cudaMallocAsync(reinterpret_cast<void**>(&pl->d_status), 256, ms);
   if (e == cudaSuccess) e = cudaMemsetAsync(pl->d_status, 0, 256, ms);
-  auto put = [&](const std::vector<ra::WorkItem>& host, ra::WorkItem** dev) {
+  auto put = [&](const auto& host, auto** dev) {
     if (e != cudaSuccess || host.empty()) return;
-    const size_t bytes = host.size() * sizeof(ra::WorkItem);
+    const size_t bytes = host.size() * sizeof(host[0]);
     e = cudaMallocAsync(reinterpret_cast<void**>(dev), bytes, ms);
     if (e == cudaSuccess) e = cudaMemcpyAsync(*dev, host.data(), bytes, cudaMemcpyHostToDevice, ms);
   };
@@ -346,6 +539,9 @@ ra_status upload(ra_plan_s* pl) {
   put(pl->step_items, &pl->d_step_items);
   put(pl->bwd_items, &pl->d_bwd_items);
   put(pl->gather_items, &pl->d_gather_items);
+  put(pl->win_items, &pl->d_win_items);
+  put(pl->win_groups, &pl->d_win_groups);
+  put(pl->win_ranges, &pl->d_win_ranges);
   // the tables are in place before any launch on another stream reads them
   if (e == cudaSuccess) e = cudaStreamSynchronize(ms);
   if (e == cudaSuccess) e = cudaEventCreateWithFlags(&pl->ev_entry, cudaEventDisableTiming);
@@ -385,9 +581,55 @@ ra::FwdParams fwd_params(const ra_plan_s* plan) {
 
 ra_status mark_use(ra_plan_s* plan, cudaStream_t st);
 
+// Launch a windowed plan's forward kernel: the steps and outputs of prm, on the items of
+// the plan (those of the gathered forward when prm.gathered).
+ra_status launch_win(ra_plan_s* plan, const ra::FwdParams& prm, const void* q, const void* k, const void* v,
+                     cudaStream_t st) {
+  const ra_problem& pb = plan->prob;
+  ra::WinParams w{};
+  w.batch = prm.batch;
+  w.heads_q = prm.heads_q;
+  w.heads_kv = prm.heads_kv;
+  w.group = prm.group;
+  w.head_dim = prm.head_dim;
+  w.n_shards = prm.n_shards;
+  w.layout = prm.layout;
+  w.window = plan->window;
+  w.sinks = plan->sinks;
+  w.seq = (int32_t)pb.seq;
+  w.s_n = (int32_t)plan->s_n;
+  w.scale = prm.scale;
+  w.scale_log2 = prm.scale_log2;
+  w.step_lo = prm.step_lo;
+  w.step_hi = prm.step_hi;
+  w.kv_rotated = prm.kv_rotated;
+  w.gathered = prm.gathered;
+  const int64_t n = (int64_t)plan->win_items.size() / 2;
+  w.n_items = (int32_t)n;
+  w.items = plan->d_win_items + (prm.gathered ? n : 0);
+  w.groups = plan->d_win_groups;
+  w.ranges = plan->d_win_ranges;
+  w.o = prm.o;
+  w.lse = prm.lse;
+  w.o_parts = prm.o_parts;
+  w.lse_parts = prm.lse_parts;
+  w.status = prm.status;
+  cudaError_t e;
+  const char* why = "windowed f32 forward launch failed";
+  if (pb.dtype == RA_DTYPE_BF16)
+    e = ra::launch_win_fwd_bf16(w, q, k, v, (int)std::min<int64_t>(n, plan->sm_count > 0 ? plan->sm_count : 148), st, &why);
+  else
+    e = ra::launch_win_fwd_f32(w, static_cast<const float*>(q), static_cast<const float*>(k),
+                               static_cast<const float*>(v), st);
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "%s: %s", why, cudaGetErrorString(e));
+  const ra_status s = mark_use(plan, st);
+  return s != RA_OK ? s : ok();
+}
+
 // Launch the plan's forward kernel (tensor-core for bf16, SIMT for f32) on stream.
 ra_status launch(ra_plan_s* plan, const ra::FwdParams& prm, const void* q, const void* k,
                  const void* v, cudaStream_t st) {
+  if (plan->window > 0) return launch_win(plan, prm, q, k, v, st);
   cudaError_t e;
   if (plan->prob.dtype == RA_DTYPE_BF16) {
     if (prm.n_items == 0) return ok();
@@ -506,6 +748,11 @@ ra_status ra::check_on_current_device(const void* const* ptrs, int n, cudaStream
       return fail(RA_ERR_INVALID_ARG, "pointer %p is not device memory", ptrs[i]);
     }
   }
+  // A capturing stream may not be asked for its device (the question would end the
+  // capture); a launch on a stream of another device fails by itself.
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) cudaGetLastError();
+  if (cap == cudaStreamCaptureStatusActive) return RA_OK;
   int sd = -1;
   const cudaError_t e = cudaStreamGetDevice(stream, &sd);
   if (e != cudaSuccess) {
@@ -516,31 +763,49 @@ ra_status ra::check_on_current_device(const void* const* ptrs, int n, cudaStream
   return RA_OK;
 }
 
-extern "C" {
-
-ra_status ra_plan(const ra_problem* prob, ra_plan_t* out) {
-  if (prob == nullptr || out == nullptr) return fail(RA_ERR_INVALID_ARG, "null argument");
-  *out = nullptr;
-  ra_status s = validate(prob);
-  if (s != RA_OK) return s;
+// A plan of a validated problem; window 0 is the whole (causal or full) prefix.
+static ra_status make_plan(const ra_problem* prob, int64_t window, int64_t sinks, ra_plan_t* out) {
   ra_plan_s* pl = new (std::nothrow) ra_plan_s();
   if (pl == nullptr) return fail(RA_ERR_UNSUPPORTED, "out of host memory");
   pl->prob = *prob;
   if (pl->prob.scale == 0.f) pl->prob.scale = 1.0f / std::sqrt((float)prob->head_dim);
   pl->s_n = prob->seq / prob->n_shards;
+  pl->window = (int32_t)std::min(window, prob->seq);  // (seq fits in 32 bits)
+  pl->sinks = (int32_t)std::min(sinks, prob->seq);
   try {
-    build_schedule(pl);
+    if (window > 0) build_win_schedule(pl);
+    else build_schedule(pl);
   } catch (const std::exception& ex) {  // host allocation of the work lists failed
     delete pl;
     return fail(RA_ERR_UNSUPPORTED, "planning failed on the host: %s", ex.what());
   }
-  s = upload(pl);
+  const ra_status s = upload(pl);
   if (s != RA_OK) {
     ra_plan_destroy(pl);
     return s;
   }
   *out = pl;
   return ok();
+}
+
+extern "C" {
+
+ra_status ra_plan(const ra_problem* prob, ra_plan_t* out) {
+  if (prob == nullptr || out == nullptr) return fail(RA_ERR_INVALID_ARG, "null argument");
+  *out = nullptr;
+  const ra_status s = validate(prob);
+  return s != RA_OK ? s : make_plan(prob, 0, 0, out);
+}
+
+ra_status ra_plan_window(const ra_problem* prob, int64_t window, int64_t sinks, ra_plan_t* out) {
+  if (prob == nullptr || out == nullptr) return fail(RA_ERR_INVALID_ARG, "null argument");
+  *out = nullptr;
+  const ra_status s = validate(prob);
+  if (s != RA_OK) return s;
+  if (prob->causal != 1) return fail(RA_ERR_INVALID_ARG, "a windowed plan is causal: causal must be 1");
+  if (window < 1) return fail(RA_ERR_INVALID_ARG, "window must be >= 1");
+  if (sinks < 0) return fail(RA_ERR_INVALID_ARG, "sinks must be >= 0");
+  return make_plan(prob, window, sinks, out);
 }
 
 ra_status ra_plan_destroy(ra_plan_t plan) {
@@ -554,7 +819,8 @@ ra_status ra_plan_destroy(ra_plan_t plan) {
     // order, and the host does not wait.
     if (plan->mem_stream != nullptr) {
       for (const ra_plan_s::StreamMark& m : plan->marks) cudaStreamWaitEvent(plan->mem_stream, m.done, 0);
-      void* mem[] = {plan->d_items, plan->d_step_items, plan->d_bwd_items, plan->d_gather_items, plan->d_status};
+      void* mem[] = {plan->d_items,     plan->d_step_items,  plan->d_bwd_items,   plan->d_gather_items,
+                     plan->d_win_items, plan->d_win_groups, plan->d_win_ranges, plan->d_status};
       for (void* p : mem)
         if (p != nullptr) cudaFreeAsync(p, plan->mem_stream);
       cudaStreamDestroy(plan->mem_stream);  // released once its queued frees have run
@@ -805,9 +1071,12 @@ ra_status ra_bwd(ra_plan_t plan, const void* q, const void* k, const void* v, co
   prm.dout = dout;
   prm.status = plan->d_status;
   prm.item_counter = plan->d_status + 1;
+  prm.window = plan->window;
+  prm.sinks = plan->sinks;
   if (pb.dtype != RA_DTYPE_BF16) {
-    e = ra::launch_bwd_f32(prm, static_cast<const float*>(q), static_cast<const float*>(k),
-                           static_cast<const float*>(v), static_cast<const float*>(dout), st);
+    e = (plan->window > 0 ? ra::launch_win_bwd_f32 : ra::launch_bwd_f32)(
+        prm, static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
+        static_cast<const float*>(dout), st);
     if (e != cudaSuccess) return fail(RA_ERR_CUDA, "f32 backward launch failed: %s", cudaGetErrorString(e));
     s = mark_use(plan, st);
     return s != RA_OK ? s : ok();

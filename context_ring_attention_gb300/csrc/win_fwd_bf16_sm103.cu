@@ -1,0 +1,684 @@
+// Windowed attention forward, bf16, d = 128, on the sm_100-family tensor cores.
+//
+// What it computes: for the query at position i, with s_ij = scale * q_i.k_j over the
+// keys it sees (j <= i and (j > i - window or j < sinks)),
+//   m = max_j s_ij,  l = sum_j e^(s_ij - m),  O_i = sum_j e^(s_ij - m) v_j / l,
+//   LSE_i = m + ln l,
+// folded tile by tile with the running maximum and sum of Module 23, "The Math: One
+// Block at a Time".  The planner lists, for every pair of query tiles, the key rows
+// that some query of it sees, shard by shard in ring order (win_internal.h); a key
+// tile starts at the first row that is seen, not at a multiple of 128.
+//
+// A windowed item meets few key tiles (9 for a 1024-token window, against hundreds of
+// a full causal prefix), so what matters is the seam between two items.  The stream of
+// (item, key tile) pairs is one stream: the products of the next item's first key tile
+// are issued as those of any next tile are, while the softmax of the current item's
+// last tile runs; a query tile's shared memory is handed back to the loads as soon as
+// its last score product is done; the next item's first K and V tiles are requested
+// before its queries.  Items cost nearly the same, so CTA b takes items b, b + grid,
+// ... of a list sorted by cost and key/value head: no counter, and launches of one
+// plan need no reset between them.
+//
+// Roles (one persistent CTA per SM, 12 warps): warp 0 TMA producer, warp 1 tcgen05
+// issuer (both converged, one elected lane issues), warps 4-7 softmax of query tile 0,
+// warps 8-11 of query tile 1 (one thread per row).
+// TMEM: S0 cols 0-127 (P0 in 64-127), S1 128-255 (P1 in 192-255), O0 256-383,
+// O1 384-511 (all 512 columns).
+//
+// Every mbarrier wait is bounded (~1 s).  On expiry the CTA raises an abort flag,
+// records the role in the plan's status word, drains its own in-flight TMA loads and
+// MMAs (bounded again), frees TMEM and returns.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sm100_ptx.cuh"
+#include "win_internal.h"
+
+namespace ra {
+namespace {
+
+constexpr int kThreads = 384;  // 3 warpgroups: {producer, MMA, 2 idle}, softmax 0, softmax 1
+constexpr uint32_t kRegsLaunch = 168;
+constexpr uint32_t kRegsOther = 120;
+constexpr uint32_t kRegsSoftmax = 192;
+static_assert(128 * kRegsOther + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
+constexpr uint32_t kTileBytes = 128 * 128 * 2;  // one 128 x 128 bf16 tile
+constexpr uint32_t kHalfBytes = 128 * 64 * 2;   // 128 rows x one 128-byte swizzle column
+constexpr int kStages = 5;
+constexpr uint32_t kOffQ = 0;                            // Q0, Q1
+constexpr uint32_t kOffKV = 2 * kTileBytes;              // K/V ring
+constexpr uint32_t kOffBar = kOffKV + kStages * kTileBytes;
+
+enum : int {
+  kQFull = 0,               // one per query tile
+  kQEmpty = kQFull + 2,
+  kKVFull = kQEmpty + 2,
+  kKVEmpty = kKVFull + kStages,
+  kSFull = kKVEmpty + kStages,
+  kPFull = kSFull + 2,
+  kOFull = kPFull + 2,
+  kDone = kOFull + 2,
+  kNumBars = kDone + 1
+};
+constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;  // TMEM base written by tcgen05.alloc
+constexpr uint32_t kOffAbort = kOffSlot + 4;
+constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;  // + slack to align the base to 1 KiB
+static_assert(8 * kNumBars + 8 <= 256, "barrier area");
+
+constexpr uint32_t kTmemCols = 512;
+__device__ __forceinline__ uint32_t col_s(int g) { return g ? 128u : 0u; }
+__device__ __forceinline__ uint32_t col_o(int g) { return g ? 384u : 256u; }
+// P (bf16, two per 32-bit column) overwrites the upper half of its tile's S columns
+// once the softmax has read S; the next S MMA of that tile is issued after the PV
+// MMA that reads P.
+constexpr uint32_t kColP = 64;
+
+constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(128, 128, false, false);  // Q, K both K-major
+constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(128, 128, false, true);  // V is MN-major
+constexpr uint64_t kWaitBudgetNs = 1000000000ull;
+constexpr uint32_t kSuspendHintNs = 2000u;  // a waiting thread sleeps up to this long per try
+constexpr float kRescaleSlack = 8.0f;  // log2 units: keep a stale max while p <= 2^8
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Ctl {
+  uint32_t bars;
+  volatile uint32_t* abort;
+  uint32_t* status;
+  __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
+};
+
+// Bounded wait for phase `parity` of a barrier; false on abort or expiry.
+__device__ __forceinline__ bool wait_bar(const Ctl& c, uint32_t bar, uint32_t parity, uint32_t who) {
+  if (ptx::mbar_test(bar, parity)) return true;
+  const uint64_t t0 = ptx::global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (ptx::mbar_wait_hint(bar, parity, kSuspendHintNs)) return true;
+    if ((it & 15u) == 0) {
+      if (*c.abort) return false;
+      if (ptx::global_timer_ns() - t0 > kWaitBudgetNs) {
+        *c.abort = 1u;
+        atomicOr(c.status, who);
+        return false;
+      }
+    }
+  }
+}
+
+// Teardown wait: ignores the abort flag, still bounded.
+__device__ __forceinline__ void drain_bar(const Ctl& c, uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (!ptx::mbar_test(bar, parity)) {
+    if (ptx::global_timer_ns() - t0 > kWaitBudgetNs) {
+      atomicOr(c.status, kStatusTimeoutTeardown);
+      return;
+    }
+  }
+}
+
+#define RA_WAIT(n, phase, who) __all_sync(0xffffffffu, wait_bar(c, c.bar(n), (phase) & 1u, who))
+
+// The ranges of a group that this launch runs, in ring order: [lo, hi) of its list.
+__device__ __forceinline__ int ranges_from(const WinParams& P, const WinGroup& gr) {
+  int x = gr.range0;
+  while (x < gr.range0 + gr.n_ranges && P.ranges[x].step < P.step_lo) ++x;
+  return x;
+}
+__device__ __forceinline__ bool range_in(const WinParams& P, const WinGroup& gr, int x) {
+  return x < gr.range0 + gr.n_ranges && P.ranges[x].step < P.step_hi;
+}
+
+// First row of the [B, Hkv, S, d] tensor (as rows of d) of a range's keys.
+__device__ __forceinline__ int32_t range_row(const WinParams& P, const WinGroup& gr, const WinRange& rg, int bh) {
+  const int b = bh / P.heads_q, kvh = (bh % P.heads_q) / P.group;
+  const int slot = P.gathered ? 0 : (P.kv_rotated ? gr.shard : rg.r);  // where the block of the step sits
+  return (int32_t)((int64_t)(b * P.heads_kv + kvh) * P.seq + (int64_t)slot * P.s_n + rg.row0);
+}
+
+// ------------------------------------------------------------------ producer --
+struct ProducerState {
+  uint32_t kv_issued, q_issued[2];
+};
+
+__device__ void run_producer(const WinParams& P, const Ctl& c, uint32_t sbase, const CUtensorMap* tq,
+                             const CUtensorMap* tk, const CUtensorMap* tv, ProducerState& st) {
+  const uint64_t keep = ptx::l2_policy_evict_last();   // K/V: re-read by the CTAs running together
+  const uint64_t once = ptx::l2_policy_evict_first();  // Q: read once
+  auto load_kv = [&](int32_t y) {  // K tile, then V tile
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const uint32_t s = st.kv_issued % kStages, use = st.kv_issued / kStages;
+      if (!RA_WAIT(kKVEmpty + (int)s, use ^ 1u, kStatusTimeoutProducer)) return false;
+      const uint32_t dst = sbase + kOffKV + s * kTileBytes;
+      const CUtensorMap* map = which ? tv : tk;
+      ptx::mbar_arrive_expect_tx_warp(c.bar(kKVFull + (int)s), kTileBytes);
+      ptx::tma_load_2d_warp_hint(dst, map, c.bar(kKVFull + (int)s), 0, y, keep);
+      ptx::tma_load_2d_warp_hint(dst + kHalfBytes, map, c.bar(kKVFull + (int)s), 64, y, keep);
+      ++st.kv_issued;
+    }
+    return true;
+  };
+  for (int idx = blockIdx.x; idx < P.n_items; idx += gridDim.x) {
+    const WinItem it = P.items[idx];
+    const WinGroup gr = P.groups[it.group];
+    int x = ranges_from(P, gr);
+    if (!range_in(P, gr, x)) continue;  // nothing to meet in these steps
+    RA_BOUNDS(c.status, gr.shard >= 0 && gr.shard < P.n_shards && gr.row0 >= 0 && gr.row0 < P.s_n && gr.row1 < P.s_n, 60);
+    bool q_loaded = false;
+    for (; range_in(P, gr, x); ++x) {
+      const WinRange rg = P.ranges[x];
+      const int32_t y = range_row(P, gr, rg, it.bh0);
+      const int n = range_tiles(rg);
+      RA_BOUNDS(c.status, y >= 0 && (int64_t)y + (rg.end - rg.row0) <= (int64_t)P.batch * P.heads_kv * P.seq &&
+                              rg.row0 >= 0 && rg.row0 < rg.end && rg.end <= (P.gathered ? P.seq : P.s_n), 61);
+      for (int kt = 0; kt < n; ++kt) {
+        if (!load_kv(y + kt * kTileRows)) return;
+        if (q_loaded) continue;
+        q_loaded = true;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (g == 1 && it.bh1 < 0) break;
+          if (!RA_WAIT(kQEmpty + g, st.q_issued[g] ^ 1u, kStatusTimeoutProducer)) return;
+          const int32_t yq = (int32_t)((int64_t)(g ? it.bh1 : it.bh0) * P.seq + (int64_t)gr.shard * P.s_n +
+                                       (g ? gr.row1 : gr.row0));
+          RA_BOUNDS(c.status, yq >= 0 && yq < (int64_t)P.batch * P.heads_q * P.seq, 62);
+          ptx::mbar_arrive_expect_tx_warp(c.bar(kQFull + g), kTileBytes);
+          ptx::tma_load_2d_warp_hint(sbase + kOffQ + g * kTileBytes, tq, c.bar(kQFull + g), 0, yq, once);
+          ptx::tma_load_2d_warp_hint(sbase + kOffQ + g * kTileBytes + kHalfBytes, tq, c.bar(kQFull + g), 64, yq, once);
+          ++st.q_issued[g];
+        }
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------------- MMA --
+constexpr uint32_t kTileDesc = kTileBytes >> 4;  // one tile in descriptor address units
+
+__device__ __forceinline__ void issue_s(uint32_t q0, uint32_t k0, uint32_t tmem, int g, uint32_t ks) {
+  const uint32_t a0 = q0 + (uint32_t)g * kTileDesc, b0 = k0 + ks * kTileDesc;
+#pragma unroll
+  for (uint32_t kk = 0; kk < 8; ++kk) {  // 8 steps of K = 16 over d = 128
+    const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3u) * 32u) >> 4;
+    ptx::mma_bf16_ss_lo_warp(tmem + col_s(g), a0 + off, b0 + off, kIdescS, kk > 0 ? 1u : 0u);
+  }
+}
+
+__device__ __forceinline__ void issue_pv(uint32_t v0, uint32_t tmem, int g, uint32_t vs, bool accumulate) {
+  const uint32_t a0 = tmem + col_s(g) + kColP;  // P in tensor memory
+  const uint32_t b0 = v0 + vs * kTileDesc;
+#pragma unroll
+  for (uint32_t kk = 0; kk < 8; ++kk)  // 8 steps of 16 keys = 8 TMEM columns of P
+    // V is [keys][d]: 16 keys = 2 groups of 8 rows (SBO 1 KiB); d halves 16 KiB apart (LBO).
+    ptx::mma_bf16_ts_lo_warp(tmem + col_o(g), a0 + kk * 8u, b0 + ((kk * 2048u) >> 4), kIdescPV,
+                             (accumulate || kk > 0) ? 1u : 0u);
+}
+
+// A segment is a run of key tiles folded into one (O, LSE): a whole item, or
+// (partials) one ring step of it.
+struct Seg {
+  int n;             // key tiles
+  bool two;          // two query tiles
+  bool first, last;  // first / last segment of its item
+};
+template <bool kPartials>
+struct SegWalk {
+  int idx, x;
+  bool inside;  // partials: in the middle of item idx
+  WinGroup gr;
+  bool two;
+  __device__ __forceinline__ void begin() {
+    idx = blockIdx.x;
+    inside = false;
+  }
+  __device__ __forceinline__ bool next(const WinParams& P, Seg& s) {
+    if (!kPartials) {
+      if (idx >= P.n_items) return false;
+      const WinItem it = P.items[idx];
+      s = {it.n_tiles, it.bh1 >= 0, true, true};
+      idx += gridDim.x;
+      return true;
+    }
+    s.first = false;
+    while (!inside) {  // the next item that meets a key in these steps
+      if (idx >= P.n_items) return false;
+      const WinItem it = P.items[idx];
+      gr = P.groups[it.group];
+      two = it.bh1 >= 0;
+      x = ranges_from(P, gr);
+      inside = range_in(P, gr, x);
+      s.first = true;
+      if (!inside) idx += gridDim.x;
+    }
+    const int step = P.ranges[x].step;
+    s.n = 0;
+    for (; range_in(P, gr, x) && P.ranges[x].step == step; ++x) s.n += range_tiles(P.ranges[x]);
+    s.two = two;
+    s.last = !range_in(P, gr, x);
+    if (s.last) {
+      inside = false;
+      idx += gridDim.x;
+    }
+    return true;
+  }
+};
+
+template <bool kPartials>
+__device__ void run_mma(const WinParams& P, const Ctl& c, uint32_t sbase, uint32_t tmem) {
+  const uint32_t q0 = ptx::desc_lo(sbase + kOffQ, 16);
+  const uint32_t k0 = ptx::desc_lo(sbase + kOffKV, 16);
+  const uint32_t v0 = ptx::desc_lo(sbase + kOffKV, kHalfBytes);
+  // the column map (S0, S1, O0, O1 = 0, 128, 256, 384) needs all 512 columns from 0
+  RA_BOUNDS(c.status, tmem == 0u && col_o(1) + 128u <= kTmemCols, 63);
+  uint32_t kv = 0, pj[2] = {0, 0}, qj[2] = {0, 0};
+  SegWalk<kPartials> walk;
+  walk.begin();
+  Seg cur, nxt;
+  if (!walk.next(P, cur)) return;
+  // Scores of a segment's key tile: the queries arrive with an item's first tile, and
+  // their shared memory is free for the next item's after its last.
+  auto scores = [&](const Seg& s, int kt, int g, uint32_t ks) {
+    if (s.first && kt == 0) {
+      if (!RA_WAIT(kQFull + g, qj[g], kStatusTimeoutMma)) return false;
+      ++qj[g];
+    }
+    issue_s(q0, k0, tmem, g, ks);
+    ptx::mma_commit_warp(c.bar(kSFull + g));
+    if (s.last && kt == s.n - 1) ptx::mma_commit_warp(c.bar(kQEmpty + g));
+    return true;
+  };
+  uint32_t ks = kv % kStages;
+  // Waits on TMA-filled buffers need no tcgen05 fence: the mbarrier completion
+  // already orders the async-proxy writes before the MMAs that read them.
+  if (!RA_WAIT(kKVFull + (int)ks, kv / kStages, kStatusTimeoutMma)) return;
+  if (!scores(cur, 0, 0, ks)) return;
+  if (cur.two && !scores(cur, 0, 1, ks)) return;
+  ptx::mma_commit_warp(c.bar(kKVEmpty + (int)ks));
+  ++kv;
+  for (int kt = 0;;) {
+    const bool seg_last = kt == cur.n - 1;
+    bool has_next = true;
+    int nkt = kt + 1;
+    nxt = cur;
+    if (seg_last) {
+      has_next = walk.next(P, nxt);
+      nkt = 0;
+    }
+    const uint32_t vs = kv % kStages;
+    if (!RA_WAIT(kKVFull + (int)vs, kv / kStages, kStatusTimeoutMma)) return;
+    ++kv;
+    if (!RA_WAIT(kPFull + 0, pj[0], kStatusTimeoutMma)) return;
+    ++pj[0];
+    ptx::tc_fence_after();
+    issue_pv(v0, tmem, 0, vs, kt > 0);
+    if (seg_last) ptx::mma_commit_warp(c.bar(kOFull + 0));
+    if (has_next) {
+      ks = kv % kStages;
+      if (!RA_WAIT(kKVFull + (int)ks, kv / kStages, kStatusTimeoutMma)) return;
+      ptx::tc_fence_after();
+      if (!scores(nxt, nkt, 0, ks)) return;
+    }
+    if (cur.two) {
+      if (!RA_WAIT(kPFull + 1, pj[1], kStatusTimeoutMma)) return;
+      ++pj[1];
+      ptx::tc_fence_after();
+      issue_pv(v0, tmem, 1, vs, kt > 0);
+      if (seg_last) ptx::mma_commit_warp(c.bar(kOFull + 1));
+    }
+    ptx::mma_commit_warp(c.bar(kKVEmpty + (int)vs));
+    if (!has_next) break;
+    if (nxt.two && !scores(nxt, nkt, 1, ks)) return;
+    ptx::mma_commit_warp(c.bar(kKVEmpty + (int)ks));
+    ++kv;
+    cur = nxt;
+    kt = nkt;
+  }
+}
+
+// ------------------------------------------------------------------- softmax --
+template <bool kPartials>
+__device__ __forceinline__ void store_segment(const WinParams& P, uint32_t tO, float m, float l, float fix,
+                                              bool valid, int64_t out_row, int part) {
+  const float inv = l > 0.f ? 1.0f / (l + fix) : 0.f;
+  const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  const int64_t rows_all = (int64_t)P.batch * P.heads_q * P.seq;
+#pragma unroll 1
+  for (int cc = 0; cc < 4; ++cc) {
+    uint32_t v[32];
+    __syncwarp();
+    ptx::tmem_ld32(tO + cc * 32, v);
+    if (!valid) continue;
+    if (kPartials) {
+      float4* dst = reinterpret_cast<float4*>(P.o_parts + ((int64_t)part * rows_all + out_row) * 128);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        dst[cc * 8 + q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
+                                      __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(P.o) + out_row * 128);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = ptx::pack_bf16x2(__uint_as_float(v[8 * q + 2 * e]) * inv, __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
+        dst[cc * 4 + q] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  if (valid) {
+    if (kPartials) P.lse_parts[(int64_t)part * rows_all + out_row] = lse;
+    else if (P.lse != nullptr) P.lse[out_row] = lse;
+  }
+}
+
+// A ring step in which the item's rows meet no key: O_t = 0, LSE_t = -inf.
+__device__ __forceinline__ void store_empty(const WinParams& P, bool valid, int64_t out_row, int part) {
+  if (!valid) return;
+  const int64_t rows_all = (int64_t)P.batch * P.heads_q * P.seq;
+  float4* dst = reinterpret_cast<float4*>(P.o_parts + ((int64_t)part * rows_all + out_row) * 128);
+  for (int q = 0; q < 32; ++q) dst[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  P.lse_parts[(int64_t)part * rows_all + out_row] = -INFINITY;
+}
+
+template <bool kPartials>
+__device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t tmem, int g, int wq, int lane) {
+  const int row = wq * 32 + lane;  // TMEM lane = query row of the tile
+  const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+  const uint32_t tS = tmem + lane_off + col_s(g);
+  const uint32_t tO = tmem + lane_off + col_o(g);
+  RA_BOUNDS(c.status, wq >= 0 && wq < 4 && (tS & 0xFFFFu) + 128u <= kTmemCols && (tO & 0xFFFFu) + 128u <= kTmemCols &&
+                          (tS & 0xFFFFu) + kColP + 64u <= kTmemCols, 64);
+  const float sl2 = P.scale_log2;
+  uint32_t sj = 0, oj = 0;
+
+  for (int idx = blockIdx.x; idx < P.n_items; idx += gridDim.x) {
+    const WinItem it = P.items[idx];
+    if (g == 1 && it.bh1 < 0) continue;
+    const WinGroup gr = P.groups[it.group];
+    const int bh = g ? it.bh1 : it.bh0;
+    const int i = (g ? gr.row1 : gr.row0) + row;
+    const bool valid = i < gr.row_end;
+    const int my_pos = (int)pos_of(P.layout, P.n_shards, P.s_n, gr.shard, valid ? i : gr.row_end - 1);
+    const int64_t out_row = (int64_t)bh * P.seq + (int64_t)gr.shard * P.s_n + i;
+    RA_BOUNDS(c.status, !valid || (bh >= 0 && out_row >= 0 && out_row < (int64_t)P.batch * P.heads_q * P.seq), 65);
+
+    float m = -INFINITY, l = 0.f, fix = 0.f;
+    bool first = true;
+    int next_part = P.step_lo;  // partials: steps below are written
+    int x = ranges_from(P, gr);
+    while (range_in(P, gr, x)) {
+      const WinRange rg = P.ranges[x];
+      ++x;
+      const bool seg_end = !range_in(P, gr, x) || (kPartials && P.ranges[x].step != rg.step);
+      if (kPartials)
+        for (; next_part < rg.step; ++next_part) store_empty(P, valid, out_row, next_part - P.step_lo);
+      // The row sees rows below sk and [lo, hi) of the block met (win_internal.h), and of
+      // those the range's own.
+      const int layout = P.gathered ? (int)RA_LAYOUT_CONTIGUOUS : P.layout;
+      const int ns = P.gathered ? 1 : P.n_shards, bs = P.gathered ? P.seq : P.s_n;
+      const int upto = rows_le(layout, ns, bs, rg.r, my_pos);
+      const int hi = (upto < rg.end ? upto : rg.end) - rg.row0;
+      const int lo = rows_le(layout, ns, bs, rg.r, my_pos - P.window) - rg.row0;
+      const int sk = rows_le(layout, ns, bs, rg.r, P.sinks - 1) - rg.row0;
+
+      const int n = range_tiles(rg);
+      for (int kt = 0; kt < n; ++kt) {
+        const int y = kt * kTileRows;
+        const bool last = seg_end && kt == n - 1;
+        const int c_hi = hi - y, c_lo = lo - y;       // columns [c_lo, c_hi), and those
+        const int c_s = sk < hi ? sk - y : c_hi;      // below c_s, are seen
+        const bool full = c_hi >= kTileRows && (c_lo <= 0 || c_s >= kTileRows);
+
+        bool ok = wait_bar(c, c.bar(kSFull + g), sj & 1u, kStatusTimeoutSoftmax);
+        ++sj;
+        if (!__all_sync(0xffffffffu, ok)) return;
+        ptx::tc_fence_after();
+
+        // The whole 128-column score row in registers (one TMEM round trip); the
+        // reducing load also returns the largest score of each 32 columns.
+        uint32_t raw[128];
+        float mx4[4];
+        ptx::tmem_ld128_max(tS, raw, mx4);
+        float* s = reinterpret_cast<float*>(raw);
+        float mx;
+        if (!__all_sync(0xffffffffu, full)) {
+          // An edge of the window, the diagonal or the sinks: the other keys score
+          // -inf, and the row max is taken over the rest.
+          const uint32_t width = (uint32_t)(c_hi > c_lo ? c_hi - c_lo : 0);
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            s[e] = ((uint32_t)(e - c_lo) < width || e < c_s) ? s[e] : -INFINITY;
+          float mx8[8];
+#pragma unroll
+          for (int a = 0; a < 8; ++a) mx8[a] = ptx::max3(s[a], s[a + 8], s[a + 16]);
+#pragma unroll
+          for (int e = 24; e + 16 <= 120; e += 16)
+#pragma unroll
+            for (int a = 0; a < 8; ++a) mx8[a] = ptx::max3(mx8[a], s[e + a], s[e + 8 + a]);
+#pragma unroll
+          for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(mx8[a], s[120 + a]);
+          mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
+                     fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        } else {
+          mx = fmaxf(ptx::max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
+        }
+        const float mt = mx * sl2;  // in log2 units; -inf stays -inf
+        float m_new = m;
+        bool resc = false;
+        if (first) {
+          m_new = mt;
+          l = fix = 0.f;
+        } else if (mt > m + kRescaleSlack) {
+          m_new = mt;
+          resc = true;
+        }
+        const float alpha = resc ? ptx::ex2_approx(m - m_new) : 1.0f;
+        m = m_new;
+        const float mref = (m == -INFINITY) ? 0.f : m;
+
+        // p = 2^(s*scale*log2e - m) (masked -inf -> 0), row sum, P to tensor memory as bf16.
+        const float2 sc2 = make_float2(sl2, sl2);
+        const float2 neg = make_float2(-mref, -mref);
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                         make_float2(0.f, 0.f)};
+        // Packed P word e overwrites register e, whose score was already consumed.
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          float2 x2 = ptx::fma2(make_float2(s[2 * e], s[2 * e + 1]), sc2, neg);
+          x2.x = ptx::ex2_approx(x2.x);
+          x2.y = ptx::ex2_approx(x2.y);
+          acc[e & 3] = ptx::add2(acc[e & 3], x2);
+          raw[e] = ptx::pack_bf16x2(x2.x, x2.y);
+        }
+        ptx::tmem_st64(tS + kColP, *reinterpret_cast<const uint32_t(*)[64]>(raw));
+        const float2 a01 = ptx::add2(acc[0], acc[1]);
+        const float2 a23 = ptx::add2(acc[2], acc[3]);
+        const float2 a = ptx::add2(a01, a23);
+        // The PV product weighs each key by its bf16-rounded p while l sums the fp32 p.
+        // `fix` holds the rounding of every tile's largest p: O is divided by l + fix, so
+        // that when one key dominates a row its rounding cancels; the LSE is that of l.
+        const float p_top = ptx::ex2_approx(ptx::fma2(make_float2(mx, mx), sc2, neg).x);
+        const float p_top_bf = __uint_as_float(ptx::pack_bf16x2(p_top, 0.f) << 16);
+        const float top_fix = p_top_bf - p_top;
+        if (!first && __any_sync(0xffffffffu, resc)) {
+          // O and l were accumulated against the old max: bring them to the new one
+          // (after the scores are consumed, so their registers are free).
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t v[32];
+            __syncwarp();
+            ptx::tmem_ld32(tO + cc * 32, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+            ptx::tmem_st32(tO + cc * 32, v);
+          }
+          l *= alpha;
+          fix *= alpha;
+        }
+        l += a.x + a.y;
+        fix += top_fix;
+        first = false;
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(c.bar(kPFull + g));
+
+        if (last) {
+          ok = wait_bar(c, c.bar(kOFull + g), oj & 1u, kStatusTimeoutSoftmax);
+          ++oj;
+          if (!__all_sync(0xffffffffu, ok)) return;
+          ptx::tc_fence_after();
+          store_segment<kPartials>(P, tO, m, l, fix, valid, out_row, rg.step - P.step_lo);
+          ptx::tc_fence_before();
+          next_part = rg.step + 1;
+          m = -INFINITY;
+          l = fix = 0.f;
+          first = true;
+        }
+        __syncwarp();
+      }
+    }
+    if (kPartials)
+      for (; next_part < P.step_hi; ++next_part) store_empty(P, valid, out_row, next_part - P.step_lo);
+  }
+}
+
+template <bool kPartials>
+__global__ void __launch_bounds__(kThreads, 1)
+    win_fwd_bf16_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, const WinParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* sgen = smem_raw + (sbase - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Ctl c{sbase + kOffBar, reinterpret_cast<volatile uint32_t*>(sgen + kOffAbort), P.status};
+
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < 2; ++g) {
+      ptx::mbar_init(c.bar(kQFull + g), 1);
+      ptx::mbar_init(c.bar(kQEmpty + g), 1);
+      ptx::mbar_init(c.bar(kSFull + g), 1);
+      ptx::mbar_init(c.bar(kPFull + g), 128);
+      ptx::mbar_init(c.bar(kOFull + g), 1);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(c.bar(kKVFull + s), 1);
+      ptx::mbar_init(c.bar(kKVEmpty + s), 1);
+    }
+    ptx::mbar_init(c.bar(kDone), 1);
+    *c.abort = 0u;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::tma_prefetch_desc(&tq);
+    ptx::tma_prefetch_desc(&tk);
+    ptx::tma_prefetch_desc(&tv);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(sbase + kOffSlot, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sgen + kOffSlot);
+
+  ProducerState ps{0u, {0u, 0u}};
+  if (warp < 4) {
+    ptx::regs_release<kRegsOther>();
+    if (warp == 0) {
+      run_producer(P, c, sbase, &tq, &tk, &tv, ps);  // whole warp; one elected lane issues
+      __syncwarp();
+    } else if (warp == 1) {
+      run_mma<kPartials>(P, c, sbase, tmem);
+      // Every MMA this warp issued must retire before TMEM is freed.
+      ptx::mma_commit_warp(c.bar(kDone));
+      drain_bar(c, c.bar(kDone), 0);
+      __syncwarp();
+    }
+  } else {
+    ptx::regs_acquire<kRegsSoftmax>();
+    run_softmax<kPartials>(P, c, tmem, (warp - 4) >> 2, warp & 3, lane);
+  }
+
+  if (warp == 0 && lane == 0 && *c.abort) {  // (every lane of warp 0 holds the same counts)
+    // Let this CTA's own TMA loads land before its shared memory goes away.
+    for (uint32_t s = 0; s < (uint32_t)kStages; ++s) {
+      if (ps.kv_issued > s) {
+        const uint32_t uses = (ps.kv_issued - 1 - s) / kStages + 1;  // loads issued to slot s
+        drain_bar(c, c.bar(kKVFull + (int)s), (uses - 1) & 1u);
+      }
+    }
+    for (int g = 0; g < 2; ++g)
+      if (ps.q_issued[g] > 0) drain_bar(c, c.bar(kQFull + g), (ps.q_issued[g] - 1) & 1u);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encoder() {
+  static EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// [rows, 128] bf16 row-major, boxes of 128 rows x 64 columns, 128-byte swizzle.
+bool encode_rows(CUtensorMap* map, const void* base, int64_t rows) {
+  EncodeTiledFn enc = get_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {128, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {128 * 2};
+  const cuuint32_t box[2] = {64, 128};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kPartials>
+cudaError_t launch_kernel(const WinParams& prm, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                          int grid, cudaStream_t stream, const char** why) {
+  static std::atomic<int> ready[kMaxDevices];
+  cudaError_t e = prepare_once(win_fwd_bf16_kernel<kPartials>, ready, kThreads, 128 * kRegsOther + 256 * kRegsSoftmax,
+                               (int)kSmemBytes, why);
+  if (e != cudaSuccess) return e;
+  win_fwd_bf16_kernel<kPartials><<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, prm);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) *why = "windowed tensor-core forward launch failed";
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_win_fwd_bf16(const WinParams& prm, const void* q, const void* k, const void* v, int grid,
+                                cudaStream_t stream, const char** why) {
+  CUtensorMap tq, tk, tv;
+  const int64_t rows_q = (int64_t)prm.batch * prm.heads_q * prm.seq;
+  const int64_t rows_kv = (int64_t)prm.batch * prm.heads_kv * prm.seq;
+  if (!encode_rows(&tq, q, rows_q) || !encode_rows(&tk, k, rows_kv) || !encode_rows(&tv, v, rows_kv)) {
+    *why = "cuTensorMapEncodeTiled failed or is unavailable";
+    return cudaErrorInvalidValue;
+  }
+  return prm.o_parts != nullptr ? launch_kernel<true>(prm, tq, tk, tv, grid, stream, why)
+                                : launch_kernel<false>(prm, tq, tk, tv, grid, stream, why);
+}
+
+}  // namespace ra

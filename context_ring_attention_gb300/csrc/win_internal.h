@@ -1,0 +1,111 @@
+// Windowed attention: a query at position i sees the keys j <= i with j > i - window
+// or j < sinks (the first tokens of the sequence, which stay visible).  Declarations
+// shared by the planner (ra_api.cu) and the kernels (win_fwd_bf16_sm103.cu,
+// win_f32.cu, bwd_bf16_sm103.cu).
+//
+// Positions rise with the local row in every layout, so the keys of shard r that a
+// query at position P sees are the rows
+//   [0, first)  with first = rows of r at positions < sinks          (the sinks), and
+//   [lo, hi)    with lo = rows at positions <= P - window,
+//                    hi = rows at positions <= P                      (the window).
+#pragma once
+
+#include "bwd_internal.h"
+
+namespace ra {
+
+// Rows of shard r at positions <= P (P may be negative): last_le + 1 in 32 bits.
+RA_HD int32_t rows_le(int layout, int n_shards, int32_t s_n, int r, int32_t P) {
+  int32_t n;
+  if (layout == RA_LAYOUT_STRIPED) {
+    n = P < r ? 0 : (int32_t)((uint32_t)(P - r) / (uint32_t)n_shards) + 1;
+  } else if (layout == RA_LAYOUT_ZIGZAG) {
+    const int32_t c = s_n >> 1;
+    const int32_t lo = r * c, hi = (2 * n_shards - 1 - r) * c;
+    if (P < hi) {
+      n = P < lo ? 0 : P - lo + 1;
+      n = n < c ? n : c;
+    } else {
+      n = c + (P - hi) + 1;
+    }
+  } else {
+    n = P < r * s_n ? 0 : P - r * s_n + 1;
+  }
+  return n < s_n ? n : s_n;
+}
+
+// End of the run of consecutive positions (contiguous, zigzag) or of equal steps
+// (striped) that local row `row` lies in.  Query and key tiles of a windowed plan stop
+// there: a tile across the two chunks of a zigzag shard would span most of the
+// sequence, and meet as many tiles.
+RA_HD int32_t run_end(int layout, int32_t s_n, int32_t row) {
+  return layout == RA_LAYOUT_ZIGZAG && row < (s_n >> 1) ? (s_n >> 1) : s_n;
+}
+
+// Key rows of shard r that some query at positions [minpos, maxpos] sees: [0, first)
+// and [lo, hi), merged into [lo, hi) (first == 0) when they touch.
+struct WinSpan {
+  int32_t first, lo, hi;
+};
+RA_HD WinSpan win_span(int layout, int n_shards, int32_t s_n, int32_t window, int32_t sinks, int r, int32_t minpos,
+                       int32_t maxpos) {
+  WinSpan s;
+  s.hi = rows_le(layout, n_shards, s_n, r, maxpos);
+  s.lo = rows_le(layout, n_shards, s_n, r, minpos - window);
+  s.first = rows_le(layout, n_shards, s_n, r, sinks - 1);
+  if (s.first > s.hi) s.first = s.hi;
+  if (s.first >= s.lo) {
+    if (s.first > 0) s.lo = 0;
+    s.first = 0;
+  }
+  return s;
+}
+
+// Forward work list of a windowed plan.  A group is the query rows of one work item
+// (one or two tiles of up to 128 rows) with the key tiles they meet; an item is a
+// group for one or two heads.
+struct alignas(16) WinGroup {
+  int32_t shard, row0;   // tile 0: local rows row0 .. min(row0 + 128, row_end)
+  int32_t row1;          // tile 1's first row (row0 when the item pairs two heads, -1: none)
+  int32_t row_end;
+  int32_t minpos, maxpos;
+  int32_t range0, n_ranges;  // its key ranges
+};
+// Key rows [row0, end) of shard r, met at ring step `step` in tiles of 128 from row0 (the
+// rows of the last tile from `end` on belong to another range or to nobody).
+struct alignas(16) WinRange {
+  int32_t step, r, row0, end;
+};
+RA_HD int32_t range_tiles(const WinRange& rg) { return (rg.end - rg.row0 + kTileRows - 1) / kTileRows; }
+struct alignas(16) WinItem {
+  int32_t group, bh0, bh1;  // bh = b*Hq + h of tile 0 and of tile 1 (-1: one tile)
+  int32_t n_tiles;          // key tiles over all its ranges
+};
+
+struct WinParams {
+  int32_t batch, heads_q, heads_kv, group, head_dim, n_shards, layout;
+  int32_t window, sinks;
+  int32_t seq, s_n;
+  int32_t n_items;
+  float scale, scale_log2;
+  int32_t step_lo, step_hi;  // ring steps of this launch
+  int32_t kv_rotated;        // as FwdParams::kv_rotated
+  int32_t gathered;          // as FwdParams::gathered
+  const WinItem* items;
+  const WinGroup* groups;
+  const WinRange* ranges;
+  void* o;
+  float* lse;
+  float* o_parts;
+  float* lse_parts;
+  uint32_t* status;
+};
+
+cudaError_t launch_win_fwd_bf16(const WinParams& prm, const void* q, const void* k, const void* v, int grid,
+                                cudaStream_t stream, const char** why);
+cudaError_t launch_win_fwd_f32(const WinParams& prm, const float* q, const float* k, const float* v,
+                               cudaStream_t stream);
+cudaError_t launch_win_bwd_f32(const BwdParams& prm, const float* q, const float* k, const float* v,
+                               const float* dout, cudaStream_t stream);
+
+}  // namespace ra

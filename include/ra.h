@@ -123,6 +123,26 @@ typedef struct ra_plan_s* ra_plan_t;
  */
 ra_status ra_plan(const ra_problem* prob, ra_plan_t* out);
 
+/*
+ * ra_plan_window -- a plan in which a query sees only the last `window` keys up to its
+ * own position and the first `sinks` keys of the sequence: key j is visible to query i
+ * (global positions) when j <= i and (j > i - window or j < sinks).  The pages' causal
+ * attention sees the whole prefix; this is its windowed form for sequences whose full
+ * prefix is not wanted.  Every entry point that takes a plan accepts it, with the same
+ * tensors: ra_fwd (fused and partials), ra_fwd_step, ra_ring_fwd, ra_fwd_gathered,
+ * ra_bwd.  Key tiles that no query of a query tile sees are neither read nor computed.
+ * prob: as for ra_plan, with causal 1.
+ * window: >= 1; a window of at least seq is the whole causal prefix.
+ * sinks: >= 0; any value from seq on is the whole causal prefix as well.
+ * ra_plan_tile_counts on it: FULL when every query of the tile sees every key, PARTIAL
+ * for the other key tiles within reach of the query tile, SKIP for the rest.
+ * K and V must be finite: a key that a query does not see enters its products with
+ * weight zero where it shares a tile with keys that are seen, and zero times an
+ * infinity or a NaN is a NaN.
+ * Errors: as ra_plan, and RA_ERR_INVALID_ARG (causal 0, window < 1, sinks < 0).
+ */
+ra_status ra_plan_window(const ra_problem* prob, int64_t window, int64_t sinks, ra_plan_t* out);
+
 /* Release a plan and its device memory.  NULL is accepted.  It does not wait:
  * kernels queued with this plan may still read its tables, so the plan records
  * an event on every stream it launched on (after its latest launch there), and
