@@ -5,7 +5,9 @@ The functions keep the C names (``ra_plan``, ``ra_plan_window``, ``ra_plan_tile_
 ``ra_fwd_static``, ``ra_fwd_static_status``, ``ra_merge_partials``, ``ra_layout_perm``, ``ra_layout_index``,
 ``ra_fwd_step``, ``ra_ring_rotate``, ``ra_ring_fwd``, ``ra_bwd``,
 ``ra_bwd_scratch_size``, ``ra_allgather_kv``, ``ra_fwd_gathered``,
-``ra_ulysses_a2a``, ``ra_sync_status``, ``ra_wait_selftest``, ``ra_last_error``).
+``ra_ulysses_a2a``, ``ra_sync_status``, ``ra_wait_selftest``, ``ra_last_error``;
+``ra_kv4_plan``, ``ra_kv4_cache_size``, ``ra_kv4_write``, ``ra_kv4_read``,
+``ra_kv4_attend``, ``ra_kv4_attend_scratch_size``, ``ra_kv4_sync_status``).
 This module only marshals arguments: PyTorch supplies device memory and the
 current stream, every step of the computation runs in the library's CUDA
 kernels, and there is no fallback -- if libra.so is missing or cannot be loaded,
@@ -32,6 +34,8 @@ __all__ = [
     "ra_layout_perm", "ra_layout_index", "ra_sync_status", "ra_last_error", "ra_fwd_static",
     "ra_fwd_static_status", "ra_fwd_step", "ra_ring_rotate", "ra_ring_fwd", "ra_bwd", "ra_bwd_scratch_size",
     "ra_allgather_kv", "ra_fwd_gathered", "ra_ulysses_a2a", "ra_wait_selftest",
+    "Kv4", "ra_kv4_plan", "ra_kv4_destroy", "ra_kv4_cache_size", "ra_kv4_write", "ra_kv4_read", "ra_kv4_attend",
+    "ra_kv4_attend_scratch_size", "ra_kv4_sync_status",
     "library_path", "load_library", "EXPORTED",
 ]
 
@@ -42,7 +46,9 @@ _STATUS = {0: "RA_OK", 1: "RA_ERR_INVALID_ARG", 2: "RA_ERR_UNSUPPORTED", 3: "RA_
 EXPORTED = ("ra_plan", "ra_plan_window", "ra_plan_destroy", "ra_plan_tile_counts", "ra_fwd", "ra_merge_partials",
             "ra_layout_perm", "ra_layout_index", "ra_sync_status", "ra_last_error", "ra_fwd_static",
             "ra_fwd_static_status", "ra_fwd_step", "ra_ring_rotate", "ra_ring_fwd", "ra_bwd", "ra_bwd_scratch_size",
-            "ra_allgather_kv", "ra_fwd_gathered", "ra_ulysses_a2a", "ra_wait_selftest")
+            "ra_allgather_kv", "ra_fwd_gathered", "ra_ulysses_a2a", "ra_wait_selftest",
+            "ra_kv4_plan", "ra_kv4_destroy", "ra_kv4_cache_size", "ra_kv4_write", "ra_kv4_read", "ra_kv4_attend",
+            "ra_kv4_attend_scratch_size", "ra_kv4_sync_status")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -60,6 +66,12 @@ class _Problem(ctypes.Structure):
                 ("heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("n_shards", ctypes.c_int32),
                 ("layout", ctypes.c_int32), ("causal", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class _Kv4Problem(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int64), ("page_rows", ctypes.c_int32), ("heads_q", ctypes.c_int32),
+                ("heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("window", ctypes.c_int64), ("sinks", ctypes.c_int64), ("scale", ctypes.c_float)]
 
 
 def library_path():
@@ -101,6 +113,14 @@ def load_library():
         "ra_fwd_gathered": ([P, VP, VP, VP, VP, VP, VP], I32),
         "ra_ulysses_a2a": ([I32, I32, I64, I32, I64, I32, I32, VP, VP, VP], I32),
         "ra_wait_selftest": ([VP], I32),
+        "ra_kv4_plan": ([ctypes.POINTER(_Kv4Problem), ctypes.POINTER(P)], I32),
+        "ra_kv4_destroy": ([P], I32),
+        "ra_kv4_cache_size": ([P, VP], I32),
+        "ra_kv4_write": ([P, VP, I64, I64, VP, VP, VP, I64, VP, VP, VP], I32),
+        "ra_kv4_read": ([P, VP, I64, I64, VP, I64, VP, VP, I32, VP, VP, VP], I32),
+        "ra_kv4_attend": ([P, VP, I64, I64, VP, VP, I64, VP, VP, VP, VP, VP], I32),
+        "ra_kv4_attend_scratch_size": ([P, I64, I64, I64, VP], I32),
+        "ra_kv4_sync_status": ([P, VP], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -138,6 +158,16 @@ def _stream(stream):
         raise ValueError(f"the stream belongs to {stream.device}; the library launches on the current device "
                          f"cuda:{cur}")
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _alloc_on(stream):
+    """Context in which buffers made for a call belong to the stream the call runs on, so that
+    the allocator does not hand them on while its kernels may still use them."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def _on_current_device(name, t):
@@ -480,7 +510,8 @@ def ra_bwd(plan, q, k, v, o, lse, dout, dq=None, dk=None, dv=None, scratch=None,
     if dv is None:
         dv = torch.empty_like(v)
     if scratch is None:
-        scratch = torch.empty(ra_bwd_scratch_size(plan) // 4, dtype=torch.float32, device=q.device)
+        with _alloc_on(stream):
+            scratch = torch.empty(ra_bwd_scratch_size(plan) // 4, dtype=torch.float32, device=q.device)
     elif (scratch.numel() * scratch.element_size() < ra_bwd_scratch_size(plan) or scratch.dtype != torch.float32
           or not scratch.is_contiguous() or scratch.device != q.device):
         raise ValueError("scratch must be a contiguous float32 tensor of at least ra_bwd_scratch_size(plan) "
@@ -559,3 +590,151 @@ def ra_ulysses_a2a(x, layout, n_shards, direction, out=None, stream=None):
     _check(load_library().ra_ulysses_a2a(int(direction), _layout(layout), int(S), N, int(B), int(H), row_bytes,
                                          _ptr(x), _ptr(out), _stream(stream)))
     return out
+
+
+class Kv4:
+    """Owns an ``ra_kv4_t``; the cache it was described for is ``self.problem``."""
+
+    def __init__(self, handle, problem):
+        self._h = handle
+        self.problem = problem
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h:
+            load_library().ra_kv4_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def ra_kv4_plan(pages, page_rows, heads_q, heads_kv, head_dim, dtype="bf16", window=0, sinks=0, scale=0.0):
+    """Describe a paged 4-bit key/value cache and the attention over it (see include/ra.h)."""
+    lib = load_library()
+    dt = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+    prob = _Kv4Problem(int(pages), int(page_rows), int(heads_q), int(heads_kv), int(head_dim), dt, int(window),
+                       int(sinks), float(scale or 0.0))
+    h = ctypes.c_void_p()
+    _check(lib.ra_kv4_plan(ctypes.byref(prob), ctypes.byref(h)))
+    info = dict(pages=int(pages), page_rows=int(page_rows), heads_q=int(heads_q), heads_kv=int(heads_kv),
+                head_dim=int(head_dim), dtype=dt, window=int(window), sinks=int(sinks), scale=float(scale or 0.0))
+    return Kv4(h, info)
+
+
+def ra_kv4_destroy(kv):
+    kv.close()
+
+
+def ra_kv4_cache_size(kv):
+    """Bytes of the cache buffer (a contiguous uint8 CUDA tensor of the caller's)."""
+    n = ctypes.c_int64()
+    _check(load_library().ra_kv4_cache_size(kv.handle, ctypes.byref(n)))
+    return n.value
+
+
+def _kv4_dtype(kv):
+    import torch
+    return torch.bfloat16 if kv.problem["dtype"] == 1 else torch.float32
+
+
+def _kv4_tables(kv, cache, batch, page_table, **per_sequence):
+    """The cache, the page table and the [batch] int32 tables of a call, all on one device."""
+    import torch
+    _need("cache", cache, (ra_kv4_cache_size(kv),), torch.uint8, cache.device)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != batch:
+        raise ValueError(f"page_table must be an int32 tensor of shape ({batch}, pages of a sequence)")
+    _need("page_table", page_table, page_table.shape, torch.int32, cache.device)
+    for name, t in per_sequence.items():
+        if t is not None:
+            _need(name, t, (batch,), torch.int32, cache.device)
+
+
+def ra_kv4_write(kv, cache, k, v, page_table, first, count=None, stream=None):
+    """Quantise rows k, v [B, Hkv, T, d] into the cache at positions first[b] + t, t < count[b]."""
+    pb = kv.problem
+    B, T = k.shape[0], k.shape[2] if k.dim() == 4 else 0
+    _kv4_tables(kv, cache, B, page_table, first=first, count=count)
+    shape = (B, pb["heads_kv"], T, pb["head_dim"])
+    _need("k", k, shape, _kv4_dtype(kv), cache.device)
+    _need("v", v, shape, _kv4_dtype(kv), cache.device)
+    _check(load_library().ra_kv4_write(kv.handle, _ptr(cache), B, T, _ptr(k), _ptr(v), _ptr(page_table),
+                                       page_table.shape[1], _ptr(first), _ptr(count), _stream(stream)))
+
+
+def ra_kv4_read(kv, cache, page_table, first, rows, count=None, k=None, v=None, stream=None):
+    """Rows [B, Hkv, rows, d] of the cache as the values they stand for -> (k, v).
+
+    Rows from count[b] on stay as they were in k and v that are passed in (both or
+    neither); they are zeros where k and v are allocated here.
+    """
+    import torch
+    pb = kv.problem
+    B, T = page_table.shape[0], int(rows)
+    _kv4_tables(kv, cache, B, page_table, first=first, count=count)
+    shape = (B, pb["heads_kv"], T, pb["head_dim"])
+    if (k is None) != (v is None):
+        raise ValueError("pass both k and v, or neither")
+    own = k is None
+    if own:
+        with _alloc_on(stream):
+            k, v = (torch.empty(shape, dtype=_kv4_dtype(kv), device=cache.device) for _ in range(2))
+    _need("k", k, shape, _kv4_dtype(kv), cache.device)
+    _need("v", v, shape, _kv4_dtype(kv), cache.device)
+    _check(load_library().ra_kv4_read(kv.handle, _ptr(cache), B, T, _ptr(page_table), page_table.shape[1],
+                                      _ptr(first), _ptr(count), int(own), _ptr(k), _ptr(v), _stream(stream)))
+    return k, v
+
+
+def ra_kv4_attend_scratch_size(kv, batch, rows, table_width):
+    """Bytes of the float32 scratch buffer ra_kv4_attend needs for these sizes (0: none)."""
+    n = ctypes.c_int64()
+    _check(load_library().ra_kv4_attend_scratch_size(kv.handle, int(batch), int(rows), int(table_width),
+                                                     ctypes.byref(n)))
+    return n.value
+
+
+def ra_kv4_attend(kv, cache, q, page_table, length, o=None, lse=None, scratch=None, stream=None):
+    """Attention of the last T tokens q [B, Hq, T, d] of every sequence over the cache -> (O, LSE).
+
+    length[b] counts the tokens of sequence b in the cache, the T new ones among them.
+    ``scratch`` (``ra_kv4_attend_scratch_size`` bytes, float32) is allocated here unless
+    passed in.
+    """
+    import torch
+    pb = kv.problem
+    if q.dim() != 4:
+        raise ValueError("q must have the shape [B, Hq, T, d]")
+    B, T = q.shape[0], q.shape[2]
+    _kv4_tables(kv, cache, B, page_table, length=length)
+    _need("q", q, (B, pb["heads_q"], T, pb["head_dim"]), _kv4_dtype(kv), cache.device)
+    with _alloc_on(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    _need("o", o, q.shape, q.dtype, q.device)
+    _need("lse", lse, q.shape[:3], torch.float32, q.device)
+    need = ra_kv4_attend_scratch_size(kv, B, T, page_table.shape[1]) // 4
+    if scratch is None and need:
+        with _alloc_on(stream):
+            scratch = torch.empty(need, dtype=torch.float32, device=q.device)
+    elif scratch is not None and (scratch.numel() < need or scratch.dtype != torch.float32
+                                  or not scratch.is_contiguous() or scratch.device != q.device):
+        raise ValueError("scratch must be a contiguous float32 tensor of at least ra_kv4_attend_scratch_size(...) "
+                         "bytes on the device of q")
+    _check(load_library().ra_kv4_attend(kv.handle, _ptr(cache), B, T, _ptr(q), _ptr(page_table), page_table.shape[1],
+                                        _ptr(length), _ptr(o), _ptr(lse), _ptr(scratch), _stream(stream)))
+    return o, lse
+
+
+def ra_kv4_sync_status(kv, stream=None):
+    """Synchronize the stream and raise RaError if a call met a page index, position, length
+    or count out of range."""
+    _check(load_library().ra_kv4_sync_status(kv.handle, _stream(stream)))

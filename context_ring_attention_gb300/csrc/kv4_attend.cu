@@ -1,0 +1,411 @@
+// Attention of a few new tokens per sequence over the 4-bit cache.
+//
+// For the query rows of one key/value head (rows of its group's heads and of the new
+// tokens, 8 to a tile) and the cached keys j that they see,
+//   s_j = sum_g [ ks_jg * sum_{c in g} q_c (n_jc - 8) + km_jg * sum_{c in g} q_c ],
+//   O   = sum_j p_j [ vs_jg * (n_jc - 8) + vm_jg ] / sum_j p_j,   p_j = e^(s_j - m),
+// with codes n, scales ks, vs and middles km = low + 8 * scale (also vm): the codes enter
+// the products as the integers -8..7, exact in bf16, and the parameters are applied per
+// group in fp32 -- to the 4 sums of a score, and to p before it is rounded for the second
+// product; the middles' share of O is a plain fp32 sum per group.  Centred codes keep the
+// rounding of p from being multiplied by the offset of the group.
+//
+// Bound by HBM at 20 * d bytes per 16 tokens and head.  The products are so few (8 query
+// rows) that the warp-level tensor instruction serves: m16n8k16 with the codes as the
+// 16-row operand -- keys x channels for the scores, channels x keys for the output -- and
+// the query rows as its 8 columns, so that nothing is computed for absent rows beyond 8,
+// and 4-bit codes become operand registers with one logical and one subtraction a pair.
+// Scores come out with keys in rows and are turned for the second product by an 8x8
+// transpose in registers.
+//
+// Split: a CTA of 4 warps takes a share of the 16-token blocks that a tile sees, its warps
+// every fourth; m, l and O are joined across warps in shared memory, and across CTAs by a
+// second kernel in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kv4_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kTile = 8;  // query rows of a tile
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleSlack = 8.0f;  // log2 units: keep a stale maximum while p <= 2^8
+
+// D = A (16 x 16, row) * B (16 x 8, col) + D, bf16 in, fp32 sums.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements held two to a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// The nibbles at bits 0-3 and 16-19 of x as a pair of bf16 numbers n - 8: 0x4300 | n is
+// 128 + n in bf16.
+__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t x) {
+  const uint32_t y = (x & 0x000f000fu) | 0x43004300u;
+  const __nv_bfloat162 z = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), __float2bfloat162_rn(136.f));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+__device__ __forceinline__ float scale_of(uint32_t par) { return __uint_as_float(par << 16); }
+__device__ __forceinline__ float low_of(uint32_t par) { return __uint_as_float(par & 0xffff0000u); }
+
+// Token of a block that row i of the score product stands for.
+__device__ __forceinline__ int token_of(int i) {
+  const int j = i & 7;
+  return (i & 8) + ((j & 1) ? 4 + ((j >> 1) ^ 1) : j >> 1);
+}
+
+// kN 32-bit words from shared or global memory, in the widest loads.
+template <int kN>
+__device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[kN]) {
+  if constexpr (kN == 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(src);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if constexpr (kN == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(src);
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(src);
+  }
+}
+
+// x as kTerms bf16 terms (packed in pairs with y): 1 rounds, 3 keep 24 bits.
+template <int kTerms>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&out)[kTerms]) {
+#pragma unroll
+  for (int n = 0; n < kTerms; ++n) {
+    out[n] = ptx::pack_bf16x2(x, y);
+    if (n + 1 < kTerms) {
+      x -= __uint_as_float(out[n] << 16);
+      y -= __uint_as_float(out[n] & 0xffff0000u);
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x) {
+  return (float)x;
+}
+
+// The blocks of a sequence that some row of its queries sees: the sinks' [0, first), then
+// from `from` on; n of them in all.
+struct Blocks {
+  int32_t first, from, n;
+};
+__device__ __forceinline__ Blocks blocks_of(const Kv4AttendParams& P, int32_t len) {
+  Blocks b;
+  const int32_t end = (len + kKvBlockRows - 1) / kKvBlockRows;
+  int64_t lo = 0;
+  if (P.window > 0) lo = (int64_t)len - P.rows - P.window + 1;
+  if (lo < 0) lo = 0;
+  b.from = (int32_t)(lo / kKvBlockRows);
+  const int32_t sink_rows = P.sinks < lo ? P.sinks : (int32_t)lo;
+  b.first = (sink_rows + kKvBlockRows - 1) / kKvBlockRows;
+  if (b.first > b.from) b.first = b.from;
+  b.n = b.first + (end - b.from);
+  return b;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4AttendParams P) {
+  using F = Kv4Block<D>;
+  constexpr int G = F::kGroups;
+  constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, c = lane & 3;
+  const int split = blockIdx.x, tile = blockIdx.y % P.tiles, h = blockIdx.y / P.tiles, b = blockIdx.z;
+  const int n_rows = P.group * P.rows;  // query rows of the head: row = group head * rows + token
+  const int row0 = tile * kTile;
+
+  int32_t len = __ldg(P.length + b);
+  if (len < 0 || len > P.t.width * P.t.page_rows) {
+    if (threadIdx.x == 0) atomicOr(P.t.status, kKv4StatusRange);
+    len = 0;
+  }
+  const Blocks blk = blocks_of(P, len);
+  const int32_t x_lo = (int32_t)((int64_t)blk.n * split / P.splits);
+  const int32_t x_hi = (int32_t)((int64_t)blk.n * (split + 1) / P.splits);
+
+  // Query fragments: lane (r, c) holds row r's channels 32g + 8c .. + 7 of every group, in
+  // the pairs (0,4), (1,5), (2,6), (3,7) that a word of codes yields.
+  uint32_t qf[G][4][kTerms];
+  float qs[G][2];  // sum of a group's channels for rows 2c and 2c + 1
+  {
+    const bool live = row0 + r < n_rows;
+    const T* qrow = static_cast<const T*>(P.q) + (((int64_t)b * P.heads_q + (int64_t)h * P.group) * P.rows + row0 + r) * D;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = live ? to_f(qrow[32 * g + 8 * c + i]) : 0.f;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        split_pair<kTerms>(x[i], x[i + 4], qf[g][i]);
+        sum += x[i] + x[i + 4];
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      qs[g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+      qs[g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+    }
+  }
+  // Positions of rows 2c and 2c + 1 (of the query), and the tokens of this lane's keys.
+  int32_t qpos[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) qpos[e] = len - P.rows + (row0 + 2 * c + e) % P.rows;
+  const int tok0 = token_of(r), tok1 = token_of(r + 8);
+  const int vt[4] = {token_of(2 * c), token_of(2 * c + 1), token_of(2 * c + 8), token_of(2 * c + 9)};
+
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[G][2][4];  // channels 32g + 4r + {0,1} and {2,3} of rows 2c, 2c + 1
+  float pm[G][2];    // sum of p * (middle of the value)
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    pm[g][0] = pm[g][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[g][i][e] = 0.f;
+  }
+
+  for (int32_t x = x_lo + warp; x < x_hi; x += kWarps) {
+    const int32_t block = x < blk.first ? x : blk.from + (x - blk.first);
+    const int32_t page_at = block / P.t.blocks_per_page;
+    const int32_t page = __ldg(P.t.page_table + (int64_t)b * P.t.width + page_at);
+    if (page < 0 || page >= P.t.pages) {
+      if (lane == 0) atomicOr(P.t.status, kKv4StatusRange);
+      continue;
+    }
+    const uint8_t* base = P.t.cache + (((int64_t)page * P.t.heads_kv + h) * P.t.blocks_per_page +
+                                       block % P.t.blocks_per_page) * F::kBytes;
+    uint32_t k0[G], k1[G], kp0[G], kp1[G], vp0[G], vp1[G], vw[4][G / 2];
+    load_words<G>(base + F::kOffK + tok0 * F::kCodeBytes + c * (4 * G), k0);
+    load_words<G>(base + F::kOffK + tok1 * F::kCodeBytes + c * (4 * G), k1);
+    load_words<G>(base + F::kOffKPar + tok0 * F::kParBytes, kp0);
+    load_words<G>(base + F::kOffKPar + tok1 * F::kParBytes, kp1);
+    load_words<G>(base + F::kOffVPar + tok0 * F::kParBytes, vp0);
+    load_words<G>(base + F::kOffVPar + tok1 * F::kParBytes, vp1);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) load_words<G / 2>(base + F::kOffV + vt[n] * F::kCodeBytes + r * (2 * G), vw[n]);
+
+    // Scores: s[0], s[1] of key tok0 for rows 2c, 2c + 1; s[2], s[3] of key tok1.
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {  // nibbles (i, i + 4) and (i + 1, i + 5) of the words
+        const uint32_t a[4] = {codes_bf16x2(k0[g] >> (4 * i)), codes_bf16x2(k1[g] >> (4 * i)),
+                               codes_bf16x2(k0[g] >> (4 * i + 4)), codes_bf16x2(k1[g] >> (4 * i + 4))};
+#pragma unroll
+        for (int n = kTerms - 1; n >= 0; --n) {
+          const uint32_t q2[2] = {qf[g][i][n], qf[g][i + 1][n]};
+          mma16816(acc, a, q2);
+        }
+      }
+      const float s0 = scale_of(kp0[g]), s1 = scale_of(kp1[g]);
+      const float m0 = fmaf(8.f, s0, low_of(kp0[g])), m1 = fmaf(8.f, s1, low_of(kp1[g]));
+      s[0] = fmaf(s0, acc[0], fmaf(m0, qs[g][0], s[0]));
+      s[1] = fmaf(s0, acc[1], fmaf(m0, qs[g][1], s[1]));
+      s[2] = fmaf(s1, acc[2], fmaf(m1, qs[g][0], s[2]));
+      s[3] = fmaf(s1, acc[3], fmaf(m1, qs[g][1], s[3]));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] *= P.scale_log2;
+
+    // Blocks that every row sees whole need no mask: they end at the first query or
+    // before, and begin within the last query's window (or lie in the sinks).
+    const int32_t key0 = block * kKvBlockRows;
+    bool seen[4] = {true, true, true, true};
+    const bool whole = key0 + 15 <= len - P.rows &&
+                       (P.window == 0 || key0 > len - 1 - P.window || key0 + 15 < P.sinks);
+    if (!whole) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int32_t j = key0 + (e < 2 ? tok0 : tok1), i = qpos[e & 1];
+        seen[e] = j <= i && (P.window == 0 || j > i - P.window || j < P.sinks);
+        if (!seen[e]) s[e] = -INFINITY;
+      }
+    }
+
+    // Running maximum, the same in all lanes of a row: moved only when a score exceeds it
+    // by the slack.
+    const bool grow = fmaxf(s[0], s[2]) > m[0] + kRescaleSlack || fmaxf(s[1], s[3]) > m[1] + kRescaleSlack;
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(s[e], s[e + 2]);
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        mx = fmaxf(mx, m[e]);
+        const float alpha = m[e] == -INFINITY ? 0.f : ptx::ex2_approx(m[e] - mx);
+        m[e] = mx;
+        l[e] *= alpha;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          pm[g][e] *= alpha;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            o[g][i][e] *= alpha;
+            o[g][i][e + 2] *= alpha;
+          }
+        }
+      }
+    }
+    float p[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float ref = m[e & 1] == -INFINITY ? 0.f : m[e & 1];
+      p[e] = ptx::ex2_approx(s[e] - ref);
+      l[e & 1] += p[e];
+    }
+
+    // O: per group, p times the value's scale as the 16 x 8 operand (keys x rows), the
+    // codes of two keys a register as the 16 x 16 one (channels x keys).
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float s0 = scale_of(vp0[g]), s1 = scale_of(vp1[g]);
+      const float m0 = fmaf(8.f, s0, low_of(vp0[g])), m1 = fmaf(8.f, s1, low_of(vp1[g]));
+      float w[4] = {p[0] * s0, p[1] * s0, p[2] * s1, p[3] * s1};
+      float y[4] = {p[0] * m0, p[1] * m0, p[2] * m1, p[3] * m1};
+      if (!whole) {  // what stands in places that are not seen may be anything
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!seen[e]) w[e] = y[e] = 0.f;
+      }
+      pm[g][0] += y[0] + y[2];
+      pm[g][1] += y[1] + y[3];
+      uint32_t w0[kTerms], w1[kTerms];
+      split_pair<kTerms>(w[0], w[1], w0);
+      split_pair<kTerms>(w[2], w[3], w1);
+      const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+      const uint32_t a01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
+      const uint32_t a23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
+      uint32_t a[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[i][0] = codes_bf16x2(a01 >> (8 * i));
+        a[i][1] = codes_bf16x2(a01 >> (8 * i + 4));
+        a[i][2] = codes_bf16x2(a23 >> (8 * i));
+        a[i][3] = codes_bf16x2(a23 >> (8 * i + 4));
+      }
+#pragma unroll
+      for (int n = kTerms - 1; n >= 0; --n) {
+        const uint32_t b2[2] = {transpose8(w0[n]), transpose8(w1[n])};
+        mma16816(o[g][0], a[0], b2);
+        mma16816(o[g][1], a[1], b2);
+      }
+    }
+  }
+
+  // Rows' sums over the lanes that held different keys.
+#pragma unroll
+  for (int d = 4; d <= 16; d <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+#pragma unroll
+      for (int g = 0; g < G; ++g) pm[g][e] += __shfl_xor_sync(0xffffffffu, pm[g][e], d);
+    }
+  }
+
+  // Join the warps.
+  __shared__ float sm_m[kWarps][kTile], sm_l[kWarps][kTile];
+  __shared__ __align__(16) float sm_o[kWarps][kTile][D + 4];
+  if (r == 0) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      sm_m[warp][2 * c + e] = m[e];
+      sm_l[warp][2 * c + e] = l[e];
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      *reinterpret_cast<float4*>(&sm_o[warp][2 * c + e][32 * g + 4 * r]) =
+          make_float4(o[g][0][e] + pm[g][e], o[g][0][e + 2] + pm[g][e], o[g][1][e] + pm[g][e], o[g][1][e + 2] + pm[g][e]);
+  __syncthreads();
+  const int64_t unit = ((int64_t)b * P.t.heads_kv + h) * P.tiles + tile;
+  for (int at = threadIdx.x; at < kTile * D; at += kWarps * 32) {
+    const int row = at / D, ch = at % D;
+    float mx = sm_m[0][row];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][row]);
+    float sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = sm_m[w][row] == -INFINITY ? 0.f : ptx::ex2_approx(sm_m[w][row] - mx);
+      // (a warp that saw nothing of this row holds zeros)
+      sum = fmaf(f, sm_l[w][row], sum);
+      acc = fmaf(f, sm_o[w][row][ch], acc);
+    }
+    if (P.splits > 1) {
+      const int64_t part = unit * P.splits + split;
+      P.part_o[(part * kTile + row) * D + ch] = acc;
+      if (ch == 0) P.part_ml[part * kTile + row] = make_float2(mx, sum);
+    } else if (row0 + row < n_rows) {
+      const int64_t out = ((int64_t)b * P.heads_q + (int64_t)h * P.group) * P.rows + row0 + row;
+      static_cast<T*>(P.o)[out * D + ch] = (T)(mx == -INFINITY ? 0.f : acc / sum);
+      if (ch == 0 && P.lse != nullptr) P.lse[out] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    }
+  }
+}
+
+// Joins the splits' parts of a tile, in order: one CTA per tile and row.
+template <typename T, int D>
+__global__ void __launch_bounds__(D) kv4_join_kernel(const Kv4AttendParams P) {
+  const int64_t unit = blockIdx.x;
+  const int row = blockIdx.y, ch = threadIdx.x;
+  const int tile = (int)(unit % P.tiles);
+  const int64_t bh = unit / P.tiles;
+  if (tile * kTile + row >= P.group * P.rows) return;
+  const float2* ml = P.part_ml + unit * P.splits * kTile + row;
+  const float* po = P.part_o + (unit * P.splits * kTile + row) * D + ch;
+  float mx = -INFINITY;
+  for (int s = 0; s < P.splits; ++s) mx = fmaxf(mx, ml[s * kTile].x);
+  float sum = 0.f, acc = 0.f;
+  for (int s = 0; s < P.splits; ++s) {
+    const float2 x = ml[s * kTile];
+    const float f = x.x == -INFINITY ? 0.f : ptx::ex2_approx(x.x - mx);
+    sum = fmaf(f, x.y, sum);
+    acc = fmaf(f, po[(int64_t)s * kTile * D], acc);
+  }
+  const int64_t out = bh * P.group * P.rows + tile * kTile + row;
+  static_cast<T*>(P.o)[out * D + ch] = (T)(mx == -INFINITY ? 0.f : acc / sum);
+  if (ch == 0 && P.lse != nullptr) P.lse[out] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
+template <typename T, int D>
+cudaError_t attend_as(const Kv4AttendParams& prm, cudaStream_t st) {
+  const dim3 grid((unsigned)prm.splits, (unsigned)(prm.t.heads_kv * prm.tiles), (unsigned)prm.t.batch);
+  kv4_attend_kernel<T, D><<<grid, kWarps * 32, 0, st>>>(prm);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || prm.splits == 1) return e;
+  const dim3 units((unsigned)((int64_t)prm.t.batch * prm.t.heads_kv * prm.tiles), kTile);
+  kv4_join_kernel<T, D><<<units, D, 0, st>>>(prm);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_attend(int dtype, int head_dim, const Kv4AttendParams& prm, cudaStream_t stream) {
+  if (dtype == RA_DTYPE_BF16)
+    return head_dim == 128 ? attend_as<__nv_bfloat16, 128>(prm, stream) : attend_as<__nv_bfloat16, 64>(prm, stream);
+  return head_dim == 128 ? attend_as<float, 128>(prm, stream) : attend_as<float, 64>(prm, stream);
+}
+
+}  // namespace ra

@@ -1,0 +1,69 @@
+// The 4-bit key/value cache (include/ra.h, ra_kv4_*): format and launchers.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "ra_internal.h"
+
+namespace ra {
+
+constexpr int kKvBlockRows = 16;  // tokens of a cache block
+
+// Offsets within a block of 16 tokens (20 * d bytes).
+template <int D>
+struct Kv4Block {
+  static constexpr int kGroups = D / 32;        // groups of 32 channels
+  static constexpr int kCodeBytes = D / 2;      // code bytes of a row
+  static constexpr int kParBytes = D / 8;       // parameter bytes of a row
+  static constexpr int kOffK = 0;
+  static constexpr int kOffKPar = 16 * kCodeBytes;
+  static constexpr int kOffV = kOffKPar + 16 * kParBytes;
+  static constexpr int kOffVPar = kOffV + 16 * kCodeBytes;
+  static constexpr int kBytes = kOffVPar + 16 * kParBytes;
+};
+
+// What write, read and attend share: the cache and its sequences.
+struct Kv4Table {
+  uint8_t* cache;
+  const int32_t* page_table;  // [batch, width]
+  int64_t width;
+  int64_t pages;
+  int32_t page_rows;
+  int32_t blocks_per_page;
+  int32_t batch, heads_kv;
+  uint32_t* status;
+};
+
+// Kernel-side status bit: an index of the page table, a length or a count out of range.
+constexpr uint32_t kKv4StatusRange = 1u;
+
+struct Kv4RowsParams {  // write, read
+  Kv4Table t;
+  int32_t rows;
+  const int32_t* first;
+  const int32_t* count;  // or nullptr: rows
+  int32_t zero_rest;     // read: rows that receive nothing become zeros
+};
+
+struct Kv4AttendParams {
+  Kv4Table t;
+  int32_t heads_q, group, rows;  // query rows per sequence
+  int32_t tiles;                 // 8-row query tiles per key/value head
+  int32_t splits;                // CTAs that share a tile's keys
+  int32_t window, sinks;         // window 0: the whole prefix
+  float scale_log2;
+  const int32_t* length;
+  const void* q;
+  void* o;
+  float* lse;      // or nullptr
+  float* part_o;   // [unit, split, 8, D], unit = (b * heads_kv + h) * tiles + tile (splits > 1)
+  float2* part_ml; // [unit, split, 8]: running maximum (log2 units) and sum
+};
+
+cudaError_t launch_kv4_write(int dtype, int head_dim, const Kv4RowsParams& prm, const void* k, const void* v,
+                             cudaStream_t stream);
+cudaError_t launch_kv4_read(int dtype, int head_dim, const Kv4RowsParams& prm, void* k, void* v, cudaStream_t stream);
+cudaError_t launch_kv4_attend(int dtype, int head_dim, const Kv4AttendParams& prm, cudaStream_t stream);
+
+}  // namespace ra

@@ -20,8 +20,9 @@
 #include <new>
 #include <vector>
 
-#include "ra_internal.h"
+#include "api_internal.h"
 #include "bwd_internal.h"
+#include "ra_internal.h"
 #include "win_internal.h"
 
 struct ra_plan_s {
@@ -61,14 +62,8 @@ struct ra_plan_s {
   ra::WinItem* d_win_items = nullptr;
   ra::WinGroup* d_win_groups = nullptr;
   ra::WinRange* d_win_ranges = nullptr;
-  // One event per stream the plan's kernels were queued on, recorded after the
-  // latest of them: ra_plan_destroy queues the frees of the device tables behind
-  // exactly this work.  A slot whose event has completed is reused for a new stream.
-  struct StreamMark {
-    cudaStream_t stream;
-    cudaEvent_t done;
-  };
-  std::vector<StreamMark> marks;
+  // ra_plan_destroy queues the frees of the device tables behind exactly this work.
+  std::vector<ra::StreamMark> marks;
 };
 
 namespace {
@@ -665,34 +660,7 @@ ra_status check_device(const ra_plan_s* plan) {
   return RA_OK;
 }
 
-// Record, on `st`, that the plan's device tables are in use by the work queued there
-// so far (ra_plan_destroy queues its frees behind it).
-ra_status mark_use(ra_plan_s* plan, cudaStream_t st) {
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) cudaGetLastError();
-  if (cap != cudaStreamCaptureStatusNone) return RA_OK;  // queued into a graph, not run yet
-  ra_plan_s::StreamMark* slot = nullptr;
-  for (ra_plan_s::StreamMark& m : plan->marks)
-    if (m.stream == st) slot = &m;
-  if (slot == nullptr)
-    for (ra_plan_s::StreamMark& m : plan->marks)
-      if (cudaEventQuery(m.done) == cudaSuccess) {  // that stream's use has ended
-        m.stream = st;
-        slot = &m;
-        break;
-      }
-  cudaGetLastError();  // a not-ready query is not an error
-  if (slot == nullptr) {
-    cudaEvent_t ev = nullptr;
-    const cudaError_t e = cudaEventCreateWithFlags(&ev, cudaEventDisableTiming);
-    if (e != cudaSuccess) return fail(RA_ERR_CUDA, "plan use event: %s", cudaGetErrorString(e));
-    plan->marks.push_back({st, ev});
-    slot = &plan->marks.back();
-  }
-  const cudaError_t e = cudaEventRecord(slot->done, st);
-  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "plan use event record: %s", cudaGetErrorString(e));
-  return RA_OK;
-}
+ra_status mark_use(ra_plan_s* plan, cudaStream_t st) { return ra::mark_use(&plan->marks, st); }
 
 size_t elem_bytes(const ra_problem& pb) { return pb.dtype == RA_DTYPE_BF16 ? 2 : 4; }
 
@@ -725,6 +693,33 @@ cudaError_t rotate_one(const ra_plan_s* plan, const void* src, void* dst, cudaSt
 }  // namespace
 
 void ra::set_last_error(const char* msg) { snprintf(g_err, sizeof(g_err), "%s", msg); }
+
+ra_status ra::mark_use(std::vector<StreamMark>* marks, cudaStream_t st) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) cudaGetLastError();
+  if (cap != cudaStreamCaptureStatusNone) return RA_OK;  // queued into a graph, not run yet
+  StreamMark* slot = nullptr;
+  for (StreamMark& m : *marks)
+    if (m.stream == st) slot = &m;
+  if (slot == nullptr)
+    for (StreamMark& m : *marks)
+      if (cudaEventQuery(m.done) == cudaSuccess) {  // that stream's use has ended
+        m.stream = st;
+        slot = &m;
+        break;
+      }
+  cudaGetLastError();  // a not-ready query is not an error
+  if (slot == nullptr) {
+    cudaEvent_t ev = nullptr;
+    const cudaError_t e = cudaEventCreateWithFlags(&ev, cudaEventDisableTiming);
+    if (e != cudaSuccess) return fail(RA_ERR_CUDA, "use event: %s", cudaGetErrorString(e));
+    marks->push_back({st, ev});
+    slot = &marks->back();
+  }
+  const cudaError_t e = cudaEventRecord(slot->done, st);
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "use event record: %s", cudaGetErrorString(e));
+  return RA_OK;
+}
 
 ra_status ra::check_on_current_device(const void* const* ptrs, int n, cudaStream_t stream) {
   int cur = -1;
@@ -818,14 +813,14 @@ ra_status ra_plan_destroy(ra_plan_t plan) {
     // status word: the frees are queued behind them (and only them), in stream
     // order, and the host does not wait.
     if (plan->mem_stream != nullptr) {
-      for (const ra_plan_s::StreamMark& m : plan->marks) cudaStreamWaitEvent(plan->mem_stream, m.done, 0);
+      for (const ra::StreamMark& m : plan->marks) cudaStreamWaitEvent(plan->mem_stream, m.done, 0);
       void* mem[] = {plan->d_items,     plan->d_step_items,  plan->d_bwd_items,   plan->d_gather_items,
                      plan->d_win_items, plan->d_win_groups, plan->d_win_ranges, plan->d_status};
       for (void* p : mem)
         if (p != nullptr) cudaFreeAsync(p, plan->mem_stream);
       cudaStreamDestroy(plan->mem_stream);  // released once its queued frees have run
     }
-    for (const ra_plan_s::StreamMark& m : plan->marks) cudaEventDestroy(m.done);
+    for (const ra::StreamMark& m : plan->marks) cudaEventDestroy(m.done);
     cudaGetLastError();
     if (plan->ev_entry) cudaEventDestroy(plan->ev_entry);
     if (plan->ev_rot) cudaEventDestroy(plan->ev_rot);

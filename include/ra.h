@@ -445,6 +445,131 @@ ra_status ra_fwd_static_status(void* stream);
  */
 ra_status ra_wait_selftest(uint32_t* status_out);
 
+/*
+ * ra_kv4_*: a paged key/value cache held in 4 bits, and the attention of new tokens over
+ * it.  No counterpart on the pages: after a prompt has gone through ring attention, its
+ * keys and values are kept here and the sequence is continued token by token.
+ *
+ * The cache is one caller-owned device buffer of ra_kv4_cache_size bytes, a pool of
+ * `pages` pages of `page_rows` tokens.  Position x of sequence b lies in page
+ * page_table[b][x / page_rows] of the pool, at row x % page_rows of it.  Page tables,
+ * lengths and counts are device arrays of int32, read by the kernels, so that a captured
+ * graph follows them.  Sequences may share pages for reading; a place is written by one
+ * row of a call only.
+ *
+ * Format.  A page holds, for each key/value head, page_rows / 16 blocks of 16 tokens; a
+ * block is 20 * d bytes: 16 rows of d/2 bytes of key codes, 16 rows of d/8 bytes of key
+ * parameters, the same for the values.  Every 32 channels of a row form a group with two
+ * bf16 parameters, scale then low (4 bytes a group, groups in order), computed in float32
+ * from the group's values x:
+ *   low = bf16(min x),  scale = bf16((max x - low) / 15), 0 when that is below 2^-100,
+ *   code = floor((x - low) / scale + 1/2) in exact arithmetic, held to 0..15 (0 when
+ *   scale is 0),  value = low + scale * code.
+ * A group with an infinity, a NaN or a range beyond float32 gets scale 0 and low NaN: all
+ * of it reads back as NaN.  Codes lie in little-endian nibbles of their row:
+ *   keys:   channel c is nibble c % 8 of 32-bit word (c % 32 / 8) * (d/32) + c / 32,
+ *   values: channel c is nibble c % 4 of 16-bit word (c % 32 / 4) * (d/32) + c / 32,
+ * the order in which the attention kernel's lanes take them.
+ *
+ * Page indices outside the pool, positions outside the page table and lengths or counts
+ * out of range are found by the kernels: such rows are not written, not read back and not
+ * attended to, and ra_kv4_sync_status reports
+ * them.
+ */
+typedef struct {
+  int64_t pages;      /* pages of the pool, >= 1                                    */
+  int32_t page_rows;  /* tokens of a page: a multiple of 16, 16..65536              */
+  int32_t heads_q;    /* Hq >= 1, multiple of heads_kv (ra_kv4_attend)              */
+  int32_t heads_kv;   /* Hkv >= 1                                                   */
+  int32_t head_dim;   /* d: 64 or 128                                               */
+  int32_t dtype;      /* ra_dtype of K, V, Q and O                                  */
+  int64_t window;     /* as ra_plan_window's; 0: the whole prefix                   */
+  int64_t sinks;      /* as ra_plan_window's                                        */
+  float scale;        /* score scale; 0 selects 1/sqrt(head_dim)                    */
+} ra_kv4_problem;
+
+typedef struct ra_kv4_s* ra_kv4_t;
+
+/*
+ * ra_kv4_plan -- validate a cache's description and create its handle, which owns a
+ * device status word and one event per stream its kernels were launched on (host-only
+ * without a device, as ra_plan).  Release it with ra_kv4_destroy.  One host thread at a
+ * time may use a handle; its calls may overlap on the GPU.
+ * Errors: RA_ERR_INVALID_ARG (null arguments, sizes < 1, page_rows, Hq % Hkv, window or
+ * sinks < 0, bad enum or scale), RA_ERR_UNSUPPORTED (head_dim, more than 2^31-1 pages,
+ * a cache beyond 2^62 bytes), RA_ERR_CUDA.
+ */
+ra_status ra_kv4_plan(const ra_kv4_problem* prob, ra_kv4_t* out);
+
+/* Release a handle (NULL is accepted).  It does not wait, as ra_plan_destroy. */
+ra_status ra_kv4_destroy(ra_kv4_t kv);
+
+/* Bytes of the cache buffer: pages * heads_kv * page_rows * d * 5/4.  Host only.
+ * Errors: RA_ERR_INVALID_ARG (null arguments). */
+ra_status ra_kv4_cache_size(ra_kv4_t kv, int64_t* bytes);
+
+/*
+ * ra_kv4_write -- quantise new keys and values into the cache.
+ * k, v: [batch, Hkv, rows, d] in the handle's dtype.  Row t of sequence b goes to
+ * position first[b] + t, for t < count[b] (count NULL: every row); later rows of a padded
+ * batch are not read.  Nothing else of the cache changes.
+ * page_table: [batch, table_width] int32; first, count: [batch] int32.
+ * Device pointers, 16-byte aligned (page_table, first, count: 4-byte).  Asynchronous on
+ * stream; allocates nothing.
+ * Errors: RA_ERR_INVALID_ARG (null/misaligned pointers, sizes < 1), RA_ERR_UNSUPPORTED
+ * (batch * Hkv * rows above 2^31-1, table_width * page_rows above 2^30),
+ * RA_ERR_NO_DEVICE, RA_ERR_CUDA.
+ */
+ra_status ra_kv4_write(ra_kv4_t kv, void* cache, int64_t batch, int64_t rows, const void* k, const void* v,
+                       const int32_t* page_table, int64_t table_width, const int32_t* first,
+                       const int32_t* count, void* stream);
+
+/*
+ * ra_kv4_read -- read keys and values back as what they stand for (low + scale * code,
+ * rounded once to the handle's dtype).
+ * k, v: [batch, Hkv, rows, d]; row t of sequence b receives position first[b] + t for
+ * t < count[b] (count NULL: every row).  Later rows stay as they were (zero_rest 0) or
+ * become zeros (1), and so do rows whose page or position is out of range.
+ * Everything else as for ra_kv4_write (zero_rest other than 0 or 1: RA_ERR_INVALID_ARG).
+ */
+ra_status ra_kv4_read(ra_kv4_t kv, const void* cache, int64_t batch, int64_t rows, const int32_t* page_table,
+                      int64_t table_width, const int32_t* first, const int32_t* count, int32_t zero_rest,
+                      void* k, void* v, void* stream);
+
+/*
+ * ra_kv4_attend -- attention of the last `rows` tokens of every sequence over its cached
+ * keys and values (the tokens' own among them: write them first).
+ * q, o: [batch, Hq, rows, d] in the handle's dtype; lse [batch, Hq, rows] float32 (may be
+ * NULL).  length: [batch] int32, the tokens of sequence b that the cache holds; query t
+ * sits at position length[b] - rows + t and sees the positions up to its own, within the
+ * handle's window and sinks.  A query that sees nothing (length 0, or a position before
+ * the first) gets O = 0, LSE = -inf.  Keys beyond a sequence's length are not looked at:
+ * what pages hold there does not matter.
+ * bf16: Q enters the products as it is and the softmax weights rounded to bf16, each
+ * times its value's scale; sums are fp32.  float32: both are split into three bf16 terms,
+ * which keeps fp32 accuracy.
+ * scratch: ra_kv4_attend_scratch_size bytes (NULL when that is 0), not shared by calls
+ * that may overlap.  Device pointers, 16-byte aligned (page_table, length: 4-byte).
+ * Asynchronous on stream; allocates nothing.
+ * Errors: as ra_kv4_write (batch, or Hkv times the 8-row query tiles, above 65535:
+ * RA_ERR_UNSUPPORTED).
+ */
+ra_status ra_kv4_attend(ra_kv4_t kv, const void* cache, int64_t batch, int64_t rows, const void* q,
+                        const int32_t* page_table, int64_t table_width, const int32_t* length, void* o,
+                        float* lse, float* scratch, void* stream);
+
+/* Bytes of ra_kv4_attend's scratch for these sizes (0 when it needs none).  Host only.
+ * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED as ra_kv4_attend. */
+ra_status ra_kv4_attend_scratch_size(ra_kv4_t kv, int64_t batch, int64_t rows, int64_t table_width,
+                                     int64_t* bytes);
+
+/*
+ * ra_kv4_sync_status -- synchronize `stream`, then read and clear the handle's status
+ * word: RA_ERR_INVALID_ARG when a call since the last one met a page index, position,
+ * length or count out of range, RA_ERR_CUDA on a CUDA error, RA_OK otherwise.
+ */
+ra_status ra_kv4_sync_status(ra_kv4_t kv, void* stream);
+
 /* Thread-local message describing the last failure on this thread ("" if none). */
 const char* ra_last_error(void);
 
