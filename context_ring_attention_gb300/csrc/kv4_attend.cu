@@ -1,20 +1,29 @@
 // Attention of a few new tokens per sequence over the 4-bit cache.
 //
 // For the query rows of one key/value head (rows of its group's heads and of the new
-// tokens, 8 to a tile) and the cached keys j that they see,
-//   s_j = sum_g [ ks_jg * sum_{c in g} q_c (n_jc - 8) + km_jg * sum_{c in g} q_c ],
-//   O   = sum_j p_j [ vs_jg * (n_jc - 8) + vm_jg ] / sum_j p_j,   p_j = e^(s_j - m),
-// with codes n, scales ks, vs and middles km = low + 8 * scale (also vm): the codes enter
-// the products as the integers -8..7, exact in bf16, and the parameters are applied per
-// group in fp32 -- to the 4 sums of a score, and to p before it is rounded for the second
-// product; the middles' share of O is a plain fp32 sum per group.  Centred codes keep the
+// tokens, 8 to a tile) and the cached keys j that they see, with codes n, scales ks, vs
+// and minima kl, vl of every group g of 32 channels,
+//   s_j = sum_g [ ks_jg * sum_{c in g} q_c n_jc + kl_jg * sum_{c in g} q_c ],
+//   O   = sum_j p_j [ vs_jg * (n_jc - 8) + (vl_jg + 8 vs_jg) ] / sum_j p_j,  p_j = e^(s_j - m).
+// The codes enter the products as exact integers and the parameters are applied per group
+// in fp32: to the 4 sums of a score, and to p before it is rounded for the second product;
+// the minima's share of O is a plain fp32 sum per group.  The values' codes are centred
+// (by a second product with the constant -8 and the same rounded p), which keeps the
 // rounding of p from being multiplied by the offset of the group.
 //
 // Bound by HBM at 20 * d bytes per 16 tokens and head.  The products are so few (8 query
 // rows) that the warp-level tensor instruction serves: m16n8k16 with the codes as the
 // 16-row operand -- keys x channels for the scores, channels x keys for the output -- and
-// the query rows as its 8 columns, so that nothing is computed for absent rows beyond 8,
-// and 4-bit codes become operand registers with one logical and one subtraction a pair.
+// the query rows as its 8 columns, so that nothing is computed for absent rows beyond 8.
+// What had to be made cheap is turning codes into operands (the first form, which made
+// bf16 n - 8 by a shift, a logical and a subtraction a pair, ran at 2.9 TB/s, bound by
+// those).  bf16 numbers whose top 8 bits are zero are the integers 0..255 times 2^-133,
+// subnormal below 128 and linear across the border, and the instruction takes them as they
+// are: a word of 8 codes yields 4 operand registers by one shift and 4 logicals, the codes
+// of the bytes' high nibbles standing for 16 n.  The other operands carry the powers of two
+// that bring the products back: the queries 2^E (E from the row's largest), the weights p
+// 2^kShift (an offset of the running maximum, which cancels in O / l).  Scales of value
+// groups from 2^-52 to 2^58 keep full precision that way.
 // Scores come out with keys in rows and are turned for the second product by an 8x8
 // transpose in registers.
 //
@@ -34,6 +43,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kTile = 8;  // query rows of a tile
+constexpr int kStages = 5;  // cache blocks a warp holds or has under way
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleSlack = 8.0f;  // log2 units: keep a stale maximum while p <= 2^8
 
@@ -51,13 +61,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// The nibbles at bits 0-3 and 16-19 of x as a pair of bf16 numbers n - 8: 0x4300 | n is
-// 128 + n in bf16.
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t x) {
-  const uint32_t y = (x & 0x000f000fu) | 0x43004300u;
-  const __nv_bfloat162 z = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), __float2bfloat162_rn(136.f));
-  return *reinterpret_cast<const uint32_t*>(&z);
-}
+// Pairs of codes as bf16 operands: n * 2^-133 from bits 0-3 and 16-19 of x, 16 n * 2^-133
+// from bits 4-7 and 20-23.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t x) { return x & 0x000f000fu; }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t x) { return x & 0x00f000f0u; }
+constexpr uint32_t kMinus8Lo = 0x80088008u, kMinus8Hi = 0x80808080u;  // the code -8 in both forms
+constexpr float kShift = 60.f;  // log2 of the factor that every p carries
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126..127
 __device__ __forceinline__ float scale_of(uint32_t par) { return __uint_as_float(par << 16); }
 __device__ __forceinline__ float low_of(uint32_t par) { return __uint_as_float(par & 0xffff0000u); }
 
@@ -67,7 +77,17 @@ __device__ __forceinline__ int token_of(int i) {
   return (i & 8) + ((j & 1) ? 4 + ((j >> 1) ^ 1) : j >> 1);
 }
 
-// kN 32-bit words from shared or global memory, in the widest loads.
+// 16 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// kN 32-bit words from shared memory, in the widest loads.
 template <int kN>
 __device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[kN]) {
   if constexpr (kN == 4) {
@@ -139,27 +159,52 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
   const int32_t x_hi = (int32_t)((int64_t)blk.n * (split + 1) / P.splits);
 
   // Query fragments: lane (r, c) holds row r's channels 32g + 8c .. + 7 of every group, in
-  // the pairs (0,4), (1,5), (2,6), (3,7) that a word of codes yields.
+  // the pairs (0,4), (1,5), (2,6), (3,7) that a word of codes yields, times 2^E; the pairs
+  // that meet 16 n are divided by 16.  E puts the row's largest channel at 2^119..2^120.
   uint32_t qf[G][4][kTerms];
-  float qs[G][2];  // sum of a group's channels for rows 2c and 2c + 1
+  float qs[G][2];   // sum of a group's channels for rows 2c and 2c + 1, in the products' unit 2^(E - 133)
+  float back[2];    // that unit's inverse, times the score scale (log2 units)
   {
     const bool live = row0 + r < n_rows;
     const T* qrow = static_cast<const T*>(P.q) + (((int64_t)b * P.heads_q + (int64_t)h * P.group) * P.rows + row0 + r) * D;
+    float x[G][8];
+    float top = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[g][i] = live ? to_f(qrow[32 * g + 8 * c + i]) : 0.f;
+        top = fmaxf(top, fabsf(x[g][i]));
+      }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // exponent of the largest channel (-126 for zeros and below); E in two factors
+    const int exp_top = max((int)(__float_as_uint(top) >> 23) - 127, -126);
+    const int e_row = 119 - exp_top;  // -9 .. 245
+    const float f0 = two_to(e_row / 2), f1 = two_to(e_row - e_row / 2);
+    float sums[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = live ? to_f(qrow[32 * g + 8 * c + i]) : 0.f;
+      for (int i = 0; i < 8; ++i) x[g][i] = x[g][i] * f0 * f1;
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        split_pair<kTerms>(x[i], x[i + 4], qf[g][i]);
-        sum += x[i] + x[i + 4];
+        const float f = (i & 1) ? 0.0625f : 1.f;
+        split_pair<kTerms>(x[g][i] * f, x[g][i + 4] * f, qf[g][i]);
+        sum += x[g][i] * two_to(-100) + x[g][i + 4] * two_to(-100);
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      qs[g][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
-      qs[g][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+      sums[g] = sum * two_to(-33);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int from = 8 * c + 4 * e;
+#pragma unroll
+      for (int g = 0; g < G; ++g) qs[g][e] = __shfl_sync(0xffffffffu, sums[g], from);
+      const int up = 133 - __shfl_sync(0xffffffffu, e_row, from);  // -112 .. 142
+      back[e] = P.scale_log2 * two_to(up / 2) * two_to(up - up / 2);
     }
   }
   // Positions of rows 2c and 2c + 1 (of the query), and the tokens of this lane's keys.
@@ -170,8 +215,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
   const int vt[4] = {token_of(2 * c), token_of(2 * c + 1), token_of(2 * c + 8), token_of(2 * c + 9)};
 
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float o[G][2][4];  // channels 32g + 4r + {0,1} and {2,3} of rows 2c, 2c + 1
-  float pm[G][2];    // sum of p * (middle of the value)
+  float o[G][2][4];  // channels 32g + 4r + {0,1} and {2,3} of rows 2c, 2c + 1 (the odd ones times 16)
+  float pm[G][2];    // sum of p * (middle of the group's range)
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     pm[g][0] = pm[g][1] = 0.f;
@@ -181,16 +226,65 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
       for (int e = 0; e < 4; ++e) o[g][i][e] = 0.f;
   }
 
-  for (int32_t x = x_lo + warp; x < x_hi; x += kWarps) {
-    const int32_t block = x < blk.first ? x : blk.from + (x - blk.first);
-    const int32_t page_at = block / P.t.blocks_per_page;
-    const int32_t page = __ldg(P.t.page_table + (int64_t)b * P.t.width + page_at);
-    if (page < 0 || page >= P.t.pages) {
-      if (lane == 0) atomicOr(P.t.status, kKv4StatusRange);
-      continue;
+  // Each warp brings its blocks through a ring of its own in shared memory, kStages - 1
+  // ahead of the one it works on.
+  extern __shared__ __align__(16) uint8_t ring[];
+  uint8_t* const mine = ring + warp * (kStages * F::kBytes);
+  const uint32_t mine_at = ptx::smem_addr(mine);
+  uint32_t bad = 0;  // stages whose page is out of range
+  auto block_at = [&](int32_t x) { return x < blk.first ? x : blk.from + (x - blk.first); };
+  // The fetched blocks' places in the page table are counted on; a division is made at the
+  // first and behind the sinks only.
+  const int32_t bpp = P.t.blocks_per_page;
+  const int32_t* table = P.t.page_table + (int64_t)b * P.t.width;
+  int32_t fx = x_lo + warp, page_at = 0, in_page = 0;
+  auto place = [&]() {
+    const int32_t block = block_at(fx);
+    page_at = block / bpp;
+    in_page = block - page_at * bpp;
+  };
+  place();
+  auto fetch = [&](int slot) {
+    if (fx < x_hi) {
+      const int32_t page = __ldg(table + page_at);
+      bad &= ~(1u << slot);
+      if (page < 0 || page >= P.t.pages) {
+        bad |= 1u << slot;
+        if (lane == 0) atomicOr(P.t.status, kKv4StatusRange);
+      } else {
+        const uint8_t* src = P.t.cache + (((int64_t)page * P.t.heads_kv + h) * bpp + in_page) * F::kBytes + lane * 16;
+        const uint32_t dst = mine_at + slot * F::kBytes + lane * 16;
+#pragma unroll
+        for (int i = 0; i * 512 < F::kBytes; ++i)
+          if (i * 512 + 512 <= F::kBytes || lane * 16 + i * 512 < F::kBytes) copy16(dst + i * 512, src + i * 512);
+      }
+      const bool crosses = fx < blk.first && fx + kWarps >= blk.first;
+      fx += kWarps;
+      in_page += kWarps;
+      if (crosses) {
+        place();
+      } else {
+        while (in_page >= bpp) {  // (at most kWarps times)
+          in_page -= bpp;
+          ++page_at;
+        }
+      }
     }
-    const uint8_t* base = P.t.cache + (((int64_t)page * P.t.heads_kv + h) * P.t.blocks_per_page +
-                                       block % P.t.blocks_per_page) * F::kBytes;
+    copies_commit();  // (an empty group where there is nothing to fetch)
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+
+  int slot = 0;
+  for (int32_t x = x_lo + warp; x < x_hi; x += kWarps) {
+    copies_wait<kStages - 2>();
+    __syncwarp();  // every lane's copies have landed, and every lane is done with the slot before
+    fetch(slot == 0 ? kStages - 1 : slot - 1);
+    const uint8_t* base = mine + slot * F::kBytes;
+    const bool skip = (bad >> slot) & 1u;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    if (skip) continue;
+    const int32_t block = block_at(x);
     uint32_t k0[G], k1[G], kp0[G], kp1[G], vp0[G], vp1[G], vw[4][G / 2];
     load_words<G>(base + F::kOffK + tok0 * F::kCodeBytes + c * (4 * G), k0);
     load_words<G>(base + F::kOffK + tok1 * F::kCodeBytes + c * (4 * G), k1);
@@ -208,23 +302,22 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {  // nibbles (i, i + 4) and (i + 1, i + 5) of the words
-        const uint32_t a[4] = {codes_bf16x2(k0[g] >> (4 * i)), codes_bf16x2(k1[g] >> (4 * i)),
-                               codes_bf16x2(k0[g] >> (4 * i + 4)), codes_bf16x2(k1[g] >> (4 * i + 4))};
+        const uint32_t x0 = k0[g] >> (4 * i), x1 = k1[g] >> (4 * i);
+        const uint32_t a[4] = {codes_lo(x0), codes_lo(x1), codes_hi(x0), codes_hi(x1)};
 #pragma unroll
         for (int n = kTerms - 1; n >= 0; --n) {
           const uint32_t q2[2] = {qf[g][i][n], qf[g][i + 1][n]};
           mma16816(acc, a, q2);
         }
       }
-      const float s0 = scale_of(kp0[g]), s1 = scale_of(kp1[g]);
-      const float m0 = fmaf(8.f, s0, low_of(kp0[g])), m1 = fmaf(8.f, s1, low_of(kp1[g]));
-      s[0] = fmaf(s0, acc[0], fmaf(m0, qs[g][0], s[0]));
-      s[1] = fmaf(s0, acc[1], fmaf(m0, qs[g][1], s[1]));
-      s[2] = fmaf(s1, acc[2], fmaf(m1, qs[g][0], s[2]));
-      s[3] = fmaf(s1, acc[3], fmaf(m1, qs[g][1], s[3]));
+      const float s0 = scale_of(kp0[g]), s1 = scale_of(kp1[g]), l0 = low_of(kp0[g]), l1 = low_of(kp1[g]);
+      s[0] = fmaf(s0, acc[0], fmaf(l0, qs[g][0], s[0]));
+      s[1] = fmaf(s0, acc[1], fmaf(l0, qs[g][1], s[1]));
+      s[2] = fmaf(s1, acc[2], fmaf(l1, qs[g][0], s[2]));
+      s[3] = fmaf(s1, acc[3], fmaf(l1, qs[g][1], s[3]));
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] *= P.scale_log2;
+    for (int e = 0; e < 4; ++e) s[e] *= back[e & 1];
 
     // Blocks that every row sees whole need no mask: they end at the first query or
     // before, and begin within the last query's window (or lie in the sinks).
@@ -268,7 +361,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
     float p[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float ref = m[e & 1] == -INFINITY ? 0.f : m[e & 1];
+      const float ref = m[e & 1] == -INFINITY ? 0.f : m[e & 1] - kShift;
       p[e] = ptx::ex2_approx(s[e] - ref);
       l[e & 1] += p[e];
     }
@@ -294,19 +387,24 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
       const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
       const uint32_t a01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
       const uint32_t a23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
+      const uint32_t minus8[4] = {kMinus8Lo, kMinus8Hi, kMinus8Lo, kMinus8Hi};
       uint32_t a[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        a[i][0] = codes_bf16x2(a01 >> (8 * i));
-        a[i][1] = codes_bf16x2(a01 >> (8 * i + 4));
-        a[i][2] = codes_bf16x2(a23 >> (8 * i));
-        a[i][3] = codes_bf16x2(a23 >> (8 * i + 4));
+        const uint32_t x01 = a01 >> (8 * i), x23 = a23 >> (8 * i);
+        a[i][0] = codes_lo(x01);
+        a[i][1] = codes_hi(x01);
+        a[i][2] = codes_lo(x23);
+        a[i][3] = codes_hi(x23);
       }
 #pragma unroll
       for (int n = kTerms - 1; n >= 0; --n) {
         const uint32_t b2[2] = {transpose8(w0[n]), transpose8(w1[n])};
-        mma16816(o[g][0], a[0], b2);
-        mma16816(o[g][1], a[1], b2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mma16816(o[g][i], a[i], b2);
+          mma16816(o[g][i], minus8, b2);
+        }
       }
     }
   }
@@ -322,22 +420,31 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
     }
   }
 
-  // Join the warps.
-  __shared__ float sm_m[kWarps][kTile], sm_l[kWarps][kTile];
-  __shared__ __align__(16) float sm_o[kWarps][kTile][D + 4];
+  // Join the warps, in the rings' memory.
+  copies_wait<0>();
+  __syncthreads();
+  using Row = float[D + 4];
+  static_assert(kWarps * kTile * (D + 4 + 2) * 4 <= kWarps * kStages * F::kBytes, "join area");
+  auto sm_o = reinterpret_cast<Row(*)[kTile]>(ring);
+  auto sm_m = reinterpret_cast<float(*)[kTile]>(ring + sizeof(Row) * kTile * kWarps);
+  auto sm_l = sm_m + kWarps;
   if (r == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       sm_m[warp][2 * c + e] = m[e];
-      sm_l[warp][2 * c + e] = l[e];
+      sm_l[warp][2 * c + e] = l[e] * two_to(-60);
     }
   }
 #pragma unroll
   for (int g = 0; g < G; ++g)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
+      // 2^-kShift brings p back, and another 2^133 (2^129 for 16 n) the codes
       *reinterpret_cast<float4*>(&sm_o[warp][2 * c + e][32 * g + 4 * r]) =
-          make_float4(o[g][0][e] + pm[g][e], o[g][0][e + 2] + pm[g][e], o[g][1][e] + pm[g][e], o[g][1][e + 2] + pm[g][e]);
+          make_float4(fmaf(o[g][0][e], two_to(73), pm[g][e] * two_to(-60)),
+                      fmaf(o[g][0][e + 2], two_to(69), pm[g][e] * two_to(-60)),
+                      fmaf(o[g][1][e], two_to(73), pm[g][e] * two_to(-60)),
+                      fmaf(o[g][1][e + 2], two_to(69), pm[g][e] * two_to(-60)));
   __syncthreads();
   const int64_t unit = ((int64_t)b * P.t.heads_kv + h) * P.tiles + tile;
   for (int at = threadIdx.x; at < kTile * D; at += kWarps * 32) {
@@ -391,9 +498,14 @@ __global__ void __launch_bounds__(D) kv4_join_kernel(const Kv4AttendParams P) {
 
 template <typename T, int D>
 cudaError_t attend_as(const Kv4AttendParams& prm, cudaStream_t st) {
+  constexpr int kSmem = kWarps * kStages * Kv4Block<D>::kBytes;
+  static std::atomic<int> ready[kMaxDevices];
+  const char* why = "";
+  cudaError_t e = prepare_once(kv4_attend_kernel<T, D>, ready, kWarps * 32, 0, kSmem, &why);
+  if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)prm.splits, (unsigned)(prm.t.heads_kv * prm.tiles), (unsigned)prm.t.batch);
-  kv4_attend_kernel<T, D><<<grid, kWarps * 32, 0, st>>>(prm);
-  cudaError_t e = cudaGetLastError();
+  kv4_attend_kernel<T, D><<<grid, kWarps * 32, kSmem, st>>>(prm);
+  e = cudaGetLastError();
   if (e != cudaSuccess || prm.splits == 1) return e;
   const dim3 units((unsigned)((int64_t)prm.t.batch * prm.t.heads_kv * prm.tiles), kTile);
   kv4_join_kernel<T, D><<<units, D, 0, st>>>(prm);
