@@ -27,13 +27,14 @@
 // Scores come out with keys in rows and are turned for the second product by an 8x8
 // transpose in registers.
 //
-// Split: a CTA of 4 warps takes a share of the 16-token blocks that a tile sees, its warps
-// every fourth; m, l and O are joined across warps in shared memory, and across CTAs by a
+// Split: a CTA of 4 warps takes a share of the 16-token blocks that a tile sees, each warp
+// a quarter; m, l and O are joined across warps in shared memory, and across CTAs by a
 // second kernel in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kv4_internal.h"
 #include "sm100_ptx.cuh"
@@ -54,6 +55,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// The same with zeros for D on the way in.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
 // Transpose of an 8 x 8 matrix of 16-bit elements held two to a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -232,51 +241,57 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
   uint8_t* const mine = ring + warp * (kStages * F::kBytes);
   const uint32_t mine_at = ptx::smem_addr(mine);
   uint32_t bad = 0;  // stages whose page is out of range
+  // A warp's blocks follow each other: their place is looked up in the page table at the
+  // first of each page, at the warp's first and behind the sinks.
+  const int32_t w_lo = x_lo + (int32_t)((int64_t)(x_hi - x_lo) * warp / kWarps);
+  const int32_t w_hi = x_lo + (int32_t)((int64_t)(x_hi - x_lo) * (warp + 1) / kWarps);
   auto block_at = [&](int32_t x) { return x < blk.first ? x : blk.from + (x - blk.first); };
-  // The fetched blocks' places in the page table are counted on; a division is made at the
-  // first and behind the sinks only.
   const int32_t bpp = P.t.blocks_per_page;
   const int32_t* table = P.t.page_table + (int64_t)b * P.t.width;
-  int32_t fx = x_lo + warp, page_at = 0, in_page = 0;
-  auto place = [&]() {
-    const int32_t block = block_at(fx);
-    page_at = block / bpp;
-    in_page = block - page_at * bpp;
-  };
-  place();
+  const int64_t page_bytes = (int64_t)P.t.heads_kv * bpp * F::kBytes;
+  const uint8_t* of_head = P.t.cache + (int64_t)h * bpp * F::kBytes + lane * 16;
+  const uint8_t* src = nullptr;  // the next block to fetch, or nullptr: its page is out of range
+  int32_t left = 0;              // blocks from there to the page's end or the sinks'
+  int32_t fx = w_lo;
   auto fetch = [&](int slot) {
-    if (fx < x_hi) {
-      const int32_t page = __ldg(table + page_at);
+    if (fx < w_hi) {
+      if (left == 0) {
+        const int32_t block = block_at(fx);
+        const int32_t page_at = block / bpp, in_page = block - page_at * bpp;
+        const int32_t page = __ldg(table + page_at);
+        src = of_head + page * page_bytes + (int64_t)in_page * F::kBytes;
+        left = bpp - in_page;
+        if (fx < blk.first) left = min(left, blk.first - fx);
+        if (page < 0 || page >= P.t.pages) {
+          src = nullptr;
+          if (lane == 0) atomicOr(P.t.status, kKv4StatusRange);
+        }
+      }
       bad &= ~(1u << slot);
-      if (page < 0 || page >= P.t.pages) {
+      if (src == nullptr) {
         bad |= 1u << slot;
-        if (lane == 0) atomicOr(P.t.status, kKv4StatusRange);
       } else {
-        const uint8_t* src = P.t.cache + (((int64_t)page * P.t.heads_kv + h) * bpp + in_page) * F::kBytes + lane * 16;
         const uint32_t dst = mine_at + slot * F::kBytes + lane * 16;
 #pragma unroll
         for (int i = 0; i * 512 < F::kBytes; ++i)
           if (i * 512 + 512 <= F::kBytes || lane * 16 + i * 512 < F::kBytes) copy16(dst + i * 512, src + i * 512);
+        src += F::kBytes;
       }
-      const bool crosses = fx < blk.first && fx + kWarps >= blk.first;
-      fx += kWarps;
-      in_page += kWarps;
-      if (crosses) {
-        place();
-      } else {
-        while (in_page >= bpp) {  // (at most kWarps times)
-          in_page -= bpp;
-          ++page_at;
-        }
-      }
+      --left;
+      ++fx;
     }
     copies_commit();  // (an empty group where there is nothing to fetch)
   };
+  // Blocks that every row sees whole need no mask: they end at the first query or before,
+  // and begin within the last query's window or lie in the sinks.
+  const int32_t whole_to = (len - P.rows + 1) >> 4;  // block + 1 <= this (arithmetic shift: may be negative)
+  const int32_t whole_from = P.window == 0 ? 0 : (max(len - P.window, 0) + 15) >> 4;
+  const int32_t whole_sinks = P.sinks >> 4;
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
   int slot = 0;
-  for (int32_t x = x_lo + warp; x < x_hi; x += kWarps) {
+  for (int32_t x = w_lo; x < w_hi; ++x) {
     copies_wait<kStages - 2>();
     __syncwarp();  // every lane's copies have landed, and every lane is done with the slot before
     fetch(slot == 0 ? kStages - 1 : slot - 1);
@@ -299,7 +314,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      float acc[4];
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {  // nibbles (i, i + 4) and (i + 1, i + 5) of the words
         const uint32_t x0 = k0[g] >> (4 * i), x1 = k1[g] >> (4 * i);
@@ -307,7 +322,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
 #pragma unroll
         for (int n = kTerms - 1; n >= 0; --n) {
           const uint32_t q2[2] = {qf[g][i][n], qf[g][i + 1][n]};
-          mma16816(acc, a, q2);
+          if (i == 0 && n == kTerms - 1) mma16816_first(acc, a, q2);
+          else mma16816(acc, a, q2);
         }
       }
       const float s0 = scale_of(kp0[g]), s1 = scale_of(kp1[g]), l0 = low_of(kp0[g]), l1 = low_of(kp1[g]);
@@ -319,16 +335,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] *= back[e & 1];
 
-    // Blocks that every row sees whole need no mask: they end at the first query or
-    // before, and begin within the last query's window (or lie in the sinks).
-    const int32_t key0 = block * kKvBlockRows;
     bool seen[4] = {true, true, true, true};
-    const bool whole = key0 + 15 <= len - P.rows &&
-                       (P.window == 0 || key0 > len - 1 - P.window || key0 + 15 < P.sinks);
+    const bool whole = block < whole_to && (block >= whole_from || block < whole_sinks);
     if (!whole) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int32_t j = key0 + (e < 2 ? tok0 : tok1), i = qpos[e & 1];
+        const int32_t j = block * kKvBlockRows + (e < 2 ? tok0 : tok1), i = qpos[e & 1];
         seen[e] = j <= i && (P.window == 0 || j > i - P.window || j < P.sinks);
         if (!seen[e]) s[e] = -INFINITY;
       }
@@ -368,45 +380,52 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
 
     // O: per group, p times the value's scale as the 16 x 8 operand (keys x rows), the
     // codes of two keys a register as the 16 x 16 one (channels x keys).
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const float s0 = scale_of(vp0[g]), s1 = scale_of(vp1[g]);
-      const float m0 = fmaf(8.f, s0, low_of(vp0[g])), m1 = fmaf(8.f, s1, low_of(vp1[g]));
-      float w[4] = {p[0] * s0, p[1] * s0, p[2] * s1, p[3] * s1};
-      float y[4] = {p[0] * m0, p[1] * m0, p[2] * m1, p[3] * m1};
-      if (!whole) {  // what stands in places that are not seen may be anything
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!seen[e]) w[e] = y[e] = 0.f;
-      }
-      pm[g][0] += y[0] + y[2];
-      pm[g][1] += y[1] + y[3];
-      uint32_t w0[kTerms], w1[kTerms];
-      split_pair<kTerms>(w[0], w[1], w0);
-      split_pair<kTerms>(w[2], w[3], w1);
-      const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
-      const uint32_t a01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
-      const uint32_t a23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
+    auto values = [&](auto masked) {
       const uint32_t minus8[4] = {kMinus8Lo, kMinus8Hi, kMinus8Lo, kMinus8Hi};
-      uint32_t a[2][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t x01 = a01 >> (8 * i), x23 = a23 >> (8 * i);
-        a[i][0] = codes_lo(x01);
-        a[i][1] = codes_hi(x01);
-        a[i][2] = codes_lo(x23);
-        a[i][3] = codes_hi(x23);
-      }
+      for (int g = 0; g < G; ++g) {
+        const float s0 = scale_of(vp0[g]), s1 = scale_of(vp1[g]);
+        const float m0 = fmaf(8.f, s0, low_of(vp0[g])), m1 = fmaf(8.f, s1, low_of(vp1[g]));
+        float w[4] = {p[0] * s0, p[1] * s0, p[2] * s1, p[3] * s1};
+        if (decltype(masked)::value) {  // what stands in places that are not seen may be anything
+          const float mid[4] = {m0, m0, m1, m1};
 #pragma unroll
-      for (int n = kTerms - 1; n >= 0; --n) {
-        const uint32_t b2[2] = {transpose8(w0[n]), transpose8(w1[n])};
+          for (int e = 0; e < 4; ++e) {
+            if (!seen[e]) w[e] = 0.f;
+            else pm[g][e & 1] = fmaf(p[e], mid[e], pm[g][e & 1]);
+          }
+        } else {
+          pm[g][0] = fmaf(p[0], m0, fmaf(p[2], m1, pm[g][0]));
+          pm[g][1] = fmaf(p[1], m0, fmaf(p[3], m1, pm[g][1]));
+        }
+        uint32_t w0[kTerms], w1[kTerms];
+        split_pair<kTerms>(w[0], w[1], w0);
+        split_pair<kTerms>(w[2], w[3], w1);
+        const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+        const uint32_t a01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
+        const uint32_t a23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
+        uint32_t a[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          mma16816(o[g][i], a[i], b2);
-          mma16816(o[g][i], minus8, b2);
+          const uint32_t x01 = a01 >> (8 * i), x23 = a23 >> (8 * i);
+          a[i][0] = codes_lo(x01);
+          a[i][1] = codes_hi(x01);
+          a[i][2] = codes_lo(x23);
+          a[i][3] = codes_hi(x23);
+        }
+#pragma unroll
+        for (int n = kTerms - 1; n >= 0; --n) {
+          const uint32_t b2[2] = {transpose8(w0[n]), transpose8(w1[n])};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma16816(o[g][i], a[i], b2);
+            mma16816(o[g][i], minus8, b2);
+          }
         }
       }
-    }
+    };
+    if (whole) values(std::false_type());
+    else values(std::true_type());
   }
 
   // Rows' sums over the lanes that held different keys.
