@@ -148,7 +148,7 @@ __device__ __forceinline__ Blocks blocks_of(const Kv4AttendParams& P, int32_t le
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4AttendParams P) {
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 1) kv4_attend_kernel(const Kv4AttendParams P) {
   using F = Kv4Block<D>;
   constexpr int G = F::kGroups;
   constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
   const int n_rows = P.group * P.rows;  // query rows of the head: row = group head * rows + token
   const int row0 = tile * kTile;
 
+  cudaTriggerProgrammaticLaunchCompletion();
   int32_t len = __ldg(P.length + b);
   if (len < 0 || len > P.t.width * P.t.page_rows) {
     if (threadIdx.x == 0) atomicOr(P.t.status, kKv4StatusRange);
@@ -171,8 +172,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
   // the pairs (0,4), (1,5), (2,6), (3,7) that a word of codes yields, times 2^E; the pairs
   // that meet 16 n are divided by 16.  E puts the row's largest channel at 2^119..2^120.
   uint32_t qf[G][4][kTerms];
-  float qs[G][2];   // sum of a group's channels for rows 2c and 2c + 1, in the products' unit 2^(E - 133)
-  float back[2];    // that unit's inverse, times the score scale (log2 units)
+  uint32_t qsum[4]; // sum of group c's channels of row r, in the scores' unit 2^(E - 133)
+  float back[2];    // that unit's inverse for rows 2c and 2c + 1, times the score scale (log2 units)
   {
     const bool live = row0 + r < n_rows;
     const T* qrow = static_cast<const T*>(P.q) + (((int64_t)b * P.heads_q + (int64_t)h * P.group) * P.rows + row0 + r) * D;
@@ -209,13 +210,34 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int from = 8 * c + 4 * e;
-#pragma unroll
-      for (int g = 0; g < G; ++g) qs[g][e] = __shfl_sync(0xffffffffu, sums[g], from);
-      const int up = 133 - __shfl_sync(0xffffffffu, e_row, from);  // -112 .. 142
+      const int up = 133 - __shfl_sync(0xffffffffu, e_row, 8 * c + 4 * e);  // -112 .. 142
       back[e] = P.scale_log2 * two_to(up / 2) * two_to(up - up / 2);
     }
+    // (0, sum of group c) in four bf16 terms; lanes beyond the groups stand for none
+    float mine_sum = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) mine_sum = c == g ? sums[g] : mine_sum;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      qsum[n] = ptx::pack_bf16x2(0.f, mine_sum);
+      mine_sum -= __uint_as_float(qsum[n] & 0xffff0000u);
+    }
   }
+  extern __shared__ __align__(16) uint8_t ring[];
+  // The fragments wait in shared memory, the same for all warps: registers are what bounds
+  // the warps of an SM.
+  uint32_t* const qsm = reinterpret_cast<uint32_t*>(ring + kWarps * kStages * F::kBytes);
+  if (warp == 0) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int n = 0; n < kTerms; ++n)
+        *reinterpret_cast<uint4*>(qsm + ((g * kTerms + n) * 32 + lane) * 4) =
+            make_uint4(qf[g][0][n], qf[g][1][n], qf[g][2][n], qf[g][3][n]);
+    }
+    *reinterpret_cast<uint4*>(qsm + G * kTerms * 32 * 4 + lane * 4) = make_uint4(qsum[0], qsum[1], qsum[2], qsum[3]);
+  }
+  __syncthreads();
   // Positions of rows 2c and 2c + 1 (of the query), and the tokens of this lane's keys.
   int32_t qpos[2];
 #pragma unroll
@@ -237,7 +259,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
 
   // Each warp brings its blocks through a ring of its own in shared memory, kStages - 1
   // ahead of the one it works on.
-  extern __shared__ __align__(16) uint8_t ring[];
   uint8_t* const mine = ring + warp * (kStages * F::kBytes);
   const uint32_t mine_at = ptx::smem_addr(mine);
   uint32_t bad = 0;  // stages whose page is out of range
@@ -305,32 +326,44 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
     load_words<G>(base + F::kOffK + tok1 * F::kCodeBytes + c * (4 * G), k1);
     load_words<G>(base + F::kOffKPar + tok0 * F::kParBytes, kp0);
     load_words<G>(base + F::kOffKPar + tok1 * F::kParBytes, kp1);
-    load_words<G>(base + F::kOffVPar + tok0 * F::kParBytes, vp0);
-    load_words<G>(base + F::kOffVPar + tok1 * F::kParBytes, vp1);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) load_words<G / 2>(base + F::kOffV + vt[n] * F::kCodeBytes + r * (2 * G), vw[n]);
 
-    // Scores: s[0], s[1] of key tok0 for rows 2c, 2c + 1; s[2], s[3] of key tok1.
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    // Scores: s[0], s[1] of key tok0 for rows 2c, 2c + 1; s[2], s[3] of key tok1.  The
+    // minima's part first, as products of their own: a parameter word is (scale, low) of
+    // key and group c, met by (0, sum of q) in bf16 terms.
+    float s[4];
+    {
+      uint32_t lw[2], qw[4];
+      lw[0] = *reinterpret_cast<const uint32_t*>(base + F::kOffKPar + tok0 * F::kParBytes + (c & (G - 1)) * 4);
+      lw[1] = *reinterpret_cast<const uint32_t*>(base + F::kOffKPar + tok1 * F::kParBytes + (c & (G - 1)) * 4);
+      load_words<4>(reinterpret_cast<const uint8_t*>(qsm + G * kTerms * 32 * 4 + lane * 4), qw);
+      const uint32_t a[4] = {lw[0], lw[1], lw[0], lw[1]};
+      const uint32_t b01[2] = {qw[0], qw[1]}, b23[2] = {qw[2], qw[3]};
+      mma16816_first(s, a, b23);
+      mma16816(s, a, b01);
+    }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       float acc[4];
+      uint32_t qg[kTerms][4];
+#pragma unroll
+      for (int n = 0; n < kTerms; ++n)
+        load_words<4>(reinterpret_cast<const uint8_t*>(qsm + ((g * kTerms + n) * 32 + lane) * 4), qg[n]);
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {  // nibbles (i, i + 4) and (i + 1, i + 5) of the words
         const uint32_t x0 = k0[g] >> (4 * i), x1 = k1[g] >> (4 * i);
         const uint32_t a[4] = {codes_lo(x0), codes_lo(x1), codes_hi(x0), codes_hi(x1)};
 #pragma unroll
         for (int n = kTerms - 1; n >= 0; --n) {
-          const uint32_t q2[2] = {qf[g][i][n], qf[g][i + 1][n]};
+          const uint32_t q2[2] = {qg[n][i], qg[n][i + 1]};
           if (i == 0 && n == kTerms - 1) mma16816_first(acc, a, q2);
           else mma16816(acc, a, q2);
         }
       }
-      const float s0 = scale_of(kp0[g]), s1 = scale_of(kp1[g]), l0 = low_of(kp0[g]), l1 = low_of(kp1[g]);
-      s[0] = fmaf(s0, acc[0], fmaf(l0, qs[g][0], s[0]));
-      s[1] = fmaf(s0, acc[1], fmaf(l0, qs[g][1], s[1]));
-      s[2] = fmaf(s1, acc[2], fmaf(l1, qs[g][0], s[2]));
-      s[3] = fmaf(s1, acc[3], fmaf(l1, qs[g][1], s[3]));
+      const float s0 = scale_of(kp0[g]), s1 = scale_of(kp1[g]);
+      s[0] = fmaf(s0, acc[0], s[0]);
+      s[1] = fmaf(s0, acc[1], s[1]);
+      s[2] = fmaf(s1, acc[2], s[2]);
+      s[3] = fmaf(s1, acc[3], s[3]);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] *= back[e & 1];
@@ -378,6 +411,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
       l[e & 1] += p[e];
     }
 
+    asm volatile("" ::: "memory");  // (the values' words are not held during the scores)
+    load_words<G>(base + F::kOffVPar + tok0 * F::kParBytes, vp0);
+    load_words<G>(base + F::kOffVPar + tok1 * F::kParBytes, vp1);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) load_words<G / 2>(base + F::kOffV + vt[n] * F::kCodeBytes + r * (2 * G), vw[n]);
     // O: per group, p times the value's scale as the 16 x 8 operand (keys x rows), the
     // codes of two keys a register as the 16 x 16 one (channels x keys).
     auto values = [&](auto masked) {
@@ -491,33 +529,78 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attend_kernel(const Kv4Attend
   }
 }
 
-// Joins the splits' parts of a tile, in order: one CTA per tile and row.
+// Joins the splits' parts of a row, in a fixed order: one CTA a row.  The splits' weights
+// 2^(m_s - m) come first, then D/4 lanes read a part's row, each warp every eighth split
+// (or every sixteenth half-warp) and the warps' sums are added.  A loop over the splits by
+// one thread a channel took 15 us for 64 splits; this takes 3.
+constexpr int kJoinWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(D) kv4_join_kernel(const Kv4AttendParams P) {
+__global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4AttendParams P) {
+  constexpr int kLanes = D / 4;                        // lanes of a part's row
+  constexpr int kParts = kJoinWarps * 32 / kLanes;     // parts read at a time
+  __shared__ float weight[kMaxSplits];
+  __shared__ float red[2][kJoinWarps];
+  __shared__ float4 sums[kParts][kLanes];
+  cudaGridDependencySynchronize();  // (the parts are written)
   const int64_t unit = blockIdx.x;
-  const int row = blockIdx.y, ch = threadIdx.x;
+  const int row = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = (int)(unit % P.tiles);
   const int64_t bh = unit / P.tiles;
   if (tile * kTile + row >= P.group * P.rows) return;
   const float2* ml = P.part_ml + unit * P.splits * kTile + row;
-  const float* po = P.part_o + (unit * P.splits * kTile + row) * D + ch;
+
   float mx = -INFINITY;
-  for (int s = 0; s < P.splits; ++s) mx = fmaxf(mx, ml[s * kTile].x);
-  float sum = 0.f, acc = 0.f;
-  for (int s = 0; s < P.splits; ++s) {
+  for (int s = threadIdx.x; s < P.splits; s += kJoinWarps * 32) mx = fmaxf(mx, ml[s * kTile].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  if (lane == 0) red[0][warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, red[0][w]);
+  float sum = 0.f;
+  for (int s = threadIdx.x; s < P.splits; s += kJoinWarps * 32) {
     const float2 x = ml[s * kTile];
     const float f = x.x == -INFINITY ? 0.f : ptx::ex2_approx(x.x - mx);
+    weight[s] = f;
     sum = fmaf(f, x.y, sum);
-    acc = fmaf(f, po[(int64_t)s * kTile * D], acc);
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (lane == 0) red[1][warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) sum += red[1][w];
+
+  const int part = threadIdx.x / kLanes, at = threadIdx.x % kLanes;
+  const float4* po = reinterpret_cast<const float4*>(P.part_o + (unit * P.splits * kTile + row) * D) + at;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = part; s < P.splits; s += kParts) {
+    const float f = weight[s];
+    const float4 x = po[(int64_t)s * (kTile * kLanes)];
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  }
+  sums[part][at] = acc;
+  __syncthreads();
   const int64_t out = bh * P.group * P.rows + tile * kTile + row;
-  static_cast<T*>(P.o)[out * D + ch] = (T)(mx == -INFINITY ? 0.f : acc / sum);
-  if (ch == 0 && P.lse != nullptr) P.lse[out] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  if (threadIdx.x < D) {
+    float y = 0.f;
+#pragma unroll
+    for (int n = 0; n < kParts; ++n) y += reinterpret_cast<const float*>(sums[n])[threadIdx.x];
+    static_cast<T*>(P.o)[out * D + threadIdx.x] = (T)(mx == -INFINITY ? 0.f : y / sum);
+  }
+  if (threadIdx.x == 0 && P.lse != nullptr) P.lse[out] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 template <typename T, int D>
 cudaError_t attend_as(const Kv4AttendParams& prm, cudaStream_t st) {
-  constexpr int kSmem = kWarps * kStages * Kv4Block<D>::kBytes;
+  constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
+  constexpr int kSmem = kWarps * kStages * Kv4Block<D>::kBytes + 32 * 16 * ((D / 32) * kTerms + 1);
   static std::atomic<int> ready[kMaxDevices];
   const char* why = "";
   cudaError_t e = prepare_once(kv4_attend_kernel<T, D>, ready, kWarps * 32, 0, kSmem, &why);
@@ -526,9 +609,19 @@ cudaError_t attend_as(const Kv4AttendParams& prm, cudaStream_t st) {
   kv4_attend_kernel<T, D><<<grid, kWarps * 32, kSmem, st>>>(prm);
   e = cudaGetLastError();
   if (e != cudaSuccess || prm.splits == 1) return e;
-  const dim3 units((unsigned)((int64_t)prm.t.batch * prm.t.heads_kv * prm.tiles), kTile);
-  kv4_join_kernel<T, D><<<units, D, 0, st>>>(prm);
-  return cudaGetLastError();
+  // The join's CTAs may be placed while the last of the others still run; they wait for
+  // the whole grid's results.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)prm.t.batch * prm.t.heads_kv * prm.tiles), kTile);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D>, prm);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace

@@ -46,6 +46,8 @@ struct Kv4RowsParams {  // write, read
   int32_t zero_rest;     // read: rows that receive nothing become zeros
 };
 
+constexpr int kMaxSplits = 1024;  // CTAs that share the keys of a query tile
+
 struct Kv4AttendParams {
   Kv4Table t;
   int32_t heads_q, group, rows;  // query rows per sequence
