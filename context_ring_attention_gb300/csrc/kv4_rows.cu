@@ -6,7 +6,11 @@
 //
 // One thread holds 8 consecutive channels of a key or value row: the 8 nibbles of one
 // 32-bit word of key codes, or two 16-bit words of value codes; four threads share a
-// group, and its minimum and maximum take two exchanges among them.
+// group, and its minimum and maximum take two exchanges among them.  A warp takes a run of
+// tokens of one head, all their loads first, and counts its place in the cache on from
+// token to token.  What bounds a plain form is not memory but the arithmetic of a code, so
+// it is kept to about a dozen instructions: rounding by adding 1.5 * 2^23, codes packed by
+// a multiply-add each, and the exact decision taken only next to a border of two codes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -20,20 +24,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Place of position `pos` of sequence b: the byte offset of its block for head h, or -1
-// (out of range, reported through the status word).
-__device__ __forceinline__ int64_t block_of(const Kv4Table& t, int b, int h, int64_t pos, int block_bytes) {
-  const int64_t page_at = pos / t.page_rows;
-  int32_t page = -1;
-  if (pos >= 0 && page_at < t.width) page = __ldg(t.page_table + (int64_t)b * t.width + page_at);
-  if (page < 0 || page >= t.pages) {
-    atomicOr(t.status, kKv4StatusRange);
-    return -1;
-  }
-  const int32_t block = (int32_t)(pos % t.page_rows) / kKvBlockRows;
-  return (((int64_t)page * t.heads_kv + h) * t.blocks_per_page + block) * block_bytes;
-}
-
 // Rows of sequence b that take part: count[b], or all.  A count out of range is reported
 // and takes none.
 __device__ __forceinline__ int32_t live_rows(const Kv4RowsParams& p, int b) {
@@ -44,25 +34,36 @@ __device__ __forceinline__ int32_t live_rows(const Kv4RowsParams& p, int b) {
   return 0;
 }
 
+// The 8 values of a thread as they come from memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* src, float (&x)[8]);
+struct Raw;
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* src, float (&x)[8]) {
-  const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src));
-  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+struct Raw<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* src) { w = __ldcs(reinterpret_cast<const uint4*>(src)); }
+  __device__ __forceinline__ void clear() { w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(a[i] << 16);
-    x[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(a[i] << 16);
+      x[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    }
   }
-}
+};
 template <>
-__device__ __forceinline__ void load8<float>(const float* src, float (&x)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(src));
-  const float4 b = __ldcs(reinterpret_cast<const float4*>(src) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
+struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* src) {
+    a = __ldcs(reinterpret_cast<const float4*>(src));
+    b = __ldcs(reinterpret_cast<const float4*>(src) + 1);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
 template <typename T>
 __device__ __forceinline__ void store8(T* dst, const float (&x)[8]);
 template <>
@@ -78,11 +79,17 @@ __device__ __forceinline__ void store8<float>(float* dst, const float (&x)[8]) {
 
 __device__ __forceinline__ float bf16_round(float x) { return __uint_as_float(ptx::pack_bf16x2(x, 0.f) << 16); }
 
-// Code of x: the border of two codes is decided exactly.  d + e is x - low without error
-// (the two terms of a floating-point sum), the quotient's floor is off by one at most, and
+// 1.5 * 2^23: a float of magnitude below 2^22 added to it is rounded to an integer, which
+// stands in the sum's low bits.
+constexpr float kRound = 12582912.f;
+constexpr uint32_t kRoundBits = 0x4B400000u;
+
+// Code of x, decided exactly where the quotient lies next to a border of two codes.
+// d + e is x - low without error (the two terms of a floating-point sum); the quotient
+// d * inv is off by 2^-22 of itself at most, so its floor is right or one off, and
 // r = d - c * scale is exact: c * scale has 12 bits, and the difference is a multiple of
-// the last place of d and smaller than d's leading bits.
-__device__ __forceinline__ uint32_t code_of(float x, float low, float scale, float inv) {
+// the last place of d and smaller than d.
+__device__ __noinline__ uint32_t code_at_border(float x, float low, float scale, float inv) {
   const float d = x - low;
   const float bb = d - x;
   const float e = (x - (d - bb)) + (-low - bb);
@@ -94,21 +101,55 @@ __device__ __forceinline__ uint32_t code_of(float x, float low, float scale, flo
   return (uint32_t)fminf(fmaxf(c, 0.f), 15.f);
 }
 
-// One group's parameters from the 8 values of each of four neighbouring lanes.
-__device__ __forceinline__ void group_params(const float (&x)[8], float& scale, float& low) {
-  float lo = x[0], hi = x[0];
-  bool fine = true;
+// The 8 codes of a thread, first in the lowest nibble.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float low, float scale) {
+  if (!(scale > 0.f)) return 0u;
+  const float inv = __frcp_rn(scale);
+  uint32_t word = 0, near_any = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    fine = fine && fabsf(x[i]) <= 3.402823466e38f;  // false for a NaN as well
+  for (int i = 7; i >= 0; --i) {
+    const float v = fminf(fmaxf((x[i] - low) * inv, 0.f), 15.f);
+    const float r = v + kRound;
+    const float off = v - (r - kRound);
+    near_any |= (fabsf(off) > 0.5f - 0x1p-14f) ? 1u << i : 0u;
+    word = word * 16u + __float_as_uint(r);  // (the constant's share is taken off below)
   }
-  if (!fine) lo = -INFINITY;  // makes the scale infinite below
+  // sum over i of kRoundBits * 16^i: only its lowest nibble positions reach 32 bits
+  constexpr uint32_t kShare = kRoundBits * 0x11111111u;
+  word -= kShare;
+  while (near_any) {
+    const int i = __ffs(near_any) - 1;
+    near_any &= near_any - 1;
+    float xi = x[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) xi = k == i ? x[k] : xi;
+    word = (word & ~(15u << (4 * i))) | (code_at_border(xi, low, scale, inv) << (4 * i));
+  }
+  return word;
+}
+
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// One group's parameters from the 8 values of each of four neighbouring lanes.  The minimum
+// and maximum pass a NaN on, and an infinity makes the range infinite: either way the scale
+// is not finite.
+__device__ __forceinline__ void group_params(const float (&x)[8], float& scale, float& low) {
+  float lo = min3_nan(min3_nan(x[0], x[1], x[2]), min3_nan(x[3], x[4], x[5]), fminf(x[6], x[7]));
+  float hi = max3_nan(max3_nan(x[0], x[1], x[2]), max3_nan(x[3], x[4], x[5]), max3_nan(x[6], x[7], x[7]));
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    const float h = __shfl_xor_sync(0xffffffffu, hi, o);
+    hi = max3_nan(hi, h, h);
   }
   low = bf16_round(lo);
   scale = bf16_round(__fdiv_rn(hi - low, 15.f));
@@ -122,129 +163,182 @@ __device__ __forceinline__ void group_params(const float (&x)[8], float& scale, 
 
 // Thread layout of a row pair (the K and the V row of one token and head): D/8 lanes for
 // K, then D/8 for V.
-template <int D>
+template <typename T, int D>
 struct Lanes {
-  static constexpr int kRow = D / 8;    // lanes of a row
-  static constexpr int kPair = D / 4;   // lanes of a token and head: 32 or 16
-  static constexpr int kPerBlock = kThreads / kPair;
+  static constexpr int kRow = D / 8;            // lanes of a row
+  static constexpr int kPair = D / 4;           // lanes of a token and head: 32 or 16
+  static constexpr int kAtOnce = 32 / kPair;    // tokens of a warp at a time
+  static constexpr int kSteps = sizeof(T) == 2 ? 8 : 4;
+  static constexpr int kRun = kAtOnce * kSteps;  // tokens of a warp
+};
+
+// The run of tokens of one sequence and head that a warp takes, and the lane's place in it.
+// The place is counted on from token to token; the page table is asked once a page.
+template <typename T, int D>
+struct Run {
+  using L = Lanes<T, D>;
+  static constexpr int kBlockBytes = Kv4Block<D>::kBytes;
+  const Kv4Table& tb;
+  bool any;          // the warp has a token
+  int b, h, t;       // the lane's current token t; the next one is kAtOnce further
+  int live;          // tokens of the sequence that take part
+  int64_t row;       // row of the first token in [batch, heads, rows]
+  uint8_t* base;     // block of the current token (nullptr: out of range)
+  int row16;         // its row there
+  int blocks;        // blocks from there to the page's end
+  int64_t page_at;   // place in the page table (-1: before the first position)
+
+  __device__ __forceinline__ explicit Run(const Kv4RowsParams& P) : tb(P.t) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t per = (uint32_t)(P.rows + L::kRun - 1) / L::kRun;  // runs of a sequence and head
+    const uint32_t id = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t bh = id / per;
+    any = bh < (uint32_t)P.t.batch * (uint32_t)P.t.heads_kv;
+    b = any ? (int)(bh / (uint32_t)P.t.heads_kv) : 0;
+    h = (int)(bh - (uint32_t)b * (uint32_t)P.t.heads_kv);
+    t = (int)(id - bh * per) * L::kRun + lane / L::kPair;
+    live = any ? live_rows(P, b) : 0;
+    row = (int64_t)bh * P.rows + t;
+    base = nullptr;
+    row16 = blocks = 0;
+    page_at = -1;
+    if (t >= live) return;
+    const int32_t f = __ldg(P.first + b);
+    int32_t in_page = 0;
+    if (f >= 0) {
+      const uint32_t pos = (uint32_t)f + (uint32_t)t;  // (below 2^32)
+      page_at = pos / (uint32_t)tb.page_rows;
+      in_page = (int32_t)(pos - (uint32_t)page_at * (uint32_t)tb.page_rows);
+    }
+    row16 = in_page % kKvBlockRows;
+    turn(in_page / kKvBlockRows);
+  }
+  // Look the current page up; its current block is number `block`.
+  __device__ __forceinline__ void turn(int block) {
+    int32_t page = -1;
+    if (page_at >= 0 && page_at < tb.width) page = __ldg(tb.page_table + (int64_t)b * tb.width + page_at);
+    base = nullptr;
+    blocks = tb.blocks_per_page - block;
+    if (page < 0 || page >= tb.pages) atomicOr(tb.status, kKv4StatusRange);
+    else base = tb.cache + (((int64_t)page * tb.heads_kv + h) * tb.blocks_per_page + block) * kBlockBytes;
+  }
+  __device__ __forceinline__ void advance() {
+    t += L::kAtOnce;
+    row16 += L::kAtOnce;
+    if (row16 < kKvBlockRows) return;
+    row16 -= kKvBlockRows;
+    if (--blocks > 0) {
+      if (base != nullptr) base += kBlockBytes;
+    } else if (t < live) {
+      if (page_at >= 0) ++page_at;
+      turn(0);
+    }
+  }
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
     kv4_write_kernel(const Kv4RowsParams P, const T* __restrict__ k, const T* __restrict__ v) {
-  using L = Lanes<D>;
+  using L = Lanes<T, D>;
   using F = Kv4Block<D>;
   constexpr int G = F::kGroups;
-  const int64_t pairs = (int64_t)P.t.batch * P.t.heads_kv * P.rows;
-  const int64_t pair = (int64_t)blockIdx.x * L::kPerBlock + threadIdx.x / L::kPair;
+  Run<T, D> run(P);
+  if (!run.any) return;  // (whole warps)
   const int at = threadIdx.x % L::kPair;
   const bool is_v = at >= L::kRow;
   const int i8 = at % L::kRow;  // channels 8*i8 .. 8*i8 + 7
   const int g = i8 / 4, c = i8 % 4;
-  int64_t base = -1;
-  int64_t pos = 0;
-  float x[8];
+  const T* src = (is_v ? v : k) + run.row * D + i8 * 8;
+  Raw<T> raw[L::kSteps];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.f;
-  if (pair < pairs) {
-    const int t = (int)(pair % P.rows);
-    const int bh = (int)(pair / P.rows), b = bh / P.t.heads_kv, h = bh % P.t.heads_kv;
-    if (t < live_rows(P, b)) {
-      const int32_t f = __ldg(P.first + b);
-      pos = f < 0 ? -1 : (int64_t)f + t;
-      base = block_of(P.t, b, h, pos, F::kBytes);
-      if (base >= 0) load8<T>((is_v ? v : k) + pair * D + i8 * 8, x);
+  for (int n = 0; n < L::kSteps; ++n)
+    if (run.t + n * L::kAtOnce < run.live) raw[n].load(src + (int64_t)n * L::kAtOnce * D);
+    else raw[n].clear();
+  // Values: a lane holds the 16-bit words of chunks 2c (low half) and 2c + 1 (high half)
+  // for group g; with the lane of the neighbouring group (4 lanes on) it makes whole 32-bit
+  // words: the even group's lane chunk 2c, the odd group's chunk 2c + 1.
+  const uint32_t at_word = is_v ? (2 * c + (g & 1)) * (G / 2) + g / 2 : c * G + g;
+#pragma unroll
+  for (int n = 0; n < L::kSteps; ++n) {
+    if (__all_sync(0xffffffffu, run.t >= run.live)) break;
+    float x[8];
+    raw[n].values(x);
+    float scale, low;
+    group_params(x, scale, low);  // (every lane takes part in the exchanges)
+    uint32_t word = codes_of(x, low, scale);
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
+    if (run.t < run.live && run.base != nullptr) {
+      uint8_t* blk = run.base;
+      if (is_v) word = (g & 1) ? (other >> 16) | (word & 0xffff0000u) : (word & 0xffffu) | (other << 16);
+      reinterpret_cast<uint32_t*>(blk + (is_v ? F::kOffV : F::kOffK) + run.row16 * F::kCodeBytes)[at_word] = word;
+      if (c == 0)
+        reinterpret_cast<uint32_t*>(blk + (is_v ? F::kOffVPar : F::kOffKPar) + run.row16 * F::kParBytes)[g] =
+            (__float_as_uint(scale) >> 16) | (__float_as_uint(low) & 0xffff0000u);
     }
+    run.advance();
   }
-  // (every lane takes part in the exchanges)
-  float scale, low;
-  group_params(x, scale, low);
-  uint32_t word = 0;
-  if (scale > 0.f) {
-    const float inv = __frcp_rn(scale);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) word |= code_of(x[i], low, scale, inv) << (4 * i);
-  }
-  // Values: this lane holds the 16-bit words of chunks 2c (low half) and 2c + 1 (high
-  // half) for group g; with the lane of the neighbouring group (4 lanes on) it makes whole
-  // 32-bit words: the even group's lane chunk 2c, the odd group's chunk 2c + 1.
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
-  if (base < 0) return;
-  const int row = (int)(pos % kKvBlockRows);
-  uint8_t* blk = P.t.cache + base;
-  uint32_t at_word;
-  if (is_v) {
-    word = (g & 1) ? (other >> 16) | (word & 0xffff0000u) : (word & 0xffffu) | (other << 16);
-    at_word = (2 * c + (g & 1)) * (G / 2) + g / 2;
-  } else {
-    at_word = c * G + g;
-  }
-  reinterpret_cast<uint32_t*>(blk + (is_v ? F::kOffV : F::kOffK) + row * F::kCodeBytes)[at_word] = word;
-  if (c == 0)
-    reinterpret_cast<uint32_t*>(blk + (is_v ? F::kOffVPar : F::kOffKPar) + row * F::kParBytes)[g] =
-        (__float_as_uint(scale) >> 16) | (__float_as_uint(low) & 0xffff0000u);
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4RowsParams P, T* __restrict__ k, T* __restrict__ v) {
-  using L = Lanes<D>;
+  using L = Lanes<T, D>;
   using F = Kv4Block<D>;
   constexpr int G = F::kGroups;
-  const int64_t pairs = (int64_t)P.t.batch * P.t.heads_kv * P.rows;
-  const int64_t pair = (int64_t)blockIdx.x * L::kPerBlock + threadIdx.x / L::kPair;
-  if (pair >= pairs) return;
+  Run<T, D> run(P);
+  if (!run.any) return;
   const int at = threadIdx.x % L::kPair;
   const bool is_v = at >= L::kRow;
   const int i8 = at % L::kRow, g = i8 / 4, c = i8 % 4;
-  const int t = (int)(pair % P.rows);
-  const int bh = (int)(pair / P.rows), b = bh / P.t.heads_kv, h = bh % P.t.heads_kv;
-  int64_t base = -1, pos = 0;
-  if (t < live_rows(P, b)) {
-    const int32_t f = __ldg(P.first + b);
-    pos = f < 0 ? -1 : (int64_t)f + t;
-    base = block_of(P.t, b, h, pos, F::kBytes);
-  }
-  T* dst = (is_v ? v : k) + pair * D + i8 * 8;
-  float x[8];
-  if (base < 0) {
-    if (!P.zero_rest) return;
+  T* dst = (is_v ? v : k) + run.row * D + i8 * 8;
+  const int t0 = run.t;
+  uint32_t word[L::kSteps], par[L::kSteps];
+  uint32_t have = 0;  // steps whose token is read
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    store8<T>(dst, x);
-    return;
+  for (int n = 0; n < L::kSteps; ++n) {
+    word[n] = par[n] = 0;
+    if (run.t < run.live && run.base != nullptr) {
+      have |= 1u << n;
+      const uint8_t* codes = run.base + (is_v ? F::kOffV : F::kOffK) + run.row16 * F::kCodeBytes;
+      if (is_v) {
+        const uint16_t* half = reinterpret_cast<const uint16_t*>(codes);
+        word[n] = half[(2 * c) * G + g] | ((uint32_t)half[(2 * c + 1) * G + g] << 16);
+      } else {
+        word[n] = reinterpret_cast<const uint32_t*>(codes)[c * G + g];
+      }
+      par[n] = reinterpret_cast<const uint32_t*>(run.base + (is_v ? F::kOffVPar : F::kOffKPar) + run.row16 * F::kParBytes)[g];
+    }
+    run.advance();
   }
-  const int row = (int)(pos % kKvBlockRows);
-  const uint8_t* blk = P.t.cache + base;
-  const uint8_t* codes = blk + (is_v ? F::kOffV : F::kOffK) + row * F::kCodeBytes;
-  uint32_t word;
-  if (is_v) {
-    const uint16_t* half = reinterpret_cast<const uint16_t*>(codes);
-    word = half[(2 * c) * G + g] | ((uint32_t)half[(2 * c + 1) * G + g] << 16);
-  } else {
-    word = reinterpret_cast<const uint32_t*>(codes)[c * G + g];
-  }
-  const uint32_t par =
-      reinterpret_cast<const uint32_t*>(blk + (is_v ? F::kOffVPar : F::kOffKPar) + row * F::kParBytes)[g];
-  const float scale = __uint_as_float(par << 16), low = __uint_as_float(par & 0xffff0000u);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(scale, (float)((word >> (4 * i)) & 15u), low);
-  store8<T>(dst, x);
+  for (int n = 0; n < L::kSteps; ++n) {
+    if (t0 + n * L::kAtOnce >= P.rows) break;
+    const float scale = __uint_as_float(par[n] << 16), low = __uint_as_float(par[n] & 0xffff0000u);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // 2^23 + code, without a conversion
+      const float code = __uint_as_float(((word[n] >> (4 * i)) & 15u) | 0x4B000000u) - 8388608.f;
+      x[i] = fmaf(scale, code, low);
+    }
+    if (((have >> n) & 1u) || P.zero_rest) store8<T>(dst + (int64_t)n * L::kAtOnce * D, x);
+  }
 }
 
-template <int D>
+template <typename T, int D>
 unsigned grid_of(const Kv4RowsParams& prm) {
-  const int64_t pairs = (int64_t)prm.t.batch * prm.t.heads_kv * prm.rows;
-  return (unsigned)((pairs + Lanes<D>::kPerBlock - 1) / Lanes<D>::kPerBlock);
+  const int64_t run = Lanes<T, D>::kRun, warps = kThreads / 32;
+  const int64_t runs = (int64_t)prm.t.batch * prm.t.heads_kv * ((prm.rows + run - 1) / run);
+  return (unsigned)((runs + warps - 1) / warps);
 }
 
 template <typename T, int D>
 cudaError_t write_as(const Kv4RowsParams& prm, const void* k, const void* v, cudaStream_t st) {
-  kv4_write_kernel<T, D><<<grid_of<D>(prm), kThreads, 0, st>>>(prm, static_cast<const T*>(k), static_cast<const T*>(v));
+  kv4_write_kernel<T, D><<<grid_of<T, D>(prm), kThreads, 0, st>>>(prm, static_cast<const T*>(k), static_cast<const T*>(v));
   return cudaGetLastError();
 }
 template <typename T, int D>
 cudaError_t read_as(const Kv4RowsParams& prm, void* k, void* v, cudaStream_t st) {
-  kv4_read_kernel<T, D><<<grid_of<D>(prm), kThreads, 0, st>>>(prm, static_cast<T*>(k), static_cast<T*>(v));
+  kv4_read_kernel<T, D><<<grid_of<T, D>(prm), kThreads, 0, st>>>(prm, static_cast<T*>(k), static_cast<T*>(v));
   return cudaGetLastError();
 }
 
