@@ -32,6 +32,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "sm100_ptx.cuh"
 #include "win_internal.h"
@@ -337,6 +338,9 @@ __device__ void run_mma(const WinParams& P, const Ctl& c, uint32_t sbase, uint32
 }
 
 // ------------------------------------------------------------------- softmax --
+// The lowest n bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : ~(~0u << n)); }
+
 template <bool kPartials>
 __device__ __forceinline__ void store_segment(const WinParams& P, uint32_t tO, float m, float l, float fix,
                                               bool valid, int64_t out_row, int part) {
@@ -436,72 +440,98 @@ __device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t tmem, int
         if (!__all_sync(0xffffffffu, ok)) return;
         ptx::tc_fence_after();
 
-        // The whole 128-column score row in registers (one TMEM round trip); the
-        // reducing load also returns the largest score of each 32 columns.
-        uint32_t raw[128];
-        float mx4[4];
-        ptx::tmem_ld128_max(tS, raw, mx4);
-        float* s = reinterpret_cast<float*>(raw);
-        float mx;
-        if (!__all_sync(0xffffffffu, full)) {
-          // An edge of the window, the diagonal or the sinks: the other keys score
-          // -inf, and the row max is taken over the rest.
-          const uint32_t width = (uint32_t)(c_hi > c_lo ? c_hi - c_lo : 0);
-#pragma unroll
-          for (int e = 0; e < 128; ++e)
-            s[e] = ((uint32_t)(e - c_lo) < width || e < c_s) ? s[e] : -INFINITY;
-          float mx8[8];
-#pragma unroll
-          for (int a = 0; a < 8; ++a) mx8[a] = ptx::max3(s[a], s[a + 8], s[a + 16]);
-#pragma unroll
-          for (int e = 24; e + 16 <= 120; e += 16)
-#pragma unroll
-            for (int a = 0; a < 8; ++a) mx8[a] = ptx::max3(mx8[a], s[e + a], s[e + 8 + a]);
-#pragma unroll
-          for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(mx8[a], s[120 + a]);
-          mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
-                     fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        } else {
-          mx = fmaxf(ptx::max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
-        }
-        const float mt = mx * sl2;  // in log2 units; -inf stays -inf
-        float m_new = m;
+        // The tile's weights into tensor memory, their sum into part, the rounding of the
+        // largest into top_fix; m moves when the tile's largest score exceeds it by the
+        // slack.  Two copies of the code: without a mask the loop over the columns stays
+        // free of branches, which the tiles inside the window need.
         bool resc = false;
-        if (first) {
-          m_new = mt;
-          l = fix = 0.f;
-        } else if (mt > m + kRescaleSlack) {
-          m_new = mt;
-          resc = true;
-        }
-        const float alpha = resc ? ptx::ex2_approx(m - m_new) : 1.0f;
-        m = m_new;
-        const float mref = (m == -INFINITY) ? 0.f : m;
-
-        // p = 2^(s*scale*log2e - m) (masked -inf -> 0), row sum, P to tensor memory as bf16.
-        const float2 sc2 = make_float2(sl2, sl2);
-        const float2 neg = make_float2(-mref, -mref);
-        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                         make_float2(0.f, 0.f)};
-        // Packed P word e overwrites register e, whose score was already consumed.
+        float alpha = 1.0f, part_sum, top_fix;
+        auto weights = [&](auto edge) {
+          // The whole 128-column score row in registers (one TMEM round trip); the
+          // reducing load also returns the largest score of each 32 columns.
+          uint32_t raw[128];
+          float mx4[4];
+          ptx::tmem_ld128_max(tS, raw, mx4);
+          float* s = reinterpret_cast<float*>(raw);
+          // At an edge of the window, on the diagonal and in the sinks, 32 columns at a
+          // time: columns that no row of the warp sees are left out of the exponentials,
+          // those that all see need no mask, and in the others the keys that are not seen
+          // score -inf.
+          uint32_t live = 15u;
+          if (decltype(edge)::value) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) {
-          float2 x2 = ptx::fma2(make_float2(s[2 * e], s[2 * e + 1]), sc2, neg);
-          x2.x = ptx::ex2_approx(x2.x);
-          x2.y = ptx::ex2_approx(x2.y);
-          acc[e & 3] = ptx::add2(acc[e & 3], x2);
-          raw[e] = ptx::pack_bf16x2(x2.x, x2.y);
-        }
-        ptx::tmem_st64(tS + kColP, *reinterpret_cast<const uint32_t(*)[64]>(raw));
-        const float2 a01 = ptx::add2(acc[0], acc[1]);
-        const float2 a23 = ptx::add2(acc[2], acc[3]);
-        const float2 a = ptx::add2(a01, a23);
-        // The PV product weighs each key by its bf16-rounded p while l sums the fp32 p.
-        // `fix` holds the rounding of every tile's largest p: O is divided by l + fix, so
-        // that when one key dominates a row its rounding cancels; the LSE is that of l.
-        const float p_top = ptx::ex2_approx(ptx::fma2(make_float2(mx, mx), sc2, neg).x);
-        const float p_top_bf = __uint_as_float(ptx::pack_bf16x2(p_top, 0.f) << 16);
-        const float top_fix = p_top_bf - p_top;
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t bits = (below(c_hi - 32 * q) & ~below(c_lo - 32 * q)) | below(c_s - 32 * q);
+              if (!__any_sync(0xffffffffu, bits != 0u)) {
+                live &= ~(1u << q);
+                mx4[q] = -INFINITY;
+              } else if (!__all_sync(0xffffffffu, bits == ~0u)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[32 * q + e] = ((bits >> e) & 1u) ? s[32 * q + e] : -INFINITY;
+                float a[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[e] = ptx::max3(s[32 * q + e], s[32 * q + e + 4], s[32 * q + e + 8]);
+#pragma unroll
+                for (int n2 = 12; n2 < 28; n2 += 8)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    a[e] = ptx::max3(a[e], s[32 * q + n2 + e], s[32 * q + n2 + e + 4]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[e] = fmaxf(a[e], s[32 * q + 28 + e]);
+                mx4[q] = fmaxf(ptx::max3(a[0], a[1], a[2]), a[3]);
+              }
+            }
+          }
+          const float mx = fmaxf(ptx::max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
+          const float mt = mx * sl2;  // in log2 units; -inf stays -inf
+          float m_new = m;
+          if (first) {
+            m_new = mt;
+            l = fix = 0.f;
+          } else if (mt > m + kRescaleSlack) {
+            m_new = mt;
+            resc = true;
+          }
+          alpha = resc ? ptx::ex2_approx(m - m_new) : 1.0f;
+          m = m_new;
+          const float mref = (m == -INFINITY) ? 0.f : m;
+
+          // p = 2^(s*scale*log2e - m) (masked -inf -> 0), row sum, P to tensor memory as bf16.
+          const float2 sc2 = make_float2(sl2, sl2);
+          const float2 neg = make_float2(-mref, -mref);
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                           make_float2(0.f, 0.f)};
+          // Packed P word e overwrites register e, whose score was already consumed.
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (!decltype(edge)::value || ((live >> q) & 1u)) {
+#pragma unroll
+              for (int e = 16 * q; e < 16 * q + 16; ++e) {
+                float2 x2 = ptx::fma2(make_float2(s[2 * e], s[2 * e + 1]), sc2, neg);
+                x2.x = ptx::ex2_approx(x2.x);
+                x2.y = ptx::ex2_approx(x2.y);
+                acc[e & 3] = ptx::add2(acc[e & 3], x2);
+                raw[e] = ptx::pack_bf16x2(x2.x, x2.y);
+              }
+            } else {
+#pragma unroll
+              for (int e = 16 * q; e < 16 * q + 16; ++e) raw[e] = 0u;
+            }
+          }
+          ptx::tmem_st64(tS + kColP, *reinterpret_cast<const uint32_t(*)[64]>(raw));
+          const float2 a01 = ptx::add2(acc[0], acc[1]);
+          const float2 a23 = ptx::add2(acc[2], acc[3]);
+          const float2 a = ptx::add2(a01, a23);
+          part_sum = a.x + a.y;
+          // The PV product weighs each key by its bf16-rounded p while l sums the fp32 p.
+          // `fix` holds the rounding of every tile's largest p: O is divided by l + fix, so
+          // that when one key dominates a row its rounding cancels; the LSE is that of l.
+          const float p_top = ptx::ex2_approx(ptx::fma2(make_float2(mx, mx), sc2, neg).x);
+          const float p_top_bf = __uint_as_float(ptx::pack_bf16x2(p_top, 0.f) << 16);
+          top_fix = p_top_bf - p_top;
+        };
+        if (__all_sync(0xffffffffu, full)) weights(std::false_type());
+        else weights(std::true_type());
         if (!first && __any_sync(0xffffffffu, resc)) {
           // O and l were accumulated against the old max: bring them to the new one
           // (after the scores are consumed, so their registers are free).
@@ -517,7 +547,7 @@ __device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t tmem, int
           l *= alpha;
           fix *= alpha;
         }
-        l += a.x + a.y;
+        l += part_sum;
         fix += top_fix;
         first = false;
         ptx::tc_fence_before();
