@@ -51,16 +51,17 @@ struct ra_plan_s {
   cudaEvent_t ev_entry = nullptr, ev_rot = nullptr, ev_step = nullptr;  // ra_ring_fwd ordering
   bool round_sync = false;  // forward kernel schedule (ra::use_round_sync)
   int sm_count = 0;
-  // Windowed plans (ra_plan_window): window 0 is the whole causal prefix.  The forward's
-  // groups come twice, over the ring's key blocks and over gathered (natural-order)
-  // keys: group g of the gathered forward is win_groups[n_win_groups + g].
+  // Windowed plans (ra_plan_window): window 0 is the whole causal prefix.  Three work lists:
+  // over the ring's key blocks (partials, steps), for the fused forward, and over gathered
+  // (natural-order) keys; those that are alike share their items.
   int32_t window = 0, sinks = 0;
+  struct WinList {
+    ra::WinView q, k;
+    int64_t first, count;
+  } win_lists[3] = {};
   std::vector<ra::WinItem> win_items;
-  std::vector<ra::WinGroup> win_groups;
   std::vector<ra::WinRange> win_ranges;
-  int64_t n_win_groups = 0;
   ra::WinItem* d_win_items = nullptr;
-  ra::WinGroup* d_win_groups = nullptr;
   ra::WinRange* d_win_ranges = nullptr;
   // ra_plan_destroy queues the frees of the device tables behind exactly this work.
   std::vector<ra::StreamMark> marks;
@@ -325,28 +326,71 @@ int32_t win_pos(const ra_problem& pb, int64_t s_n, int p, int64_t row) {
   return (int32_t)ra::pos_of(pb.layout, pb.n_shards, s_n, p, row);
 }
 
-// Key ranges of a group over the ring (gathered: over the natural-order keys), appended
-// to the plan's list; returns the number of key tiles.
-int32_t add_ranges(ra_plan_s* pl, ra::WinGroup* gr, bool gathered) {
-  const ra_problem& pb = pl->prob;
-  const int N = pb.n_shards;
+// Key ranges of the queries of shard p at positions [minpos, maxpos], appended to the plan's
+// list; returns the number of key tiles.
+int32_t add_ranges(ra_plan_s* pl, const ra::WinView& k, int p, int32_t minpos, int32_t maxpos) {
+  const int N = k.shards;
   int32_t tiles = 0;
-  gr->range0 = (int32_t)pl->win_ranges.size();
   auto add = [&](int step, int r, int32_t from, int32_t to) {
     if (to <= from) return;
-    pl->win_ranges.push_back({step, r, from, to});
-    tiles += ra::range_tiles(pl->win_ranges.back());
+    pl->win_ranges.push_back({step, r, from / k.stripe * k.stripe, to});
+    tiles += ra::range_tiles(pl->win_ranges.back(), k.tile);
   };
-  for (int t = 0; t < (gathered ? 1 : N); ++t) {
-    const int r = gathered ? 0 : (gr->shard - t + N) % N;
-    const ra::WinSpan sp =
-        ra::win_span(gathered ? (int)RA_LAYOUT_CONTIGUOUS : pb.layout, gathered ? 1 : N,
-                     (int32_t)(gathered ? pb.seq : pl->s_n), pl->window, pl->sinks, r, gr->minpos, gr->maxpos);
+  for (int t = 0; t < N; ++t) {
+    const int r = N == 1 ? 0 : (p - t + N) % N;
+    const ra::WinSpan sp = ra::win_span(k.layout, N, k.s_n, pl->window, pl->sinks, r, minpos, maxpos);
     add(t, r, 0, sp.first);
     add(t, r, sp.lo, sp.hi);
   }
-  gr->n_ranges = (int32_t)pl->win_ranges.size() - gr->range0;
   return tiles;
+}
+
+// A forward work list over the views q and k.
+ra_plan_s::WinList add_win_list(ra_plan_s* pl, const ra::WinView& q, const ra::WinView& k) {
+  const ra_problem& pb = pl->prob;
+  const int G = pb.heads_q / pb.heads_kv;
+  const bool head_pairs = G % 2 == 0;
+  // The query rows of an item, each with its key ranges: one tile for two heads of a
+  // key/value head's group, or (odd group) two consecutive tiles of one head.
+  struct Rows {
+    ra::WinItem item;
+    int32_t tiles;
+  };
+  std::vector<Rows> rows;
+  auto pos = [&](int p, int32_t row) { return (int32_t)ra::pos_of(q.layout, q.shards, q.s_n, p, row); };
+  for (int p = 0; p < q.shards; ++p)
+    for (int32_t row = 0; row < q.s_n;) {
+      Rows x{};
+      x.item.shard = p;
+      x.item.row0 = row;
+      x.item.row_end = ra::run_end(q.layout, q.s_n, row);
+      x.item.row1 = head_pairs ? row : (row + q.tile < x.item.row_end ? row + q.tile : -1);
+      const int32_t end = std::min((x.item.row1 < 0 ? row : x.item.row1) + q.tile, x.item.row_end);
+      x.item.range0 = (int32_t)pl->win_ranges.size();
+      x.tiles = x.item.n_tiles = add_ranges(pl, k, p, pos(p, row), pos(p, end - 1));
+      x.item.n_ranges = (int32_t)pl->win_ranges.size() - x.item.range0;
+      rows.push_back(x);
+      row = end;
+    }
+  // Longest first with key/value heads grouped (the order of ra::schedule_before).
+  std::vector<Keyed> list;
+  for (size_t g = 0; g < rows.size(); ++g)
+    for (int64_t b = 0; b < pb.batch; ++b)
+      for (int h = 0; h < pb.heads_q; h += head_pairs ? 2 : 1) {
+        ra::WorkItem w{};
+        w.bh0 = (int32_t)(b * pb.heads_q + h);
+        w.bh1 = head_pairs ? w.bh0 + 1 : (rows[g].item.row1 >= 0 ? w.bh0 : -1);
+        w.shard = (int32_t)g;
+        w.cost = rows[g].tiles;
+        list.push_back({w, (int64_t)list.size()});
+      }
+  const ra_plan_s::WinList out{q, k, (int64_t)pl->win_items.size(), (int64_t)list.size()};
+  for (const ra::WorkItem& w : schedule(list, pb.heads_q, G)) {
+    pl->win_items.push_back(rows[w.shard].item);
+    pl->win_items.back().bh0 = w.bh0;
+    pl->win_items.back().bh1 = w.bh1;
+  }
+  return out;
 }
 
 // FULL / PARTIAL / SKIP counts of a windowed plan: a 128-row key tile is visited when
@@ -450,54 +494,25 @@ void build_win_schedule(ra_plan_s* pl) {
   pl->n_ktiles = pl->n_qtiles;
   win_tile_counts(pl);
   if (pb.dtype != RA_DTYPE_BF16) return;  // the SIMT kernels walk rows, not items
-  const int G = pb.heads_q / pb.heads_kv;
-  const bool head_pairs = G % 2 == 0;
-
-  // Query groups: one 128-row tile for two heads of a key/value head's group, or (odd
-  // group) two consecutive tiles of one head.
-  std::vector<int32_t> tiles;
-  for (int p = 0; p < N; ++p)
-    for (int32_t row = 0; row < s_n;) {
-      ra::WinGroup gr{};
-      gr.shard = p;
-      gr.row0 = row;
-      gr.row_end = ra::run_end(pb.layout, s_n, row);
-      gr.row1 = head_pairs ? row : (row + ra::kTileRows < gr.row_end ? row + ra::kTileRows : -1);
-      const int32_t end = std::min((gr.row1 < 0 ? row : gr.row1) + ra::kTileRows, gr.row_end);
-      gr.minpos = win_pos(pb, s_n, p, row);
-      gr.maxpos = win_pos(pb, s_n, p, end - 1);
-      pl->win_groups.push_back(gr);
-      row = end;
-    }
-  pl->n_win_groups = (int64_t)pl->win_groups.size();
-  for (int64_t g = 0; g < pl->n_win_groups; ++g) tiles.push_back(add_ranges(pl, &pl->win_groups[g], false));
-  std::vector<int32_t> gathered_tiles;
-  for (int64_t g = 0; g < pl->n_win_groups; ++g) {
-    ra::WinGroup gr = pl->win_groups[g];
-    gathered_tiles.push_back(add_ranges(pl, &gr, true));
-    pl->win_groups.push_back(gr);
+  // Walked shard by shard, as the ring steps and the partials need it, and in the order of
+  // positions, where a key tile then holds consecutive positions and the window's edges fall
+  // into as few tiles as they can: the fused forward of contiguous shards (which are one
+  // run of rows) and of striped ones.  A stripe of more than 128 shards exceeds a tile, and
+  // zigzag chunks are runs of consecutive positions as they are.
+  const ra::WinView ring{pb.layout, N, s_n, 1, ra::kTileRows};
+  ra::WinView natural{RA_LAYOUT_CONTIGUOUS, 1, (int32_t)pb.seq, 1, ra::kTileRows};
+  ra::WinView rows = natural;
+  if (pb.layout == RA_LAYOUT_STRIPED && N > 1) {
+    rows.stripe = N;
+    rows.tile = ra::kTileRows / N * N;
   }
-
-  // Items, longest first with key/value heads grouped (the order of ra::schedule_before).
-  std::vector<Keyed> list;
-  int64_t seqno = 0;
-  for (int64_t g = 0; g < pl->n_win_groups; ++g)
-    for (int64_t b = 0; b < pb.batch; ++b)
-      for (int h = 0; h < pb.heads_q; h += head_pairs ? 2 : 1) {
-        ra::WorkItem w{};
-        w.bh0 = (int32_t)(b * pb.heads_q + h);
-        w.bh1 = head_pairs ? w.bh0 + 1 : (pl->win_groups[g].row1 >= 0 ? w.bh0 : -1);
-        w.shard = (int32_t)g;
-        w.cost = tiles[g];
-        w.pad = gathered_tiles[g];
-        list.push_back({w, seqno++});
-      }
-  const std::vector<ra::WorkItem> order = schedule(list, pb.heads_q, G);
-  // the gathered forward's items: the same order, its own groups and counts
-  for (int gathered = 0; gathered < 2; ++gathered)
-    for (const ra::WorkItem& w : order)
-      pl->win_items.push_back({w.shard + (gathered ? (int32_t)pl->n_win_groups : 0), w.bh0, w.bh1,
-                               gathered ? w.pad : w.cost});
+  const bool by_position = pb.layout != RA_LAYOUT_ZIGZAG && N <= ra::kTileRows;
+  pl->win_lists[0] = add_win_list(pl, ring, ring);
+  pl->win_lists[1] = N == 1 || !by_position ? pl->win_lists[0] : add_win_list(pl, rows, rows);
+  pl->win_lists[2] = N == 1 ? pl->win_lists[0]
+                     : pb.layout == RA_LAYOUT_CONTIGUOUS && by_position
+                         ? pl->win_lists[1]
+                         : add_win_list(pl, by_position ? rows : ring, natural);
   build_win_bwd(pl);
 }
 
@@ -535,7 +550,6 @@ ra_status upload(ra_plan_s* pl) {
   put(pl->bwd_items, &pl->d_bwd_items);
   put(pl->gather_items, &pl->d_gather_items);
   put(pl->win_items, &pl->d_win_items);
-  put(pl->win_groups, &pl->d_win_groups);
   put(pl->win_ranges, &pl->d_win_ranges);
   // the tables are in place before any launch on another stream reads them
   if (e == cudaSuccess) e = cudaStreamSynchronize(ms);
@@ -587,22 +601,24 @@ ra_status launch_win(ra_plan_s* plan, const ra::FwdParams& prm, const void* q, c
   w.heads_kv = prm.heads_kv;
   w.group = prm.group;
   w.head_dim = prm.head_dim;
-  w.n_shards = prm.n_shards;
-  w.layout = prm.layout;
+  const int which = prm.gathered ? 2 : (prm.o_parts != nullptr ? 0 : 1);
+  const ra_plan_s::WinList& list = plan->win_lists[which];
+  w.q = list.q;
+  w.k = list.k;
+  if (pb.dtype != RA_DTYPE_BF16) {  // rows, not items
+    w.q = {pb.layout, pb.n_shards, (int32_t)plan->s_n, 1, 0};
+    w.k = prm.gathered ? ra::WinView{RA_LAYOUT_CONTIGUOUS, 1, (int32_t)pb.seq, 1, 0} : w.q;
+  }
   w.window = plan->window;
   w.sinks = plan->sinks;
   w.seq = (int32_t)pb.seq;
-  w.s_n = (int32_t)plan->s_n;
   w.scale = prm.scale;
   w.scale_log2 = prm.scale_log2;
   w.step_lo = prm.step_lo;
-  w.step_hi = prm.step_hi;
+  w.step_hi = std::min<int32_t>(prm.step_hi, w.k.shards);
   w.kv_rotated = prm.kv_rotated;
-  w.gathered = prm.gathered;
-  const int64_t n = (int64_t)plan->win_items.size() / 2;
-  w.n_items = (int32_t)n;
-  w.items = plan->d_win_items + (prm.gathered ? n : 0);
-  w.groups = plan->d_win_groups;
+  w.n_items = (int32_t)list.count;
+  w.items = plan->d_win_items + list.first;
   w.ranges = plan->d_win_ranges;
   w.o = prm.o;
   w.lse = prm.lse;
@@ -612,7 +628,7 @@ ra_status launch_win(ra_plan_s* plan, const ra::FwdParams& prm, const void* q, c
   cudaError_t e;
   const char* why = "windowed f32 forward launch failed";
   if (pb.dtype == RA_DTYPE_BF16)
-    e = ra::launch_win_fwd_bf16(w, q, k, v, (int)std::min<int64_t>(n, plan->sm_count > 0 ? plan->sm_count : 148), st, &why);
+    e = ra::launch_win_fwd_bf16(w, q, k, v, (int)std::min<int64_t>(list.count, plan->sm_count > 0 ? plan->sm_count : 148), st, &why);
   else
     e = ra::launch_win_fwd_f32(w, static_cast<const float*>(q), static_cast<const float*>(k),
                                static_cast<const float*>(v), st);
@@ -814,8 +830,8 @@ ra_status ra_plan_destroy(ra_plan_t plan) {
     // order, and the host does not wait.
     if (plan->mem_stream != nullptr) {
       for (const ra::StreamMark& m : plan->marks) cudaStreamWaitEvent(plan->mem_stream, m.done, 0);
-      void* mem[] = {plan->d_items,     plan->d_step_items,  plan->d_bwd_items,   plan->d_gather_items,
-                     plan->d_win_items, plan->d_win_groups, plan->d_win_ranges, plan->d_status};
+      void* mem[] = {plan->d_items,     plan->d_step_items, plan->d_bwd_items, plan->d_gather_items,
+                     plan->d_win_items, plan->d_win_ranges, plan->d_status};
       for (void* p : mem)
         if (p != nullptr) cudaFreeAsync(p, plan->mem_stream);
       cudaStreamDestroy(plan->mem_stream);  // released once its queued frees have run

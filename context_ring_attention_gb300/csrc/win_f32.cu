@@ -42,13 +42,13 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int64_t rows_all = (int64_t)P.batch * P.heads_q * P.seq;
   const int64_t grow = (int64_t)blockIdx.x * kWarps + warp;  // global query row
   if (grow >= rows_all) return;
-  const int d = P.head_dim, N = P.n_shards;
+  const int d = P.head_dim, N = P.k.shards;
   const int64_t bh = grow / P.seq;
   const int srow = (int)(grow % P.seq);
-  const int p = srow / P.s_n, i = srow % P.s_n;
+  const int p = srow / P.q.s_n, i = srow % P.q.s_n;
   const int b = (int)(bh / P.heads_q), h = (int)(bh % P.heads_q);
   const int64_t kv_base = ((int64_t)b * P.heads_kv + h / P.group) * P.seq;
-  const int my_pos = (int)pos_of(P.layout, N, P.s_n, p, i);
+  const int my_pos = (int)pos_of(P.q.layout, P.q.shards, P.q.s_n, p, i);
 
   for (int c = lane; c < d; c += 32) qs[warp][c] = q[grow * d + c];
   __syncwarp();
@@ -60,13 +60,12 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int x = 0; x < kMaxD / 32; ++x) acc[x] = 0.f;
 
   for (int t = P.step_lo; t < P.step_hi; ++t) {
-    const int r = P.gathered ? 0 : (p - t + N) % N;
-    const int slot = P.gathered ? 0 : (P.kv_rotated ? p : r);  // where the block of step t sits
-    const WinSpan sp = win_span(P.gathered ? (int)RA_LAYOUT_CONTIGUOUS : P.layout, P.gathered ? 1 : N,
-                                P.gathered ? P.seq : P.s_n, P.window, P.sinks, r, my_pos, my_pos);
-    RA_BOUNDS(P.status, sp.first >= 0 && sp.lo >= 0 && sp.hi <= (P.gathered ? P.seq : P.s_n) && slot >= 0 && slot < N, 70);
-    const float* kb = k + (kv_base + (int64_t)slot * P.s_n) * d;
-    const float* vb = v + (kv_base + (int64_t)slot * P.s_n) * d;
+    const int r = N == 1 ? 0 : (p - t + N) % N;
+    const int slot = P.kv_rotated ? p : r;  // where the block of step t sits
+    const WinSpan sp = win_span(P.k.layout, N, P.k.s_n, P.window, P.sinks, r, my_pos, my_pos);
+    RA_BOUNDS(P.status, sp.first >= 0 && sp.lo >= 0 && sp.hi <= P.k.s_n && slot >= 0 && slot < N, 70);
+    const float* kb = k + (kv_base + (int64_t)slot * P.k.s_n) * d;
+    const float* vb = v + (kv_base + (int64_t)slot * P.k.s_n) * d;
     for (int run = 0; run < 2; ++run) {  // the sinks, then the window
       const int end = run ? sp.hi : sp.first;
       for (int j0 = run ? sp.lo : 0; j0 < end; j0 += 32) {

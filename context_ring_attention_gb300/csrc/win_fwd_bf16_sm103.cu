@@ -20,8 +20,8 @@
 // plan need no reset between them.
 //
 // Roles (one persistent CTA per SM, 12 warps): warp 0 TMA producer, warp 1 tcgen05
-// issuer (both converged, one elected lane issues), warps 4-7 softmax of query tile 0,
-// warps 8-11 of query tile 1 (one thread per row).
+// issuer (both converged, one elected lane issues), warp 2 the work items' records, warps
+// 4-7 softmax of query tile 0, warps 8-11 of query tile 1 (one thread per row).
 // TMEM: S0 cols 0-127 (P0 in 64-127), S1 128-255 (P1 in 192-255), O0 256-383,
 // O1 384-511 (all 512 columns).
 //
@@ -47,10 +47,22 @@ constexpr uint32_t kRegsSoftmax = 192;
 static_assert(128 * kRegsOther + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kTileBytes = 128 * 128 * 2;  // one 128 x 128 bf16 tile
 constexpr uint32_t kHalfBytes = 128 * 64 * 2;   // 128 rows x one 128-byte swizzle column
-constexpr int kStages = 5;
-constexpr uint32_t kOffQ = 0;                            // Q0, Q1
-constexpr uint32_t kOffKV = 2 * kTileBytes;              // K/V ring
-constexpr uint32_t kOffBar = kOffKV + kStages * kTileBytes;
+constexpr int kStages = 3;                      // K/V ring: 4 and 5 were no faster (2061, 2106 against 2043 us)
+constexpr int kItemSlots = 4;                   // work items under way from the record warp to the others
+constexpr int kSlotRanges = 12;                 // ranges of an item kept with it (more are read from memory)
+constexpr uint32_t kStageRow = 144;             // 128 bytes of an output row, and 16 so that the lanes'
+                                                // 16-byte writes fall into different banks
+constexpr uint32_t kOffQ = 0;                   // Q0, Q1
+constexpr uint32_t kOffKV = 2 * kTileBytes;
+constexpr uint32_t kOffOut = kOffKV + kStages * kTileBytes;  // half rows of O on their way out
+constexpr uint32_t kOffRec = kOffOut + 256 * kStageRow;
+struct alignas(16) Record {
+  WinItem it;
+  int32_t x0, xn;  // its ranges within this launch: P.ranges[x0 .. x0 + xn)
+  int32_t pad[2];
+  WinRange ranges[kSlotRanges];
+};
+constexpr uint32_t kOffBar = kOffRec + kItemSlots * (uint32_t)sizeof(Record);
 
 enum : int {
   kQFull = 0,               // one per query tile
@@ -61,12 +73,15 @@ enum : int {
   kPFull = kSFull + 2,
   kOFull = kPFull + 2,
   kDone = kOFull + 2,
-  kNumBars = kDone + 1
+  kItemFull = kDone + 1,
+  kItemEmpty = kItemFull + kItemSlots,
+  kNumBars = kItemEmpty + kItemSlots
 };
+constexpr uint32_t kItemConsumers = 10;  // producer, MMA and 8 softmax warps
 constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;  // TMEM base written by tcgen05.alloc
 constexpr uint32_t kOffAbort = kOffSlot + 4;
 constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;  // + slack to align the base to 1 KiB
-static_assert(8 * kNumBars + 8 <= 256, "barrier area");
+static_assert(8 * kNumBars + 8 <= 256 && kOffBar % 16 == 0 && kSmemBytes <= 232448, "shared memory");
 
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t col_s(int g) { return g ? 128u : 0u; }
@@ -120,21 +135,75 @@ __device__ __forceinline__ void drain_bar(const Ctl& c, uint32_t bar, uint32_t p
 
 #define RA_WAIT(n, phase, who) __all_sync(0xffffffffu, wait_bar(c, c.bar(n), (phase) & 1u, who))
 
-// The ranges of a group that this launch runs, in ring order: [lo, hi) of its list.
-__device__ __forceinline__ int ranges_from(const WinParams& P, const WinGroup& gr) {
-  int x = gr.range0;
-  while (x < gr.range0 + gr.n_ranges && P.ranges[x].step < P.step_lo) ++x;
-  return x;
+// 4-D tiled load (element of a row, row of the stripe, stripe, head); a converged warp
+// executes it and one elected lane issues.
+__device__ __forceinline__ void tma_load_4d_warp_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                                      int32_t i, int32_t bh, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(0), "r"(i), "r"(bh), "l"(policy)
+      : "memory");
 }
-__device__ __forceinline__ bool range_in(const WinParams& P, const WinGroup& gr, int x) {
-  return x < gr.range0 + gr.n_ranges && P.ranges[x].step < P.step_hi;
+// Bulk copy shared -> global of this thread, and the waits for its copies: until they have
+// read shared memory, and until they are done.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// ------------------------------------------------------------------- records --
+// Warp 2 brings the items and their ranges of this CTA into shared memory, a few items
+// ahead: reading them where they are needed took each role 1 to 2 us at every item.
+__device__ void run_records(const WinParams& P, const Ctl& c, Record* recs, int lane) {
+  for (uint32_t u = 0;; ++u) {
+    const int idx = (int)(blockIdx.x + u * gridDim.x);
+    const uint32_t slot = u % kItemSlots;
+    if (!RA_WAIT(kItemEmpty + (int)slot, (u / kItemSlots) ^ 1u, kStatusTimeoutProducer)) return;
+    Record& r = recs[slot];
+    const bool end = idx >= P.n_items;
+    if (end) {
+      if (lane == 0) r.it.bh0 = -1;
+    } else {
+      const int4 w = lane < 3 ? reinterpret_cast<const int4*>(P.items + idx)[lane] : make_int4(0, 0, 0, 0);
+      if (lane < 3) reinterpret_cast<int4*>(&r.it)[lane] = w;
+      int x0 = __shfl_sync(0xffffffffu, w.z, 1);                // range0
+      const int x_end = x0 + __shfl_sync(0xffffffffu, w.w, 1);  // + n_ranges
+      int xn = x_end - x0;
+      if (P.step_lo > 0 || P.step_hi < P.k.shards) {  // ranges are in the order of their steps
+        while (x0 < x_end && P.ranges[x0].step < P.step_lo) ++x0;
+        for (xn = 0; x0 + xn < x_end && P.ranges[x0 + xn].step < P.step_hi;) ++xn;
+      }
+      if (lane == 0) {
+        r.x0 = x0;
+        r.xn = xn;
+      }
+      if (lane < kSlotRanges && lane < xn)
+        *reinterpret_cast<int4*>(&r.ranges[lane]) = *reinterpret_cast<const int4*>(&P.ranges[x0 + lane]);
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(c.bar(kItemFull + (int)slot));
+    if (end) return;
+  }
 }
 
-// First row of the [B, Hkv, S, d] tensor (as rows of d) of a range's keys.
-__device__ __forceinline__ int32_t range_row(const WinParams& P, const WinGroup& gr, const WinRange& rg, int bh) {
-  const int b = bh / P.heads_q, kvh = (bh % P.heads_q) / P.group;
-  const int slot = P.gathered ? 0 : (P.kv_rotated ? gr.shard : rg.r);  // where the block of the step sits
-  return (int32_t)((int64_t)(b * P.heads_kv + kvh) * P.seq + (int64_t)slot * P.s_n + rg.row0);
+// Consumer side: the record of this role's u-th item (nullptr at the end or on abort), and
+// giving it back.
+__device__ __forceinline__ const Record* next_record(const Ctl& c, const Record* recs, uint32_t u, uint32_t who) {
+  const uint32_t slot = u % kItemSlots;
+  if (!RA_WAIT(kItemFull + (int)slot, u / kItemSlots, who)) return nullptr;
+  return recs[slot].it.bh0 < 0 ? nullptr : recs + slot;
+}
+__device__ __forceinline__ void release_record(const Ctl& c, uint32_t u, int lane) {
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(c.bar(kItemEmpty + (int)(u % kItemSlots)));
+}
+__device__ __forceinline__ WinRange range_at(const WinParams& P, const Record* r, int k) {
+  return k < kSlotRanges ? r->ranges[k] : P.ranges[r->x0 + k];
 }
 
 // ------------------------------------------------------------------ producer --
@@ -142,55 +211,60 @@ struct ProducerState {
   uint32_t kv_issued, q_issued[2];
 };
 
-__device__ void run_producer(const WinParams& P, const Ctl& c, uint32_t sbase, const CUtensorMap* tq,
-                             const CUtensorMap* tk, const CUtensorMap* tv, ProducerState& st) {
+__device__ void run_producer(const WinParams& P, const Ctl& c, uint32_t sbase, const Record* recs,
+                             const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, ProducerState& st,
+                             int lane) {
   const uint64_t keep = ptx::l2_policy_evict_last();   // K/V: re-read by the CTAs running together
   const uint64_t once = ptx::l2_policy_evict_first();  // Q: read once
-  auto load_kv = [&](int32_t y) {  // K tile, then V tile
+  const uint32_t kv_bytes = (uint32_t)P.k.tile * 256u, q_bytes = (uint32_t)P.q.tile * 256u;
+  auto load_kv = [&](int32_t i, int32_t bh) {  // K tile, then V tile
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const uint32_t s = st.kv_issued % kStages, use = st.kv_issued / kStages;
       if (!RA_WAIT(kKVEmpty + (int)s, use ^ 1u, kStatusTimeoutProducer)) return false;
       const uint32_t dst = sbase + kOffKV + s * kTileBytes;
       const CUtensorMap* map = which ? tv : tk;
-      ptx::mbar_arrive_expect_tx_warp(c.bar(kKVFull + (int)s), kTileBytes);
-      ptx::tma_load_2d_warp_hint(dst, map, c.bar(kKVFull + (int)s), 0, y, keep);
-      ptx::tma_load_2d_warp_hint(dst + kHalfBytes, map, c.bar(kKVFull + (int)s), 64, y, keep);
+      ptx::mbar_arrive_expect_tx_warp(c.bar(kKVFull + (int)s), kv_bytes);
+      tma_load_4d_warp_hint(dst, map, c.bar(kKVFull + (int)s), 0, i, bh, keep);
+      tma_load_4d_warp_hint(dst + kHalfBytes, map, c.bar(kKVFull + (int)s), 64, i, bh, keep);
       ++st.kv_issued;
     }
     return true;
   };
-  for (int idx = blockIdx.x; idx < P.n_items; idx += gridDim.x) {
-    const WinItem it = P.items[idx];
-    const WinGroup gr = P.groups[it.group];
-    int x = ranges_from(P, gr);
-    if (!range_in(P, gr, x)) continue;  // nothing to meet in these steps
-    RA_BOUNDS(c.status, gr.shard >= 0 && gr.shard < P.n_shards && gr.row0 >= 0 && gr.row0 < P.s_n && gr.row1 < P.s_n, 60);
+  for (uint32_t u = 0;; ++u) {
+    const Record* r = next_record(c, recs, u, kStatusTimeoutProducer);
+    if (r == nullptr) return;
+    const WinItem it = r->it;
+    RA_BOUNDS(c.status, it.shard >= 0 && it.shard < P.q.shards && it.row0 >= 0 && it.row0 < P.q.s_n && it.row1 < P.q.s_n, 60);
+    const int kv_bh = it.bh0 / P.heads_q * P.heads_kv + (it.bh0 % P.heads_q) / P.group;
+    RA_BOUNDS(c.status, kv_bh >= 0 && kv_bh < P.batch * P.heads_kv, 61);
     bool q_loaded = false;
-    for (; range_in(P, gr, x); ++x) {
-      const WinRange rg = P.ranges[x];
-      const int32_t y = range_row(P, gr, rg, it.bh0);
-      const int n = range_tiles(rg);
-      RA_BOUNDS(c.status, y >= 0 && (int64_t)y + (rg.end - rg.row0) <= (int64_t)P.batch * P.heads_kv * P.seq &&
-                              rg.row0 >= 0 && rg.row0 < rg.end && rg.end <= (P.gathered ? P.seq : P.s_n), 61);
-      for (int kt = 0; kt < n; ++kt) {
-        if (!load_kv(y + kt * kTileRows)) return;
+    for (int k = 0; k < r->xn; ++k) {
+      const WinRange rg = range_at(P, r, k);
+      const int slot = P.kv_rotated ? it.shard : rg.r;  // where the block of the step sits
+      RA_BOUNDS(c.status, slot >= 0 && slot < P.k.shards && rg.row0 >= 0 && rg.row0 < rg.end && rg.end <= P.k.s_n &&
+                              rg.row0 % P.k.stripe == 0, 61);
+      int32_t i = (slot * P.k.s_n + rg.row0) / P.k.stripe;
+      for (int n = range_tiles(rg, P.k.tile); n > 0; --n, i += P.k.tile / P.k.stripe) {
+        RA_BOUNDS(c.status, i >= 0 && i < P.seq / P.k.stripe, 61);
+        if (!load_kv(i, kv_bh)) return;
         if (q_loaded) continue;
         q_loaded = true;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           if (g == 1 && it.bh1 < 0) break;
           if (!RA_WAIT(kQEmpty + g, st.q_issued[g] ^ 1u, kStatusTimeoutProducer)) return;
-          const int32_t yq = (int32_t)((int64_t)(g ? it.bh1 : it.bh0) * P.seq + (int64_t)gr.shard * P.s_n +
-                                       (g ? gr.row1 : gr.row0));
-          RA_BOUNDS(c.status, yq >= 0 && yq < (int64_t)P.batch * P.heads_q * P.seq, 62);
-          ptx::mbar_arrive_expect_tx_warp(c.bar(kQFull + g), kTileBytes);
-          ptx::tma_load_2d_warp_hint(sbase + kOffQ + g * kTileBytes, tq, c.bar(kQFull + g), 0, yq, once);
-          ptx::tma_load_2d_warp_hint(sbase + kOffQ + g * kTileBytes + kHalfBytes, tq, c.bar(kQFull + g), 64, yq, once);
+          const int32_t iq = (it.shard * P.q.s_n + (g ? it.row1 : it.row0)) / P.q.stripe;
+          const int32_t bh = g ? it.bh1 : it.bh0;
+          RA_BOUNDS(c.status, iq >= 0 && iq < P.seq / P.q.stripe && bh < P.batch * P.heads_q, 62);
+          ptx::mbar_arrive_expect_tx_warp(c.bar(kQFull + g), q_bytes);
+          tma_load_4d_warp_hint(sbase + kOffQ + g * kTileBytes, tq, c.bar(kQFull + g), 0, iq, bh, once);
+          tma_load_4d_warp_hint(sbase + kOffQ + g * kTileBytes + kHalfBytes, tq, c.bar(kQFull + g), 64, iq, bh, once);
           ++st.q_issued[g];
         }
       }
     }
+    release_record(c, u, lane);
   }
 }
 
@@ -206,6 +280,8 @@ __device__ __forceinline__ void issue_s(uint32_t q0, uint32_t k0, uint32_t tmem,
   }
 }
 
+// (Products of fewer keys for the sinks' tile, by a descriptor and a count held in
+// registers, cost 2.5% in the issue and gained nothing: the tile's time is the softmax's.)
 __device__ __forceinline__ void issue_pv(uint32_t v0, uint32_t tmem, int g, uint32_t vs, bool accumulate) {
   const uint32_t a0 = tmem + col_s(g) + kColP;  // P in tensor memory
   const uint32_t b0 = v0 + vs * kTileDesc;
@@ -225,48 +301,50 @@ struct Seg {
 };
 template <bool kPartials>
 struct SegWalk {
-  int idx, x;
-  bool inside;  // partials: in the middle of item idx
-  WinGroup gr;
-  bool two;
+  uint32_t u;      // record in hand, or the next one
+  int k;           // partials: next range of it; -1: none in hand
+  const Record* r;
   __device__ __forceinline__ void begin() {
-    idx = blockIdx.x;
-    inside = false;
+    u = 0;
+    k = -1;
   }
-  __device__ __forceinline__ bool next(const WinParams& P, Seg& s) {
+  __device__ __forceinline__ bool next(const WinParams& P, const Ctl& c, const Record* recs, int lane, Seg& s) {
     if (!kPartials) {
-      if (idx >= P.n_items) return false;
-      const WinItem it = P.items[idx];
-      s = {it.n_tiles, it.bh1 >= 0, true, true};
-      idx += gridDim.x;
+      r = next_record(c, recs, u, kStatusTimeoutMma);
+      if (r == nullptr) return false;
+      s = {r->it.n_tiles, r->it.bh1 >= 0, true, true};
+      release_record(c, u++, lane);
       return true;
     }
-    s.first = false;
-    while (!inside) {  // the next item that meets a key in these steps
-      if (idx >= P.n_items) return false;
-      const WinItem it = P.items[idx];
-      gr = P.groups[it.group];
-      two = it.bh1 >= 0;
-      x = ranges_from(P, gr);
-      inside = range_in(P, gr, x);
-      s.first = true;
-      if (!inside) idx += gridDim.x;
+    s.first = k < 0;
+    while (k < 0) {  // the next item that meets a key in these steps
+      r = next_record(c, recs, u, kStatusTimeoutMma);
+      if (r == nullptr) return false;
+      k = 0;
+      if (r->xn == 0) {
+        release_record(c, u++, lane);
+        k = -1;
+      }
     }
-    const int step = P.ranges[x].step;
+    s.two = r->it.bh1 >= 0;
+    const int step = range_at(P, r, k).step;
     s.n = 0;
-    for (; range_in(P, gr, x) && P.ranges[x].step == step; ++x) s.n += range_tiles(P.ranges[x]);
-    s.two = two;
-    s.last = !range_in(P, gr, x);
+    for (; k < r->xn; ++k) {
+      const WinRange rg = range_at(P, r, k);
+      if (rg.step != step) break;
+      s.n += range_tiles(rg, P.k.tile);
+    }
+    s.last = k == r->xn;
     if (s.last) {
-      inside = false;
-      idx += gridDim.x;
+      release_record(c, u++, lane);
+      k = -1;
     }
     return true;
   }
 };
 
 template <bool kPartials>
-__device__ void run_mma(const WinParams& P, const Ctl& c, uint32_t sbase, uint32_t tmem) {
+__device__ void run_mma(const WinParams& P, const Ctl& c, uint32_t sbase, const Record* recs, uint32_t tmem, int lane) {
   const uint32_t q0 = ptx::desc_lo(sbase + kOffQ, 16);
   const uint32_t k0 = ptx::desc_lo(sbase + kOffKV, 16);
   const uint32_t v0 = ptx::desc_lo(sbase + kOffKV, kHalfBytes);
@@ -276,7 +354,7 @@ __device__ void run_mma(const WinParams& P, const Ctl& c, uint32_t sbase, uint32
   SegWalk<kPartials> walk;
   walk.begin();
   Seg cur, nxt;
-  if (!walk.next(P, cur)) return;
+  if (!walk.next(P, c, recs, lane, cur)) return;
   // Scores of a segment's key tile: the queries arrive with an item's first tile, and
   // their shared memory is free for the next item's after its last.
   auto scores = [&](const Seg& s, int kt, int g, uint32_t ks) {
@@ -303,7 +381,7 @@ __device__ void run_mma(const WinParams& P, const Ctl& c, uint32_t sbase, uint32
     int nkt = kt + 1;
     nxt = cur;
     if (seg_last) {
-      has_next = walk.next(P, nxt);
+      has_next = walk.next(P, c, recs, lane, nxt);
       nkt = 0;
     }
     const uint32_t vs = kv % kStages;
@@ -341,34 +419,41 @@ __device__ void run_mma(const WinParams& P, const Ctl& c, uint32_t sbase, uint32
 // The lowest n bits (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : ~(~0u << n)); }
 
+// The finished rows of a segment.  bf16 rows go out through shared memory, half a row at a
+// time: a thread writes its 128 bytes there and sends them on as one bulk copy.  (Written
+// straight from the registers, every 16-byte store of a warp touches 32 lines, and the rows
+// of an item took 1.4 to 2.2 us.)
 template <bool kPartials>
-__device__ __forceinline__ void store_segment(const WinParams& P, uint32_t tO, float m, float l, float fix,
+__device__ __forceinline__ void store_segment(const WinParams& P, uint32_t tO, uint32_t out, float m, float l, float fix,
                                               bool valid, int64_t out_row, int part) {
   const float inv = l > 0.f ? 1.0f / (l + fix) : 0.f;
   const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   const int64_t rows_all = (int64_t)P.batch * P.heads_q * P.seq;
 #pragma unroll 1
-  for (int cc = 0; cc < 4; ++cc) {
-    uint32_t v[32];
+  for (int cc = 0; cc < 2; ++cc) {
+    uint32_t v[64];
     __syncwarp();
-    ptx::tmem_ld32(tO + cc * 32, v);
-    if (!valid) continue;
+    ptx::tmem_ld32x2(tO + cc * 64, tO + cc * 64 + 32, v);
     if (kPartials) {
+      if (!valid) continue;
       float4* dst = reinterpret_cast<float4*>(P.o_parts + ((int64_t)part * rows_all + out_row) * 128);
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        dst[cc * 8 + q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
-                                      __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
+      for (int q = 0; q < 16; ++q)
+        dst[cc * 16 + q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
+                                       __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
     } else {
-      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(P.o) + out_row * 128);
+      bulk_wait_read();  // the half before has left
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 8; ++q) {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           w[e] = ptx::pack_bf16x2(__uint_as_float(v[8 * q + 2 * e]) * inv, __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
-        dst[cc * 4 + q] = make_uint4(w[0], w[1], w[2], w[3]);
+        ptx::st_shared_v4(out + q * 16, w[0], w[1], w[2], w[3]);
       }
+      ptx::fence_proxy_async_smem();
+      if (valid) bulk_store(reinterpret_cast<uint8_t*>(P.o) + out_row * 256 + cc * 128, out, 128);
+      bulk_commit();
     }
   }
   if (valid) {
@@ -387,52 +472,59 @@ __device__ __forceinline__ void store_empty(const WinParams& P, bool valid, int6
 }
 
 template <bool kPartials>
-__device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t tmem, int g, int wq, int lane) {
+__device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t sbase, const Record* recs, uint32_t tmem, int g,
+                            int wq, int lane) {
   const int row = wq * 32 + lane;  // TMEM lane = query row of the tile
   const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
   const uint32_t tS = tmem + lane_off + col_s(g);
   const uint32_t tO = tmem + lane_off + col_o(g);
+  const uint32_t out = sbase + kOffOut + (uint32_t)(g * 128 + row) * kStageRow;
   RA_BOUNDS(c.status, wq >= 0 && wq < 4 && (tS & 0xFFFFu) + 128u <= kTmemCols && (tO & 0xFFFFu) + 128u <= kTmemCols &&
-                          (tS & 0xFFFFu) + kColP + 64u <= kTmemCols, 64);
+                          (tS & 0xFFFFu) + kColP + 64u <= kTmemCols && out + 128u <= sbase + kOffRec, 64);
   const float sl2 = P.scale_log2;
   uint32_t sj = 0, oj = 0;
 
-  for (int idx = blockIdx.x; idx < P.n_items; idx += gridDim.x) {
-    const WinItem it = P.items[idx];
-    if (g == 1 && it.bh1 < 0) continue;
-    const WinGroup gr = P.groups[it.group];
+  for (uint32_t u = 0;; ++u) {
+    const Record* rec = next_record(c, recs, u, kStatusTimeoutSoftmax);
+    if (rec == nullptr) return;
+    const WinItem it = rec->it;
+    const int xn = g == 1 && it.bh1 < 0 ? -1 : rec->xn;
+    if (xn < 0) {
+      release_record(c, u, lane);
+      continue;
+    }
     const int bh = g ? it.bh1 : it.bh0;
-    const int i = (g ? gr.row1 : gr.row0) + row;
-    const bool valid = i < gr.row_end;
-    const int my_pos = (int)pos_of(P.layout, P.n_shards, P.s_n, gr.shard, valid ? i : gr.row_end - 1);
-    const int64_t out_row = (int64_t)bh * P.seq + (int64_t)gr.shard * P.s_n + i;
+    const int i = (g ? it.row1 : it.row0) + row;
+    const bool valid = i < it.row_end && row < P.q.tile;
+    const int my_pos = (int)pos_of(P.q.layout, P.q.shards, P.q.s_n, it.shard, valid ? i : it.row_end - 1);
+    const int head_row = it.shard * P.q.s_n + i;
+    const int64_t out_row = (int64_t)bh * P.seq + (P.q.stripe == 1 ? head_row
+                                                                   : head_row % P.q.stripe * (P.seq / P.q.stripe) +
+                                                                         head_row / P.q.stripe);
     RA_BOUNDS(c.status, !valid || (bh >= 0 && out_row >= 0 && out_row < (int64_t)P.batch * P.heads_q * P.seq), 65);
 
     float m = -INFINITY, l = 0.f, fix = 0.f;
     bool first = true;
     int next_part = P.step_lo;  // partials: steps below are written
-    int x = ranges_from(P, gr);
-    while (range_in(P, gr, x)) {
-      const WinRange rg = P.ranges[x];
-      ++x;
-      const bool seg_end = !range_in(P, gr, x) || (kPartials && P.ranges[x].step != rg.step);
+    for (int k = 0; k < xn; ++k) {
+      const WinRange rg = range_at(P, rec, k);
+      const bool seg_end = k == xn - 1 || (kPartials && range_at(P, rec, k + 1).step != rg.step);
       if (kPartials)
         for (; next_part < rg.step; ++next_part) store_empty(P, valid, out_row, next_part - P.step_lo);
       // The row sees rows below sk and [lo, hi) of the block met (win_internal.h), and of
       // those the range's own.
-      const int layout = P.gathered ? (int)RA_LAYOUT_CONTIGUOUS : P.layout;
-      const int ns = P.gathered ? 1 : P.n_shards, bs = P.gathered ? P.seq : P.s_n;
-      const int upto = rows_le(layout, ns, bs, rg.r, my_pos);
+      const int upto = rows_le(P.k.layout, P.k.shards, P.k.s_n, rg.r, my_pos);
       const int hi = (upto < rg.end ? upto : rg.end) - rg.row0;
-      const int lo = rows_le(layout, ns, bs, rg.r, my_pos - P.window) - rg.row0;
-      const int sk = rows_le(layout, ns, bs, rg.r, P.sinks - 1) - rg.row0;
+      const int lo = rows_le(P.k.layout, P.k.shards, P.k.s_n, rg.r, my_pos - P.window) - rg.row0;
+      const int sk = rows_le(P.k.layout, P.k.shards, P.k.s_n, rg.r, P.sinks - 1) - rg.row0;
 
-      const int n = range_tiles(rg);
+      const int n = range_tiles(rg, P.k.tile);
       for (int kt = 0; kt < n; ++kt) {
-        const int y = kt * kTileRows;
+        const int y = kt * P.k.tile;
         const bool last = seg_end && kt == n - 1;
-        const int c_hi = hi - y, c_lo = lo - y;       // columns [c_lo, c_hi), and those
-        const int c_s = sk < hi ? sk - y : c_hi;      // below c_s, are seen
+        // columns [c_lo, c_hi), and those below c_s, are seen
+        const int c_hi = hi - y < P.k.tile ? hi - y : P.k.tile, c_lo = lo - y;
+        const int c_s = sk - y < c_hi ? sk - y : c_hi;
         const bool full = c_hi >= kTileRows && (c_lo <= 0 || c_s >= kTileRows);
 
         bool ok = wait_bar(c, c.bar(kSFull + g), sj & 1u, kStatusTimeoutSoftmax);
@@ -558,7 +650,7 @@ __device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t tmem, int
           ++oj;
           if (!__all_sync(0xffffffffu, ok)) return;
           ptx::tc_fence_after();
-          store_segment<kPartials>(P, tO, m, l, fix, valid, out_row, rg.step - P.step_lo);
+          store_segment<kPartials>(P, tO, out, m, l, fix, valid, out_row, rg.step - P.step_lo);
           ptx::tc_fence_before();
           next_part = rg.step + 1;
           m = -INFINITY;
@@ -570,6 +662,7 @@ __device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t tmem, int
     }
     if (kPartials)
       for (; next_part < P.step_hi; ++next_part) store_empty(P, valid, out_row, next_part - P.step_lo);
+    release_record(c, u, lane);
   }
 }
 
@@ -583,8 +676,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sgen = smem_raw + (sbase - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ctl c{sbase + kOffBar, reinterpret_cast<volatile uint32_t*>(sgen + kOffAbort), P.status};
+  Record* recs = reinterpret_cast<Record*>(sgen + kOffRec);
 
+  // The rows that shorter boxes never fill meet weights of zero: they have to be finite.
+  if (P.k.tile < kTileRows) {
+    for (uint32_t at = threadIdx.x * 16; at < kStages * kTileBytes; at += kThreads * 16)
+      ptx::st_shared_v4(sbase + kOffKV + at, 0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+  }
   if (threadIdx.x == 0) {
+    for (int s = 0; s < kItemSlots; ++s) {
+      ptx::mbar_init(c.bar(kItemFull + s), 1);
+      ptx::mbar_init(c.bar(kItemEmpty + s), kItemConsumers);
+    }
     for (int g = 0; g < 2; ++g) {
       ptx::mbar_init(c.bar(kQFull + g), 1);
       ptx::mbar_init(c.bar(kQEmpty + g), 1);
@@ -618,18 +722,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     ptx::regs_release<kRegsOther>();
     if (warp == 0) {
-      run_producer(P, c, sbase, &tq, &tk, &tv, ps);  // whole warp; one elected lane issues
+      run_producer(P, c, sbase, recs, &tq, &tk, &tv, ps, lane);  // whole warp; one elected lane issues
       __syncwarp();
     } else if (warp == 1) {
-      run_mma<kPartials>(P, c, sbase, tmem);
+      run_mma<kPartials>(P, c, sbase, recs, tmem, lane);
       // Every MMA this warp issued must retire before TMEM is freed.
       ptx::mma_commit_warp(c.bar(kDone));
       drain_bar(c, c.bar(kDone), 0);
       __syncwarp();
+    } else if (warp == 2) {
+      run_records(P, c, recs, lane);
     }
   } else {
     ptx::regs_acquire<kRegsSoftmax>();
-    run_softmax<kPartials>(P, c, tmem, (warp - 4) >> 2, warp & 3, lane);
+    run_softmax<kPartials>(P, c, sbase, recs, tmem, (warp - 4) >> 2, warp & 3, lane);
+    bulk_wait_done();  // this thread's rows have left shared memory
   }
 
   if (warp == 0 && lane == 0 && *c.abort) {  // (every lane of warp 0 holds the same counts)
@@ -670,15 +777,17 @@ EncodeTiledFn get_encoder() {
   return fn;
 }
 
-// [rows, 128] bf16 row-major, boxes of 128 rows x 64 columns, 128-byte swizzle.
-bool encode_rows(CUtensorMap* map, const void* base, int64_t rows) {
+// [heads, S, 128] bf16 rows as (element, row of a stripe, stripe, head), boxes of 64 elements
+// x the tile's rows, 128-byte swizzle.  Rows past the end of a head read as zeros.
+bool encode_view(CUtensorMap* map, const void* base, const WinView& view, int64_t seq, int64_t heads) {
   EncodeTiledFn enc = get_encoder();
   if (!enc) return false;
-  const cuuint64_t dims[2] = {128, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {128 * 2};
-  const cuuint32_t box[2] = {64, 128};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+  const uint64_t per = (uint64_t)(seq / view.stripe);
+  const cuuint64_t dims[4] = {128, (cuuint64_t)view.stripe, per, (cuuint64_t)heads};
+  const cuuint64_t strides[3] = {view.stripe == 1 ? 256 : per * 256, 256, (uint64_t)seq * 256};
+  const cuuint32_t box[4] = {64, (cuuint32_t)view.stripe, (cuuint32_t)(view.tile / view.stripe), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -701,9 +810,9 @@ cudaError_t launch_kernel(const WinParams& prm, const CUtensorMap& tq, const CUt
 cudaError_t launch_win_fwd_bf16(const WinParams& prm, const void* q, const void* k, const void* v, int grid,
                                 cudaStream_t stream, const char** why) {
   CUtensorMap tq, tk, tv;
-  const int64_t rows_q = (int64_t)prm.batch * prm.heads_q * prm.seq;
-  const int64_t rows_kv = (int64_t)prm.batch * prm.heads_kv * prm.seq;
-  if (!encode_rows(&tq, q, rows_q) || !encode_rows(&tk, k, rows_kv) || !encode_rows(&tv, v, rows_kv)) {
+  const int64_t hq = (int64_t)prm.batch * prm.heads_q, hk = (int64_t)prm.batch * prm.heads_kv;
+  if (!encode_view(&tq, q, prm.q, prm.seq, hq) || !encode_view(&tk, k, prm.k, prm.seq, hk) ||
+      !encode_view(&tv, v, prm.k, prm.seq, hk)) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }

@@ -61,38 +61,43 @@ RA_HD WinSpan win_span(int layout, int n_shards, int32_t s_n, int32_t window, in
   return s;
 }
 
-// Forward work list of a windowed plan.  A group is the query rows of one work item
-// (one or two tiles of up to 128 rows) with the key tiles they meet; an item is a
-// group for one or two heads.
-struct alignas(16) WinGroup {
-  int32_t shard, row0;   // tile 0: local rows row0 .. min(row0 + 128, row_end)
-  int32_t row1;          // tile 1's first row (row0 when the item pairs two heads, -1: none)
-  int32_t row_end;
-  int32_t minpos, maxpos;
-  int32_t range0, n_ranges;  // its key ranges
+// How the rows of a head are walked: as `shards` shards of s_n rows in their layout, or
+// (shards == 1) in the order of their positions.  stripe > 1: position x lies at row
+// (x mod stripe) * (S / stripe) + x / stripe, a striped layout walked in natural order; its
+// tiles begin at multiples of the stripe and hold `tile` rows, the largest multiple of it
+// up to 128 (one tensor-map box of stripe x tile/stripe rows).
+struct WinView {
+  int32_t layout, shards, s_n;
+  int32_t stripe, tile;
 };
-// Key rows [row0, end) of shard r, met at ring step `step` in tiles of 128 from row0 (the
-// rows of the last tile from `end` on belong to another range or to nobody).
+
+// Forward work item of a windowed plan: one or two tiles of query rows (one tile for two
+// heads, or two consecutive tiles of one head) with the key ranges they meet.
+struct alignas(16) WinItem {
+  int32_t bh0, bh1;          // b*Hq + h of tile 0 and of tile 1 (-1: one tile)
+  int32_t shard, row0;       // tile 0: local rows row0 .. min(row0 + tile, row_end)
+  int32_t row1, row_end;     // tile 1's first row
+  int32_t range0, n_ranges;  // its key ranges
+  int32_t n_tiles;           // key tiles over all of them
+  int32_t pad[3];
+};
+// Key rows [row0, end) of shard r, met at ring step `step` in tiles from row0 on (the rows
+// of the last tile from `end` on belong to another range or to nobody).
 struct alignas(16) WinRange {
   int32_t step, r, row0, end;
 };
-RA_HD int32_t range_tiles(const WinRange& rg) { return (rg.end - rg.row0 + kTileRows - 1) / kTileRows; }
-struct alignas(16) WinItem {
-  int32_t group, bh0, bh1;  // bh = b*Hq + h of tile 0 and of tile 1 (-1: one tile)
-  int32_t n_tiles;          // key tiles over all its ranges
-};
+RA_HD int32_t range_tiles(const WinRange& rg, int32_t tile) { return (rg.end - rg.row0 + tile - 1) / tile; }
 
 struct WinParams {
-  int32_t batch, heads_q, heads_kv, group, head_dim, n_shards, layout;
+  int32_t batch, heads_q, heads_kv, group, head_dim;
+  WinView q, k;
   int32_t window, sinks;
-  int32_t seq, s_n;
+  int32_t seq;
   int32_t n_items;
   float scale, scale_log2;
   int32_t step_lo, step_hi;  // ring steps of this launch
   int32_t kv_rotated;        // as FwdParams::kv_rotated
-  int32_t gathered;          // as FwdParams::gathered
   const WinItem* items;
-  const WinGroup* groups;
   const WinRange* ranges;
   void* o;
   float* lse;
