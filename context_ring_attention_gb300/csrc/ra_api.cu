@@ -332,9 +332,12 @@ int32_t add_ranges(ra_plan_s* pl, const ra::WinView& k, int p, int32_t minpos, i
   const int N = k.shards;
   int32_t tiles = 0;
   auto add = [&](int step, int r, int32_t from, int32_t to) {
-    if (to <= from) return;
-    pl->win_ranges.push_back({step, r, from / k.stripe * k.stripe, to});
-    tiles += ra::range_tiles(pl->win_ranges.back(), k.tile);
+    while (from < to) {  // (a range stays within a run of equally spaced positions)
+      const int32_t end = std::min(to, ra::run_end(k.layout, k.s_n, from)), row0 = from / k.stripe * k.stripe;
+      pl->win_ranges.push_back({(int16_t)step, (int16_t)r, row0, end, (int32_t)ra::pos_of(k.layout, N, k.s_n, r, row0)});
+      tiles += ra::range_tiles(pl->win_ranges.back(), k.tile);
+      from = end;
+    }
   };
   for (int t = 0; t < N; ++t) {
     const int r = N == 1 ? 0 : (p - t + N) % N;
@@ -366,6 +369,8 @@ ra_plan_s::WinList add_win_list(ra_plan_s* pl, const ra::WinView& q, const ra::W
       x.item.row_end = ra::run_end(q.layout, q.s_n, row);
       x.item.row1 = head_pairs ? row : (row + q.tile < x.item.row_end ? row + q.tile : -1);
       const int32_t end = std::min((x.item.row1 < 0 ? row : x.item.row1) + q.tile, x.item.row_end);
+      x.item.pos0 = pos(p, row);
+      x.item.pos1 = x.item.row1 < 0 ? 0 : pos(p, x.item.row1);
       x.item.range0 = (int32_t)pl->win_ranges.size();
       x.tiles = x.item.n_tiles = add_ranges(pl, k, p, pos(p, row), pos(p, end - 1));
       x.item.n_ranges = (int32_t)pl->win_ranges.size() - x.item.range0;
@@ -499,8 +504,8 @@ void build_win_schedule(ra_plan_s* pl) {
   // into as few tiles as they can: the fused forward of contiguous shards (which are one
   // run of rows) and of striped ones.  A stripe of more than 128 shards exceeds a tile, and
   // zigzag chunks are runs of consecutive positions as they are.
-  const ra::WinView ring{pb.layout, N, s_n, 1, ra::kTileRows};
-  ra::WinView natural{RA_LAYOUT_CONTIGUOUS, 1, (int32_t)pb.seq, 1, ra::kTileRows};
+  const ra::WinView ring{pb.layout, N, s_n, 1, ra::kTileRows, pb.layout == RA_LAYOUT_STRIPED ? N : 1};
+  const ra::WinView natural{RA_LAYOUT_CONTIGUOUS, 1, (int32_t)pb.seq, 1, ra::kTileRows, 1};
   ra::WinView rows = natural;
   if (pb.layout == RA_LAYOUT_STRIPED && N > 1) {
     rows.stripe = N;
@@ -606,8 +611,8 @@ ra_status launch_win(ra_plan_s* plan, const ra::FwdParams& prm, const void* q, c
   w.q = list.q;
   w.k = list.k;
   if (pb.dtype != RA_DTYPE_BF16) {  // rows, not items
-    w.q = {pb.layout, pb.n_shards, (int32_t)plan->s_n, 1, 0};
-    w.k = prm.gathered ? ra::WinView{RA_LAYOUT_CONTIGUOUS, 1, (int32_t)pb.seq, 1, 0} : w.q;
+    w.q = {pb.layout, pb.n_shards, (int32_t)plan->s_n, 1, 0, 0};
+    w.k = prm.gathered ? ra::WinView{RA_LAYOUT_CONTIGUOUS, 1, (int32_t)pb.seq, 1, 0, 0} : w.q;
   }
   w.window = plan->window;
   w.sinks = plan->sinks;

@@ -146,16 +146,6 @@ __device__ __forceinline__ void tma_load_4d_warp_hint(uint32_t dst, const CUtens
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(0), "r"(i), "r"(bh), "l"(policy)
       : "memory");
 }
-// Bulk copy shared -> global of this thread, and the waits for its copies: until they have
-// read shared memory, and until they are done.
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // ------------------------------------------------------------------- records --
 // Warp 2 brings the items and their ranges of this CTA into shared memory, a few items
 // ahead: reading them where they are needed took each role 1 to 2 us at every item.
@@ -420,15 +410,16 @@ __device__ void run_mma(const WinParams& P, const Ctl& c, uint32_t sbase, const 
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : ~(~0u << n)); }
 
 // The finished rows of a segment.  bf16 rows go out through shared memory, half a row at a
-// time: a thread writes its 128 bytes there and sends them on as one bulk copy.  (Written
-// straight from the registers, every 16-byte store of a warp touches 32 lines, and the rows
-// of an item took 1.4 to 2.2 us.)
+// time, so that 8 lanes write 128 consecutive bytes: written from where they stand, every
+// 16-byte store of a warp touches 32 lines, and the rows of an item took 1.4 to 2.2 us.
+// (Sent from shared memory as a bulk copy per row they took 2.6.)
 template <bool kPartials>
-__device__ __forceinline__ void store_segment(const WinParams& P, uint32_t tO, uint32_t out, float m, float l, float fix,
-                                              bool valid, int64_t out_row, int part) {
+__device__ __forceinline__ void store_segment(const WinParams& P, uint32_t tO, uint8_t* stage, float m, float l,
+                                              float fix, bool valid, int64_t out_row, int part, int lane) {
   const float inv = l > 0.f ? 1.0f / (l + fix) : 0.f;
   const float lse = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   const int64_t rows_all = (int64_t)P.batch * P.heads_q * P.seq;
+  const int to = valid ? (int)out_row : -1;  // (rows fit in 31 bits)
 #pragma unroll 1
   for (int cc = 0; cc < 2; ++cc) {
     uint32_t v[64];
@@ -442,18 +433,22 @@ __device__ __forceinline__ void store_segment(const WinParams& P, uint32_t tO, u
         dst[cc * 16 + q] = make_float4(__uint_as_float(v[4 * q]) * inv, __uint_as_float(v[4 * q + 1]) * inv,
                                        __uint_as_float(v[4 * q + 2]) * inv, __uint_as_float(v[4 * q + 3]) * inv);
     } else {
-      bulk_wait_read();  // the half before has left
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           w[e] = ptx::pack_bf16x2(__uint_as_float(v[8 * q + 2 * e]) * inv, __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
-        ptx::st_shared_v4(out + q * 16, w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(stage + lane * kStageRow + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      ptx::fence_proxy_async_smem();
-      if (valid) bulk_store(reinterpret_cast<uint8_t*>(P.o) + out_row * 256 + cc * 128, out, 128);
-      bulk_commit();
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {  // rows 4q .. 4q + 3
+        const int r = 4 * q + (lane >> 3);
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + r * kStageRow + (lane & 7) * 16);
+        const int row = __shfl_sync(0xffffffffu, to, r);
+        if (row >= 0) reinterpret_cast<uint4*>(P.o)[(int64_t)row * 16 + cc * 8 + (lane & 7)] = x;
+      }
     }
   }
   if (valid) {
@@ -472,15 +467,14 @@ __device__ __forceinline__ void store_empty(const WinParams& P, bool valid, int6
 }
 
 template <bool kPartials>
-__device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t sbase, const Record* recs, uint32_t tmem, int g,
+__device__ void run_softmax(const WinParams& P, const Ctl& c, uint8_t* stage, const Record* recs, uint32_t tmem, int g,
                             int wq, int lane) {
   const int row = wq * 32 + lane;  // TMEM lane = query row of the tile
   const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
   const uint32_t tS = tmem + lane_off + col_s(g);
   const uint32_t tO = tmem + lane_off + col_o(g);
-  const uint32_t out = sbase + kOffOut + (uint32_t)(g * 128 + row) * kStageRow;
   RA_BOUNDS(c.status, wq >= 0 && wq < 4 && (tS & 0xFFFFu) + 128u <= kTmemCols && (tO & 0xFFFFu) + 128u <= kTmemCols &&
-                          (tS & 0xFFFFu) + kColP + 64u <= kTmemCols && out + 128u <= sbase + kOffRec, 64);
+                          (tS & 0xFFFFu) + kColP + 64u <= kTmemCols, 64);
   const float sl2 = P.scale_log2;
   uint32_t sj = 0, oj = 0;
 
@@ -496,7 +490,7 @@ __device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t sbase, co
     const int bh = g ? it.bh1 : it.bh0;
     const int i = (g ? it.row1 : it.row0) + row;
     const bool valid = i < it.row_end && row < P.q.tile;
-    const int my_pos = (int)pos_of(P.q.layout, P.q.shards, P.q.s_n, it.shard, valid ? i : it.row_end - 1);
+    const int my_pos = (g ? it.pos1 : it.pos0) + row * P.q.apart;  // (of rows that are not valid: any)
     const int head_row = it.shard * P.q.s_n + i;
     const int64_t out_row = (int64_t)bh * P.seq + (P.q.stripe == 1 ? head_row
                                                                    : head_row % P.q.stripe * (P.seq / P.q.stripe) +
@@ -511,12 +505,17 @@ __device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t sbase, co
       const bool seg_end = k == xn - 1 || (kPartials && range_at(P, rec, k + 1).step != rg.step);
       if (kPartials)
         for (; next_part < rg.step; ++next_part) store_empty(P, valid, out_row, next_part - P.step_lo);
-      // The row sees rows below sk and [lo, hi) of the block met (win_internal.h), and of
-      // those the range's own.
-      const int upto = rows_le(P.k.layout, P.k.shards, P.k.s_n, rg.r, my_pos);
-      const int hi = (upto < rg.end ? upto : rg.end) - rg.row0;
-      const int lo = rows_le(P.k.layout, P.k.shards, P.k.s_n, rg.r, my_pos - P.window) - rg.row0;
-      const int sk = rows_le(P.k.layout, P.k.shards, P.k.s_n, rg.r, P.sinks - 1) - rg.row0;
+      // Of the range's rows the query sees those below sk and [lo, hi): rows at positions
+      // up to its own, and not up to window positions before it unless they are sinks.
+      const int rows = rg.end - rg.row0;
+      const int d_hi = my_pos - rg.pos0, d_lo = d_hi - P.window, d_sk = P.sinks - 1 - rg.pos0;
+      int hi = d_hi + 1, lo = d_lo + 1, sk = d_sk + 1;
+      if (P.k.apart > 1) {
+        hi = d_hi < 0 ? 0 : d_hi / P.k.apart + 1;
+        lo = d_lo < 0 ? 0 : d_lo / P.k.apart + 1;
+        sk = d_sk < 0 ? 0 : d_sk / P.k.apart + 1;
+      }
+      hi = hi < rows ? hi : rows;
 
       const int n = range_tiles(rg, P.k.tile);
       for (int kt = 0; kt < n; ++kt) {
@@ -650,7 +649,7 @@ __device__ void run_softmax(const WinParams& P, const Ctl& c, uint32_t sbase, co
           ++oj;
           if (!__all_sync(0xffffffffu, ok)) return;
           ptx::tc_fence_after();
-          store_segment<kPartials>(P, tO, out, m, l, fix, valid, out_row, rg.step - P.step_lo);
+          store_segment<kPartials>(P, tO, stage, m, l, fix, valid, out_row, rg.step - P.step_lo, lane);
           ptx::tc_fence_before();
           next_part = rg.step + 1;
           m = -INFINITY;
@@ -735,8 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     ptx::regs_acquire<kRegsSoftmax>();
-    run_softmax<kPartials>(P, c, sbase, recs, tmem, (warp - 4) >> 2, warp & 3, lane);
-    bulk_wait_done();  // this thread's rows have left shared memory
+    run_softmax<kPartials>(P, c, sgen + kOffOut + (warp - 4) * 32 * kStageRow, recs, tmem, (warp - 4) >> 2, warp & 3, lane);
   }
 
   if (warp == 0 && lane == 0 && *c.abort) {  // (every lane of warp 0 holds the same counts)

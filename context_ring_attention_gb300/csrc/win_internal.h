@@ -69,6 +69,7 @@ RA_HD WinSpan win_span(int layout, int n_shards, int32_t s_n, int32_t window, in
 struct WinView {
   int32_t layout, shards, s_n;
   int32_t stripe, tile;
+  int32_t apart;  // positions between neighbouring rows (shards, when striped shard by shard)
 };
 
 // Forward work item of a windowed plan: one or two tiles of query rows (one tile for two
@@ -79,14 +80,20 @@ struct alignas(16) WinItem {
   int32_t row1, row_end;     // tile 1's first row
   int32_t range0, n_ranges;  // its key ranges
   int32_t n_tiles;           // key tiles over all of them
-  int32_t pad[3];
+  int32_t pos0, pos1;        // positions of the tiles' first rows
+  int32_t pad;
 };
 // Key rows [row0, end) of shard r, met at ring step `step` in tiles from row0 on (the rows
-// of the last tile from `end` on belong to another range or to nobody).
+// of the last tile from `end` on belong to another range or to nobody).  Row row0 + x is at
+// position pos0 + x * apart.
 struct alignas(16) WinRange {
-  int32_t step, r, row0, end;
+  int16_t step, r;
+  int32_t row0, end, pos0;
 };
-RA_HD int32_t range_tiles(const WinRange& rg, int32_t tile) { return (rg.end - rg.row0 + tile - 1) / tile; }
+RA_HD int32_t range_tiles(const WinRange& rg, int32_t tile) {
+  const int32_t rows = rg.end - rg.row0;
+  return tile == kTileRows ? (rows + kTileRows - 1) / kTileRows : (rows + tile - 1) / tile;
+}
 
 struct WinParams {
   int32_t batch, heads_q, heads_kv, group, head_dim;
