@@ -50,7 +50,6 @@
 
 #include "bwd_internal.h"
 #include "sm100_ptx.cuh"
-#include "win_internal.h"
 
 namespace ra {
 namespace {
@@ -174,58 +173,18 @@ __global__ void __launch_bounds__(32) wait_selftest_kernel(uint32_t* status, uin
 // from the first that sees key position kmin.  Pass 1 (item = query tile of shard
 // p whose last query sits at position maxq): step t meets shard r = (p - t) mod N,
 // key tiles 0..last_le(r, maxq)/64.
-// Windowed plans (kWin): a key tile's queries end window - 1 positions past its last
-// key (none end early when the tile holds a sink); a query tile's keys are the tiles of
-// the sinks, then, `jump` tiles further, those from the first key its first query sees.
-// An item's tile stops at run_end, and WorkItem::pad holds the position at its other
-// end: of its last key (pass 0), of its first query (pass 1).
 struct Walk {
   int t, g, it, lo, hi, shard;
-  int first, jump;  // kWin, pass 1: tile `it` is it, or it + jump from `first` on
 };
-
-template <bool kWin>
-__device__ __forceinline__ int walk_tile(const Walk& w) {
-  return kWin && w.it >= w.first ? w.it + w.jump : w.it;
-}
-
-// Last position whose query sees the key at position P.
-__device__ __forceinline__ int last_seeing(const BwdParams& P, int pos) {
-  const int64_t far = (int64_t)pos + P.window - 1;
-  return (int)(pos < P.sinks || far > P.seq - 1 ? P.seq - 1 : far);
-}
 
 __device__ __forceinline__ int n_stream_tiles(const BwdParams& P) {
   return (int)((P.s_n + kStreamRows - 1) / kStreamRows);
 }
 
-template <int kPass, bool kWin>
+template <int kPass>
 __device__ __forceinline__ void walk_step_bounds(Walk& w, const BwdParams& P, const WorkItem& it) {
   const int N = P.n_shards;
-  if (kWin) {
-    const int s_n = (int)P.s_n;
-    w.first = w.jump = 0;
-    if (kPass == 0) {
-      w.shard = (it.shard + w.t) % N;
-      const int kmax = it.pad, kmin = it.maxq;
-      // (positions rise along the tile: its first key is a sink if any is)
-      const int lo = rows_le(P.layout, N, s_n, w.shard, kmin - 1);
-      const int hi = rows_le(P.layout, N, s_n, w.shard, last_seeing(P, kmin < P.sinks ? kmin : kmax));
-      w.lo = lo / kStreamRows;
-      w.hi = hi > lo ? (hi + kStreamRows - 1) / kStreamRows : w.lo;
-    } else {
-      w.shard = (it.shard - w.t + N) % N;
-      const WinSpan sp = win_span(P.layout, N, s_n, P.window, P.sinks, w.shard, it.pad, it.maxq);
-      w.first = w.hi = (sp.first + kStreamRows - 1) / kStreamRows;
-      w.lo = 0;
-      if (sp.hi > sp.lo) {
-        const int from = sp.lo / kStreamRows, to = (sp.hi + kStreamRows - 1) / kStreamRows;
-        if (w.first > from) w.first = from;  // the window starts in the sinks' last tile
-        w.jump = from - w.first;
-        w.hi = w.first + (to - from);
-      }
-    }
-  } else if (kPass == 0) {
+  if (kPass == 0) {
     w.shard = (it.shard + w.t) % N;
     w.hi = n_stream_tiles(P);
     w.lo = 0;
@@ -246,7 +205,7 @@ __device__ __forceinline__ void walk_step_bounds(Walk& w, const BwdParams& P, co
 }
 
 // Advance to the next non-empty (t, g) range starting at the current one.
-template <int kPass, bool kWin>
+template <int kPass>
 __device__ __forceinline__ void walk_settle(Walk& w, const BwdParams& P, const WorkItem& it) {
   const int groups = kPass == 0 ? P.group : 1;
   while (w.t < P.n_shards) {
@@ -257,33 +216,33 @@ __device__ __forceinline__ void walk_settle(Walk& w, const BwdParams& P, const W
     }
     w.g = 0;
     if (++w.t >= P.n_shards) return;
-    walk_step_bounds<kPass, kWin>(w, P, it);
+    walk_step_bounds<kPass>(w, P, it);
     w.it = w.lo;
   }
 }
 
-template <int kPass, bool kWin>
+template <int kPass>
 __device__ __forceinline__ void walk_begin(Walk& w, const BwdParams& P, const WorkItem& it) {
   w.t = 0;
   w.g = 0;
-  walk_step_bounds<kPass, kWin>(w, P, it);
+  walk_step_bounds<kPass>(w, P, it);
   w.it = w.lo;
-  walk_settle<kPass, kWin>(w, P, it);
+  walk_settle<kPass>(w, P, it);
 }
 
-template <int kPass, bool kWin>
+template <int kPass>
 __device__ __forceinline__ void walk_next(Walk& w, const BwdParams& P, const WorkItem& it) {
   ++w.it;
-  walk_settle<kPass, kWin>(w, P, it);
+  walk_settle<kPass>(w, P, it);
 }
 
 // Number of streamed tiles of an item (the walk's length).
-template <int kPass, bool kWin>
+template <int kPass>
 __device__ __forceinline__ int item_tiles(const BwdParams& P, const WorkItem& it) {
   int n = 0;
   Walk w;
   for (w.t = 0; w.t < P.n_shards; ++w.t) {
-    walk_step_bounds<kPass, kWin>(w, P, it);
+    walk_step_bounds<kPass>(w, P, it);
     if (w.hi > w.lo) n += (w.hi - w.lo) * (kPass == 0 ? P.group : 1);
   }
   return n;
@@ -331,7 +290,7 @@ struct ProducerState {
   uint32_t fix_issued;  // items whose own tiles were issued
 };
 
-template <int kPass, bool kWin>
+template <int kPass>
 __device__ void run_producer(const BwdParams& P, const Ctl& c, uint32_t sbase, volatile int32_t* slots,
                              const CUtensorMap* tx0, const CUtensorMap* tx1, const CUtensorMap* ty0,
                              const CUtensorMap* ty1, ProducerState& st) {
@@ -386,14 +345,13 @@ __device__ void run_producer(const BwdParams& P, const Ctl& c, uint32_t sbase, v
       h_base = (it.bh0 % P.heads_q) / P.group;
     }
     Walk w;
-    walk_begin<kPass, kWin>(w, P, it);
+    walk_begin<kPass>(w, P, it);
     bool ok = true;
     while (w.t < P.n_shards) {
       const int64_t head_row = kPass == 0 ? ((int64_t)b * P.heads_q + h_base + w.g) * P.seq
                                           : ((int64_t)b * P.heads_kv + h_base) * P.seq;
-      const int tile = walk_tile<kWin>(w);
-      const int32_t y = (int32_t)(head_row + (int64_t)w.shard * P.s_n + (int64_t)tile * kStreamRows);
-      RA_BOUNDS(c.status, w.shard >= 0 && w.shard < P.n_shards && tile >= 0 && (int64_t)tile * kStreamRows < P.s_n &&
+      const int32_t y = (int32_t)(head_row + (int64_t)w.shard * P.s_n + (int64_t)w.it * kStreamRows);
+      RA_BOUNDS(c.status, w.shard >= 0 && w.shard < P.n_shards && w.it >= 0 && (int64_t)w.it * kStreamRows < P.s_n &&
                               w.g >= 0 && w.g < (kPass == 0 ? P.group : 1), 23);
       RA_BOUNDS(c.status, y >= 0 && y < (kPass == 0 ? rows_q : rows_kv), 24);
       const uint32_t s = s_it % C::kStages, phase = (s_it / C::kStages) & 1u;
@@ -408,17 +366,17 @@ __device__ void run_producer(const BwdParams& P, const Ctl& c, uint32_t sbase, v
       ptx::tma_load_2d_warp_hint(dst + kStrBytes, ty1, c.bar(kStFull + (int)s), 0, y, keep);
       ptx::tma_load_2d_warp_hint(dst + kStrBytes + kStrHalf, ty1, c.bar(kStFull + (int)s), 64, y, keep);
       RA_BOUNDS(c.status,
-                kPass != 0 || bwd_scalar_index((int64_t)b * P.heads_q + h_base + w.g, w.shard, (int64_t)tile * kStreamRows,
+                kPass != 0 || bwd_scalar_index((int64_t)b * P.heads_q + h_base + w.g, w.shard, (int64_t)w.it * kStreamRows,
                                                P.n_shards, P.n64) + 128 <=
                                   (int64_t)P.batch * P.heads_q * P.n_shards * P.n64 * 128,
                 25);
       if (kPass == 0)  // the tile's 64 lse2 and 64 D values (one 512-byte block)
         ptx::bulk_load_warp(dst + 2 * kStrBytes,
                             P.lse2d + bwd_scalar_index((int64_t)b * P.heads_q + h_base + w.g, w.shard,
-                                                       (int64_t)tile * kStreamRows, P.n_shards, P.n64),
+                                                       (int64_t)w.it * kStreamRows, P.n_shards, P.n64),
                             kLseBytes, c.bar(kStFull + (int)s));
       st.str_issued = ++s_it;
-      walk_next<kPass, kWin>(w, P, it);
+      walk_next<kPass>(w, P, it);
     }
     if (!ok) break;
     if (P.round_sync) {
@@ -461,7 +419,7 @@ __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a_tmem, uint32_t b
                              (accumulate || kk > 0) ? 1u : 0u);
 }
 
-template <int kPass, bool kWin>
+template <int kPass>
 __device__ void run_mma(const BwdParams& P, const Ctl& c, uint32_t sbase, volatile int32_t* slots, uint32_t tmem) {
   using C = Cfg<kPass>;
   constexpr uint32_t NB = (uint32_t)C::kBufs;
@@ -488,7 +446,7 @@ __device__ void run_mma(const BwdParams& P, const Ctl& c, uint32_t sbase, volati
     const int idx = next_item(c, slots, u, lane);
     if (idx < 0) break;
     const WorkItem it = P.items[idx];
-    const uint32_t n = (uint32_t)item_tiles<kPass, kWin>(P, it);
+    const uint32_t n = (uint32_t)item_tiles<kPass>(P, it);
     if (!__all_sync(0xffffffffu, wait_bar(c, c.bar(kFixFull), u & 1u, kStatusTimeoutMma))) return;
     ptx::tc_fence_after();  // pass 1: Q and dO were stored into tensor memory by other warps
     // Run NB - 1 tiles ahead: buffer (J + NB - 1) % NB was last used by tile J - 1,
@@ -561,7 +519,7 @@ __device__ __forceinline__ void p_ds_pair(float2 s2, float2 dp2, float2 l2, floa
   dw = ptx::pack_bf16x2(ds.x, ds.y);
 }
 
-template <int kPass, bool kWin>
+template <int kPass>
 __device__ void run_elementwise(const BwdParams& P, const Ctl& c, const uint8_t* sgen, volatile int32_t* slots,
                                 uint32_t tmem, int g, int wq, int lane) {
   using C = Cfg<kPass>;
@@ -575,11 +533,10 @@ __device__ void run_elementwise(const BwdParams& P, const Ctl& c, const uint8_t*
     const int idx = next_item(c, slots, u, lane);
     if (idx < 0) break;
     const WorkItem it = P.items[idx];
-    const uint32_t n = (uint32_t)item_tiles<kPass, kWin>(P, it);
+    const uint32_t n = (uint32_t)item_tiles<kPass>(P, it);
     const int64_t i_own = (int64_t)it.row0 + row;  // local row of the item's own tile
-    const int64_t own_end = kWin ? run_end(P.layout, (int)P.s_n, it.row0) : P.s_n;
-    const bool valid = i_own < own_end;
-    const int64_t my_pos = pos_of(P.layout, N, P.s_n, it.shard, valid ? i_own : own_end - 1);
+    const bool valid = i_own < P.s_n;
+    const int64_t my_pos = pos_of(P.layout, N, P.s_n, it.shard, valid ? i_own : P.s_n - 1);
     const int64_t out_row = (int64_t)it.bh0 * P.seq + (int64_t)it.shard * P.s_n + i_own;
     RA_BOUNDS(c.status,
               !valid || (out_row >= 0 && out_row < (int64_t)P.batch * (kPass == 0 ? P.heads_kv : P.heads_q) * P.seq), 27);
@@ -612,35 +569,18 @@ __device__ void run_elementwise(const BwdParams& P, const Ctl& c, const uint8_t*
     }
 
     Walk w;
-    walk_begin<kPass, kWin>(w, P, it);
+    walk_begin<kPass>(w, P, it);
     for (uint32_t i = 0; i < n; ++i) {
       const uint32_t J = s_it + i;
-      const int64_t tile_lo = (int64_t)walk_tile<kWin>(w) * kStreamRows;  // first local row of the streamed tile
+      const int64_t tile_lo = (int64_t)w.it * kStreamRows;  // first local row of the streamed tile
       const int shard = w.shard;
-      walk_next<kPass, kWin>(w, P, it);
+      walk_next<kPass>(w, P, it);
       if ((int)(J & 1u) != g) continue;
       // Columns [c_lo, c_hi) of this tile are live for this row.
       int c_lo = 0;
       const int64_t left = P.s_n - tile_lo;
       int c_hi = left < kStreamRows ? (int)left : kStreamRows;
-      int c_s = 0;  // kWin, pass 1: columns below it are sinks, live as well
-      if (kWin) {
-        const int left32 = c_hi;
-        auto in_tile = [&](int row) {
-          const int x = row - (int)tile_lo;
-          return x < 0 ? 0 : (x > left32 ? left32 : x);
-        };
-        if (kPass == 0) {
-          c_lo = in_tile(rows_le(P.layout, N, (int)P.s_n, shard, (int)my_pos - 1));
-          c_hi = in_tile(rows_le(P.layout, N, (int)P.s_n, shard, last_seeing(P, (int)my_pos)));
-        } else {
-          c_lo = in_tile(rows_le(P.layout, N, (int)P.s_n, shard, (int)my_pos - P.window));
-          c_hi = in_tile(rows_le(P.layout, N, (int)P.s_n, shard, (int)my_pos));
-          c_s = in_tile(rows_le(P.layout, N, (int)P.s_n, shard, P.sinks - 1));
-          c_s = c_s < c_hi ? c_s : c_hi;
-          if (c_s >= c_lo) c_lo = 0;
-        }
-      } else if (P.causal) {
+      if (P.causal) {
         if (kPass == 0) {  // queries of `shard` at or after this key's position
           const int64_t f = first_ge(P.layout, N, P.s_n, shard, my_pos) - tile_lo;
           c_lo = f < 0 ? 0 : (f > kStreamRows ? kStreamRows : (int)f);
@@ -674,10 +614,8 @@ __device__ void run_elementwise(const BwdParams& P, const Ctl& c, const uint8_t*
             L = make_float4(own_l.x, own_l.x, own_l.x, own_l.x);
             D = make_float4(own_d.x, own_d.x, own_d.x, own_d.x);
           }
-          auto live = [&](int cc) {
-            return full || (cc >= c_lo && cc < c_hi) || (kWin && kPass == 1 && cc < c_s);
-          };
-          const bool a0 = live(c0), a1 = live(c0 + 1), b0 = live(c0 + 2), b1 = live(c0 + 3);
+          const bool a0 = full || (c0 >= c_lo && c0 < c_hi), a1 = full || (c0 + 1 >= c_lo && c0 + 1 < c_hi);
+          const bool b0 = full || (c0 + 2 >= c_lo && c0 + 2 < c_hi), b1 = full || (c0 + 3 >= c_lo && c0 + 3 < c_hi);
           const int r0 = 4 * q;
           p_ds_pair(make_float2(__uint_as_float(raw[r0]), __uint_as_float(raw[r0 + 1])),
                     make_float2(__uint_as_float(raw[32 + r0]), __uint_as_float(raw[32 + r0 + 1])),
@@ -714,7 +652,7 @@ __device__ void run_elementwise(const BwdParams& P, const Ctl& c, const uint8_t*
   }
 }
 
-template <int kPass, bool kWin>
+template <int kPass>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_bf16_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ CUtensorMap tx1,
                     const __grid_constant__ CUtensorMap ty0, const __grid_constant__ CUtensorMap ty1,
@@ -771,17 +709,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     ptx::regs_release<kRegsOther>();
     if (warp == 0) {
-      run_producer<kPass, kWin>(P, c, sbase, slots, &tx0, &tx1, &ty0, &ty1, ps);
+      run_producer<kPass>(P, c, sbase, slots, &tx0, &tx1, &ty0, &ty1, ps);
       __syncwarp();
     } else if (warp == 1) {
-      run_mma<kPass, kWin>(P, c, sbase, slots, tmem);
+      run_mma<kPass>(P, c, sbase, slots, tmem);
       ptx::mma_commit_warp(c.bar(kDone));
       drain_bar(c, c.bar(kDone), 0);
       __syncwarp();
     }
   } else {
     ptx::regs_acquire<kRegsCompute>();
-    run_elementwise<kPass, kWin>(P, c, sgen, slots, tmem, (warp - 4) >> 2, warp & 3, lane);
+    run_elementwise<kPass>(P, c, sgen, slots, tmem, (warp - 4) >> 2, warp & 3, lane);
   }
 
   if (warp == 0 && lane == 0 && *c.abort) {
@@ -834,12 +772,12 @@ bool encode_bf16(CUtensorMap* map, const void* base, int64_t rows, uint32_t box_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kPass, bool kWin>
+template <int kPass>
 cudaError_t launch_pass(const BwdParams& prm, const CUtensorMap& tx0, const CUtensorMap& tx1, const CUtensorMap& ty0,
                         const CUtensorMap& ty1, int grid, cudaStream_t stream, const char** why) {
   using C = Cfg<kPass>;
   static std::atomic<int> ready[kMaxDevices];
-  cudaError_t e = prepare_once(bwd_bf16_kernel<kPass, kWin>, ready, kThreads, 128 * kRegsOther + 256 * kRegsCompute,
+  cudaError_t e = prepare_once(bwd_bf16_kernel<kPass>, ready, kThreads, 128 * kRegsOther + 256 * kRegsCompute,
                                (int)C::kSmemBytes, why);
   if (e != cudaSuccess) return e;
   if (prm.round_sync) {
@@ -854,10 +792,10 @@ cudaError_t launch_pass(const BwdParams& prm, const CUtensorMap& tx0, const CUte
     coop[0].val.cooperative = 1;
     cfg.attrs = coop;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, bwd_bf16_kernel<kPass, kWin>, tx0, tx1, ty0, ty1, prm);
+    e = cudaLaunchKernelEx(&cfg, bwd_bf16_kernel<kPass>, tx0, tx1, ty0, ty1, prm);
     if (e == cudaSuccess) e = cudaGetLastError();
   } else {
-    bwd_bf16_kernel<kPass, kWin><<<grid, kThreads, C::kSmemBytes, stream>>>(tx0, tx1, ty0, ty1, prm);
+    bwd_bf16_kernel<kPass><<<grid, kThreads, C::kSmemBytes, stream>>>(tx0, tx1, ty0, ty1, prm);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) *why = "tensor-core backward launch failed";
@@ -887,11 +825,8 @@ cudaError_t launch_bwd_bf16(int pass, const BwdParams& prm, const void* q, const
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }
-  if (prm.window > 0)
-    return pass == 0 ? launch_pass<0, true>(prm, a, b, y0, y1, grid, stream, why)
-                     : launch_pass<1, true>(prm, a, b, y0, y1, grid, stream, why);
-  return pass == 0 ? launch_pass<0, false>(prm, a, b, y0, y1, grid, stream, why)
-                   : launch_pass<1, false>(prm, a, b, y0, y1, grid, stream, why);
+  return pass == 0 ? launch_pass<0>(prm, a, b, y0, y1, grid, stream, why)
+                   : launch_pass<1>(prm, a, b, y0, y1, grid, stream, why);
 }
 
 }  // namespace ra

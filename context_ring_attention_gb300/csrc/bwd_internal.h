@@ -35,7 +35,6 @@ struct BwdParams {
   const WorkItem* items;
   uint32_t* status;
   uint32_t* item_counter;
-  int32_t window, sinks;  // windowed plans (win_internal.h); window 0: the whole causal prefix
 };
 
 // Launchers (each returns cudaGetLastError() of its launch).

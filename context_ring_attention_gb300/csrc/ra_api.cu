@@ -61,6 +61,16 @@ struct ra_plan_s {
   } win_lists[3] = {};
   std::vector<ra::WinItem> win_items;
   std::vector<ra::WinRange> win_ranges;
+  // Backward: pass 0's items (key tiles), then pass 1's (query tiles); the key tiles that were
+  // cut, and the floats of scratch for the rows' scalars and for their parts.
+  std::vector<ra::WinBwdItem> win_bwd_items;
+  std::vector<ra::WinBwdRange> win_bwd_ranges;
+  std::vector<ra::WinBwdSplit> win_splits;
+  ra::WinView win_own{}, win_str{};
+  int64_t n_win_bwd_kv = 0, win_scalars = 0, win_parts = 0;
+  ra::WinBwdItem* d_win_bwd_items = nullptr;
+  ra::WinBwdRange* d_win_bwd_ranges = nullptr;
+  ra::WinBwdSplit* d_win_splits = nullptr;
   ra::WinItem* d_win_items = nullptr;
   ra::WinRange* d_win_ranges = nullptr;
   // ra_plan_destroy queues the frees of the device tables behind exactly this work.
@@ -438,57 +448,183 @@ void win_tile_counts(ra_plan_s* pl) {
     }
 }
 
-// Backward work lists of a windowed plan, as build_bwd_schedule: an item's own tile
-// stops at run_end, and WorkItem::pad holds the position at its other end.
-void build_win_bwd(ra_plan_s* pl) {
+// Backward work lists of a windowed plan (win_internal.h), walked by position or shard by
+// shard as the forward's.
+void build_win_bwd(ra_plan_s* pl, const ra::WinView& own, const ra::WinView& str) {
   const ra_problem& pb = pl->prob;
-  const int N = pb.n_shards;
-  const int32_t s_n = (int32_t)pl->s_n;
+  const int N = own.shards;
   const int G = pb.heads_q / pb.heads_kv;
-  std::vector<Keyed> kv, qs;
-  int64_t seqno = 0;
-  for (int p = 0; p < N; ++p)
-    for (int32_t row = 0; row < s_n;) {
-      const int32_t end = std::min(row + 128, ra::run_end(pb.layout, s_n, row));
-      const int32_t first = win_pos(pb, s_n, p, row), last = win_pos(pb, s_n, p, end - 1);
-      // the tile as keys: 64-row query tiles of every shard that see it
-      const int64_t far = (int64_t)last + pl->window - 1;
-      const int32_t upto = (int32_t)(first < pl->sinks ? pb.seq - 1 : std::min<int64_t>(far, pb.seq - 1));
-      int32_t as_kv = 0, as_q = 0;
-      for (int t = 0; t < N; ++t) {
-        const int32_t lo = ra::rows_le(pb.layout, N, s_n, (p + t) % N, first - 1);
-        const int32_t hi = ra::rows_le(pb.layout, N, s_n, (p + t) % N, upto);
-        if (hi > lo) as_kv += ((hi + 63) / 64 - lo / 64) * G;
-        // and as queries: 64-row key tiles it meets
-        const ra::WinSpan sp = ra::win_span(pb.layout, N, s_n, pl->window, pl->sinks, (p - t + N) % N, first, last);
-        as_q += (sp.first + 63) / 64 + (sp.hi > sp.lo ? (sp.hi + 63) / 64 - sp.lo / 64 : 0);
-      }
+  const int32_t last_pos = (int32_t)pb.seq - 1;
+  pl->win_own = own;
+  pl->win_str = str;
+  pl->win_scalars = pb.batch * (int64_t)pb.heads_q * N * ((str.s_n + str.tile - 1) / str.tile) * 128;
+
+  // Ranges are gathered in `now`, then appended to the plan's list with an item.
+  std::vector<ra::WinBwdRange> now;
+  auto tiles_now = [&] {
+    int32_t n = 0;
+    for (const ra::WinBwdRange& x : now) n += ra::range_tiles64(x, str.tile);
+    return n;
+  };
+  auto add = [&](int r, int32_t from, int32_t to) {
+    if (to > from) now.push_back({r, from / str.tile * str.tile, to, from});
+  };
+  // Queries at positions [from, to], shard by shard from the one the key block sits on.
+  auto queries = [&](int shard, int32_t from, int32_t to) {
+    now.clear();
+    for (int t = 0; t < N; ++t) {
+      const int p = (shard + t) % N;
+      add(p, ra::view_rows_le(str, p, from - 1), ra::view_rows_le(str, p, to));
+    }
+  };
+  auto put_ranges = [&](ra::WinBwdItem* it, const std::vector<ra::WinBwdRange>& list) {
+    it->range0 = (int32_t)pl->win_bwd_ranges.size();
+    it->n_ranges = (int32_t)list.size();
+    pl->win_bwd_ranges.insert(pl->win_bwd_ranges.end(), list.begin(), list.end());
+  };
+  auto tile_at = [&](int p, int32_t row) {
+    ra::WinBwdItem it{};
+    it.shard = p;
+    it.row0 = row;
+    it.row_end = std::min(row + own.tile, ra::run_end(own.layout, own.s_n, row));
+    it.pos0 = (int32_t)ra::pos_of(own.layout, N, own.s_n, p, row);
+    it.g1 = 1;
+    it.part = -1;
+    return it;
+  };
+  auto last_of = [&](const ra::WinBwdItem& it) {
+    return (int32_t)ra::pos_of(own.layout, N, own.s_n, it.shard, it.row_end - 1);
+  };
+  // Items of one tile for every (batch, head), in the order of ra::schedule_before.
+  auto emit = [&](std::vector<ra::WinBwdItem>& tiles, bool kv) {
+    std::vector<Keyed> list;
+    for (size_t x = 0; x < tiles.size(); ++x)
       for (int64_t b = 0; b < pb.batch; ++b)
-        for (int h = 0; h < pb.heads_q; ++h) {
+        for (int h = 0; h < pb.heads_q; h += kv ? G : 1) {
           ra::WorkItem w{};
           w.bh0 = (int32_t)(b * pb.heads_q + h);
-          w.bh1 = -1;
-          w.shard = p;
-          w.row0 = row;
-          w.maxq = last;
-          w.pad = first;
-          w.cost = as_q;
-          qs.push_back({w, seqno++});
-          if (h % G) continue;
-          w.maxq = first;
-          w.pad = last;
-          w.cost = as_kv;
-          kv.push_back({w, seqno++});
+          w.shard = (int32_t)x;
+          w.cost = tiles[x].n_tiles;
+          list.push_back({w, (int64_t)list.size()});
         }
-      row = end;
+    for (const ra::WorkItem& w : schedule(list, pb.heads_q, G)) {
+      ra::WinBwdItem it = tiles[w.shard];
+      it.bh = kv ? w.bh0 / pb.heads_q * pb.heads_kv + w.bh0 % pb.heads_q / G : w.bh0;
+      if (it.part >= 0) it.part += (int64_t)it.bh * it.pad2;  // the parts of a head
+      pl->win_bwd_items.push_back(it);
     }
-  // (schedule groups by the query head bh0: the key tiles' is the first of their group)
-  pl->bwd_items = schedule(kv, pb.heads_q, G);
-  for (ra::WorkItem& w : pl->bwd_items)
-    w.bh0 = (int32_t)(w.bh0 / pb.heads_q * pb.heads_kv + w.bh0 % pb.heads_q / G);
-  pl->n_bwd_kv = (int64_t)pl->bwd_items.size();
-  const std::vector<ra::WorkItem> q_sorted = schedule(qs, pb.heads_q, G);
-  pl->bwd_items.insert(pl->bwd_items.end(), q_sorted.begin(), q_sorted.end());
+  };
+
+  // Pass 0: first the tiles without a sink (their size bounds the pieces), then the others.
+  std::vector<ra::WinBwdItem> tiles, sink_tiles;
+  int32_t normal = 8;
+  for (int p = 0; p < N; ++p)
+    for (int32_t row = 0; row < own.s_n;) {
+      ra::WinBwdItem it = tile_at(p, row);
+      row = it.row_end;
+      it.g1 = G;
+      if (it.pos0 < pl->sinks) {
+        sink_tiles.push_back(it);
+        continue;
+      }
+      queries(p, it.pos0, (int32_t)std::min<int64_t>((int64_t)last_of(it) + pl->window - 1, last_pos));
+      it.n_tiles = tiles_now() * G;
+      normal = std::max(normal, it.n_tiles);
+      put_ranges(&it, now);
+      tiles.push_back(it);
+    }
+  int64_t parts = 0;  // floats per key/value head
+  std::vector<ra::WinBwdSplit> splits;
+  for (ra::WinBwdItem it : sink_tiles) {
+    const int32_t reach = (int32_t)std::min<int64_t>((int64_t)last_of(it) + pl->window - 1, last_pos);
+    queries(it.shard, it.pos0, last_pos);
+    it.n_tiles = tiles_now() * G;
+    if (it.n_tiles <= 2 * normal || reach == last_pos) {
+      put_ranges(&it, now);
+      tiles.push_back(it);
+      continue;
+    }
+    // The near queries in one part of all rows, the far ones, which see the sinks alone, in
+    // pieces of up to `normal` tiles: of several heads while their far queries are few.
+    const int32_t first_not = (pl->sinks - it.pos0 + own.apart - 1) / own.apart;  // rows that are sinks
+    ra::WinBwdSplit sp{0, it.shard, it.row0, it.row_end, parts, 0, 0, std::min(first_not, it.row_end - it.row0), {}};
+    ra::WinBwdItem near = it;
+    queries(it.shard, it.pos0, reach);
+    near.n_tiles = tiles_now() * G;
+    near.part = parts;
+    near.part_rows = 128;
+    parts += 2 * 128 * 128;
+    put_ranges(&near, now);
+    tiles.push_back(near);
+    sp.far = parts;
+    queries(it.shard, reach + 1, last_pos);
+    const int32_t per_head = tiles_now();
+    const int heads = std::max(1, std::min(G, normal / std::max(per_head, 1)));
+    std::vector<ra::WinBwdRange> piece;
+    auto flush = [&](int g0, int g1) {
+      ra::WinBwdItem far = it;
+      far.g0 = g0;
+      far.g1 = g1;
+      far.part = parts;
+      far.part_rows = sp.far_rows;
+      far.n_tiles = 0;
+      for (const ra::WinBwdRange& x : piece) far.n_tiles += ra::range_tiles64(x, str.tile) * (g1 - g0);
+      put_ranges(&far, piece);
+      tiles.push_back(far);
+      parts += 2 * (int64_t)sp.far_rows * 128;
+      ++sp.n_far;
+      piece.clear();
+    };
+    for (int g0 = 0; g0 < G; g0 += heads) {
+      const int g1 = std::min(G, g0 + heads);
+      const int32_t most = std::max(1, normal / (g1 - g0));  // tiles of a piece, per head
+      int32_t have = 0;
+      for (ra::WinBwdRange x : now)
+        while (x.first < x.end) {
+          ra::WinBwdRange cut = x;
+          cut.end = std::min<int64_t>(x.end, (int64_t)x.row0 + (int64_t)(most - have) * str.tile);
+          piece.push_back(cut);
+          have += ra::range_tiles64(cut, str.tile);
+          x.first = x.row0 = cut.end;
+          if (have == most) {
+            flush(g0, g1);
+            have = 0;
+          }
+        }
+      if (!piece.empty()) flush(g0, g1);
+    }
+    splits.push_back(sp);
+  }
+  for (ra::WinBwdItem& it : tiles) it.pad2 = parts;
+  emit(tiles, true);
+  pl->n_win_bwd_kv = (int64_t)pl->win_bwd_items.size();
+  pl->win_parts = parts * pb.batch * pb.heads_kv;
+  for (int64_t bh = 0; bh < pb.batch * pb.heads_kv; ++bh)
+    for (ra::WinBwdSplit sp : splits) {
+      sp.bh = (int32_t)bh;
+      sp.near += bh * parts;
+      sp.far += bh * parts;
+      pl->win_splits.push_back(sp);
+    }
+
+  // Pass 1
+  tiles.clear();
+  for (int p = 0; p < N; ++p)
+    for (int32_t row = 0; row < own.s_n;) {
+      ra::WinBwdItem it = tile_at(p, row);
+      row = it.row_end;
+      now.clear();
+      for (int t = 0; t < N; ++t) {
+        const int r = (p - t + N) % N;
+        const ra::WinSpan sp = ra::win_span(str.layout, N, str.s_n, pl->window, pl->sinks, r, it.pos0, last_of(it));
+        add(r, 0, sp.first);
+        add(r, sp.lo, sp.hi);
+      }
+      it.n_tiles = tiles_now();
+      put_ranges(&it, now);
+      tiles.push_back(it);
+    }
+  emit(tiles, false);
 }
 
 void build_win_schedule(ra_plan_s* pl) {
@@ -507,18 +643,22 @@ void build_win_schedule(ra_plan_s* pl) {
   const ra::WinView ring{pb.layout, N, s_n, 1, ra::kTileRows, pb.layout == RA_LAYOUT_STRIPED ? N : 1};
   const ra::WinView natural{RA_LAYOUT_CONTIGUOUS, 1, (int32_t)pb.seq, 1, ra::kTileRows, 1};
   ra::WinView rows = natural;
-  if (pb.layout == RA_LAYOUT_STRIPED && N > 1) {
+  if (pb.layout == RA_LAYOUT_STRIPED && N > 1 && N <= ra::kTileRows) {
     rows.stripe = N;
     rows.tile = ra::kTileRows / N * N;
   }
-  const bool by_position = pb.layout != RA_LAYOUT_ZIGZAG && N <= ra::kTileRows;
+  const bool by_position = pb.layout == RA_LAYOUT_CONTIGUOUS || (pb.layout == RA_LAYOUT_STRIPED && N <= ra::kTileRows);
   pl->win_lists[0] = add_win_list(pl, ring, ring);
   pl->win_lists[1] = N == 1 || !by_position ? pl->win_lists[0] : add_win_list(pl, rows, rows);
   pl->win_lists[2] = N == 1 ? pl->win_lists[0]
                      : pb.layout == RA_LAYOUT_CONTIGUOUS && by_position
                          ? pl->win_lists[1]
                          : add_win_list(pl, by_position ? rows : ring, natural);
-  build_win_bwd(pl);
+  // (a streamed tile of the backward holds 64 rows)
+  ra::WinView own = ring, str = ring;
+  if (pb.layout != RA_LAYOUT_ZIGZAG && (N <= 64 || pb.layout == RA_LAYOUT_CONTIGUOUS)) own = str = rows;
+  str.tile = 64 / str.stripe * str.stripe;
+  build_win_bwd(pl, own, str);
 }
 
 ra_status upload(ra_plan_s* pl) {
@@ -556,6 +696,9 @@ ra_status upload(ra_plan_s* pl) {
   put(pl->gather_items, &pl->d_gather_items);
   put(pl->win_items, &pl->d_win_items);
   put(pl->win_ranges, &pl->d_win_ranges);
+  put(pl->win_bwd_items, &pl->d_win_bwd_items);
+  put(pl->win_bwd_ranges, &pl->d_win_bwd_ranges);
+  put(pl->win_splits, &pl->d_win_splits);
   // the tables are in place before any launch on another stream reads them
   if (e == cudaSuccess) e = cudaStreamSynchronize(ms);
   if (e == cudaSuccess) e = cudaEventCreateWithFlags(&pl->ev_entry, cudaEventDisableTiming);
@@ -637,6 +780,52 @@ ra_status launch_win(ra_plan_s* plan, const ra::FwdParams& prm, const void* q, c
   else
     e = ra::launch_win_fwd_f32(w, static_cast<const float*>(q), static_cast<const float*>(k),
                                static_cast<const float*>(v), st);
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "%s: %s", why, cudaGetErrorString(e));
+  const ra_status s = mark_use(plan, st);
+  return s != RA_OK ? s : ok();
+}
+
+// The bf16 backward of a windowed plan: scalars of the rows, dK and dV, dQ, and the sums of
+// the key tiles that were cut.
+ra_status launch_win_bwd(ra_plan_s* plan, const void* q, const void* k, const void* v, const void* o, const float* lse,
+                         const void* dout, void* dq, void* dk, void* dv, float* scratch, cudaStream_t st) {
+  const ra_problem& pb = plan->prob;
+  ra::WinBwdParams w{};
+  w.batch = (int32_t)pb.batch;
+  w.heads_q = pb.heads_q;
+  w.heads_kv = pb.heads_kv;
+  w.group = pb.heads_q / pb.heads_kv;
+  w.own = plan->win_own;
+  w.str = plan->win_str;
+  w.window = plan->window;
+  w.sinks = plan->sinks;
+  w.seq = (int32_t)pb.seq;
+  w.blocks = (w.str.s_n + w.str.tile - 1) / w.str.tile;
+  w.scale = pb.scale;
+  w.scale_log2 = pb.scale * 1.4426950408889634f;
+  w.lse2d = scratch;
+  w.n_scalars = plan->win_scalars;
+  w.parts = scratch + plan->win_scalars;
+  w.dq = dq;
+  w.dk = dk;
+  w.dv = dv;
+  w.q = q;
+  w.dout = dout;
+  w.ranges = plan->d_win_bwd_ranges;
+  w.status = plan->d_status;
+  const int sms = plan->sm_count > 0 ? plan->sm_count : 148;
+  const char* why = "backward preparation launch failed";
+  cudaError_t e = ra::launch_win_bwd_prep(w, o, lse, scratch, sms, st);
+  for (int pass = 0; pass < 2 && e == cudaSuccess; ++pass) {
+    const int64_t n = pass == 0 ? plan->n_win_bwd_kv : (int64_t)plan->win_bwd_items.size() - plan->n_win_bwd_kv;
+    w.items = plan->d_win_bwd_items + (pass == 0 ? 0 : plan->n_win_bwd_kv);
+    w.n_items = (int32_t)n;
+    e = ra::launch_win_bwd_bf16(pass, w, q, k, v, dout, (int)std::min<int64_t>(n, sms), st, &why);
+  }
+  if (e == cudaSuccess && !plan->win_splits.empty()) {
+    why = "sum of the parts: launch failed";
+    e = ra::launch_win_bwd_join(w, plan->d_win_splits, (int)plan->win_splits.size(), st);
+  }
   if (e != cudaSuccess) return fail(RA_ERR_CUDA, "%s: %s", why, cudaGetErrorString(e));
   const ra_status s = mark_use(plan, st);
   return s != RA_OK ? s : ok();
@@ -835,8 +1024,9 @@ ra_status ra_plan_destroy(ra_plan_t plan) {
     // order, and the host does not wait.
     if (plan->mem_stream != nullptr) {
       for (const ra::StreamMark& m : plan->marks) cudaStreamWaitEvent(plan->mem_stream, m.done, 0);
-      void* mem[] = {plan->d_items,     plan->d_step_items, plan->d_bwd_items, plan->d_gather_items,
-                     plan->d_win_items, plan->d_win_ranges, plan->d_status};
+      void* mem[] = {plan->d_items,      plan->d_step_items,    plan->d_bwd_items,      plan->d_gather_items,
+                     plan->d_win_items,  plan->d_win_ranges,    plan->d_win_bwd_items,  plan->d_win_bwd_ranges,
+                     plan->d_win_splits, plan->d_status};
       for (void* p : mem)
         if (p != nullptr) cudaFreeAsync(p, plan->mem_stream);
       cudaStreamDestroy(plan->mem_stream);  // released once its queued frees have run
@@ -1042,6 +1232,10 @@ ra_status ra_ring_fwd(ra_plan_t plan, const void* q, const void* k, const void* 
 ra_status ra_bwd_scratch_size(ra_plan_t plan, int64_t* bytes) {
   if (plan == nullptr || bytes == nullptr) return fail(RA_ERR_INVALID_ARG, "null argument");
   const ra_problem& pb = plan->prob;
+  if (plan->window > 0 && pb.dtype == RA_DTYPE_BF16) {
+    *bytes = (plan->win_scalars + plan->win_parts) * (int64_t)sizeof(float);
+    return ok();
+  }
   const int64_t n64 = (plan->s_n + 63) / 64;
   *bytes = pb.batch * (int64_t)pb.heads_q * pb.n_shards * n64 * 128 * (int64_t)sizeof(float);
   return ok();
@@ -1060,6 +1254,8 @@ ra_status ra_bwd(ra_plan_t plan, const void* q, const void* k, const void* v, co
   if (s == RA_OK) s = ra::check_on_current_device(ptrs, 10, static_cast<cudaStream_t>(stream));
   if (s != RA_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (plan->window > 0 && pb.dtype == RA_DTYPE_BF16)
+    return launch_win_bwd(plan, q, k, v, o, lse, dout, dq, dk, dv, scratch, st);
   const int64_t n64 = (plan->s_n + 63) / 64;
   cudaError_t e = ra::launch_bwd_prep(pb.dtype, pb.batch * (int64_t)pb.heads_q, pb.seq, pb.n_shards, pb.head_dim, o,
                                       dout, lse, scratch, st);
@@ -1087,12 +1283,11 @@ ra_status ra_bwd(ra_plan_t plan, const void* q, const void* k, const void* v, co
   prm.dout = dout;
   prm.status = plan->d_status;
   prm.item_counter = plan->d_status + 1;
-  prm.window = plan->window;
-  prm.sinks = plan->sinks;
   if (pb.dtype != RA_DTYPE_BF16) {
-    e = (plan->window > 0 ? ra::launch_win_bwd_f32 : ra::launch_bwd_f32)(
-        prm, static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
-        static_cast<const float*>(dout), st);
+    const float *qf = static_cast<const float*>(q), *kf = static_cast<const float*>(k), *vf = static_cast<const float*>(v),
+                *df = static_cast<const float*>(dout);
+    e = plan->window > 0 ? ra::launch_win_bwd_f32(prm, plan->window, plan->sinks, qf, kf, vf, df, st)
+                         : ra::launch_bwd_f32(prm, qf, kf, vf, df, st);
     if (e != cudaSuccess) return fail(RA_ERR_CUDA, "f32 backward launch failed: %s", cudaGetErrorString(e));
     s = mark_use(plan, st);
     return s != RA_OK ? s : ok();

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 __global__ void __launch_bounds__(kWarps * 32)
-    win_bwd_f32_dq_kernel(const BwdParams P, const float* __restrict__ q, const float* __restrict__ k,
+    win_bwd_f32_dq_kernel(const BwdParams P, int window, int sinks, const float* __restrict__ q, const float* __restrict__ k,
                           const float* __restrict__ v, const float* __restrict__ dout) {
   __shared__ float qs[kWarps][kMaxD], dos[kWarps][kMaxD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int x = 0; x < kMaxD / 32; ++x) acc[x] = 0.f;
   for (int t = 0; t < N; ++t) {
     const int r = (p - t + N) % N;
-    const WinSpan sp = win_span(P.layout, N, (int)P.s_n, P.window, P.sinks, r, my_pos, my_pos);
+    const WinSpan sp = win_span(P.layout, N, (int)P.s_n, window, sinks, r, my_pos, my_pos);
     const float* kb = k + (kv_base + (int64_t)r * P.s_n) * d;
     const float* vb = v + (kv_base + (int64_t)r * P.s_n) * d;
     for (int run = 0; run < 2; ++run) {
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 __global__ void __launch_bounds__(kWarps * 32)
-    win_bwd_f32_dkdv_kernel(const BwdParams P, const float* __restrict__ q, const float* __restrict__ k,
+    win_bwd_f32_dkdv_kernel(const BwdParams P, int window, int sinks, const float* __restrict__ q, const float* __restrict__ k,
                             const float* __restrict__ v, const float* __restrict__ dout) {
   __shared__ float ks[kWarps][kMaxD], vs[kWarps][kMaxD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
   for (int x = 0; x < kMaxD / 32; ++x) dk[x] = dv[x] = 0.f;
   // the queries that see this key: up to window - 1 positions on, or all later ones
-  const int64_t far = key_pos < P.sinks ? P.seq - 1 : (int64_t)key_pos + P.window - 1;
+  const int64_t far = key_pos < sinks ? P.seq - 1 : (int64_t)key_pos + window - 1;
   const int last_pos = (int)(far < P.seq - 1 ? far : P.seq - 1);
   for (int t = 0; t < N; ++t) {
     const int p = (r + t) % N;  // the device this block sits on at step t
@@ -257,16 +257,16 @@ cudaError_t launch_win_fwd_f32(const WinParams& prm, const float* q, const float
   return cudaGetLastError();
 }
 
-cudaError_t launch_win_bwd_f32(const BwdParams& prm, const float* q, const float* k, const float* v,
-                               const float* dout, cudaStream_t stream) {
+cudaError_t launch_win_bwd_f32(const BwdParams& prm, int window, int sinks, const float* q, const float* k,
+                               const float* v, const float* dout, cudaStream_t stream) {
   const int64_t rows_q = (int64_t)prm.batch * prm.heads_q * prm.seq;
   const int64_t rows_kv = (int64_t)prm.batch * prm.heads_kv * prm.seq;
   const int64_t bq = (rows_q + kWarps - 1) / kWarps, bk = (rows_kv + kWarps - 1) / kWarps;
   if (bq > 0x7fffffff || bk > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  win_bwd_f32_dq_kernel<<<(unsigned)bq, kWarps * 32, 0, stream>>>(prm, q, k, v, dout);
+  win_bwd_f32_dq_kernel<<<(unsigned)bq, kWarps * 32, 0, stream>>>(prm, window, sinks, q, k, v, dout);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  win_bwd_f32_dkdv_kernel<<<(unsigned)bk, kWarps * 32, 0, stream>>>(prm, q, k, v, dout);
+  win_bwd_f32_dkdv_kernel<<<(unsigned)bk, kWarps * 32, 0, stream>>>(prm, window, sinks, q, k, v, dout);
   return cudaGetLastError();
 }
 

@@ -1,7 +1,7 @@
 // Windowed attention: a query at position i sees the keys j <= i with j > i - window
 // or j < sinks (the first tokens of the sequence, which stay visible).  Declarations
 // shared by the planner (ra_api.cu) and the kernels (win_fwd_bf16_sm103.cu,
-// win_f32.cu, bwd_bf16_sm103.cu).
+// win_bwd_bf16_sm103.cu, win_f32.cu).
 //
 // Positions rise with the local row in every layout, so the keys of shard r that a
 // query at position P sees are the rows
@@ -113,11 +113,77 @@ struct WinParams {
   uint32_t* status;
 };
 
+// Rows of shard r of a view at positions <= P.
+RA_HD int32_t view_rows_le(const WinView& v, int r, int32_t P) {
+  if (v.shards > 1) return rows_le(v.layout, v.shards, v.s_n, r, P);
+  return P < 0 ? 0 : (P < v.s_n ? P + 1 : v.s_n);
+}
+
+// Backward.  Rows [first, end) of shard r, streamed in tiles of the view's rows from row0 on,
+// the start of the tile that `first` lies in.
+struct alignas(16) WinBwdRange {
+  int32_t r, row0, end, first;
+};
+RA_HD int32_t range_tiles64(const WinBwdRange& rg, int32_t tile) {
+  const int32_t rows = rg.end - rg.row0;
+  return tile == 64 ? (rows + 63) / 64 : (rows + tile - 1) / tile;
+}
+// One own tile (pass 0: keys, bh = b*Hkv + kv head; pass 1: queries, bh = b*Hq + h) and the
+// ranges it meets, for heads g0 .. g1 - 1 of the group (pass 1: one).
+struct alignas(16) WinBwdItem {
+  int32_t bh, shard, row0, row_end;
+  int32_t range0, n_ranges, n_tiles, pos0;
+  int32_t g0, g1;
+  int32_t part_rows;  // rows of the partial sums
+  int32_t pad;
+  int64_t part;       // pass 0: where they go (float index in parts), -1: straight to dV, dK
+  int64_t pad2;
+};
+// A key tile that was cut: one part of all its rows (128) from the near queries, n_far parts
+// of its sinks' rows from the others; each holds dV rows, then dK rows.
+struct alignas(16) WinBwdSplit {
+  int32_t bh, shard, row0, row_end;
+  int64_t near, far;
+  int32_t n_far, far_rows;
+  int32_t pad[2];
+};
+
+struct WinBwdParams {
+  int32_t batch, heads_q, heads_kv, group;
+  WinView own, str;     // the items' tiles (up to 128 rows) and the streamed ones (up to 64)
+  int32_t window, sinks;
+  int32_t seq;
+  int32_t n_items;
+  int32_t blocks;       // streamed tiles of a shard
+  float scale, scale_log2;
+  const float* lse2d;   // per streamed tile of queries 64 lse2 values, then 64 D values
+  int64_t n_scalars;
+  void* dq;
+  void* dk;
+  void* dv;
+  const void* q;        // pass 1 reads its own query rows of Q and dO directly
+  const void* dout;
+  float* parts;
+  const WinBwdItem* items;
+  const WinBwdRange* ranges;
+  uint32_t* status;
+};
+// Block of scalars of streamed tile `tile` of a shard (bh = b*Hq + h).
+RA_HD int64_t win_scalar_block(const WinBwdParams& P, int64_t bh, int shard, int tile) {
+  return (bh * P.str.shards + shard) * P.blocks + tile;
+}
+
+cudaError_t launch_win_bwd_prep(const WinBwdParams& prm, const void* o, const float* lse, float* out, int sms,
+                                cudaStream_t stream);
+// pass 0: dK and dV (items are key tiles); pass 1: dQ (items are query tiles).
+cudaError_t launch_win_bwd_bf16(int pass, const WinBwdParams& prm, const void* q, const void* k, const void* v,
+                                const void* dout, int grid, cudaStream_t stream, const char** why);
+cudaError_t launch_win_bwd_join(const WinBwdParams& prm, const WinBwdSplit* splits, int n, cudaStream_t stream);
 cudaError_t launch_win_fwd_bf16(const WinParams& prm, const void* q, const void* k, const void* v, int grid,
                                 cudaStream_t stream, const char** why);
 cudaError_t launch_win_fwd_f32(const WinParams& prm, const float* q, const float* k, const float* v,
                                cudaStream_t stream);
-cudaError_t launch_win_bwd_f32(const BwdParams& prm, const float* q, const float* k, const float* v,
-                               const float* dout, cudaStream_t stream);
+cudaError_t launch_win_bwd_f32(const BwdParams& prm, int window, int sinks, const float* q, const float* k,
+                               const float* v, const float* dout, cudaStream_t stream);
 
 }  // namespace ra
