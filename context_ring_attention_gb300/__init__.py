@@ -23,6 +23,7 @@ instead: the same library with the kernels' bounds checks compiled in, which
 ``ra_sync_status`` reports as RaError(RA_ERR_BOUNDS).
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -144,26 +145,26 @@ def _layout(layout):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     import torch
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        # (the raw handle: building a Stream object for it takes longer than a launch)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
+        return stream
     cur = torch.cuda.current_device()
     if stream.device.index != cur:
         raise ValueError(f"the stream belongs to {stream.device}; the library launches on the current device "
                          f"cuda:{cur}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _alloc_on(stream):
     """Context in which buffers made for a call belong to the stream the call runs on, so that
     the allocator does not hand them on while its kernels may still use them."""
-    import contextlib
     import torch
     if stream is None:
         return contextlib.nullcontext()
@@ -265,13 +266,20 @@ def _check_qkv(plan, **tensors):
         _on_current_device(name, t)
 
 
-def _need(name, t, shape, dtype, device):
-    """``t`` must be a contiguous tensor of exactly this shape and dtype on ``device``:
-    the library sees only its pointer, so a smaller buffer would be overrun."""
+def _need_like(name, t, shape, dtype, device):
+    """``t`` must be a contiguous tensor of exactly this shape and dtype on ``device``, a device
+    that was checked already."""
     import torch
-    if (not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(int(x) for x in shape) or t.dtype != dtype
-            or not t.is_contiguous() or t.device != device):
+    if (not isinstance(t, torch.Tensor) or t.shape != tuple(shape) or t.dtype != dtype or t.device != device
+            or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _need(name, t, shape, dtype, device):
+    """``t`` must be a contiguous tensor of exactly this shape and dtype on ``device``, which
+    must be the current device: the library sees only its pointer, so a smaller buffer would
+    be overrun."""
+    _need_like(name, t, shape, dtype, device)
     _on_current_device(name, t)
 
 
@@ -598,6 +606,8 @@ class Kv4:
     def __init__(self, handle, problem):
         self._h = handle
         self.problem = problem
+        self._bytes = None    # of the cache
+        self._scratch = {}    # bytes of attention scratch by (batch, rows, table width)
 
     @property
     def handle(self):
@@ -634,9 +644,11 @@ def ra_kv4_destroy(kv):
 
 def ra_kv4_cache_size(kv):
     """Bytes of the cache buffer (a contiguous uint8 CUDA tensor of the caller's)."""
-    n = ctypes.c_int64()
-    _check(load_library().ra_kv4_cache_size(kv.handle, ctypes.byref(n)))
-    return n.value
+    if kv._bytes is None:
+        n = ctypes.c_int64()
+        _check(load_library().ra_kv4_cache_size(kv.handle, ctypes.byref(n)))
+        kv._bytes = n.value
+    return kv._bytes
 
 
 def _kv4_dtype(kv):
@@ -650,10 +662,10 @@ def _kv4_tables(kv, cache, batch, page_table, **per_sequence):
     _need("cache", cache, (ra_kv4_cache_size(kv),), torch.uint8, cache.device)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != batch:
         raise ValueError(f"page_table must be an int32 tensor of shape ({batch}, pages of a sequence)")
-    _need("page_table", page_table, page_table.shape, torch.int32, cache.device)
+    _need_like("page_table", page_table, page_table.shape, torch.int32, cache.device)
     for name, t in per_sequence.items():
         if t is not None:
-            _need(name, t, (batch,), torch.int32, cache.device)
+            _need_like(name, t, (batch,), torch.int32, cache.device)
 
 
 def ra_kv4_write(kv, cache, k, v, page_table, first, count=None, stream=None):
@@ -662,8 +674,8 @@ def ra_kv4_write(kv, cache, k, v, page_table, first, count=None, stream=None):
     B, T = k.shape[0], k.shape[2] if k.dim() == 4 else 0
     _kv4_tables(kv, cache, B, page_table, first=first, count=count)
     shape = (B, pb["heads_kv"], T, pb["head_dim"])
-    _need("k", k, shape, _kv4_dtype(kv), cache.device)
-    _need("v", v, shape, _kv4_dtype(kv), cache.device)
+    _need_like("k", k, shape, _kv4_dtype(kv), cache.device)
+    _need_like("v", v, shape, _kv4_dtype(kv), cache.device)
     _check(load_library().ra_kv4_write(kv.handle, _ptr(cache), B, T, _ptr(k), _ptr(v), _ptr(page_table),
                                        page_table.shape[1], _ptr(first), _ptr(count), _stream(stream)))
 
@@ -685,8 +697,8 @@ def ra_kv4_read(kv, cache, page_table, first, rows, count=None, k=None, v=None, 
     if own:
         with _alloc_on(stream):
             k, v = (torch.empty(shape, dtype=_kv4_dtype(kv), device=cache.device) for _ in range(2))
-    _need("k", k, shape, _kv4_dtype(kv), cache.device)
-    _need("v", v, shape, _kv4_dtype(kv), cache.device)
+    _need_like("k", k, shape, _kv4_dtype(kv), cache.device)
+    _need_like("v", v, shape, _kv4_dtype(kv), cache.device)
     _check(load_library().ra_kv4_read(kv.handle, _ptr(cache), B, T, _ptr(page_table), page_table.shape[1],
                                       _ptr(first), _ptr(count), int(own), _ptr(k), _ptr(v), _stream(stream)))
     return k, v
@@ -694,10 +706,12 @@ def ra_kv4_read(kv, cache, page_table, first, rows, count=None, k=None, v=None, 
 
 def ra_kv4_attend_scratch_size(kv, batch, rows, table_width):
     """Bytes of the float32 scratch buffer ra_kv4_attend needs for these sizes (0: none)."""
-    n = ctypes.c_int64()
-    _check(load_library().ra_kv4_attend_scratch_size(kv.handle, int(batch), int(rows), int(table_width),
-                                                     ctypes.byref(n)))
-    return n.value
+    key = (int(batch), int(rows), int(table_width))
+    if key not in kv._scratch:
+        n = ctypes.c_int64()
+        _check(load_library().ra_kv4_attend_scratch_size(kv.handle, *key, ctypes.byref(n)))
+        kv._scratch[key] = n.value
+    return kv._scratch[key]
 
 
 def ra_kv4_attend(kv, cache, q, page_table, length, o=None, lse=None, scratch=None, stream=None):
@@ -713,22 +727,23 @@ def ra_kv4_attend(kv, cache, q, page_table, length, o=None, lse=None, scratch=No
         raise ValueError("q must have the shape [B, Hq, T, d]")
     B, T = q.shape[0], q.shape[2]
     _kv4_tables(kv, cache, B, page_table, length=length)
-    _need("q", q, (B, pb["heads_q"], T, pb["head_dim"]), _kv4_dtype(kv), cache.device)
+    _need_like("q", q, (B, pb["heads_q"], T, pb["head_dim"]), _kv4_dtype(kv), cache.device)
+    need = ra_kv4_attend_scratch_size(kv, B, T, page_table.shape[1]) // 4
+    if scratch is not None and (scratch.numel() < need or scratch.dtype != torch.float32
+                                  or not scratch.is_contiguous() or scratch.device != q.device):
+        raise ValueError("scratch must be a contiguous float32 tensor of at least ra_kv4_attend_scratch_size(...) "
+                         "bytes on the device of q")
+    if o is not None:
+        _need_like("o", o, q.shape, q.dtype, q.device)
+    if lse is not None:
+        _need_like("lse", lse, q.shape[:3], torch.float32, q.device)
     with _alloc_on(stream):
         if o is None:
             o = torch.empty_like(q)
         if lse is None:
             lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    _need("o", o, q.shape, q.dtype, q.device)
-    _need("lse", lse, q.shape[:3], torch.float32, q.device)
-    need = ra_kv4_attend_scratch_size(kv, B, T, page_table.shape[1]) // 4
-    if scratch is None and need:
-        with _alloc_on(stream):
+        if scratch is None and need:
             scratch = torch.empty(need, dtype=torch.float32, device=q.device)
-    elif scratch is not None and (scratch.numel() < need or scratch.dtype != torch.float32
-                                  or not scratch.is_contiguous() or scratch.device != q.device):
-        raise ValueError("scratch must be a contiguous float32 tensor of at least ra_kv4_attend_scratch_size(...) "
-                         "bytes on the device of q")
     _check(load_library().ra_kv4_attend(kv.handle, _ptr(cache), B, T, _ptr(q), _ptr(page_table), page_table.shape[1],
                                         _ptr(length), _ptr(o), _ptr(lse), _ptr(scratch), _stream(stream)))
     return o, lse
