@@ -83,10 +83,12 @@ __device__ __forceinline__ float bf16_round(float x) { return __uint_as_float(pt
 // stands in the sum's low bits.
 constexpr float kRound = 12582912.f;
 constexpr uint32_t kRoundBits = 0x4B400000u;
+// The constant's share in the sum over i = 0..7 of bits(r_i) * 16^i, in 32 bits.
+constexpr uint32_t kRoundShare = kRoundBits * 0x11111111u;
 
 // Code of x, decided exactly where the quotient lies next to a border of two codes.
 // d + e is x - low without error (the two terms of a floating-point sum); the quotient
-// d * inv is off by 2^-22 of itself at most, so its floor is right or one off, and
+// d * inv is off by 2^-21 of itself at most, so its floor is right or one off, and
 // r = d - c * scale is exact: c * scale has 12 bits, and the difference is a multiple of
 // the last place of d and smaller than d.
 __device__ __noinline__ uint32_t code_at_border(float x, float low, float scale, float inv) {
@@ -101,10 +103,10 @@ __device__ __noinline__ uint32_t code_at_border(float x, float low, float scale,
   return (uint32_t)fminf(fmaxf(c, 0.f), 15.f);
 }
 
-// The 8 codes of a thread, first in the lowest nibble.
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float low, float scale) {
-  if (!(scale > 0.f)) return 0u;
-  const float inv = __frcp_rn(scale);
+// The 8 codes of a thread, first in the lowest nibble: float32 rows, whose low is a rounded
+// minimum, so that a quotient may lie outside 0..15 and d is seldom exact.  Codes off the
+// borders are sure from the approximate quotient.
+__device__ __forceinline__ uint32_t codes_near(const float (&x)[8], float low, float scale, float inv) {
   uint32_t word = 0, near_any = 0;
 #pragma unroll
   for (int i = 7; i >= 0; --i) {
@@ -114,9 +116,7 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float low, flo
     near_any |= (fabsf(off) > 0.5f - 0x1p-14f) ? 1u << i : 0u;
     word = word * 16u + __float_as_uint(r);  // (the constant's share is taken off below)
   }
-  // sum over i of kRoundBits * 16^i: only its lowest nibble positions reach 32 bits
-  constexpr uint32_t kShare = kRoundBits * 0x11111111u;
-  word -= kShare;
+  word -= kRoundShare;
   while (near_any) {
     const int i = __ffs(near_any) - 1;
     near_any &= near_any - 1;
@@ -126,6 +126,35 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float low, flo
     word = (word & ~(15u << (4 * i))) | (code_at_border(xi, low, scale, inv) << (4 * i));
   }
   return word;
+}
+
+// bf16 rows: low is the minimum itself, so that no quotient lies below 0, and the scale's
+// rounding takes none above 15.03.  The quotient is taken a little low (2^-20 of itself,
+// more than its error), which leaves one question, whether d reaches the border above the
+// code, and that is answered exactly by r = d - c * scale, where d is exact: checked, and
+// otherwise (exponents more than 16 apart) left to the path above.  Ties are common among
+// bf16 values and cost nothing here.
+__device__ __forceinline__ uint32_t codes_bf16(const float (&x)[8], float low, float scale, float inv) {
+  const float half = 0.5f * scale, under = inv * (1.f - 0x1p-20f);
+  uint32_t word = 0;
+  bool exact = true;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    const float d = x[i] - low;
+    exact = exact && d + low == x[i];
+    float r = fmaf(d, under, kRound);
+    if (fmaf(kRound - r, scale, d) >= half) r += 1.f;
+    word = word * 16u + __float_as_uint(r);
+  }
+  return exact ? word - kRoundShare : codes_near(x, low, scale, inv);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float low, float scale) {
+  if (!(scale > 0.f)) return 0u;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));  // (2^-100 <= scale: no underflow)
+  return sizeof(T) == 2 ? codes_bf16(x, low, scale, inv) : codes_near(x, low, scale, inv);
 }
 
 __device__ __forceinline__ float min3_nan(float a, float b, float c) {
@@ -265,7 +294,7 @@ __global__ void __launch_bounds__(kThreads)
     raw[n].values(x);
     float scale, low;
     group_params(x, scale, low);  // (every lane takes part in the exchanges)
-    uint32_t word = codes_of(x, low, scale);
+    uint32_t word = codes_of<T>(x, low, scale);
     const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
     if (run.t < run.live && run.base != nullptr) {
       uint8_t* blk = run.base;
