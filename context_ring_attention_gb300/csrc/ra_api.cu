@@ -1010,6 +1010,13 @@ ra_status ra_plan_window(const ra_problem* prob, int64_t window, int64_t sinks, 
   if (prob->causal != 1) return fail(RA_ERR_INVALID_ARG, "a windowed plan is causal: causal must be 1");
   if (window < 1) return fail(RA_ERR_INVALID_ARG, "window must be >= 1");
   if (sinks < 0) return fail(RA_ERR_INVALID_ARG, "sinks must be >= 0");
+  // Positions, and their differences of a window, stay in 32 bits; and a work item ends well
+  // within the kernels' wait budget (its record is waited for until then): 2^24 keys are
+  // 131072 tiles, a fifth of a second.  The backward's items hold a group's heads.
+  if (prob->seq > (int64_t(1) << 30)) return fail(RA_ERR_UNSUPPORTED, "seq above 2^30 under a window");
+  const int64_t reach = std::min(prob->seq, std::min(window, prob->seq) + std::min(sinks, prob->seq));
+  if (prob->dtype == RA_DTYPE_BF16 && reach > (int64_t(1) << 24) / std::max(1, prob->heads_q / prob->heads_kv / 2))
+    return fail(RA_ERR_UNSUPPORTED, "window + sinks above 2^24 / max(1, heads_q / heads_kv / 2) keys (bf16)");
   return make_plan(prob, window, sinks, out);
 }
 

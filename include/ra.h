@@ -136,10 +136,14 @@ ra_status ra_plan(const ra_problem* prob, ra_plan_t* out);
  * sinks: >= 0; any value from seq on is the whole causal prefix as well.
  * ra_plan_tile_counts on it: FULL when every query of the tile sees every key, PARTIAL
  * for the other key tiles within reach of the query tile, SKIP for the rest.
- * K and V must be finite: a key that a query does not see enters its products with
- * weight zero where it shares a tile with keys that are seen, and zero times an
- * infinity or a NaN is a NaN.
- * Errors: as ra_plan, and RA_ERR_INVALID_ARG (causal 0, window < 1, sinks < 0).
+ * K and V (and Q and dO in ra_bwd) must be finite: a key that a query does not see
+ * enters its products with weight zero where it shares a tile with keys that are seen,
+ * and zero times an infinity or a NaN is a NaN.
+ * Its LSE is that of the unrounded weights.  Its kernels hold no counters: calls that
+ * share the plan may be captured into graphs (keep the plan while a graph of them lives).
+ * Errors: as ra_plan, and RA_ERR_INVALID_ARG (causal 0, window < 1, sinks < 0),
+ * RA_ERR_UNSUPPORTED (seq above 2^30; BF16: window + sinks, within seq, above 2^24 over
+ * max(1, Hq / Hkv / 2)).
  */
 ra_status ra_plan_window(const ra_problem* prob, int64_t window, int64_t sinks, ra_plan_t* out);
 
@@ -284,7 +288,8 @@ ra_status ra_bwd(ra_plan_t plan, const void* q, const void* k, const void* v, co
 /*
  * ra_bwd_scratch_size -- bytes of the scratch buffer ra_bwd needs for this plan:
  * 512 bytes per 64-row block of every (batch, query head, shard), about
- * 8 * B * Hq * S bytes.  Host only.  Errors: RA_ERR_INVALID_ARG (null arguments).
+ * 8 * B * Hq * S bytes; for a windowed BF16 plan also the fp32 partial sums of the key
+ * tiles that hold sinks.  Host only.  Errors: RA_ERR_INVALID_ARG (null arguments).
  */
 ra_status ra_bwd_scratch_size(ra_plan_t plan, int64_t* bytes);
 
@@ -493,8 +498,9 @@ typedef struct ra_kv4_s* ra_kv4_t;
 /*
  * ra_kv4_plan -- validate a cache's description and create its handle, which owns a
  * device status word and one event per stream its kernels were launched on (host-only
- * without a device, as ra_plan).  Release it with ra_kv4_destroy.  One host thread at a
- * time may use a handle; its calls may overlap on the GPU.
+ * without a device, as ra_plan).  Release it with ra_kv4_destroy, after the graphs that
+ * captured its calls.  One host thread at a time may use a handle; its calls may overlap
+ * on the GPU.
  * Errors: RA_ERR_INVALID_ARG (null arguments, sizes < 1, page_rows, Hq % Hkv, window or
  * sinks < 0, bad enum or scale), RA_ERR_UNSUPPORTED (head_dim, more than 2^31-1 pages,
  * a cache beyond 2^62 bytes), RA_ERR_CUDA.
@@ -547,7 +553,9 @@ ra_status ra_kv4_read(ra_kv4_t kv, const void* cache, int64_t batch, int64_t row
  * what pages hold there does not matter.
  * bf16: Q enters the products as it is and the softmax weights rounded to bf16, each
  * times its value's scale; sums are fp32.  float32: both are split into three bf16 terms,
- * which keeps fp32 accuracy.
+ * which keeps fp32 accuracy.  A value group's scale (its range / 15) times the largest
+ * weight must stay below 2^58; groups of scales below 2^-52 lose precision relative to
+ * themselves.
  * scratch: ra_kv4_attend_scratch_size bytes (NULL when that is 0), not shared by calls
  * that may overlap.  Device pointers, 16-byte aligned (page_table, length: 4-byte).
  * Asynchronous on stream; allocates nothing.

@@ -44,6 +44,20 @@ def test_refusals(window, sinks, kw, status):
     assert err.value.name == status
 
 
+def test_reach_beyond_the_kernels_is_refused():
+    """Sequences above 2^30 positions, and windows whose work items would outlast the
+    kernels' bounded waits.  (float32 plans have no work lists: building them is quick.)"""
+    big = dict(batch=1, heads_q=1, heads_kv=1, n_shards=1, head_dim=64, dtype="f32")
+    _plan(4, 0, seq=1 << 30, **big)
+    with pytest.raises(ra.RaError) as err:
+        _plan(4, 0, seq=(1 << 30) + 1, **big)
+    assert err.value.name == "RA_ERR_UNSUPPORTED"
+    for window, sinks, heads in ((1 << 24, 1, 1), (1 << 25, 0, 2), (1 << 22, 1, 16), (1, 1 << 25, 1)):
+        with pytest.raises(ra.RaError) as err:
+            _plan(window, sinks, batch=1, seq=1 << 26, heads_q=heads, heads_kv=1, n_shards=1)
+        assert err.value.name == "RA_ERR_UNSUPPORTED"
+
+
 def test_non_causal_is_refused():
     lib = ra.load_library()
     prob = ra._Problem(1, 512, 4, 2, 128, 4, 0, 0, 1, 0.0)
