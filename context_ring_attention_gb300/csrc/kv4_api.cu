@@ -129,8 +129,9 @@ ra_status split_of(const ra_kv4_s* kv, int64_t batch, int64_t rows, int64_t tabl
     keys = std::min(keys, pb.window + rows + pb.sinks + 32);
   const int64_t units = batch * pb.heads_kv * out->tiles;
   const int64_t sms = kv->sm_count > 0 ? kv->sm_count : 148;
-  const int64_t most = std::max<int64_t>(1, keys / (16 * 8));
-  out->splits = std::max<int64_t>(1, std::min({(4 * sms + units - 1) / units, most, int64_t(65535)}));
+  const int64_t want = (batch == 1 ? 4 : 8) * sms;
+  const int64_t most = std::max<int64_t>(1, keys / (16 * 16));
+  out->splits = std::max<int64_t>(1, std::min({(want + units - 1) / units, most, int64_t(ra::kMaxSplits)}));
   return RA_OK;
 }
 
