@@ -108,12 +108,15 @@ struct Split {
   int64_t tiles, splits;
 };
 
-// Shares of the keys: as many CTAs as the GPU holds (4 an SM) for one sequence, whose shares
-// are equal, and twice that for several, whose lengths differ, so that the short ones'
-// CTAs make room for more (64k tokens: 29 against 35 us with twice as many; 8 sequences of
-// up to 64k: 128 against 114 us).  No CTA gets fewer than 16 blocks of 16 tokens, four a
-// warp: below that the join costs more than the share saves (8k tokens: 10.5 us, with 8
-// blocks 12.1, with 32 11.5).
+// Shares of the keys: as many CTAs as the GPU holds (3 an SM) for one sequence, whose shares
+// are equal (64k tokens: 27 us; with twice as many shares 35), and twice that for several,
+// whose lengths differ, so that the short ones' CTAs make room for more.  With 3, 6 and 9 CTAs
+// an SM: 32 sequences under a window of 8192 tokens 96, 86 and 84 us; 8 of up to 64k 117, 117
+// and 112; 16 of up to 8k 40, 41 and 45; 4 of 64k in fp32 117, 110 and 116.  Rounded down,
+// since one CTA too many is a wave of its own (4 new tokens of 8k: 16 against 19 us; 64
+// sequences of up to 2k: 36 against 42).  No CTA gets fewer than 16 blocks of 16 tokens, four
+// a warp: below that the join costs more than the share saves (8k tokens, one block a warp at
+// a time: 10.5 us; with 8 blocks 12.1, with 32 11.5).
 ra_status split_of(const ra_kv4_s* kv, int64_t batch, int64_t rows, int64_t table_width, Split* out) {
   const ra_kv4_problem& pb = kv->prob;
   if (batch < 1 || rows < 1 || table_width < 1)
@@ -129,9 +132,9 @@ ra_status split_of(const ra_kv4_s* kv, int64_t batch, int64_t rows, int64_t tabl
     keys = std::min(keys, pb.window + rows + pb.sinks + 32);
   const int64_t units = batch * pb.heads_kv * out->tiles;
   const int64_t sms = kv->sm_count > 0 ? kv->sm_count : 148;
-  const int64_t want = (batch == 1 ? 4 : 8) * sms;
+  const int64_t want = (batch == 1 ? 3 : 6) * sms;
   const int64_t most = std::max<int64_t>(1, keys / (16 * 16));
-  out->splits = std::max<int64_t>(1, std::min({(want + units - 1) / units, most, int64_t(ra::kMaxSplits)}));
+  out->splits = std::max<int64_t>(1, std::min({want / units, most, int64_t(ra::kMaxSplits)}));
   return RA_OK;
 }
 

@@ -29,7 +29,18 @@
 //
 // Split: a CTA of 4 warps takes a share of the 16-token blocks that a tile sees, each warp
 // a quarter; m, l and O are joined across warps in shared memory, and across CTAs by a
-// second kernel in a fixed order.
+// second kernel in a fixed order.  A warp works on two blocks at a time: with one at a time
+// and four CTAs an SM (128 registers) its chains of dependent instructions, from the scores
+// to the weights, were what it waited for; two blocks (166 registers, three CTAs an SM) took
+// one sequence of 1M tokens from 276 to 257 us and 16 new tokens of 64k from 180 to 136.
+// Two blocks in 128 registers: 276 us; two pairs a warp in shared memory for three: 260.
+//
+// Measured (32 query and 8 key/value heads, d = 128, bf16, one new token): 1M tokens 257 us,
+// 1.34 GB of cache at 5.2 TB/s (0.77 of a plain copy's rate); 64k tokens 27 us; 32 sequences
+// of 2k to 32k under a window of 8192 tokens 86 us.  What bounds it is the issue of
+// instructions, some 390 a block and warp, about half of them for turning codes and weights
+// into operands.  fp32 takes three terms per query and weight and three times the products:
+// 4 sequences of 64k tokens 110 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -44,13 +55,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kTile = 8;  // query rows of a tile
-constexpr int kStages = 5;  // cache blocks a warp holds or has under way
+constexpr int kPairs = 3;  // pairs of cache blocks a warp holds or has under way
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleSlack = 8.0f;  // log2 units: keep a stale maximum while p <= 2^8
 
 // D = A (16 x 16, row) * B (16 x 8, col) + D, bf16 in, fp32 sums.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -58,7 +69,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 // The same with zeros for D on the way in.
 __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -67,7 +78,7 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a
 // Transpose of an 8 x 8 matrix of 16-bit elements held two to a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 // Pairs of codes as bf16 operands: n * 2^-133 from bits 0-3 and 16-19 of x, 16 n * 2^-133
@@ -148,7 +159,7 @@ __device__ __forceinline__ Blocks blocks_of(const Kv4AttendParams& P, int32_t le
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 1) kv4_attend_kernel(const Kv4AttendParams P) {
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_attend_kernel(const Kv4AttendParams P) {
   using F = Kv4Block<D>;
   constexpr int G = F::kGroups;
   constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
@@ -226,7 +237,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 1) kv4_atten
   extern __shared__ __align__(16) uint8_t ring[];
   // The fragments wait in shared memory, the same for all warps: registers are what bounds
   // the warps of an SM.
-  uint32_t* const qsm = reinterpret_cast<uint32_t*>(ring + kWarps * kStages * F::kBytes);
+  uint32_t* const qsm = reinterpret_cast<uint32_t*>(ring + kWarps * kPairs * 2 * F::kBytes);
   if (warp == 0) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -257,11 +268,11 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 1) kv4_atten
       for (int e = 0; e < 4; ++e) o[g][i][e] = 0.f;
   }
 
-  // Each warp brings its blocks through a ring of its own in shared memory, kStages - 1
-  // ahead of the one it works on.
-  uint8_t* const mine = ring + warp * (kStages * F::kBytes);
+  // Each warp brings its blocks, two at a time, through slots of its own in shared memory:
+  // the next pairs are under way while it works on one.
+  uint8_t* const mine = ring + warp * (kPairs * 2 * F::kBytes);
   const uint32_t mine_at = ptx::smem_addr(mine);
-  uint32_t bad = 0;  // stages whose page is out of range
+  uint32_t bad = 0;  // blocks of the slots that are not there: the page is out of range, or past the end
   // A warp's blocks follow each other: their place is looked up in the page table at the
   // first of each page, at the warp's first and behind the sinks.
   const int32_t w_lo = x_lo + (int32_t)((int64_t)(x_hi - x_lo) * warp / kWarps);
@@ -274,33 +285,35 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 1) kv4_atten
   const uint8_t* src = nullptr;  // the next block to fetch, or nullptr: its page is out of range
   int32_t left = 0;              // blocks from there to the page's end or the sinks'
   int32_t fx = w_lo;
-  auto fetch = [&](int slot) {
-    if (fx < w_hi) {
-      if (left == 0) {
-        const int32_t block = block_at(fx);
-        const int32_t page_at = block / bpp, in_page = block - page_at * bpp;
-        const int32_t page = __ldg(table + page_at);
-        src = of_head + page * page_bytes + (int64_t)in_page * F::kBytes;
-        left = bpp - in_page;
-        if (fx < blk.first) left = min(left, blk.first - fx);
-        if (page < 0 || page >= P.t.pages) {
-          src = nullptr;
-          if (lane == 0) atomicOr(P.t.status, kKv4StatusRange);
-        }
+  auto fetch_one = [&](int at) {
+    bad |= 1u << at;
+    if (fx >= w_hi) return;
+    if (left == 0) {
+      const int32_t block = block_at(fx);
+      const int32_t page_at = block / bpp, in_page = block - page_at * bpp;
+      const int32_t page = __ldg(table + page_at);
+      src = of_head + page * page_bytes + (int64_t)in_page * F::kBytes;
+      left = bpp - in_page;
+      if (fx < blk.first) left = min(left, blk.first - fx);
+      if (page < 0 || page >= P.t.pages) {
+        src = nullptr;
+        if (lane == 0) atomicOr(P.t.status, kKv4StatusRange);
       }
-      bad &= ~(1u << slot);
-      if (src == nullptr) {
-        bad |= 1u << slot;
-      } else {
-        const uint32_t dst = mine_at + slot * F::kBytes + lane * 16;
-#pragma unroll
-        for (int i = 0; i * 512 < F::kBytes; ++i)
-          if (i * 512 + 512 <= F::kBytes || lane * 16 + i * 512 < F::kBytes) copy16(dst + i * 512, src + i * 512);
-        src += F::kBytes;
-      }
-      --left;
-      ++fx;
     }
+    if (src != nullptr) {
+      bad &= ~(1u << at);
+      const uint32_t dst = mine_at + at * F::kBytes + lane * 16;
+#pragma unroll
+      for (int i = 0; i * 512 < F::kBytes; ++i)
+        if (i * 512 + 512 <= F::kBytes || lane * 16 + i * 512 < F::kBytes) copy16(dst + i * 512, src + i * 512);
+      src += F::kBytes;
+    }
+    --left;
+    ++fx;
+  };
+  auto fetch = [&](int slot) {
+    fetch_one(2 * slot);
+    fetch_one(2 * slot + 1);
     copies_commit();  // (an empty group where there is nothing to fetch)
   };
   // Blocks that every row sees whole need no mask: they end at the first query or before,
@@ -309,88 +322,110 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 1) kv4_atten
   const int32_t whole_from = P.window == 0 ? 0 : (max(len - P.window, 0) + 15) >> 4;
   const int32_t whole_sinks = P.sinks >> 4;
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  for (int i = 0; i < kPairs; ++i) fetch(i);
 
   int slot = 0;
-  for (int32_t x = w_lo; x < w_hi; ++x) {
-    copies_wait<kStages - 2>();
-    __syncwarp();  // every lane's copies have landed, and every lane is done with the slot before
-    fetch(slot == 0 ? kStages - 1 : slot - 1);
-    const uint8_t* base = mine + slot * F::kBytes;
-    const bool skip = (bad >> slot) & 1u;
-    slot = slot == kStages - 1 ? 0 : slot + 1;
-    if (skip) continue;
-    const int32_t block = block_at(x);
-    uint32_t k0[G], k1[G], kp0[G], kp1[G], vp0[G], vp1[G], vw[4][G / 2];
-    load_words<G>(base + F::kOffK + tok0 * F::kCodeBytes + c * (4 * G), k0);
-    load_words<G>(base + F::kOffK + tok1 * F::kCodeBytes + c * (4 * G), k1);
-    load_words<G>(base + F::kOffKPar + tok0 * F::kParBytes, kp0);
-    load_words<G>(base + F::kOffKPar + tok1 * F::kParBytes, kp1);
+  for (int32_t x = w_lo; x < w_hi; x += 2, slot = slot == kPairs - 1 ? 0 : slot + 1) {
+    copies_wait<kPairs - 1>();
+    __syncwarp();  // every lane's copies have landed
+    const uint8_t* base[2] = {mine + (2 * slot) * F::kBytes, mine + (2 * slot + 1) * F::kBytes};
+    const uint32_t gone = (bad >> (2 * slot)) & 3u;
 
-    // Scores: s[0], s[1] of key tok0 for rows 2c, 2c + 1; s[2], s[3] of key tok1.  The
-    // minima's part first, as products of their own: a parameter word is (scale, low) of
-    // key and group c, met by (0, sum of q) in bf16 terms.
-    float s[4];
+    // Scores: s[n][0], s[n][1] of key tok0 of block n for rows 2c, 2c + 1; s[n][2], s[n][3]
+    // of key tok1.  The minima's part first, as products of their own: a parameter word is
+    // (scale, low) of key and group c, met by (0, sum of q) in bf16 terms.
+    float s[2][4];
+    uint32_t kp0[2][G], kp1[2][G];
     {
-      uint32_t lw[2], qw[4];
-      lw[0] = *reinterpret_cast<const uint32_t*>(base + F::kOffKPar + tok0 * F::kParBytes + (c & (G - 1)) * 4);
-      lw[1] = *reinterpret_cast<const uint32_t*>(base + F::kOffKPar + tok1 * F::kParBytes + (c & (G - 1)) * 4);
+      uint32_t qw[4];
       load_words<4>(reinterpret_cast<const uint8_t*>(qsm + G * kTerms * 32 * 4 + lane * 4), qw);
-      const uint32_t a[4] = {lw[0], lw[1], lw[0], lw[1]};
       const uint32_t b01[2] = {qw[0], qw[1]}, b23[2] = {qw[2], qw[3]};
-      mma16816_first(s, a, b23);
-      mma16816(s, a, b01);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        uint32_t lw[2];
+        lw[0] = *reinterpret_cast<const uint32_t*>(base[n] + F::kOffKPar + tok0 * F::kParBytes + (c & (G - 1)) * 4);
+        lw[1] = *reinterpret_cast<const uint32_t*>(base[n] + F::kOffKPar + tok1 * F::kParBytes + (c & (G - 1)) * 4);
+        const uint32_t a[4] = {lw[0], lw[1], lw[0], lw[1]};
+        mma16816_first(s[n], a, b23);
+        mma16816(s[n], a, b01);
+        load_words<G>(base[n] + F::kOffKPar + tok0 * F::kParBytes, kp0[n]);
+        load_words<G>(base[n] + F::kOffKPar + tok1 * F::kParBytes, kp1[n]);
+      }
     }
+    {
+      uint32_t k0[2][G], k1[2][G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float acc[4];
-      uint32_t qg[kTerms][4];
+      for (int n = 0; n < 2; ++n) {
+        load_words<G>(base[n] + F::kOffK + tok0 * F::kCodeBytes + c * (4 * G), k0[n]);
+        load_words<G>(base[n] + F::kOffK + tok1 * F::kCodeBytes + c * (4 * G), k1[n]);
+      }
 #pragma unroll
-      for (int n = 0; n < kTerms; ++n)
-        load_words<4>(reinterpret_cast<const uint8_t*>(qsm + ((g * kTerms + n) * 32 + lane) * 4), qg[n]);
+      for (int g = 0; g < G; ++g) {
+        float acc[2][4];
+        uint32_t qg[kTerms][4];
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {  // nibbles (i, i + 4) and (i + 1, i + 5) of the words
-        const uint32_t x0 = k0[g] >> (4 * i), x1 = k1[g] >> (4 * i);
-        const uint32_t a[4] = {codes_lo(x0), codes_lo(x1), codes_hi(x0), codes_hi(x1)};
+        for (int n = 0; n < kTerms; ++n)
+          load_words<4>(reinterpret_cast<const uint8_t*>(qsm + ((g * kTerms + n) * 32 + lane) * 4), qg[n]);
 #pragma unroll
-        for (int n = kTerms - 1; n >= 0; --n) {
-          const uint32_t q2[2] = {qg[n][i], qg[n][i + 1]};
-          if (i == 0 && n == kTerms - 1) mma16816_first(acc, a, q2);
-          else mma16816(acc, a, q2);
+        for (int i = 0; i < 4; i += 2) {  // nibbles (i, i + 4) and (i + 1, i + 5) of the words
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t x0 = k0[n][g] >> (4 * i), x1 = k1[n][g] >> (4 * i);
+            const uint32_t a[4] = {codes_lo(x0), codes_lo(x1), codes_hi(x0), codes_hi(x1)};
+#pragma unroll
+            for (int t = kTerms - 1; t >= 0; --t) {
+              const uint32_t q2[2] = {qg[t][i], qg[t][i + 1]};
+              if (i == 0 && t == kTerms - 1) mma16816_first(acc[n], a, q2);
+              else mma16816(acc[n], a, q2);
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float s0 = scale_of(kp0[n][g]), s1 = scale_of(kp1[n][g]);
+          s[n][0] = fmaf(s0, acc[n][0], s[n][0]);
+          s[n][1] = fmaf(s0, acc[n][1], s[n][1]);
+          s[n][2] = fmaf(s1, acc[n][2], s[n][2]);
+          s[n][3] = fmaf(s1, acc[n][3], s[n][3]);
         }
       }
-      const float s0 = scale_of(kp0[g]), s1 = scale_of(kp1[g]);
-      s[0] = fmaf(s0, acc[0], s[0]);
-      s[1] = fmaf(s0, acc[1], s[1]);
-      s[2] = fmaf(s1, acc[2], s[2]);
-      s[3] = fmaf(s1, acc[3], s[3]);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] *= back[e & 1];
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] *= back[e & 1];
 
-    bool seen[4] = {true, true, true, true};
-    const bool whole = block < whole_to && (block >= whole_from || block < whole_sinks);
+    const int32_t first_block = block_at(x), second_block = block_at(x + 1);
+    uint32_t seen = 0xffu;  // bit 4n + e
+    const bool whole = gone == 0u && first_block < whole_to && second_block < whole_to &&
+                       (first_block >= whole_from || first_block < whole_sinks) &&
+                       (second_block >= whole_from || second_block < whole_sinks);
     if (!whole) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int32_t j = block * kKvBlockRows + (e < 2 ? tok0 : tok1), i = qpos[e & 1];
-        seen[e] = j <= i && (P.window == 0 || j > i - P.window || j < P.sinks);
-        if (!seen[e]) s[e] = -INFINITY;
-      }
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int32_t j = (n ? second_block : first_block) * kKvBlockRows + (e < 2 ? tok0 : tok1), i = qpos[e & 1];
+          if (((gone >> n) & 1u) || !(j <= i && (P.window == 0 || j > i - P.window || j < P.sinks))) {
+            seen &= ~(1u << (4 * n + e));
+            s[n][e] = -INFINITY;
+          }
+        }
     }
 
     // Running maximum, the same in all lanes of a row: moved only when a score exceeds it
     // by the slack.
-    const bool grow = fmaxf(s[0], s[2]) > m[0] + kRescaleSlack || fmaxf(s[1], s[3]) > m[1] + kRescaleSlack;
-    if (__any_sync(0xffffffffu, grow)) {
+    float mx[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(s[0][e], s[0][e + 2]), fmaxf(s[1][e], s[1][e + 2]));
+    if (__any_sync(0xffffffffu, mx[0] > m[0] + kRescaleSlack || mx[1] > m[1] + kRescaleSlack)) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = fmaxf(s[e], s[e + 2]);
 #pragma unroll
-        for (int d = 4; d <= 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        mx = fmaxf(mx, m[e]);
-        const float alpha = m[e] == -INFINITY ? 0.f : ptx::ex2_approx(m[e] - mx);
-        m[e] = mx;
+        for (int d = 4; d <= 16; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+        mx[e] = fmaxf(mx[e], m[e]);
+        const float alpha = m[e] == -INFINITY ? 0.f : ptx::ex2_approx(m[e] - mx[e]);
+        m[e] = mx[e];
         l[e] *= alpha;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -403,67 +438,77 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 1) kv4_atten
         }
       }
     }
-    float p[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float ref = m[e & 1] == -INFINITY ? 0.f : m[e & 1] - kShift;
-      p[e] = ptx::ex2_approx(s[e] - ref);
-      l[e & 1] += p[e];
+    for (int e = 0; e < 2; ++e) {
+      const float ref = m[e] == -INFINITY ? 0.f : m[e] - kShift;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = e; i < 4; i += 2) {
+          s[n][i] = ptx::ex2_approx(s[n][i] - ref);  // p from here on
+          l[e] += s[n][i];
+        }
     }
 
-    asm volatile("" ::: "memory");  // (the values' words are not held during the scores)
-    load_words<G>(base + F::kOffVPar + tok0 * F::kParBytes, vp0);
-    load_words<G>(base + F::kOffVPar + tok1 * F::kParBytes, vp1);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) load_words<G / 2>(base + F::kOffV + vt[n] * F::kCodeBytes + r * (2 * G), vw[n]);
     // O: per group, p times the value's scale as the 16 x 8 operand (keys x rows), the
     // codes of two keys a register as the 16 x 16 one (channels x keys).
     auto values = [&](auto masked) {
       const uint32_t minus8[4] = {kMinus8Lo, kMinus8Hi, kMinus8Lo, kMinus8Hi};
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const float s0 = scale_of(vp0[g]), s1 = scale_of(vp1[g]);
-        const float m0 = fmaf(8.f, s0, low_of(vp0[g])), m1 = fmaf(8.f, s1, low_of(vp1[g]));
-        float w[4] = {p[0] * s0, p[1] * s0, p[2] * s1, p[3] * s1};
-        if (decltype(masked)::value) {  // what stands in places that are not seen may be anything
-          const float mid[4] = {m0, m0, m1, m1};
+      for (int n = 0; n < 2; ++n) {
+        asm volatile("" ::: "memory");  // (one block's words are held at a time)
+        uint32_t vp0[G], vp1[G], vw[4][G / 2];
+        load_words<G>(base[n] + F::kOffVPar + tok0 * F::kParBytes, vp0);
+        load_words<G>(base[n] + F::kOffVPar + tok1 * F::kParBytes, vp1);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (!seen[e]) w[e] = 0.f;
-            else pm[g][e & 1] = fmaf(p[e], mid[e], pm[g][e & 1]);
+        for (int i = 0; i < 4; ++i) load_words<G / 2>(base[n] + F::kOffV + vt[i] * F::kCodeBytes + r * (2 * G), vw[i]);
+        const float(&p)[4] = s[n];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float s0 = scale_of(vp0[g]), s1 = scale_of(vp1[g]);
+          const float m0 = fmaf(8.f, s0, low_of(vp0[g])), m1 = fmaf(8.f, s1, low_of(vp1[g]));
+          float w[4] = {p[0] * s0, p[1] * s0, p[2] * s1, p[3] * s1};
+          if (decltype(masked)::value) {  // what stands in places that are not seen may be anything
+            const float mid[4] = {m0, m0, m1, m1};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (!((seen >> (4 * n + e)) & 1u)) w[e] = 0.f;
+              else pm[g][e & 1] = fmaf(p[e], mid[e], pm[g][e & 1]);
+            }
+          } else {
+            pm[g][0] = fmaf(p[0], m0, fmaf(p[2], m1, pm[g][0]));
+            pm[g][1] = fmaf(p[1], m0, fmaf(p[3], m1, pm[g][1]));
           }
-        } else {
-          pm[g][0] = fmaf(p[0], m0, fmaf(p[2], m1, pm[g][0]));
-          pm[g][1] = fmaf(p[1], m0, fmaf(p[3], m1, pm[g][1]));
-        }
-        uint32_t w0[kTerms], w1[kTerms];
-        split_pair<kTerms>(w[0], w[1], w0);
-        split_pair<kTerms>(w[2], w[3], w1);
-        const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
-        const uint32_t a01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
-        const uint32_t a23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
-        uint32_t a[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t x01 = a01 >> (8 * i), x23 = a23 >> (8 * i);
-          a[i][0] = codes_lo(x01);
-          a[i][1] = codes_hi(x01);
-          a[i][2] = codes_lo(x23);
-          a[i][3] = codes_hi(x23);
-        }
-#pragma unroll
-        for (int n = kTerms - 1; n >= 0; --n) {
-          const uint32_t b2[2] = {transpose8(w0[n]), transpose8(w1[n])};
+          uint32_t w0[kTerms], w1[kTerms];
+          split_pair<kTerms>(w[0], w[1], w0);
+          split_pair<kTerms>(w[2], w[3], w1);
+          const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+          const uint32_t a01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
+          const uint32_t a23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
+          uint32_t a[2][4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            mma16816(o[g][i], a[i], b2);
-            mma16816(o[g][i], minus8, b2);
+            const uint32_t x01 = a01 >> (8 * i), x23 = a23 >> (8 * i);
+            a[i][0] = codes_lo(x01);
+            a[i][1] = codes_hi(x01);
+            a[i][2] = codes_lo(x23);
+            a[i][3] = codes_hi(x23);
+          }
+#pragma unroll
+          for (int t = kTerms - 1; t >= 0; --t) {
+            const uint32_t b2[2] = {transpose8(w0[t]), transpose8(w1[t])};
+            mma16816(o[g][0], a[0], b2);
+            mma16816(o[g][1], a[1], b2);
+            mma16816(o[g][0], minus8, b2);
+            mma16816(o[g][1], minus8, b2);
           }
         }
       }
     };
     if (whole) values(std::false_type());
     else values(std::true_type());
+    __syncwarp();  // every lane is done with the slot
+    fetch(slot);
   }
 
   // Rows' sums over the lanes that held different keys.
@@ -481,7 +526,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 1) kv4_atten
   copies_wait<0>();
   __syncthreads();
   using Row = float[D + 4];
-  static_assert(kWarps * kTile * (D + 4 + 2) * 4 <= kWarps * kStages * F::kBytes, "join area");
+  static_assert(kWarps * kTile * (D + 4 + 2) * 4 <= kWarps * kPairs * 2 * F::kBytes, "join area");
   auto sm_o = reinterpret_cast<Row(*)[kTile]>(ring);
   auto sm_m = reinterpret_cast<float(*)[kTile]>(ring + sizeof(Row) * kTile * kWarps);
   auto sm_l = sm_m + kWarps;
@@ -600,7 +645,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Atte
 template <typename T, int D>
 cudaError_t attend_as(const Kv4AttendParams& prm, cudaStream_t st) {
   constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
-  constexpr int kSmem = kWarps * kStages * Kv4Block<D>::kBytes + 32 * 16 * ((D / 32) * kTerms + 1);
+  constexpr int kSmem = kWarps * kPairs * 2 * Kv4Block<D>::kBytes + 32 * 16 * ((D / 32) * kTerms + 1);
   static std::atomic<int> ready[kMaxDevices];
   const char* why = "";
   cudaError_t e = prepare_once(kv4_attend_kernel<T, D>, ready, kWarps * 32, 0, kSmem, &why);
