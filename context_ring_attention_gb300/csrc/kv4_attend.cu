@@ -38,7 +38,7 @@
 // Measured (32 query and 8 key/value heads, d = 128, bf16, one new token): 1M tokens 257 us,
 // 1.34 GB of cache at 5.2 TB/s (0.77 of a plain copy's rate); 64k tokens 27 us; 32 sequences
 // of 2k to 32k under a window of 8192 tokens 86 us.  What bounds it is the issue of
-// instructions, some 390 a block and warp, about half of them for turning codes and weights
+// instructions, some 350 a block and warp, about half of them for turning codes and weights
 // into operands.  fp32 takes three terms per query and weight and three times the products:
 // 4 sequences of 64k tokens 110 us.
 #include <cuda_bf16.h>

@@ -8,9 +8,17 @@
 // 32-bit word of key codes, or two 16-bit words of value codes; four threads share a
 // group, and its minimum and maximum take two exchanges among them.  A warp takes a run of
 // tokens of one head, all their loads first, and counts its place in the cache on from
-// token to token.  What bounds a plain form is not memory but the arithmetic of a code, so
-// it is kept to about a dozen instructions: rounding by adding 1.5 * 2^23, codes packed by
-// a multiply-add each, and the exact decision taken only next to a border of two codes.
+// token to token.  What bounds a plain form is not memory but the arithmetic of a code
+// (190 instructions a row and thread, 76% of the issue slots, are left), so it is kept to
+// about a dozen: rounding by adding 1.5 * 2^23, codes packed by a multiply-add each, pairs
+// of values by one instruction, and the exact decision taken only next to a border of two
+// codes.
+//
+// Measured (bf16, d = 128, 32768 tokens of 8 heads): write 54 us for 134 MB of rows and
+// 42 MB of cache, 3.2 TB/s; read 37 us for the same bytes, 4.7 TB/s.  Pairs by one
+// instruction took the write from 62 us to 59.5, the quotient by 15 without a division to
+// 57.5, and 64 registers, for four CTAs an SM instead of three, to 54.
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -128,6 +136,28 @@ __device__ __forceinline__ uint32_t codes_near(const float (&x)[8], float low, f
   return word;
 }
 
+// Two fp32 operations by one instruction.
+__device__ __forceinline__ uint64_t pair_bits(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 pair_of(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return pair_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return pair_of(r);
+}
+
 // bf16 rows: low is the minimum itself, so that no quotient lies below 0, and the scale's
 // rounding takes none above 15.03.  The quotient is taken a little low (2^-20 of itself,
 // more than its error), which leaves one question, whether d reaches the border above the
@@ -136,15 +166,21 @@ __device__ __forceinline__ uint32_t codes_near(const float (&x)[8], float low, f
 // bf16 values and cost nothing here.
 __device__ __forceinline__ uint32_t codes_bf16(const float (&x)[8], float low, float scale, float inv) {
   const float half = 0.5f * scale, under = inv * (1.f - 0x1p-20f);
+  const float2 low2 = {low, low}, under2 = {under, under}, scale2 = {scale, scale}, round2 = {kRound, kRound};
+  const float2 minus2 = {-1.f, -1.f};
   uint32_t word = 0;
   bool exact = true;
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float d = x[i] - low;
-    exact = exact && d + low == x[i];
-    float r = fmaf(d, under, kRound);
-    if (fmaf(kRound - r, scale, d) >= half) r += 1.f;
-    word = word * 16u + __float_as_uint(r);
+  for (int i = 6; i >= 0; i -= 2) {  // two at a time, by the paired fp32 instructions
+    const float2 xi = {x[i], x[i + 1]};
+    const float2 d = fma2(low2, minus2, xi), again = add2(d, low2);
+    exact = exact && again.x == x[i] && again.y == x[i + 1];
+    float2 r = fma2(d, under2, round2);
+    const float2 rest = fma2(fma2(r, minus2, round2), scale2, d);
+    if (rest.x >= half) r.x += 1.f;
+    if (rest.y >= half) r.y += 1.f;
+    word = word * 16u + __float_as_uint(r.y);
+    word = word * 16u + __float_as_uint(r.x);
   }
   return exact ? word - kRoundShare : codes_near(x, low, scale, inv);
 }
@@ -168,20 +204,51 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return d;
 }
 
-// One group's parameters from the 8 values of each of four neighbouring lanes.  The minimum
-// and maximum pass a NaN on, and an infinity makes the range infinite: either way the scale
-// is not finite.
-__device__ __forceinline__ void group_params(const float (&x)[8], float& scale, float& low) {
-  float lo = min3_nan(min3_nan(x[0], x[1], x[2]), min3_nan(x[3], x[4], x[5]), fminf(x[6], x[7]));
-  float hi = max3_nan(max3_nan(x[0], x[1], x[2]), max3_nan(x[3], x[4], x[5]), max3_nan(x[6], x[7], x[7]));
+// Minimum and maximum of the 8 values of each of four neighbouring lanes.  The maximum
+// passes a NaN on, and an infinity makes the range infinite: either way the scale is not
+// finite.
+__device__ __forceinline__ void group_bounds(const Raw<float>& raw, float& lo, float& hi) {
+  float x[8];
+  raw.values(x);
+  lo = min3_nan(min3_nan(x[0], x[1], x[2]), min3_nan(x[3], x[4], x[5]), fminf(x[6], x[7]));
+  hi = max3_nan(max3_nan(x[0], x[1], x[2]), max3_nan(x[3], x[4], x[5]), max3_nan(x[6], x[7], x[7]));
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     const float h = __shfl_xor_sync(0xffffffffu, hi, o);
     hi = max3_nan(hi, h, h);
   }
+}
+// bf16 rows: by pairs, the exchanges on the minimum and the maximum's negative together.
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ void group_bounds(const Raw<__nv_bfloat16>& raw, float& lo, float& hi) {
+  const uint32_t l2 = min2_nan(min2_nan(raw.w.x, raw.w.y), min2_nan(raw.w.z, raw.w.w));
+  const uint32_t h2 = max2_nan(max2_nan(raw.w.x, raw.w.y), max2_nan(raw.w.z, raw.w.w)) ^ 0x80008000u;
+  uint32_t both = min2_nan(__byte_perm(l2, h2, 0x5410), __byte_perm(l2, h2, 0x7632));
+  both = min2_nan(both, __shfl_xor_sync(0xffffffffu, both, 1));
+  both = min2_nan(both, __shfl_xor_sync(0xffffffffu, both, 2));
+  lo = __uint_as_float(both << 16);
+  hi = -__uint_as_float(both & 0xffff0000u);
+}
+
+// A group's scale and low: zeros for a scale below 2^-100, NaN for low where the range is not finite.
+__device__ __forceinline__ void params_of(float lo, float hi, float& scale, float& low) {
   low = bf16_round(lo);
-  scale = bf16_round(__fdiv_rn(hi - low, 15.f));
+  // (hi - low) / 15, correctly rounded: the quotient by the correctly rounded reciprocal, its
+  // exact remainder, and one correction by that (Markstein's theorem; the same bits as the
+  // division for every significand)
+  constexpr float kFifteenth = 1.f / 15.f;
+  const float range = hi - low, q = range * kFifteenth;
+  scale = bf16_round(fmaf(fmaf(-15.f, q, range), kFifteenth, q));
   if (!(fabsf(scale) <= 3.402823466e38f)) {
     scale = 0.f;
     low = __uint_as_float(0x7fff0000u);  // NaN
@@ -266,7 +333,7 @@ struct Run {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1)
     kv4_write_kernel(const Kv4RowsParams P, const T* __restrict__ k, const T* __restrict__ v) {
   using L = Lanes<T, D>;
   using F = Kv4Block<D>;
@@ -292,8 +359,9 @@ __global__ void __launch_bounds__(kThreads)
     if (__all_sync(0xffffffffu, run.t >= run.live)) break;
     float x[8];
     raw[n].values(x);
-    float scale, low;
-    group_params(x, scale, low);  // (every lane takes part in the exchanges)
+    float lo, hi, scale, low;
+    group_bounds(raw[n], lo, hi);  // (every lane takes part in the exchanges)
+    params_of(lo, hi, scale, low);
     uint32_t word = codes_of<T>(x, low, scale);
     const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
     if (run.t < run.live && run.base != nullptr) {
