@@ -558,7 +558,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float f = sm_m[w][row] == -INFINITY ? 0.f : ptx::ex2_approx(sm_m[w][row] - mx);
-      // (a warp that saw nothing of this row holds zeros)
+      // (a warp that saw nothing of this row holds zeros, one that saw only NaN a sum of NaN:
+      // a row is empty when its sum is 0)
       sum = fmaf(f, sm_l[w][row], sum);
       acc = fmaf(f, sm_o[w][row][ch], acc);
     }
@@ -568,8 +569,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
       if (ch == 0) P.part_ml[part * kTile + row] = make_float2(mx, sum);
     } else if (row0 + row < n_rows) {
       const int64_t out = ((int64_t)b * P.heads_q + (int64_t)h * P.group) * P.rows + row0 + row;
-      static_cast<T*>(P.o)[out * D + ch] = (T)(mx == -INFINITY ? 0.f : acc / sum);
-      if (ch == 0 && P.lse != nullptr) P.lse[out] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+      static_cast<T*>(P.o)[out * D + ch] = (T)(sum == 0.f ? 0.f : acc / sum);
+      if (ch == 0 && P.lse != nullptr) P.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
     }
   }
 }
@@ -637,9 +638,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Atte
     float y = 0.f;
 #pragma unroll
     for (int n = 0; n < kParts; ++n) y += reinterpret_cast<const float*>(sums[n])[threadIdx.x];
-    static_cast<T*>(P.o)[out * D + threadIdx.x] = (T)(mx == -INFINITY ? 0.f : y / sum);
+    static_cast<T*>(P.o)[out * D + threadIdx.x] = (T)(sum == 0.f ? 0.f : y / sum);
   }
-  if (threadIdx.x == 0 && P.lse != nullptr) P.lse[out] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  if (threadIdx.x == 0 && P.lse != nullptr) P.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 template <typename T, int D>

@@ -404,3 +404,22 @@ def test_prompt_then_tokens(dtype):
         more = u * mag.amax(-1)
         assert_within(lse[i], lw, lb + more, "LSE")
         assert_within(o[i], ow, ob * (1 + 2 * more[..., None] / u) + u * 3 * ob / u, "O")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("length,page_rows", [(1, 16), (9, 16), (700, 64)])
+def test_rows_that_see_only_nan(dtype, length, page_rows):
+    """A query whose visible keys are all NaN gets NaN, not the zeros of an empty row; with
+    700 keys they are shared by several CTAs.  The other sequence is as it was."""
+    rng = np.random.default_rng(length)
+    kv, cache, _, table = _filled(rng, [length, length], page_rows, 1, 64, dtype, heads_q=2)
+    q = _dev(rng.normal(size=(2, 2, 1, 64)), dtype)
+    tab, n = _i32(table), _i32([length, length])
+    o0, lse0 = ra.ra_kv4_attend(kv, cache, q, tab, n)
+    bad = torch.full((2, 1, length, 64), float("nan"), dtype=DT[dtype], device="cuda")
+    good = _dev(rng.normal(size=(2, 1, length, 64)), dtype)
+    ra.ra_kv4_write(kv, cache, bad, good, tab, _i32([0, 0]), _i32([length, 0]))
+    o, lse = ra.ra_kv4_attend(kv, cache, q, tab, n)
+    ra.ra_kv4_sync_status(kv)
+    assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.equal(o[1], o0[1]) and torch.equal(lse[1], lse0[1])
