@@ -448,6 +448,8 @@ void win_tile_counts(ra_plan_s* pl) {
     }
 }
 
+constexpr int32_t kMostTiles = 1 << 19;  // streamed tiles of a backward item: about half a second
+
 // Backward work lists of a windowed plan (win_internal.h), walked by position or shard by
 // shard as the forward's.
 void build_win_bwd(ra_plan_s* pl, const ra::WinView& own, const ra::WinView& str) {
@@ -533,13 +535,26 @@ void build_win_bwd(ra_plan_s* pl, const ra::WinView& own, const ra::WinView& str
       put_ranges(&it, now);
       tiles.push_back(it);
     }
+  // Pieces no smaller than a ten-thousandth of the whole pass: with many tiles of sinks they
+  // balance without being cut finely, and their sums would take more memory than the tensors.
+  // And none beyond a quarter second, the longest that a record is waited for being one.
+  int64_t total = 0;
+  for (const ra::WinBwdItem& it : tiles) total += it.n_tiles;
+  for (ra::WinBwdItem& it : sink_tiles) {
+    queries(it.shard, it.pos0, last_pos);
+    it.n_tiles = tiles_now() * G;
+    total += it.n_tiles;
+  }
+  total *= pb.batch * pb.heads_kv;
+  normal = std::max(normal, (int32_t)std::min<int64_t>(total / 10000, kMostTiles / 2));
+  const int32_t whole = std::max(normal, std::min(2 * normal, kMostTiles));  // tiles of a sink tile left as it is
   int64_t parts = 0;  // floats per key/value head
   std::vector<ra::WinBwdSplit> splits;
   for (ra::WinBwdItem it : sink_tiles) {
     const int32_t reach = (int32_t)std::min<int64_t>((int64_t)last_of(it) + pl->window - 1, last_pos);
     queries(it.shard, it.pos0, last_pos);
     it.n_tiles = tiles_now() * G;
-    if (it.n_tiles <= 2 * normal || reach == last_pos) {
+    if (it.n_tiles <= whole || reach == last_pos) {
       put_ranges(&it, now);
       tiles.push_back(it);
       continue;
@@ -923,7 +938,12 @@ ra_status ra::mark_use(std::vector<StreamMark>* marks, cudaStream_t st) {
     cudaEvent_t ev = nullptr;
     const cudaError_t e = cudaEventCreateWithFlags(&ev, cudaEventDisableTiming);
     if (e != cudaSuccess) return fail(RA_ERR_CUDA, "use event: %s", cudaGetErrorString(e));
-    marks->push_back({st, ev});
+    try {
+      marks->push_back({st, ev});
+    } catch (const std::exception&) {
+      cudaEventDestroy(ev);
+      return fail(RA_ERR_UNSUPPORTED, "out of host memory");
+    }
     slot = &marks->back();
   }
   const cudaError_t e = cudaEventRecord(slot->done, st);

@@ -113,6 +113,17 @@ def test_a_window_reduces_the_tiles():
     assert (part[0] + part[1]).max() <= 32 * 34 < (whole[0] + whole[1]).min()
 
 
+@pytest.mark.parametrize("seq,sinks", [(131072, 65536), (1 << 20, 1 << 19)])
+def test_many_sinks_are_planned_with_bounded_scratch(seq, sinks):
+    """Half the sequence sinks, the window one token: the pieces that the sinks' far queries are
+    cut into stay as many as balance needs (10000, and the heads' last ones of every tile of
+    sinks), each with the sums of 128 rows of dK and dV at most."""
+    plan = _plan(1, sinks, seq=seq, n_shards=8, heads_q=32, heads_kv=8, layout="contiguous")
+    tiles = 8 * sinks // 128
+    scalars = 8 * 32 * seq
+    assert ra.ra_bwd_scratch_size(plan) <= scalars + (10000 + tiles * (1 + 4)) * 2 * 128 * 128 * 4
+
+
 def test_plan_without_a_device_refuses_to_compute():
     if torch.cuda.is_available():
         pytest.skip("a device is present")
