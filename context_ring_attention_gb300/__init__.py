@@ -607,7 +607,7 @@ class Kv4:
         self._h = handle
         self.problem = problem
         self._bytes = None    # of the cache
-        self._scratch = {}    # bytes of attention scratch by (batch, rows, table width)
+        self._scratch = (None, 0)  # (batch, rows, table width) of the last attention call, its bytes of scratch
 
     @property
     def handle(self):
@@ -671,7 +671,7 @@ def _kv4_tables(kv, cache, batch, page_table, **per_sequence):
 def ra_kv4_write(kv, cache, k, v, page_table, first, count=None, stream=None):
     """Quantise rows k, v [B, Hkv, T, d] into the cache at positions first[b] + t, t < count[b]."""
     pb = kv.problem
-    B, T = k.shape[0], k.shape[2] if k.dim() == 4 else 0
+    B, T = (k.shape[0], k.shape[2]) if k.dim() == 4 else (0, 0)
     _kv4_tables(kv, cache, B, page_table, first=first, count=count)
     shape = (B, pb["heads_kv"], T, pb["head_dim"])
     _need_like("k", k, shape, _kv4_dtype(kv), cache.device)
@@ -707,11 +707,11 @@ def ra_kv4_read(kv, cache, page_table, first, rows, count=None, k=None, v=None, 
 def ra_kv4_attend_scratch_size(kv, batch, rows, table_width):
     """Bytes of the float32 scratch buffer ra_kv4_attend needs for these sizes (0: none)."""
     key = (int(batch), int(rows), int(table_width))
-    if key not in kv._scratch:
+    if kv._scratch[0] != key:
         n = ctypes.c_int64()
         _check(load_library().ra_kv4_attend_scratch_size(kv.handle, *key, ctypes.byref(n)))
-        kv._scratch[key] = n.value
-    return kv._scratch[key]
+        kv._scratch = (key, n.value)
+    return kv._scratch[1]
 
 
 def ra_kv4_attend(kv, cache, q, page_table, length, o=None, lse=None, scratch=None, stream=None):

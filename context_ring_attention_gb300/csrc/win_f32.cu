@@ -10,7 +10,8 @@
 // against the 4, so that a value read from shared memory enters 4 products, and then holds
 // d/32 output columns of the 4.  At the end the groups' sums are joined in order.
 // What bounds these sizes is the latency of the chunks in turn, hence the groups: the
-// chunk loop of a key tile that holds a sink spans the sequence.
+// chunk loop of a key tile that holds a sink spans the sequence.  Measured (96 tokens, 2
+// heads, d = 32): forward 6.4 us, gradients 24 us in three launches.
 // Ring steps and partials, which fold one shard's block at a time, keep a warp per row.
 #include <cuda_runtime.h>
 

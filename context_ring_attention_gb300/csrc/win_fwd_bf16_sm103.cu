@@ -19,6 +19,14 @@
 // ... of a list sorted by cost and key/value head: no counter, and launches of one
 // plan need no reset between them.
 //
+// Measured (one query tile pair meets 9 or 10 key tiles): 32768 tokens in 8 zigzag shards,
+// 32 query and 8 key/value heads x 2, window 4096 and 4 sinks, 1.33 ms, 0.81 of the tensor
+// cores' measured rate on the visible pairs; 131072 tokens in 8 contiguous shards, window
+// 1024, 1.89 ms (0.64: the tiles at a window's two edges are half empty); 900 tokens of 4
+// heads 12.7 us.  What bounds it: each softmax thread has a row of 128 scores to bring from
+// tensor memory and back per product pair, and the two query tiles' softmax and products
+// overlap only so far (tensor cores 59% busy at 32768 tokens and a window of 1024).
+//
 // Roles (one persistent CTA per SM, 12 warps): warp 0 TMA producer, warp 1 tcgen05
 // issuer (both converged, one elected lane issues), warp 2 the work items' records, warps
 // 4-7 softmax of query tile 0, warps 8-11 of query tile 1 (one thread per row).
@@ -47,7 +55,7 @@ constexpr uint32_t kRegsSoftmax = 192;
 static_assert(128 * kRegsOther + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split");
 constexpr uint32_t kTileBytes = 128 * 128 * 2;  // one 128 x 128 bf16 tile
 constexpr uint32_t kHalfBytes = 128 * 64 * 2;   // 128 rows x one 128-byte swizzle column
-constexpr int kStages = 3;                      // K/V ring: 4 and 5 were no faster (2061, 2106 against 2043 us)
+constexpr int kStages = 3;                      // K/V ring: 4 and 5 were no faster (131072 tokens: 2061, 2106 against 2043 us)
 constexpr int kItemSlots = 4;                   // work items under way from the record warp to the others
 constexpr int kSlotRanges = 12;                 // ranges of an item kept with it (more are read from memory)
 constexpr uint32_t kStageRow = 144;             // 128 bytes of an output row, and 16 so that the lanes'
