@@ -51,6 +51,19 @@ EXPORTED = ("ra_plan", "ra_plan_window", "ra_plan_destroy", "ra_plan_tile_counts
             "ra_kv4_plan", "ra_kv4_destroy", "ra_kv4_cache_size", "ra_kv4_write", "ra_kv4_read", "ra_kv4_attend",
             "ra_kv4_attend_scratch_size", "ra_kv4_sync_status")
 
+_TORCH = None
+
+
+def _torch():
+    """The torch module, imported at the first call that needs it (the helpers below run several
+    times a call, where an import statement costs more than the check it is for)."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
 
@@ -173,11 +186,10 @@ def _alloc_on(stream):
 
 def _on_current_device(name, t):
     """The kernels run on the current CUDA device: every buffer must live there."""
-    import torch
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    cur = torch.cuda.current_device()
-    if t.device.index != cur:
+    cur = (_TORCH or _torch())._C._cuda_getDevice()  # (a CUDA tensor exists: the runtime is up)
+    if t.get_device() != cur:
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{cur} "
                          f"(make its device current, e.g. with torch.cuda.device)")
 
@@ -188,6 +200,7 @@ class Plan:
     def __init__(self, handle, problem):
         self._h = handle
         self.problem = problem
+        self._bwd_scratch = None  # bytes of ra_bwd's scratch
 
     @property
     def handle(self):
@@ -254,23 +267,23 @@ def ra_plan_tile_counts(plan):
 
 
 def _check_qkv(plan, **tensors):
-    """Shape/dtype/contiguity of q ([B, Hq, S, d]) and K/V-like ([B, Hkv, S, d]) arguments."""
-    import torch
+    """Shape/dtype/contiguity of q ([B, Hq, S, d]) and K/V-like ([B, Hkv, S, d]) arguments, all
+    on the current device."""
+    torch = _TORCH or _torch()
     pb = plan.problem
     B, S, d = pb["batch"], pb["seq"], pb["head_dim"]
     dt = torch.bfloat16 if pb["dtype"] == 1 else torch.float32
     for name, t in tensors.items():
-        heads = pb["heads_q"] if name == "q" else pb["heads_kv"]
-        if tuple(t.shape) != (B, heads, S, d) or t.dtype != dt or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"{name} must be a contiguous CUDA {dt} tensor of shape {(B, heads, S, d)}")
+        shape = (B, pb["heads_q"] if name == "q" else pb["heads_kv"], S, d)
+        if t.shape != shape or t.dtype != dt or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{name} must be a contiguous CUDA {dt} tensor of shape {shape}")
         _on_current_device(name, t)
 
 
 def _need_like(name, t, shape, dtype, device):
     """``t`` must be a contiguous tensor of exactly this shape and dtype on ``device``, a device
     that was checked already."""
-    import torch
-    if (not isinstance(t, torch.Tensor) or t.shape != tuple(shape) or t.dtype != dtype or t.device != device
+    if (not isinstance(t, (_TORCH or _torch()).Tensor) or t.shape != tuple(shape) or t.dtype != dtype or t.device != device
             or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
@@ -292,11 +305,10 @@ def _same_device(device, **tensors):
 def ra_fwd(plan, q, k, v, o=None, lse=None, partials=False, o_parts=None, lse_parts=None,
            stream=None):
     """Ring-attention forward.  Fused: returns (O, LSE).  partials=True: (O_parts, LSE_parts)."""
-    import torch
+    torch = _TORCH or _torch()
     pb = plan.problem
     B, Hq, S, d, N = pb["batch"], pb["heads_q"], pb["seq"], pb["head_dim"], pb["n_shards"]
     _check_qkv(plan, q=q, k=k, v=v)
-    _same_device(q.device, k=k, v=v)
     lib = load_library()
     if partials:
         if o_parts is None:
@@ -310,10 +322,12 @@ def ra_fwd(plan, q, k, v, o=None, lse=None, partials=False, o_parts=None, lse_pa
         return o_parts, lse_parts
     if o is None:
         o = torch.empty_like(q)
+    else:
+        _need_like("o", o, q.shape, q.dtype, q.device)
     if lse is None:
         lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
-    _need("o", o, q.shape, q.dtype, q.device)
-    _need("lse", lse, (B, Hq, S), torch.float32, q.device)
+    else:
+        _need_like("lse", lse, (B, Hq, S), torch.float32, q.device)
     _check(lib.ra_fwd(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), None, None,
                       _stream(stream)))
     return o, lse
@@ -505,7 +519,7 @@ def ra_bwd(plan, q, k, v, o, lse, dout, dq=None, dk=None, dv=None, scratch=None,
     ``o`` and ``lse`` are the forward's outputs for the same q, k, v; ``scratch``
     (``ra_bwd_scratch_size`` bytes, float32) is allocated here unless passed in.
     """
-    import torch
+    torch = _TORCH or _torch()
     pb = plan.problem
     B, Hq, S = pb["batch"], pb["heads_q"], pb["seq"]
     _check_qkv(plan, q=q, k=k, v=v)
@@ -513,10 +527,16 @@ def ra_bwd(plan, q, k, v, o, lse, dout, dq=None, dk=None, dv=None, scratch=None,
     _check_qkv(plan, q=dout)
     if dq is None:
         dq = torch.empty_like(q)
+    else:
+        _need_like("dq", dq, q.shape, q.dtype, q.device)
     if dk is None:
         dk = torch.empty_like(k)
+    else:
+        _need_like("dk", dk, k.shape, k.dtype, k.device)
     if dv is None:
         dv = torch.empty_like(v)
+    else:
+        _need_like("dv", dv, v.shape, v.dtype, v.device)
     if scratch is None:
         with _alloc_on(stream):
             scratch = torch.empty(ra_bwd_scratch_size(plan) // 4, dtype=torch.float32, device=q.device)
@@ -524,11 +544,7 @@ def ra_bwd(plan, q, k, v, o, lse, dout, dq=None, dk=None, dv=None, scratch=None,
           or not scratch.is_contiguous() or scratch.device != q.device):
         raise ValueError("scratch must be a contiguous float32 tensor of at least ra_bwd_scratch_size(plan) "
                          "bytes on the device of q")
-    _same_device(q.device, k=k, v=v, o=o, dout=dout)
-    _need("lse", lse, (B, Hq, S), torch.float32, q.device)
-    _need("dq", dq, q.shape, q.dtype, q.device)
-    _need("dk", dk, k.shape, k.dtype, q.device)
-    _need("dv", dv, v.shape, v.dtype, q.device)
+    _need_like("lse", lse, (B, Hq, S), torch.float32, q.device)
     _check(load_library().ra_bwd(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout),
                                  _ptr(dq), _ptr(dk), _ptr(dv), _ptr(scratch), _stream(stream)))
     return dq, dk, dv
@@ -536,9 +552,11 @@ def ra_bwd(plan, q, k, v, o, lse, dout, dq=None, dk=None, dv=None, scratch=None,
 
 def ra_bwd_scratch_size(plan):
     """Bytes of the float32 scratch buffer ra_bwd needs for this plan."""
-    n = ctypes.c_int64()
-    _check(load_library().ra_bwd_scratch_size(plan.handle, ctypes.byref(n)))
-    return n.value
+    if plan._bwd_scratch is None:
+        n = ctypes.c_int64()
+        _check(load_library().ra_bwd_scratch_size(plan.handle, ctypes.byref(n)))
+        plan._bwd_scratch = n.value
+    return plan._bwd_scratch
 
 
 def ra_allgather_kv(plan, k, v, k_all=None, v_all=None, stream=None):
@@ -652,13 +670,13 @@ def ra_kv4_cache_size(kv):
 
 
 def _kv4_dtype(kv):
-    import torch
+    torch = _TORCH or _torch()
     return torch.bfloat16 if kv.problem["dtype"] == 1 else torch.float32
 
 
 def _kv4_tables(kv, cache, batch, page_table, **per_sequence):
     """The cache, the page table and the [batch] int32 tables of a call, all on one device."""
-    import torch
+    torch = _TORCH or _torch()
     _need("cache", cache, (ra_kv4_cache_size(kv),), torch.uint8, cache.device)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != batch:
         raise ValueError(f"page_table must be an int32 tensor of shape ({batch}, pages of a sequence)")
@@ -686,7 +704,7 @@ def ra_kv4_read(kv, cache, page_table, first, rows, count=None, k=None, v=None, 
     Rows from count[b] on stay as they were in k and v that are passed in (both or
     neither); they are zeros where k and v are allocated here.
     """
-    import torch
+    torch = _TORCH or _torch()
     pb = kv.problem
     B, T = page_table.shape[0], int(rows)
     _kv4_tables(kv, cache, B, page_table, first=first, count=count)
@@ -697,8 +715,9 @@ def ra_kv4_read(kv, cache, page_table, first, rows, count=None, k=None, v=None, 
     if own:
         with _alloc_on(stream):
             k, v = (torch.empty(shape, dtype=_kv4_dtype(kv), device=cache.device) for _ in range(2))
-    _need_like("k", k, shape, _kv4_dtype(kv), cache.device)
-    _need_like("v", v, shape, _kv4_dtype(kv), cache.device)
+    else:
+        _need_like("k", k, shape, _kv4_dtype(kv), cache.device)
+        _need_like("v", v, shape, _kv4_dtype(kv), cache.device)
     _check(load_library().ra_kv4_read(kv.handle, _ptr(cache), B, T, _ptr(page_table), page_table.shape[1],
                                       _ptr(first), _ptr(count), int(own), _ptr(k), _ptr(v), _stream(stream)))
     return k, v
@@ -721,7 +740,7 @@ def ra_kv4_attend(kv, cache, q, page_table, length, o=None, lse=None, scratch=No
     ``scratch`` (``ra_kv4_attend_scratch_size`` bytes, float32) is allocated here unless
     passed in.
     """
-    import torch
+    torch = _TORCH or _torch()
     pb = kv.problem
     if q.dim() != 4:
         raise ValueError("q must have the shape [B, Hq, T, d]")
