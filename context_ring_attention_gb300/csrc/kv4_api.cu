@@ -105,18 +105,21 @@ ra_status launched(ra_kv4_s* kv, cudaError_t e, const char* what, cudaStream_t s
 
 // Query tiles of a key/value head, and the CTAs among which a tile's keys are split.
 struct Split {
-  int64_t tiles, splits;
+  int64_t tiles, slots;
+  bool in_row;  // the sequences' blocks are shared in a row
 };
 
-// Shares of the keys: as many CTAs as the GPU holds (3 an SM) for one sequence, whose shares
-// are equal (64k tokens: 27 us; with twice as many shares 35), and twice that for several,
-// whose lengths differ, so that the short ones' CTAs make room for more.  With 3, 6 and 9 CTAs
-// an SM: 32 sequences under a window of 8192 tokens 96, 86 and 84 us; 8 of up to 64k 117, 117
-// and 112; 16 of up to 8k 40, 41 and 45; 4 of 64k in fp32 117, 110 and 116.  Rounded down,
-// since one CTA too many is a wave of its own (4 new tokens of 8k: 16 against 19 us; 64
-// sequences of up to 2k: 36 against 42).  No CTA gets fewer than 16 blocks of 16 tokens, four
-// a warp: below that the join costs more than the share saves (8k tokens, one block a warp at
-// a time: 10.5 us; with 8 blocks 12.1, with 32 11.5).
+// Shares of the keys: as many CTAs as the GPU holds at once, 3 an SM (fp32: 2), each with the
+// same number of blocks -- of one sequence, or of all sequences laid in a row, where a CTA's
+// share may be the end of one and the beginning of the next.  Shares per sequence, of equal
+// number whatever its length, took 86 us for 32 sequences under a window of 8192 tokens (in a
+// row 79), 117 for 8 of up to 64k (101) and 41 for 16 of up to 8k (37).  Beyond that many
+// sequences each has one CTA and the GPU deals them out, unless they are up to twice as many
+// and long: 64 sequences of up to 16k tokens 206 us one a sequence, 163 in a row, 100 of up to
+// 4k 89 and 87, but 64 of up to 2k 36 and 42; 200 of up to 4k 146 and 155 us.
+// No CTA gets fewer than 16 blocks of 16 tokens, four a warp: below that the join costs more
+// than the share saves (8k tokens, one block a warp at a time: 10.5 us; with 8 blocks 12.1,
+// with 32 11.5).
 ra_status split_of(const ra_kv4_s* kv, int64_t batch, int64_t rows, int64_t table_width, Split* out) {
   const ra_kv4_problem& pb = kv->prob;
   if (batch < 1 || rows < 1 || table_width < 1)
@@ -130,13 +133,19 @@ ra_status split_of(const ra_kv4_s* kv, int64_t batch, int64_t rows, int64_t tabl
   int64_t keys = table_width * pb.page_rows;
   if (pb.window > 0 && pb.window < kMaxPositions && pb.sinks < kMaxPositions)
     keys = std::min(keys, pb.window + rows + pb.sinks + 32);
-  const int64_t units = batch * pb.heads_kv * out->tiles;
   const int64_t sms = kv->sm_count > 0 ? kv->sm_count : 148;
-  const int64_t want = (batch == 1 ? 3 : 6) * sms;
-  const int64_t most = std::max<int64_t>(1, keys / (16 * 16));
-  out->splits = std::max<int64_t>(1, std::min({want / units, most, int64_t(ra::kMaxSplits)}));
+  const int64_t per_sm = pb.dtype == RA_DTYPE_BF16 ? 3 : 2;
+  const int64_t most = batch * std::max<int64_t>(1, keys / (16 * 16));
+  const int64_t slots = std::min({per_sm * sms / (pb.heads_kv * out->tiles), most, int64_t(ra::kMaxSlots)});
+  const bool countable = batch <= INT32_MAX / (keys / ra::kKvBlockRows + 3);  // blocks in all, in 31 bits
+  const bool few = batch <= slots || (batch <= 2 * slots && keys >= 4096);
+  out->in_row = countable && batch > 1 && slots > 1 && few && most > batch;
+  out->slots = batch == 1 || out->in_row ? std::max<int64_t>(1, slots) : batch;
   return RA_OK;
 }
+
+// Whether a sequence may be spread over several CTAs, whose parts are then joined.
+bool joined(const Split& sp, int64_t batch) { return sp.in_row || sp.slots > batch; }
 
 }  // namespace
 
@@ -233,8 +242,10 @@ ra_status ra_kv4_attend_scratch_size(ra_kv4_t kv, int64_t batch, int64_t rows, i
   Split sp;
   const ra_status s = split_of(kv, batch, rows, table_width, &sp);
   if (s != RA_OK) return s;
-  const int64_t parts = sp.splits == 1 ? 0 : batch * kv->prob.heads_kv * sp.tiles * sp.splits;
-  *bytes = parts * 8 * (kv->prob.head_dim + 2) * (int64_t)sizeof(float);
+  const int64_t parts = !joined(sp, batch) ? 0 : kv->prob.heads_kv * sp.tiles * sp.slots * 2;
+  const int64_t part = 8 * (kv->prob.head_dim + 2) * (int64_t)sizeof(float);
+  // (the sequences' first and last slots behind the parts, in as many bytes as whole parts)
+  *bytes = parts == 0 ? 0 : (parts + (batch * (int64_t)sizeof(int2) + part - 1) / part) * part;
   return ok();
 }
 
@@ -248,10 +259,10 @@ ra_status ra_kv4_attend(ra_kv4_t kv, const void* cache, int64_t batch, int64_t r
   Split sp;
   ra_status s = split_of(kv, batch, rows, table_width, &sp);
   if (s != RA_OK) return s;
-  if (sp.splits > 1 && scratch == nullptr)
+  if (joined(sp, batch) && scratch == nullptr)
     return fail(RA_ERR_INVALID_ARG, "null scratch (ra_kv4_attend_scratch_size bytes are needed)");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const void* t16[] = {cache, q, o, lse, sp.splits > 1 ? scratch : nullptr};
+  const void* t16[] = {cache, q, o, lse, joined(sp, batch) ? scratch : nullptr};
   const void* t4[] = {page_table, length};
   s = check_call(kv, batch, rows, table_width, t16, 5, t4, 2, st);
   if (s != RA_OK) return s;
@@ -261,7 +272,8 @@ ra_status ra_kv4_attend(ra_kv4_t kv, const void* cache, int64_t batch, int64_t r
   prm.group = pb.heads_q / pb.heads_kv;
   prm.rows = (int32_t)rows;
   prm.tiles = (int32_t)sp.tiles;
-  prm.splits = (int32_t)sp.splits;
+  prm.slots = (int32_t)sp.slots;
+  prm.in_row = sp.in_row;
   prm.window = (int32_t)std::min(pb.window, kMaxPositions);
   prm.sinks = (int32_t)std::min(pb.sinks, kMaxPositions);
   prm.scale_log2 = pb.scale * 1.4426950408889634f;
@@ -269,9 +281,11 @@ ra_status ra_kv4_attend(ra_kv4_t kv, const void* cache, int64_t batch, int64_t r
   prm.q = q;
   prm.o = o;
   prm.lse = lse;
-  if (sp.splits > 1) {
+  if (joined(sp, batch)) {
+    const int64_t parts = pb.heads_kv * sp.tiles * sp.slots * 2;
     prm.part_o = scratch;
-    prm.part_ml = reinterpret_cast<float2*>(scratch + batch * pb.heads_kv * sp.tiles * sp.splits * 8 * pb.head_dim);
+    prm.part_ml = reinterpret_cast<float2*>(scratch + parts * 8 * pb.head_dim);
+    prm.shares = reinterpret_cast<int2*>(prm.part_ml + parts * 8);
   }
   return launched(kv, ra::launch_kv4_attend(pb.dtype, pb.head_dim, prm, st), "cache attention launch", st);
 }

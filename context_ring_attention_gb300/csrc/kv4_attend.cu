@@ -31,16 +31,16 @@
 // a quarter; m, l and O are joined across warps in shared memory, and across CTAs by a
 // second kernel in a fixed order.  A warp works on two blocks at a time: with one at a time
 // and four CTAs an SM (128 registers) its chains of dependent instructions, from the scores
-// to the weights, were what it waited for; two blocks (166 registers, three CTAs an SM) took
-// one sequence of 1M tokens from 276 to 257 us and 16 new tokens of 64k from 180 to 136.
-// Two blocks in 128 registers: 276 us; two pairs a warp in shared memory for three: 260.
+// to the weights, were what it waited for; two blocks (three CTAs an SM) took one sequence of
+// 1M tokens from 276 to 257 us and 16 new tokens of 64k from 180 to 136.  Two blocks in 128
+// registers: 276 us; two pairs a warp in shared memory for three: 260.
 //
 // Measured (32 query and 8 key/value heads, d = 128, bf16, one new token): 1M tokens 257 us,
-// 1.34 GB of cache at 5.2 TB/s (0.77 of a plain copy's rate); 64k tokens 27 us; 32 sequences
-// of 2k to 32k under a window of 8192 tokens 86 us.  What bounds it is the issue of
-// instructions, some 350 a block and warp, about half of them for turning codes and weights
-// into operands.  fp32 takes three terms per query and weight and three times the products:
-// 4 sequences of 64k tokens 110 us.
+// 1.34 GB of cache at 5.2 TB/s (0.77 of a plain copy's rate); 64k tokens 28 us; 32 sequences
+// of 2k to 32k under a window of 8192 tokens 79 us.  What bounds it is the issue of
+// instructions (59% of the slots with 11 warps an SM), some 350 a block and warp, about half
+// of them for turning codes and weights into operands.  fp32 takes three terms per query and
+// weight and three times the products: 4 sequences of 64k tokens 95 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -55,6 +55,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kTile = 8;  // query rows of a tile
+constexpr int kMinBlocks = 16;  // of a share: four a warp
+constexpr int kSnap = 8;
 constexpr int kPairs = 3;  // pairs of cache blocks a warp holds or has under way
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleSlack = 8.0f;  // log2 units: keep a stale maximum while p <= 2^8
@@ -158,26 +160,121 @@ __device__ __forceinline__ Blocks blocks_of(const Kv4AttendParams& P, int32_t le
   return b;
 }
 
-template <typename T, int D>
+// Tokens of sequence b that the cache holds; a length out of range counts as none.
+__device__ __forceinline__ int32_t length_of(const Kv4AttendParams& P, int b, bool& bad) {
+  const int32_t len = __ldg(P.length + b);
+  bad = len < 0 || len > P.t.width * P.t.page_rows;
+  return bad ? 0 : len;
+}
+
+// The share of a slot: n blocks of the sequences one after the other, from block `off` of
+// sequence b on.  (A sequence without blocks stands in the row with one, so that its rows are
+// written.)
+struct Share {
+  int32_t b, off, n;
+};
+// N blocks in all make up to `slots` equal shares of kMinBlocks or more; a border that would
+// fall within kSnap blocks of a sequence's end is put there.  Every CTA finds its own from the
+// lengths.
+template <bool kInRow>
+__device__ __forceinline__ Share share_of(const Kv4AttendParams& P, int slot) {
+  bool bad;
+  auto blocks = [&](int b) { return b < P.t.batch ? max(1, blocks_of(P, length_of(P, b, bad)).n) : 0; };
+  if (!kInRow && P.slots == P.t.batch) return {slot, 0, blocks(slot)};
+  auto border = [&](int32_t total, int i) {
+    const int32_t shares = kInRow ? max(1, min(P.slots, total / kMinBlocks)) : P.slots;
+    return i >= shares ? total : (int32_t)((int64_t)total * i / shares);
+  };
+  if (!kInRow) {  // one sequence; every slot has a part, if of no blocks
+    const int32_t total = blocks(0), from = border(total, slot);
+    return {0, from, border(total, slot + 1) - from};
+  }
+  __shared__ int32_t sums[kWarps], ends[kWarps];
+  __shared__ int32_t found[2][3];  // of either border: sequence, block of it, place
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t mine = blocks(threadIdx.x);
+  int32_t total = mine;  // (the host keeps the sum within 31 bits)
+  for (int b = threadIdx.x + kWarps * 32; b < P.t.batch; b += kWarps * 32) total += blocks(b);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0) sums[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += sums[w];
+  const int32_t at[2] = {border(total, slot), border(total, slot + 1)};
+  if (at[0] == at[1]) return {0, 0, 0};
+  if (threadIdx.x == 0) found[1][2] = total;  // (where at[1] is the end of all)
+  int32_t base = 0;
+  for (int b0 = 0; b0 < P.t.batch && base <= at[1]; b0 += kWarps * 32) {  // (uniform)
+    const int b = b0 + threadIdx.x;
+    const int32_t n = b0 == 0 ? mine : blocks(b);
+    int32_t end = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t x = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end += x;
+    }
+    __syncthreads();  // (the last chunk's ends are read no more; found[1] has its default)
+    if (lane == 31) ends[warp] = end;
+    __syncthreads();
+    end += base;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) end += ends[w];
+      base += ends[w];
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int32_t off = at[x] - (end - n);
+      if (off < 0 || off >= n) continue;
+      const bool down = off <= kSnap, up = !down && n - off <= kSnap;
+      found[x][0] = up ? b + 1 : b;
+      found[x][1] = down || up ? 0 : off;
+      found[x][2] = down ? end - n : up ? end : at[x];
+    }
+  }
+  __syncthreads();
+  return {found[0][0], found[0][1], found[1][2] - found[0][2]};
+}
+
+// kInRow: the sequences' blocks are shared in a row, so that a CTA may have parts of several;
+// otherwise it has (a share of) one.  (As one kernel a single sequence of 1M tokens took 4%
+// longer, and one of 8k 12 us for 10.)
+template <typename T, int D, bool kInRow>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_attend_kernel(const Kv4AttendParams P) {
   using F = Kv4Block<D>;
   constexpr int G = F::kGroups;
   constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
-  const int split = blockIdx.x, tile = blockIdx.y % P.tiles, h = blockIdx.y / P.tiles, b = blockIdx.z;
+  // One sequence: the shares of a head next to each other (1M tokens 256 us, the heads of a
+  // share next to each other 262); several: the heads, whose blocks lie in the same pages (64
+  // sequences of up to 2k 37 against 39.5).
+  const bool one = !kInRow && P.t.batch == 1;
+  const int cta = one ? blockIdx.x : blockIdx.y, ht = one ? blockIdx.y : blockIdx.x;
+  const int tile = ht % P.tiles, h = ht / P.tiles;
   const int n_rows = P.group * P.rows;  // query rows of the head: row = group head * rows + token
   const int row0 = tile * kTile;
 
   cudaTriggerProgrammaticLaunchCompletion();
-  int32_t len = __ldg(P.length + b);
-  if (len < 0 || len > P.t.width * P.t.page_rows) {
-    if (threadIdx.x == 0) atomicOr(P.t.status, kKv4StatusRange);
-    len = 0;
+  if (!kInRow && row0 + r < n_rows) {  // the queries are on their way while the length is asked for
+    const T* qrow = static_cast<const T*>(P.q) +
+                    (((int64_t)(one ? 0 : cta) * P.heads_q + (int64_t)h * P.group) * P.rows + row0 + r) * D;
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(qrow + c * (D / 4)));
   }
+  const Share share = share_of<kInRow>(P, cta);
+  int32_t off = share.off, rest = share.n;
+  for (int b = share.b; !kInRow || rest > 0; ++b) {
+  bool bad_length;
+  const int32_t len = length_of(P, b, bad_length);
+  if (bad_length && threadIdx.x == 0) atomicOr(P.t.status, kKv4StatusRange);
   const Blocks blk = blocks_of(P, len);
-  const int32_t x_lo = (int32_t)((int64_t)blk.n * split / P.splits);
-  const int32_t x_hi = (int32_t)((int64_t)blk.n * (split + 1) / P.splits);
+  const int32_t x_lo = min(off, blk.n), x_hi = min(off + rest, blk.n);
+  // the sequence begins and ends in this share
+  const bool begins = kInRow ? off == 0 : P.slots == P.t.batch || cta == 0;
+  const bool ends = kInRow ? off + rest >= blk.n : P.slots == P.t.batch || cta == P.slots - 1;
+  rest -= max(1, blk.n) - off;
+  off = 0;
 
   // Query fragments: lane (r, c) holds row r's channels 32g + 8c .. + 7 of every group, in
   // the pairs (0,4), (1,5), (2,6), (3,7) that a word of codes yields, times 2^E; the pairs
@@ -548,7 +645,6 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
                       fmaf(o[g][1][e], two_to(73), pm[g][e] * two_to(-60)),
                       fmaf(o[g][1][e + 2], two_to(69), pm[g][e] * two_to(-60)));
   __syncthreads();
-  const int64_t unit = ((int64_t)b * P.t.heads_kv + h) * P.tiles + tile;
   for (int at = threadIdx.x; at < kTile * D; at += kWarps * 32) {
     const int row = at / D, ch = at % D;
     float mx = sm_m[0][row];
@@ -563,8 +659,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
       sum = fmaf(f, sm_l[w][row], sum);
       acc = fmaf(f, sm_o[w][row][ch], acc);
     }
-    if (P.splits > 1) {
-      const int64_t part = unit * P.splits + split;
+    if (!(begins && ends)) {
+      const int64_t part = ((int64_t)ht * P.slots + cta) * 2 + begins;
       P.part_o[(part * kTile + row) * D + ch] = acc;
       if (ch == 0) P.part_ml[part * kTile + row] = make_float2(mx, sum);
     } else if (row0 + row < n_rows) {
@@ -573,31 +669,42 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
       if (ch == 0 && P.lse != nullptr) P.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
     }
   }
+  if (!kInRow) break;
+  if (ht == 0 && threadIdx.x == 0) {
+    if (begins) P.shares[b].x = cta;
+    if (ends) P.shares[b].y = cta;
+  }
+  __syncthreads();  // (the next sequence's fragments and blocks come into the same memory)
+  }
 }
 
-// Joins the splits' parts of a row, in a fixed order: one CTA a row.  The splits' weights
-// 2^(m_s - m) come first, then D/4 lanes read a part's row, each warp every eighth split
-// (or every sixteenth half-warp) and the warps' sums are added.  A loop over the splits by
-// one thread a channel took 15 us for 64 splits; this takes 3.
+// Joins the parts of a row, in a fixed order: one CTA a row.  The parts' weights
+// 2^(m_s - m) come first, then D/4 lanes read a part's row, each warp every eighth part
+// (or every sixteenth half-warp) and the warps' sums are added.  A loop over the parts by
+// one thread a channel took 15 us for 64 of them; this takes 3.
 constexpr int kJoinWarps = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4AttendParams P) {
   constexpr int kLanes = D / 4;                        // lanes of a part's row
   constexpr int kParts = kJoinWarps * 32 / kLanes;     // parts read at a time
-  __shared__ float weight[kMaxSplits];
+  __shared__ float weight[kMaxSlots];
   __shared__ float red[2][kJoinWarps];
   __shared__ float4 sums[kParts][kLanes];
-  cudaGridDependencySynchronize();  // (the parts are written)
-  const int64_t unit = blockIdx.x;
-  const int row = blockIdx.y;
+  cudaGridDependencySynchronize();  // (the parts and their places are written)
+  const int unit = blockIdx.x, row = blockIdx.y;  // unit = (b * heads_kv + h) * tiles + tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tile = (int)(unit % P.tiles);
-  const int64_t bh = unit / P.tiles;
+  const int tile = unit % P.tiles, bh = unit / P.tiles, b = bh / P.t.heads_kv;
   if (tile * kTile + row >= P.group * P.rows) return;
-  const float2* ml = P.part_ml + unit * P.splits * kTile + row;
+  const int2 share = P.t.batch == 1 ? make_int2(0, P.slots - 1) : P.shares[b];  // (first slot, last slot)
+  const int n = share.y - share.x + 1;
+  if (n == 1) return;  // (that CTA wrote the row)
+  // a slot has two parts: of a sequence that it has the beginning of the second
+  const int64_t part0 = ((int64_t)(unit - b * P.t.heads_kv * P.tiles) * P.slots + share.x) * 2;
+  auto part_at = [&](int s) { return part0 + (s == 0 ? 1 : 2 * s); };
+  const float2* ml = P.part_ml + row;
 
   float mx = -INFINITY;
-  for (int s = threadIdx.x; s < P.splits; s += kJoinWarps * 32) mx = fmaxf(mx, ml[s * kTile].x);
+  for (int s = threadIdx.x; s < n; s += kJoinWarps * 32) mx = fmaxf(mx, ml[part_at(s) * kTile].x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   if (lane == 0) red[0][warp] = mx;
@@ -605,8 +712,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Atte
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, red[0][w]);
   float sum = 0.f;
-  for (int s = threadIdx.x; s < P.splits; s += kJoinWarps * 32) {
-    const float2 x = ml[s * kTile];
+  for (int s = threadIdx.x; s < n; s += kJoinWarps * 32) {
+    const float2 x = ml[part_at(s) * kTile];
     const float f = x.x == -INFINITY ? 0.f : ptx::ex2_approx(x.x - mx);
     weight[s] = f;
     sum = fmaf(f, x.y, sum);
@@ -620,12 +727,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Atte
   for (int w = 0; w < kJoinWarps; ++w) sum += red[1][w];
 
   const int part = threadIdx.x / kLanes, at = threadIdx.x % kLanes;
-  const float4* po = reinterpret_cast<const float4*>(P.part_o + (unit * P.splits * kTile + row) * D) + at;
+  const float4* po = reinterpret_cast<const float4*>(P.part_o + row * D) + at;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = part; s < P.splits; s += kParts) {
+  for (int s = part; s < n; s += kParts) {
     const float f = weight[s];
-    const float4 x = po[(int64_t)s * (kTile * kLanes)];
+    const float4 x = po[part_at(s) * (kTile * kLanes)];
     acc.x = fmaf(f, x.x, acc.x);
     acc.y = fmaf(f, x.y, acc.y);
     acc.z = fmaf(f, x.z, acc.z);
@@ -633,28 +740,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Atte
   }
   sums[part][at] = acc;
   __syncthreads();
-  const int64_t out = bh * P.group * P.rows + tile * kTile + row;
+  const int64_t out = (int64_t)bh * P.group * P.rows + tile * kTile + row;
   if (threadIdx.x < D) {
     float y = 0.f;
 #pragma unroll
-    for (int n = 0; n < kParts; ++n) y += reinterpret_cast<const float*>(sums[n])[threadIdx.x];
+    for (int x = 0; x < kParts; ++x) y += reinterpret_cast<const float*>(sums[x])[threadIdx.x];
     static_cast<T*>(P.o)[out * D + threadIdx.x] = (T)(sum == 0.f ? 0.f : y / sum);
   }
   if (threadIdx.x == 0 && P.lse != nullptr) P.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kInRow>
 cudaError_t attend_as(const Kv4AttendParams& prm, cudaStream_t st) {
   constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
   constexpr int kSmem = kWarps * kPairs * 2 * Kv4Block<D>::kBytes + 32 * 16 * ((D / 32) * kTerms + 1);
   static std::atomic<int> ready[kMaxDevices];
   const char* why = "";
-  cudaError_t e = prepare_once(kv4_attend_kernel<T, D>, ready, kWarps * 32, 0, kSmem, &why);
+  cudaError_t e = prepare_once(kv4_attend_kernel<T, D, kInRow>, ready, kWarps * 32, 0, kSmem, &why);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)prm.splits, (unsigned)(prm.t.heads_kv * prm.tiles), (unsigned)prm.t.batch);
-  kv4_attend_kernel<T, D><<<grid, kWarps * 32, kSmem, st>>>(prm);
+  const unsigned heads = (unsigned)(prm.t.heads_kv * prm.tiles), slots = (unsigned)prm.slots;
+  const dim3 grid = prm.t.batch == 1 ? dim3(slots, heads) : dim3(heads, slots);
+  kv4_attend_kernel<T, D, kInRow><<<grid, kWarps * 32, kSmem, st>>>(prm);
   e = cudaGetLastError();
-  if (e != cudaSuccess || prm.splits == 1) return e;
+  if (e != cudaSuccess || (!kInRow && prm.slots == prm.t.batch)) return e;
   // The join's CTAs may be placed while the last of the others still run; they wait for
   // the whole grid's results.
   cudaLaunchConfig_t cfg = {};
@@ -673,9 +781,15 @@ cudaError_t attend_as(const Kv4AttendParams& prm, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv4_attend(int dtype, int head_dim, const Kv4AttendParams& prm, cudaStream_t stream) {
-  if (dtype == RA_DTYPE_BF16)
-    return head_dim == 128 ? attend_as<__nv_bfloat16, 128>(prm, stream) : attend_as<__nv_bfloat16, 64>(prm, stream);
-  return head_dim == 128 ? attend_as<float, 128>(prm, stream) : attend_as<float, 64>(prm, stream);
+  const bool in_row = prm.in_row != 0;
+  if (dtype == RA_DTYPE_BF16) {
+    if (head_dim == 128)
+      return in_row ? attend_as<__nv_bfloat16, 128, true>(prm, stream) : attend_as<__nv_bfloat16, 128, false>(prm, stream);
+    return in_row ? attend_as<__nv_bfloat16, 64, true>(prm, stream) : attend_as<__nv_bfloat16, 64, false>(prm, stream);
+  }
+  if (head_dim == 128)
+    return in_row ? attend_as<float, 128, true>(prm, stream) : attend_as<float, 128, false>(prm, stream);
+  return in_row ? attend_as<float, 64, true>(prm, stream) : attend_as<float, 64, false>(prm, stream);
 }
 
 }  // namespace ra

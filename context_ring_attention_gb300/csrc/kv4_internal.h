@@ -46,21 +46,24 @@ struct Kv4RowsParams {  // write, read
   int32_t zero_rest;     // read: rows that receive nothing become zeros
 };
 
-constexpr int kMaxSplits = 1024;  // CTAs that share the keys of a query tile
+constexpr int kMaxSlots = 1024;  // CTAs among which the sequences of a head and query tile are split
 
 struct Kv4AttendParams {
   Kv4Table t;
   int32_t heads_q, group, rows;  // query rows per sequence
   int32_t tiles;                 // 8-row query tiles per key/value head
-  int32_t splits;                // CTAs that share a tile's keys
+  int32_t slots;                 // CTAs of a key/value head and tile
+  int32_t in_row;                // they share the sequences' blocks in a row; else one a sequence (or several for one)
   int32_t window, sinks;         // window 0: the whole prefix
   float scale_log2;
   const int32_t* length;
   const void* q;
   void* o;
   float* lse;      // or nullptr
-  float* part_o;   // [unit, split, 8, D], unit = (b * heads_kv + h) * tiles + tile (splits > 1)
-  float2* part_ml; // [unit, split, 8]: running maximum (log2 units) and sum
+  // in_row, or several slots for one sequence:
+  float* part_o;   // [head * tiles + tile, slot, 2, 8, D]
+  float2* part_ml; // [head * tiles + tile, slot, 2, 8]: running maximum (log2 units) and sum
+  int2* shares;    // [batch]: a sequence's first and last slot (batch > 1)
 };
 
 cudaError_t launch_kv4_write(int dtype, int head_dim, const Kv4RowsParams& prm, const void* k, const void* v,

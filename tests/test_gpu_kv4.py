@@ -423,3 +423,56 @@ def test_rows_that_see_only_nan(dtype, length, page_rows):
     ra.ra_kv4_sync_status(kv)
     assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
     assert torch.equal(o[1], o0[1]) and torch.equal(lse[1], lse0[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,hk,d,window,sinks", [(150, 1, 64, 0, 0), (70, 8, 128, 0, 0), (150, 1, 128, 40, 3)])
+def test_many_ragged_sequences(dtype, n, hk, d, window, sinks):
+    """More sequences than threads of a CTA, empty ones among them, and more sequences than
+    CTAs of a head: shares that hold the end of one sequence, several whole ones and the
+    beginning of another."""
+    rng = np.random.default_rng(n + d)
+    lengths = [int(x) for x in rng.integers(0, 90, n)]
+    lengths[0], lengths[7], lengths[n // 2], lengths[-1] = 0, 600, 333, 0
+    kv, cache, ref, table = _filled(rng, lengths, 32, hk, d, dtype, heads_q=2 * hk, window=window, sinks=sinks)
+    table = np.concatenate([table, np.full((n, 132 - table.shape[1]), -1)], 1)  # room for 4224 tokens
+    assert ra.ra_kv4_attend_scratch_size(kv, n, 1, table.shape[1]) > 0 or window
+    _check_attend(kv, cache, ref, table, lengths, 2 * hk, 1, d, dtype, window, sinks, rng)
+
+
+def test_shares_follow_the_lengths_in_a_graph():
+    """A captured call shares the blocks out anew at every replay."""
+    rng = np.random.default_rng(21)
+    top = [700, 320, 900, 64]
+    kv, cache, ref, table = _filled(rng, top, 32, 2, 64, "bf16", heads_q=4)
+    q = _dev(rng.normal(size=(4, 4, 1, 64)), "bf16")
+    tab, n = _i32(table), _i32(top)
+    need = ra.ra_kv4_attend_scratch_size(kv, 4, 1, table.shape[1])
+    assert need > 0
+    o, lse, scratch = torch.empty_like(q), torch.empty((4, 4, 1), device="cuda"), torch.empty(need // 4, device="cuda")
+    call = lambda: ra.ra_kv4_attend(kv, cache, q, tab, n, o=o, lse=lse, scratch=scratch)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lengths in (top, [1, 320, 0, 64], [0, 0, 900, 0], [0, 0, 0, 0], [700, 1, 1, 1]):
+        n.copy_(_i32(lengths))
+        o.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = o.clone(), lse.clone()
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+        for b, length in enumerate(lengths):
+            alone = ra.ra_kv4_attend(kv, cache, q[b:b + 1].contiguous(), tab[b:b + 1].contiguous(), _i32([length]))
+            if length == 0:
+                assert torch.isneginf(lse[b]).all() and (o[b] == 0).all()
+                continue
+            # The same sums cut otherwise.  Each side rounds every weight (2^-8 of it) and the
+            # output once; the statistic's exponentials are off by 2^-21, its 900 additions by
+            # 2^-24 each at most.
+            top = float(np.abs(ref.rows(table[b], np.arange(length))[1]).max())
+            assert torch.allclose(o[b].float(), alone[0][0].float(), rtol=2.0 ** -7, atol=2.0 ** -7 * top)
+            assert torch.allclose(lse[b], alone[1][0], rtol=2.0 ** -22, atol=2 * (2.0 ** -21 + 900 * 2.0 ** -24))
