@@ -119,7 +119,9 @@ struct Split {
 // 4k 89 and 87, but 64 of up to 2k 36 and 42; 200 of up to 4k 146 and 155 us.
 // No CTA gets fewer than 16 blocks of 16 tokens, four a warp: below that the join costs more
 // than the share saves (8k tokens, one block a warp at a time: 10.5 us; with 8 blocks 12.1,
-// with 32 11.5).
+// with 32 11.5).  Several sequences are shared out only where one may be of 1536 tokens or
+// more: 32 of up to 512 take 11 us with a CTA each, 18 in a row; of up to 1024 15 and 21; 4 of
+// up to 1024 12.7 and 15.3, of up to 2048 19.7 and 12.5.
 ra_status split_of(const ra_kv4_s* kv, int64_t batch, int64_t rows, int64_t table_width, Split* out) {
   const ra_kv4_problem& pb = kv->prob;
   if (batch < 1 || rows < 1 || table_width < 1)
@@ -135,12 +137,15 @@ ra_status split_of(const ra_kv4_s* kv, int64_t batch, int64_t rows, int64_t tabl
     keys = std::min(keys, pb.window + rows + pb.sinks + 32);
   const int64_t sms = kv->sm_count > 0 ? kv->sm_count : 148;
   const int64_t per_sm = pb.dtype == RA_DTYPE_BF16 ? 3 : 2;
-  const int64_t most = batch * std::max<int64_t>(1, keys / (16 * 16));
-  const int64_t slots = std::min({per_sm * sms / (pb.heads_kv * out->tiles), most, int64_t(ra::kMaxSlots)});
-  const bool countable = batch <= INT32_MAX / (keys / ra::kKvBlockRows + 3);  // blocks in all, in 31 bits
-  const bool few = batch <= slots || (batch <= 2 * slots && keys >= 4096);
-  out->in_row = countable && batch > 1 && slots > 1 && few && most > batch;
-  out->slots = batch == 1 || out->in_row ? std::max<int64_t>(1, slots) : batch;
+  const int64_t slots = std::min(per_sm * sms / (pb.heads_kv * out->tiles), int64_t(ra::kMaxSlots));
+  if (batch == 1) {
+    out->in_row = false;
+    out->slots = std::max<int64_t>(1, std::min(slots, keys / (16 * 16)));
+  } else {
+    const bool countable = batch <= INT32_MAX / (keys / ra::kKvBlockRows + 3);  // blocks in all, in 31 bits
+    out->in_row = countable && slots > 1 && keys >= 1536 && (batch <= slots || (batch <= 2 * slots && keys >= 4096));
+    out->slots = out->in_row ? slots : batch;
+  }
   return RA_OK;
 }
 

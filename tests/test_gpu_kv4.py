@@ -219,6 +219,7 @@ def test_shared_pages_and_own_outputs():
     lengths = [900, 640]
     kv, cache, ref, table = _filled(rng, lengths, 32, 2, 64, "f32", heads_q=8)
     table[1, :3] = table[0, :3]
+    table = np.concatenate([table, np.full((2, 60 - table.shape[1]), -1)], 1)  # room for 1920 tokens
     need = ra.ra_kv4_attend_scratch_size(kv, 2, 1, table.shape[1])
     assert need > 0
     scratch = torch.full((need // 4 + 3,), float("nan"), device="cuda")
@@ -445,6 +446,7 @@ def test_shares_follow_the_lengths_in_a_graph():
     rng = np.random.default_rng(21)
     top = [700, 320, 900, 64]
     kv, cache, ref, table = _filled(rng, top, 32, 2, 64, "bf16", heads_q=4)
+    table = np.concatenate([table, np.full((4, 60 - table.shape[1]), -1)], 1)  # room for 1920 tokens
     q = _dev(rng.normal(size=(4, 4, 1, 64)), "bf16")
     tab, n = _i32(table), _i32(top)
     need = ra.ra_kv4_attend_scratch_size(kv, 4, 1, table.shape[1])
@@ -476,3 +478,16 @@ def test_shares_follow_the_lengths_in_a_graph():
             top = float(np.abs(ref.rows(table[b], np.arange(length))[1]).max())
             assert torch.allclose(o[b].float(), alone[0][0].float(), rtol=2.0 ** -7, atol=2.0 ** -7 * top)
             assert torch.allclose(lse[b], alone[1][0], rtol=2.0 ** -22, atol=2 * (2.0 ** -21 + 900 * 2.0 ** -24))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1500, 20), (1700, 0)])
+@pytest.mark.parametrize("t,hq,hk", [(1, 4, 1), (5, 16, 2), (9, 3, 3)])
+def test_shared_in_a_row(dtype, window, sinks, t, hq, hk):
+    """Few long sequences of different lengths, several query tiles, sinks behind which the
+    window begins within a share."""
+    rng = np.random.default_rng(window + t)
+    lengths = [2300, 0, 1801, 40, 3]
+    kv, cache, ref, table = _filled(rng, lengths, 48, hk, 128, dtype, heads_q=hq, window=window, sinks=sinks)
+    assert ra.ra_kv4_attend_scratch_size(kv, 5, t, table.shape[1]) > 0
+    _check_attend(kv, cache, ref, table, lengths, hq, t, 128, dtype, window, sinks, rng)
