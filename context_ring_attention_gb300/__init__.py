@@ -52,6 +52,7 @@ EXPORTED = ("ra_plan", "ra_plan_window", "ra_plan_destroy", "ra_plan_tile_counts
             "ra_kv4_attend_scratch_size", "ra_kv4_sync_status")
 
 _TORCH = None
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _torch():
@@ -162,7 +163,7 @@ def _ptr(t):
 
 
 def _stream(stream):
-    import torch
+    torch = _TORCH or _torch()
     if stream is None:
         # (the raw handle: building a Stream object for it takes longer than a launch)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
@@ -178,10 +179,12 @@ def _stream(stream):
 def _alloc_on(stream):
     """Context in which buffers made for a call belong to the stream the call runs on, so that
     the allocator does not hand them on while its kernels may still use them."""
-    import torch
+    torch = _TORCH or _torch()
     if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        return _NO_CONTEXT
+    if isinstance(stream, int):  # (1 is the runtime's name of the default stream)
+        stream = torch.cuda.ExternalStream(0 if stream == 1 else stream)
+    return torch.cuda.stream(stream)
 
 
 def _on_current_device(name, t):
@@ -674,26 +677,29 @@ def _kv4_dtype(kv):
     return torch.bfloat16 if kv.problem["dtype"] == 1 else torch.float32
 
 
-def _kv4_tables(kv, cache, batch, page_table, **per_sequence):
-    """The cache, the page table and the [batch] int32 tables of a call, all on one device."""
+def _kv4_tables(kv, cache, batch, page_table, name, table, count=None):
+    """The cache, the page table and the [batch] int32 tables of a call, all on one device, which
+    is returned."""
     torch = _TORCH or _torch()
-    _need("cache", cache, (ra_kv4_cache_size(kv),), torch.uint8, cache.device)
+    device, i32 = cache.device, torch.int32
+    _need("cache", cache, (kv._bytes or ra_kv4_cache_size(kv),), torch.uint8, device)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != batch:
         raise ValueError(f"page_table must be an int32 tensor of shape ({batch}, pages of a sequence)")
-    _need_like("page_table", page_table, page_table.shape, torch.int32, cache.device)
-    for name, t in per_sequence.items():
-        if t is not None:
-            _need_like(name, t, (batch,), torch.int32, cache.device)
+    _need_like("page_table", page_table, page_table.shape, i32, device)
+    _need_like(name, table, (batch,), i32, device)
+    if count is not None:
+        _need_like("count", count, (batch,), i32, device)
+    return device
 
 
 def ra_kv4_write(kv, cache, k, v, page_table, first, count=None, stream=None):
     """Quantise rows k, v [B, Hkv, T, d] into the cache at positions first[b] + t, t < count[b]."""
     pb = kv.problem
     B, T = (k.shape[0], k.shape[2]) if k.dim() == 4 else (0, 0)
-    _kv4_tables(kv, cache, B, page_table, first=first, count=count)
+    device, dtype = _kv4_tables(kv, cache, B, page_table, "first", first, count), _kv4_dtype(kv)
     shape = (B, pb["heads_kv"], T, pb["head_dim"])
-    _need_like("k", k, shape, _kv4_dtype(kv), cache.device)
-    _need_like("v", v, shape, _kv4_dtype(kv), cache.device)
+    _need_like("k", k, shape, dtype, device)
+    _need_like("v", v, shape, dtype, device)
     _check(load_library().ra_kv4_write(kv.handle, _ptr(cache), B, T, _ptr(k), _ptr(v), _ptr(page_table),
                                        page_table.shape[1], _ptr(first), _ptr(count), _stream(stream)))
 
@@ -707,17 +713,18 @@ def ra_kv4_read(kv, cache, page_table, first, rows, count=None, k=None, v=None, 
     torch = _TORCH or _torch()
     pb = kv.problem
     B, T = page_table.shape[0], int(rows)
-    _kv4_tables(kv, cache, B, page_table, first=first, count=count)
+    device, dtype = _kv4_tables(kv, cache, B, page_table, "first", first, count), _kv4_dtype(kv)
     shape = (B, pb["heads_kv"], T, pb["head_dim"])
     if (k is None) != (v is None):
         raise ValueError("pass both k and v, or neither")
     own = k is None
     if own:
         with _alloc_on(stream):
-            k, v = (torch.empty(shape, dtype=_kv4_dtype(kv), device=cache.device) for _ in range(2))
+            k = torch.empty(shape, dtype=dtype, device=device)
+            v = torch.empty_like(k)
     else:
-        _need_like("k", k, shape, _kv4_dtype(kv), cache.device)
-        _need_like("v", v, shape, _kv4_dtype(kv), cache.device)
+        _need_like("k", k, shape, dtype, device)
+        _need_like("v", v, shape, dtype, device)
     _check(load_library().ra_kv4_read(kv.handle, _ptr(cache), B, T, _ptr(page_table), page_table.shape[1],
                                       _ptr(first), _ptr(count), int(own), _ptr(k), _ptr(v), _stream(stream)))
     return k, v
@@ -744,25 +751,25 @@ def ra_kv4_attend(kv, cache, q, page_table, length, o=None, lse=None, scratch=No
     pb = kv.problem
     if q.dim() != 4:
         raise ValueError("q must have the shape [B, Hq, T, d]")
-    B, T = q.shape[0], q.shape[2]
-    _kv4_tables(kv, cache, B, page_table, length=length)
-    _need_like("q", q, (B, pb["heads_q"], T, pb["head_dim"]), _kv4_dtype(kv), cache.device)
+    B, Hq, T, d = q.shape
+    device = _kv4_tables(kv, cache, B, page_table, "length", length)
+    _need_like("q", q, (B, pb["heads_q"], T, pb["head_dim"]), _kv4_dtype(kv), device)
     need = ra_kv4_attend_scratch_size(kv, B, T, page_table.shape[1]) // 4
     if scratch is not None and (scratch.numel() < need or scratch.dtype != torch.float32
-                                  or not scratch.is_contiguous() or scratch.device != q.device):
+                                  or not scratch.is_contiguous() or scratch.device != device):
         raise ValueError("scratch must be a contiguous float32 tensor of at least ra_kv4_attend_scratch_size(...) "
                          "bytes on the device of q")
     if o is not None:
-        _need_like("o", o, q.shape, q.dtype, q.device)
+        _need_like("o", o, q.shape, q.dtype, device)
     if lse is not None:
-        _need_like("lse", lse, q.shape[:3], torch.float32, q.device)
+        _need_like("lse", lse, (B, Hq, T), torch.float32, device)
     with _alloc_on(stream):
         if o is None:
             o = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=device)
         if scratch is None and need:
-            scratch = torch.empty(need, dtype=torch.float32, device=q.device)
+            scratch = torch.empty(need, dtype=torch.float32, device=device)
     _check(load_library().ra_kv4_attend(kv.handle, _ptr(cache), B, T, _ptr(q), _ptr(page_table), page_table.shape[1],
                                         _ptr(length), _ptr(o), _ptr(lse), _ptr(scratch), _stream(stream)))
     return o, lse
