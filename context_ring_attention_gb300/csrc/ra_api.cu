@@ -68,6 +68,8 @@ struct ra_plan_s {
   std::vector<ra::WinBwdSplit> win_splits;
   ra::WinView win_own{}, win_str{};
   int64_t n_win_bwd_kv = 0, win_scalars = 0, win_parts = 0;
+  int win_bwd_grid[2] = {0, 0};  // CTAs of the two passes,
+  bool win_bwd_both = false;     // which run side by side
   ra::WinBwdItem* d_win_bwd_items = nullptr;
   ra::WinBwdRange* d_win_bwd_ranges = nullptr;
   ra::WinBwdSplit* d_win_splits = nullptr;
@@ -642,6 +644,41 @@ void build_win_bwd(ra_plan_s* pl, const ra::WinView& own, const ra::WinView& str
   emit(tiles, false);
 }
 
+// CTAs of the backward's passes.  They do not depend on each other: where one alone leaves SMs
+// idle, or ends in a wave that does, they run side by side in one launch.  Times are estimated
+// in streamed tiles (a pass 0 tile takes 1.4 of pass 1's, an item 4 more for its beginning and
+// end, a launch 6); side by side has to promise 5%.  Measured, one after the other and side by
+// side, under a window of 512: 900 tokens of 4 heads 31 and 21 us, 1024 of 32 heads 91 and 68,
+// 4096 of 8 heads 78 and 55, of 32 heads 196 and 178; no difference from 8192 of 32 heads on.
+void choose_win_bwd_grids(ra_plan_s* pl, int sms) {
+  struct Pass {
+    int64_t n, sum, longest;
+    double time(int g) const {
+      return std::max<double>(longest, (double)((n + g - 1) / g) * ((double)sum / (double)n));
+    }
+  } pass[2] = {};
+  for (size_t x = 0; x < pl->win_bwd_items.size(); ++x) {
+    Pass& p = pass[(int64_t)x < pl->n_win_bwd_kv ? 0 : 1];
+    const int64_t cost = pl->win_bwd_items[x].n_tiles + 4;
+    ++p.n;
+    p.sum += cost;
+    p.longest = std::max(p.longest, cost);
+  }
+  constexpr double kTile0 = 1.4, kLaunch = 6;
+  double best = 0.95 * (kTile0 * pass[0].time(sms) + pass[1].time(sms) + kLaunch);
+  for (int x = 0; x < 2; ++x) pl->win_bwd_grid[x] = (int)std::min<int64_t>(pass[x].n, sms);
+  pl->win_bwd_both = false;
+  for (int g = 1; g < sms; ++g) {
+    const double t = std::max(kTile0 * pass[0].time(g), pass[1].time(sms - g));
+    if (t < best) {
+      best = t;
+      pl->win_bwd_both = true;
+      pl->win_bwd_grid[0] = (int)std::min<int64_t>(pass[0].n, g);
+      pl->win_bwd_grid[1] = (int)std::min<int64_t>(pass[1].n, sms - g);
+    }
+  }
+}
+
 void build_win_schedule(ra_plan_s* pl) {
   const ra_problem& pb = pl->prob;
   const int N = pb.n_shards;
@@ -831,12 +868,14 @@ ra_status launch_win_bwd(ra_plan_s* plan, const void* q, const void* k, const vo
   const int sms = plan->sm_count > 0 ? plan->sm_count : 148;
   const char* why = "backward preparation launch failed";
   cudaError_t e = ra::launch_win_bwd_prep(w, o, lse, scratch, sms, st);
-  for (int pass = 0; pass < 2 && e == cudaSuccess; ++pass) {
+  ra::WinBwdParams prm[2] = {w, w};
+  for (int pass = 0; pass < 2; ++pass) {
     const int64_t n = pass == 0 ? plan->n_win_bwd_kv : (int64_t)plan->win_bwd_items.size() - plan->n_win_bwd_kv;
-    w.items = plan->d_win_bwd_items + (pass == 0 ? 0 : plan->n_win_bwd_kv);
-    w.n_items = (int32_t)n;
-    e = ra::launch_win_bwd_bf16(pass, w, q, k, v, dout, (int)std::min<int64_t>(n, sms), st, &why);
+    prm[pass].items = plan->d_win_bwd_items + (pass == 0 ? 0 : plan->n_win_bwd_kv);
+    prm[pass].n_items = (int32_t)n;
   }
+  if (e == cudaSuccess)
+    e = ra::launch_win_bwd_bf16(prm, q, k, v, dout, plan->win_bwd_grid, plan->win_bwd_both, st, &why);
   if (e == cudaSuccess && !plan->win_splits.empty()) {
     why = "sum of the parts: launch failed";
     e = ra::launch_win_bwd_join(w, plan->d_win_splits, (int)plan->win_splits.size(), st);
@@ -1005,6 +1044,7 @@ static ra_status make_plan(const ra_problem* prob, int64_t window, int64_t sinks
     return fail(RA_ERR_UNSUPPORTED, "planning failed on the host: %s", ex.what());
   }
   const ra_status s = upload(pl);
+  if (!pl->win_bwd_items.empty()) choose_win_bwd_grids(pl, pl->sm_count > 0 ? pl->sm_count : 148);
   if (s != RA_OK) {
     ra_plan_destroy(pl);
     return s;

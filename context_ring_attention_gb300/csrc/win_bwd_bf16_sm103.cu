@@ -40,6 +40,13 @@
 // at 448.
 // Every wait is bounded (~1 s); on expiry the CTA records it in the status word, drains its
 // own copies and MMAs, frees TMEM and returns.
+//
+// Measured: 32768 tokens in 8 zigzag shards, 32 query and 8 key/value heads, window 4096, 4
+// sinks: 5.46 ms (pass 0 3.10, pass 1 2.23, preparation 0.08), 945 TFLOP/s of the formula's 10 d
+// a visible pair, 1355 of the 14 d executed (0.70 of the measured rate).  What bounds it: pass 0's
+// products with N = 64 read the 128-row own tile from shared memory for every streamed tile;
+// pass 1's chain of score product, elementwise step and dQ product is exposed (tensor cores 53%
+// and 45% busy).  900 tokens of 4 heads: 21 us in three launches, the passes side by side.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -163,10 +170,10 @@ __device__ __forceinline__ void tma_load_4d_warp_hint(uint32_t dst, const CUtens
       : "memory");
 }
 // ------------------------------------------------------------------- records --
-__device__ void run_records(const WinBwdParams& P, const Ctl& c, Record* recs, int lane) {
+__device__ void run_records(const WinBwdParams& P, const Ctl& c, Record* recs, int lane, uint32_t first, uint32_t stride) {
   constexpr int kWords = sizeof(WinBwdItem) / 16;
   for (uint32_t u = 0;; ++u) {
-    const int idx = (int)(blockIdx.x + u * gridDim.x);
+    const int idx = (int)(first + u * stride);
     const uint32_t slot = u % kItemSlots;
     if (!RA_WAIT(kItemEmpty + (int)slot, (u / kItemSlots) ^ 1u, kStatusTimeoutProducer)) return;
     Record& r = recs[slot];
@@ -565,11 +572,10 @@ __device__ void run_elementwise(const WinBwdParams& P, const Ctl& c, uint8_t* sg
   }
 }
 
+// A CTA of one pass, taking items first, first + stride, ...
 template <int kPass>
-__global__ void __launch_bounds__(kThreads, 1)
-    win_bwd_bf16_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ CUtensorMap tx1,
-                    const __grid_constant__ CUtensorMap ty0, const __grid_constant__ CUtensorMap ty1,
-                    const WinBwdParams P) {
+__device__ __forceinline__ void run_pass(const CUtensorMap& tx0, const CUtensorMap& tx1, const CUtensorMap& ty0,
+                                         const CUtensorMap& ty1, const WinBwdParams& P, uint32_t first, uint32_t stride) {
   using C = Cfg<kPass>;
   using B = Bars<kPass>;
   static_assert(8 * B::kNum + 8 <= 512 && C::kOffBar % 16 == 0 && C::kSmemBytes <= 232448, "shared memory");
@@ -611,8 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
-    ptx::tma_prefetch_desc(&tx0);
-    ptx::tma_prefetch_desc(&tx1);
+    if (kPass == 0) {
+      ptx::tma_prefetch_desc(&tx0);
+      ptx::tma_prefetch_desc(&tx1);
+    }
     ptx::tma_prefetch_desc(&ty0);
     ptx::tma_prefetch_desc(&ty1);
   }
@@ -637,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_bar(c, c.bar(kDone), 0);
       __syncwarp();
     } else if (warp == 2) {
-      run_records(P, c, recs, lane);
+      run_records(P, c, recs, lane, first, stride);
     }
   } else {
     ptx::regs_acquire<kRegsCompute>();
@@ -661,6 +669,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Maps of a pass: own tiles of K and V (pass 0), streamed tiles of Q and dO (pass 0) or K and
+// V (pass 1; its own rows of Q and dO are read without a map).
+struct Maps {
+  CUtensorMap own_k, own_v, y0, y1;
+};
+
+template <int kPass>
+__global__ void __launch_bounds__(kThreads, 1)
+    win_bwd_bf16_kernel(const __grid_constant__ Maps t, const __grid_constant__ WinBwdParams P) {
+  run_pass<kPass>(t.own_k, t.own_v, t.y0, t.y1, P, blockIdx.x, gridDim.x);
+}
+// Both passes side by side: the first `n0` CTAs take pass 0's items, the others pass 1's.
+__global__ void __launch_bounds__(kThreads, 1)
+    win_bwd_both_kernel(const __grid_constant__ Maps t0, const __grid_constant__ Maps t1,
+                        const __grid_constant__ WinBwdParams P0, const __grid_constant__ WinBwdParams P1, uint32_t n0) {
+  if (blockIdx.x < n0) run_pass<0>(t0.own_k, t0.own_v, t0.y0, t0.y1, P0, blockIdx.x, n0);
+  else run_pass<1>(t1.own_k, t1.own_v, t1.y0, t1.y1, P1, blockIdx.x - n0, gridDim.x - n0);
 }
 
 // -------------------------------------------------------------- preparation --
@@ -762,14 +789,25 @@ bool encode_view(CUtensorMap* map, const void* base, const WinView& view, int64_
 }
 
 template <int kPass>
-cudaError_t launch_pass(const WinBwdParams& prm, const CUtensorMap& tx0, const CUtensorMap& tx1, const CUtensorMap& ty0,
-                        const CUtensorMap& ty1, int grid, cudaStream_t stream, const char** why) {
+cudaError_t launch_pass(const WinBwdParams& prm, const Maps& maps, int grid, cudaStream_t stream, const char** why) {
   using C = Cfg<kPass>;
   static std::atomic<int> ready[kMaxDevices];
   cudaError_t e = prepare_once(win_bwd_bf16_kernel<kPass>, ready, kThreads, 128 * kRegsOther + 256 * kRegsCompute,
                                (int)C::kSmemBytes, why);
   if (e != cudaSuccess) return e;
-  win_bwd_bf16_kernel<kPass><<<grid, kThreads, C::kSmemBytes, stream>>>(tx0, tx1, ty0, ty1, prm);
+  win_bwd_bf16_kernel<kPass><<<grid, kThreads, C::kSmemBytes, stream>>>(maps, prm);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) *why = "windowed tensor-core backward launch failed";
+  return e;
+}
+
+cudaError_t launch_both(const WinBwdParams (&prm)[2], const Maps (&maps)[2], const int (&grid)[2], cudaStream_t stream,
+                        const char** why) {
+  constexpr int kSmem = Cfg<0>::kSmemBytes > Cfg<1>::kSmemBytes ? Cfg<0>::kSmemBytes : Cfg<1>::kSmemBytes;
+  static std::atomic<int> ready[kMaxDevices];
+  cudaError_t e = prepare_once(win_bwd_both_kernel, ready, kThreads, 128 * kRegsOther + 256 * kRegsCompute, kSmem, why);
+  if (e != cudaSuccess) return e;
+  win_bwd_both_kernel<<<grid[0] + grid[1], kThreads, kSmem, stream>>>(maps[0], maps[1], prm[0], prm[1], (uint32_t)grid[0]);
   e = cudaGetLastError();
   if (e != cudaSuccess) *why = "windowed tensor-core backward launch failed";
   return e;
@@ -791,23 +829,22 @@ cudaError_t launch_win_bwd_join(const WinBwdParams& prm, const WinBwdSplit* spli
   return cudaGetLastError();
 }
 
-cudaError_t launch_win_bwd_bf16(int pass, const WinBwdParams& prm, const void* q, const void* k, const void* v,
-                                const void* dout, int grid, cudaStream_t stream, const char** why) {
-  CUtensorMap a, b, y0, y1;
-  const int64_t hq = (int64_t)prm.batch * prm.heads_q, hk = (int64_t)prm.batch * prm.heads_kv;
-  bool ok;
-  if (pass == 0)  // own tiles K, V; streamed Q, dO and {lse2, D}
-    ok = encode_view(&a, k, prm.own, prm.seq, hk) && encode_view(&b, v, prm.own, prm.seq, hk) &&
-         encode_view(&y0, q, prm.str, prm.seq, hq) && encode_view(&y1, dout, prm.str, prm.seq, hq);
-  else            // own tiles Q, dO (read without a map); streamed K, V
-    ok = encode_view(&a, q, prm.own, prm.seq, hq) && encode_view(&b, dout, prm.own, prm.seq, hq) &&
-         encode_view(&y0, k, prm.str, prm.seq, hk) && encode_view(&y1, v, prm.str, prm.seq, hk);
-  if (!ok) {
+cudaError_t launch_win_bwd_bf16(const WinBwdParams (&prm)[2], const void* q, const void* k, const void* v,
+                                const void* dout, const int (&grid)[2], bool both, cudaStream_t stream, const char** why) {
+  Maps maps[2];
+  const WinBwdParams& p = prm[0];
+  const int64_t hq = (int64_t)p.batch * p.heads_q, hk = (int64_t)p.batch * p.heads_kv;
+  if (!encode_view(&maps[0].own_k, k, p.own, p.seq, hk) || !encode_view(&maps[0].own_v, v, p.own, p.seq, hk) ||
+      !encode_view(&maps[0].y0, q, p.str, p.seq, hq) || !encode_view(&maps[0].y1, dout, p.str, p.seq, hq) ||
+      !encode_view(&maps[1].y0, k, p.str, p.seq, hk) || !encode_view(&maps[1].y1, v, p.str, p.seq, hk)) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }
-  return pass == 0 ? launch_pass<0>(prm, a, b, y0, y1, grid, stream, why)
-                   : launch_pass<1>(prm, a, b, y0, y1, grid, stream, why);
+  maps[1].own_k = maps[0].own_k;  // (not used)
+  maps[1].own_v = maps[0].own_v;
+  if (both) return launch_both(prm, maps, grid, stream, why);
+  const cudaError_t e = launch_pass<0>(prm[0], maps[0], grid[0], stream, why);
+  return e != cudaSuccess ? e : launch_pass<1>(prm[1], maps[1], grid[1], stream, why);
 }
 
 }  // namespace ra

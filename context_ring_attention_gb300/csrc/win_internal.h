@@ -175,9 +175,10 @@ RA_HD int64_t win_scalar_block(const WinBwdParams& P, int64_t bh, int shard, int
 
 cudaError_t launch_win_bwd_prep(const WinBwdParams& prm, const void* o, const float* lse, float* out, int sms,
                                 cudaStream_t stream);
-// pass 0: dK and dV (items are key tiles); pass 1: dQ (items are query tiles).
-cudaError_t launch_win_bwd_bf16(int pass, const WinBwdParams& prm, const void* q, const void* k, const void* v,
-                                const void* dout, int grid, cudaStream_t stream, const char** why);
+// pass 0: dK and dV (items are key tiles); pass 1: dQ (items are query tiles); each with grid
+// CTAs, one after the other or (both) side by side in one launch.
+cudaError_t launch_win_bwd_bf16(const WinBwdParams (&prm)[2], const void* q, const void* k, const void* v,
+                                const void* dout, const int (&grid)[2], bool both, cudaStream_t stream, const char** why);
 cudaError_t launch_win_bwd_join(const WinBwdParams& prm, const WinBwdSplit* splits, int n, cudaStream_t stream);
 cudaError_t launch_win_fwd_bf16(const WinParams& prm, const void* q, const void* k, const void* v, int grid,
                                 cudaStream_t stream, const char** why);
