@@ -109,14 +109,16 @@ struct Split {
   bool in_row;  // the sequences' blocks are shared in a row
 };
 
-// Shares of the keys: as many CTAs as the GPU holds at once, 3 an SM (fp32: 2), each with the
-// same number of blocks -- of one sequence, or of all sequences laid in a row, where a CTA's
-// share may be the end of one and the beginning of the next.  Shares per sequence, of equal
-// number whatever its length, took 86 us for 32 sequences under a window of 8192 tokens (in a
-// row 79), 117 for 8 of up to 64k (101) and 41 for 16 of up to 8k (37).  Beyond that many
-// sequences each has one CTA and the GPU deals them out, unless they are up to twice as many
-// and long: 64 sequences of up to 16k tokens 206 us one a sequence, 163 in a row, 100 of up to
-// 4k 89 and 87, but 64 of up to 2k 36 and 42; 200 of up to 4k 146 and 155 us.
+// Shares of the keys: as many CTAs as the GPU holds at once -- 3 an SM, fp32 2, few rows of
+// d = 64 4 (4 sequences of 64k 36 us, with 3 38) -- each with the same number of blocks: of one
+// sequence, or of all sequences laid in a row, where a CTA's share may be the end of one and
+// the beginning of the next.  The figures of this rule were taken with 8 query rows a product:
+// shares per sequence, of equal number whatever its length, took 86 us for 32 sequences under a
+// window of 8192 tokens (in a row 79), 117 for 8 of up to 64k (101) and 41 for 16 of up to 8k
+// (37).  Beyond that many sequences each has one CTA and the GPU deals them out, unless they
+// are up to twice as many and long: 64 sequences of up to 16k tokens 206 us one a sequence, 163
+// in a row, 100 of up to 4k 89 and 87, but 64 of up to 2k 36 and 42; 200 of up to 4k 146 and
+// 155 us.
 // No CTA gets fewer than 16 blocks of 16 tokens, four a warp: below that the join costs more
 // than the share saves (8k tokens, one block a warp at a time: 10.5 us; with 8 blocks 12.1,
 // with 32 11.5).  Several sequences are shared out only where one may be of 1536 tokens or
@@ -136,7 +138,8 @@ ra_status split_of(const ra_kv4_s* kv, int64_t batch, int64_t rows, int64_t tabl
   if (pb.window > 0 && pb.window < kMaxPositions && pb.sinks < kMaxPositions)
     keys = std::min(keys, pb.window + rows + pb.sinks + 32);
   const int64_t sms = kv->sm_count > 0 ? kv->sm_count : 148;
-  const int64_t per_sm = pb.dtype == RA_DTYPE_BF16 ? 3 : 2;
+  const bool half = rows * (pb.heads_q / pb.heads_kv) <= 4;  // the kernel's form for few rows
+  const int64_t per_sm = pb.dtype != RA_DTYPE_BF16 ? 2 : half && pb.head_dim == 64 ? 4 : 3;
   const int64_t slots = std::min(per_sm * sms / (pb.heads_kv * out->tiles), int64_t(ra::kMaxSlots));
   if (batch == 1) {
     out->in_row = false;

@@ -35,12 +35,12 @@
 // 1M tokens from 276 to 257 us and 16 new tokens of 64k from 180 to 136.  Two blocks in 128
 // registers: 276 us; two pairs a warp in shared memory for three: 260.
 //
-// Measured (32 query and 8 key/value heads, d = 128, bf16, one new token): 1M tokens 257 us,
-// 1.34 GB of cache at 5.2 TB/s (0.77 of a plain copy's rate); 64k tokens 28 us; 32 sequences
-// of 2k to 32k under a window of 8192 tokens 79 us.  What bounds it is the issue of
-// instructions (59% of the slots with 11 warps an SM), some 350 a block and warp, about half
-// of them for turning codes and weights into operands.  fp32 takes three terms per query and
-// weight and three times the products: 4 sequences of 64k tokens 95 us.
+// Measured (32 query and 8 key/value heads, d = 128, bf16, one new token): 1M tokens 234 us,
+// 1.34 GB of cache at 5.7 TB/s (0.84 of a plain copy's rate); 64k tokens 26.5 us; 32 sequences
+// of 2k to 32k under a window of 8192 tokens 71 us.  What bounds it is the issue of
+// instructions, some 300 a block and warp, more than half of them for turning codes and weights
+// into operands.  fp32 takes three terms per query and weight and three times the products:
+// 4 sequences of 64k tokens 84 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -240,13 +240,22 @@ __device__ __forceinline__ Share share_of(const Kv4AttendParams& P, int slot) {
 // kInRow: the sequences' blocks are shared in a row, so that a CTA may have parts of several;
 // otherwise it has (a share of) one.  (As one kernel a single sequence of 1M tokens took 4%
 // longer, and one of 8k 12 us for 10.)
-template <typename T, int D, bool kInRow>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_attend_kernel(const Kv4AttendParams P) {
+// kHalf: up to 4 query rows, one new token of a group of up to 4 heads.  The products have 8
+// columns: the first 4 are then the rows over the first of the warp's two blocks, the others
+// the same rows over the second, each with a maximum and sums of its own, joined at the end as
+// the warps' are.  Scores, exponentials and weights take half the instructions (one sequence of
+// 1M tokens 258 us with 4 empty columns, 234 so; 32 under a window of 8192 79 and 71).
+template <typename T, int D, bool kInRow, bool kHalf>
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64 ? 4 : 3 : 3) : 1) kv4_attend_kernel(const Kv4AttendParams P) {
   using F = Kv4Block<D>;
   constexpr int G = F::kGroups;
   constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
+  constexpr int kSets = kHalf ? 1 : 2;  // sets of scores: of either block, or of both
+  constexpr int kRows = kHalf ? kTile / 2 : kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
+  const int rq = kHalf ? r & 3 : r;  // query row of the fragments' column r
+  const bool second = kHalf && c >= 2;  // this lane's columns are of the second block
   // One sequence: the shares of a head next to each other (1M tokens 256 us, the heads of a
   // share next to each other 262); several: the heads, whose blocks lie in the same pages (64
   // sequences of up to 2k 37 against 39.5).
@@ -283,8 +292,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
   uint32_t qsum[4]; // sum of group c's channels of row r, in the scores' unit 2^(E - 133)
   float back[2];    // that unit's inverse for rows 2c and 2c + 1, times the score scale (log2 units)
   {
-    const bool live = row0 + r < n_rows;
-    const T* qrow = static_cast<const T*>(P.q) + (((int64_t)b * P.heads_q + (int64_t)h * P.group) * P.rows + row0 + r) * D;
+    const bool live = row0 + rq < n_rows;
+    const T* qrow = static_cast<const T*>(P.q) + (((int64_t)b * P.heads_q + (int64_t)h * P.group) * P.rows + row0 + rq) * D;
     float x[G][8];
     float top = 0.f;
 #pragma unroll
@@ -334,22 +343,30 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
   extern __shared__ __align__(16) uint8_t ring[];
   // The fragments wait in shared memory, the same for all warps: registers are what bounds
   // the warps of an SM.
+  constexpr int kFrags = G * kTerms * (kHalf ? 2 : 1);
   uint32_t* const qsm = reinterpret_cast<uint32_t*>(ring + kWarps * kPairs * 2 * F::kBytes);
   if (warp == 0) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
 #pragma unroll
-      for (int n = 0; n < kTerms; ++n)
-        *reinterpret_cast<uint4*>(qsm + ((g * kTerms + n) * 32 + lane) * 4) =
-            make_uint4(qf[g][0][n], qf[g][1][n], qf[g][2][n], qf[g][3][n]);
+      for (int n = 0; n < kTerms; ++n) {
+        const uint4 f = make_uint4(qf[g][0][n], qf[g][1][n], qf[g][2][n], qf[g][3][n]), none = make_uint4(0u, 0u, 0u, 0u);
+        uint4* at = reinterpret_cast<uint4*>(qsm + ((g * kTerms + n) * 32 + lane) * 4);
+        if (!kHalf) {
+          at[0] = f;
+        } else {  // for the first block in columns 0-3, for the second in 4-7
+          at[0] = r < 4 ? f : none;
+          at[G * kTerms * 32] = r < 4 ? none : f;
+        }
+      }
     }
-    *reinterpret_cast<uint4*>(qsm + G * kTerms * 32 * 4 + lane * 4) = make_uint4(qsum[0], qsum[1], qsum[2], qsum[3]);
+    *reinterpret_cast<uint4*>(qsm + kFrags * 32 * 4 + lane * 4) = make_uint4(qsum[0], qsum[1], qsum[2], qsum[3]);
   }
   __syncthreads();
   // Positions of rows 2c and 2c + 1 (of the query), and the tokens of this lane's keys.
   int32_t qpos[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) qpos[e] = len - P.rows + (row0 + 2 * c + e) % P.rows;
+  for (int e = 0; e < 2; ++e) qpos[e] = len - P.rows + (row0 + ((2 * c + e) & (kRows - 1))) % P.rows;
   const int tok0 = token_of(r), tok1 = token_of(r + 8);
   const int vt[4] = {token_of(2 * c), token_of(2 * c + 1), token_of(2 * c + 8), token_of(2 * c + 9)};
 
@@ -427,26 +444,34 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
     __syncwarp();  // every lane's copies have landed
     const uint8_t* base[2] = {mine + (2 * slot) * F::kBytes, mine + (2 * slot + 1) * F::kBytes};
     const uint32_t gone = (bad >> (2 * slot)) & 3u;
+    auto own = [&](int n) { return kHalf ? (second ? base[1] : base[0]) : base[n]; };  // the block of score set n
 
     // Scores: s[n][0], s[n][1] of key tok0 of block n for rows 2c, 2c + 1; s[n][2], s[n][3]
     // of key tok1.  The minima's part first, as products of their own: a parameter word is
     // (scale, low) of key and group c, met by (0, sum of q) in bf16 terms.
-    float s[2][4];
-    uint32_t kp0[2][G], kp1[2][G];
+    float s[kSets][4];
+    uint32_t kp0[kSets][G], kp1[kSets][G];
     {
       uint32_t qw[4];
-      load_words<4>(reinterpret_cast<const uint8_t*>(qsm + G * kTerms * 32 * 4 + lane * 4), qw);
+      load_words<4>(reinterpret_cast<const uint8_t*>(qsm + kFrags * 32 * 4 + lane * 4), qw);
       const uint32_t b01[2] = {qw[0], qw[1]}, b23[2] = {qw[2], qw[3]};
+      float low[2][4];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         uint32_t lw[2];
         lw[0] = *reinterpret_cast<const uint32_t*>(base[n] + F::kOffKPar + tok0 * F::kParBytes + (c & (G - 1)) * 4);
         lw[1] = *reinterpret_cast<const uint32_t*>(base[n] + F::kOffKPar + tok1 * F::kParBytes + (c & (G - 1)) * 4);
         const uint32_t a[4] = {lw[0], lw[1], lw[0], lw[1]};
-        mma16816_first(s[n], a, b23);
-        mma16816(s[n], a, b01);
-        load_words<G>(base[n] + F::kOffKPar + tok0 * F::kParBytes, kp0[n]);
-        load_words<G>(base[n] + F::kOffKPar + tok1 * F::kParBytes, kp1[n]);
+        mma16816_first(low[n], a, b23);
+        mma16816(low[n], a, b01);
+      }
+#pragma unroll
+      for (int n = 0; n < kSets; ++n) {
+        // (the minima's products of the two blocks are apart, since what is not seen may be NaN)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = kHalf ? (second ? low[1][e] : low[0][e]) : low[n][e];
+        load_words<G>(own(n) + F::kOffKPar + tok0 * F::kParBytes, kp0[n]);
+        load_words<G>(own(n) + F::kOffKPar + tok1 * F::kParBytes, kp1[n]);
       }
     }
     {
@@ -458,27 +483,30 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        float acc[2][4];
-        uint32_t qg[kTerms][4];
+        float acc[kSets][4];
+        uint32_t qg[kHalf ? 2 : 1][kTerms][4];
 #pragma unroll
-        for (int n = 0; n < kTerms; ++n)
-          load_words<4>(reinterpret_cast<const uint8_t*>(qsm + ((g * kTerms + n) * 32 + lane) * 4), qg[n]);
+        for (int y = 0; y < (kHalf ? 2 : 1); ++y)
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t)
+            load_words<4>(reinterpret_cast<const uint8_t*>(qsm + (((y * G + g) * kTerms + t) * 32 + lane) * 4), qg[y][t]);
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {  // nibbles (i, i + 4) and (i + 1, i + 5) of the words
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const uint32_t x0 = k0[n][g] >> (4 * i), x1 = k1[n][g] >> (4 * i);
             const uint32_t a[4] = {codes_lo(x0), codes_lo(x1), codes_hi(x0), codes_hi(x1)};
+            const int set = kHalf ? 0 : n, y = kHalf ? n : 0;
 #pragma unroll
             for (int t = kTerms - 1; t >= 0; --t) {
-              const uint32_t q2[2] = {qg[t][i], qg[t][i + 1]};
-              if (i == 0 && t == kTerms - 1) mma16816_first(acc[n], a, q2);
-              else mma16816(acc[n], a, q2);
+              const uint32_t q2[2] = {qg[y][t][i], qg[y][t][i + 1]};
+              if (i == 0 && t == kTerms - 1 && y == 0) mma16816_first(acc[set], a, q2);
+              else mma16816(acc[set], a, q2);
             }
           }
         }
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < kSets; ++n) {
           const float s0 = scale_of(kp0[n][g]), s1 = scale_of(kp1[n][g]);
           s[n][0] = fmaf(s0, acc[n][0], s[n][0]);
           s[n][1] = fmaf(s0, acc[n][1], s[n][1]);
@@ -488,7 +516,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
       }
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < kSets; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[n][e] *= back[e & 1];
 
@@ -499,11 +527,12 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
                        (second_block >= whole_from || second_block < whole_sinks);
     if (!whole) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < kSets; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int32_t j = (n ? second_block : first_block) * kKvBlockRows + (e < 2 ? tok0 : tok1), i = qpos[e & 1];
-          if (((gone >> n) & 1u) || !(j <= i && (P.window == 0 || j > i - P.window || j < P.sinks))) {
+          const bool last = kHalf ? second : n == 1;
+          const int32_t j = (last ? second_block : first_block) * kKvBlockRows + (e < 2 ? tok0 : tok1), i = qpos[e & 1];
+          if (((gone >> (last ? 1 : 0)) & 1u) || !(j <= i && (P.window == 0 || j > i - P.window || j < P.sinks))) {
             seen &= ~(1u << (4 * n + e));
             s[n][e] = -INFINITY;
           }
@@ -514,7 +543,10 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
     // by the slack.
     float mx[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(s[0][e], s[0][e + 2]), fmaxf(s[1][e], s[1][e + 2]));
+    for (int e = 0; e < 2; ++e) {
+      mx[e] = fmaxf(s[0][e], s[0][e + 2]);
+      if (!kHalf) mx[e] = fmaxf(mx[e], fmaxf(s[kSets - 1][e], s[kSets - 1][e + 2]));
+    }
     if (__any_sync(0xffffffffu, mx[0] > m[0] + kRescaleSlack || mx[1] > m[1] + kRescaleSlack)) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -539,7 +571,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
     for (int e = 0; e < 2; ++e) {
       const float ref = m[e] == -INFINITY ? 0.f : m[e] - kShift;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < kSets; ++n)
 #pragma unroll
         for (int i = e; i < 4; i += 2) {
           s[n][i] = ptx::ex2_approx(s[n][i] - ref);  // p from here on
@@ -551,14 +583,18 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
     // codes of two keys a register as the 16 x 16 one (channels x keys).
     auto values = [&](auto masked) {
       const uint32_t minus8[4] = {kMinus8Lo, kMinus8Hi, kMinus8Lo, kMinus8Hi};
+      constexpr int kWith = kHalf ? 2 : 1;  // blocks of a score set
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        asm volatile("" ::: "memory");  // (one block's words are held at a time)
-        uint32_t vp0[G], vp1[G], vw[4][G / 2];
-        load_words<G>(base[n] + F::kOffVPar + tok0 * F::kParBytes, vp0);
-        load_words<G>(base[n] + F::kOffVPar + tok1 * F::kParBytes, vp1);
+      for (int n = 0; n < kSets; ++n) {
+        asm volatile("" ::: "memory");  // (one set's words are held at a time)
+        uint32_t vp0[G], vp1[G], vw[kWith][4][G / 2];
+        load_words<G>(own(n) + F::kOffVPar + tok0 * F::kParBytes, vp0);
+        load_words<G>(own(n) + F::kOffVPar + tok1 * F::kParBytes, vp1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_words<G / 2>(base[n] + F::kOffV + vt[i] * F::kCodeBytes + r * (2 * G), vw[i]);
+        for (int y = 0; y < kWith; ++y)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            load_words<G / 2>(base[kHalf ? y : n] + F::kOffV + vt[i] * F::kCodeBytes + r * (2 * G), vw[y][i]);
         const float(&p)[4] = s[n];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -576,28 +612,41 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
             pm[g][0] = fmaf(p[0], m0, fmaf(p[2], m1, pm[g][0]));
             pm[g][1] = fmaf(p[1], m0, fmaf(p[3], m1, pm[g][1]));
           }
-          uint32_t w0[kTerms], w1[kTerms];
+          uint32_t w0[kTerms], w1[kTerms], b2[kTerms][2];
           split_pair<kTerms>(w[0], w[1], w0);
           split_pair<kTerms>(w[2], w[3], w1);
-          const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
-          const uint32_t a01 = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel);
-          const uint32_t a23 = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
-          uint32_t a[2][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t x01 = a01 >> (8 * i), x23 = a23 >> (8 * i);
-            a[i][0] = codes_lo(x01);
-            a[i][1] = codes_hi(x01);
-            a[i][2] = codes_lo(x23);
-            a[i][3] = codes_hi(x23);
+          for (int t = 0; t < kTerms; ++t) {
+            b2[t][0] = transpose8(w0[t]);
+            b2[t][1] = transpose8(w1[t]);
+          }
+#pragma unroll
+          for (int y = 0; y < kWith; ++y) {
+            const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+            const uint32_t a01 = __byte_perm(vw[y][0][g / 2], vw[y][1][g / 2], sel);
+            const uint32_t a23 = __byte_perm(vw[y][2][g / 2], vw[y][3][g / 2], sel);
+            uint32_t a[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t x01 = a01 >> (8 * i), x23 = a23 >> (8 * i);
+              a[i][0] = codes_lo(x01);
+              a[i][1] = codes_hi(x01);
+              a[i][2] = codes_lo(x23);
+              a[i][3] = codes_hi(x23);
+            }
+            // columns 0-3 are the first block's weights, 4-7 the second's
+            const uint32_t mine_only = kHalf ? ((r < 4) == (y == 0) ? ~0u : 0u) : ~0u;
+#pragma unroll
+            for (int t = kTerms - 1; t >= 0; --t) {
+              const uint32_t by[2] = {b2[t][0] & mine_only, b2[t][1] & mine_only};
+              mma16816(o[g][0], a[0], by);
+              mma16816(o[g][1], a[1], by);
+            }
           }
 #pragma unroll
           for (int t = kTerms - 1; t >= 0; --t) {
-            const uint32_t b2[2] = {transpose8(w0[t]), transpose8(w1[t])};
-            mma16816(o[g][0], a[0], b2);
-            mma16816(o[g][1], a[1], b2);
-            mma16816(o[g][0], minus8, b2);
-            mma16816(o[g][1], minus8, b2);
+            mma16816(o[g][0], minus8, b2[t]);
+            mma16816(o[g][1], minus8, b2[t]);
           }
         }
       }
@@ -645,20 +694,25 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 3 : 1) kv4_atten
                       fmaf(o[g][1][e], two_to(73), pm[g][e] * two_to(-60)),
                       fmaf(o[g][1][e + 2], two_to(69), pm[g][e] * two_to(-60)));
   __syncthreads();
-  for (int at = threadIdx.x; at < kTile * D; at += kWarps * 32) {
+  for (int at = threadIdx.x; at < kRows * D; at += kWarps * 32) {
     const int row = at / D, ch = at % D;
-    float mx = sm_m[0][row];
+    float mx = -INFINITY;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][row]);
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int col = row; col < kTile; col += kRows) mx = fmaxf(mx, sm_m[w][col]);
     float sum = 0.f, acc = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = sm_m[w][row] == -INFINITY ? 0.f : ptx::ex2_approx(sm_m[w][row] - mx);
-      // (a warp that saw nothing of this row holds zeros, one that saw only NaN a sum of NaN:
-      // a row is empty when its sum is 0)
-      sum = fmaf(f, sm_l[w][row], sum);
-      acc = fmaf(f, sm_o[w][row][ch], acc);
-    }
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int y = 0; y < kTile / kRows; ++y) {
+        const int col = row + y * kRows;
+        const float f = sm_m[w][col] == -INFINITY ? 0.f : ptx::ex2_approx(sm_m[w][col] - mx);
+        // (a warp that saw nothing of this row holds zeros, one that saw only NaN a sum of NaN:
+        // a row is empty when its sum is 0)
+        sum = fmaf(f, sm_l[w][col], sum);
+        acc = fmaf(f, sm_o[w][col][ch], acc);
+      }
     if (!(begins && ends)) {
       const int64_t part = ((int64_t)ht * P.slots + cta) * 2 + begins;
       P.part_o[(part * kTile + row) * D + ch] = acc;
@@ -750,17 +804,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Atte
   if (threadIdx.x == 0 && P.lse != nullptr) P.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
-template <typename T, int D, bool kInRow>
+template <typename T, int D, bool kInRow, bool kHalf>
 cudaError_t attend_as(const Kv4AttendParams& prm, cudaStream_t st) {
   constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
-  constexpr int kSmem = kWarps * kPairs * 2 * Kv4Block<D>::kBytes + 32 * 16 * ((D / 32) * kTerms + 1);
+  constexpr int kSmem = kWarps * kPairs * 2 * Kv4Block<D>::kBytes + 32 * 16 * ((D / 32) * kTerms * (kHalf ? 2 : 1) + 1);
   static std::atomic<int> ready[kMaxDevices];
   const char* why = "";
-  cudaError_t e = prepare_once(kv4_attend_kernel<T, D, kInRow>, ready, kWarps * 32, 0, kSmem, &why);
+  cudaError_t e = prepare_once(kv4_attend_kernel<T, D, kInRow, kHalf>, ready, kWarps * 32, 0, kSmem, &why);
   if (e != cudaSuccess) return e;
   const unsigned heads = (unsigned)(prm.t.heads_kv * prm.tiles), slots = (unsigned)prm.slots;
   const dim3 grid = prm.t.batch == 1 ? dim3(slots, heads) : dim3(heads, slots);
-  kv4_attend_kernel<T, D, kInRow><<<grid, kWarps * 32, kSmem, st>>>(prm);
+  kv4_attend_kernel<T, D, kInRow, kHalf><<<grid, kWarps * 32, kSmem, st>>>(prm);
   e = cudaGetLastError();
   if (e != cudaSuccess || (!kInRow && prm.slots == prm.t.batch)) return e;
   // The join's CTAs may be placed while the last of the others still run; they wait for
@@ -781,15 +835,21 @@ cudaError_t attend_as(const Kv4AttendParams& prm, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv4_attend(int dtype, int head_dim, const Kv4AttendParams& prm, cudaStream_t stream) {
-  const bool in_row = prm.in_row != 0;
-  if (dtype == RA_DTYPE_BF16) {
-    if (head_dim == 128)
-      return in_row ? attend_as<__nv_bfloat16, 128, true>(prm, stream) : attend_as<__nv_bfloat16, 128, false>(prm, stream);
-    return in_row ? attend_as<__nv_bfloat16, 64, true>(prm, stream) : attend_as<__nv_bfloat16, 64, false>(prm, stream);
-  }
-  if (head_dim == 128)
-    return in_row ? attend_as<float, 128, true>(prm, stream) : attend_as<float, 128, false>(prm, stream);
-  return in_row ? attend_as<float, 64, true>(prm, stream) : attend_as<float, 64, false>(prm, stream);
+  auto rows = [&](auto type, auto d, auto in_row) {
+    using T = decltype(type);
+    constexpr int D = decltype(d)::value;
+    constexpr bool kInRow = decltype(in_row)::value;
+    return prm.group * prm.rows <= kTile / 2 ? attend_as<T, D, kInRow, true>(prm, stream)
+                                             : attend_as<T, D, kInRow, false>(prm, stream);
+  };
+  auto in_row = [&](auto type, auto d) {
+    return prm.in_row != 0 ? rows(type, d, std::true_type()) : rows(type, d, std::false_type());
+  };
+  auto dim = [&](auto type) {
+    return head_dim == 128 ? in_row(type, std::integral_constant<int, 128>())
+                           : in_row(type, std::integral_constant<int, 64>());
+  };
+  return dtype == RA_DTYPE_BF16 ? dim(__nv_bfloat16()) : dim(float());
 }
 
 }  // namespace ra
