@@ -1,6 +1,6 @@
 // Writing rows into the 4-bit cache and reading them back.
 //
-// Per group of 32 channels (include/ra.h): low = bf16(min), scale = bf16((max - low)/15),
+// Per group of 32 channels (include/ra.h): low = bf16(min), scale = bf16((max - low) * 1/15),
 // code = floor((x - low)/scale + 1/2), value = low + scale * code.  Both kernels are bound
 // by HBM: a token and head move 2 * d * sizeof(T) bytes of rows and 2 * d * 5/8 of cache.
 //
@@ -16,7 +16,7 @@
 //
 // Measured (bf16, d = 128, 32768 tokens of 8 heads): write 54 us for 134 MB of rows and
 // 42 MB of cache, 3.2 TB/s; read 26 us for the same bytes, 6.7 TB/s.  Pairs by one
-// instruction took the write from 62 us to 59.5, the quotient by 15 without a division to
+// instruction took the write from 62 us to 59.5, a product with 1/15 instead of a division to
 // 57.5, and 64 registers, for four CTAs an SM instead of three, to 54.  The read loads words
 // of two groups and exchanges halves (by 16-bit loads it took 37 us, so 31) and makes floats
 // of codes by one byte permutation each and pairs of values by one instruction.
@@ -244,12 +244,8 @@ __device__ __forceinline__ void group_bounds(const Raw<__nv_bfloat16>& raw, floa
 // A group's scale and low: zeros for a scale below 2^-100, NaN for low where the range is not finite.
 __device__ __forceinline__ void params_of(float lo, float hi, float& scale, float& low) {
   low = bf16_round(lo);
-  // (hi - low) / 15, correctly rounded: the quotient by the correctly rounded reciprocal, its
-  // exact remainder, and one correction by that (Markstein's theorem; the same bits as the
-  // division for every significand)
-  constexpr float kFifteenth = 1.f / 15.f;
-  const float range = hi - low, q = range * kFifteenth;
-  scale = bf16_round(fmaf(fmaf(-15.f, q, range), kFifteenth, q));
+  constexpr float kFifteenth = 1.f / 15.f;  // (part of the format: the product is rounded, not a quotient)
+  scale = bf16_round((hi - low) * kFifteenth);
   if (!(fabsf(scale) <= 3.402823466e38f)) {
     scale = 0.f;
     low = __uint_as_float(0x7fff0000u);  // NaN

@@ -467,7 +467,8 @@ ra_status ra_wait_selftest(uint32_t* status_out);
  * parameters, the same for the values.  Every 32 channels of a row form a group with two
  * bf16 parameters, scale then low (4 bytes a group, groups in order), computed in float32
  * from the group's values x:
- *   low = bf16(min x),  scale = bf16((max x - low) / 15), 0 when that is below 2^-100,
+ *   low = bf16(min x),  scale = bf16((max x - low) * r), 0 when that is below 2^-100, with
+ *   r the float32 next to 1/15,
  *   code = floor((x - low) / scale + 1/2) in exact arithmetic, held to 0..15 (0 when
  *   scale is 0),  value = low + scale * code.
  * A group with an infinity, a NaN or a range beyond float32 gets scale 0 and low NaN: all

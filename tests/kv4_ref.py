@@ -18,8 +18,8 @@ def quantise(x):
     g = x.reshape(x.shape[:-1] + (-1, 32))
     with np.errstate(over="ignore", invalid="ignore"):
         low = bf16(g.min(-1))
-        span = (g.max(-1) - low).astype(np.float32).astype(np.float64)
-        scale = bf16((span / 15).astype(np.float32).astype(np.float64))
+        span = (g.max(-1) - low).astype(np.float32)
+        scale = bf16(span * (np.float32(1) / np.float32(15)))  # a float32 product
         bad = ~(np.isfinite(g).all(-1) & np.isfinite(scale) & np.isfinite(low))
         scale = np.where(bad | (scale < 2.0 ** -100), 0.0, scale)
         codes = np.zeros(g.shape, np.int64)
