@@ -550,59 +550,50 @@ void build_win_bwd(ra_plan_s* pl, const ra::WinView& own, const ra::WinView& str
   total *= pb.batch * pb.heads_kv;
   normal = std::max(normal, (int32_t)std::min<int64_t>(total / 10000, kMostTiles / 2));
   const int32_t whole = std::max(normal, std::min(2 * normal, kMostTiles));  // tiles of a sink tile left as it is
+  // Where the tiles are too few for the SMs (37, a quarter of them, or less) the chain of
+  // streamed tiles of one is the pass: those of more than one and a half times an SM's share (8
+  // tiles at least) are cut too.  Whole and cut: 1024 tokens of 8 query heads for 2, window 512,
+  // 65 and 23 us; 810 of 4 for 1, 36 and 25; 4096 of 4 for 1 under a window of as many 225 and
+  // 105.  With 64 tiles and more there is nothing to gain, and the parts have to be written and
+  // added: 4096 tokens of 8 for 2 in zigzag shards 54 and 72.
+  const int32_t share = (int32_t)std::clamp<int64_t>(total / 148, 8, kMostTiles / 2);
+  const bool small = share < normal &&
+                     (int64_t)(tiles.size() + sink_tiles.size()) * pb.batch * pb.heads_kv <= 37;
   int64_t parts = 0;  // floats per key/value head
   std::vector<ra::WinBwdSplit> splits;
-  for (ra::WinBwdItem it : sink_tiles) {
-    const int32_t reach = (int32_t)std::min<int64_t>((int64_t)last_of(it) + pl->window - 1, last_pos);
-    queries(it.shard, it.pos0, last_pos);
-    it.n_tiles = tiles_now() * G;
-    if (it.n_tiles <= whole || reach == last_pos) {
-      put_ranges(&it, now);
-      tiles.push_back(it);
-      continue;
-    }
-    // The near queries in one part of all rows, the far ones, which see the sinks alone, in
-    // pieces of up to `normal` tiles: of several heads while their far queries are few.
-    const int32_t first_not = (pl->sinks - it.pos0 + own.apart - 1) / own.apart;  // rows that are sinks
-    ra::WinBwdSplit sp{0, it.shard, it.row0, it.row_end, parts, 0, 0, std::min(first_not, it.row_end - it.row0), {}};
-    ra::WinBwdItem near = it;
-    queries(it.shard, it.pos0, reach);
-    near.n_tiles = tiles_now() * G;
-    near.part = parts;
-    near.part_rows = 128;
-    parts += 2 * 128 * 128;
-    put_ranges(&near, now);
-    tiles.push_back(near);
-    sp.far = parts;
-    queries(it.shard, reach + 1, last_pos);
+  // The heads' queries `now` of a tile in pieces of up to `limit` streamed tiles, each with a
+  // part of `rows` rows: of several heads while these have few.  Returns the number of pieces.
+  std::vector<ra::WinBwdItem> pieces;
+  auto cut = [&](const ra::WinBwdItem& it, int32_t limit, int32_t rows) {
     const int32_t per_head = tiles_now();
-    const int heads = std::max(1, std::min(G, normal / std::max(per_head, 1)));
+    const int heads = std::max(1, std::min(G, limit / std::max(per_head, 1)));
     std::vector<ra::WinBwdRange> piece;
+    int32_t count = 0;
     auto flush = [&](int g0, int g1) {
-      ra::WinBwdItem far = it;
-      far.g0 = g0;
-      far.g1 = g1;
-      far.part = parts;
-      far.part_rows = sp.far_rows;
-      far.n_tiles = 0;
-      for (const ra::WinBwdRange& x : piece) far.n_tiles += ra::range_tiles64(x, str.tile) * (g1 - g0);
-      put_ranges(&far, piece);
-      tiles.push_back(far);
-      parts += 2 * (int64_t)sp.far_rows * 128;
-      ++sp.n_far;
+      ra::WinBwdItem x = it;
+      x.g0 = g0;
+      x.g1 = g1;
+      x.part = parts;
+      x.part_rows = rows;
+      x.n_tiles = 0;
+      for (const ra::WinBwdRange& y : piece) x.n_tiles += ra::range_tiles64(y, str.tile) * (g1 - g0);
+      put_ranges(&x, piece);
+      pieces.push_back(x);
+      parts += 2 * (int64_t)rows * 128;
+      ++count;
       piece.clear();
     };
     for (int g0 = 0; g0 < G; g0 += heads) {
       const int g1 = std::min(G, g0 + heads);
-      const int32_t most = std::max(1, normal / (g1 - g0));  // tiles of a piece, per head
+      const int32_t most = std::max(1, limit / (g1 - g0));  // tiles of a piece, per head
       int32_t have = 0;
       for (ra::WinBwdRange x : now)
         while (x.first < x.end) {
-          ra::WinBwdRange cut = x;
-          cut.end = std::min<int64_t>(x.end, (int64_t)x.row0 + (int64_t)(most - have) * str.tile);
-          piece.push_back(cut);
-          have += ra::range_tiles64(cut, str.tile);
-          x.first = x.row0 = cut.end;
+          ra::WinBwdRange part = x;
+          part.end = std::min<int64_t>(x.end, (int64_t)x.row0 + (int64_t)(most - have) * str.tile);
+          piece.push_back(part);
+          have += ra::range_tiles64(part, str.tile);
+          x.first = x.row0 = part.end;
           if (have == most) {
             flush(g0, g1);
             have = 0;
@@ -610,8 +601,45 @@ void build_win_bwd(ra_plan_s* pl, const ra::WinView& own, const ra::WinView& str
         }
       if (!piece.empty()) flush(g0, g1);
     }
+    return count;
+  };
+  std::vector<ra::WinBwdItem> all;
+  all.swap(tiles);
+  for (ra::WinBwdItem it : all) {
+    if (!small || it.n_tiles <= share + share / 2) {
+      tiles.push_back(it);
+      continue;
+    }
+    queries(it.shard, it.pos0, (int32_t)std::min<int64_t>((int64_t)last_of(it) + pl->window - 1, last_pos));
+    ra::WinBwdSplit sp{0, it.shard, it.row0, it.row_end, parts, 0, 0, 0, 0, 0};
+    sp.n_near = cut(it, share, 128);
+    sp.far = parts;
     splits.push_back(sp);
   }
+  for (ra::WinBwdItem it : sink_tiles) {
+    const int32_t reach = (int32_t)std::min<int64_t>((int64_t)last_of(it) + pl->window - 1, last_pos);
+    queries(it.shard, it.pos0, last_pos);
+    it.n_tiles = tiles_now() * G;
+    const bool far = it.n_tiles > whole && reach < last_pos;
+    if (!far && (!small || it.n_tiles <= share + share / 2)) {
+      put_ranges(&it, now);
+      tiles.push_back(it);
+      continue;
+    }
+    // The near queries in parts of all rows (one, unless the problem is small), the far ones,
+    // which see the sinks alone, in pieces of up to `normal` tiles.
+    const int32_t first_not = (pl->sinks - it.pos0 + own.apart - 1) / own.apart;  // rows that are sinks
+    ra::WinBwdSplit sp{0, it.shard, it.row0, it.row_end, parts, 0, 0, std::min(first_not, it.row_end - it.row0), 0, 0};
+    if (far) queries(it.shard, it.pos0, reach);
+    sp.n_near = cut(it, small ? share : INT32_MAX, 128);
+    sp.far = parts;
+    if (far) {
+      queries(it.shard, reach + 1, last_pos);
+      sp.n_far = cut(it, small ? share : normal, sp.far_rows);
+    }
+    splits.push_back(sp);
+  }
+  tiles.insert(tiles.end(), pieces.begin(), pieces.end());
   for (ra::WinBwdItem& it : tiles) it.pad2 = parts;
   emit(tiles, true);
   pl->n_win_bwd_kv = (int64_t)pl->win_bwd_items.size();

@@ -16,7 +16,8 @@
 // query of the sequence, up to hundreds of times what the other tiles meet, and would end
 // the launch alone: its far queries (past the window's reach) are cut into pieces the size
 // of an ordinary item, which leave their sums in fp32 for a last kernel to add in order.
-// (8k tokens, window 512, 4 sinks: 552 us with the tile as one item.)
+// (8k tokens, window 512, 4 sinks: 552 us with the tile as one item.)  Where there are few
+// tiles in all, the others' queries are cut in the same way.
 //
 // How (one persistent CTA per SM, 12 warps):
 //   warp 0     TMA producer: pass 0's own tiles (K, V) once per item, then 64-row tiles of
@@ -735,24 +736,31 @@ __global__ void __launch_bounds__(kPrepWarps * 32)
   }
 }
 
-// Adds the parts of the key tiles that were cut, in order: one CTA per row of a tile and of
-// dV or dK, one thread per column.
-__global__ void __launch_bounds__(128) win_bwd_join_kernel(const WinBwdParams P, const WinBwdSplit* __restrict__ splits) {
+// Adds the parts of the key tiles that were cut, in order: a CTA takes 8 rows of a tile's dV or
+// dK, a warp a row, a lane 4 columns.
+constexpr int kJoinRows = 8;
+__global__ void __launch_bounds__(kJoinRows * 32) win_bwd_join_kernel(const WinBwdParams P, const WinBwdSplit* __restrict__ splits) {
   const WinBwdSplit sp = splits[blockIdx.x];
-  const int row = blockIdx.y, which = blockIdx.z, col = threadIdx.x;
+  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5), which = blockIdx.z, lane = threadIdx.x & 31;
   const int i = sp.row0 + row;
   if (i >= sp.row_end || row >= P.own.tile) return;
-  float sum = P.parts[sp.near + ((int64_t)which * 128 + row) * 128 + col];
-  if (row < sp.far_rows) {
-    const float* far = P.parts + sp.far + ((int64_t)which * sp.far_rows + row) * 128 + col;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int64_t first, int rows, int n) {
+    const float4* from = reinterpret_cast<const float4*>(P.parts + first + ((int64_t)which * rows + row) * 128) + lane;
 #pragma unroll 8
-    for (int n = 0; n < sp.n_far; ++n) sum += far[(int64_t)n * 2 * sp.far_rows * 128];
-  }
+    for (int x = 0; x < n; ++x) {
+      const float4 y = from[(int64_t)x * 2 * rows * 32];
+      sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+    }
+  };
+  add(sp.near, 128, sp.n_near);
+  if (row < sp.far_rows) add(sp.far, sp.far_rows, sp.n_far);
   const int head_row = sp.shard * P.own.s_n + i;
   const int64_t out = (int64_t)sp.bh * P.seq + (P.own.stripe == 1 ? head_row
                                                                   : head_row % P.own.stripe * (P.seq / P.own.stripe) +
                                                                         head_row / P.own.stripe);
-  reinterpret_cast<__nv_bfloat16*>(which ? P.dk : P.dv)[out * 128 + col] = __float2bfloat16(sum);
+  reinterpret_cast<uint2*>(which ? P.dk : P.dv)[out * 32 + lane] =
+      make_uint2(ptx::pack_bf16x2(sum.x, sum.y), ptx::pack_bf16x2(sum.z, sum.w));
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -825,7 +833,7 @@ cudaError_t launch_win_bwd_prep(const WinBwdParams& prm, const void* o, const fl
 }
 
 cudaError_t launch_win_bwd_join(const WinBwdParams& prm, const WinBwdSplit* splits, int n, cudaStream_t stream) {
-  win_bwd_join_kernel<<<dim3((unsigned)n, 128, 2), 128, 0, stream>>>(prm, splits);
+  win_bwd_join_kernel<<<dim3((unsigned)n, 128 / kJoinRows, 2), kJoinRows * 32, 0, stream>>>(prm, splits);
   return cudaGetLastError();
 }
 

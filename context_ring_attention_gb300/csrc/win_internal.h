@@ -139,13 +139,13 @@ struct alignas(16) WinBwdItem {
   int64_t part;       // pass 0: where they go (float index in parts), -1: straight to dV, dK
   int64_t pad2;
 };
-// A key tile that was cut: one part of all its rows (128) from the near queries, n_far parts
-// of its sinks' rows from the others; each holds dV rows, then dK rows.
+// A key tile that was cut: n_near parts of all its rows (128) from the queries that may see any
+// of them, n_far parts of its sinks' rows from the others; each holds dV rows, then dK rows.
 struct alignas(16) WinBwdSplit {
   int32_t bh, shard, row0, row_end;
   int64_t near, far;
-  int32_t n_far, far_rows;
-  int32_t pad[2];
+  int32_t n_far, far_rows, n_near;
+  int32_t pad;
 };
 
 struct WinBwdParams {

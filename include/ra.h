@@ -289,7 +289,7 @@ ra_status ra_bwd(ra_plan_t plan, const void* q, const void* k, const void* v, co
  * ra_bwd_scratch_size -- bytes of the scratch buffer ra_bwd needs for this plan:
  * 512 bytes per 64-row block of every (batch, query head, shard), about
  * 8 * B * Hq * S bytes; for a windowed BF16 plan also the fp32 partial sums of the key
- * tiles that hold sinks.  Host only.  Errors: RA_ERR_INVALID_ARG (null arguments).
+ * tiles that are cut (those that hold sinks, and all of a small problem's).  Host only.  Errors: RA_ERR_INVALID_ARG (null arguments).
  */
 ra_status ra_bwd_scratch_size(ra_plan_t plan, int64_t* bytes);
 

@@ -138,6 +138,24 @@ def test_large_logits_rescale():
         assert_within(g_, w_, b_, name)
 
 
+@pytest.mark.parametrize("layout", oracle.LAYOUTS)
+@pytest.mark.parametrize("shape,mask", [((1, 1024, 8, 2, 4), (512, 4)), ((2, 810, 4, 1, 1), (253, 1)),
+                                        ((1, 2048, 4, 1, 2), (2048, 0)), ((1, 1500, 6, 1, 3), (400, 300)),
+                                        ((1, 2048, 16, 8, 2), (300, 5))], ids=str)
+def test_bf16_gradients_of_cut_tiles(shape, layout, mask):
+    """Few key tiles with long chains of queries, which are cut into pieces by heads and by
+    queries, with and without sinks; and passes side by side in more than one wave."""
+    plan, q, k, v, do, pos = _setup(shape, layout, *mask, seed=sum(shape) + mask[0])
+    o, lse = ra.ra_fwd(plan, q, k, v)
+    grads = ra.ra_bwd(plan, q, k, v, o, lse, do)
+    ra.ra_sync_status(plan)
+    want, bound = window_ref.backward(q, k, v, o, lse, do, pos, *mask, BF16_U)
+    for name, g_, w_, b_ in zip(("dQ", "dK", "dV"), grads, want, bound):
+        assert_within(g_, w_, b_, name)
+    for a, b in zip(grads, ra.ra_bwd(plan, q, k, v, o, lse, do)):
+        assert torch.equal(a, b)
+
+
 def test_long_window_one_head_pair():
     """32k tokens, 4096-token window: 512 rows spread over the sequence, all of dK and dV of
     the sinks (each gathers every later query)."""
