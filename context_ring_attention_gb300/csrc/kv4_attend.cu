@@ -32,8 +32,8 @@
 // second kernel in a fixed order.  A warp works on two blocks at a time: with one at a time
 // and four CTAs an SM (128 registers) its chains of dependent instructions, from the scores
 // to the weights, were what it waited for; two blocks (three CTAs an SM) took one sequence of
-// 1M tokens from 276 to 257 us and 16 new tokens of 64k from 180 to 136.  Two blocks in 128
-// registers: 276 us; two pairs a warp in shared memory for three: 260.
+// 1M tokens from 276 to 257 us (before the form for few rows) and 16 new tokens of 64k from 180
+// to 136.  Two blocks in 128 registers: 276 us; two pairs a warp in shared memory for three: 260.
 //
 // Measured (32 query and 8 key/value heads, d = 128, bf16, one new token): 1M tokens 234 us,
 // 1.34 GB of cache at 5.7 TB/s (0.84 of a plain copy's rate); 64k tokens 26.5 us; 32 sequences
@@ -256,9 +256,9 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
   const int r = lane >> 2, c = lane & 3;
   const int rq = kHalf ? r & 3 : r;  // query row of the fragments' column r
   const bool second = kHalf && c >= 2;  // this lane's columns are of the second block
-  // One sequence: the shares of a head next to each other (1M tokens 256 us, the heads of a
-  // share next to each other 262); several: the heads, whose blocks lie in the same pages (64
-  // sequences of up to 2k 37 against 39.5).
+  // One sequence: the shares of a head next to each other (1M tokens 2% faster than with the
+  // heads of a share next to each other); several: the heads, whose blocks lie in the same
+  // pages (64 sequences of up to 2k 6% faster).
   const bool one = !kInRow && P.t.batch == 1;
   const int cta = one ? blockIdx.x : blockIdx.y, ht = one ? blockIdx.y : blockIdx.x;
   const int tile = ht % P.tiles, h = ht / P.tiles;
