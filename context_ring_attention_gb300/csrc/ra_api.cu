@@ -353,7 +353,10 @@ int32_t add_ranges(ra_plan_s* pl, const ra::WinView& k, int p, int32_t minpos, i
   };
   for (int t = 0; t < N; ++t) {
     const int r = N == 1 ? 0 : (p - t + N) % N;
-    const ra::WinSpan sp = ra::win_span(k.layout, N, k.s_n, pl->window, pl->sinks, r, minpos, maxpos);
+    ra::WinSpan sp = ra::win_span(k.layout, N, k.s_n, pl->window, pl->sinks, r, minpos, maxpos);
+    // A range begins with a whole stripe: where the window's first stripe holds sinks, the two
+    // are one range, or these sinks would be in both.
+    if (sp.lo / k.stripe * k.stripe < sp.first) sp.first = sp.lo = 0;
     add(t, r, 0, sp.first);
     add(t, r, sp.lo, sp.hi);
   }

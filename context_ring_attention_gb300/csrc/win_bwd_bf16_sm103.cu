@@ -470,31 +470,13 @@ __device__ void run_elementwise(const WinBwdParams& P, const Ctl& c, uint8_t* sg
       for (int k = 0; k < it.n_ranges; ++k) {
         const WinBwdRange rg = range_at(P, rec, k);
         const int n = range_tiles64(rg, P.str.tile);
-        // Rows [lo, hi) of the streamed shard are live for this row, and (pass 1) those
-        // below sk, the sinks; of both the range's own.  Pass 0: the queries from the key's position on, up to
-        // window - 1 later, or all of them when the key is a sink.
-        int lo, hi, sk = 0;
-        if (kPass == 0) {
-          const int64_t far = (int64_t)my_pos + P.window - 1;
-          const int last = my_pos < P.sinks || far > P.seq - 1 ? P.seq - 1 : (int)far;
-          lo = view_rows_le(P.str, rg.r, my_pos - 1);
-          hi = view_rows_le(P.str, rg.r, last);
-        } else {
-          lo = view_rows_le(P.str, rg.r, my_pos - P.window);
-          hi = view_rows_le(P.str, rg.r, my_pos);
-          sk = view_rows_le(P.str, rg.r, P.sinks - 1);
-        }
-        lo = (lo > rg.first ? lo : rg.first) - rg.row0;
-        hi = (hi < rg.end ? hi : rg.end) - rg.row0;
-        sk = (sk < rg.end ? sk : rg.end) - rg.row0;
-        sk = sk < hi ? sk : hi;
-        const int from = rg.first - rg.row0;  // rows before it belong to another range
+        const WinBwdColumns own = range_columns<kPass>(P, rg, my_pos);
         for (int kt = 0; kt < n; ++kt, ++J) {
           if ((int)(J & 1u) != g) continue;
           // Columns [c_lo, c_hi) and [c_f, c_s) of this tile are live for this row.
           const int y = kt * P.str.tile;
-          const int c_hi = hi - y < P.str.tile ? hi - y : P.str.tile, c_lo = lo - y;
-          const int c_s = sk - y < c_hi ? sk - y : c_hi, c_f = from - y;
+          const int c_hi = own.hi - y < P.str.tile ? own.hi - y : P.str.tile, c_lo = own.lo - y;
+          const int c_s = own.sk - y < c_hi ? own.sk - y : c_hi, c_f = own.from - y;
           const bool ok = wait_bar(c, c.bar(kSFull + (int)(J % NB)), (J / NB) & 1u, kStatusTimeoutSoftmax);
           if (!__all_sync(0xffffffffu, ok)) return;
           ptx::tc_fence_after();

@@ -7,7 +7,8 @@
 // folded tile by tile with the running maximum and sum of Module 23, "The Math: One
 // Block at a Time".  The planner lists, for every pair of query tiles, the key rows
 // that some query of it sees, shard by shard in ring order (win_internal.h); a key
-// tile starts at the first row that is seen, not at a multiple of 128.
+// tile starts at the first row that is seen (striped layouts walked by position: at the
+// start of its stripe), not at a multiple of 128.
 //
 // A windowed item meets few key tiles (9 for a 1024-token window, against hundreds of
 // a full causal prefix), so what matters is the seam between two items.  The stream of
@@ -513,25 +514,14 @@ __device__ void run_softmax(const WinParams& P, const Ctl& c, uint8_t* stage, co
       const bool seg_end = k == xn - 1 || (kPartials && range_at(P, rec, k + 1).step != rg.step);
       if (kPartials)
         for (; next_part < rg.step; ++next_part) store_empty(P, valid, out_row, next_part - P.step_lo);
-      // Of the range's rows the query sees those below sk and [lo, hi): rows at positions
-      // up to its own, and not up to window positions before it unless they are sinks.
-      const int rows = rg.end - rg.row0;
-      const int d_hi = my_pos - rg.pos0, d_lo = d_hi - P.window, d_sk = P.sinks - 1 - rg.pos0;
-      int hi = d_hi + 1, lo = d_lo + 1, sk = d_sk + 1;
-      if (P.k.apart > 1) {
-        hi = d_hi < 0 ? 0 : d_hi / P.k.apart + 1;
-        lo = d_lo < 0 ? 0 : d_lo / P.k.apart + 1;
-        sk = d_sk < 0 ? 0 : d_sk / P.k.apart + 1;
-      }
-      hi = hi < rows ? hi : rows;
-
+      const WinColumns seen = range_columns(rg, P.k.apart, P.window, P.sinks, my_pos);
       const int n = range_tiles(rg, P.k.tile);
       for (int kt = 0; kt < n; ++kt) {
         const int y = kt * P.k.tile;
         const bool last = seg_end && kt == n - 1;
         // columns [c_lo, c_hi), and those below c_s, are seen
-        const int c_hi = hi - y < P.k.tile ? hi - y : P.k.tile, c_lo = lo - y;
-        const int c_s = sk - y < c_hi ? sk - y : c_hi;
+        const int c_hi = seen.hi - y < P.k.tile ? seen.hi - y : P.k.tile, c_lo = seen.lo - y;
+        const int c_s = seen.sk - y < c_hi ? seen.sk - y : c_hi;
         const bool full = c_hi >= kTileRows && (c_lo <= 0 || c_s >= kTileRows);
 
         bool ok = wait_bar(c, c.bar(kSFull + g), sj & 1u, kStatusTimeoutSoftmax);

@@ -95,6 +95,25 @@ RA_HD int32_t range_tiles(const WinRange& rg, int32_t tile) {
   return tile == kTileRows ? (rows + kTileRows - 1) / kTileRows : (rows + tile - 1) / tile;
 }
 
+// The keys of a range that the query at position pos sees, as columns counted from the range's
+// first row: those below sk, and [lo, hi) -- rows at positions up to its own, and not up to
+// window positions before it unless they are sinks.
+struct WinColumns {
+  int32_t lo, hi, sk;
+};
+RA_HD WinColumns range_columns(const WinRange& rg, int32_t apart, int32_t window, int32_t sinks, int32_t pos) {
+  const int32_t rows = rg.end - rg.row0;
+  const int32_t d_hi = pos - rg.pos0, d_lo = d_hi - window, d_sk = sinks - 1 - rg.pos0;
+  WinColumns c{d_lo + 1, d_hi + 1, d_sk + 1};
+  if (apart > 1) {
+    c.hi = d_hi < 0 ? 0 : d_hi / apart + 1;
+    c.lo = d_lo < 0 ? 0 : d_lo / apart + 1;
+    c.sk = d_sk < 0 ? 0 : d_sk / apart + 1;
+  }
+  c.hi = c.hi < rows ? c.hi : rows;
+  return c;
+}
+
 struct WinParams {
   int32_t batch, heads_q, heads_kv, group, head_dim;
   WinView q, k;
@@ -168,6 +187,33 @@ struct WinBwdParams {
   const WinBwdRange* ranges;
   uint32_t* status;
 };
+// The rows of a range that are live for the own row at position pos, counted from the range's
+// row0: [lo, hi) and [from, sk), of both the range's own.  Pass 0: the queries from the key's
+// position on, up to window - 1 later, or all of them when the key is a sink.  Pass 1: the
+// window's keys, and the sinks.
+struct WinBwdColumns {
+  int32_t lo, hi, sk, from;  // (rows before `from` belong to another range)
+};
+template <int kPass>
+RA_HD WinBwdColumns range_columns(const WinBwdParams& P, const WinBwdRange& rg, int32_t pos) {
+  WinBwdColumns c{0, 0, 0, 0};
+  if (kPass == 0) {
+    const int64_t far = (int64_t)pos + P.window - 1;
+    const int32_t last = pos < P.sinks || far > P.seq - 1 ? P.seq - 1 : (int32_t)far;
+    c.lo = view_rows_le(P.str, rg.r, pos - 1);
+    c.hi = view_rows_le(P.str, rg.r, last);
+  } else {
+    c.lo = view_rows_le(P.str, rg.r, pos - P.window);
+    c.hi = view_rows_le(P.str, rg.r, pos);
+    c.sk = view_rows_le(P.str, rg.r, P.sinks - 1);
+  }
+  c.lo = (c.lo > rg.first ? c.lo : rg.first) - rg.row0;
+  c.hi = (c.hi < rg.end ? c.hi : rg.end) - rg.row0;
+  c.sk = (c.sk < rg.end ? c.sk : rg.end) - rg.row0;
+  c.sk = c.sk < c.hi ? c.sk : c.hi;
+  c.from = rg.first - rg.row0;
+  return c;
+}
 // Block of scalars of streamed tile `tile` of a shard (bh = b*Hq + h).
 RA_HD int64_t win_scalar_block(const WinBwdParams& P, int64_t bh, int shard, int tile) {
   return (bh * P.str.shards + shard) * P.blocks + tile;

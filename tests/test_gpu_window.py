@@ -156,6 +156,24 @@ def test_bf16_gradients_of_cut_tiles(shape, layout, mask):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("shape,mask", [((1, 900, 4, 2, 3), (122, 4)), ((1, 512, 4, 2, 8), (124, 4)),
+                                        ((2, 512, 3, 1, 8), (122, 1)), ((1, 512, 2, 2, 4), (126, 1)),
+                                        ((1, 600, 3, 1, 100), (150, 30))], ids=str)
+def test_first_stripe_of_the_window_holds_the_last_sink(shape, mask):
+    """Striped shards walked by position, where a range of keys begins with its stripe: a sink
+    in the window's first stripe enters once."""
+    plan, q, k, v, do, pos = _setup(shape, "striped", *mask, seed=sum(shape) + mask[0])
+    o, lse = ra.ra_fwd(plan, q, k, v)
+    grads = ra.ra_bwd(plan, q, k, v, o, lse, do)
+    ra.ra_sync_status(plan)
+    ow, lw, ob, lb = window_ref.forward(q, k, v, pos, *mask, BF16_U)
+    assert_within(o, ow, ob, "O")
+    assert_within(lse, lw, lb, "LSE")
+    want, bound = window_ref.backward(q, k, v, o, lse, do, pos, *mask, BF16_U)
+    for name, g_, w_, b_ in zip(("dQ", "dK", "dV"), grads, want, bound):
+        assert_within(g_, w_, b_, name)
+
+
 def test_long_window_one_head_pair():
     """32k tokens, 4096-token window: 512 rows spread over the sequence, all of dK and dV of
     the sinks (each gathers every later query)."""
