@@ -161,16 +161,21 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // bf16 rows: low is the minimum itself, so that no quotient lies below 0, and the scale's
 // rounding takes none above 15.03.  The quotient is taken a little low (2^-20 of itself,
-// more than its error), which leaves one question, whether d reaches the border above the
-// code, and that is answered exactly by r = d - c * scale, where d is exact: checked, and
-// otherwise (exponents more than 16 apart) left to the path above.  Ties are common among
+// more than its error), which leaves one question, whether x - low reaches the border above
+// the code.  It is answered by r = d - c * scale, an exact difference, where d = x - low has
+// not been rounded across a border.  d + low == x says so where |low| >= |x| or low <= 0: d is
+// x - low itself, or rounded away from low; between the two lies no number of x's 8 bits or of
+// a border's 13, except x, which x - low reaches as d does.  A positive low may be lost without
+// a trace, d = x, where x itself is a border that x - low does not reach: it is below 2^-24 * x
+// then, and x below 16 scales, so that groups of 0 < low < 2^-16 * scale, and values that fail
+// the test (exponents more than 16 apart), are left to the path above.  Ties are common among
 // bf16 values and cost nothing here.
 __device__ __forceinline__ uint32_t codes_bf16(const float (&x)[8], float low, float scale, float inv) {
   const float half = 0.5f * scale, under = inv * (1.f - 0x1p-20f);
   const float2 low2 = {low, low}, under2 = {under, under}, scale2 = {scale, scale}, round2 = {kRound, kRound};
   const float2 minus2 = {-1.f, -1.f};
   uint32_t word = 0;
-  bool exact = true;
+  bool exact = !(low > 0.f && low < scale * 0x1p-16f);
 #pragma unroll
   for (int i = 6; i >= 0; i -= 2) {  // two at a time, by the paired fp32 instructions
     const float2 xi = {x[i], x[i + 1]};

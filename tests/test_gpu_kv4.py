@@ -1,6 +1,9 @@
 """GPU tests of the 4-bit cache: bytes written, values read back, attention over it, and a
 sequence continued from a windowed prompt, against the plain form in kv4_ref.py."""
 
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
@@ -129,6 +132,36 @@ def test_float32_codes_next_to_borders():
     ra.ra_kv4_write(kv, cache, torch.from_numpy(x).cuda(), torch.from_numpy(x).cuda(), _i32([[0]]), _i32([0]))
     ra.ra_kv4_sync_status(kv)
     assert np.array_equal(cache.cpu().numpy().reshape(ref.bytes.shape), ref.bytes)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_minima_far_below_the_values(dtype, d):
+    """Values on the border of two codes above a minimum so small that x - low rounds to x: the
+    quotient lies below the border for a positive minimum, and above it for a negative one."""
+    rows = []
+    for scale in (1.0, 0.75, 129 / 128 * 2.0 ** 40, 2.0 ** -60):
+        for e in (-16, -18, -20, -23, -24, -25, -30, -45, -126):
+            for sign in (1, -1):
+                g = np.full(32, sign * 1.5 * 2.0 ** e * (scale if e > -126 else 1))
+                g[1:16] = (np.arange(15) + 0.5) * scale  # borders (those that the dtype holds)
+                g[16:31] = np.arange(1, 16) * scale
+                rows.append(np.tile(g, d // 32))
+    x = torch.from_numpy(np.stack(rows)[None, None]).to(DT[dtype]).double().numpy()
+    t = x.shape[2]
+    kv = ra.ra_kv4_plan(1, 80, 1, 1, d, dtype=dtype)
+    cache = torch.full((ra.ra_kv4_cache_size(kv),), 0xAB, dtype=torch.uint8, device="cuda")
+    ra.ra_kv4_write(kv, cache, _dev(x, dtype), _dev(x, dtype), _i32([[0]]), _i32([0]))
+    got = ra.ra_kv4_read(kv, cache, _i32([[0]]), _i32([0]), t)
+    ra.ra_kv4_sync_status(kv)
+    _, scale, low = kv4_ref.quantise(x)  # (the parameters; a difference in 64 bits may round as well)
+    exact = np.empty(x.shape, np.int64)
+    for at in np.ndindex(x.shape):
+        s, l = (Fraction(float(p[at[:-1] + (at[-1] // 32,)])) for p in (scale, low))
+        exact[at] = min(max(math.floor((Fraction(float(x[at])) - l) / s + Fraction(1, 2)), 0), 15)
+    for values in got:  # a value is nearest to its own code, whatever the dtype's rounding
+        codes = (values.double().cpu().numpy() - np.repeat(low, 32, -1)) / np.repeat(scale, 32, -1)
+        assert np.array_equal(np.rint(codes), exact)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
