@@ -596,6 +596,11 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
           for (int i = 0; i < 4; ++i)
             load_words<G / 2>(base[kHalf ? y : n] + F::kOffV + vt[i] * F::kCodeBytes + r * (2 * G), vw[y][i]);
         const float(&p)[4] = s[n];
+        // the middles meet the weights without their 2^kShift: their sums stay as far below
+        // float32's largest number as the values do
+        const float2 down = {two_to(-60), two_to(-60)};
+        const float2 p01 = ptx::mul2(make_float2(p[0], p[1]), down), p23 = ptx::mul2(make_float2(p[2], p[3]), down);
+        const float p1[4] = {p01.x, p01.y, p23.x, p23.y};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const float s0 = scale_of(vp0[g]), s1 = scale_of(vp1[g]);
@@ -606,11 +611,11 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (!((seen >> (4 * n + e)) & 1u)) w[e] = 0.f;
-              else pm[g][e & 1] = fmaf(p[e], mid[e], pm[g][e & 1]);
+              else pm[g][e & 1] = fmaf(p1[e], mid[e], pm[g][e & 1]);
             }
           } else {
-            pm[g][0] = fmaf(p[0], m0, fmaf(p[2], m1, pm[g][0]));
-            pm[g][1] = fmaf(p[1], m0, fmaf(p[3], m1, pm[g][1]));
+            pm[g][0] = fmaf(p1[0], m0, fmaf(p1[2], m1, pm[g][0]));
+            pm[g][1] = fmaf(p1[1], m0, fmaf(p1[3], m1, pm[g][1]));
           }
           uint32_t w0[kTerms], w1[kTerms], b2[kTerms][2];
           split_pair<kTerms>(w[0], w[1], w0);
@@ -689,10 +694,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
     for (int e = 0; e < 2; ++e)
       // 2^-kShift brings p back, and another 2^133 (2^129 for 16 n) the codes
       *reinterpret_cast<float4*>(&sm_o[warp][2 * c + e][32 * g + 4 * r]) =
-          make_float4(fmaf(o[g][0][e], two_to(73), pm[g][e] * two_to(-60)),
-                      fmaf(o[g][0][e + 2], two_to(69), pm[g][e] * two_to(-60)),
-                      fmaf(o[g][1][e], two_to(73), pm[g][e] * two_to(-60)),
-                      fmaf(o[g][1][e + 2], two_to(69), pm[g][e] * two_to(-60)));
+          make_float4(fmaf(o[g][0][e], two_to(73), pm[g][e]), fmaf(o[g][0][e + 2], two_to(69), pm[g][e]),
+                      fmaf(o[g][1][e], two_to(73), pm[g][e]), fmaf(o[g][1][e + 2], two_to(69), pm[g][e]));
   __syncthreads();
   for (int at = threadIdx.x; at < kRows * D; at += kWarps * 32) {
     const int row = at / D, ch = at % D;

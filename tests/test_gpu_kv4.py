@@ -524,3 +524,25 @@ def test_shared_in_a_row(dtype, window, sinks, t, hq, hk):
     kv, cache, ref, table = _filled(rng, lengths, 48, hk, 128, dtype, heads_q=hq, window=window, sinks=sinks)
     assert ra.ra_kv4_attend_scratch_size(kv, 5, t, table.shape[1]) > 0
     _check_attend(kv, cache, ref, table, lengths, hq, t, 128, dtype, window, sinks, rng)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths,hq", [([4], 2), ([300, 9], 12), ([5000], 2)], ids=str)
+@pytest.mark.parametrize("size", [1e19, 1e20, 1e25])
+def test_values_far_from_zero(dtype, lengths, hq, size):
+    """Value groups of one large constant (scale 0), as many of equal weight as sum past
+    float32 when a weight carries 2^60, beside groups of ordinary size and of a large scale."""
+    rng = np.random.default_rng(len(lengths))
+    d, hk = 64, 2
+    kv, cache, ref, table = _filled(rng, lengths, 32, hk, d, dtype, heads_q=hq)
+    t = max(lengths)
+    k = np.repeat(_rows(rng, len(lengths), hk, 1, d, dtype), t, 2)  # keys alike: equal weights
+    v = _rows(rng, len(lengths), hk, t, d, dtype)
+    # (a bf16 number: the float32 1e25 is 2^74 above its group's low, which makes a scale of
+    # 2^70.6, and the scales that the attention takes end at 2^58)
+    v[..., :32] = kv4_ref.bf16(size)
+    v[:, 1, :, 32:] *= 2.0 ** 50
+    v = torch.from_numpy(v).to(DT[dtype]).double().numpy()
+    ref.write(k, v, table, [0] * len(lengths), lengths)
+    ra.ra_kv4_write(kv, cache, _dev(k, dtype), _dev(v, dtype), _i32(table), _i32([0] * len(lengths)), _i32(lengths))
+    _check_attend(kv, cache, ref, table, lengths, hq, 1, d, dtype, 0, 0, rng)
