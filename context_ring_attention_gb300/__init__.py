@@ -9,9 +9,9 @@ The functions keep the C names (``ra_plan``, ``ra_plan_window``, ``ra_plan_tile_
 ``ra_kv4_plan``, ``ra_kv4_cache_size``, ``ra_kv4_write``, ``ra_kv4_read``,
 ``ra_kv4_attend``, ``ra_kv4_attend_scratch_size``, ``ra_kv4_sync_status``).
 This module only marshals arguments: PyTorch supplies device memory and the
-current stream, every step of the computation runs in the library's CUDA
-kernels, and there is no fallback -- if libra.so is missing or cannot be loaded,
-every call raises.  Because the library sees only pointers, every tensor a caller
+current stream (outputs and scratch made for a call with a ``stream`` of its own belong to
+that stream), every step of the computation runs in the library's CUDA kernels, and there is
+no fallback -- if libra.so is missing or cannot be loaded, every call raises.  Because the library sees only pointers, every tensor a caller
 passes (outputs and scratch included) is checked here for its exact shape, dtype,
 contiguity and device before anything is launched.
 
@@ -314,23 +314,25 @@ def ra_fwd(plan, q, k, v, o=None, lse=None, partials=False, o_parts=None, lse_pa
     _check_qkv(plan, q=q, k=k, v=v)
     lib = load_library()
     if partials:
-        if o_parts is None:
-            o_parts = torch.empty((N, B, Hq, S, d), dtype=torch.float32, device=q.device)
-        if lse_parts is None:
-            lse_parts = torch.empty((N, B, Hq, S), dtype=torch.float32, device=q.device)
+        with _alloc_on(stream):
+            if o_parts is None:
+                o_parts = torch.empty((N, B, Hq, S, d), dtype=torch.float32, device=q.device)
+            if lse_parts is None:
+                lse_parts = torch.empty((N, B, Hq, S), dtype=torch.float32, device=q.device)
         _need("o_parts", o_parts, (N, B, Hq, S, d), torch.float32, q.device)
         _need("lse_parts", lse_parts, (N, B, Hq, S), torch.float32, q.device)
         _check(lib.ra_fwd(plan.handle, _ptr(q), _ptr(k), _ptr(v), None, None, _ptr(o_parts),
                           _ptr(lse_parts), _stream(stream)))
         return o_parts, lse_parts
-    if o is None:
-        o = torch.empty_like(q)
-    else:
+    if o is not None:
         _need_like("o", o, q.shape, q.dtype, q.device)
-    if lse is None:
-        lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
-    else:
+    if lse is not None:
         _need_like("lse", lse, (B, Hq, S), torch.float32, q.device)
+    with _alloc_on(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
     _check(lib.ra_fwd(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), None, None,
                       _stream(stream)))
     return o, lse
@@ -350,10 +352,11 @@ def ra_merge_partials(o_parts, lse_parts, out_dtype=None, o=None, lse=None, stre
     _on_current_device("o_parts", o_parts)
     _same_device(o_parts.device, lse_parts=lse_parts)
     out_dtype = out_dtype or torch.float32
-    if o is None:
-        o = torch.empty(o_parts.shape[1:], dtype=out_dtype, device=o_parts.device)
-    if lse is None:
-        lse = torch.empty(lse_parts.shape[1:], dtype=torch.float32, device=o_parts.device)
+    with _alloc_on(stream):
+        if o is None:
+            o = torch.empty(o_parts.shape[1:], dtype=out_dtype, device=o_parts.device)
+        if lse is None:
+            lse = torch.empty(lse_parts.shape[1:], dtype=torch.float32, device=o_parts.device)
     if o.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("o must be float32 or bfloat16")
     _need("o", o, o_parts.shape[1:], o.dtype, o_parts.device)
@@ -378,7 +381,8 @@ def ra_layout_perm(x, layout, n_shards, inverse=False, seq_dim=None, out=None, s
     outer = int(np.prod(x.shape[:seq_dim], dtype=np.int64)) if seq_dim else 1
     row_bytes = int(np.prod(x.shape[seq_dim + 1:], dtype=np.int64)) * x.element_size()
     if out is None:
-        out = torch.empty_like(x)
+        with _alloc_on(stream):
+            out = torch.empty_like(x)
     _need("out", out, x.shape, x.dtype, x.device)
     _check(load_library().ra_layout_perm(_layout(layout), seq, int(n_shards), int(bool(inverse)), outer,
                                          row_bytes, _ptr(x), _ptr(out), _stream(stream)))
@@ -419,10 +423,11 @@ def ra_fwd_static(batch, seq, heads_q, heads_kv, n_shards, layout, causal, q, k,
         raise ValueError("q must be a CUDA tensor")
     _need("k", k, (batch, heads_kv, seq, 128), torch.bfloat16, q.device)
     _need("v", v, (batch, heads_kv, seq, 128), torch.bfloat16, q.device)
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((batch, heads_q, seq), dtype=torch.float32, device=q.device)
+    with _alloc_on(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((batch, heads_q, seq), dtype=torch.float32, device=q.device)
     _need("o", o, q.shape, q.dtype, q.device)
     _need("lse", lse, (batch, heads_q, seq), torch.float32, q.device)
     prob = _Problem(int(batch), int(seq), int(heads_q), int(heads_kv), 128, int(n_shards), _layout(layout),
@@ -449,10 +454,11 @@ def ra_fwd_step(plan, step, q, k_blk, v_blk, o_part=None, lse_part=None, stream=
     B, Hq, S, d = pb["batch"], pb["heads_q"], pb["seq"], pb["head_dim"]
     _check_qkv(plan, q=q, k_blk=k_blk, v_blk=v_blk)
     _same_device(q.device, k_blk=k_blk, v_blk=v_blk)
-    if o_part is None:
-        o_part = torch.empty((B, Hq, S, d), dtype=torch.float32, device=q.device)
-    if lse_part is None:
-        lse_part = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
+    with _alloc_on(stream):
+        if o_part is None:
+            o_part = torch.empty((B, Hq, S, d), dtype=torch.float32, device=q.device)
+        if lse_part is None:
+            lse_part = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
     _need("o_part", o_part, (B, Hq, S, d), torch.float32, q.device)
     _need("lse_part", lse_part, (B, Hq, S), torch.float32, q.device)
     _check(load_library().ra_fwd_step(plan.handle, int(step), _ptr(q), _ptr(k_blk), _ptr(v_blk), _ptr(o_part),
@@ -464,10 +470,11 @@ def ra_ring_rotate(plan, k_src, v_src, k_dst=None, v_dst=None, stream=None):
     """Pass every shard's K/V block on to the next shard -> (k_dst, v_dst)."""
     import torch
     _check_qkv(plan, k_src=k_src, v_src=v_src)
-    if k_dst is None:
-        k_dst = torch.empty_like(k_src)
-    if v_dst is None:
-        v_dst = torch.empty_like(v_src)
+    with _alloc_on(stream):
+        if k_dst is None:
+            k_dst = torch.empty_like(k_src)
+        if v_dst is None:
+            v_dst = torch.empty_like(v_src)
     _check_qkv(plan, k_dst=k_dst, v_dst=v_dst)
     _same_device(k_src.device, v_src=v_src, k_dst=k_dst, v_dst=v_dst)
     _check(load_library().ra_ring_rotate(plan.handle, _ptr(k_src), _ptr(v_src), _ptr(k_dst), _ptr(v_dst),
@@ -487,19 +494,20 @@ def ra_ring_fwd(plan, q, k, v, o=None, lse=None, k_buf=None, v_buf=None, o_parts
     pb = plan.problem
     B, Hq, S, d, N = pb["batch"], pb["heads_q"], pb["seq"], pb["head_dim"], pb["n_shards"]
     _check_qkv(plan, q=q, k=k, v=v)
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
-    if N > 1:
-        if k_buf is None:
-            k_buf = torch.empty((2,) + tuple(k.shape), dtype=k.dtype, device=k.device)
-        if v_buf is None:
-            v_buf = torch.empty((2,) + tuple(v.shape), dtype=v.dtype, device=v.device)
-    if o_parts is None:
-        o_parts = torch.empty((N, B, Hq, S, d), dtype=torch.float32, device=q.device)
-    if lse_parts is None:
-        lse_parts = torch.empty((N, B, Hq, S), dtype=torch.float32, device=q.device)
+    with _alloc_on(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
+        if N > 1:
+            if k_buf is None:
+                k_buf = torch.empty((2,) + tuple(k.shape), dtype=k.dtype, device=k.device)
+            if v_buf is None:
+                v_buf = torch.empty((2,) + tuple(v.shape), dtype=v.dtype, device=v.device)
+        if o_parts is None:
+            o_parts = torch.empty((N, B, Hq, S, d), dtype=torch.float32, device=q.device)
+        if lse_parts is None:
+            lse_parts = torch.empty((N, B, Hq, S), dtype=torch.float32, device=q.device)
     _same_device(q.device, k=k, v=v)
     _need("o", o, q.shape, q.dtype, q.device)
     _need("lse", lse, (B, Hq, S), torch.float32, q.device)
@@ -528,25 +536,26 @@ def ra_bwd(plan, q, k, v, o, lse, dout, dq=None, dk=None, dv=None, scratch=None,
     _check_qkv(plan, q=q, k=k, v=v)
     _check_qkv(plan, q=o)
     _check_qkv(plan, q=dout)
-    if dq is None:
-        dq = torch.empty_like(q)
-    else:
+    if dq is not None:
         _need_like("dq", dq, q.shape, q.dtype, q.device)
-    if dk is None:
-        dk = torch.empty_like(k)
-    else:
+    if dk is not None:
         _need_like("dk", dk, k.shape, k.dtype, k.device)
-    if dv is None:
-        dv = torch.empty_like(v)
-    else:
+    if dv is not None:
         _need_like("dv", dv, v.shape, v.dtype, v.device)
-    if scratch is None:
-        with _alloc_on(stream):
-            scratch = torch.empty(ra_bwd_scratch_size(plan) // 4, dtype=torch.float32, device=q.device)
-    elif (scratch.numel() * scratch.element_size() < ra_bwd_scratch_size(plan) or scratch.dtype != torch.float32
-          or not scratch.is_contiguous() or scratch.device != q.device):
+    if scratch is not None and (scratch.numel() * scratch.element_size() < ra_bwd_scratch_size(plan)
+                                or scratch.dtype != torch.float32 or not scratch.is_contiguous()
+                                or scratch.device != q.device):
         raise ValueError("scratch must be a contiguous float32 tensor of at least ra_bwd_scratch_size(plan) "
                          "bytes on the device of q")
+    with _alloc_on(stream):
+        if dq is None:
+            dq = torch.empty_like(q)
+        if dk is None:
+            dk = torch.empty_like(k)
+        if dv is None:
+            dv = torch.empty_like(v)
+        if scratch is None:
+            scratch = torch.empty(ra_bwd_scratch_size(plan) // 4, dtype=torch.float32, device=q.device)
     _need_like("lse", lse, (B, Hq, S), torch.float32, q.device)
     _check(load_library().ra_bwd(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout),
                                  _ptr(dq), _ptr(dk), _ptr(dv), _ptr(scratch), _stream(stream)))
@@ -566,10 +575,11 @@ def ra_allgather_kv(plan, k, v, k_all=None, v_all=None, stream=None):
     """Gather every shard's K/V block into one natural-order copy -> (k_all, v_all)."""
     import torch
     _check_qkv(plan, k=k, v=v)
-    if k_all is None:
-        k_all = torch.empty_like(k)
-    if v_all is None:
-        v_all = torch.empty_like(v)
+    with _alloc_on(stream):
+        if k_all is None:
+            k_all = torch.empty_like(k)
+        if v_all is None:
+            v_all = torch.empty_like(v)
     _check_qkv(plan, k_all=k_all, v_all=v_all)
     _same_device(k.device, v=v, k_all=k_all, v_all=v_all)
     _check(load_library().ra_allgather_kv(plan.handle, _ptr(k), _ptr(v), _ptr(k_all), _ptr(v_all),
@@ -582,10 +592,11 @@ def ra_fwd_gathered(plan, q, k_all, v_all, o=None, lse=None, stream=None):
     import torch
     pb = plan.problem
     _check_qkv(plan, q=q, k_all=k_all, v_all=v_all)
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((pb["batch"], pb["heads_q"], pb["seq"]), dtype=torch.float32, device=q.device)
+    with _alloc_on(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((pb["batch"], pb["heads_q"], pb["seq"]), dtype=torch.float32, device=q.device)
     _same_device(q.device, k_all=k_all, v_all=v_all)
     _need("o", o, q.shape, q.dtype, q.device)
     _need("lse", lse, (pb["batch"], pb["heads_q"], pb["seq"]), torch.float32, q.device)
@@ -614,7 +625,8 @@ def ra_ulysses_a2a(x, layout, n_shards, direction, out=None, stream=None):
         out_shape = (B, H, S) + tuple(x.shape[4:])
     row_bytes = int(np.prod(x.shape[3 if direction == 0 else 4:], dtype=np.int64)) * x.element_size()
     if out is None:
-        out = torch.empty(out_shape, dtype=x.dtype, device=x.device)
+        with _alloc_on(stream):
+            out = torch.empty(out_shape, dtype=x.dtype, device=x.device)
     _need("out", out, out_shape, x.dtype, x.device)
     _check(load_library().ra_ulysses_a2a(int(direction), _layout(layout), int(S), N, int(B), int(H), row_bytes,
                                          _ptr(x), _ptr(out), _stream(stream)))
