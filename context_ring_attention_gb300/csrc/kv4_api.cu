@@ -308,6 +308,11 @@ ra_status ra_kv4_sync_status(ra_kv4_t kv, void* stream) {
   if (e != cudaSuccess) return fail(RA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
   if (word == 0) return ok();
   cudaMemset(kv->d_status, 0, sizeof(word));
+  if (word & ra::kStatusBounds) {
+    char msg[200];
+    const ra_status code = ra::status_word_error(word, msg, sizeof(msg));
+    return fail(code, "%s", msg);
+  }
   return fail(RA_ERR_INVALID_ARG, "a page index, position, length or count was out of range");
 }
 

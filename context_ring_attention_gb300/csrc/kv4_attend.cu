@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
   const Share share = share_of<kInRow>(P, cta);
   int32_t off = share.off, rest = share.n;
   for (int b = share.b; !kInRow || rest > 0; ++b) {
+  RA_BOUNDS(P.t.status, b >= 0 && b < P.t.batch && h < P.t.heads_kv && share.off >= 0 && share.n >= 0, 95);
   bool bad_length;
   const int32_t len = length_of(P, b, bad_length);
   if (bad_length && threadIdx.x == 0) atomicOr(P.t.status, kKv4StatusRange);
@@ -405,6 +406,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
     if (left == 0) {
       const int32_t block = block_at(fx);
       const int32_t page_at = block / bpp, in_page = block - page_at * bpp;
+      RA_BOUNDS(P.t.status, block >= 0 && page_at < P.t.width, 96);
       const int32_t page = __ldg(table + page_at);
       src = of_head + page * page_bytes + (int64_t)in_page * F::kBytes;
       left = bpp - in_page;
@@ -416,6 +418,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
     }
     if (src != nullptr) {
       bad &= ~(1u << at);
+      RA_BOUNDS(P.t.status, in_pool<D>(P.t, src - lane * 16) && at >= 0 && at < 2 * kPairs, 97);
       const uint32_t dst = mine_at + at * F::kBytes + lane * 16;
 #pragma unroll
       for (int i = 0; i * 512 < F::kBytes; ++i)
@@ -718,10 +721,12 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
       }
     if (!(begins && ends)) {
       const int64_t part = ((int64_t)ht * P.slots + cta) * 2 + begins;
+      RA_BOUNDS(P.t.status, P.part_o != nullptr && part >= 0 && part < (int64_t)P.t.heads_kv * P.tiles * P.slots * 2, 98);
       P.part_o[(part * kTile + row) * D + ch] = acc;
       if (ch == 0) P.part_ml[part * kTile + row] = make_float2(mx, sum);
     } else if (row0 + row < n_rows) {
       const int64_t out = ((int64_t)b * P.heads_q + (int64_t)h * P.group) * P.rows + row0 + row;
+      RA_BOUNDS(P.t.status, out >= 0 && out < (int64_t)P.t.batch * P.heads_q * P.rows, 99);
       static_cast<T*>(P.o)[out * D + ch] = (T)(sum == 0.f ? 0.f : acc / sum);
       if (ch == 0 && P.lse != nullptr) P.lse[out] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
     }
@@ -753,6 +758,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Atte
   const int tile = unit % P.tiles, bh = unit / P.tiles, b = bh / P.t.heads_kv;
   if (tile * kTile + row >= P.group * P.rows) return;
   const int2 share = P.t.batch == 1 ? make_int2(0, P.slots - 1) : P.shares[b];  // (first slot, last slot)
+  RA_BOUNDS(P.t.status, b < P.t.batch && share.x >= 0 && share.x <= share.y && share.y < P.slots, 100);
   const int n = share.y - share.x + 1;
   if (n == 1) return;  // (that CTA wrote the row)
   // a slot has two parts: of a sequence that it has the beginning of the second
@@ -798,6 +804,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Atte
   sums[part][at] = acc;
   __syncthreads();
   const int64_t out = (int64_t)bh * P.group * P.rows + tile * kTile + row;
+  RA_BOUNDS(P.t.status, out >= 0 && out < (int64_t)P.t.batch * P.heads_q * P.rows, 101);
   if (threadIdx.x < D) {
     float y = 0.f;
 #pragma unroll

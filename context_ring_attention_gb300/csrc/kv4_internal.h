@@ -35,6 +35,14 @@ struct Kv4Table {
   uint32_t* status;
 };
 
+// Whether block `at` lies in the pool (debug bounds checks).
+template <int D>
+__device__ __forceinline__ bool in_pool(const Kv4Table& t, const uint8_t* at) {
+  const int64_t off = at - t.cache;
+  return off >= 0 && off % Kv4Block<D>::kBytes == 0 &&
+         off / Kv4Block<D>::kBytes < t.pages * t.heads_kv * t.blocks_per_page;
+}
+
 // Kernel-side status bit: an index of the page table, a length or a count out of range.
 constexpr uint32_t kKv4StatusRange = 1u;
 

@@ -319,6 +319,11 @@ struct Run {
     blocks = tb.blocks_per_page - block;
     if (page < 0 || page >= tb.pages) atomicOr(tb.status, kKv4StatusRange);
     else base = tb.cache + (((int64_t)page * tb.heads_kv + h) * tb.blocks_per_page + block) * kBlockBytes;
+    RA_BOUNDS(tb.status, b >= 0 && b < tb.batch && h >= 0 && h < tb.heads_kv && block >= 0 && block < tb.blocks_per_page, 90);
+  }
+  // The current place, and the row of [batch, heads, rows] that goes with it, exist.
+  __device__ __forceinline__ bool sound(int32_t rows) const {
+    return in_pool<D>(tb, base) && row16 >= 0 && row16 < kKvBlockRows && t >= 0 && t < rows;
   }
   __device__ __forceinline__ void advance() {
     t += L::kAtOnce;
@@ -350,8 +355,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1)
   Raw<T> raw[L::kSteps];
 #pragma unroll
   for (int n = 0; n < L::kSteps; ++n)
-    if (run.t + n * L::kAtOnce < run.live) raw[n].load(src + (int64_t)n * L::kAtOnce * D);
-    else raw[n].clear();
+    if (run.t + n * L::kAtOnce < run.live) {
+      RA_BOUNDS(P.t.status, run.row >= 0 && run.row + n * L::kAtOnce < (int64_t)P.t.batch * P.t.heads_kv * P.rows, 91);
+      raw[n].load(src + (int64_t)n * L::kAtOnce * D);
+    } else {
+      raw[n].clear();
+    }
   // Values: a lane holds the 16-bit words of chunks 2c (low half) and 2c + 1 (high half)
   // for group g; with the lane of the neighbouring group (4 lanes on) it makes whole 32-bit
   // words: the even group's lane chunk 2c, the odd group's chunk 2c + 1.
@@ -368,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1)
     const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 4);
     if (run.t < run.live && run.base != nullptr) {
       uint8_t* blk = run.base;
+      RA_BOUNDS(P.t.status, run.sound(P.rows) && at_word < F::kCodeBytes / 4 && g < G, 92);
       if (is_v) word = (g & 1) ? (other >> 16) | (word & 0xffff0000u) : (word & 0xffffu) | (other << 16);
       reinterpret_cast<uint32_t*>(blk + (is_v ? F::kOffV : F::kOffK) + run.row16 * F::kCodeBytes)[at_word] = word;
       if (c == 0)
@@ -400,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 1) kv4_read_ker
     word[n] = par[n] = 0;
     if (run.t < run.live && run.base != nullptr) {
       have |= 1u << n;
+      RA_BOUNDS(P.t.status, run.sound(P.rows) && at_word < F::kCodeBytes / 4 && g < G, 93);
       const uint8_t* codes = run.base + (is_v ? F::kOffV : F::kOffK) + run.row16 * F::kCodeBytes;
       word[n] = reinterpret_cast<const uint32_t*>(codes)[at_word];
       par[n] = reinterpret_cast<const uint32_t*>(run.base + (is_v ? F::kOffVPar : F::kOffKPar) + run.row16 * F::kParBytes)[g];
@@ -425,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 1) kv4_read_ker
       x[2 * i] = y.x;
       x[2 * i + 1] = y.y;
     }
+    RA_BOUNDS(P.t.status, !in || (run.row >= 0 && run.row + n * L::kAtOnce < (int64_t)P.t.batch * P.t.heads_kv * P.rows), 94);
     if (in && (((have >> n) & 1u) || P.zero_rest)) store8<T>(dst + (int64_t)n * L::kAtOnce * D, x);
   }
 }

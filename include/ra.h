@@ -576,7 +576,8 @@ ra_status ra_kv4_attend_scratch_size(ra_kv4_t kv, int64_t batch, int64_t rows, i
 /*
  * ra_kv4_sync_status -- synchronize `stream`, then read and clear the handle's status
  * word: RA_ERR_INVALID_ARG when a call since the last one met a page index, position,
- * length or count out of range, RA_ERR_CUDA on a CUDA error, RA_OK otherwise.
+ * length or count out of range, RA_ERR_CUDA on a CUDA error, RA_ERR_BOUNDS when a bounds
+ * check of the debug build failed, RA_OK otherwise.
  */
 ra_status ra_kv4_sync_status(ra_kv4_t kv, void* stream);
 
