@@ -307,7 +307,11 @@ ra_status ra_kv4_sync_status(ra_kv4_t kv, void* stream) {
   e = cudaMemcpy(&word, kv->d_status, sizeof(word), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return fail(RA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
   if (word == 0) return ok();
-  cudaMemset(kv->d_status, 0, sizeof(word));
+  // Cleared before the next call can set it: a stream that does not wait for the default one
+  // could otherwise have its report cleared.
+  e = cudaMemset(kv->d_status, 0, sizeof(word));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
   if (word & ra::kStatusBounds) {
     char msg[200];
     const ra_status code = ra::status_word_error(word, msg, sizeof(msg));

@@ -1511,7 +1511,10 @@ ra_status ra_sync_status(ra_plan_t plan, void* stream) {
   e = cudaMemcpy(&word, plan->d_status, sizeof(word), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return fail(RA_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
   if (word != 0) {
-    cudaMemset(plan->d_status, 0, sizeof(word));
+    // cleared before a launch on a stream that does not wait for the default one can set it
+    e = cudaMemset(plan->d_status, 0, sizeof(word));
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) return fail(RA_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
     char msg[200];
     const ra_status code = ra::status_word_error(word, msg, sizeof(msg));
     return fail(code, "%s", msg);

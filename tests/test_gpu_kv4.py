@@ -546,3 +546,19 @@ def test_values_far_from_zero(dtype, lengths, hq, size):
     ref.write(k, v, table, [0] * len(lengths), lengths)
     ra.ra_kv4_write(kv, cache, _dev(k, dtype), _dev(v, dtype), _i32(table), _i32([0] * len(lengths)), _i32(lengths))
     _check_attend(kv, cache, ref, table, lengths, hq, 1, d, dtype, 0, 0, rng)
+
+
+def test_reports_on_a_stream_of_its_own():
+    """A report cleared, and the next one made at once by a stream that does not wait for the
+    default one: none is lost."""
+    kv = ra.ra_kv4_plan(1, 16, 1, 1, 64)
+    cache = torch.zeros(ra.ra_kv4_cache_size(kv), dtype=torch.uint8, device="cuda")
+    x = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    bad, zero = _i32([[3]]), _i32([0])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(100):
+        ra.ra_kv4_write(kv, cache, x, x, bad, zero, stream=side)
+        with pytest.raises(ra.RaError):
+            ra.ra_kv4_sync_status(kv, side)
+    ra.ra_kv4_sync_status(kv, side)
