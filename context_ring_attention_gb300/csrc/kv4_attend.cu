@@ -22,8 +22,11 @@
 // are: a word of 8 codes yields 4 operand registers by one shift and 4 logicals, the codes
 // of the bytes' high nibbles standing for 16 n.  The other operands carry the powers of two
 // that bring the products back: the queries 2^E (E from the row's largest), the weights p
-// 2^kShift (an offset of the running maximum, which cancels in O / l).  Scales of value
-// groups from 2^-52 to 2^58 keep full precision that way.
+// 2^kShift.  Scales of value groups from 2^-52 to 2^58 keep full precision that way.
+// The instruction aligns a product by its operands' exponents, which for n are those of 128
+// (for 16 n those of 128 too, or n's own from 8 on): measured, a product n * q is off by up to
+// 2^-18 of q, 16 n * q by 2^-22, which bf16 results do not see.  fp32 takes all codes as 16 n, by
+// two shifts more a word (84 us became 86 for the figure below).
 // Scores come out with keys in rows and are turned for the second product by an 8x8
 // transpose in registers.
 //
@@ -40,7 +43,7 @@
 // of 2k to 32k under a window of 8192 tokens 71 us.  What bounds it is the issue of
 // instructions, some 300 a block and warp, more than half of them for turning codes and weights
 // into operands.  fp32 takes three terms per query and weight and three times the products:
-// 4 sequences of 64k tokens 84 us.
+// 4 sequences of 64k tokens 86 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -87,8 +90,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // from bits 4-7 and 20-23.
 __device__ __forceinline__ uint32_t codes_lo(uint32_t x) { return x & 0x000f000fu; }
 __device__ __forceinline__ uint32_t codes_hi(uint32_t x) { return x & 0x00f000f0u; }
+// The first of the two by the number of terms: the second form, brought there, where there are 3.
+template <int kTerms>
+__device__ __forceinline__ uint32_t codes_first(uint32_t word, int at) {
+  if (kTerms == 1) return codes_lo(word >> at);
+  return codes_hi(at == 0 ? word << 4 : word >> (at - 4));
+}
 constexpr uint32_t kMinus8Lo = 0x80088008u, kMinus8Hi = 0x80808080u;  // the code -8 in both forms
-constexpr float kShift = 60.f;  // log2 of the factor that every p carries
+constexpr int kShift = 60;  // log2 of the factor that every p carries into the products
+// The part of it that the exponential's argument brings: all, without another instruction, for
+// bf16; none for fp32, where an argument near 60 would lose 2^-19.
+template <int kTerms>
+constexpr int kInExponent = kTerms == 1 ? kShift : 0;
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126..127
 __device__ __forceinline__ float scale_of(uint32_t par) { return __uint_as_float(par << 16); }
 __device__ __forceinline__ float low_of(uint32_t par) { return __uint_as_float(par & 0xffff0000u); }
@@ -249,7 +262,7 @@ template <typename T, int D, bool kInRow, bool kHalf>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64 ? 4 : 3 : 3) : 1) kv4_attend_kernel(const Kv4AttendParams P) {
   using F = Kv4Block<D>;
   constexpr int G = F::kGroups;
-  constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
+  constexpr int kTerms = sizeof(T) == 2 ? 1 : 3, kIn = kInExponent<kTerms>;
   constexpr int kSets = kHalf ? 1 : 2;  // sets of scores: of either block, or of both
   constexpr int kRows = kHalf ? kTile / 2 : kTile;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -288,7 +301,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
 
   // Query fragments: lane (r, c) holds row r's channels 32g + 8c .. + 7 of every group, in
   // the pairs (0,4), (1,5), (2,6), (3,7) that a word of codes yields, times 2^E; the pairs
-  // that meet 16 n are divided by 16.  E puts the row's largest channel at 2^119..2^120.
+  // that meet 16 n (fp32: all) are divided by 16.  E puts the row's largest channel at 2^119..2^120.
   uint32_t qf[G][4][kTerms];
   uint32_t qsum[4]; // sum of group c's channels of row r, in the scores' unit 2^(E - 133)
   float back[2];    // that unit's inverse for rows 2c and 2c + 1, times the score scale (log2 units)
@@ -318,7 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float f = (i & 1) ? 0.0625f : 1.f;
+        const float f = (i & 1) || kTerms > 1 ? 0.0625f : 1.f;
         split_pair<kTerms>(x[g][i] * f, x[g][i + 4] * f, qf[g][i]);
         sum += x[g][i] * two_to(-100) + x[g][i + 4] * two_to(-100);
       }
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
   const int vt[4] = {token_of(2 * c), token_of(2 * c + 1), token_of(2 * c + 8), token_of(2 * c + 9)};
 
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float o[G][2][4];  // channels 32g + 4r + {0,1} and {2,3} of rows 2c, 2c + 1 (the odd ones times 16)
+  float o[G][2][4];  // channels 32g + 4r + {0,1} and {2,3} of rows 2c, 2c + 1 (the odd ones, in fp32 all, times 16)
   float pm[G][2];    // sum of p * (middle of the group's range)
 #pragma unroll
   for (int g = 0; g < G; ++g) {
@@ -497,8 +510,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
         for (int i = 0; i < 4; i += 2) {  // nibbles (i, i + 4) and (i + 1, i + 5) of the words
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const uint32_t x0 = k0[n][g] >> (4 * i), x1 = k1[n][g] >> (4 * i);
-            const uint32_t a[4] = {codes_lo(x0), codes_lo(x1), codes_hi(x0), codes_hi(x1)};
+            const uint32_t a[4] = {codes_first<kTerms>(k0[n][g], 4 * i), codes_first<kTerms>(k1[n][g], 4 * i),
+                                   codes_hi(k0[n][g] >> (4 * i)), codes_hi(k1[n][g] >> (4 * i))};
             const int set = kHalf ? 0 : n, y = kHalf ? n : 0;
 #pragma unroll
             for (int t = kTerms - 1; t >= 0; --t) {
@@ -572,7 +585,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float ref = m[e] == -INFINITY ? 0.f : m[e] - kShift;
+      const float ref = m[e] == -INFINITY ? 0.f : m[e] - (float)kIn;
 #pragma unroll
       for (int n = 0; n < kSets; ++n)
 #pragma unroll
@@ -585,7 +598,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
     // O: per group, p times the value's scale as the 16 x 8 operand (keys x rows), the
     // codes of two keys a register as the 16 x 16 one (channels x keys).
     auto values = [&](auto masked) {
-      const uint32_t minus8[4] = {kMinus8Lo, kMinus8Hi, kMinus8Lo, kMinus8Hi};
+      constexpr uint32_t kFirst8 = kTerms == 1 ? kMinus8Lo : kMinus8Hi;
+      const uint32_t minus8[4] = {kFirst8, kMinus8Hi, kFirst8, kMinus8Hi};
       constexpr int kWith = kHalf ? 2 : 1;  // blocks of a score set
 #pragma unroll
       for (int n = 0; n < kSets; ++n) {
@@ -598,27 +612,32 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             load_words<G / 2>(base[kHalf ? y : n] + F::kOffV + vt[i] * F::kCodeBytes + r * (2 * G), vw[y][i]);
-        const float(&p)[4] = s[n];
-        // the middles meet the weights without their 2^kShift: their sums stay as far below
-        // float32's largest number as the values do
-        const float2 down = {two_to(-60), two_to(-60)};
-        const float2 p01 = ptx::mul2(make_float2(p[0], p[1]), down), p23 = ptx::mul2(make_float2(p[2], p[3]), down);
-        const float p1[4] = {p01.x, p01.y, p23.x, p23.y};
+        // pw: the products' weights, which carry 2^kShift; p: the middles' without it, so that
+        // their sums stay as far below float32's largest number as the values do
+        const float other = two_to(kIn ? -kIn : kShift);
+        float p[4], pw[4];
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float2 x = {s[n][i], s[n][i + 1]};
+          const float2 y = ptx::mul2(x, make_float2(other, other));
+          p[i] = kIn ? y.x : x.x, p[i + 1] = kIn ? y.y : x.y;
+          pw[i] = kIn ? x.x : y.x, pw[i + 1] = kIn ? x.y : y.y;
+        }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const float s0 = scale_of(vp0[g]), s1 = scale_of(vp1[g]);
           const float m0 = fmaf(8.f, s0, low_of(vp0[g])), m1 = fmaf(8.f, s1, low_of(vp1[g]));
-          float w[4] = {p[0] * s0, p[1] * s0, p[2] * s1, p[3] * s1};
+          float w[4] = {pw[0] * s0, pw[1] * s0, pw[2] * s1, pw[3] * s1};
           if (decltype(masked)::value) {  // what stands in places that are not seen may be anything
             const float mid[4] = {m0, m0, m1, m1};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (!((seen >> (4 * n + e)) & 1u)) w[e] = 0.f;
-              else pm[g][e & 1] = fmaf(p1[e], mid[e], pm[g][e & 1]);
+              else pm[g][e & 1] = fmaf(p[e], mid[e], pm[g][e & 1]);
             }
           } else {
-            pm[g][0] = fmaf(p1[0], m0, fmaf(p1[2], m1, pm[g][0]));
-            pm[g][1] = fmaf(p1[1], m0, fmaf(p1[3], m1, pm[g][1]));
+            pm[g][0] = fmaf(p[0], m0, fmaf(p[2], m1, pm[g][0]));
+            pm[g][1] = fmaf(p[1], m0, fmaf(p[3], m1, pm[g][1]));
           }
           uint32_t w0[kTerms], w1[kTerms], b2[kTerms][2];
           split_pair<kTerms>(w[0], w[1], w0);
@@ -637,9 +656,9 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t x01 = a01 >> (8 * i), x23 = a23 >> (8 * i);
-              a[i][0] = codes_lo(x01);
+              a[i][0] = codes_first<kTerms>(a01, 8 * i);
               a[i][1] = codes_hi(x01);
-              a[i][2] = codes_lo(x23);
+              a[i][2] = codes_first<kTerms>(a23, 8 * i);
               a[i][3] = codes_hi(x23);
             }
             // columns 0-3 are the first block's weights, 4-7 the second's
@@ -684,11 +703,12 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
   auto sm_o = reinterpret_cast<Row(*)[kTile]>(ring);
   auto sm_m = reinterpret_cast<float(*)[kTile]>(ring + sizeof(Row) * kTile * kWarps);
   auto sm_l = sm_m + kWarps;
+  constexpr int kTo = (kTerms == 1 ? 133 : 129) - kShift;
   if (r == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       sm_m[warp][2 * c + e] = m[e];
-      sm_l[warp][2 * c + e] = l[e] * two_to(-60);
+      sm_l[warp][2 * c + e] = l[e] * two_to(-kIn);
     }
   }
 #pragma unroll
@@ -697,8 +717,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? (kHalf ? D == 64
     for (int e = 0; e < 2; ++e)
       // 2^-kShift brings p back, and another 2^133 (2^129 for 16 n) the codes
       *reinterpret_cast<float4*>(&sm_o[warp][2 * c + e][32 * g + 4 * r]) =
-          make_float4(fmaf(o[g][0][e], two_to(73), pm[g][e]), fmaf(o[g][0][e + 2], two_to(69), pm[g][e]),
-                      fmaf(o[g][1][e], two_to(73), pm[g][e]), fmaf(o[g][1][e + 2], two_to(69), pm[g][e]));
+          make_float4(fmaf(o[g][0][e], two_to(kTo), pm[g][e]), fmaf(o[g][0][e + 2], two_to(129 - kShift), pm[g][e]),
+                      fmaf(o[g][1][e], two_to(kTo), pm[g][e]), fmaf(o[g][1][e + 2], two_to(129 - kShift), pm[g][e]));
   __syncthreads();
   for (int at = threadIdx.x; at < kRows * D; at += kWarps * 32) {
     const int row = at / D, ch = at % D;

@@ -554,10 +554,11 @@ ra_status ra_kv4_read(ra_kv4_t kv, const void* cache, int64_t batch, int64_t row
  * what pages hold there does not matter.
  * bf16: Q enters the products as it is and the softmax weights rounded to bf16, each
  * times its value's scale; sums are fp32.  float32: both are split into three bf16 terms,
- * which keeps fp32 accuracy.  A value group's scale (its range / 15) times the largest
- * weight must stay below 2^58, and its values below 2^89 (their weighted sum, not yet
- * divided, is an fp32 number); groups of scales below 2^-52 lose precision relative to
- * themselves.
+ * which keep their 24 bits; the fp32 sums run over codes, so that O is off by 5e-7 to 7e-7
+ * (relative) where sums over the values themselves give 1e-7 to 3e-7.  A value group's
+ * scale (its range / 15) times the largest weight must stay below 2^58, and its values
+ * below 2^89 (their weighted sum, not yet divided, is an fp32 number); groups of scales
+ * below 2^-52 lose precision relative to themselves.
  * scratch: ra_kv4_attend_scratch_size bytes (NULL when that is 0), not shared by calls
  * that may overlap.  Device pointers, 16-byte aligned (page_table, length: 4-byte).
  * Asynchronous on stream; allocates nothing.
