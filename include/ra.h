@@ -532,8 +532,8 @@ ra_status ra_kv4_write(ra_kv4_t kv, void* cache, int64_t batch, int64_t rows, co
                        const int32_t* count, void* stream);
 
 /*
- * ra_kv4_read -- read keys and values back as what they stand for (low + scale * code,
- * rounded once to the handle's dtype).
+ * ra_kv4_read -- read keys and values back as what they stand for: low + scale * code in
+ * float32 (the product is exact, the sum rounded), then rounded to the handle's dtype.
  * k, v: [batch, Hkv, rows, d]; row t of sequence b receives position first[b] + t for
  * t < count[b] (count NULL: every row).  Later rows stay as they were (zero_rest 0) or
  * become zeros (1), and so do rows whose page or position is out of range.

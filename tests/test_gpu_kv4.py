@@ -189,6 +189,26 @@ def test_read_back(dtype, d):
         assert (k2[b, :, count[b]:] == 0).all() and (v2[b, :, count[b]:] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_are_float32_sums(dtype):
+    """low + scale * code is a float32 number first: where it lies a hair from the middle of two
+    bf16 numbers (a minimum of -2^-40, 3 * 129/128), the second rounding starts from the middle."""
+    x = np.zeros((1, 1, 1, 64))
+    x[..., :32] = np.linspace(0, 15.125, 32)
+    x[..., 0], x[..., 31] = -2.0 ** -40, 15.125
+    x[..., 32:] = -x[..., :32]
+    x = torch.from_numpy(x).to(DT[dtype]).double().numpy()
+    codes, scale, low = kv4_ref.quantise(x)
+    assert scale[0, 0, 0, 0] == 129 / 128 and 3 in codes[0, 0, 0, :32]
+    want = (np.repeat(low, 32, -1) + np.repeat(scale, 32, -1) * codes).astype(np.float32)  # (exact in 64 bits)
+    kv = ra.ra_kv4_plan(1, 16, 1, 1, 64, dtype=dtype)
+    cache = torch.zeros(ra.ra_kv4_cache_size(kv), dtype=torch.uint8, device="cuda")
+    ra.ra_kv4_write(kv, cache, _dev(x, dtype), _dev(x, dtype), _i32([[0]]), _i32([0]))
+    for got in ra.ra_kv4_read(kv, cache, _i32([[0]]), _i32([0]), 1):
+        assert torch.equal(got.cpu(), torch.from_numpy(want).to(DT[dtype]))
+    ra.ra_kv4_sync_status(kv)
+
+
 def _check_attend(kv, cache, ref, table, lengths, hq, t, d, dtype, window, sinks, rng, **kw):
     q = _rows(rng, len(lengths), hq, t, d, dtype) * 0.7
     q = torch.from_numpy(q).to(DT[dtype])
