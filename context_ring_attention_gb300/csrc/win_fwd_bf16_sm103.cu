@@ -29,8 +29,9 @@
 // overlap only so far (tensor cores 59% busy at 32768 tokens and a window of 1024).
 //
 // Roles (one persistent CTA per SM, 12 warps): warp 0 TMA producer, warp 1 tcgen05
-// issuer (both converged, one elected lane issues), warp 2 the work items' records, warps
-// 4-7 softmax of query tile 0, warps 8-11 of query tile 1 (one thread per row).
+// issuer (both converged, one elected lane issues), warp 2 the work items' records, warp 3
+// (partials) the rows of items that meet no key in the launch's steps, warps 4-7 softmax of
+// query tile 0, warps 8-11 of query tile 1 (one thread per row).
 // TMEM: S0 cols 0-127 (P0 in 64-127), S1 128-255 (P1 in 192-255), O0 256-383,
 // O1 384-511 (all 512 columns).
 //
@@ -156,11 +157,40 @@ __device__ __forceinline__ void tma_load_4d_warp_hint(uint32_t dst, const CUtens
       : "memory");
 }
 // ------------------------------------------------------------------- records --
+// The item's ranges that belong to the steps of this launch (they are in the order of their
+// steps): P.ranges[x0 .. x0 + xn).  A whole warp calls it, w is the item's record, 16 bytes a lane.
+__device__ __forceinline__ void ranges_of_launch(const WinParams& P, const int4& w, int lane, int& x0, int& xn) {
+  x0 = __shfl_sync(0xffffffffu, w.z, 1);  // range0
+  xn = __shfl_sync(0xffffffffu, w.w, 1);  // n_ranges
+  if (P.step_lo == 0 && P.step_hi >= P.k.shards) return;
+  int before = 0, in = 0;
+  for (int k = 0; k < xn; k += 32) {
+    const int step = k + lane < xn ? P.ranges[x0 + k + lane].step : P.step_hi;
+    before += __popc(__ballot_sync(0xffffffffu, step < P.step_lo));
+    in += __popc(__ballot_sync(0xffffffffu, step >= P.step_lo && step < P.step_hi));
+  }
+  x0 += before;
+  xn = in;
+}
+__device__ __forceinline__ int4 item_words(const WinParams& P, int idx, int lane) {
+  return lane < 3 ? reinterpret_cast<const int4*>(P.items + idx)[lane] : make_int4(0, 0, 0, 0);
+}
+
 // Warp 2 brings the items and their ranges of this CTA into shared memory, a few items
-// ahead: reading them where they are needed took each role 1 to 2 us at every item.
+// ahead: reading them where they are needed took each role 1 to 2 us at every item.  Items that
+// meet no key in the launch's steps are not among them: the MMA warp asks for the next item
+// before it issues the last product that the softmax warps wait for, and a row of such items,
+// each to be given back by all roles, would fill the slots meanwhile, for good.
 __device__ void run_records(const WinParams& P, const Ctl& c, Record* recs, int lane) {
-  for (uint32_t u = 0;; ++u) {
-    const int idx = (int)(blockIdx.x + u * gridDim.x);
+  int idx = (int)blockIdx.x;
+  for (uint32_t u = 0;; ++u, idx += (int)gridDim.x) {
+    int4 w;
+    int x0 = 0, xn = 0;
+    for (; idx < P.n_items; idx += (int)gridDim.x) {
+      w = item_words(P, idx, lane);
+      ranges_of_launch(P, w, lane, x0, xn);
+      if (xn > 0) break;
+    }
     const uint32_t slot = u % kItemSlots;
     if (!RA_WAIT(kItemEmpty + (int)slot, (u / kItemSlots) ^ 1u, kStatusTimeoutProducer)) return;
     Record& r = recs[slot];
@@ -168,15 +198,7 @@ __device__ void run_records(const WinParams& P, const Ctl& c, Record* recs, int 
     if (end) {
       if (lane == 0) r.it.bh0 = -1;
     } else {
-      const int4 w = lane < 3 ? reinterpret_cast<const int4*>(P.items + idx)[lane] : make_int4(0, 0, 0, 0);
       if (lane < 3) reinterpret_cast<int4*>(&r.it)[lane] = w;
-      int x0 = __shfl_sync(0xffffffffu, w.z, 1);                // range0
-      const int x_end = x0 + __shfl_sync(0xffffffffu, w.w, 1);  // + n_ranges
-      int xn = x_end - x0;
-      if (P.step_lo > 0 || P.step_hi < P.k.shards) {  // ranges are in the order of their steps
-        while (x0 < x_end && P.ranges[x0].step < P.step_lo) ++x0;
-        for (xn = 0; x0 + xn < x_end && P.ranges[x0 + xn].step < P.step_hi;) ++xn;
-      }
       if (lane == 0) {
         r.x0 = x0;
         r.xn = xn;
@@ -187,6 +209,40 @@ __device__ void run_records(const WinParams& P, const Ctl& c, Record* recs, int 
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(c.bar(kItemFull + (int)slot));
     if (end) return;
+  }
+}
+
+// Row of [batch, heads, S] that row `row` of an item's tile g is (-1: none).
+__device__ __forceinline__ int64_t row_of_tile(const WinParams& P, const WinItem& it, int g, int row) {
+  const int i = (g ? it.row1 : it.row0) + row;
+  if (i >= it.row_end || row >= P.q.tile) return -1;
+  const int head_row = it.shard * P.q.s_n + i;
+  return (int64_t)(g ? it.bh1 : it.bh0) * P.seq +
+         (P.q.stripe == 1 ? head_row : head_row % P.q.stripe * (P.seq / P.q.stripe) + head_row / P.q.stripe);
+}
+
+// Partials, warp 3: the rows of the items that meet no key in the launch's steps, O_t = 0 and
+// LSE_t = -inf in each of them.  (Partials are walked shard by shard: a tile's rows follow each
+// other in the tensor.)
+__device__ void run_empty(const WinParams& P, int lane) {
+  const int64_t rows_all = (int64_t)P.batch * P.heads_q * P.seq;
+  for (int idx = (int)blockIdx.x; idx < P.n_items; idx += (int)gridDim.x) {
+    const int4 w = item_words(P, idx, lane);
+    int x0, xn;
+    ranges_of_launch(P, w, lane, x0, xn);
+    if (xn > 0) continue;
+    const WinItem it = P.items[idx];
+    for (int g = 0; g < (it.bh1 >= 0 ? 2 : 1); ++g) {
+      const int left = it.row_end - (g ? it.row1 : it.row0), rows = left < P.q.tile ? left : P.q.tile;
+      const int64_t first = row_of_tile(P, it, g, 0);
+      RA_BOUNDS(P.status, P.q.stripe == 1 && first >= 0 && first + rows <= rows_all, 66);
+      for (int part = 0; part < P.step_hi - P.step_lo; ++part) {
+        float4* o = reinterpret_cast<float4*>(P.o_parts + ((int64_t)part * rows_all + first) * 128) + lane;
+#pragma unroll 8
+        for (int row = 0; row < rows; ++row) o[row * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int row = lane; row < rows; row += 32) P.lse_parts[(int64_t)part * rows_all + first + row] = -INFINITY;
+      }
+    }
   }
 }
 
@@ -316,14 +372,10 @@ struct SegWalk {
       return true;
     }
     s.first = k < 0;
-    while (k < 0) {  // the next item that meets a key in these steps
+    if (k < 0) {
       r = next_record(c, recs, u, kStatusTimeoutMma);
       if (r == nullptr) return false;
       k = 0;
-      if (r->xn == 0) {
-        release_record(c, u++, lane);
-        k = -1;
-      }
     }
     s.two = r->it.bh1 >= 0;
     const int step = range_at(P, r, k).step;
@@ -496,15 +548,10 @@ __device__ void run_softmax(const WinParams& P, const Ctl& c, uint8_t* stage, co
       release_record(c, u, lane);
       continue;
     }
-    const int bh = g ? it.bh1 : it.bh0;
-    const int i = (g ? it.row1 : it.row0) + row;
-    const bool valid = i < it.row_end && row < P.q.tile;
+    const int64_t out_row = row_of_tile(P, it, g, row);
+    const bool valid = out_row >= 0;
     const int my_pos = (g ? it.pos1 : it.pos0) + row * P.q.apart;  // (of rows that are not valid: any)
-    const int head_row = it.shard * P.q.s_n + i;
-    const int64_t out_row = (int64_t)bh * P.seq + (P.q.stripe == 1 ? head_row
-                                                                   : head_row % P.q.stripe * (P.seq / P.q.stripe) +
-                                                                         head_row / P.q.stripe);
-    RA_BOUNDS(c.status, !valid || (bh >= 0 && out_row >= 0 && out_row < (int64_t)P.batch * P.heads_q * P.seq), 65);
+    RA_BOUNDS(c.status, !valid || ((g ? it.bh1 : it.bh0) >= 0 && out_row < (int64_t)P.batch * P.heads_q * P.seq), 65);
 
     float m = -INFINITY, l = 0.f, fix = 0.f;
     bool first = true;
@@ -729,6 +776,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 2) {
       run_records(P, c, recs, lane);
+    } else if (kPartials) {
+      run_empty(P, lane);
     }
   } else {
     ptx::regs_acquire<kRegsSoftmax>();

@@ -174,6 +174,35 @@ def test_first_stripe_of_the_window_holds_the_last_sink(shape, mask):
         assert_within(g_, w_, b_, name)
 
 
+@pytest.mark.parametrize("layout,mask", [("zigzag", (300, 4)), ("contiguous", (1, 0)), ("striped", (40, 200)),
+                                         ("contiguous", (5000, 1))], ids=str)
+def test_steps_in_which_most_items_meet_no_key(layout, mask):
+    """Ring steps of a long sequence under a short window: a CTA has long rows of items without
+    a key in the step between few with one, or none of these at all."""
+    plan, q, k, v, _, pos = _setup((1, 16384, 16, 4, 8), layout, *mask, seed=mask[0])
+    n, s_n = 8, 2048
+    op, lp = ra.ra_fwd(plan, q, k, v, partials=True)
+    ra.ra_sync_status(plan)
+    kb, vb = k, v
+    for t in range(n):
+        o_t = torch.full_like(op[0], 7.0)
+        o_t, lse_t = ra.ra_fwd_step(plan, t, q, kb, vb, o_part=o_t)
+        ra.ra_sync_status(plan)
+        assert torch.equal(o_t, op[t]) and torch.equal(lse_t, lp[t]), f"step {t}"
+        for p in range(n):
+            rows, r = slice(p * s_n, (p + 1) * s_n), (p - t) % n
+            seen = window_ref.visible(pos[rows], pos[r * s_n:(r + 1) * s_n], *mask).any(1)
+            assert torch.equal(torch.isneginf(lse_t[0, 0, rows]), ~seen)
+        if t + 1 < n:
+            kb, vb = ra.ra_ring_rotate(plan, kb, vb)
+    o, lse = ra.ra_fwd(plan, q, k, v)
+    o2, lse2 = ra.ra_ring_fwd(plan, q, k, v)
+    ra.ra_sync_status(plan)
+    # both round the weights and the outputs to bf16; the statistics are fp32 sums of the same terms
+    assert (o.float() - o2.float()).abs().max() <= 3 * BF16_U * v.abs().max()
+    assert (lse - lse2).abs().max() <= 2.0 ** -13
+
+
 def test_long_window_one_head_pair():
     """32k tokens, 4096-token window: 512 rows spread over the sequence, all of dK and dV of
     the sinks (each gathers every later query)."""
