@@ -38,11 +38,14 @@
 // 1M tokens from 276 to 257 us (before the form for few rows) and 16 new tokens of 64k from 180
 // to 136.  Two blocks in 128 registers: 276 us; two pairs a warp in shared memory for three: 260.
 //
-// Measured (32 query and 8 key/value heads, d = 128, bf16, one new token): 1M tokens 234 us,
-// 1.34 GB of cache at 5.7 TB/s (0.84 of a plain copy's rate); 64k tokens 26.5 us; 32 sequences
-// of 2k to 32k under a window of 8192 tokens 71 us.  What bounds it is the issue of
-// instructions, some 300 a block and warp, more than half of them for turning codes and weights
-// into operands.  fp32 takes three terms per query and weight and three times the products:
+// Measured (32 query and 8 key/value heads, d = 128, bf16, one new token): 1M tokens 235 us,
+// 1.34 GB of cache at 5.7 TB/s (0.84 of a plain copy's rate); 64k tokens 26.7 us; 32 sequences
+// of 2k to 32k under a window of 8192 tokens 70 us.  What bounds it is the latency of
+// dependent instructions with 11 warps an SM (55% of the issue slots, HBM 65%, the largest
+// stall a fixed wait): some 300 instructions a block and warp, more than half of them for
+// turning codes and weights into operands.  Every tile of 8 query rows reads and unpacks the
+// cache for itself: 2 new tokens over 1M take 258 us, 16 over 64k (8 tiles) 136, 4 over 8
+// sequences of up to 32k (2 tiles) 100.  fp32 takes three terms per query and weight and three times the products:
 // 4 sequences of 64k tokens 86 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -14,10 +14,12 @@
 // of values by one instruction, and the exact decision taken only next to a border of two
 // codes.
 //
-// Measured (bf16, d = 128, 32768 tokens of 8 heads): write 54 us for 134 MB of rows and
-// 42 MB of cache, 3.2 TB/s; read 26 us for the same bytes, 6.7 TB/s.  Pairs by one
-// instruction took the write from 62 us to 59.5, a product with 1/15 instead of a division to
-// 57.5, and 64 registers, for four CTAs an SM instead of three, to 54.  The read loads words
+// Measured (bf16, d = 128, 32768 tokens of 8 heads): write 55 us for 134 MB of rows and
+// 42 MB of cache, 3.2 TB/s; read 27 us for the same bytes, 6.5 TB/s.  float32, 16384 tokens
+// (134 MB of rows, 21 MB of cache): write 40 us, read 26.  Pairs by one instruction took the
+// write from 62 us to 59.5, a quotient by 15 without a division to 57.5 (the product that the
+// format has now was not timed against it alone), and 64 registers, for four CTAs an SM instead
+// of three, to 54.  The read loads words
 // of two groups and exchanges halves (by 16-bit loads it took 37 us, so 31) and makes floats
 // of codes by one byte permutation each and pairs of values by one instruction.
 #include <cuda_bf16.h>

@@ -553,8 +553,8 @@ void build_win_bwd(ra_plan_s* pl, const ra::WinView& own, const ra::WinView& str
   total *= pb.batch * pb.heads_kv;
   normal = std::max(normal, (int32_t)std::min<int64_t>(total / 10000, kMostTiles / 2));
   const int32_t whole = std::max(normal, std::min(2 * normal, kMostTiles));  // tiles of a sink tile left as it is
-  // Where the tiles are too few for the SMs (37, a quarter of them, or less) the chain of
-  // streamed tiles of one is the pass: those of more than one and a half times an SM's share (8
+  // Where the tiles are too few for the SMs (37, a quarter of 148, or less: the lists are built
+  // before a device is known) the chain of streamed tiles of one is the pass: those of more than one and a half times an SM's share (8
   // tiles at least) are cut too.  Whole and cut: 1024 tokens of 8 query heads for 2, window 512,
   // 65 and 23 us; 810 of 4 for 1, 36 and 25; 4096 of 4 for 1 under a window of as many 225 and
   // 105.  With 64 tiles and more there is nothing to gain, and the parts have to be written and

@@ -20,11 +20,13 @@
 // ... of a list sorted by cost and key/value head: no counter, and launches of one
 // plan need no reset between them.
 //
-// Measured (one query tile pair meets 9 or 10 key tiles): 32768 tokens in 8 zigzag shards,
-// 32 query and 8 key/value heads x 2, window 4096 and 4 sinks, 1.33 ms, 0.81 of the tensor
-// cores' measured rate on the visible pairs; 131072 tokens in 8 contiguous shards, window
-// 1024, 1.89 ms (0.64: the tiles at a window's two edges are half empty); 900 tokens of 4
-// heads 12.7 us.  What bounds it: each softmax thread has a row of 128 scores to bring from
+// Measured, 32 query and 8 key/value heads: 32768 tokens in 8 zigzag shards, window 4096 and 4
+// sinks, 1.30 to 1.39 ms by the clock, 0.77 to 0.82 of the tensor cores' measured rate on the
+// visible pairs; 131072 tokens in 32 contiguous shards, window 1024 and 64 sinks, 1.87 to 1.98
+// ms (0.61 to 0.64: a pair of query tiles meets 10 key tiles, of which the two at the window's
+// edges and the sinks' are partly empty); 900 tokens of 4 heads 13 us.  The first workload's
+// eight partials in one launch 2.58 ms (4.3 GB of fp32 rows, a thread writing its own row in
+// 16-byte pieces), ring steps 0.12 ms (no keys) to 0.64, the ring driver 3.95.  What bounds it: each softmax thread has a row of 128 scores to bring from
 // tensor memory and back per product pair, and the two query tiles' softmax and products
 // overlap only so far (tensor cores 59% busy at 32768 tokens and a window of 1024).
 //

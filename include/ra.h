@@ -138,7 +138,8 @@ ra_status ra_plan(const ra_problem* prob, ra_plan_t* out);
  * for the other key tiles within reach of the query tile, SKIP for the rest.
  * K and V (and Q and dO in ra_bwd) must be finite: a key that a query does not see
  * enters its products with weight zero where it shares a tile with keys that are seen,
- * and zero times an infinity or a NaN is a NaN.
+ * and zero times an infinity or a NaN is a NaN.  A row of Q that is not finite leaves its
+ * own row of O and LSE undefined, in ra_fwd as under ra_plan, and no other.
  * Its LSE is that of the unrounded weights.  Its kernels hold no counters: calls that
  * share the plan may be captured into graphs (keep the plan while a graph of them lives).
  * Errors: as ra_plan, and RA_ERR_INVALID_ARG (causal 0, window < 1, sinks < 0),
