@@ -7,7 +7,10 @@ The functions keep the C names (``ra_plan``, ``ra_plan_window``, ``ra_plan_tile_
 ``ra_bwd_scratch_size``, ``ra_allgather_kv``, ``ra_fwd_gathered``,
 ``ra_ulysses_a2a``, ``ra_sync_status``, ``ra_wait_selftest``, ``ra_last_error``;
 ``ra_kv4_plan``, ``ra_kv4_cache_size``, ``ra_kv4_write``, ``ra_kv4_read``,
-``ra_kv4_attend``, ``ra_kv4_attend_scratch_size``, ``ra_kv4_sync_status``).
+``ra_kv4_attend``, ``ra_kv4_attend_scratch_size``, ``ra_kv4_sync_status``;
+``ra_rope_plan``, ``ra_rope``, ``ra_rope_bwd``;
+``ra_paged_plan``, ``ra_paged_append``, ``ra_paged_attend``, ``ra_paged_attend_scratch_size``,
+``ra_paged_weigh``, ``ra_paged_evict``, ``ra_paged_sync_status``).
 This module only marshals arguments: PyTorch supplies device memory and the
 current stream (outputs and scratch made for a call with a ``stream`` of its own belong to
 that stream), every step of the computation runs in the library's CUDA kernels, and there is
@@ -16,7 +19,8 @@ passes (outputs and scratch included) is checked here for its exact shape, dtype
 contiguity and device before anything is launched.
 
 Tensors are ``[B, H, S, d]`` contiguous with S in layout order (shard p owns rows
-[p*S/N, (p+1)*S/N)); ``ra_layout_perm`` moves natural order <-> layout order.
+[p*S/N, (p+1)*S/N)); ``ra_layout_perm`` moves natural order <-> layout order.  The rotations
+take them with any strides, and the paged cache takes packed tensors ``[tokens, H, d]``.
 
 With RA_LIBRARY_VARIANT=debug in the environment the binding loads libra_debug.so
 instead: the same library with the kernels' bounds checks compiled in, which
@@ -37,11 +41,15 @@ __all__ = [
     "ra_allgather_kv", "ra_fwd_gathered", "ra_ulysses_a2a", "ra_wait_selftest",
     "Kv4", "ra_kv4_plan", "ra_kv4_destroy", "ra_kv4_cache_size", "ra_kv4_write", "ra_kv4_read", "ra_kv4_attend",
     "ra_kv4_attend_scratch_size", "ra_kv4_sync_status",
+    "Rope", "ROPE_SCALINGS", "ra_rope_plan", "ra_rope_destroy", "ra_rope", "ra_rope_bwd",
+    "Paged", "ra_paged_plan", "ra_paged_destroy", "ra_paged_cache_shape", "ra_paged_append", "ra_paged_attend",
+    "ra_paged_attend_scratch_size", "ra_paged_weigh", "ra_paged_evict", "ra_paged_sync_status",
     "library_path", "load_library", "EXPORTED",
 ]
 
 LAYOUTS = {"contiguous": 0, "striped": 1, "zigzag": 2}
 DTYPES = {"f32": 0, "bf16": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 _STATUS = {0: "RA_OK", 1: "RA_ERR_INVALID_ARG", 2: "RA_ERR_UNSUPPORTED", 3: "RA_ERR_CUDA",
            4: "RA_ERR_TIMEOUT", 5: "RA_ERR_NO_DEVICE", 6: "RA_ERR_BOUNDS"}
 EXPORTED = ("ra_plan", "ra_plan_window", "ra_plan_destroy", "ra_plan_tile_counts", "ra_fwd", "ra_merge_partials",
@@ -49,7 +57,10 @@ EXPORTED = ("ra_plan", "ra_plan_window", "ra_plan_destroy", "ra_plan_tile_counts
             "ra_fwd_static_status", "ra_fwd_step", "ra_ring_rotate", "ra_ring_fwd", "ra_bwd", "ra_bwd_scratch_size",
             "ra_allgather_kv", "ra_fwd_gathered", "ra_ulysses_a2a", "ra_wait_selftest",
             "ra_kv4_plan", "ra_kv4_destroy", "ra_kv4_cache_size", "ra_kv4_write", "ra_kv4_read", "ra_kv4_attend",
-            "ra_kv4_attend_scratch_size", "ra_kv4_sync_status")
+            "ra_kv4_attend_scratch_size", "ra_kv4_sync_status",
+            "ra_rope_plan", "ra_rope_destroy", "ra_rope", "ra_rope_bwd",
+            "ra_paged_plan", "ra_paged_destroy", "ra_paged_append", "ra_paged_attend", "ra_paged_attend_scratch_size",
+            "ra_paged_weigh", "ra_paged_evict", "ra_paged_sync_status")
 
 _TORCH = None
 _NO_CONTEXT = contextlib.nullcontext()
@@ -84,6 +95,19 @@ class _Problem(ctypes.Structure):
 
 
 class _Kv4Problem(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int64), ("page_rows", ctypes.c_int32), ("heads_q", ctypes.c_int32),
+                ("heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("window", ctypes.c_int64), ("sinks", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
+class _RopeProblem(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("base", ctypes.c_double), ("scaling", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("original", ctypes.c_int64), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class _PagedProblem(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_int64), ("page_rows", ctypes.c_int32), ("heads_q", ctypes.c_int32),
                 ("heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("window", ctypes.c_int64), ("sinks", ctypes.c_int64), ("scale", ctypes.c_float)]
@@ -136,6 +160,18 @@ def load_library():
         "ra_kv4_attend": ([P, VP, I64, I64, VP, VP, I64, VP, VP, VP, VP, VP], I32),
         "ra_kv4_attend_scratch_size": ([P, I64, I64, I64, VP], I32),
         "ra_kv4_sync_status": ([P, VP], I32),
+        "ra_rope_plan": ([ctypes.POINTER(_RopeProblem), ctypes.POINTER(P)], I32),
+        "ra_rope_destroy": ([P], I32),
+        "ra_rope": ([P, I64, I64, I32, I32, I32, I32, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP], I32),
+        "ra_rope_bwd": ([P, I64, I64, I32, I32, I32, I32, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP], I32),
+        "ra_paged_plan": ([ctypes.POINTER(_PagedProblem), ctypes.POINTER(P)], I32),
+        "ra_paged_destroy": ([P], I32),
+        "ra_paged_append": ([P, P, VP, I64, I64, VP, VP, VP, VP, VP, VP, VP, VP, VP, I64, VP, VP, VP, VP], I32),
+        "ra_paged_attend": ([P, VP, I64, I64, VP, VP, VP, I64, VP, VP, VP, VP, VP, VP, VP], I32),
+        "ra_paged_attend_scratch_size": ([P, I64, I64, I64, VP], I32),
+        "ra_paged_weigh": ([P, VP, I64, I64, VP, VP, VP, VP, I64, VP, VP, VP, VP, I64, VP], I32),
+        "ra_paged_evict": ([P, VP, I64, VP, I64, VP, VP, VP, I64, I64, I64, I64, VP, I64, VP, VP, VP], I32),
+        "ra_paged_sync_status": ([P, VP], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -791,3 +827,328 @@ def ra_kv4_sync_status(kv, stream=None):
     """Synchronize the stream and raise RaError if a call met a page index, position, length
     or count out of range."""
     _check(load_library().ra_kv4_sync_status(kv.handle, _stream(stream)))
+
+
+class Rope:
+    """Owns an ``ra_rope_t``; the rotation it was described for is ``self.problem``."""
+
+    def __init__(self, handle, problem):
+        self._h = handle
+        self.problem = problem
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h:
+            load_library().ra_rope_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def ra_rope_plan(head_dim, rotary_dim=0, base=10000.0, interleaved=False, scaling="none", factor=1.0, original=0,
+                 low=1.0, high=4.0, amplitude=1.0, dtype="bf16"):
+    """Describe a rotation by positions (see include/ra.h); rotary_dim 0 is the whole head.
+
+    ``scaling``: "none", "linear", "base", "bands" or "ramp", for contexts ``factor`` times
+    longer than the ``original`` tokens; ``low`` and ``high`` are turns within those.
+    """
+    lib = load_library()
+    dt = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+    kind = ROPE_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    if not amplitude > 0:
+        raise ValueError("amplitude must be > 0")
+    prob = _RopeProblem(int(head_dim), int(rotary_dim) or int(head_dim), int(bool(interleaved)), dt, float(base), kind,
+                        float(factor), int(original), float(low), float(high), float(amplitude))
+    h = ctypes.c_void_p()
+    _check(lib.ra_rope_plan(ctypes.byref(prob), ctypes.byref(h)))
+    info = dict(head_dim=prob.head_dim, rotary_dim=prob.rotary_dim, interleaved=bool(interleaved), dtype=dt,
+                base=float(base), scaling=kind, factor=float(factor), original=int(original), low=float(low),
+                high=float(high), amplitude=float(amplitude))
+    return Rope(h, info)
+
+
+def ra_rope_destroy(rope):
+    rope.close()
+
+
+def _strides(t):
+    """Strides of all axes but the last, in elements, as a host array (0 along an axis of one)."""
+    return (ctypes.c_int64 * (t.dim() - 1))(*[st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride()[:-1])])
+
+
+def _need_rows(name, t, shape, dtype, device):
+    """``t`` must be of this shape, dtype and device (checked already), its last axis contiguous."""
+    if (not isinstance(t, (_TORCH or _torch()).Tensor) or t.shape != tuple(shape) or t.dtype != dtype or t.device != device
+            or (t.stride(-1) != 1 and t.shape[-1] > 1)):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, contiguous along its "
+                         f"last axis")
+
+
+def _rope_call(call, rope, q, k, layout, n_shards, position, q_out, k_out, stream):
+    torch = _TORCH or _torch()
+    pb = rope.problem
+    dtype = torch.bfloat16 if pb["dtype"] == 1 else torch.float32
+    if q.dim() != 4:
+        raise ValueError("q must have the shape [B, Hq, S, d]")
+    B, Hq, S, _ = q.shape
+    device = q.device
+    _need_rows("q", q, (B, Hq, S, pb["head_dim"]), dtype, device)
+    _on_current_device("q", q)
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[1] if k.dim() == 4 else 0
+        _need_rows("k", k, (B, Hk, S, pb["head_dim"]), dtype, device)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if position is not None:
+        _need_like("position", position, (B, S), torch.int32, device)
+    if q_out is not None:
+        _need_rows("q_out", q_out, q.shape, dtype, device)
+    if k_out is not None:
+        _need_rows("k_out", k_out, k.shape, dtype, device)
+    if q_out is None or (k is not None and k_out is None):
+        with _alloc_on(stream):
+            if q_out is None:
+                q_out = torch.empty((B, Hq, S, pb["head_dim"]), dtype=dtype, device=device)
+            if k is not None and k_out is None:
+                k_out = torch.empty((B, Hk, S, pb["head_dim"]), dtype=dtype, device=device)
+    key = k is not None
+    _check(call(rope.handle, B, S, Hq, Hk, _layout(layout), int(n_shards), _ptr(position), _ptr(q), _strides(q), _ptr(k),
+                _strides(k) if key else None, _ptr(q_out), _strides(q_out), _ptr(k_out), _strides(k_out) if key else None,
+                _stream(stream)))
+    return (q_out, k_out) if key else q_out
+
+
+def ra_rope(rope, q, k=None, layout="contiguous", n_shards=1, position=None, q_out=None, k_out=None, stream=None):
+    """Rotate q [B, Hq, S, d] and k [B, Hkv, S, d] by their positions -> (q_out, k_out), or q_out without k.
+
+    Row i of shard p stands at its natural position of the layout, unless ``position``
+    [B, S] int32 gives them.  All tensors may have strides of their own; the outputs are
+    contiguous unless passed in, and may be the inputs themselves.
+    """
+    return _rope_call(load_library().ra_rope, rope, q, k, layout, n_shards, position, q_out, k_out, stream)
+
+
+def ra_rope_bwd(rope, dq, dk=None, layout="contiguous", n_shards=1, position=None, q_out=None, k_out=None, stream=None):
+    """Gradients with respect to ra_rope's inputs from those with respect to its outputs."""
+    return _rope_call(load_library().ra_rope_bwd, rope, dq, dk, layout, n_shards, position, q_out, k_out, stream)
+
+
+class Paged:
+    """Owns an ``ra_paged_t``; the cache it was described for is ``self.problem``."""
+
+    def __init__(self, handle, problem):
+        self._h = handle
+        self.problem = problem
+        pb = problem
+        self._shape = (pb["pages"], 2, pb["heads_kv"], pb["page_rows"], pb["head_dim"])
+        self._scratch = (None, 0)  # (batch, tokens, table width) of the last attention call, its bytes of scratch
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h:
+            load_library().ra_paged_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def ra_paged_plan(pages, page_rows, heads_q, heads_kv, head_dim, dtype="bf16", window=0, sinks=0, scale=0.0):
+    """Describe a paged key/value cache and the attention over it (see include/ra.h)."""
+    lib = load_library()
+    dt = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+    prob = _PagedProblem(int(pages), int(page_rows), int(heads_q), int(heads_kv), int(head_dim), dt, int(window),
+                         int(sinks), float(scale or 0.0))
+    h = ctypes.c_void_p()
+    _check(lib.ra_paged_plan(ctypes.byref(prob), ctypes.byref(h)))
+    info = dict(pages=int(pages), page_rows=int(page_rows), heads_q=int(heads_q), heads_kv=int(heads_kv),
+                head_dim=int(head_dim), dtype=dt, window=int(window), sinks=int(sinks), scale=float(scale or 0.0))
+    return Paged(h, info)
+
+
+def ra_paged_destroy(kv):
+    kv.close()
+
+
+def ra_paged_cache_shape(kv):
+    """Shape of the cache, a contiguous CUDA tensor of the caller's in the handle's dtype:
+    [pages, keys and values, Hkv, page_rows, d]."""
+    return kv._shape
+
+
+def _paged_tables(kv, cache, page_table, length, offset=None):
+    """The cache and the int32 tables of a call, all on one device -> (dtype, device, batch)."""
+    torch = _TORCH or _torch()
+    dtype = torch.bfloat16 if kv.problem["dtype"] == 1 else torch.float32
+    device, i32 = cache.device, torch.int32
+    _need("cache", cache, kv._shape, dtype, device)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 tensor of shape (sequences, pages of a sequence)")
+    batch = page_table.shape[0]
+    _need_like("page_table", page_table, page_table.shape, i32, device)
+    _need_like("length", length, (batch,), i32, device)
+    if offset is not None:
+        _need_like("offset", offset, (batch + 1,), i32, device)
+    return dtype, device, batch
+
+
+def ra_paged_append(kv, cache, k, v, page_table, offset, length, rope=None, position=None, q=None, q_out=None,
+                    stream=None):
+    """New tokens' keys and values k, v [tokens, Hkv, d] into the cache -> q_out (None without q).
+
+    Sequence b has the tokens offset[b] .. offset[b+1]-1 and length[b] slots in use, those
+    among them.  With ``rope`` the keys, and the queries q [tokens, Hq, d], are rotated by
+    ``position`` [tokens] (default: the tokens' slots) on the way.
+    """
+    torch = _TORCH or _torch()
+    pb = kv.problem
+    dtype, device, batch = _paged_tables(kv, cache, page_table, length, offset=offset)
+    T = k.shape[0] if k.dim() == 3 else 0
+    _need_rows("k", k, (T, pb["heads_kv"], pb["head_dim"]), dtype, device)
+    _need_rows("v", v, (T, pb["heads_kv"], pb["head_dim"]), dtype, device)
+    if position is not None:
+        _need_like("position", position, (T,), torch.int32, device)
+    if q is not None:
+        _need_rows("q", q, (T, pb["heads_q"], pb["head_dim"]), dtype, device)
+        if q_out is None:
+            with _alloc_on(stream):
+                q_out = torch.empty((T, pb["heads_q"], pb["head_dim"]), dtype=dtype, device=device)
+        else:
+            _need_rows("q_out", q_out, q.shape, dtype, device)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check(load_library().ra_paged_append(
+        kv.handle, None if rope is None else rope.handle, _ptr(cache), batch, T, _ptr(k), _strides(k), _ptr(v), _strides(v),
+        _ptr(q), None if q is None else _strides(q), _ptr(q_out), None if q is None else _strides(q_out),
+        _ptr(page_table), page_table.shape[1], _ptr(offset), _ptr(length), _ptr(position), _stream(stream)))
+    return q_out
+
+
+def ra_paged_attend_scratch_size(kv, batch, tokens, table_width):
+    """Bytes of the float32 scratch buffer ra_paged_attend needs for these sizes (0: none)."""
+    key = (int(batch), int(tokens), int(table_width))
+    if kv._scratch[0] != key:
+        n = ctypes.c_int64()
+        _check(load_library().ra_paged_attend_scratch_size(kv.handle, *key, ctypes.byref(n)))
+        kv._scratch = (key, n.value)
+    return kv._scratch[1]
+
+
+def ra_paged_attend(kv, cache, q, page_table, offset, length, o=None, lse=None, scratch=None, stream=None):
+    """Attention of the new tokens q [tokens, Hq, d] over their sequences' slots -> (O, LSE [tokens, Hq]).
+
+    ``scratch`` (``ra_paged_attend_scratch_size`` bytes, float32) is allocated here unless
+    passed in.  Rows of no sequence stay as they were (in tensors made here: undefined).
+    """
+    torch = _TORCH or _torch()
+    pb = kv.problem
+    dtype, device, batch = _paged_tables(kv, cache, page_table, length, offset=offset)
+    T = q.shape[0] if q.dim() == 3 else 0
+    shape = (T, pb["heads_q"], pb["head_dim"])
+    _need_rows("q", q, shape, dtype, device)
+    need = ra_paged_attend_scratch_size(kv, batch, T, page_table.shape[1]) // 4
+    if scratch is not None and (scratch.numel() < need or scratch.dtype != torch.float32
+                                  or not scratch.is_contiguous() or scratch.device != device):
+        raise ValueError("scratch must be a contiguous float32 tensor of at least ra_paged_attend_scratch_size(...) "
+                         "bytes on the device of q")
+    if o is not None:
+        _need_rows("o", o, shape, dtype, device)
+    if lse is not None:
+        _need_like("lse", lse, (T, pb["heads_q"]), torch.float32, device)
+    with _alloc_on(stream):
+        if o is None:
+            o = torch.empty(shape, dtype=dtype, device=device)
+        if lse is None:
+            lse = torch.empty((T, pb["heads_q"]), dtype=torch.float32, device=device)
+        if scratch is None and need:
+            scratch = torch.empty(need, dtype=torch.float32, device=device)
+    _check(load_library().ra_paged_attend(kv.handle, _ptr(cache), batch, T, _ptr(q), _strides(q), _ptr(page_table),
+                                          page_table.shape[1], _ptr(offset), _ptr(length), _ptr(o), _strides(o), _ptr(lse),
+                                          _ptr(scratch), _stream(stream)))
+    return o, lse
+
+
+def _need_weights(name, t, kv, batch, device):
+    torch = _TORCH or _torch()
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a float32 tensor of shape (sequences, Hkv, slots)")
+    _need_like(name, t, (batch, kv.problem["heads_kv"], t.shape[2]), torch.float32, device)
+
+
+def ra_paged_weigh(kv, cache, q, lse, page_table, offset, length, weight, weight_in=None, stream=None):
+    """Attention weight of every slot from the new tokens, added to ``weight_in`` (default: zeros) -> weight.
+
+    weight, weight_in: [sequences, Hkv, slots] float32, and may be one tensor; the slots of the
+    call's own tokens start from zero.  lse: what ra_paged_attend returned for q.
+    """
+    torch = _TORCH or _torch()
+    pb = kv.problem
+    dtype, device, batch = _paged_tables(kv, cache, page_table, length, offset=offset)
+    T = q.shape[0] if q.dim() == 3 else 0
+    _need_rows("q", q, (T, pb["heads_q"], pb["head_dim"]), dtype, device)
+    _need_like("lse", lse, (T, pb["heads_q"]), torch.float32, device)
+    _need_weights("weight", weight, kv, batch, device)
+    if weight_in is not None:
+        _need_like("weight_in", weight_in, weight.shape, torch.float32, device)
+    _check(load_library().ra_paged_weigh(kv.handle, _ptr(cache), batch, T, _ptr(q), _strides(q), _ptr(lse), _ptr(page_table),
+                                         page_table.shape[1], _ptr(offset), _ptr(length), _ptr(weight_in), _ptr(weight),
+                                         weight.shape[2], _stream(stream)))
+    return weight
+
+
+def ra_paged_evict(kv, cache, page_table, length, weight, keep, first=0, recent=0, new_table=None, weight_out=None,
+                   kept=None, new_length=None, stream=None):
+    """Keep ``keep`` slots of every sequence and head: the first, the most recent, the heaviest -> (kept, new_length).
+
+    The slots that stay move together, in place or into the pages of ``new_table``;
+    weight_out (default: weight itself) receives their weights.
+    kept: [sequences, Hkv, keep] int32, the slots they had (-1: none).
+    """
+    torch = _TORCH or _torch()
+    dtype, device, batch = _paged_tables(kv, cache, page_table, length)
+    _need_weights("weight", weight, kv, batch, device)
+    if weight_out is None:
+        weight_out = weight
+    else:
+        _need_like("weight_out", weight_out, weight.shape, torch.float32, device)
+    if new_table is None:
+        new_table = page_table
+    elif not isinstance(new_table, torch.Tensor) or new_table.dim() != 2:
+        raise ValueError("new_table must be an int32 tensor of shape (sequences, pages of a sequence)")
+    else:
+        _need_like("new_table", new_table, (batch, new_table.shape[1]), torch.int32, device)
+    keep, hk = int(keep), kv.problem["heads_kv"]
+    if kept is not None:
+        _need_like("kept", kept, (batch, hk, keep), torch.int32, device)
+    if new_length is not None:
+        _need_like("new_length", new_length, (batch,), torch.int32, device)
+    if kept is None or new_length is None:
+        with _alloc_on(stream):
+            if kept is None:
+                kept = torch.empty((batch, hk, max(keep, 0)), dtype=torch.int32, device=device)
+            if new_length is None:
+                new_length = torch.empty((batch,), dtype=torch.int32, device=device)
+    _check(load_library().ra_paged_evict(kv.handle, _ptr(cache), batch, _ptr(page_table), page_table.shape[1], _ptr(length),
+                                         _ptr(weight), _ptr(weight_out), weight.shape[2], keep, int(first), int(recent),
+                                         _ptr(new_table), new_table.shape[1], _ptr(kept), _ptr(new_length), _stream(stream)))
+    return kept, new_length
+
+
+def ra_paged_sync_status(kv, stream=None):
+    """Synchronize the stream and raise RaError if a call met a page index, offset, length or
+    slot out of range."""
+    _check(load_library().ra_paged_sync_status(kv.handle, _stream(stream)))

@@ -1,0 +1,118 @@
+// New tokens of a packed batch into the paged cache (include/ra.h, ra_paged_append): their
+// queries and keys rotated by their positions, keys and values to the pages of their sequences.
+//
+// Bound by HBM: every row is read and written once, in one launch.  As in the ring's rotation
+// (rope.cu) a thread has two 16-byte vectors of one token, computes their angles once and takes
+// the rows of the token in turn: queries, keys, values.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "paged_internal.h"
+
+namespace ra {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKnown = 256;  // sequences whose offsets a block keeps in shared memory
+
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(kThreads) append_kernel(const PagedAppendParams P) {
+  constexpr int kPairs = kWide ? RopeUnit<T>::kPairs : 1;
+  __shared__ int32_t offsets[kKnown];
+  const bool known = P.t.batch <= kKnown;
+  if (known) {
+    for (int b = threadIdx.x; b < P.t.batch; b += kThreads) offsets[b] = P.t.offset[b];
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && blockIdx.y == 0)  // the sequences that no token is found in are checked too
+    for (int b = threadIdx.x; b < P.t.batch; b += kThreads) paged_seq(P.t, b);
+  const int units = rope_units<T>(P.rope, kWide, P.d);
+  const int64_t n = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (n / units >= P.t.tokens) return;
+  const int token = (int)(n / units), unit = (int)(n - (int64_t)token * units);
+  // the last sequence that begins at the token or before it
+  int b = 0;
+  for (int end = P.t.batch; end - b > 1;) {
+    const int mid = (b + end) >> 1;
+    ((known ? offsets[mid] : __ldg(P.t.offset + mid)) <= token ? b : end) = mid;
+  }
+  const PagedSeq seq = paged_seq(P.t, b);
+  const int i = token - seq.token0;
+  if (i < 0 || i >= seq.count) return;  // a token of no sequence
+  const int slot = seq.slot0() + i;
+  const RopePlace at = rope_place<T>(P.rope, kWide, unit);
+
+  const bool turned = at.pair >= 0 && P.rope.speed != nullptr;
+  float c[kPairs], s[kPairs];
+  if (turned) {
+    const int64_t pos = P.position != nullptr ? P.position[token] : slot;
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) rope_angle(P.rope.speed[at.pair + e], pos, P.rope.amplitude, 1.0f, c[e], s[e]);
+  }
+  const int page = paged_page(P.t, b, slot / P.t.page_rows);
+  T* cache = static_cast<T*>(P.t.cache);
+  const int hk = P.t.heads_kv, heads = P.heads_q + 2 * hk;
+#pragma unroll 2
+  for (int h = blockIdx.y; h < heads; h += gridDim.y) {
+    const int g = h - P.heads_q;  // key (below heads_kv) or value head
+    const T* src;
+    T* dst;
+    if (g < 0) {
+      src = static_cast<const T*>(P.q) + token * P.qs.token + h * P.qs.head;
+      dst = static_cast<T*>(P.q_out) + token * P.qos.token + h * P.qos.head;
+    } else {
+      if (page < 0) break;
+      const int which = g >= hk;
+      const int64_t row = paged_row(P.t, page, which, which ? g - hk : g, slot % P.t.page_rows);
+      src = which ? static_cast<const T*>(P.v) + token * P.vs.token + (g - hk) * P.vs.head
+                  : static_cast<const T*>(P.k) + token * P.ks.token + g * P.ks.head;
+      dst = cache + row * P.d;
+      RA_BOUNDS(P.t.status, row >= 0 && row < (int64_t)P.t.pages * 2 * hk * P.t.page_rows, 110);
+    }
+    const bool turn = turned && g < hk;
+    if constexpr (kWide) {
+      RopeUnit<T> u;
+      u.load(src, at.first, at.second);
+      if (turn) u.turn(c, s, P.rope.interleaved);
+      u.store(dst, at.first, at.second);
+    } else {
+      const T x1 = src[at.first];
+      if (at.second < 0) {
+        dst[at.first] = x1;
+        continue;
+      }
+      const T x2 = src[at.second];
+      if (turn) {
+        const float a = rope_load(&x1), e = rope_load(&x2);
+        rope_store(dst + at.first, a * c[0] - e * s[0]);
+        rope_store(dst + at.second, a * s[0] + e * c[0]);
+      } else {
+        dst[at.first] = x1;
+        dst[at.second] = x2;
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch(const PagedAppendParams& prm, int sm_count, cudaStream_t stream) {
+  const int units = prm.wide ? prm.d / (2 * RopeUnit<T>::kVec) : (prm.rope.rot >> 1) + (prm.d - prm.rope.rot);
+  const int64_t blocks = ((int64_t)prm.t.tokens * units + kThreads - 1) / kThreads;
+  // Rows of a token are shared out among blocks where the tokens alone leave the GPU idle.
+  const int heads = prm.heads_q + 2 * prm.t.heads_kv;
+  const int split = (int)std::min<int64_t>(std::min(heads, 65535), std::max<int64_t>(1, (int64_t)sm_count * 8 / blocks));
+  const dim3 grid((unsigned)blocks, (unsigned)split);
+  if (prm.wide) append_kernel<T, true><<<grid, kThreads, 0, stream>>>(prm);
+  else append_kernel<T, false><<<grid, kThreads, 0, stream>>>(prm);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(int dtype, const PagedAppendParams& prm, int sm_count, cudaStream_t stream) {
+  return dtype == RA_DTYPE_BF16 ? launch<__nv_bfloat16>(prm, sm_count, stream) : launch<float>(prm, sm_count, stream);
+}
+
+}  // namespace ra

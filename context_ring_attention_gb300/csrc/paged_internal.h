@@ -1,0 +1,155 @@
+// The paged key/value cache (include/ra.h, ra_paged_*): its layout, the sequences of a packed
+// batch, which keys a run of tokens sees, and the launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ra_internal.h"
+#include "rope_internal.h"
+
+namespace ra {
+
+constexpr uint32_t kPagedStatusRange = 1u << 5;  // a page, offset, length or slot out of range
+constexpr int kMaxSequences = 4096;              // of a call: their shares are summed in shared memory
+
+// What the calls share: the cache [pages, 2, heads_kv, page_rows, d] and its sequences.
+struct PagedTable {
+  void* cache;
+  const int32_t* page_table;  // [batch, width]
+  const int32_t* offset;      // [batch + 1]
+  const int32_t* length;      // [batch]
+  int64_t width;
+  int32_t pages, page_rows, batch, heads_kv, tokens;
+  uint32_t* status;
+};
+
+struct PagedStrides {  // elements
+  int64_t token, head;
+};
+
+struct PagedAppendParams {
+  PagedTable t;
+  RopeTable rope;  // speed nullptr: keys as they are
+  int32_t d, heads_q;  // heads_q 0: no queries
+  bool wide;
+  const int32_t* position;  // [tokens] or nullptr: the slot
+  const void *q, *k, *v;
+  void* q_out;
+  PagedStrides qs, ks, vs, qos;
+};
+
+struct PagedAttendParams {
+  PagedTable t;
+  int32_t heads_q, group, slots;  // slots: CTAs per key/value head at most
+  int32_t window, sinks;          // window 0: the whole prefix
+  float scale_log2;
+  const void* q;
+  void* o;
+  PagedStrides qs, os;
+  float* lse;        // [tokens, heads_q] or nullptr
+  float* part_o;     // [head, slot, 2, kRowsTile, d]
+  float2* part_ml;   // [head, slot, 2, kRowsTile]: running maximum (log2 units) and sum
+  int4* joins;       // [head, slot]: first query row, rows, last slot of an item cut here (rows 0: none)
+};
+
+struct PagedWeighParams {
+  PagedTable t;
+  int32_t heads_q, group;
+  int32_t window, sinks;
+  float scale_log2;
+  const void* q;
+  PagedStrides qs;
+  const float* lse;        // [tokens, heads_q]
+  const float* weight_in;  // [batch, heads_kv, weight_width] or nullptr
+  float* weight;
+  int64_t weight_width;
+};
+
+struct PagedEvictParams {
+  PagedTable t;  // (offset nullptr, tokens 0)
+  int32_t d;
+  const int32_t* new_table;  // [batch, new_width]
+  int64_t new_width;
+  const float* weight_in;    // [batch, heads_kv, weight_width]
+  float* weight;             // or nullptr
+  int64_t weight_width;
+  int32_t keep, first, recent;
+  int32_t* kept;        // [batch, heads_kv, keep]
+  int32_t* new_length;  // [batch]
+};
+
+cudaError_t launch_paged_append(int dtype, const PagedAppendParams& prm, int sm_count, cudaStream_t stream);
+cudaError_t launch_paged_rows(int dtype, int head_dim, const PagedAttendParams& prm, cudaStream_t stream);
+cudaError_t launch_paged_weigh_rows(int dtype, int head_dim, const PagedWeighParams& prm, int sm_count,
+                                    cudaStream_t stream);
+cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, cudaStream_t stream);
+
+constexpr int kRowsTile = 16;   // query rows of an item of the row kernels
+constexpr int kRowsBlock = 16;  // keys of a block
+
+#ifdef __CUDACC__
+// A sequence of the batch.  Offsets that do not rise within 0..tokens, or a length that is
+// negative, smaller than the new tokens' count or beyond the page table: reported, and the
+// sequence has no tokens and no keys.
+struct PagedSeq {
+  int token0, count, length;
+  __device__ __forceinline__ int slot0() const { return length - count; }
+};
+__device__ __forceinline__ PagedSeq paged_seq(const PagedTable& t, int b) {
+  const int a = t.offset != nullptr ? __ldg(t.offset + b) : 0, e = t.offset != nullptr ? __ldg(t.offset + b + 1) : 0;
+  const int n = __ldg(t.length + b);
+  if (a < 0 || e < a || e > t.tokens || n < e - a || n > t.width * t.page_rows) {
+    atomicOr(t.status, kPagedStatusRange);
+    return {0, 0, 0};
+  }
+  return {a, e - a, n};
+}
+
+// Page of a sequence's entry; -1, and a report, where the table names none.
+__device__ __forceinline__ int paged_page(const PagedTable& t, int b, int entry) {
+  const int page = __ldg(t.page_table + b * t.width + entry);
+  if (page >= 0 && page < t.pages) return page;
+  atomicOr(t.status, kPagedStatusRange);
+  return -1;
+}
+
+// Row of the cache, as [rows, d], that holds a page's row (which: 0 keys, 1 values).
+__device__ __forceinline__ int64_t paged_row(const PagedTable& t, int page, int which, int head, int r) {
+  return (((int64_t)page * 2 + which) * t.heads_kv + head) * t.page_rows + r;
+}
+
+// The slots that some token of the slots [s0, s1] sees: [0, sink) and [lo, hi), sink <= lo.
+struct PagedSpan {
+  int sink, lo, hi;
+  __device__ __forceinline__ bool holds(int j) const { return j < hi && (j >= lo || j < sink); }
+};
+__device__ __forceinline__ PagedSpan paged_span(int window, int sinks, int s0, int s1) {
+  PagedSpan sp;
+  sp.hi = s1 + 1 > 0 ? s1 + 1 : 0;
+  sp.lo = window > 0 ? max(0, s0 - window + 1) : 0;
+  sp.sink = min(min(sinks, sp.lo), sp.hi);
+  return sp;
+}
+// The blocks of kB slots that a span touches, in order: the k-th is block at(k).
+template <int kB>
+struct PagedBlocks {
+  int head, skip, n;  // blocks of the sinks, then block head + skip on
+  __device__ __forceinline__ explicit PagedBlocks(const PagedSpan& sp) {
+    const int last = (sp.hi + kB - 1) / kB;
+    int first = sp.lo / kB;
+    head = (sp.sink + kB - 1) / kB;
+    if (sp.sink > 0 && head >= first) head = first = 0;  // the sinks' blocks reach the window's
+    skip = first - head;
+    n = last - skip;
+  }
+  __device__ __forceinline__ int at(int k) const { return k < head ? k : k + skip; }
+};
+// Whether token slot s sees slot j.
+__device__ __forceinline__ bool paged_sees(int window, int sinks, int s, int j) {
+  return j <= s && (window == 0 || j > s - window || j < sinks);
+}
+#endif
+
+}  // namespace ra

@@ -1,0 +1,561 @@
+// Attention over the paged cache for few query rows per sequence, and in float32 for any.
+//
+// For the 16 query rows of an item (rows of a key/value head's group and of the new tokens) and
+// the cached keys j that they see,
+//   m = max_j s_j,  s_j = scale * q.k_j,  l = sum_j e^(s_j - m),  O = sum_j e^(s_j - m) v_j / l,
+//   LSE = m + ln l,
+// folded block by block of 16 keys with the running maximum and sum.
+//
+// Bound by HBM: the keys and values are read once for the rows of a group.  bf16 takes the
+// warp-level tensor instruction m16n8k16 with the query rows as its 16 rows: for so few rows
+// the 5th-generation one would spend its 128 rows on padding, and the products are far from
+// the bound.  Each warp takes every fourth block of its CTA's share through a ring of its own
+// (cp.async, 16 bytes a lane, rows swizzled for ldmatrix); rows that no query sees arrive as zeros, so that what a page holds
+// there does not matter.  The warps' sums are joined in shared memory, the parts of an item
+// that several CTAs share by a second kernel, both in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "paged_share.cuh"
+#include "sm100_ptx.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;   // blocks of a warp's ring
+constexpr int kMinUnits = 16;  // of a share: four blocks a warp
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 16 bytes from global to shared memory, asynchronously; zeros where !live.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// A CTA's walk over its share: items and the units [u0, u1) of each.
+struct Walk {
+  int64_t x, x1, all;
+  int slots;
+  int b, tile;
+  int64_t item_x;  // the item's first unit
+  PagedSeq seq;
+};
+// Where this CTA's share begins; false where it has none.
+__device__ __forceinline__ bool walk_begin(const PagedAttendParams& P, const int64_t* prefix, Walk& w) {
+  w.all = prefix[P.t.batch];
+  w.slots = (int)max((int64_t)1, min((int64_t)P.slots, w.all / kMinUnits));
+  const int c = (int)blockIdx.x;
+  if (w.all == 0 || c >= w.slots) return false;
+  w.x = w.all * c / w.slots;
+  w.x1 = w.all * (c + 1) / w.slots;
+  w.b = paged_find(prefix, P.t.batch, w.x);
+  w.seq = paged_seq(P.t, w.b);
+  w.tile = paged_find_item<kRowsTile, kRowsBlock>(w.seq, P.group, P.window, P.sinks, w.x - prefix[w.b], w.item_x);
+  w.item_x += prefix[w.b];
+  return true;
+}
+// To the item at x (the share's current item is done).
+__device__ __forceinline__ void walk_next(const PagedAttendParams& P, const int64_t* prefix, Walk& w) {
+  w.item_x = w.x;
+  ++w.tile;
+  if (w.x < prefix[w.b + 1]) return;
+  while (w.b + 1 < P.t.batch && prefix[w.b + 1] <= w.x) ++w.b;
+  w.seq = paged_seq(P.t, w.b);
+  w.tile = 0;
+}
+
+// The part of an item that is cut: its sums in scratch, and, where it begins, how to join it.
+__device__ __forceinline__ int64_t part_at(const PagedAttendParams& P, const Walk& w, const PagedItem& it, int u0, int n) {
+  const int64_t me = (int64_t)blockIdx.y * P.slots + blockIdx.x;
+  if (u0 > 0) return me * 2;
+  if (threadIdx.x == 0) {
+    const int last = (int)(((w.item_x + n) * w.slots - 1) / w.all);
+    P.joins[me] = make_int4(w.seq.token0 * P.group + it.row0, it.rows, last, 0);
+  }
+  return me * 2 + 1;
+}
+
+// Where row `row` (over the tokens' groups) of this head lies.
+template <typename T>
+__device__ __forceinline__ T* row_of(const PagedStrides& s, const void* base, int group, int head, int row) {
+  const int token = row / group;
+  return static_cast<T*>(const_cast<void*>(base)) + token * s.token + (int64_t)(head * group + row - token * group) * s.head;
+}
+
+// ------------------------------------------------------------------------ bf16 --
+template <int D>
+struct Bf16 {
+  static constexpr int kRowBytes = D * 2;
+  static constexpr int kChunks = D / 8;  // of 16 bytes in a row
+  static constexpr int kBlockBytes = kRowsBlock * kRowBytes;
+  static constexpr int kRing = kWarps * kStages * 2 * kBlockBytes;
+  static constexpr int kJoinRow = D + 4;  // floats
+  static_assert(kWarps * kRowsTile * (kJoinRow + 2) * 4 <= kRing, "the warps' sums lie in the ring");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) rows_bf16_kernel(const PagedAttendParams P) {
+  using G = Bf16<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem + G::kRing);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
+  if (P.joins != nullptr && threadIdx.x == 0) P.joins[(int64_t)head * P.slots + blockIdx.x] = make_int4(0, 0, 0, 0);
+  paged_prefix<kRowsTile, kRowsBlock, kWarps>(P.t, P.group, P.window, P.sinks, prefix);
+  Walk w;
+  if (!walk_begin(P, prefix, w)) return;
+
+  const uint32_t ring = ptx::smem_addr(smem) + warp * kStages * 2 * G::kBlockBytes;
+  const __nv_bfloat16* cache = static_cast<const __nv_bfloat16*>(P.t.cache);
+  const int quad = lane >> 2, two = (lane & 3) * 2;
+  float* sums = reinterpret_cast<float*>(smem);
+  float2* stats = reinterpret_cast<float2*>(sums + kWarps * kRowsTile * G::kJoinRow);
+
+  for (;; walk_next(P, prefix, w)) {
+    const PagedItem it = paged_item<kRowsTile>(w.seq, P.group, w.tile);
+    const PagedSpan span = paged_span(P.window, P.sinks, it.s0, it.s1);
+    const PagedBlocks<kRowsBlock> blocks(span);
+    const int n = max(1, blocks.n);
+    const int u0 = (int)(w.x - w.item_x), u1 = (int)min((int64_t)n, w.x1 - w.item_x);
+    const int n_live = min(u1, blocks.n);
+    const int mine = n_live > u0 + warp ? (n_live - u0 - warp + kWarps - 1) / kWarps : 0;  // blocks of this warp
+
+    // The rows as the first operand: rows quad and quad + 8, channels two.. and two + 8..
+    RA_BOUNDS(P.t.status, it.row0 >= 0 && it.rows > 0 && w.seq.token0 + w.seq.count <= P.t.tokens && u0 >= 0 && u0 < u1 && u1 <= n, 116);
+    const int row_a = w.seq.token0 * P.group + it.row0 + quad;
+    uint32_t q[D / 16][4];
+    int slot[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool live = quad + 8 * i < it.rows;
+      slot[i] = live ? w.seq.slot0() + (it.row0 + quad + 8 * i) / P.group : -1;
+      const __nv_bfloat16* src = live ? row_of<const __nv_bfloat16>(P.qs, P.q, P.group, head, row_a + 8 * i) : nullptr;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          q[kk][i + 2 * e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + e * 8 + two)) : 0u;
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    // Block i of this warp into its ring; a lane keeps the page of one of the next 32.
+    int pages = -1;
+    uint32_t bad = 0u;  // stages whose page is none
+    auto load = [&](int i) {
+      if ((i & 31) == 0) {
+        const int k = u0 + warp + (i + lane) * kWarps;
+        pages = i + lane < mine ? paged_page(P.t, w.b, blocks.at(k) * kRowsBlock / P.t.page_rows) : -1;
+      }
+      if (i < mine) {
+        const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+        const int j0 = blocks.at(u0 + warp + i * kWarps) * kRowsBlock, s = i % kStages;
+        bad = page < 0 ? bad | (1u << s) : bad & ~(1u << s);
+        const int64_t row0 = paged_row(P.t, max(page, 0), 0, head, j0 % P.t.page_rows);
+        RA_BOUNDS(P.t.status, row0 >= 0 && row0 + kRowsBlock <= (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 111);
+        const int64_t to_v = (int64_t)P.t.heads_kv * P.t.page_rows * D;
+        const uint32_t dst = ring + s * 2 * G::kBlockBytes;
+#pragma unroll
+        for (int x = 0; x < G::kChunks / 2; ++x) {
+          const int id = lane + 32 * x, r = id / G::kChunks, ch = id % G::kChunks;
+          const bool live = page >= 0 && span.holds(j0 + r);
+          const __nv_bfloat16* src = cache + (row0 + r) * D + ch * 8;
+          const uint32_t to = dst + r * G::kRowBytes + ((ch ^ (r & 7)) * 16);
+          copy16(to, src, live);
+          copy16(to + G::kBlockBytes, src + to_v, live);
+        }
+      }
+      copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) load(i);
+    for (int i = 0; i < mine; ++i) {
+      copies_wait<kStages - 2>();
+      __syncwarp();
+      load(i + kStages - 1);
+      const int st = i % kStages;
+      const uint32_t kb = ring + st * 2 * G::kBlockBytes, vb = kb + G::kBlockBytes;
+      const int j0 = blocks.at(u0 + warp + i * kWarps) * kRowsBlock;
+      // Scores: rows x 16 keys, as two products of 8 keys.
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const int kr = (lane & 7) + ((lane >> 4) << 3);  // key of this lane's address; its half of 16 channels:
+      const int kc = (lane >> 3) & 1;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t r[4];
+        ldmatrix4(r, kb + kr * G::kRowBytes + (((2 * kk + kc) ^ (kr & 7)) * 16));
+        mma16816(s[0], q[kk], r[0], r[1]);
+        mma16816(s[1], q[kk], r[2], r[3]);
+      }
+      // Blocks that every row sees whole need no mask.
+      const bool whole = !((bad >> st) & 1u) && j0 + kRowsBlock - 1 <= it.s0 &&
+                         (P.window == 0 || j0 > it.s1 - P.window || j0 + kRowsBlock <= P.sinks);
+      if (!whole) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (((bad >> st) & 1u) || !paged_sees(P.window, P.sinks, slot[e >> 1], j0 + c * 8 + two + (e & 1)))
+              s[c][e] = -INFINITY;
+      }
+      uint32_t p[4];
+#pragma unroll
+      for (int i2 = 0; i2 < 2; ++i2) {  // rows quad, quad + 8
+        float mx = fmaxf(fmaxf(s[0][2 * i2], s[0][2 * i2 + 1]), fmaxf(s[1][2 * i2], s[1][2 * i2 + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float m_new = fmaxf(m[i2], mx * P.scale_log2);
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = ptx::ex2_approx(m[i2] - ref);  // (0 from -inf)
+        m[i2] = m_new;
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float a = ptx::ex2_approx(fmaf(s[c][2 * i2], P.scale_log2, -ref));
+          const float e = ptx::ex2_approx(fmaf(s[c][2 * i2 + 1], P.scale_log2, -ref));
+          sum += a + e;
+          p[i2 + 2 * c] = ptx::pack_bf16x2(a, e);
+        }
+        l[i2] = l[i2] * alpha + sum;
+        if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            o[c][2 * i2] *= alpha;
+            o[c][2 * i2 + 1] *= alpha;
+          }
+        }
+      }
+      // O += P V: 16 keys x 8 channels at a time.
+      const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t r[4];
+        ldmatrix4t(r, vb + vr * G::kRowBytes + (((2 * c + vc) ^ (vr & 7)) * 16));
+        mma16816(o[2 * c], p, r[0], r[1]);
+        mma16816(o[2 * c + 1], p, r[2], r[3]);
+      }
+      __syncwarp();
+    }
+    copies_wait<0>();
+    __syncthreads();  // every warp is done with its ring
+
+    // The warps' sums side by side, then joined.
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if ((lane & 3) == 0) stats[warp * kRowsTile + quad + 8 * i] = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+        *reinterpret_cast<float2*>(sums + (warp * kRowsTile + quad + 8 * i) * G::kJoinRow + c * 8 + two) =
+            make_float2(o[c][2 * i], o[c][2 * i + 1]);
+    }
+    __syncthreads();
+    const bool cut = u0 > 0 || u1 < n;
+    const int64_t part = cut ? part_at(P, w, it, u0, n) : 0;
+    for (int id = threadIdx.x; id < kRowsTile * G::kChunks; id += kThreads) {
+      const int r = id / G::kChunks, ch = id % G::kChunks;
+      float mr = -INFINITY, lr = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) mr = fmaxf(mr, stats[v * kRowsTile + r].x);
+      const float ref = mr == -INFINITY ? 0.f : mr;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float2 ml = stats[v * kRowsTile + r];
+        const float f = ptx::ex2_approx(ml.x - ref);
+        lr += ml.y * f;
+        const float4* src = reinterpret_cast<const float4*>(sums + (v * kRowsTile + r) * G::kJoinRow + ch * 8);
+        const float4 a = src[0], e = src[1];
+        x[0] += a.x * f, x[1] += a.y * f, x[2] += a.z * f, x[3] += a.w * f;
+        x[4] += e.x * f, x[5] += e.y * f, x[6] += e.z * f, x[7] += e.w * f;
+      }
+      if (cut) {
+        float4* dst = reinterpret_cast<float4*>(P.part_o + (part * kRowsTile + r) * D + ch * 8);
+        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+        if (ch == 0) P.part_ml[part * kRowsTile + r] = make_float2(mr, lr);
+      } else if (r < it.rows) {
+        const int row = w.seq.token0 * P.group + it.row0 + r;
+        const float inv = lr > 0.f ? 1.0f / lr : (lr == 0.f ? 0.f : lr);
+        __nv_bfloat16* dst = row_of<__nv_bfloat16>(P.os, P.o, P.group, head, row) + ch * 8;
+        uint4 y;
+        y.x = ptx::pack_bf16x2(x[0] * inv, x[1] * inv);
+        y.y = ptx::pack_bf16x2(x[2] * inv, x[3] * inv);
+        y.z = ptx::pack_bf16x2(x[4] * inv, x[5] * inv);
+        y.w = ptx::pack_bf16x2(x[6] * inv, x[7] * inv);
+        *reinterpret_cast<uint4*>(dst) = y;
+        if (ch == 0 && P.lse != nullptr) {
+          const int token = row / P.group;
+          P.lse[(int64_t)token * P.heads_q + head * P.group + row - token * P.group] =
+              lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2;
+        }
+      }
+    }
+    __syncthreads();  // the ring is free for the next item
+    w.x = w.item_x + u1;
+    if (w.x >= w.x1) return;
+  }
+}
+
+// --------------------------------------------------------------------- float32 --
+// A CTA meets 32 keys (two blocks) at a time; a warp has 4 of the 16 rows, a lane scores one
+// key against them, and then holds D / 32 channels of their outputs.
+template <int D>
+struct F32 {
+  static constexpr int kRow = D + 4;  // floats; 8 lanes' 16-byte reads of a column fall into different banks
+  static constexpr int kKeys = 2 * kRowsBlock;
+  static constexpr int kStage = 2 * kKeys * kRow * 4;
+  static constexpr int kQ = kRowsTile * D * 4;
+  static constexpr int kBytes = 2 * kStage + kQ;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendParams P) {
+  using G = F32<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* qs = reinterpret_cast<float*>(smem + 2 * G::kStage);
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem + G::kBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
+  if (P.joins != nullptr && threadIdx.x == 0) P.joins[(int64_t)head * P.slots + blockIdx.x] = make_int4(0, 0, 0, 0);
+  paged_prefix<kRowsTile, kRowsBlock, kWarps>(P.t, P.group, P.window, P.sinks, prefix);
+  Walk w;
+  if (!walk_begin(P, prefix, w)) return;
+  const float* cache = static_cast<const float*>(P.t.cache);
+  constexpr int kPer = kRowsTile / kWarps, kCh = D / 32;
+
+  for (;; walk_next(P, prefix, w)) {
+    const PagedItem it = paged_item<kRowsTile>(w.seq, P.group, w.tile);
+    const PagedSpan span = paged_span(P.window, P.sinks, it.s0, it.s1);
+    const PagedBlocks<kRowsBlock> blocks(span);
+    const int n = max(1, blocks.n);
+    const int u0 = (int)(w.x - w.item_x), u1 = (int)min((int64_t)n, w.x1 - w.item_x);
+    const int n_live = min(u1, blocks.n);
+    const int steps = n_live > u0 ? (n_live - u0 + 1) / 2 : 0;
+    RA_BOUNDS(P.t.status, it.row0 >= 0 && it.rows > 0 && w.seq.token0 + w.seq.count <= P.t.tokens && u0 >= 0 && u0 < u1 && u1 <= n, 117);
+    const int row0 = w.seq.token0 * P.group + it.row0;
+    for (int id = threadIdx.x; id < kRowsTile * (D / 4); id += kThreads) {
+      const int r = id / (D / 4), ch = id % (D / 4);
+      reinterpret_cast<float4*>(qs)[id] = r < it.rows
+          ? __ldg(reinterpret_cast<const float4*>(row_of<const float>(P.qs, P.q, P.group, head, row0 + r)) + ch)
+          : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // Slot of key i of a step; -1 past the share's end.
+    auto slot_of = [&](int step, int i) {
+      const int k = u0 + 2 * step + (i >> 4);
+      return k < n_live ? blocks.at(k) * kRowsBlock + (i & 15) : -1;
+    };
+    auto load = [&](int step) {
+      if (step < steps) {
+        float* dst = reinterpret_cast<float*>(smem + (step & 1) * G::kStage);
+        for (int id = threadIdx.x; id < G::kKeys * (D / 4); id += kThreads) {
+          const int i = id / (D / 4), ch = id % (D / 4), j = slot_of(step, i);
+          const int page = j >= 0 && span.holds(j) ? paged_page(P.t, w.b, j / P.t.page_rows) : -1;
+          const float* src = cache + paged_row(P.t, max(page, 0), 0, head, max(j, 0) % P.t.page_rows) * D + ch * 4;
+          const uint32_t to = ptx::smem_addr(dst + i * G::kRow + ch * 4);
+          copy16(to, src, page >= 0);
+          copy16(to + G::kKeys * G::kRow * 4, src + (int64_t)P.t.heads_kv * P.t.page_rows * D, page >= 0);
+        }
+      }
+      copies_commit();
+    };
+    int slot[kPer];
+    float m[kPer], l[kPer], acc[kPer][kCh];
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      const int row = warp * kPer + r;
+      slot[r] = row < it.rows ? w.seq.slot0() + (it.row0 + row) / P.group : -1;
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kCh; ++c) acc[r][c] = 0.f;
+    }
+    load(0);
+    for (int step = 0; step < steps; ++step) {
+      load(step + 1);
+      copies_wait<1>();
+      __syncthreads();
+      const float* ks = reinterpret_cast<const float*>(smem + (step & 1) * G::kStage);
+      const float* vs = ks + G::kKeys * G::kRow;
+      float s[kPer];
+#pragma unroll
+      for (int r = 0; r < kPer; ++r) s[r] = 0.f;
+#pragma unroll 8
+      for (int c = 0; c < D / 4; ++c) {
+        const float4 k4 = *reinterpret_cast<const float4*>(ks + lane * G::kRow + c * 4);
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) {
+          const float4 q4 = *reinterpret_cast<const float4*>(qs + (warp * kPer + r) * D + c * 4);
+          s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
+        }
+      }
+      const int j = slot_of(step, lane);
+      const bool there = j >= 0 && span.holds(j) && paged_page(P.t, w.b, j / P.t.page_rows) >= 0;
+      float p[kPer];
+#pragma unroll
+      for (int r = 0; r < kPer; ++r) {
+        const float x = there && paged_sees(P.window, P.sinks, slot[r], j) ? s[r] : -INFINITY;
+        float mx = x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float m_new = fmaxf(m[r], mx * P.scale_log2);
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = exp2f(m[r] - ref);
+        m[r] = m_new;
+        p[r] = exp2f(fmaf(x, P.scale_log2, -ref));
+        l[r] = l[r] * alpha + p[r];
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) acc[r][c] *= alpha;
+      }
+#pragma unroll 4
+      for (int i = 0; i < G::kKeys; ++i) {
+        float v[kCh];
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) v[c] = vs[i * G::kRow + lane + 32 * c];
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) {
+          const float pr = __shfl_sync(0xffffffffu, p[r], i);
+#pragma unroll
+          for (int c = 0; c < kCh; ++c) acc[r][c] = fmaf(pr, v[c], acc[r][c]);
+        }
+      }
+      __syncthreads();
+    }
+    copies_wait<0>();
+    const bool cut = u0 > 0 || u1 < n;
+    const int64_t part = cut ? part_at(P, w, it, u0, n) : 0;
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+      const int at = warp * kPer + r;
+      if (cut) {
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) P.part_o[(part * kRowsTile + at) * D + lane + 32 * c] = acc[r][c];
+        if (lane == 0) P.part_ml[part * kRowsTile + at] = make_float2(m[r], l[r]);
+      } else if (at < it.rows) {
+        const int row = row0 + at;
+        const float inv = l[r] > 0.f ? 1.0f / l[r] : (l[r] == 0.f ? 0.f : l[r]);
+        float* dst = row_of<float>(P.os, P.o, P.group, head, row);
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) dst[lane + 32 * c] = acc[r][c] * inv;
+        if (lane == 0 && P.lse != nullptr) {
+          const int token = row / P.group;
+          P.lse[(int64_t)token * P.heads_q + head * P.group + row - token * P.group] =
+              l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+        }
+      }
+    }
+    __syncthreads();
+    w.x = w.item_x + u1;
+    if (w.x >= w.x1) return;
+  }
+}
+
+// ---------------------------------------------------------------- cut items --
+// The item that slot x's share begins and does not end: its first part there, the others at the
+// beginning of the slots up to the last.  A thread has 4 channels of a row.
+template <typename T, int D>
+__global__ void __launch_bounds__(kRowsTile * D / 4) rows_join_kernel(const PagedAttendParams P) {
+  const int head = (int)blockIdx.y;
+  const int64_t me = (int64_t)head * P.slots + blockIdx.x;
+  const int4 rec = P.joins[me];
+  const int r = threadIdx.x / (D / 4), ch = threadIdx.x % (D / 4);
+  if (r >= rec.y) return;
+  const int count = rec.z - (int)blockIdx.x + 1;
+  auto part = [&](int i) { return (i == 0 ? me * 2 + 1 : (me + i) * 2) * kRowsTile + r; };
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) m = fmaxf(m, P.part_ml[part(i)].x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const float2 ml = P.part_ml[part(i)];
+    const float f = exp2f(ml.x - ref);
+    const float4 y = *reinterpret_cast<const float4*>(P.part_o + part(i) * D + ch * 4);
+    l = fmaf(ml.y, f, l);
+    x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+  }
+  const int row = rec.x + r;
+  const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+  T* dst = row_of<T>(P.os, P.o, P.group, head, row) + ch * 4;
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(ptx::pack_bf16x2(x.x * inv, x.y * inv), ptx::pack_bf16x2(x.z * inv, x.w * inv));
+  } else {
+    *reinterpret_cast<float4*>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  }
+  if (ch == 0 && P.lse != nullptr) {
+    const int token = row / P.group;
+    P.lse[(int64_t)token * P.heads_q + head * P.group + row - token * P.group] =
+        l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
+template <typename Kernel>
+cudaError_t raise_smem(Kernel kernel, std::atomic<int>* ready, int bytes) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  if (cached && ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && cached) ready[dev].store(1, std::memory_order_release);
+  return e;
+}
+
+template <typename T, int D>
+cudaError_t launch(const PagedAttendParams& prm, cudaStream_t stream) {
+  const dim3 grid((unsigned)prm.slots, (unsigned)prm.t.heads_kv);
+  const int prefix = (prm.t.batch + 1) * 8, most = (kMaxSequences + 1) * 8;
+  static std::atomic<int> ready[kMaxDevices];
+  if constexpr (sizeof(T) == 2) {
+    const cudaError_t e = raise_smem(rows_bf16_kernel<D>, ready, Bf16<D>::kRing + most);
+    if (e != cudaSuccess) return e;
+    rows_bf16_kernel<D><<<grid, kThreads, Bf16<D>::kRing + prefix, stream>>>(prm);
+  } else {
+    const cudaError_t e = raise_smem(rows_f32_kernel<D>, ready, F32<D>::kBytes + most);
+    if (e != cudaSuccess) return e;
+    rows_f32_kernel<D><<<grid, kThreads, F32<D>::kBytes + prefix, stream>>>(prm);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || prm.slots == 1) return e;
+  rows_join_kernel<T, D><<<grid, kRowsTile * D / 4, 0, stream>>>(prm);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_rows(int dtype, int head_dim, const PagedAttendParams& prm, cudaStream_t stream) {
+  if (dtype == RA_DTYPE_BF16)
+    return head_dim == 128 ? launch<__nv_bfloat16, 128>(prm, stream) : launch<__nv_bfloat16, 64>(prm, stream);
+  return head_dim == 128 ? launch<float, 128>(prm, stream) : launch<float, 64>(prm, stream);
+}
+
+}  // namespace ra

@@ -583,6 +583,246 @@ ra_status ra_kv4_attend_scratch_size(ra_kv4_t kv, int64_t batch, int64_t rows, i
  */
 ra_status ra_kv4_sync_status(ra_kv4_t kv, void* stream);
 
+/*
+ * ra_rope_*: rotary positions.  No counterpart on the pages, whose attention takes queries and
+ * keys as they come: a model that uses the ring rotates them by their positions in the whole
+ * sequence first, which a shard's rows do not show by their place.
+ *
+ * The first rotary_dim channels of a row form pairs: channels j and j + rotary_dim/2, or
+ * interleaved 2j and 2j + 1 (j < rotary_dim/2).  At position n the pair (x1, x2) becomes
+ *   A (x1 cos a - x2 sin a),  A (x1 sin a + x2 cos a),  a = n * w_j,
+ * and the other channels are copied.  w_j = base^(-2j / rotary_dim), scaled for contexts longer
+ * than `original` tokens:
+ *   NONE    as it is;
+ *   LINEAR  w_j / factor (positions interpolated);
+ *   BASE    base * factor^(rotary_dim / (rotary_dim - 2)) in place of base (rotary_dim 2: as it is);
+ *   BANDS   t_j w_j + (1 - t_j) w_j / factor, t_j = (r_j - low) / (high - low) held to 0..1, where
+ *           r_j = original * w_j / 2 pi are the pair's turns within `original` tokens;
+ *   RAMP    (1 - t_j) w_j + t_j w_j / factor, t_j = (j - j0) / (j1 - j0) held to 0..1, where j0 =
+ *           max(floor(i(high)), 0), j1 = min(ceil(i(low)), rotary_dim - 1), j1 - j0 at least 0.001,
+ *           and i(r) = rotary_dim * ln(original / 2 pi r) / (2 ln base).
+ * Angles are taken modulo a turn exactly (64-bit fractions of a turn), products and sums in
+ * float32, one rounding to the dtype.
+ */
+typedef enum {
+  RA_ROPE_NONE = 0,
+  RA_ROPE_LINEAR = 1,
+  RA_ROPE_BASE = 2,
+  RA_ROPE_BANDS = 3,
+  RA_ROPE_RAMP = 4
+} ra_rope_scaling;
+
+typedef struct {
+  int32_t head_dim;     /* d, 2..1024                                           */
+  int32_t rotary_dim;   /* channels that are rotated, the first ones: even, <= d */
+  int32_t interleaved;  /* 0: channels j and j + rotary_dim/2; 1: 2j and 2j + 1  */
+  int32_t dtype;        /* ra_dtype of the rows                                 */
+  double base;          /* > 1                                                  */
+  int32_t scaling;      /* ra_rope_scaling                                      */
+  double factor;        /* >= 1 (scaling other than NONE)                       */
+  int64_t original;     /* >= 1 (BANDS, RAMP)                                   */
+  double low, high;     /* turns within `original` tokens, 0 < low < high (BANDS, RAMP) */
+  double amplitude;     /* A; 0 selects 1                                       */
+} ra_rope_problem;
+
+typedef struct ra_rope_s* ra_rope_t;
+
+/*
+ * ra_rope_plan -- validate a rotation's description and compute its speeds (in float64).  The
+ * handle owns a small device table and one event per stream it was used on (host-only without
+ * a device, as ra_plan).  Release it with ra_rope_destroy, after the graphs that captured its
+ * calls.  One host thread at a time may use a handle; its calls may overlap on the GPU.
+ * Errors: RA_ERR_INVALID_ARG (null arguments, sizes, bad enum or factor), RA_ERR_UNSUPPORTED
+ * (head_dim above 1024), RA_ERR_CUDA.
+ */
+ra_status ra_rope_plan(const ra_rope_problem* prob, ra_rope_t* out);
+
+/* Release a handle (NULL is accepted).  It does not wait, as ra_plan_destroy. */
+ra_status ra_rope_destroy(ra_rope_t rope);
+
+/*
+ * ra_rope -- rotate queries and keys in one launch.
+ * q, q_out: [batch, heads_q, seq, d]; k, k_out: [batch, heads_kv, seq, d] (heads_kv 0: none, and
+ * NULL pointers).  Each has its own strides (host arrays of 3: batch, head, row, in elements, not
+ * negative; the d channels of a row follow each other), so that projections' outputs are read
+ * where they lie and the ring's tensors are written in order.  Rows are written once: strides of
+ * an output that put two rows in one place are refused, and an output may be its own input (the
+ * same pointer and strides), but not overlap an input otherwise.
+ * position: [batch, seq] int32, any value; NULL: row i of shard p stands at pos(p, i) of the
+ * layout (see above; seq has to divide into its shards), the natural position.
+ * Device pointers aligned to their elements (position: 4 bytes); 16-byte aligned rows of
+ * rotary_dim and d multiples of 32 bytes go 16 bytes at a time.  Asynchronous on stream;
+ * allocates nothing.
+ * Errors: RA_ERR_INVALID_ARG (null/misaligned pointers, sizes, strides, layout),
+ * RA_ERR_UNSUPPORTED (batch * seq * d above 2^38, more than 2^20 heads), RA_ERR_NO_DEVICE,
+ * RA_ERR_CUDA.
+ */
+ra_status ra_rope(ra_rope_t rope, int64_t batch, int64_t seq, int32_t heads_q, int32_t heads_kv, int32_t layout,
+                  int32_t n_shards, const int32_t* position, const void* q, const int64_t* q_strides, const void* k,
+                  const int64_t* k_strides, void* q_out, const int64_t* q_out_strides, void* k_out,
+                  const int64_t* k_out_strides, void* stream);
+
+/*
+ * ra_rope_bwd -- gradients with respect to what ra_rope was given, from those with respect to
+ * what it returned: the transposed rotation, A (y1 cos a + y2 sin a), A (y2 cos a - y1 sin a).
+ * Everything else as for ra_rope.
+ */
+ra_status ra_rope_bwd(ra_rope_t rope, int64_t batch, int64_t seq, int32_t heads_q, int32_t heads_kv, int32_t layout,
+                      int32_t n_shards, const int32_t* position, const void* dq, const int64_t* dq_strides,
+                      const void* dk, const int64_t* dk_strides, void* dq_out, const int64_t* dq_out_strides,
+                      void* dk_out, const int64_t* dk_out_strides, void* stream);
+
+/*
+ * ra_paged_*: a paged key/value cache in the tensors' own type, filled chunk by chunk, the
+ * attention of new tokens over it, and its eviction by accumulated attention weight.  No
+ * counterpart on the pages: prompts that arrive in pieces, and sequences continued from them.
+ *
+ * The cache is one caller-owned device buffer [pages, 2, Hkv, page_rows, d]: a page's keys, then
+ * its values.  Slot x of sequence b lies in page page_table[b][x / page_rows], at row
+ * x % page_rows.
+ *
+ * A call takes a packed batch: the new tokens of `batch` sequences one after the other, tensors
+ * [tokens, heads, d] with strides of their own (host arrays of 2: token, head, in elements,
+ * multiples of 16 bytes).  Sequence b has the tokens offset[b] .. offset[b+1] - 1 (none is fine)
+ * and, those among them, length[b] slots in use: its i-th new token has slot length[b] -
+ * (offset[b+1] - offset[b]) + i.  Tokens before offset[0] and from offset[batch] on belong to no
+ * sequence; nothing is read or written for them.
+ * page_table: [batch, table_width] int32; offset: [batch + 1] int32; length: [batch] int32, all
+ * on the device and read by the kernels, so that a captured graph follows them.  Sequences may
+ * share pages for reading; a place is written by one row of a call only.
+ *
+ * Offsets that fall or leave 0..tokens, lengths that are negative, smaller than the sequence's
+ * new tokens or beyond its page table, and page indices outside the pool are found by the
+ * kernels: such sequences are left out (their rows stay as they were), the slots of such pages
+ * are not written, not moved and not attended to, and ra_paged_sync_status reports them.
+ * Entries of the page table for slots that no token of the call sees are not read.
+ */
+typedef struct {
+  int64_t pages;      /* pages of the pool, >= 1                                    */
+  int32_t page_rows;  /* slots of a page: a multiple of 16, 16..65536               */
+  int32_t heads_q;    /* Hq >= 1, multiple of heads_kv                              */
+  int32_t heads_kv;   /* Hkv >= 1                                                   */
+  int32_t head_dim;   /* d: 64 or 128                                               */
+  int32_t dtype;      /* ra_dtype of the cache, Q, K, V and O                       */
+  int64_t window;     /* as ra_plan_window's, counted in slots; 0: the whole prefix */
+  int64_t sinks;      /* as ra_plan_window's                                        */
+  float scale;        /* score scale; 0 selects 1/sqrt(head_dim)                    */
+} ra_paged_problem;
+
+typedef struct ra_paged_s* ra_paged_t;
+
+/*
+ * ra_paged_plan -- validate a cache's description and create its handle, which owns a device
+ * status word and one event per stream its kernels were launched on (host-only without a
+ * device, as ra_plan).  Release it with ra_paged_destroy, after the graphs that captured its
+ * calls.  One host thread at a time may use a handle; its calls may overlap on the GPU.
+ * Errors: RA_ERR_INVALID_ARG (null arguments, sizes < 1, page_rows, Hq % Hkv, window or sinks
+ * < 0, bad enum or scale), RA_ERR_UNSUPPORTED (head_dim, more than 65535 key/value heads, more
+ * than 2^31-1 rows of d channels), RA_ERR_CUDA.
+ */
+ra_status ra_paged_plan(const ra_paged_problem* prob, ra_paged_t* out);
+
+/* Release a handle (NULL is accepted).  It does not wait, as ra_plan_destroy. */
+ra_status ra_paged_destroy(ra_paged_t kv);
+
+/*
+ * ra_paged_append -- the new tokens' keys and values into the cache, in one launch with the
+ * rotation of their keys and queries.
+ * k, v: [tokens, Hkv, d]; q, q_out: [tokens, Hq, d], or both NULL.
+ * rope: the rotation of keys and queries (of the cache's dtype and head_dim); NULL: keys are
+ * written as they are, and q has to be NULL.  Results are those of ra_rope, bit for bit.
+ * position: [tokens] int32, the tokens' positions in the rotation; NULL: their slots (the same
+ * until an eviction has moved slots together).
+ * q_out may be q with the same strides; no output may overlap an input otherwise.
+ * Device pointers, 16-byte aligned (page_table, offset, length, position: 4-byte).
+ * Asynchronous on stream; allocates nothing.
+ * Errors: RA_ERR_INVALID_ARG (null/misaligned pointers, sizes < 1, strides, a rotation of
+ * another type), RA_ERR_UNSUPPORTED (table_width * page_rows above 2^30, more than 4096
+ * sequences, tokens * (Hq + 2 Hkv) above 2^30), RA_ERR_NO_DEVICE, RA_ERR_CUDA.
+ */
+ra_status ra_paged_append(ra_paged_t kv, ra_rope_t rope, void* cache, int64_t batch, int64_t tokens, const void* k,
+                          const int64_t* k_strides, const void* v, const int64_t* v_strides, const void* q,
+                          const int64_t* q_strides, void* q_out, const int64_t* q_out_strides,
+                          const int32_t* page_table, int64_t table_width, const int32_t* offset,
+                          const int32_t* length, const int32_t* position, void* stream);
+
+/*
+ * ra_paged_attend -- attention of the new tokens over their sequences' slots (their own among
+ * them: append them first).  A token at slot s sees the slots j <= s, within the handle's
+ * window and sinks (j > s - window or j < sinks).
+ * q, o: [tokens, Hq, d]; lse: [tokens, Hq] float32, contiguous (may be NULL).  A token all of
+ * whose slots lie in pages out of range gets O = 0, LSE = -inf.
+ * Slots that no token of the call sees may hold anything.  Values that some of them see must be
+ * finite: they enter the products of the others with weight zero.
+ * bf16: the softmax weights are rounded to bf16 for the second product; sums are fp32.
+ * scratch: ra_paged_attend_scratch_size bytes (NULL when that is 0), not shared by calls that
+ * may overlap.  o may not overlap an input.
+ * Device pointers, 16-byte aligned (page_table, offset, length, lse: 4-byte).  Asynchronous on
+ * stream; allocates nothing.
+ * Errors: as ra_paged_append.
+ */
+ra_status ra_paged_attend(ra_paged_t kv, const void* cache, int64_t batch, int64_t tokens, const void* q,
+                          const int64_t* q_strides, const int32_t* page_table, int64_t table_width,
+                          const int32_t* offset, const int32_t* length, void* o, const int64_t* o_strides,
+                          float* lse, float* scratch, void* stream);
+
+/* Bytes of ra_paged_attend's scratch for these sizes (0 when it needs none).  Host only.
+ * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED as ra_paged_attend. */
+ra_status ra_paged_attend_scratch_size(ra_paged_t kv, int64_t batch, int64_t tokens, int64_t table_width,
+                                       int64_t* bytes);
+
+/*
+ * ra_paged_weigh -- the attention weight that every slot receives from the new tokens, added to
+ * what it received before: for slot j < length[b] of key/value head h,
+ *   weight[b, h, j] = (weight_in[b, h, j] for slots before the call's tokens, else 0)
+ *                     + sum over the tokens and query heads of the group that see j of
+ *                       e^(scale q.k_j - LSE).
+ * q: [tokens, Hq, d] as in ra_paged_attend; lse: [tokens, Hq] float32, what that call returned.
+ * weight_in, weight: [batch, Hkv, weight_width] float32, contiguous; weight_in may be weight, or
+ * NULL (zeros).  Slots from length[b] on stay as they were, and so do slots in pages out of
+ * range; slots from weight_width on are reported (ra_paged_sync_status).  Deterministic.
+ * Device pointers, 16-byte aligned (tables, lse and weights: 4-byte).  Asynchronous on stream;
+ * allocates nothing.
+ * Errors: as ra_paged_append (weight_width outside 1..2^30: RA_ERR_INVALID_ARG).
+ */
+ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_t tokens, const void* q,
+                         const int64_t* q_strides, const float* lse, const int32_t* page_table,
+                         int64_t table_width, const int32_t* offset, const int32_t* length,
+                         const float* weight_in, float* weight, int64_t weight_width, void* stream);
+
+/*
+ * ra_paged_evict -- keep at most `keep` slots of every sequence and key/value head: its `first`
+ * first ones, its `recent` last ones, and of the others the heaviest; ties go to the lowest slot,
+ * NaN counts as lighter than anything.  A sequence of up to `keep` slots keeps them all.  The
+ * slots that stay move together in their order, each head by itself: slot kept[b, h, i] becomes
+ * slot i.
+ * length: [batch] int32.  weight_in: [batch, Hkv, weight_width] float32, weight (may be weight_in
+ * or NULL) receives the weights of the slots that stay; other entries stay as they were.
+ * new_table: [batch, new_width] int32, the pages that the sequences have afterwards: page_table
+ * itself (in place), an array with the same entries, or pages that no sequence of the call has
+ * (the old pages then keep what they hold, for others that share them).
+ * kept: [batch, Hkv, keep] int32, -1 behind the last; new_length: [batch] int32 (not length).
+ * A sequence whose length is beyond the page table or weight_width, or whose slots do not fit in
+ * new_width pages, is left as it is, with new_length 0, and reported.
+ * Rotated keys stay valid: they keep the positions that they were rotated by; later tokens are
+ * appended with positions of their own.
+ * Device pointers, 16-byte aligned (tables and weights: 4-byte).  Asynchronous on stream;
+ * allocates nothing.
+ * Errors: as ra_paged_append (keep, first, recent, new_width, weight_width: RA_ERR_INVALID_ARG).
+ */
+ra_status ra_paged_evict(ra_paged_t kv, void* cache, int64_t batch, const int32_t* page_table, int64_t table_width,
+                         const int32_t* length, const float* weight_in, float* weight, int64_t weight_width,
+                         int64_t keep, int64_t first, int64_t recent, const int32_t* new_table, int64_t new_width,
+                         int32_t* kept, int32_t* new_length, void* stream);
+
+/*
+ * ra_paged_sync_status -- synchronize `stream`, then read and clear the handle's status word:
+ * RA_ERR_INVALID_ARG when a call since the last one met a page index, offset, length or slot out
+ * of range, RA_ERR_TIMEOUT when a device-side wait ran out of budget, RA_ERR_CUDA on a CUDA
+ * error, RA_ERR_BOUNDS when a bounds check of the debug build failed, RA_OK otherwise.
+ */
+ra_status ra_paged_sync_status(ra_paged_t kv, void* stream);
+
 /* Thread-local message describing the last failure on this thread ("" if none). */
 const char* ra_last_error(void);
 
