@@ -40,6 +40,7 @@ ra_status ok() {
 
 constexpr int64_t kMaxPositions = int64_t(1) << 30;  // of a sequence: slot arithmetic stays in 32 bits
 constexpr int kMaxSlots = 1024;                      // CTAs of a key/value head
+constexpr int64_t kMaxChunkSlots = int64_t(1) << 25;  // of a sequence in the chunk kernel: an item ends well within its wait budget
 
 ra_status validate(const ra_paged_problem* p) {
   if (p->pages < 1 || p->heads_q < 1 || p->heads_kv < 1 || p->head_dim < 1)
@@ -88,9 +89,9 @@ ra_status strides_of(const ra_paged_s* kv, const char* what, const int64_t* s, i
                      ra::PagedStrides* out) {
   if (s == nullptr) return fail(RA_ERR_INVALID_ARG, "%s: null strides", what);
   *out = {s[0], s[1]};
-  const int64_t d = kv->prob.head_dim, e = elem_bytes(kv->prob), most = int64_t(1) << 40;
+  const int64_t d = kv->prob.head_dim, e = elem_bytes(kv->prob), most = int64_t(1) << 38;
   if (s[0] < 0 || s[1] < 0 || s[0] > most || s[1] > most)
-    return fail(RA_ERR_INVALID_ARG, "%s: a stride is negative or beyond 2^40 elements", what);
+    return fail(RA_ERR_INVALID_ARG, "%s: a stride is negative or beyond 2^38 elements", what);
   if (s[0] * e % 16 || s[1] * e % 16) return fail(RA_ERR_INVALID_ARG, "%s: strides are not multiples of 16 bytes", what);
   if (!written) return RA_OK;
   const bool heads_inside = s[1] <= s[0];
@@ -136,6 +137,30 @@ int row_slots(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width
   const int64_t sms = kv->sm_count > 0 ? kv->sm_count : 148;
   return (int)std::max<int64_t>(1, std::min({shares, 2 * sms / pb.heads_kv, (int64_t)kMaxSlots}));
 }
+
+// Shares of a CTA of the chunk kernel at most: where more than one item reads a sequence's keys,
+// and these may be more than a round's (paged_chunk_sm103.cu).
+int chunk_rounds(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width) {
+  const ra_paged_problem& pb = kv->prob;
+  if (tokens <= 2 * (128 / (pb.heads_q / pb.heads_kv))) return 1;
+  const int64_t bytes = std::min(batch, tokens) * width * pb.page_rows * pb.heads_kv * 4 / 1024 * pb.head_dim;  // KiB
+  return (int)std::max<int64_t>(1, std::min<int64_t>(ra::kMaxRounds, bytes / (64 << 10)));
+}
+
+// Whether a call goes to the chunk kernel, whose query tiles have 128 rows: from 16 rows per
+// sequence and head on in the mean.
+bool takes_chunks(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width) {
+  const ra_paged_problem& pb = kv->prob;
+  const int64_t group = pb.heads_q / pb.heads_kv;
+  return pb.dtype == RA_DTYPE_BF16 && group <= 128 && batch <= ra::kMaxChunkSequences &&
+         width * pb.page_rows <= kMaxChunkSlots && tokens * group > 16 * batch;
+}
+
+int64_t chunk_scratch(const ra_paged_s* kv, int64_t shares) {
+  const int64_t rows = shares * 2 * 2 * 128;
+  return rows * (kv->prob.head_dim * 4 + 16) + shares * 16;
+}
+int chunk_grid(const ra_paged_s* kv) { return kv->sm_count > 0 ? kv->sm_count : 148; }
 
 int64_t rows_scratch(const ra_paged_s* kv, int slots) {
   if (slots == 1) return 0;
@@ -255,7 +280,9 @@ ra_status ra_paged_attend_scratch_size(ra_paged_t kv, int64_t batch, int64_t tok
   if (kv == nullptr || bytes == nullptr) return fail(RA_ERR_INVALID_ARG, "null argument");
   const ra_status s = check_sizes(kv, batch, tokens, table_width);
   if (s != RA_OK) return s;
-  *bytes = rows_scratch(kv, row_slots(kv, batch, tokens, table_width));
+  *bytes = takes_chunks(kv, batch, tokens, table_width)
+               ? chunk_scratch(kv, (int64_t)chunk_grid(kv) * chunk_rounds(kv, batch, tokens, table_width))
+               : rows_scratch(kv, row_slots(kv, batch, tokens, table_width));
   return ok();
 }
 
@@ -273,15 +300,44 @@ ra_status ra_paged_attend(ra_paged_t kv, const void* cache, int64_t batch, int64
   s = strides_of(kv, "q", q_strides, tokens, pb.heads_q, false, &prm.qs);
   if (s == RA_OK) s = strides_of(kv, "o", o_strides, tokens, pb.heads_q, true, &prm.os);
   if (s != RA_OK) return s;
-  const int slots = row_slots(kv, batch, tokens, table_width);
-  if (rows_scratch(kv, slots) > 0 && scratch == nullptr)
+  if ((tokens > 1 && prm.qs.token == 0) || (pb.heads_q > 1 && prm.qs.head == 0))
+    return fail(RA_ERR_INVALID_ARG, "q: rows lie in one place");
+  const bool chunks = takes_chunks(kv, batch, tokens, table_width);
+  const int slots = chunks ? 0 : row_slots(kv, batch, tokens, table_width);
+  if (slots != 1 && scratch == nullptr)
     return fail(RA_ERR_INVALID_ARG, "null scratch (ra_paged_attend_scratch_size bytes are needed)");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const void* t16[] = {cache, q, o, slots > 1 ? scratch : nullptr};
+  const void* t16[] = {cache, q, o, slots != 1 ? scratch : nullptr};
   const void* t4[] = {page_table, offset, length, lse};
   s = check_call(kv, batch, tokens, table_width, t16, 4, t4, 4, st);
   if (s != RA_OK) return s;
   prm.t = table_of(kv, cache, batch, tokens, page_table, table_width, offset, length);
+  if (chunks) {
+    ra::PagedChunkParams c{};
+    c.t = prm.t;
+    c.heads_q = pb.heads_q;
+    c.group = pb.heads_q / pb.heads_kv;
+    c.window = (int32_t)std::min(pb.window, kMaxPositions);
+    c.sinks = pb.window > 0 ? (int32_t)std::min(pb.sinks, kMaxPositions) : 0;
+    for (c.piece = 16; c.piece < 128 && pb.page_rows % (2 * c.piece) == 0;) c.piece *= 2;
+    c.rounds = chunk_rounds(kv, batch, tokens, table_width);
+    c.row_bytes = pb.head_dim * 2;
+    c.scale_log2 = pb.scale * 1.4426950408889634f;
+    c.q = q;
+    c.o = o;
+    c.qs = prm.qs;
+    c.os = prm.os;
+    c.lse = lse;
+    const int grid = chunk_grid(kv);
+    const int64_t shares = (int64_t)grid * c.rounds, rows = shares * 2 * 2 * 128;
+    c.part_o = scratch;
+    c.part_ml = reinterpret_cast<float4*>(scratch + rows * pb.head_dim);
+    c.joins = reinterpret_cast<ra::PagedJoin*>(c.part_ml + rows);
+    const char* why = "";
+    const cudaError_t e = ra::launch_paged_chunk(pb.head_dim, c, grid, st, &why);
+    if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache attention: %s (%s)", why, cudaGetErrorString(e));
+    return launched(kv, e, "cache attention", st);
+  }
   prm.heads_q = pb.heads_q;
   prm.group = pb.heads_q / pb.heads_kv;
   prm.slots = slots;

@@ -54,6 +54,28 @@ struct PagedAttendParams {
   int4* joins;       // [head, slot]: first query row, rows, last slot of an item cut here (rows 0: none)
 };
 
+// An item that share x of the chunk kernel begins and does not end (tokens 0: none).
+struct alignas(16) PagedJoin {
+  int32_t head, token, tokens, last;  // last: the share that ends it
+};
+
+struct PagedChunkParams {
+  PagedTable t;
+  int32_t heads_q, group;
+  int32_t window, sinks;
+  int32_t piece;      // rows that are brought at a time: the largest power of two in 16..128 that divides a page
+  int32_t rounds;     // shares of a CTA at most
+  int32_t row_bytes;
+  float scale_log2;
+  const void* q;
+  void* o;
+  PagedStrides qs, os;
+  float* lse;        // [tokens, heads_q] or nullptr
+  float* part_o;     // [share, 2, tile, d / 4, 128, 4]
+  float4* part_ml;   // [share, 2, tile, 128]: running maximum (log2 units), sum, its correction
+  PagedJoin* joins;  // [share]
+};
+
 struct PagedWeighParams {
   PagedTable t;
   int32_t heads_q, group;
@@ -82,9 +104,20 @@ struct PagedEvictParams {
 
 cudaError_t launch_paged_append(int dtype, const PagedAppendParams& prm, int sm_count, cudaStream_t stream);
 cudaError_t launch_paged_rows(int dtype, int head_dim, const PagedAttendParams& prm, cudaStream_t stream);
+cudaError_t launch_paged_chunk(int head_dim, const PagedChunkParams& prm, int grid, cudaStream_t stream, const char** why);
 cudaError_t launch_paged_weigh_rows(int dtype, int head_dim, const PagedWeighParams& prm, int sm_count,
                                     cudaStream_t stream);
 cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, cudaStream_t stream);
+
+constexpr int kMaxChunkSequences = 2048;  // of a call of the chunk kernels (shared memory)
+constexpr int kMaxRounds = 8;
+
+// Tensor maps of the chunk kernels (paged_maps.cu): rows of d bf16 in boxes of 64 channels by
+// `box` rows; a packed tensor [tokens, heads, d] in boxes of 64 channels, `group` heads and
+// `box` tokens.  128-byte swizzle; beyond the end zeros.
+bool encode_rows(void* map, const void* base, int64_t rows, int d, int box);
+bool encode_packed(void* map, const void* base, const PagedStrides& s, int64_t tokens, int64_t heads, int d, int group,
+                   int box);
 
 constexpr int kRowsTile = 16;   // query rows of an item of the row kernels
 constexpr int kRowsBlock = 16;  // keys of a block
