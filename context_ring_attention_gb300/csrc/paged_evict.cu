@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictPara
     const uint32_t t = ties_before + (uint32_t)sum - (tie ? 1u : 0u);
     if (sure || (tie && t < left)) {
       const uint32_t to = s + min(t, left);
-      RA_BOUNDS(P.t.status, to < (uint32_t)P.keep, 113);
+      RA_BOUNDS(P.t.status, to < (uint32_t)P.keep, 118);
       kept[to] = (int32_t)j;
       if (out != nullptr) out[to] = wj;
     }
@@ -172,7 +172,7 @@ __device__ __forceinline__ MoveRow move_row(const PagedEvictParams& P, int row_b
   if (from_page < 0) return {-1, 0};
   const int64_t from = paged_row(P.t, from_page, which, head, s % pr), to = paged_row(P.t, to_page, which, head, j % pr);
   if (from == to) return {-1, 0};
-  RA_BOUNDS(P.t.status, s >= j && from >= 0 && to >= 0, 114);
+  RA_BOUNDS(P.t.status, s >= j && from >= 0 && to >= 0, 119);
   return {from * row_bytes, to * row_bytes};
 }
 

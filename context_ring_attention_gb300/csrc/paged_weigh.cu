@@ -4,10 +4,11 @@
 // over the query rows i of the head's group that see j.  Given the rows' LSE no softmax is
 // left: the sums run down the columns, each column belongs to one warp, and no order varies.
 //
-// Bound by HBM for few rows: the keys are read once.  bf16: a warp has 32 keys in registers as
-// the second operand of m16n8k16 and takes the query rows 16 at a time.  The products run over
-// channels in the order in which a 16-byte load of a row brings them, the same for queries and
-// keys, so that neither passes through shared memory.  float32: a warp has 32 keys, one a lane.
+// Bound by HBM for few rows: the keys are read once.  bf16: the blocks of 16 keys of all
+// sequences are laid in a row and shared out among the warps in equal runs; a warp streams its
+// run through a ring of its own (cp.async, 16 bytes a lane) and scores the keys against 16 query
+// rows at a time by m16n8k16, the rows of a sequence of up to 16 staying in registers.
+// float32: a warp has 32 keys, one a lane.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,24 +27,40 @@ constexpr int kKeys = 32;                  // of a warp
 constexpr int kChunk = kWarps * kKeys;     // of a CTA at a time
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 16 or 4 bytes from global to shared memory, asynchronously; zeros where !live.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// Sums of the sequences' chunks of keys (as paged_prefix, of lengths).
-__device__ void chunk_prefix(const PagedTable& t, int32_t* prefix) {
+// Sums of the sequences' blocks of kB slots (as paged_prefix, of lengths).
+template <int kB>
+__device__ void slot_prefix(const PagedTable& t, int64_t* prefix) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
-    int before = 0;
+    int64_t before = 0;
     for (int b0 = 0; b0 < t.batch; b0 += 32) {
-      int x = b0 + lane < t.batch ? (paged_seq(t, b0 + lane).length + kChunk - 1) / kChunk : 0;
+      int64_t x = b0 + lane < t.batch ? (paged_seq(t, b0 + lane).length + kB - 1) / kB : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
       if (b0 + lane < t.batch) prefix[b0 + lane + 1] = before + x;
@@ -54,148 +71,264 @@ __device__ void chunk_prefix(const PagedTable& t, int32_t* prefix) {
   __syncthreads();
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) weigh_kernel(const PagedWeighParams P) {
-  extern __shared__ int32_t prefix[];
-  chunk_prefix(P.t, prefix);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
-  const int chunks = prefix[P.t.batch];
-  const T* cache = static_cast<const T*>(P.t.cache);
-  int b = 0;
-  for (int c = (int)blockIdx.x; c < chunks; c += (int)gridDim.x) {
-    while (prefix[b + 1] <= c) ++b;
-    const PagedSeq seq = paged_seq(P.t, b);
-    const int j0 = (c - prefix[b]) * kChunk + warp * kKeys;
-    if (j0 >= seq.length) continue;
-    RA_BOUNDS(P.t.status, b < P.t.batch && seq.token0 + seq.count <= P.t.tokens, 115);
-    const int rows = seq.count * P.group, row0 = seq.token0 * P.group;
-    // Tiles of 16 rows that see one of this warp's keys: behind a key's own slot all tokens of
-    // the call do, up to the window (sinks: to the end).
-    const int jl = min(j0 + kKeys, seq.length) - 1;
+// What both kernels know of a sequence for one head.
+template <typename T>
+struct Rows {
+  const PagedWeighParams& P;
+  PagedSeq seq;
+  int head;
+  // Tiles of 16 rows that see one of the slots [j0, j0 + n): behind a key's own slot all tokens
+  // of the call do, up to the window (sinks: to the end).
+  __device__ __forceinline__ void tiles(int j0, int n, int& tile0, int& tile1) const {
+    const int jl = min(j0 + n, seq.length) - 1;
     const int tok0 = max(0, j0 - seq.slot0());
     const int64_t far = P.window > 0 && j0 >= P.sinks ? (int64_t)jl + P.window - seq.slot0() : seq.count;
     const int tok1 = (int)max((int64_t)0, min((int64_t)seq.count, far));
-    const int tile1 = tok1 > tok0 ? (tok1 * P.group + 15) / 16 : 0, tile0 = tok0 * P.group / 16;
-    // Slots that no token of the call sees keep what they had; their pages are not looked up.
-    auto seen = [&](int j) {
-      return seq.count > 0 && (P.window == 0 || j > seq.slot0() - P.window || j < P.sinks);
-    };
-    auto row_ptr = [&](int r) {
-      const int row = row0 + r, token = row / P.group;
-      return static_cast<const T*>(P.q) + token * P.qs.token + (int64_t)(head * P.group + row - token * P.group) * P.qs.head;
-    };
-    auto lse_of = [&](int r) {
-      const int row = row0 + r, token = row / P.group;
-      return __ldg(P.lse + (int64_t)token * P.heads_q + head * P.group + row - token * P.group);
-    };
-    auto put = [&](int j, float sum) {
-      if (j >= P.weight_width) {
-        atomicOr(P.t.status, kPagedStatusRange);
-        return;
+    tile0 = tok0 * P.group / 16;
+    tile1 = tok1 > tok0 ? (tok1 * P.group + 15) / 16 : 0;
+  }
+  // Slots that no token of the call sees keep what they had; their pages are not looked up.
+  __device__ __forceinline__ bool seen(int j) const {
+    return seq.count > 0 && (P.window == 0 || j > seq.slot0() - P.window || j < P.sinks);
+  }
+  __device__ __forceinline__ const T* row_ptr(int r) const {
+    const int row = seq.token0 * P.group + r, token = row / P.group;
+    return static_cast<const T*>(P.q) + token * P.qs.token + (int64_t)(head * P.group + row - token * P.group) * P.qs.head;
+  }
+  __device__ __forceinline__ float lse_of(int r) const {
+    const int row = seq.token0 * P.group + r, token = row / P.group;
+    return __ldg(P.lse + (int64_t)token * P.heads_q + head * P.group + row - token * P.group);
+  }
+};
+
+constexpr int kStages = 4;  // blocks of a warp's ring
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighParams P) {
+  constexpr int kRowBytes = D * 2, kChunks = D / 8, kBlockBytes = kRowsBlock * kRowBytes;
+  constexpr int kStageBytes = kBlockBytes + kRowsBlock * 4;  // keys, and what they had before
+  extern __shared__ __align__(128) uint8_t smem_bytes[];
+  uint8_t* smem = smem_bytes;
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem + kWarps * kStages * kStageBytes);
+  slot_prefix<kRowsBlock>(P.t, prefix);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
+  const int quad = lane >> 2, two = (lane & 3) * 2;
+  const __nv_bfloat16* cache = static_cast<const __nv_bfloat16*>(P.t.cache);
+  const int64_t all = prefix[P.t.batch], me = (int64_t)blockIdx.x * kWarps + warp, runs = (int64_t)gridDim.x * kWarps;
+  const int64_t x0 = all * me / runs;
+  const int n = (int)(all * (me + 1) / runs - x0);
+  if (n <= 0) return;
+  const uint32_t ring = ptx::smem_addr(smem) + warp * kStages * kStageBytes;
+  int b_first = 0;  // sequence of the run's first block
+  for (int end = P.t.batch; end - b_first > 1;) {
+    const int mid = (b_first + end) >> 1;
+    (prefix[mid] <= x0 ? b_first : end) = mid;
+  }
+  while (prefix[b_first + 1] <= x0) ++b_first;
+
+  // Block i of the run into the ring; a lane knows sequence, slot and page of one of the next 32.
+  int known_b = b_first, known_j = 0, known_page = -1;
+  uint32_t bad = 0u;  // stages whose page is none
+  auto load = [&](int i) {
+    if ((i & 31) == 0 && i < n) {
+      int b = __shfl_sync(0xffffffffu, known_b, 31);  // (the last block known so far)
+      if (i == 0) b = b_first;
+      const int64_t x = min(x0 + i + lane, x0 + n - 1);
+      while (prefix[b + 1] <= x) ++b;
+      known_b = b;
+      known_j = (int)(x - prefix[b]) * kRowsBlock;
+      const Rows<__nv_bfloat16> rows{P, paged_seq(P.t, b), head};
+      // (of a block the first slot or the last one is seen, or none)
+      const bool look = rows.seen(known_j) || rows.seen(min(known_j + kRowsBlock, rows.seq.length) - 1);
+      known_page = look ? paged_page(P.t, b, known_j / P.t.page_rows) : -2;
+    }
+    if (i < n) {
+      const int b = __shfl_sync(0xffffffffu, known_b, i & 31), j0 = __shfl_sync(0xffffffffu, known_j, i & 31);
+      const int page = __shfl_sync(0xffffffffu, known_page, i & 31), s = i % kStages;
+      bad = page == -1 ? bad | (1u << s) : bad & ~(1u << s);
+      const int64_t row0 = paged_row(P.t, max(page, 0), 0, head, j0 % P.t.page_rows);
+      RA_BOUNDS(P.t.status, row0 >= 0 && row0 + kRowsBlock <= (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 115);
+      const uint32_t dst = ring + s * kStageBytes;
+#pragma unroll
+      for (int x = 0; x < kChunks / 2; ++x) {
+        const int id = lane + 32 * x, r = id / kChunks, ch = id % kChunks;
+        copy16(dst + r * kRowBytes + ((ch ^ (r & 7)) * 16), cache + (row0 + r) * D + ch * 8, page >= 0);
       }
-      const int64_t at = ((int64_t)b * P.t.heads_kv + head) * P.weight_width + j;
-      RA_BOUNDS(P.t.status, j >= 0 && j < seq.length && at < (int64_t)P.t.batch * P.t.heads_kv * P.weight_width, 112);
-      P.weight[at] = (P.weight_in != nullptr && j < seq.slot0() ? P.weight_in[at] : 0.f) + sum;
-    };
-    if constexpr (sizeof(T) == 2) {
-      const int quad = lane >> 2, two = (lane & 3) * 2, ch = (lane & 3) * 8;
-      uint4 k[kKeys / 8][D / 32];
-      uint32_t there = 0u;  // keys quad + 8 i, unless their page is none
-#pragma unroll
-      for (int i = 0; i < kKeys / 8; ++i) {
-        const int j = j0 + quad + 8 * i;
-        const bool look = j < seq.length && seen(j);
-        const int page = look ? paged_page(P.t, b, j / P.t.page_rows) : -1;
-        if (page >= 0 || !look) there |= 1u << i;
-        const T* src = cache + paged_row(P.t, max(page, 0), 0, head, j % P.t.page_rows) * D + ch;
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x)
-          k[i][x] = page >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + 32 * x)) : make_uint4(0u, 0u, 0u, 0u);
+      if (lane < kRowsBlock) {
+        const int j = j0 + lane;
+        const bool had = P.weight_in != nullptr && j < P.weight_width && j < paged_seq(P.t, b).slot0();
+        const int64_t at = ((int64_t)b * P.t.heads_kv + head) * P.weight_width + j;
+        copy4(dst + kBlockBytes + lane * 4, had ? P.weight_in + at : P.weight, had);
       }
-      float sum[kKeys / 8][2];
+    }
+    copies_commit();
+  };
 #pragma unroll
-      for (int i = 0; i < kKeys / 8; ++i) sum[i][0] = sum[i][1] = 0.f;
-      for (int t = tile0; t < tile1; ++t) {
-        const int ra = t * 16 + quad;
-        uint4 q[2][D / 32];
-        float lse2[2];
-        int slot[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool live = ra + 8 * i < rows;
-          slot[i] = live ? seq.slot0() + (ra + 8 * i) / P.group : -1;
-          const T* src = live ? row_ptr(ra + 8 * i) + ch : nullptr;
-          lse2[i] = live ? lse_of(ra + 8 * i) * kLog2e : 0.f;
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x)
-            q[i][x] = live ? __ldg(reinterpret_cast<const uint4*>(src + 32 * x)) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < kKeys / 8; ++i) {
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            mma16816(s, q[0][x].x, q[1][x].x, q[0][x].y, q[1][x].y, k[i][x].x, k[i][x].y);
-            mma16816(s, q[0][x].z, q[1][x].z, q[0][x].w, q[1][x].w, k[i][x].z, k[i][x].w);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool sees = paged_sees(P.window, P.sinks, slot[e >> 1], j0 + 8 * i + two + (e & 1));
-            const float p = ptx::ex2_approx(fmaf(s[e], P.scale_log2, -lse2[e >> 1]));
-            sum[i][e & 1] += sees ? p : 0.f;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kKeys / 8; ++i)
+  for (int i = 0; i < kStages - 1; ++i) load(i);
+
+  int b = b_first, held = -1;  // held: the tile of sequence b that is in registers
+  Rows<__nv_bfloat16> rows{P, paged_seq(P.t, b), head};
+  uint32_t q[D / 16][4];
+  float lse2[2] = {0.f, 0.f};
+  int slot[2] = {-1, -1};
+  for (int i = 0; i < n; ++i) {
+    copies_wait<kStages - 2>();
+    __syncwarp();
+    load(i + kStages - 1);
+    const int st = i % kStages;
+    if (prefix[b + 1] <= x0 + i) {
+      while (prefix[b + 1] <= x0 + i) ++b;
+      rows.seq = paged_seq(P.t, b);
+      held = -1;
+    }
+    const int j0 = (int)(x0 + i - prefix[b]) * kRowsBlock;
+    const int rows_n = rows.seq.count * P.group;
+    int tile0, tile1;
+    rows.tiles(j0, kRowsBlock, tile0, tile1);
+    const uint32_t kb = ring + st * kStageBytes;
+    float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // keys two, two + 1 of each 8
+    for (int t = tile0; t < tile1; ++t) {
+      if (t != held) {
+        // The rows as the first operand: rows quad and quad + 8, channels two.. and two + 8..
+        held = t;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          const int r = t * 16 + quad + 8 * e;
+          const bool live = r < rows_n;
+          slot[e] = live ? rows.seq.slot0() + r / P.group : -1;
+          lse2[e] = live ? rows.lse_of(r) * kLog2e : 0.f;
+          const __nv_bfloat16* src = live ? rows.row_ptr(r) : nullptr;
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) sum[i][e] += __shfl_xor_sync(0xffffffffu, sum[i][e], o);
-          const int j = j0 + 8 * i + two + e;
-          // (the lane with this key's page: quad == two + e)
-          const uint32_t ok = __shfl_sync(0xffffffffu, there, (two + e) * 4);
-          if (quad == 0 && j < seq.length && ((ok >> i) & 1u)) put(j, sum[i][e]);
-        }
-    } else {
-      const int j = j0 + lane;
-      const bool look = j < seq.length && seen(j);
-      const int page = look ? paged_page(P.t, b, j / P.t.page_rows) : -1;
-      const float4* k = reinterpret_cast<const float4*>(cache + paged_row(P.t, max(page, 0), 0, head, j % P.t.page_rows) * D);
-      float sum = 0.f;
-      for (int r0 = tile0 * 16; r0 < min(rows, tile1 * 16); r0 += 4) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        const float4* q[4];
+          for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = reinterpret_cast<const float4*>(row_ptr(min(r0 + i, rows - 1)));
-#pragma unroll 4
-        for (int c4 = 0; c4 < D / 4; ++c4) {
-          const float4 kk = page >= 0 ? __ldg(k + c4) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 qq = __ldg(q[i] + c4);
-            s[i] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, s[i]))));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (r0 + i >= rows) break;
-          const bool sees = paged_sees(P.window, P.sinks, seq.slot0() + (r0 + i) / P.group, j);
-          const float p = exp2f(fmaf(s[i], P.scale_log2, -lse_of(r0 + i) * kLog2e));
-          sum += sees ? p : 0.f;
+            for (int f = 0; f < 2; ++f)
+              q[kk][e + 2 * f] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + f * 8 + two)) : 0u;
         }
       }
-      if (j < seq.length && (page >= 0 || !look)) put(j, sum);
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t r[4];
+        ldmatrix4(r, kb + kr * kRowBytes + (((2 * kk + kc) ^ (kr & 7)) * 16));
+        mma16816(s[0], q[kk], r[0], r[1]);
+        mma16816(s[1], q[kk], r[2], r[3]);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool sees = paged_sees(P.window, P.sinks, slot[e >> 1], j0 + 8 * c + two + (e & 1));
+          const float p = ptx::ex2_approx(fmaf(s[c][e], P.scale_log2, -lse2[e >> 1]));
+          sum[c][e & 1] += sees ? p : 0.f;
+        }
+    }
+    // Down the columns; then lane l has slot j0 + l.
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) sum[c][e] += __shfl_xor_sync(0xffffffffu, sum[c][e], o);
+    const int from = (lane & 7) >> 1;
+    const float a0 = __shfl_sync(0xffffffffu, sum[0][0], from), a1 = __shfl_sync(0xffffffffu, sum[0][1], from);
+    const float c0 = __shfl_sync(0xffffffffu, sum[1][0], from), c1 = __shfl_sync(0xffffffffu, sum[1][1], from);
+    const int j = j0 + lane;
+    if (lane < kRowsBlock && j < rows.seq.length && !(((bad >> st) & 1u) && rows.seen(j))) {
+      if (j < P.weight_width) {
+        const float had = *reinterpret_cast<const float*>(smem + (kb - ptx::smem_addr(smem)) + kBlockBytes + lane * 4);
+        const int64_t at = ((int64_t)b * P.t.heads_kv + head) * P.weight_width + j;
+        RA_BOUNDS(P.t.status, j >= 0 && at < (int64_t)P.t.batch * P.t.heads_kv * P.weight_width, 112);
+        P.weight[at] = had + (lane < 8 ? ((lane & 1) ? a1 : a0) : ((lane & 1) ? c1 : c0));
+      } else {
+        atomicOr(P.t.status, kPagedStatusRange);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) weigh_f32_kernel(const PagedWeighParams P) {
+  extern __shared__ int64_t prefix[];
+  slot_prefix<kChunk>(P.t, prefix);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
+  const int64_t chunks = prefix[P.t.batch];
+  const float* cache = static_cast<const float*>(P.t.cache);
+  int b = 0;
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    while (prefix[b + 1] <= c) ++b;
+    const Rows<float> rows{P, paged_seq(P.t, b), head};
+    const int j0 = (int)(c - prefix[b]) * kChunk + warp * kKeys, j = j0 + lane;
+    if (j0 >= rows.seq.length) continue;
+    const int rows_n = rows.seq.count * P.group;
+    int tile0, tile1;
+    rows.tiles(j0, kKeys, tile0, tile1);
+    const bool look = j < rows.seq.length && rows.seen(j);
+    const int page = look ? paged_page(P.t, b, j / P.t.page_rows) : -1;
+    const float4* k = reinterpret_cast<const float4*>(cache + paged_row(P.t, max(page, 0), 0, head, j % P.t.page_rows) * D);
+    float sum = 0.f;
+    for (int r0 = tile0 * 16; r0 < min(rows_n, tile1 * 16); r0 += 4) {
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      const float4* q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = reinterpret_cast<const float4*>(rows.row_ptr(min(r0 + i, rows_n - 1)));
+#pragma unroll 4
+      for (int c4 = 0; c4 < D / 4; ++c4) {
+        const float4 kk = page >= 0 ? __ldg(k + c4) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 qq = __ldg(q[i] + c4);
+          s[i] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, s[i]))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (r0 + i >= rows_n) break;
+        const bool sees = paged_sees(P.window, P.sinks, rows.seq.slot0() + (r0 + i) / P.group, j);
+        const float p = exp2f(fmaf(s[i], P.scale_log2, -rows.lse_of(r0 + i) * kLog2e));
+        sum += sees ? p : 0.f;
+      }
+    }
+    if (j < rows.seq.length && (page >= 0 || !look)) {
+      if (j < P.weight_width) {
+        const int64_t at = ((int64_t)b * P.t.heads_kv + head) * P.weight_width + j;
+        RA_BOUNDS(P.t.status, at < (int64_t)P.t.batch * P.t.heads_kv * P.weight_width, 113);
+        P.weight[at] = (P.weight_in != nullptr && j < rows.seq.slot0() ? P.weight_in[at] : 0.f) + sum;
+      } else {
+        atomicOr(P.t.status, kPagedStatusRange);
+      }
     }
   }
 }
 
-template <typename T, int D>
-cudaError_t launch(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
-  const int64_t most = (int64_t)prm.t.batch * ((prm.t.width * prm.t.page_rows + kChunk - 1) / kChunk);
-  const int64_t want = std::max<int64_t>(1, (int64_t)sm_count * 4 / prm.t.heads_kv);
-  const dim3 grid((unsigned)std::min(most, want), (unsigned)prm.t.heads_kv);
-  weigh_kernel<T, D><<<grid, kThreads, (prm.t.batch + 1) * 4, stream>>>(prm);
+// CTAs per head: as many as the GPU holds at once, each with work at the sizes given.
+unsigned slots_of(const PagedWeighParams& prm, int sm_count, int per_sm, int own) {
+  const int64_t most = (int64_t)std::min(prm.t.batch, 1 << 20) * ((prm.t.width * prm.t.page_rows + own - 1) / own);
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)sm_count * per_sm / prm.t.heads_kv));
+}
+
+template <int D>
+cudaError_t launch_bf16(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
+  constexpr int kRing = kWarps * kStages * (kRowsBlock * D * 2 + kRowsBlock * 4);
+  static std::atomic<int> ready[kMaxDevices];
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  if (!cached || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(weigh_bf16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + (kMaxSequences + 1) * 8);
+    if (e != cudaSuccess) return e;
+    if (cached) ready[dev].store(1, std::memory_order_release);
+  }
+  const dim3 grid(slots_of(prm, sm_count, 3, kWarps * kRowsBlock), (unsigned)prm.t.heads_kv);
+  weigh_bf16_kernel<D><<<grid, kThreads, kRing + (prm.t.batch + 1) * 8, stream>>>(prm);
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_f32(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
+  const dim3 grid(slots_of(prm, sm_count, 4, kChunk), (unsigned)prm.t.heads_kv);
+  weigh_f32_kernel<D><<<grid, kThreads, (prm.t.batch + 1) * 8, stream>>>(prm);
   return cudaGetLastError();
 }
 
@@ -204,9 +337,8 @@ cudaError_t launch(const PagedWeighParams& prm, int sm_count, cudaStream_t strea
 cudaError_t launch_paged_weigh_rows(int dtype, int head_dim, const PagedWeighParams& prm, int sm_count,
                                     cudaStream_t stream) {
   if (dtype == RA_DTYPE_BF16)
-    return head_dim == 128 ? launch<__nv_bfloat16, 128>(prm, sm_count, stream)
-                           : launch<__nv_bfloat16, 64>(prm, sm_count, stream);
-  return head_dim == 128 ? launch<float, 128>(prm, sm_count, stream) : launch<float, 64>(prm, sm_count, stream);
+    return head_dim == 128 ? launch_bf16<128>(prm, sm_count, stream) : launch_bf16<64>(prm, sm_count, stream);
+  return head_dim == 128 ? launch_f32<128>(prm, sm_count, stream) : launch_f32<64>(prm, sm_count, stream);
 }
 
 }  // namespace ra
