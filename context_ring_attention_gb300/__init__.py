@@ -10,7 +10,7 @@ The functions keep the C names (``ra_plan``, ``ra_plan_window``, ``ra_plan_tile_
 ``ra_kv4_attend``, ``ra_kv4_attend_scratch_size``, ``ra_kv4_sync_status``;
 ``ra_rope_plan``, ``ra_rope``, ``ra_rope_bwd``;
 ``ra_paged_plan``, ``ra_paged_append``, ``ra_paged_attend``, ``ra_paged_attend_scratch_size``,
-``ra_paged_weigh``, ``ra_paged_evict``, ``ra_paged_sync_status``).
+``ra_paged_weigh``, ``ra_paged_weigh_scratch_size``, ``ra_paged_evict``, ``ra_paged_sync_status``).
 This module only marshals arguments: PyTorch supplies device memory and the
 current stream (outputs and scratch made for a call with a ``stream`` of its own belong to
 that stream), every step of the computation runs in the library's CUDA kernels, and there is
@@ -43,7 +43,8 @@ __all__ = [
     "ra_kv4_attend_scratch_size", "ra_kv4_sync_status",
     "Rope", "ROPE_SCALINGS", "ra_rope_plan", "ra_rope_destroy", "ra_rope", "ra_rope_bwd",
     "Paged", "ra_paged_plan", "ra_paged_destroy", "ra_paged_cache_shape", "ra_paged_append", "ra_paged_attend",
-    "ra_paged_attend_scratch_size", "ra_paged_weigh", "ra_paged_evict", "ra_paged_sync_status",
+    "ra_paged_attend_scratch_size", "ra_paged_weigh", "ra_paged_weigh_scratch_size", "ra_paged_evict",
+    "ra_paged_sync_status",
     "library_path", "load_library", "EXPORTED",
 ]
 
@@ -60,7 +61,7 @@ EXPORTED = ("ra_plan", "ra_plan_window", "ra_plan_destroy", "ra_plan_tile_counts
             "ra_kv4_attend_scratch_size", "ra_kv4_sync_status",
             "ra_rope_plan", "ra_rope_destroy", "ra_rope", "ra_rope_bwd",
             "ra_paged_plan", "ra_paged_destroy", "ra_paged_append", "ra_paged_attend", "ra_paged_attend_scratch_size",
-            "ra_paged_weigh", "ra_paged_evict", "ra_paged_sync_status")
+            "ra_paged_weigh", "ra_paged_weigh_scratch_size", "ra_paged_evict", "ra_paged_sync_status")
 
 _TORCH = None
 _NO_CONTEXT = contextlib.nullcontext()
@@ -169,7 +170,8 @@ def load_library():
         "ra_paged_append": ([P, P, VP, I64, I64, VP, VP, VP, VP, VP, VP, VP, VP, VP, I64, VP, VP, VP, VP], I32),
         "ra_paged_attend": ([P, VP, I64, I64, VP, VP, VP, I64, VP, VP, VP, VP, VP, VP, VP], I32),
         "ra_paged_attend_scratch_size": ([P, I64, I64, I64, VP], I32),
-        "ra_paged_weigh": ([P, VP, I64, I64, VP, VP, VP, VP, I64, VP, VP, VP, VP, I64, VP], I32),
+        "ra_paged_weigh": ([P, VP, I64, I64, VP, VP, VP, VP, I64, VP, VP, VP, VP, I64, VP, VP], I32),
+        "ra_paged_weigh_scratch_size": ([P, I64, I64, I64, VP], I32),
         "ra_paged_evict": ([P, VP, I64, VP, I64, VP, VP, VP, I64, I64, I64, I64, VP, I64, VP, VP, VP], I32),
         "ra_paged_sync_status": ([P, VP], I32),
     }
@@ -949,7 +951,8 @@ class Paged:
         self.problem = problem
         pb = problem
         self._shape = (pb["pages"], 2, pb["heads_kv"], pb["page_rows"], pb["head_dim"])
-        self._scratch = (None, 0)  # (batch, tokens, table width) of the last attention call, its bytes of scratch
+        # (batch, tokens, table width) of the last call, its bytes of scratch: attention's, the weights'
+        self._scratch, self._weigh_scratch = (None, 0), (None, 0)
 
     @property
     def handle(self):
@@ -1061,10 +1064,8 @@ def ra_paged_attend(kv, cache, q, page_table, offset, length, o=None, lse=None, 
     shape = (T, pb["heads_q"], pb["head_dim"])
     _need_rows("q", q, shape, dtype, device)
     need = ra_paged_attend_scratch_size(kv, batch, T, page_table.shape[1]) // 4
-    if scratch is not None and (scratch.numel() < need or scratch.dtype != torch.float32
-                                  or not scratch.is_contiguous() or scratch.device != device):
-        raise ValueError("scratch must be a contiguous float32 tensor of at least ra_paged_attend_scratch_size(...) "
-                         "bytes on the device of q")
+    if scratch is not None:
+        _need_scratch("ra_paged_attend_scratch_size", scratch, need, device)
     if o is not None:
         _need_rows("o", o, shape, dtype, device)
     if lse is not None:
@@ -1089,7 +1090,23 @@ def _need_weights(name, t, kv, batch, device):
     _need_like(name, t, (batch, kv.problem["heads_kv"], t.shape[2]), torch.float32, device)
 
 
-def ra_paged_weigh(kv, cache, q, lse, page_table, offset, length, weight, weight_in=None, stream=None):
+def ra_paged_weigh_scratch_size(kv, batch, tokens, table_width):
+    """Bytes of the float32 scratch buffer ra_paged_weigh needs for these sizes (0: none)."""
+    key = (int(batch), int(tokens), int(table_width))
+    if kv._weigh_scratch[0] != key:
+        n = ctypes.c_int64()
+        _check(load_library().ra_paged_weigh_scratch_size(kv.handle, *key, ctypes.byref(n)))
+        kv._weigh_scratch = (key, n.value)
+    return kv._weigh_scratch[1]
+
+
+def _need_scratch(name, scratch, need, device):
+    if (scratch.numel() < need or scratch.dtype != (_TORCH or _torch()).float32 or not scratch.is_contiguous()
+            or scratch.device != device):
+        raise ValueError(f"scratch must be a contiguous float32 tensor of at least {name}(...) bytes on {device}")
+
+
+def ra_paged_weigh(kv, cache, q, lse, page_table, offset, length, weight, weight_in=None, scratch=None, stream=None):
     """Attention weight of every slot from the new tokens, added to ``weight_in`` (default: zeros) -> weight.
 
     weight, weight_in: [sequences, Hkv, slots] float32, and may be one tensor; the slots of the
@@ -1104,9 +1121,15 @@ def ra_paged_weigh(kv, cache, q, lse, page_table, offset, length, weight, weight
     _need_weights("weight", weight, kv, batch, device)
     if weight_in is not None:
         _need_like("weight_in", weight_in, weight.shape, torch.float32, device)
+    need = ra_paged_weigh_scratch_size(kv, batch, T, page_table.shape[1]) // 4
+    if scratch is not None:
+        _need_scratch("ra_paged_weigh_scratch_size", scratch, need, device)
+    elif need:
+        with _alloc_on(stream):
+            scratch = torch.empty(need, dtype=torch.float32, device=device)
     _check(load_library().ra_paged_weigh(kv.handle, _ptr(cache), batch, T, _ptr(q), _strides(q), _ptr(lse), _ptr(page_table),
                                          page_table.shape[1], _ptr(offset), _ptr(length), _ptr(weight_in), _ptr(weight),
-                                         weight.shape[2], _stream(stream)))
+                                         weight.shape[2], _ptr(scratch), _stream(stream)))
     return weight
 
 

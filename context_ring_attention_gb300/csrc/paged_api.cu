@@ -40,7 +40,8 @@ ra_status ok() {
 
 constexpr int64_t kMaxPositions = int64_t(1) << 30;  // of a sequence: slot arithmetic stays in 32 bits
 constexpr int kMaxSlots = 1024;                      // CTAs of a key/value head
-constexpr int64_t kMaxChunkSlots = int64_t(1) << 25;  // of a sequence in the chunk kernel: an item ends well within its wait budget
+// Of a sequence in the chunk kernels, so that an item, 2^18 tiles at most, ends well within their wait budget.
+constexpr int64_t kMaxChunkSlots = int64_t(1) << 25, kMaxChunkTiles = int64_t(1) << 18;
 
 ra_status validate(const ra_paged_problem* p) {
   if (p->pages < 1 || p->heads_q < 1 || p->heads_kv < 1 || p->head_dim < 1)
@@ -153,12 +154,20 @@ bool takes_chunks(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t w
   const ra_paged_problem& pb = kv->prob;
   const int64_t group = pb.heads_q / pb.heads_kv;
   return pb.dtype == RA_DTYPE_BF16 && group <= 128 && batch <= ra::kMaxChunkSequences &&
-         width * pb.page_rows <= kMaxChunkSlots && tokens * group > 16 * batch;
+         width * pb.page_rows <= kMaxChunkSlots && tokens / (128 / group) <= kMaxChunkTiles && tokens * group > 16 * batch;
 }
 
 int64_t chunk_scratch(const ra_paged_s* kv, int64_t shares) {
   const int64_t rows = shares * 2 * 2 * 128;
   return rows * (kv->prob.head_dim * 4 + 16) + shares * 16;
+}
+// Bytes of the weights' chunk kernel: a sum per key for two parts of every share, and the joins.
+int64_t weigh_scratch(int64_t grid) { return grid * (2 * 256 * 4 + 16); }
+// The largest power of two in 16..128 that divides a page.
+int piece_of(const ra_paged_problem& pb) {
+  int piece = 16;
+  while (piece < 128 && pb.page_rows % (2 * piece) == 0) piece *= 2;
+  return piece;
 }
 int chunk_grid(const ra_paged_s* kv) { return kv->sm_count > 0 ? kv->sm_count : 148; }
 
@@ -319,7 +328,7 @@ ra_status ra_paged_attend(ra_paged_t kv, const void* cache, int64_t batch, int64
     c.group = pb.heads_q / pb.heads_kv;
     c.window = (int32_t)std::min(pb.window, kMaxPositions);
     c.sinks = pb.window > 0 ? (int32_t)std::min(pb.sinks, kMaxPositions) : 0;
-    for (c.piece = 16; c.piece < 128 && pb.page_rows % (2 * c.piece) == 0;) c.piece *= 2;
+    c.piece = piece_of(pb);
     c.rounds = chunk_rounds(kv, batch, tokens, table_width);
     c.row_bytes = pb.head_dim * 2;
     c.scale_log2 = pb.scale * 1.4426950408889634f;
@@ -356,10 +365,18 @@ ra_status ra_paged_attend(ra_paged_t kv, const void* cache, int64_t batch, int64
   return launched(kv, ra::launch_paged_rows(pb.dtype, pb.head_dim, prm, st), "cache attention launch", st);
 }
 
+ra_status ra_paged_weigh_scratch_size(ra_paged_t kv, int64_t batch, int64_t tokens, int64_t table_width, int64_t* bytes) {
+  if (kv == nullptr || bytes == nullptr) return fail(RA_ERR_INVALID_ARG, "null argument");
+  const ra_status s = check_sizes(kv, batch, tokens, table_width);
+  if (s != RA_OK) return s;
+  *bytes = takes_chunks(kv, batch, tokens, table_width) ? weigh_scratch(chunk_grid(kv)) : 0;
+  return ok();
+}
+
 ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_t tokens, const void* q,
                          const int64_t* q_strides, const float* lse, const int32_t* page_table, int64_t table_width,
                          const int32_t* offset, const int32_t* length, const float* weight_in, float* weight,
-                         int64_t weight_width, void* stream) {
+                         int64_t weight_width, float* scratch, void* stream) {
   if (kv == nullptr) return fail(RA_ERR_INVALID_ARG, "null handle");
   if (cache == nullptr || q == nullptr || lse == nullptr || page_table == nullptr || offset == nullptr ||
       length == nullptr || weight == nullptr)
@@ -367,15 +384,45 @@ ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_
   if (weight_width < 1 || weight_width > kMaxPositions)
     return fail(RA_ERR_INVALID_ARG, "weight_width must be in 1..2^30");
   const ra_paged_problem& pb = kv->prob;
-  ra::PagedWeighParams prm{};
-  ra_status s = strides_of(kv, "q", q_strides, tokens, pb.heads_q, false, &prm.qs);
+  ra_status s = check_sizes(kv, batch, tokens, table_width);
   if (s != RA_OK) return s;
+  ra::PagedWeighParams prm{};
+  s = strides_of(kv, "q", q_strides, tokens, pb.heads_q, false, &prm.qs);
+  if (s != RA_OK) return s;
+  if ((tokens > 1 && prm.qs.token == 0) || (pb.heads_q > 1 && prm.qs.head == 0))
+    return fail(RA_ERR_INVALID_ARG, "q: rows lie in one place");
+  const bool chunks = takes_chunks(kv, batch, tokens, table_width);
+  if (chunks && scratch == nullptr)
+    return fail(RA_ERR_INVALID_ARG, "null scratch (ra_paged_weigh_scratch_size bytes are needed)");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const void* t16[] = {cache, q};
+  const void* t16[] = {cache, q, chunks ? scratch : nullptr};
   const void* t4[] = {page_table, offset, length, lse, weight_in, weight};
-  s = check_call(kv, batch, tokens, table_width, t16, 2, t4, 6, st);
+  s = check_call(kv, batch, tokens, table_width, t16, 3, t4, 6, st);
   if (s != RA_OK) return s;
   prm.t = table_of(kv, cache, batch, tokens, page_table, table_width, offset, length);
+  if (chunks) {
+    ra::PagedWeighChunkParams c{};
+    c.t = prm.t;
+    c.heads_q = pb.heads_q;
+    c.group = pb.heads_q / pb.heads_kv;
+    c.window = (int32_t)std::min(pb.window, kMaxPositions);
+    c.sinks = pb.window > 0 ? (int32_t)std::min(pb.sinks, kMaxPositions) : 0;
+    c.piece = piece_of(pb);
+    c.scale_log2 = pb.scale * 1.4426950408889634f;
+    c.q = q;
+    c.qs = prm.qs;
+    c.lse = lse;
+    c.weight_in = weight_in;
+    c.weight = weight;
+    c.weight_width = weight_width;
+    const int grid = chunk_grid(kv);
+    c.parts = scratch;
+    c.joins = reinterpret_cast<ra::PagedWeighJoin*>(scratch + (int64_t)grid * 2 * 256);
+    const char* why = "";
+    const cudaError_t e = ra::launch_paged_weigh_chunk(pb.head_dim, c, grid, st, &why);
+    if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache weights: %s (%s)", why, cudaGetErrorString(e));
+    return launched(kv, e, "cache weights", st);
+  }
   prm.heads_q = pb.heads_q;
   prm.group = pb.heads_q / pb.heads_kv;
   prm.window = (int32_t)std::min(pb.window, kMaxPositions);

@@ -32,8 +32,7 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "paged_share.cuh"
-#include "sm100_ptx.cuh"
+#include "paged_sm103.cuh"
 
 namespace ra {
 namespace {
@@ -103,55 +102,8 @@ __device__ __forceinline__ uint32_t col_o(int g) { return g ? 384u : 256u; }
 // softmax has read S; the next S MMA of that tile is issued after the PV MMA that reads P.
 constexpr uint32_t kColP = 64;
 constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kTile, kTile, false, false);  // Q, K both K-major
-constexpr uint64_t kWaitBudgetNs = 1000000000ull;
-constexpr uint32_t kSuspendHintNs = 2000u;
 constexpr float kRescaleSlack = 8.0f;  // log2 units: keep a stale max while p <= 2^8
 constexpr float kLn2 = 0.6931471805599453f;
-
-struct Ctl {
-  uint32_t bars;
-  volatile uint32_t* abort;
-  uint32_t* status;
-  __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
-};
-
-// Bounded wait for phase `parity` of a barrier; false on abort or expiry.
-__device__ __forceinline__ bool wait_bar(const Ctl& c, uint32_t bar, uint32_t parity, uint32_t who) {
-  if (ptx::mbar_test(bar, parity)) return true;
-  const uint64_t t0 = ptx::global_timer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (ptx::mbar_wait_hint(bar, parity, kSuspendHintNs)) return true;
-    if ((it & 15u) == 0) {
-      if (*c.abort) return false;
-      if (ptx::global_timer_ns() - t0 > kWaitBudgetNs) {
-        *c.abort = 1u;
-        atomicOr(c.status, who);
-        return false;
-      }
-    }
-  }
-}
-// Teardown wait: ignores the abort flag, still bounded.
-__device__ __forceinline__ void drain_bar(const Ctl& c, uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = ptx::global_timer_ns();
-  while (!ptx::mbar_test(bar, parity)) {
-    if (ptx::global_timer_ns() - t0 > kWaitBudgetNs) {
-      atomicOr(c.status, kStatusTimeoutTeardown);
-      return;
-    }
-  }
-}
-#define RA_WAIT(n, phase, who) __all_sync(0xffffffffu, wait_bar(c, c.bar(n), (phase) & 1u, who))
-
-__device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
-                                                 int32_t z) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
 
 // --------------------------------------------------------------------- shares --
 // Tokens of an item and its key tiles.
@@ -176,34 +128,14 @@ struct Shares {
 // Prefix sums of the sequences' units (one head), and the number of shares: as many as CTAs, times
 // the rounds.  Every thread calls it; it ends with a barrier.
 __device__ Shares shares_of(const PagedChunkParams& P, int per_item, int64_t* prefix, int64_t* scratch) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t again = 0;  // slots that more than one item reads
-  for (int b = warp; b < P.t.batch; b += kWarps) {
+  paged_sums<kWarps>(P.t.batch, prefix, [&](int b) {
     const PagedSeq q = paged_seq(P.t, b);
     const int items = (q.count + per_item - 1) / per_item;
-    int64_t sum = 0;
-    for (int i = lane; i < items; i += 32) sum += item_units(P, q, per_item, i);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) prefix[b + 1] = sum;
     if (items > 1) again += q.length;
-  }
-  if (lane == 0) scratch[warp] = again;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t before = 0;
-    for (int b0 = 0; b0 < P.t.batch; b0 += 32) {
-      int64_t x = b0 + lane < P.t.batch ? prefix[b0 + lane + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (b0 + lane < P.t.batch) prefix[b0 + lane + 1] = before + x;
-      before += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) prefix[0] = 0;
-  }
+    return warp_total(items, [&](int i) { return item_units(P, q, per_item, i); });
+  });
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = again;
   __syncthreads();
   again = 0;
   for (int i = 0; i < kWarps; ++i) again += scratch[i];
@@ -233,25 +165,8 @@ __device__ void run_records(const PagedChunkParams& P, const Ctl& c, Record* rec
         b = paged_find(prefix, P.t.batch, y);
         q = paged_seq(P.t, b);
         const int items = (q.count + per_item - 1) / per_item;
-        int64_t first = head * sh.per_head + prefix[b];
-        for (int i0 = 0; i0 < items; i0 += 32) {
-          const int64_t own = i0 + lane < items ? item_units(P, q, per_item, i0 + lane) : 0;
-          int64_t z = own;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, z, o);
-            if (lane >= o) z += v;
-          }
-          const uint32_t past = __ballot_sync(0xffffffffu, first + z > x);
-          if (past) {
-            const int src = __ffs(past) - 1;
-            first += __shfl_sync(0xffffffffu, z - own, src);
-            i = i0 + src;
-            break;
-          }
-          first += __shfl_sync(0xffffffffu, z, 31);
-        }
-        item_x = first;
+        i = warp_find(items, y - prefix[b], item_x, [&](int i) { return item_units(P, q, per_item, i); });
+        item_x += head * sh.per_head + prefix[b];
       } else {  // to the next item
         item_x = x;
         ++i;

@@ -89,6 +89,27 @@ struct PagedWeighParams {
   int64_t weight_width;
 };
 
+// An item that share x of the chunk kernel begins and does not end (last < 0: none).
+struct alignas(16) PagedWeighJoin {
+  int32_t head, b, key0, last;  // last: the share that ends it
+};
+
+struct PagedWeighChunkParams {
+  PagedTable t;
+  int32_t heads_q, group;
+  int32_t window, sinks;
+  int32_t piece;  // as in PagedChunkParams
+  float scale_log2;
+  const void* q;
+  PagedStrides qs;
+  const float* lse;
+  const float* weight_in;
+  float* weight;
+  int64_t weight_width;
+  float* parts;           // [share, 2, 256]
+  PagedWeighJoin* joins;  // [share]
+};
+
 struct PagedEvictParams {
   PagedTable t;  // (offset nullptr, tokens 0)
   int32_t d;
@@ -107,6 +128,8 @@ cudaError_t launch_paged_rows(int dtype, int head_dim, const PagedAttendParams& 
 cudaError_t launch_paged_chunk(int head_dim, const PagedChunkParams& prm, int grid, cudaStream_t stream, const char** why);
 cudaError_t launch_paged_weigh_rows(int dtype, int head_dim, const PagedWeighParams& prm, int sm_count,
                                     cudaStream_t stream);
+cudaError_t launch_paged_weigh_chunk(int head_dim, const PagedWeighChunkParams& prm, int grid, cudaStream_t stream,
+                                     const char** why);
 cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, cudaStream_t stream);
 
 constexpr int kMaxChunkSequences = 2048;  // of a call of the chunk kernels (shared memory)

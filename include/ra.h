@@ -750,7 +750,7 @@ ra_status ra_paged_append(ra_paged_t kv, ra_rope_t rope, void* cache, int64_t ba
  * ra_paged_attend -- attention of the new tokens over their sequences' slots (their own among
  * them: append them first).  A token at slot s sees the slots j <= s, within the handle's
  * window and sinks (j > s - window or j < sinks).
- * q, o: [tokens, Hq, d]; lse: [tokens, Hq] float32, contiguous (may be NULL).  A token all of
+ * q, o: [tokens, Hq, d], no two rows in one place; lse: [tokens, Hq] float32, contiguous (may be NULL).  A token all of
  * whose slots lie in pages out of range gets O = 0, LSE = -inf.
  * Slots that no token of the call sees may hold anything.  Values that some of them see must be
  * finite: they enter the products of the others with weight zero.
@@ -781,14 +781,22 @@ ra_status ra_paged_attend_scratch_size(ra_paged_t kv, int64_t batch, int64_t tok
  * weight_in, weight: [batch, Hkv, weight_width] float32, contiguous; weight_in may be weight, or
  * NULL (zeros).  Slots from length[b] on stay as they were, and so do slots in pages out of
  * range; slots from weight_width on are reported (ra_paged_sync_status).  Deterministic.
+ * scratch: ra_paged_weigh_scratch_size bytes (NULL when that is 0), not shared by calls that
+ * may overlap.
  * Device pointers, 16-byte aligned (tables, lse and weights: 4-byte).  Asynchronous on stream;
  * allocates nothing.
- * Errors: as ra_paged_append (weight_width outside 1..2^30: RA_ERR_INVALID_ARG).
+ * Errors: as ra_paged_attend (weight_width outside 1..2^30: RA_ERR_INVALID_ARG).
  */
 ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_t tokens, const void* q,
                          const int64_t* q_strides, const float* lse, const int32_t* page_table,
                          int64_t table_width, const int32_t* offset, const int32_t* length,
-                         const float* weight_in, float* weight, int64_t weight_width, void* stream);
+                         const float* weight_in, float* weight, int64_t weight_width, float* scratch,
+                         void* stream);
+
+/* Bytes of ra_paged_weigh's scratch for these sizes (0 when it needs none).  Host only.
+ * Errors: RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED as ra_paged_weigh. */
+ra_status ra_paged_weigh_scratch_size(ra_paged_t kv, int64_t batch, int64_t tokens, int64_t table_width,
+                                      int64_t* bytes);
 
 /*
  * ra_paged_evict -- keep at most `keep` slots of every sequence and key/value head: its `first`

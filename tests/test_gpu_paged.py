@@ -383,11 +383,12 @@ def test_graphs_follow_the_tables(counts):
         t.o, t.lse, t.turned = torch.empty_like(t.qd), torch.empty((t.tokens, 8), device="cuda"), torch.empty_like(t.qd)
         t.scratch = torch.empty(max(1, ra.ra_paged_attend_scratch_size(t.kv, 3, t.tokens, t.ref.width) // 4), device="cuda")
         t.weight = torch.zeros((3, 2, 1000), device="cuda")
+        t.more = torch.empty(max(1, ra.ra_paged_weigh_scratch_size(t.kv, 3, t.tokens, t.ref.width) // 4), device="cuda")
 
         def step(t=t):
             ra.ra_paged_append(t.kv, t.cache, t.k, t.v, t.table, t.offset, t.length, rope=rope, q=t.qd, q_out=t.turned)
             ra.ra_paged_attend(t.kv, t.cache, t.turned, t.table, t.offset, t.length, o=t.o, lse=t.lse, scratch=t.scratch)
-            ra.ra_paged_weigh(t.kv, t.cache, t.turned, t.lse, t.table, t.offset, t.length, t.weight)
+            ra.ra_paged_weigh(t.kv, t.cache, t.turned, t.lse, t.table, t.offset, t.length, t.weight, scratch=t.more)
 
         step()
         torch.cuda.synchronize()

@@ -76,9 +76,13 @@ def test_shape_and_scratch():
     for args, status in (((0, 1, 1), "RA_ERR_INVALID_ARG"), ((1, 0, 1), "RA_ERR_INVALID_ARG"),
                          ((1, 1, 0), "RA_ERR_INVALID_ARG"), ((4097, 1, 1), "RA_ERR_UNSUPPORTED"),
                          ((1, 1 << 28, 1), "RA_ERR_UNSUPPORTED"), ((1, 1, (1 << 30) // 32 + 1), "RA_ERR_UNSUPPORTED")):
-        with pytest.raises(ra.RaError) as err:
-            ra.ra_paged_attend_scratch_size(kv, *args)
-        assert err.value.name == status
+        for size in (ra.ra_paged_attend_scratch_size, ra.ra_paged_weigh_scratch_size):
+            with pytest.raises(ra.RaError) as err:
+                size(kv, *args)
+            assert err.value.name == status
+    # chunks: parts of every share; float32 and few rows need none for the weights
+    assert ra.ra_paged_weigh_scratch_size(kv, 1, 100, 64) > 0 and ra.ra_paged_attend_scratch_size(kv, 1, 100, 64) % 16 == 0
+    assert ra.ra_paged_weigh_scratch_size(kv, 100, 100, 64) == ra.ra_paged_weigh_scratch_size(_kv(dtype="f32"), 1, 100, 64) == 0
 
 
 def _buffer():
@@ -129,8 +133,8 @@ def test_refused_paged_calls():
     def attend(kv=h, cache=a, b=1, t=2, q=a, qs=q4, tab=a, w=1, off=a, ln=a, o=a, os=q4, lse=a, scratch=a):
         return lib.ra_paged_attend(kv, cache, b, t, q, qs, tab, w, off, ln, o, os, lse, scratch, None)
 
-    def weigh(kv=h, cache=a, b=1, t=2, q=a, qs=q4, lse=a, tab=a, w=1, off=a, ln=a, win=a, wout=a, ww=8):
-        return lib.ra_paged_weigh(kv, cache, b, t, q, qs, lse, tab, w, off, ln, win, wout, ww, None)
+    def weigh(kv=h, cache=a, b=1, t=2, q=a, qs=q4, lse=a, tab=a, w=1, off=a, ln=a, win=a, wout=a, ww=8, scratch=a):
+        return lib.ra_paged_weigh(kv, cache, b, t, q, qs, lse, tab, w, off, ln, win, wout, ww, scratch, None)
 
     def evict(kv=h, cache=a, b=1, tab=a, w=1, ln=a, win=a, wout=a, ww=8, keep=4, first=1, recent=1, new=a, nw=1, kept=a,
               nl=a + 16):
@@ -149,9 +153,11 @@ def test_refused_paged_calls():
             dict(rope=None, q=None, qo=None), dict(rope=other.handle), dict(rope=f32.handle)]:
         assert append(**kw) == 1, kw
     for kw in shared + packed + [dict(q=None), dict(o=None), dict(o=a + 8), dict(os=_s(0, 128)), dict(os=None), dict(lse=a + 2),
-                                 dict(w=4096, scratch=None), dict(w=4096, scratch=a + 8)]:
+                                 dict(w=4096, scratch=None), dict(w=4096, scratch=a + 8),
+                                 dict(t=20, scratch=None), dict(t=20, scratch=a + 4), dict(qs=_s(512, 0))]:
         assert attend(**kw) == 1, kw
-    for kw in shared + packed + [dict(q=None), dict(lse=None), dict(wout=None), dict(win=a + 2), dict(ww=0), dict(ww=1 << 31)]:
+    for kw in shared + packed + [dict(q=None), dict(lse=None), dict(wout=None), dict(win=a + 2), dict(ww=0), dict(ww=1 << 31),
+                                 dict(t=20, scratch=None), dict(t=20, scratch=a + 4), dict(qs=_s(0, 128))]:
         assert weigh(**kw) == 1, kw
     for kw in shared + [dict(win=None), dict(wout=a + 2), dict(ww=0), dict(keep=0), dict(first=-1), dict(recent=-1),
                         dict(first=3, recent=2), dict(first=5), dict(keep=1 << 31), dict(new=None), dict(nw=0),
@@ -217,7 +223,7 @@ def test_the_binding_checks_every_tensor(monkeypatch):
         attend=dict(cache=t["cache"].float(), q=t["q"].transpose(1, 2), o=t["q"][:2], lse=t["lse"].double(),
                     scratch=torch.zeros(1 << 20, dtype=torch.float64), offset=t["offset"].long(), length=t["length"][:1],
                     page_table=t["table"].t()),
-        weigh=dict(lse=t["lse"][:2], weight=t["weight"][:1], weight_in=t["weight"][:, :, :5], q=t["x"], cache=t["cache"][:, :1]),
+        weigh=dict(scratch=torch.zeros(1 << 20, dtype=torch.float64), lse=t["lse"][:2], weight=t["weight"][:1], weight_in=t["weight"][:, :, :5], q=t["x"], cache=t["cache"][:, :1]),
         evict=dict(weight=t["weight"][0], weight_out=t["weight"].bfloat16(), new_table=t["table"][:1], kept=t["lse"],
                    new_length=t["offset"], length=t["offset"], page_table=t["table"].long()),
         rope=dict(q=t["x"][0], k=t["y"][:, :, :4], q_out=t["x"][:, :2], k_out=t["y"].transpose(2, 3), position=t["position"]))
@@ -232,7 +238,7 @@ def test_the_binding_checks_every_tensor(monkeypatch):
         calls["append"](q=None, q_out=t["q"])
 
 
-@pytest.mark.parametrize("name", ["append", "attend", "evict", "rope"])
+@pytest.mark.parametrize("name", ["append", "attend", "weigh", "evict", "rope"])
 def test_buffers_are_made_on_the_calls_stream(monkeypatch, name):
     inside, made = [], []
 
@@ -249,7 +255,8 @@ def test_buffers_are_made_on_the_calls_stream(monkeypatch, name):
     monkeypatch.setattr(ra, "_alloc_on", lambda s: _Context() if s is stream else pytest.fail("another stream"))
     monkeypatch.setattr(ra, "_stream", lambda s: 0)
     monkeypatch.setattr(ra, "_on_current_device", lambda *a: None)
-    monkeypatch.setattr(ra, "ra_paged_attend_scratch_size", lambda *a: 4096)
+    for size in ("ra_paged_attend_scratch_size", "ra_paged_weigh_scratch_size"):
+        monkeypatch.setattr(ra, size, lambda *a: 4096)
     real = torch.empty
     monkeypatch.setattr(torch, "empty", lambda *a, **kw: (made.append(bool(inside)), real(*a, **kw))[1])
     _binding_calls(kv, rope, t, stream)[name]()
