@@ -161,8 +161,14 @@ int64_t chunk_scratch(const ra_paged_s* kv, int64_t shares) {
   const int64_t rows = shares * 2 * 2 * 128;
   return rows * (kv->prob.head_dim * 4 + 16) + shares * 16;
 }
-// Bytes of the weights' chunk kernel: a sum per key for two parts of every share, and the joins.
-int64_t weigh_scratch(int64_t grid) { return grid * (2 * 256 * 4 + 16); }
+// Scratch of the weights' chunk kernel: 16 bytes a row of every query tile, a sum per key for two
+// parts of every share, the joins, the sequences' first tiles.
+int64_t weigh_tiles(const ra_paged_s* kv, int64_t batch, int64_t tokens) {
+  return tokens / (128 / (kv->prob.heads_q / kv->prob.heads_kv)) + batch;
+}
+int64_t weigh_scratch(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t grid) {
+  return kv->prob.heads_kv * weigh_tiles(kv, batch, tokens) * 128 * 16 + grid * (2 * 256 * 4 + 16) + (batch + 3) / 4 * 16;
+}
 // The largest power of two in 16..128 that divides a page.
 int piece_of(const ra_paged_problem& pb) {
   int piece = 16;
@@ -369,7 +375,7 @@ ra_status ra_paged_weigh_scratch_size(ra_paged_t kv, int64_t batch, int64_t toke
   if (kv == nullptr || bytes == nullptr) return fail(RA_ERR_INVALID_ARG, "null argument");
   const ra_status s = check_sizes(kv, batch, tokens, table_width);
   if (s != RA_OK) return s;
-  *bytes = takes_chunks(kv, batch, tokens, table_width) ? weigh_scratch(chunk_grid(kv)) : 0;
+  *bytes = takes_chunks(kv, batch, tokens, table_width) ? weigh_scratch(kv, batch, tokens, chunk_grid(kv)) : 0;
   return ok();
 }
 
@@ -408,6 +414,7 @@ ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_
     c.window = (int32_t)std::min(pb.window, kMaxPositions);
     c.sinks = pb.window > 0 ? (int32_t)std::min(pb.sinks, kMaxPositions) : 0;
     c.piece = piece_of(pb);
+    c.scale = pb.scale;
     c.scale_log2 = pb.scale * 1.4426950408889634f;
     c.q = q;
     c.qs = prm.qs;
@@ -416,8 +423,11 @@ ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_
     c.weight = weight;
     c.weight_width = weight_width;
     const int grid = chunk_grid(kv);
-    c.parts = scratch;
-    c.joins = reinterpret_cast<ra::PagedWeighJoin*>(scratch + (int64_t)grid * 2 * 256);
+    c.tiles = (int32_t)weigh_tiles(kv, batch, tokens);
+    c.extra = reinterpret_cast<uint4*>(scratch);
+    c.parts = scratch + (int64_t)pb.heads_kv * c.tiles * 128 * 4;
+    c.joins = reinterpret_cast<ra::PagedWeighJoin*>(c.parts + (int64_t)grid * 2 * 256);
+    c.extra_at = reinterpret_cast<int32_t*>(c.joins + grid);
     const char* why = "";
     const cudaError_t e = ra::launch_paged_weigh_chunk(pb.head_dim, c, grid, st, &why);
     if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache weights: %s (%s)", why, cudaGetErrorString(e));

@@ -99,7 +99,7 @@ struct PagedWeighChunkParams {
   int32_t heads_q, group;
   int32_t window, sinks;
   int32_t piece;  // as in PagedChunkParams
-  float scale_log2;
+  float scale, scale_log2;
   const void* q;
   PagedStrides qs;
   const float* lse;
@@ -107,6 +107,9 @@ struct PagedWeighChunkParams {
   float* weight;
   int64_t weight_width;
   float* parts;           // [share, 2, 256]
+  uint4* extra;           // [head, tiles, 128]: the rows' LSE as bf16 channels
+  int32_t* extra_at;      // [batch]: the sequences' first tiles
+  int32_t tiles;          // tokens / (128 / group) + batch at most
   PagedWeighJoin* joins;  // [share]
 };
 

@@ -14,14 +14,18 @@
 // Bound by the tensor cores and the exponentials alike: a pair of tiles of 128 x 128 scores is
 // 512 cycles of either (d = 128).
 //
-// Roles (one CTA per SM, 12 warps): warp 0 TMA producer, warp 1 tcgen05 issuer, warp 2 the
-// items' records, warp 3 the rows' LSE, warps 4-7 sums of key tile 0, warps 8-11 of key tile 1
-// (one thread per key).  TMEM: two buffers of 128 columns per key tile.
+// Roles (one CTA per SM, 20 warps): warp 0 TMA producer, warp 1 tcgen05 issuer, warp 2 the
+// items' records, warps 4-19 sums: four for each key tile and half of the
+// columns (two threads per key, whose sums meet in shared memory at an item's end).  With one
+// thread per key, two warps per scheduler, neither unit was busy half of the time.
+// TMEM: scores of the two key tiles 0-127 and 128-255, the keys 256-319 and 320-383, their extra
+// channels 384-391.
 //
 // Every mbarrier wait is bounded as in paged_chunk_sm103.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -30,26 +34,22 @@
 namespace ra {
 namespace {
 
-constexpr int kWarps = 12;
+constexpr int kWarps = 20;
 constexpr int kThreads = kWarps * 32;
-constexpr uint32_t kRegsLaunch = 168;
-constexpr uint32_t kRegsOther = 120;
-constexpr uint32_t kRegsSums = 192;
-static_assert(128 * kRegsOther + 256 * kRegsSums <= kThreads * kRegsLaunch, "register split");
 constexpr int kTile = 128;
 constexpr int kPair = 2 * kTile;  // keys of an item
-constexpr int kKeySlots = 3;      // key tiles in shared memory: an item's two and the next one's first
+constexpr int kKeySlots = 2;      // key tiles on their way to tensor memory
 constexpr int kStages = 3;        // query tiles
-constexpr int kLseSlots = 4;
 constexpr int kItemSlots = 4;
 constexpr int kMinUnits = 2;      // query tiles of a share
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kExtra = kTile * 32;  // bytes of a tile's 16 channels more: [2][128 rows][16 bytes], the second half zeros
 
 struct alignas(16) Record {
   int32_t head, b, key0, part;    // part: where to leave the sums, or -1: the item is whole
   int32_t token0, count, length;  // of the sequence
   int32_t t0, n;                  // query tiles [t0, t0 + n); n 0: no more items
-  int32_t pad[3];
+  int32_t extra;                  // place of the sequence's first tile among the tiles' extra channels
+  int32_t pad[2];
   __device__ __forceinline__ int slot0() const { return length - count; }
 };
 
@@ -59,10 +59,11 @@ struct Smem {
   static constexpr uint32_t kHalf = kTile * 128;
   static constexpr uint32_t kOffK = 0;
   static constexpr uint32_t kOffQ = kKeySlots * kTileBytes;
-  static constexpr uint32_t kOffLse = kOffQ + kStages * kTileBytes;
-  static constexpr uint32_t kOffRec = kOffLse + kLseSlots * kTile * 4;
+  static constexpr uint32_t kOffExtra = kOffQ + kStages * kTileBytes;
+  static constexpr uint32_t kOffHalf = kOffExtra + kStages * kExtra;  // sums of the second halves, by item slot
+  static constexpr uint32_t kOffRec = kOffHalf + kItemSlots * kPair * 4;
   static constexpr uint32_t kOffBar = kOffRec + kItemSlots * (uint32_t)sizeof(Record);
-  static constexpr uint32_t kOffPrefix = kOffBar + 384;
+  static constexpr uint32_t kOffPrefix = kOffBar + 448;
   static constexpr uint32_t kFixed = kOffPrefix + 1024;  // + slack to align the base to 1 KiB
 };
 
@@ -71,22 +72,38 @@ enum : int {
   kKEmpty = kKFull + kKeySlots,
   kQFull = kKEmpty + kKeySlots,
   kQEmpty = kQFull + kStages,
-  kSFull = kQEmpty + kStages,  // key tile * 2 + buffer
-  kSEmpty = kSFull + 4,
-  kLFull = kSEmpty + 4,
-  kLEmpty = kLFull + kLseSlots,
-  kItemFull = kLEmpty + kLseSlots,
+  kSFull = kQEmpty + kStages,  // one per key tile
+  kSEmpty = kSFull + 2,
+  kKReady = kSEmpty + 2,       // keys in tensor memory
+  kHalfSum = kKReady + 2,  // key tile * kItemSlots + item slot
+  kItemFull = kHalfSum + 2 * kItemSlots,
   kItemEmpty = kItemFull + kItemSlots,
   kDone = kItemEmpty + kItemSlots,
   kNumBars = kDone + 1
 };
-constexpr uint32_t kItemConsumers = 11;  // producer, MMA, LSE and 8 warps of sums
+constexpr uint32_t kItemConsumers = 18;  // producer, MMA and 16 warps of sums
 constexpr uint32_t kOffSlot = 8 * kNumBars, kOffAbort = kOffSlot + 4, kOffNotes = kOffSlot + 8;
-static_assert(kOffNotes + 4 * 2 * kItemSlots <= 384, "barriers");
+static_assert(kOffNotes + 4 * 2 * kItemSlots <= 448, "barriers");
 
 constexpr uint32_t kTmemCols = 512;
-__device__ __forceinline__ uint32_t col_s(int g, int buf) { return (uint32_t)(2 * g + buf) * 128u; }
+__device__ __forceinline__ uint32_t col_s(int g) { return (uint32_t)g * 128u; }
+__device__ __forceinline__ uint32_t col_k(int g) { return 256u + (uint32_t)g * 64u; }  // two channels a column
+constexpr uint32_t kColOnes = 384;                                                     // 16 channels: 1, 1, 1, 0 ..
+
 constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kTile, kTile, false, false);  // K, Q both K-major
+// An operand without a swizzle: groups of 8 rows of 16 bytes follow each other (128 bytes), the
+// two halves of the 16 channels lie 2 KiB apart.
+__device__ __forceinline__ uint64_t plain_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(2048u >> 4) << 16) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1 << 46);
+}
+// D[tmem] += A[tmem] * B[smem], one step of 16; a converged warp executes it, one elected lane issues.
+__device__ __forceinline__ void mma_extra_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc)
+      : "memory");
+}
 
 // --------------------------------------------------------------------- shares --
 // Whether some token of the call sees slot j of a sequence.
@@ -185,6 +202,7 @@ __device__ void run_records(const PagedWeighChunkParams& P, const Ctl& c, Record
         r.length = q.length;
         r.t0 = t.t0 + u0;
         r.n = u1 - u0;
+        r.extra = __ldg(P.extra_at + b);
         if (cut && u0 == 0) P.joins[s] = {head, b, i * kPair, (int)(((item_x + t.n) * sh.count - 1) / sh.all)};
         ptx::mbar_arrive(c.bar(kItemFull + (int)slot));
       }
@@ -270,15 +288,18 @@ __device__ void run_producer(const PagedWeighChunkParams& P, const Ctl& c, uint3
       const uint32_t dst = sbase + S::kOffQ + s * S::kTileBytes;
       const int h = r->head * P.group, token = r->token0 + t * per_tile;
       RA_BOUNDS(c.status, token >= 0 && token < P.t.tokens && h + P.group <= P.heads_q, 133);
-      ptx::mbar_arrive_expect_tx_warp(c.bar(kQFull + (int)s), q_bytes);
+      ptx::mbar_arrive_expect_tx_warp(c.bar(kQFull + (int)s), q_bytes + kExtra / 2);
       tma_load_3d_warp(dst, tq, c.bar(kQFull + (int)s), 0, h, token);
       if (D == 128) tma_load_3d_warp(dst + S::kHalf, tq, c.bar(kQFull + (int)s), 64, h, token);
+      const int at = min(r->extra + t, P.tiles - 1);
+      RA_BOUNDS(c.status, r->extra >= 0 && r->extra + t < P.tiles, 136);
+      ptx::bulk_load_warp(sbase + S::kOffExtra + s * kExtra, P.extra + ((int64_t)r->head * P.tiles + at) * kTile, kExtra / 2,
+                          c.bar(kQFull + (int)s));
       ++st.q_issued;
       return true;
     };
-    // (the second key tile's place is the one that the item before frees last)
-    if (!load_keys(0) || !load_queries(r->t0) || !load_keys(1)) return;
-    for (int t = 1; t < r->n; ++t)
+    if (!load_keys(0) || !load_keys(1)) return;
+    for (int t = 0; t < r->n; ++t)
       if (!load_queries(r->t0 + t)) return;
     release_record(c, u, lane);
   }
@@ -288,8 +309,9 @@ __device__ void run_producer(const PagedWeighChunkParams& P, const Ctl& c, uint3
 template <int D>
 __device__ void run_mma(const Ctl& c, uint32_t sbase, const Record* recs, uint32_t tmem, int lane) {
   using S = Smem<D>;
-  const uint32_t k0 = ptx::desc_lo(sbase + S::kOffK, 16), q0 = ptx::desc_lo(sbase + S::kOffQ, 16);
-  RA_BOUNDS(c.status, tmem == 0u && col_s(1, 1) + 128u <= kTmemCols, 134);
+  const uint32_t q0 = ptx::desc_lo(sbase + S::kOffQ, 16);
+  const uint64_t extra0 = plain_desc(sbase + S::kOffExtra);
+  RA_BOUNDS(c.status, tmem == 0u && kColOnes + 8u <= kTmemCols, 134);
   uint32_t tile = 0;
   for (uint32_t u = 0;; ++u) {
     const Record* r = next_record(c, recs, u, kStatusTimeoutMma);
@@ -301,60 +323,51 @@ __device__ void run_mma(const Ctl& c, uint32_t sbase, const Record* recs, uint32
       if (!RA_WAIT(kQFull + (int)qs, tile / kStages, kStatusTimeoutMma)) return;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const uint32_t k = 2 * u + g, ks = k % kKeySlots;
-        if (t == 0 && !RA_WAIT(kKFull + (int)ks, k / kKeySlots, kStatusTimeoutMma)) return;
-        const int buf = (int)(tile & 1u);
-        if (!RA_WAIT(kSEmpty + 2 * g + buf, (tile >> 1) ^ 1u, kStatusTimeoutMma)) return;
+        if (t == 0 && !RA_WAIT(kKReady + g, u, kStatusTimeoutMma)) return;
+        if (!RA_WAIT(kSEmpty + g, tile ^ 1u, kStatusTimeoutMma)) return;
         ptx::tc_fence_after();
-        const uint32_t a0 = k0 + ks * (S::kTileBytes >> 4), b0 = q0 + qs * (S::kTileBytes >> 4);
+        const uint32_t b0 = q0 + qs * (S::kTileBytes >> 4);
 #pragma unroll
         for (uint32_t kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * S::kHalf + (kk & 3u) * 32u) >> 4;
-          ptx::mma_bf16_ss_lo_warp(tmem + col_s(g, buf), a0 + off, b0 + off, kIdescS, kk > 0 ? 1u : 0u);
+          ptx::mma_bf16_ts_lo_warp(tmem + col_s(g), tmem + col_k(g) + kk * 8u, b0 + off, kIdescS, kk > 0 ? 1u : 0u);
         }
-        ptx::mma_commit_warp(c.bar(kSFull + 2 * g + buf));
-        if (t == n - 1) ptx::mma_commit_warp(c.bar(kKEmpty + (int)ks));
+        // (last: the scores' own sums are not cut at the size of the LSE)
+        mma_extra_warp(tmem + col_s(g), tmem + kColOnes, extra0 + qs * (kExtra >> 4), kIdescS);
+        ptx::mma_commit_warp(c.bar(kSFull + g));
       }
       ptx::mma_commit_warp(c.bar(kQEmpty + (int)qs));
     }
   }
 }
 
-// ----------------------------------------------------------------------- LSE --
-// Warp 3: the negated LSE of every query tile's rows, in log2 units.
-__device__ void run_lse(const PagedWeighChunkParams& P, const Ctl& c, const Record* recs, float* lse, int per_tile, int lane) {
-  uint32_t tile = 0;
-  for (uint32_t u = 0;; ++u) {
-    const Record* r = next_record(c, recs, u, kStatusTimeoutSoftmax);
-    if (r == nullptr) return;
-    for (int t = 0; t < r->n; ++t, ++tile) {
-      float x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = lane + 32 * i, tok = row / P.group, token = (r->t0 + t) * per_tile + tok;
-        x[i] = -INFINITY;
-        if (tok < per_tile && token < r->count)
-          x[i] = -kLog2e * __ldg(P.lse + (int64_t)(r->token0 + token) * P.heads_q + r->head * P.group + row - tok * P.group);
-      }
-      const uint32_t s = tile % kLseSlots;
-      if (!RA_WAIT(kLEmpty + (int)s, (tile / kLseSlots) ^ 1u, kStatusTimeoutSoftmax)) return;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) lse[s * kTile + lane + 32 * i] = x[i];
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(c.bar(kLFull + (int)s));
-    }
-    release_record(c, u, lane);
-  }
-}
-
 // ---------------------------------------------------------------------- sums --
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : ~(~0u << n)); }
+// 32 or 16 registers per thread -> 32 lanes by as many columns of tensor memory, waited.
+__device__ __forceinline__ void tmem_st32_words(uint32_t taddr, const uint32_t (&r)[32]) { ptx::tmem_st32(taddr, r); }
+__device__ __forceinline__ void tmem_st16_words(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
 __device__ __forceinline__ int clamped(int64_t x) { return (int)max((int64_t)-1, min((int64_t)(kTile + 1), x)); }
 
-__device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, const Record* recs, const volatile uint32_t* notes,
-                         const float* lse, uint32_t tmem, int g, int wq, int per_tile, int lane) {
+template <int D>
+__device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, uint32_t sbase, const Record* recs,
+                         const volatile uint32_t* notes,
+                         float* halves, uint32_t tmem, int g, int half, int wq, int per_tile, int lane) {
   const int row = wq * 32 + lane;  // TMEM lane = key of the tile
-  const uint32_t tS = tmem + ((uint32_t)(wq * 32) << 16);
+  const uint32_t tS = tmem + ((uint32_t)(wq * 32) << 16) + half * 64;
   RA_BOUNDS(c.status, wq >= 0 && wq < 4, 135);
   const float2 sc2 = make_float2(P.scale_log2, P.scale_log2);
   uint32_t tile = 0;
@@ -363,6 +376,29 @@ __device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, const Rec
     if (r == nullptr) return;
     const int j = r->key0 + g * kTile + row, slot0 = r->slot0(), count = r->count, n = r->n, t0 = r->t0;
     const bool mine = j < r->length && seen_by_some(P, slot0, count, j);
+    // The keys into tensor memory, from where the products take them: as operands from shared
+    // memory both sides together cost more of its cycles than the product takes.  The products of
+    // the item before are done (its last scores were waited for).
+    {
+      const int ks = g;  // (two places, two tiles an item)
+      if (!RA_WAIT(kKFull + ks, u, kStatusTimeoutSoftmax)) return;
+      uint32_t w[D / 4];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {  // 16 bytes at a time of this thread's half of the row
+        const int ch = half * (D / 16) + i;
+        const uint32_t at = sbase + Smem<D>::kOffK + ks * Smem<D>::kTileBytes + (ch >> 3) * Smem<D>::kHalf + row * 128 +
+                            (((ch & 7) ^ (row & 7)) * 16);
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3]) : "r"(at) : "memory");
+      }
+      const uint32_t to = tmem + ((uint32_t)(wq * 32) << 16) + col_k(g) + half * (D / 4);
+      if constexpr (D == 128) tmem_st32_words(to, w);
+      else tmem_st16_words(to, w);
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(c.bar(kKReady + g));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(c.bar(kKEmpty + ks));
+    }
     float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     for (int t = 0; t < n; ++t, ++tile) {
       const int first = slot0 + (t0 + t) * per_tile;  // slot of the tile's first token
@@ -374,32 +410,27 @@ __device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, const Rec
         if (P.window > 0 && j >= P.sinks) c_hi = min(c_hi, clamped((int64_t)j + P.window - first) * P.group);
       }
       const bool full = c_lo <= 0 && c_hi >= per_tile * P.group;
-      const int buf = (int)(tile & 1u);
-      const uint32_t ls = tile % kLseSlots;
-      bool ok = wait_bar(c, c.bar(kLFull + (int)ls), (tile / kLseSlots) & 1u, kStatusTimeoutSoftmax);
-      ok = ok && wait_bar(c, c.bar(kSFull + 2 * g + buf), (tile >> 1) & 1u, kStatusTimeoutSoftmax);
+      const bool ok = wait_bar(c, c.bar(kSFull + g), tile & 1u, kStatusTimeoutSoftmax);
       if (!__all_sync(0xffffffffu, ok)) return;
       ptx::tc_fence_after();
-      uint32_t raw[128];
-      ptx::tmem_ld128(tS + col_s(g, buf), raw);
+      uint32_t raw[64];
+      ptx::tmem_ld32x2(tS + col_s(g), tS + col_s(g) + 32, raw);
       ptx::tc_fence_before();
-      ptx::mbar_arrive(c.bar(kSEmpty + 2 * g + buf));
+      ptx::mbar_arrive(c.bar(kSEmpty + g));
       const float* s = reinterpret_cast<const float*>(raw);
-      const float4* neg = reinterpret_cast<const float4*>(lse + ls * kTile);
       auto sums = [&](auto edge) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t bits = ~0u;
           if (decltype(edge)::value) {
-            bits = below(c_hi - 32 * q) & ~below(c_lo - 32 * q);
+            bits = below(c_hi - 64 * half - 32 * q) & ~below(c_lo - 64 * half - 32 * q);
             if (!__any_sync(0xffffffffu, bits != 0u)) continue;
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {  // columns 32 q + 4 e ..
+          for (int e = 0; e < 8; ++e) {  // columns 32 q + 4 e .. of this half
             const int col = 32 * q + 4 * e;
-            const float4 l4 = neg[col / 4];
-            float2 x = ptx::fma2(make_float2(s[col], s[col + 1]), sc2, make_float2(l4.x, l4.y));
-            float2 y = ptx::fma2(make_float2(s[col + 2], s[col + 3]), sc2, make_float2(l4.z, l4.w));
+            float2 x = ptx::mul2(make_float2(s[col], s[col + 1]), sc2);
+            float2 y = ptx::mul2(make_float2(s[col + 2], s[col + 3]), sc2);
             x.x = ptx::ex2_approx(x.x);
             x.y = ptx::ex2_approx(x.y);
             y.x = ptx::ex2_approx(y.x);
@@ -417,15 +448,23 @@ __device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, const Rec
       };
       if (__all_sync(0xffffffffu, full)) sums(std::false_type());
       else sums(std::true_type());
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(c.bar(kLEmpty + (int)ls));
     }
     const float2 a = ptx::add2(ptx::add2(acc[0], acc[1]), ptx::add2(acc[2], acc[3]));
-    const bool bad = (notes[2 * (u % kItemSlots) + g] >> (row / P.piece)) & 1u;
-    if (mine) {
-      // (a sum of weights is never negative: -1 stands for a key whose page is none)
-      if (r->part >= 0) P.parts[(int64_t)r->part * kPair + g * kTile + row] = bad ? -1.f : a.x + a.y;
-      else if (!bad) put(P, r->b, r->head, j, slot0, a.x + a.y);
+    // (an item's place is written again four items on, when this item's record was given back)
+    const uint32_t slot = u % kItemSlots;
+    float* other = halves + slot * kPair + g * kTile + row;
+    if (half == 1) {
+      *other = a.x + a.y;
+      ptx::mbar_arrive(c.bar(kHalfSum + g * kItemSlots + (int)slot));
+    } else {
+      if (!RA_WAIT(kHalfSum + g * kItemSlots + (int)slot, u / kItemSlots, kStatusTimeoutSoftmax)) return;
+      const float sum = (a.x + a.y) + *other;
+      const bool bad = (notes[2 * slot + g] >> (row / P.piece)) & 1u;
+      if (mine) {
+        // (a sum of weights is never negative: -1 stands for a key whose page is none)
+        if (r->part >= 0) P.parts[(int64_t)r->part * kPair + g * kTile + row] = bad ? -1.f : sum;
+        else if (!bad) put(P, r->b, r->head, j, slot0, sum);
+      }
     }
     release_record(c, u, lane);
   }
@@ -445,7 +484,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ctl c{sbase + S::kOffBar, reinterpret_cast<volatile uint32_t*>(ctl + kOffAbort), P.t.status};
   uint32_t* notes = reinterpret_cast<uint32_t*>(ctl + kOffNotes);
   Record* recs = reinterpret_cast<Record*>(sgen + S::kOffRec);
-  float* lse = reinterpret_cast<float*>(sgen + S::kOffLse);
   int64_t* prefix = reinterpret_cast<int64_t*>(sgen + S::kOffPrefix);
   const int per_tile = kTile / P.group;
 
@@ -461,17 +499,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   sh.count = (int)max((int64_t)1, min((int64_t)gridDim.x, sh.all / kMinUnits));
   if (sh.all == 0 || (int)blockIdx.x >= sh.count) return;
 
-  // Rows that a query tile's box never fills meet an LSE of infinity: they have to be finite.
+  for (uint32_t at = threadIdx.x * 16; at < kStages * kExtra; at += kThreads * 16)
+    ptx::st_shared_v4(sbase + S::kOffExtra + at, 0u, 0u, 0u, 0u);
+  ptx::fence_proxy_async_smem();
+  // Rows that a query tile's box never fills have no weight: they have to be finite.
   if (per_tile * P.group < kTile) {
     for (uint32_t at = threadIdx.x * 16; at < kStages * S::kTileBytes; at += kThreads * 16)
       ptx::st_shared_v4(sbase + S::kOffQ + at, 0u, 0u, 0u, 0u);
     ptx::fence_proxy_async_smem();
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kKeySlots; ++s) ptx::mbar_init(c.bar(kKFull + s), 1), ptx::mbar_init(c.bar(kKEmpty + s), 1);
+    for (int s = 0; s < kKeySlots; ++s) ptx::mbar_init(c.bar(kKFull + s), 1), ptx::mbar_init(c.bar(kKEmpty + s), 8);
     for (int s = 0; s < kStages; ++s) ptx::mbar_init(c.bar(kQFull + s), 1), ptx::mbar_init(c.bar(kQEmpty + s), 1);
-    for (int s = 0; s < 4; ++s) ptx::mbar_init(c.bar(kSFull + s), 1), ptx::mbar_init(c.bar(kSEmpty + s), kTile);
-    for (int s = 0; s < kLseSlots; ++s) ptx::mbar_init(c.bar(kLFull + s), 1), ptx::mbar_init(c.bar(kLEmpty + s), 8);
+    for (int g = 0; g < 2; ++g) {
+      ptx::mbar_init(c.bar(kSFull + g), 1);
+      ptx::mbar_init(c.bar(kSEmpty + g), 2 * kTile);
+      ptx::mbar_init(c.bar(kKReady + g), 2 * kTile);
+    }
+    for (int s = 0; s < 2 * kItemSlots; ++s) ptx::mbar_init(c.bar(kHalfSum + s), kTile);
     for (int s = 0; s < kItemSlots; ++s) {
       ptx::mbar_init(c.bar(kItemFull + s), 1);
       ptx::mbar_init(c.bar(kItemEmpty + s), kItemConsumers);
@@ -492,10 +537,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(ctl + kOffSlot);
+  if (warp >= 4 && warp < 8) {  // the keys' extra channels
+    const uint32_t ones[8] = {0x3f803f80u, 0x3f80u, 0u, 0u, 0u, 0u, 0u, 0u};
+    tmem_st8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColOnes, ones);
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
 
   ProducerState ps{0u, 0u};
   if (warp < 4) {
-    ptx::regs_release<kRegsOther>();
     if (warp == 0) {
       run_producer<D>(P, c, sbase, recs, notes, &tq, &tkv, ps, per_tile, lane);
       __syncwarp();
@@ -507,12 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 2) {
       run_records(P, c, recs, prefix, sh, per_tile, lane);
-    } else {
-      run_lse(P, c, recs, lse, per_tile, lane);
     }
   } else {
-    ptx::regs_acquire<kRegsSums>();
-    run_sums(P, c, recs, notes, lse, tmem, (warp - 4) >> 2, warp & 3, per_tile, lane);
+    const int w = (warp - 4) >> 2;
+    run_sums<D>(P, c, sbase, recs, notes, reinterpret_cast<float*>(sgen + S::kOffHalf), tmem, w & 1, w >> 1, warp & 3, per_tile, lane);
   }
 
   if (warp == 0 && lane == 0 && *c.abort) {  // (every lane of warp 0 holds the same counts)
@@ -528,6 +577,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------ extra channels --
+// -LSE / scale of every query tile's rows as three bf16 terms; of rows of no token a number that
+// leaves nothing of their weights.  A thread has a row; the tiles of the sequences follow each other.
+__global__ void __launch_bounds__(kTile) paged_weigh_extra_kernel(const PagedWeighChunkParams P) {
+  extern __shared__ int64_t prefix[];
+  const int per_tile = kTile / P.group;
+  paged_sums<kTile / 32>(P.t.batch, prefix, [&](int b) { return (int64_t)((paged_seq(P.t, b).count + per_tile - 1) / per_tile); });
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int b = threadIdx.x; b < P.t.batch; b += kTile) P.extra_at[b] = (int32_t)min(prefix[b], (int64_t)P.tiles - 1);
+  const int head = (int)blockIdx.y, row = threadIdx.x, tok = row / P.group;
+  const float inv = -1.0f / P.scale;
+  // (offsets that fall can make sequences share tokens: no more tiles than there is room for)
+  const int tiles = (int)min(prefix[P.t.batch], (int64_t)P.tiles);
+  for (int i = (int)blockIdx.x; i < tiles; i += (int)gridDim.x) {
+    const int b = paged_find(prefix, P.t.batch, i);
+    const PagedSeq q = paged_seq(P.t, b);
+    const int token = (i - (int)prefix[b]) * per_tile + tok;
+    float x = -1e30f;
+    if (tok < per_tile && token < q.count)
+      x = inv * __ldg(P.lse + (int64_t)(q.token0 + token) * P.heads_q + head * P.group + row - tok * P.group);
+    const uint32_t hi = ptx::pack_bf16x2(x, 0.f) & 0xffffu;
+    const float r1 = x - __uint_as_float(hi << 16);  // (exact; NaN where x is not finite)
+    const uint32_t mid = fabsf(r1) <= 3e38f ? ptx::pack_bf16x2(r1, 0.f) & 0xffffu : 0u;
+    const float r2 = r1 - __uint_as_float(mid << 16);
+    const uint32_t lo = fabsf(r2) <= 3e38f ? ptx::pack_bf16x2(r2, 0.f) & 0xffffu : 0u;
+    P.extra[((int64_t)head * P.tiles + i) * kTile + row] = make_uint4(hi | (mid << 16), lo, 0u, 0u);
   }
 }
 
@@ -557,8 +635,15 @@ cudaError_t launch(const PagedWeighChunkParams& prm, int grid, cudaStream_t stre
   static std::atomic<int> ready[kMaxDevices];
   constexpr uint32_t kMost = Smem<D>::kFixed + (kMaxChunkSequences + 1) * 8;
   static_assert(kMost <= 232448, "shared memory");
-  cudaError_t e = prepare_once(paged_weigh_chunk_kernel<D>, ready, kThreads, 128 * kRegsOther + 256 * kRegsSums, (int)kMost, why);
+  cudaError_t e = prepare_once(paged_weigh_chunk_kernel<D>, ready, kThreads, 0, (int)kMost, why);
   if (e != cudaSuccess) return e;
+  const dim3 extra((unsigned)std::min(prm.tiles, 1024), (unsigned)prm.t.heads_kv);
+  paged_weigh_extra_kernel<<<extra, kTile, (prm.t.batch + 1) * 8, stream>>>(prm);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    *why = "launch failed";
+    return e;
+  }
   paged_weigh_chunk_kernel<D><<<grid, kThreads, Smem<D>::kFixed + (prm.t.batch + 1) * 8, stream>>>(tq, tkv, prm);
   e = cudaGetLastError();
   if (e == cudaSuccess) {
