@@ -615,8 +615,8 @@ __device__ void run_softmax(const PagedChunkParams& P, const Ctl& c, uint8_t* st
       l += part_sum;
       fix += top_fix;
       ptx::tc_fence_before();
-      ptx::mbar_arrive(c.bar(kPFull + g));
       __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(c.bar(kPFull + g));
     }
     bool ok = wait_bar(c, c.bar(kOFull + g), oj & 1u, kStatusTimeoutSoftmax);
     ++oj;
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(c.bar(kQFull + g), 1);
       ptx::mbar_init(c.bar(kQEmpty + g), 1);
       ptx::mbar_init(c.bar(kSFull + g), 1);
-      ptx::mbar_init(c.bar(kPFull + g), 128);
+      ptx::mbar_init(c.bar(kPFull + g), 4);
       ptx::mbar_init(c.bar(kOFull + g), 1);
     }
     for (int s = 0; s < kStages; ++s) {

@@ -395,9 +395,11 @@ __device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, uint32_t 
       if constexpr (D == 128) tmem_st32_words(to, w);
       else tmem_st16_words(to, w);
       ptx::tc_fence_before();
-      ptx::mbar_arrive(c.bar(kKReady + g));
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(c.bar(kKEmpty + ks));
+      if (lane == 0) {
+        ptx::mbar_arrive(c.bar(kKReady + g));
+        ptx::mbar_arrive(c.bar(kKEmpty + ks));
+      }
     }
     float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     for (int t = 0; t < n; ++t, ++tile) {
@@ -416,7 +418,8 @@ __device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, uint32_t 
       uint32_t raw[64];
       ptx::tmem_ld32x2(tS + col_s(g), tS + col_s(g) + 32, raw);
       ptx::tc_fence_before();
-      ptx::mbar_arrive(c.bar(kSEmpty + g));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(c.bar(kSEmpty + g));  // (a warp's 32 arrivals would come one after the other)
       const float* s = reinterpret_cast<const float*>(raw);
       auto sums = [&](auto edge) {
 #pragma unroll
@@ -455,7 +458,8 @@ __device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, uint32_t 
     float* other = halves + slot * kPair + g * kTile + row;
     if (half == 1) {
       *other = a.x + a.y;
-      ptx::mbar_arrive(c.bar(kHalfSum + g * kItemSlots + (int)slot));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(c.bar(kHalfSum + g * kItemSlots + (int)slot));
     } else {
       if (!RA_WAIT(kHalfSum + g * kItemSlots + (int)slot, u / kItemSlots, kStatusTimeoutSoftmax)) return;
       const float sum = (a.x + a.y) + *other;
@@ -513,10 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) ptx::mbar_init(c.bar(kQFull + s), 1), ptx::mbar_init(c.bar(kQEmpty + s), 1);
     for (int g = 0; g < 2; ++g) {
       ptx::mbar_init(c.bar(kSFull + g), 1);
-      ptx::mbar_init(c.bar(kSEmpty + g), 2 * kTile);
-      ptx::mbar_init(c.bar(kKReady + g), 2 * kTile);
+      ptx::mbar_init(c.bar(kSEmpty + g), 8);
+      ptx::mbar_init(c.bar(kKReady + g), 8);
     }
-    for (int s = 0; s < 2 * kItemSlots; ++s) ptx::mbar_init(c.bar(kHalfSum + s), kTile);
+    for (int s = 0; s < 2 * kItemSlots; ++s) ptx::mbar_init(c.bar(kHalfSum + s), 4);
     for (int s = 0; s < kItemSlots; ++s) {
       ptx::mbar_init(c.bar(kItemFull + s), 1);
       ptx::mbar_init(c.bar(kItemEmpty + s), kItemConsumers);
