@@ -837,6 +837,7 @@ class Rope:
     def __init__(self, handle, problem):
         self._h = handle
         self.problem = problem
+        self.dtype = _torch().bfloat16 if problem["dtype"] == 1 else _torch().float32
 
     @property
     def handle(self):
@@ -880,52 +881,69 @@ def ra_rope_destroy(rope):
     rope.close()
 
 
-def _strides(t):
-    """Strides of all axes but the last, in elements, as a host array (0 along an axis of one)."""
-    return (ctypes.c_int64 * (t.dim() - 1))(*[st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride()[:-1])])
+_I64x2, _I64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
 
 
-def _need_rows(name, t, shape, dtype, device):
-    """``t`` must be of this shape, dtype and device (checked already), its last axis contiguous."""
-    if (not isinstance(t, (_TORCH or _torch()).Tensor) or t.shape != tuple(shape) or t.dtype != dtype or t.device != device
-            or (t.stride(-1) != 1 and t.shape[-1] > 1)):
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, contiguous along its "
-                         f"last axis")
+def _bad_rows(name, shape, dtype, device):
+    return ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, contiguous along its last axis")
+
+
+def _rows4(name, t, shape, dtype, device):
+    """Strides of ``t`` along its first three axes as a host array (0 along an axis of one), once it
+    is a tensor of this shape, dtype and device (checked already), its last axis contiguous."""
+    if not isinstance(t, _TORCH.Tensor) or t.shape != shape or t.dtype != dtype or t.device != device:
+        raise _bad_rows(name, shape, dtype, device)
+    a, b, c, e = t.stride()
+    if e != 1 and shape[3] > 1:
+        raise _bad_rows(name, shape, dtype, device)
+    return _I64x3(a if shape[0] > 1 else 0, b if shape[1] > 1 else 0, c if shape[2] > 1 else 0)
+
+
+def _rows3(name, t, shape, dtype, device):
+    """As _rows4, of a packed tensor."""
+    if not isinstance(t, _TORCH.Tensor) or t.shape != shape or t.dtype != dtype or t.device != device:
+        raise _bad_rows(name, shape, dtype, device)
+    a, b, e = t.stride()
+    if e != 1 and shape[2] > 1:
+        raise _bad_rows(name, shape, dtype, device)
+    return _I64x2(a if shape[0] > 1 else 0, b if shape[1] > 1 else 0)
 
 
 def _rope_call(call, rope, q, k, layout, n_shards, position, q_out, k_out, stream):
     torch = _TORCH or _torch()
-    pb = rope.problem
-    dtype = torch.bfloat16 if pb["dtype"] == 1 else torch.float32
+    d, dtype = rope.problem["head_dim"], rope.dtype
     if q.dim() != 4:
         raise ValueError("q must have the shape [B, Hq, S, d]")
     B, Hq, S, _ = q.shape
-    device = q.device
-    _need_rows("q", q, (B, Hq, S, pb["head_dim"]), dtype, device)
+    device, shape = q.device, (B, Hq, S, d)
+    qs = _rows4("q", q, shape, dtype, device)
     _on_current_device("q", q)
-    Hk = 0
-    if k is not None:
-        Hk = k.shape[1] if k.dim() == 4 else 0
-        _need_rows("k", k, (B, Hk, S, pb["head_dim"]), dtype, device)
-    elif k_out is not None:
-        raise ValueError("k_out without k")
     if position is not None:
         _need_like("position", position, (B, S), torch.int32, device)
-    if q_out is not None:
-        _need_rows("q_out", q_out, q.shape, dtype, device)
-    if k_out is not None:
-        _need_rows("k_out", k_out, k.shape, dtype, device)
-    if q_out is None or (k is not None and k_out is None):
+    if q_out is None:
         with _alloc_on(stream):
-            if q_out is None:
-                q_out = torch.empty((B, Hq, S, pb["head_dim"]), dtype=dtype, device=device)
-            if k is not None and k_out is None:
-                k_out = torch.empty((B, Hk, S, pb["head_dim"]), dtype=dtype, device=device)
-    key = k is not None
-    _check(call(rope.handle, B, S, Hq, Hk, _layout(layout), int(n_shards), _ptr(position), _ptr(q), _strides(q), _ptr(k),
-                _strides(k) if key else None, _ptr(q_out), _strides(q_out), _ptr(k_out), _strides(k_out) if key else None,
-                _stream(stream)))
-    return (q_out, k_out) if key else q_out
+            q_out = torch.empty(shape, dtype=dtype, device=device)
+        qos = _I64x3(Hq * S * d, S * d, d)
+    else:
+        qos = _rows4("q_out", q_out, shape, dtype, device)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        _check(call(rope.handle, B, S, Hq, 0, _layout(layout), int(n_shards), _ptr(position), q.data_ptr(), qs, None, None,
+                    q_out.data_ptr(), qos, None, None, _stream(stream)))
+        return q_out
+    Hk = k.shape[1] if k.dim() == 4 else 0
+    shape = (B, Hk, S, d)
+    ks = _rows4("k", k, shape, dtype, device)
+    if k_out is None:
+        with _alloc_on(stream):
+            k_out = torch.empty(shape, dtype=dtype, device=device)
+        kos = _I64x3(Hk * S * d, S * d, d)
+    else:
+        kos = _rows4("k_out", k_out, shape, dtype, device)
+    _check(call(rope.handle, B, S, Hq, Hk, _layout(layout), int(n_shards), _ptr(position), q.data_ptr(), qs, k.data_ptr(), ks,
+                q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream(stream)))
+    return q_out, k_out
 
 
 def ra_rope(rope, q, k=None, layout="contiguous", n_shards=1, position=None, q_out=None, k_out=None, stream=None):
@@ -950,6 +968,7 @@ class Paged:
         self._h = handle
         self.problem = problem
         pb = problem
+        self.dtype = _torch().bfloat16 if pb["dtype"] == 1 else _torch().float32
         self._shape = (pb["pages"], 2, pb["heads_kv"], pb["page_rows"], pb["head_dim"])
         # (batch, tokens, table width) of the last call, its bytes of scratch: attention's, the weights'
         self._scratch, self._weigh_scratch = (None, 0), (None, 0)
@@ -996,17 +1015,16 @@ def ra_paged_cache_shape(kv):
 def _paged_tables(kv, cache, page_table, length, offset=None):
     """The cache and the int32 tables of a call, all on one device -> (dtype, device, batch)."""
     torch = _TORCH or _torch()
-    dtype = torch.bfloat16 if kv.problem["dtype"] == 1 else torch.float32
-    device, i32 = cache.device, torch.int32
+    dtype, device, i32 = kv.dtype, cache.device, torch.int32
     _need("cache", cache, kv._shape, dtype, device)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 tensor of shape (sequences, pages of a sequence)")
-    batch = page_table.shape[0]
-    _need_like("page_table", page_table, page_table.shape, i32, device)
+    batch, width = page_table.shape
+    _need_like("page_table", page_table, (batch, width), i32, device)
     _need_like("length", length, (batch,), i32, device)
     if offset is not None:
         _need_like("offset", offset, (batch + 1,), i32, device)
-    return dtype, device, batch
+    return dtype, device, batch, width
 
 
 def ra_paged_append(kv, cache, k, v, page_table, offset, length, rope=None, position=None, q=None, q_out=None,
@@ -1019,25 +1037,26 @@ def ra_paged_append(kv, cache, k, v, page_table, offset, length, rope=None, posi
     """
     torch = _TORCH or _torch()
     pb = kv.problem
-    dtype, device, batch = _paged_tables(kv, cache, page_table, length, offset=offset)
-    T = k.shape[0] if k.dim() == 3 else 0
-    _need_rows("k", k, (T, pb["heads_kv"], pb["head_dim"]), dtype, device)
-    _need_rows("v", v, (T, pb["heads_kv"], pb["head_dim"]), dtype, device)
+    dtype, device, batch, width = _paged_tables(kv, cache, page_table, length, offset)
+    T, d = k.shape[0] if k.dim() == 3 else 0, pb["head_dim"]
+    shape = (T, pb["heads_kv"], d)
+    ks, vs = _rows3("k", k, shape, dtype, device), _rows3("v", v, shape, dtype, device)
     if position is not None:
         _need_like("position", position, (T,), torch.int32, device)
+    qs = qos = None
     if q is not None:
-        _need_rows("q", q, (T, pb["heads_q"], pb["head_dim"]), dtype, device)
+        shape = (T, pb["heads_q"], d)
+        qs = _rows3("q", q, shape, dtype, device)
         if q_out is None:
             with _alloc_on(stream):
-                q_out = torch.empty((T, pb["heads_q"], pb["head_dim"]), dtype=dtype, device=device)
-        else:
-            _need_rows("q_out", q_out, q.shape, dtype, device)
+                q_out = torch.empty(shape, dtype=dtype, device=device)
+        qos = _rows3("q_out", q_out, shape, dtype, device)
     elif q_out is not None:
         raise ValueError("q_out without q")
     _check(load_library().ra_paged_append(
-        kv.handle, None if rope is None else rope.handle, _ptr(cache), batch, T, _ptr(k), _strides(k), _ptr(v), _strides(v),
-        _ptr(q), None if q is None else _strides(q), _ptr(q_out), None if q is None else _strides(q_out),
-        _ptr(page_table), page_table.shape[1], _ptr(offset), _ptr(length), _ptr(position), _stream(stream)))
+        kv.handle, None if rope is None else rope.handle, cache.data_ptr(), batch, T, k.data_ptr(), ks, v.data_ptr(), vs,
+        _ptr(q), qs, _ptr(q_out), qos, page_table.data_ptr(), width, offset.data_ptr(), length.data_ptr(), _ptr(position),
+        _stream(stream)))
     return q_out
 
 
@@ -1059,26 +1078,25 @@ def ra_paged_attend(kv, cache, q, page_table, offset, length, o=None, lse=None, 
     """
     torch = _TORCH or _torch()
     pb = kv.problem
-    dtype, device, batch = _paged_tables(kv, cache, page_table, length, offset=offset)
+    dtype, device, batch, width = _paged_tables(kv, cache, page_table, length, offset)
     T = q.shape[0] if q.dim() == 3 else 0
     shape = (T, pb["heads_q"], pb["head_dim"])
-    _need_rows("q", q, shape, dtype, device)
-    need = ra_paged_attend_scratch_size(kv, batch, T, page_table.shape[1]) // 4
+    qs = _rows3("q", q, shape, dtype, device)
+    need = ra_paged_attend_scratch_size(kv, batch, T, width) // 4
     if scratch is not None:
         _need_scratch("ra_paged_attend_scratch_size", scratch, need, device)
-    if o is not None:
-        _need_rows("o", o, shape, dtype, device)
     if lse is not None:
         _need_like("lse", lse, (T, pb["heads_q"]), torch.float32, device)
     with _alloc_on(stream):
         if o is None:
             o = torch.empty(shape, dtype=dtype, device=device)
         if lse is None:
-            lse = torch.empty((T, pb["heads_q"]), dtype=torch.float32, device=device)
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=device)
         if scratch is None and need:
             scratch = torch.empty(need, dtype=torch.float32, device=device)
-    _check(load_library().ra_paged_attend(kv.handle, _ptr(cache), batch, T, _ptr(q), _strides(q), _ptr(page_table),
-                                          page_table.shape[1], _ptr(offset), _ptr(length), _ptr(o), _strides(o), _ptr(lse),
+    os = _rows3("o", o, shape, dtype, device)
+    _check(load_library().ra_paged_attend(kv.handle, cache.data_ptr(), batch, T, q.data_ptr(), qs, page_table.data_ptr(), width,
+                                          offset.data_ptr(), length.data_ptr(), o.data_ptr(), os, lse.data_ptr(),
                                           _ptr(scratch), _stream(stream)))
     return o, lse
 
@@ -1114,22 +1132,22 @@ def ra_paged_weigh(kv, cache, q, lse, page_table, offset, length, weight, weight
     """
     torch = _TORCH or _torch()
     pb = kv.problem
-    dtype, device, batch = _paged_tables(kv, cache, page_table, length, offset=offset)
+    dtype, device, batch, width = _paged_tables(kv, cache, page_table, length, offset)
     T = q.shape[0] if q.dim() == 3 else 0
-    _need_rows("q", q, (T, pb["heads_q"], pb["head_dim"]), dtype, device)
+    qs = _rows3("q", q, (T, pb["heads_q"], pb["head_dim"]), dtype, device)
     _need_like("lse", lse, (T, pb["heads_q"]), torch.float32, device)
     _need_weights("weight", weight, kv, batch, device)
     if weight_in is not None:
         _need_like("weight_in", weight_in, weight.shape, torch.float32, device)
-    need = ra_paged_weigh_scratch_size(kv, batch, T, page_table.shape[1]) // 4
+    need = ra_paged_weigh_scratch_size(kv, batch, T, width) // 4
     if scratch is not None:
         _need_scratch("ra_paged_weigh_scratch_size", scratch, need, device)
     elif need:
         with _alloc_on(stream):
             scratch = torch.empty(need, dtype=torch.float32, device=device)
-    _check(load_library().ra_paged_weigh(kv.handle, _ptr(cache), batch, T, _ptr(q), _strides(q), _ptr(lse), _ptr(page_table),
-                                         page_table.shape[1], _ptr(offset), _ptr(length), _ptr(weight_in), _ptr(weight),
-                                         weight.shape[2], _ptr(scratch), _stream(stream)))
+    _check(load_library().ra_paged_weigh(kv.handle, cache.data_ptr(), batch, T, q.data_ptr(), qs, lse.data_ptr(),
+                                         page_table.data_ptr(), width, offset.data_ptr(), length.data_ptr(), _ptr(weight_in),
+                                         weight.data_ptr(), weight.shape[2], _ptr(scratch), _stream(stream)))
     return weight
 
 
@@ -1142,7 +1160,7 @@ def ra_paged_evict(kv, cache, page_table, length, weight, keep, first=0, recent=
     kept: [sequences, Hkv, keep] int32, the slots they had (-1: none).
     """
     torch = _TORCH or _torch()
-    dtype, device, batch = _paged_tables(kv, cache, page_table, length)
+    _, device, batch, width = _paged_tables(kv, cache, page_table, length)
     _need_weights("weight", weight, kv, batch, device)
     if weight_out is None:
         weight_out = weight
@@ -1165,7 +1183,7 @@ def ra_paged_evict(kv, cache, page_table, length, weight, keep, first=0, recent=
                 kept = torch.empty((batch, hk, max(keep, 0)), dtype=torch.int32, device=device)
             if new_length is None:
                 new_length = torch.empty((batch,), dtype=torch.int32, device=device)
-    _check(load_library().ra_paged_evict(kv.handle, _ptr(cache), batch, _ptr(page_table), page_table.shape[1], _ptr(length),
+    _check(load_library().ra_paged_evict(kv.handle, _ptr(cache), batch, _ptr(page_table), width, _ptr(length),
                                          _ptr(weight), _ptr(weight_out), weight.shape[2], keep, int(first), int(recent),
                                          _ptr(new_table), new_table.shape[1], _ptr(kept), _ptr(new_length), _stream(stream)))
     return kept, new_length

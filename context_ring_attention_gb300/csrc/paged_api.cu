@@ -148,13 +148,23 @@ int chunk_rounds(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t wi
   return (int)std::max<int64_t>(1, std::min<int64_t>(ra::kMaxRounds, bytes / (64 << 10)));
 }
 
-// Whether a call goes to the chunk kernel, whose query tiles have 128 rows: from 16 rows per
-// sequence and head on in the mean.
-bool takes_chunks(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width) {
+// Which kernels a call takes.  A sequence with up to 16 query rows a head belongs to the row
+// kernels, which read its keys at the rate of HBM; one with more to the chunk kernels, whose query
+// tiles have 128 rows.  The counts are on the device: where a call may have sequences of both
+// kinds it launches both, each leaving out the other's sequences (a launch without work of its
+// own costs about 5 us).  A call whose largest sequence can have 128 rows at most (if every
+// sequence has a token) takes the row kernels alone.
+struct Route {
+  bool rows, chunks;
+};
+Route route_of(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width) {
   const ra_paged_problem& pb = kv->prob;
   const int64_t group = pb.heads_q / pb.heads_kv;
-  return pb.dtype == RA_DTYPE_BF16 && group <= 128 && batch <= ra::kMaxChunkSequences &&
-         width * pb.page_rows <= kMaxChunkSlots && tokens / (128 / group) <= kMaxChunkTiles && tokens * group > 16 * batch;
+  if (pb.dtype != RA_DTYPE_BF16 || group > 128 || batch > ra::kMaxChunkSequences || width * pb.page_rows > kMaxChunkSlots ||
+      tokens / (128 / group) > kMaxChunkTiles)
+    return {true, false};
+  if (batch == 1) return {tokens * group <= ra::kFewRows, tokens * group > ra::kFewRows};
+  return {true, (tokens - batch + 1) * group > 128};
 }
 
 int64_t chunk_scratch(const ra_paged_s* kv, int64_t shares) {
@@ -295,9 +305,10 @@ ra_status ra_paged_attend_scratch_size(ra_paged_t kv, int64_t batch, int64_t tok
   if (kv == nullptr || bytes == nullptr) return fail(RA_ERR_INVALID_ARG, "null argument");
   const ra_status s = check_sizes(kv, batch, tokens, table_width);
   if (s != RA_OK) return s;
-  *bytes = takes_chunks(kv, batch, tokens, table_width)
-               ? chunk_scratch(kv, (int64_t)chunk_grid(kv) * chunk_rounds(kv, batch, tokens, table_width))
-               : rows_scratch(kv, row_slots(kv, batch, tokens, table_width));
+  const Route route = route_of(kv, batch, tokens, table_width);
+  *bytes = 0;
+  if (route.chunks) *bytes += chunk_scratch(kv, (int64_t)chunk_grid(kv) * chunk_rounds(kv, batch, tokens, table_width));
+  if (route.rows) *bytes += rows_scratch(kv, row_slots(kv, batch, tokens, table_width));
   return ok();
 }
 
@@ -317,19 +328,21 @@ ra_status ra_paged_attend(ra_paged_t kv, const void* cache, int64_t batch, int64
   if (s != RA_OK) return s;
   if ((tokens > 1 && prm.qs.token == 0) || (pb.heads_q > 1 && prm.qs.head == 0))
     return fail(RA_ERR_INVALID_ARG, "q: rows lie in one place");
-  const bool chunks = takes_chunks(kv, batch, tokens, table_width);
-  const int slots = chunks ? 0 : row_slots(kv, batch, tokens, table_width);
-  if (slots != 1 && scratch == nullptr)
+  const Route route = route_of(kv, batch, tokens, table_width);
+  const int slots = route.rows ? row_slots(kv, batch, tokens, table_width) : 1;
+  const bool parts = route.chunks || slots > 1;
+  if (parts && scratch == nullptr)
     return fail(RA_ERR_INVALID_ARG, "null scratch (ra_paged_attend_scratch_size bytes are needed)");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const void* t16[] = {cache, q, o, slots != 1 ? scratch : nullptr};
+  const void* t16[] = {cache, q, o, parts ? scratch : nullptr};
   const void* t4[] = {page_table, offset, length, lse};
   s = check_call(kv, batch, tokens, table_width, t16, 4, t4, 4, st);
   if (s != RA_OK) return s;
   prm.t = table_of(kv, cache, batch, tokens, page_table, table_width, offset, length);
-  if (chunks) {
+  if (route.chunks) {
     ra::PagedChunkParams c{};
     c.t = prm.t;
+    c.t.few = route.rows ? ra::kManyOnly : ra::kAllRows;
     c.heads_q = pb.heads_q;
     c.group = pb.heads_q / pb.heads_kv;
     c.window = (int32_t)std::min(pb.window, kMaxPositions);
@@ -351,7 +364,9 @@ ra_status ra_paged_attend(ra_paged_t kv, const void* cache, int64_t batch, int64
     const char* why = "";
     const cudaError_t e = ra::launch_paged_chunk(pb.head_dim, c, grid, st, &why);
     if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache attention: %s (%s)", why, cudaGetErrorString(e));
-    return launched(kv, e, "cache attention", st);
+    if (!route.rows) return launched(kv, e, "cache attention", st);
+    prm.t.few = ra::kFewOnly;
+    scratch += chunk_scratch(kv, shares) / 4;
   }
   prm.heads_q = pb.heads_q;
   prm.group = pb.heads_q / pb.heads_kv;
@@ -363,10 +378,10 @@ ra_status ra_paged_attend(ra_paged_t kv, const void* cache, int64_t batch, int64
   prm.o = o;
   prm.lse = lse;
   if (slots > 1) {
-    const int64_t parts = (int64_t)pb.heads_kv * slots * 2;
+    const int64_t n = (int64_t)pb.heads_kv * slots * 2;
     prm.part_o = scratch;
-    prm.part_ml = reinterpret_cast<float2*>(scratch + parts * ra::kRowsTile * pb.head_dim);
-    prm.joins = reinterpret_cast<int4*>(prm.part_ml + parts * ra::kRowsTile);
+    prm.part_ml = reinterpret_cast<float2*>(scratch + n * ra::kRowsTile * pb.head_dim);
+    prm.joins = reinterpret_cast<int4*>(prm.part_ml + n * ra::kRowsTile);
   }
   return launched(kv, ra::launch_paged_rows(pb.dtype, pb.head_dim, prm, st), "cache attention launch", st);
 }
@@ -375,7 +390,7 @@ ra_status ra_paged_weigh_scratch_size(ra_paged_t kv, int64_t batch, int64_t toke
   if (kv == nullptr || bytes == nullptr) return fail(RA_ERR_INVALID_ARG, "null argument");
   const ra_status s = check_sizes(kv, batch, tokens, table_width);
   if (s != RA_OK) return s;
-  *bytes = takes_chunks(kv, batch, tokens, table_width) ? weigh_scratch(kv, batch, tokens, chunk_grid(kv)) : 0;
+  *bytes = route_of(kv, batch, tokens, table_width).chunks ? weigh_scratch(kv, batch, tokens, chunk_grid(kv)) : 0;
   return ok();
 }
 
@@ -397,18 +412,19 @@ ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_
   if (s != RA_OK) return s;
   if ((tokens > 1 && prm.qs.token == 0) || (pb.heads_q > 1 && prm.qs.head == 0))
     return fail(RA_ERR_INVALID_ARG, "q: rows lie in one place");
-  const bool chunks = takes_chunks(kv, batch, tokens, table_width);
-  if (chunks && scratch == nullptr)
+  const Route route = route_of(kv, batch, tokens, table_width);
+  if (route.chunks && scratch == nullptr)
     return fail(RA_ERR_INVALID_ARG, "null scratch (ra_paged_weigh_scratch_size bytes are needed)");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const void* t16[] = {cache, q, chunks ? scratch : nullptr};
+  const void* t16[] = {cache, q, route.chunks ? scratch : nullptr};
   const void* t4[] = {page_table, offset, length, lse, weight_in, weight};
   s = check_call(kv, batch, tokens, table_width, t16, 3, t4, 6, st);
   if (s != RA_OK) return s;
   prm.t = table_of(kv, cache, batch, tokens, page_table, table_width, offset, length);
-  if (chunks) {
+  if (route.chunks) {
     ra::PagedWeighChunkParams c{};
     c.t = prm.t;
+    c.t.few = route.rows ? ra::kManyOnly : ra::kAllRows;
     c.heads_q = pb.heads_q;
     c.group = pb.heads_q / pb.heads_kv;
     c.window = (int32_t)std::min(pb.window, kMaxPositions);
@@ -431,7 +447,8 @@ ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_
     const char* why = "";
     const cudaError_t e = ra::launch_paged_weigh_chunk(pb.head_dim, c, grid, st, &why);
     if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache weights: %s (%s)", why, cudaGetErrorString(e));
-    return launched(kv, e, "cache weights", st);
+    if (!route.rows) return launched(kv, e, "cache weights", st);
+    prm.t.few = ra::kFewOnly;
   }
   prm.heads_q = pb.heads_q;
   prm.group = pb.heads_q / pb.heads_kv;
@@ -481,7 +498,7 @@ ra_status ra_paged_evict(ra_paged_t kv, void* cache, int64_t batch, const int32_
   prm.recent = (int32_t)recent;
   prm.kept = kept;
   prm.new_length = new_length;
-  return launched(kv, ra::launch_paged_evict(pb.dtype, prm, st), "cache eviction launch", st);
+  return launched(kv, ra::launch_paged_evict(pb.dtype, prm, kv->sm_count, st), "cache eviction launch", st);
 }
 
 ra_status ra_paged_sync_status(ra_paged_t kv, void* stream) {

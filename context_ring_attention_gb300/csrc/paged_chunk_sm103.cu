@@ -131,7 +131,7 @@ __device__ Shares shares_of(const PagedChunkParams& P, int per_item, int64_t* pr
   int64_t again = 0;  // slots that more than one item reads
   paged_sums<kWarps>(P.t.batch, prefix, [&](int b) {
     const PagedSeq q = paged_seq(P.t, b);
-    const int items = (q.count + per_item - 1) / per_item;
+    const int items = paged_mine(P.t, q, P.group) ? (q.count + per_item - 1) / per_item : 0;
     if (items > 1) again += q.length;
     return warp_total(items, [&](int i) { return item_units(P, q, per_item, i); });
   });
@@ -729,45 +729,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- cut items --
-// The item that share x begins and does not end: its first part there, the others at the
-// beginning of the shares up to the last.  A thread has 4 channels of a row, a CTA 8 rows by
-// 32 columns of them at a time.
+// The item that share s begins and does not end: its first part there, the others at the
+// beginning of the shares up to the last.  A thread has 4 channels of a row.
 template <int D>
-__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const PagedChunkParams P) {
-  const PagedJoin rec = P.joins[blockIdx.x];
-  if (rec.tokens == 0) return;
-  const int per_tile = kTile / P.group;
-  const int rows = rec.tokens * P.group;
-  const int count = rec.last - (int)blockIdx.x + 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // A warp has 32 rows of one column group, so that reads are whole lines.
-  for (int id = blockIdx.y * 8 + warp; id < (2 * kTile / 32) * (D / 4); id += gridDim.y * 8) {
-    const int q = id % (D / 4), r = id / (D / 4) * 32 + lane;  // column group; row over both tiles
-    const int g = r >> 7, in_tile = r & 127;
-    const int token = in_tile / P.group;
-    if (token >= per_tile || g * per_tile + token >= rec.tokens || (g * per_tile + token) * P.group >= rows) continue;
-    auto row_of = [&](int i) { return ((i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i)) * 2 + g) * kTile + in_tile; };
-    float m = -INFINITY;
-    for (int i = 0; i < count; ++i) m = fmaxf(m, P.part_ml[row_of(i)].x);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, fix = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const PagedChunkParams P, int shares) {
+  for (int s = (int)blockIdx.x; s < shares; s += (int)gridDim.x) {
+    const PagedJoin rec = P.joins[s];
+    if (rec.tokens == 0) continue;
+    const int per_tile = kTile / P.group;
+    const int count = rec.last - s + 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // A warp has 32 rows of one column group, so that reads are whole lines.
+    for (int id = blockIdx.y * 8 + warp; id < (2 * kTile / 32) * (D / 4); id += gridDim.y * 8) {
+      const int q = id % (D / 4), r = id / (D / 4) * 32 + lane;  // column group; row over both tiles
+      const int g = r >> 7, in_tile = r & 127;
+      const int token = in_tile / P.group;
+      if (token >= per_tile || g * per_tile + token >= rec.tokens) continue;
+      auto row_of = [&](int i) { return ((i == 0 ? 2 * s + 1 : 2 * (s + i)) * 2 + g) * kTile + in_tile; };
+      float m = -INFINITY;
+      for (int i = 0; i < count; ++i) m = fmaxf(m, P.part_ml[row_of(i)].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+      float l = 0.f, fix = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-    for (int i = 0; i < count; ++i) {
-      const int row = row_of(i);
-      const float4 ml = P.part_ml[row];
-      const float f = exp2f(ml.x - ref);
-      const float4 y = reinterpret_cast<const float4*>(P.part_o)[((int64_t)(row >> 7) * (D / 4) + q) * kTile + in_tile];
-      l = fmaf(ml.y, f, l);
-      fix = fmaf(ml.z, f, fix);
-      x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+      for (int i = 0; i < count; ++i) {
+        const int row = row_of(i);
+        const float4 ml = P.part_ml[row];
+        const float f = exp2f(ml.x - ref);
+        const float4 y = reinterpret_cast<const float4*>(P.part_o)[((int64_t)(row >> 7) * (D / 4) + q) * kTile + in_tile];
+        l = fmaf(ml.y, f, l);
+        fix = fmaf(ml.z, f, fix);
+        x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+      }
+      const float inv = l == 0.f ? 0.f : 1.0f / (l + fix);
+      const int at = rec.token + g * per_tile + token, head = rec.head * P.group + in_tile - token * P.group;
+      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.o) + at * P.os.token + head * P.os.head + q * 4);
+      *dst = make_uint2(ptx::pack_bf16x2(x.x * inv, x.y * inv), ptx::pack_bf16x2(x.z * inv, x.w * inv));
+      if (q == 0 && P.lse != nullptr)
+        P.lse[(int64_t)at * P.heads_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
-    const float inv = l == 0.f ? 0.f : 1.0f / (l + fix);
-    const int at = rec.token + g * per_tile + token, head = rec.head * P.group + in_tile - token * P.group;
-    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.o) + at * P.os.token + head * P.os.head + q * 4);
-    *dst = make_uint2(ptx::pack_bf16x2(x.x * inv, x.y * inv), ptx::pack_bf16x2(x.z * inv, x.w * inv));
-    if (q == 0 && P.lse != nullptr)
-      P.lse[(int64_t)at * P.heads_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -788,7 +788,7 @@ cudaError_t launch(const PagedChunkParams& prm, int grid, cudaStream_t stream, c
   paged_chunk_kernel<D><<<grid, kThreads, Smem<D>::kFixed + (prm.t.batch + 1) * 8, stream>>>(tq, tkv, prm);
   e = cudaGetLastError();
   if (e == cudaSuccess) {
-    paged_chunk_join_kernel<D><<<dim3((unsigned)(grid * prm.rounds), 8), 256, 0, stream>>>(prm);
+    paged_chunk_join_kernel<D><<<dim3((unsigned)grid, 8), 256, 0, stream>>>(prm, grid * prm.rounds);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) *why = "launch failed";

@@ -2,14 +2,17 @@
 // and key/value head the `keep` slots that stay are the first ones, the most recent ones, and
 // of the others the heaviest, ties to the lowest slot; they move together in their order.
 //
-// Two kernels.  The first decides: a CTA per head and sequence finds the weight of the last
-// slot that stays by its bits, 11 at a time from the top (a histogram in shared memory of the
-// slots that agree so far), and lists the slots in order with one scan.  Counts are whole
-// numbers: their order does not matter.  The second moves rows: a CTA has 64 bytes of every
-// row of a head's keys or values, so that the list is walked in order by CTAs that do not
-// depend on each other.  A row's new place is never behind its old one; a CTA that has read all
-// rows up to some place may write up to it, also where old and new pages are the same.
-// Bound by HBM: the kept rows are read and written once.
+// Two kernels.  The first decides: a cluster of CTAs per head and sequence (one CTA for short
+// ones) finds the weight of the last slot that stays by its bits, 11 at a time from the top (a
+// histogram in shared memory of the slots that agree so far, summed over the cluster), and lists
+// the slots in order with a scan.  Counts are whole numbers: their order does not matter.
+//
+// The second moves rows, bound by HBM: the kept rows are read and written once.  Into other pages
+// the CTAs take runs of rows.  In place a row's new one is never behind its old one, so that a CTA
+// that has read all rows up to some place may write up to it: a CTA walks the whole list in
+// order, for a piece of every row of a head's keys or values, reading a step ahead.  Where each
+// row lies is looked up for many rows at once, before their turn.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -20,9 +23,12 @@
 namespace ra {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kPickThreads = 1024;
 constexpr int kBins = 2048;       // 11 bits a pass
-constexpr int kMaxKnown = 49152;  // weights that the CTA keeps in shared memory
+constexpr int kMaxKnown = 49152;  // weights that a CTA keeps in shared memory
+constexpr int kMaxCluster = 8;
 
 // Whole numbers in the order of the weights: NaN lowest, then -inf .. +inf, -0 as +0.
 __device__ __forceinline__ uint32_t rank_of(float w) {
@@ -58,36 +64,43 @@ __device__ __forceinline__ uint64_t scan(uint64_t x, uint64_t* sums, uint64_t& t
 }
 
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictParams P, int known) {
-  extern __shared__ uint32_t ranks[];  // [known]
+  extern __shared__ __align__(16) float weights[];  // [known]
   __shared__ uint32_t bins[kBins];
   __shared__ uint64_t sums[32];
   __shared__ uint32_t found[2];
-  const int head = (int)blockIdx.x, b = (int)blockIdx.y, tid = threadIdx.x;
+  __shared__ uint64_t own_count;  // of this CTA's slots: sure << 32 | ties
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int head = (int)blockIdx.x / ctas, b = (int)blockIdx.y, tid = threadIdx.x;
   int n = paged_seq(P.t, b).length;
   if (n > P.weight_width || min(n, P.keep) > P.new_width * P.t.page_rows) {
     if (tid == 0) atomicOr(P.t.status, kPagedStatusRange);
     n = 0;
   }
-  const int m = min(n, P.keep);
-  if (head == 0 && tid == 0) P.new_length[b] = m;
+  const int m = min(n, P.keep), all = ctas * kPickThreads, me = rank * kPickThreads + tid;
+  if (head == 0 && me == 0) P.new_length[b] = m;
   const int64_t row = (int64_t)b * P.t.heads_kv + head;
   const float* w = P.weight_in + row * P.weight_width;
   float* out = P.weight != nullptr ? P.weight + row * P.weight_width : nullptr;
   int32_t* kept = P.kept + row * P.keep;
-  for (int64_t j = m + tid; j < P.keep; j += kPickThreads) kept[j] = -1;
+  for (int64_t j = m + me; j < P.keep; j += all) kept[j] = -1;
   if (n <= P.keep) {
-    for (int j = tid; j < n; j += kPickThreads) {
+    for (int j = me; j < n; j += all) {
       kept[j] = j;
       if (out != nullptr && out != w) out[j] = w[j];
     }
     return;
   }
+  // This CTA's slots [s0, s1), their weights in shared memory where they fit.  (In place a weight
+  // may be written over before another CTA has read it: then one CTA takes all, in order.)
+  int s0 = (int)((int64_t)n * rank / ctas) & ~3, s1 = rank + 1 == ctas ? n : (int)((int64_t)n * (rank + 1) / ctas) & ~3;
+  const bool in_smem = (n + ctas - 1) / ctas + 4 <= known;
+  if (!in_smem && out == w) s0 = rank == 0 ? 0 : n, s1 = n;
+  if (in_smem)
+    for (int j = s0 + tid; j < s1; j += kPickThreads) weights[j - s0] = w[j];
+  auto weight_at = [&](int j) { return in_smem ? weights[j - s0] : w[j]; };
   // The slots [lo, hi) compete for `places`.
   const int lo = P.first, hi = n - P.recent, places = P.keep - P.first - P.recent;
-  const bool in_smem = n <= known;
-  if (in_smem)
-    for (int j = tid; j < n; j += kPickThreads) ranks[j] = rank_of(w[j]);
-  auto rank_at = [&](int j) { return in_smem ? ranks[j] : rank_of(w[j]); };
 
   // The lowest rank that stays, and how many slots of that very rank do.
   uint32_t prefix = 0u, left = (uint32_t)places;
@@ -97,14 +110,18 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictPara
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
       for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0u;
       __syncthreads();
-      for (int j = lo + tid; j < hi; j += kPickThreads) {
-        const uint32_t r = rank_at(j);
+      for (int j = max(s0, lo) + tid; j < min(s1, hi); j += kPickThreads) {
+        const uint32_t r = rank_of(weight_at(j));
         if (pass == 0 || (r >> (shift + width)) == prefix) atomicAdd(&bins[(r >> shift) & ((1u << width) - 1u)], 1u);
       }
-      __syncthreads();
+      cluster.sync();
       // From the highest bin down: the one in which `left` slots are reached.
       const int top = kBins - 1 - 2 * tid;
-      const uint32_t a = bins[top], c = bins[top - 1];
+      uint32_t a = 0u, c = 0u;
+      for (int i = 0; i < ctas; ++i) {
+        const uint32_t* other = cluster.map_shared_rank(bins, i);
+        a += other[top], c += other[top - 1];
+      }
       uint64_t total;
       const uint64_t sum = scan((uint64_t)a + c, sums, total);
       const uint64_t before = sum - a - c;
@@ -113,108 +130,147 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictPara
         found[0] = (uint32_t)(second ? top - 1 : top);
         found[1] = (uint32_t)(left - before - (second ? a : 0u));
       }
-      __syncthreads();
+      cluster.sync();  // (nobody reads these bins any more)
       prefix = (prefix << width) | found[0];
       left = found[1];
-      __syncthreads();
     }
   }
-  // In order: slots that stay for certain, and of those of the lowest rank the first `left`.
-  uint32_t sure_before = 0u, ties_before = 0u;
-  for (int64_t j0 = 0; j0 < n; j0 += kPickThreads) {
-    const int64_t j = j0 + tid;
-    bool sure = false, tie = false;
-    float wj = 0.f;
-    if (j < n) {
-      if (out != nullptr) wj = w[j];
-      if (j < lo || j >= hi) {
-        sure = true;
-      } else if (places > 0) {
-        const uint32_t r = rank_at((int)j);
-        sure = r > prefix;
-        tie = r == prefix;
+  // Slots that stay for certain, and those of the lowest rank, of which the first `left` do.
+  auto kinds = [&](int j, bool& sure, bool& tie) {
+    sure = tie = false;
+    if (j >= s1) return;
+    if (j < lo || j >= hi) {
+      sure = true;
+    } else if (places > 0) {
+      const uint32_t r = rank_of(weight_at(j));
+      sure = r > prefix;
+      tie = r == prefix;
+    }
+  };
+  uint64_t before = 0;
+  if (ctas > 1) {  // those of the CTAs before this one
+    uint64_t mine = 0, total;
+    for (int j = s0 + tid; j < s1; j += kPickThreads) {
+      bool sure, tie;
+      kinds(j, sure, tie);
+      mine += ((uint64_t)sure << 32) | (uint64_t)tie;
+    }
+    scan(mine, sums, total);
+    if (tid == 0) own_count = total;
+    cluster.sync();
+    for (int i = 0; i < rank; ++i) before += *cluster.map_shared_rank(&own_count, i);
+    cluster.sync();  // (no CTA leaves while another reads its count)
+  } else {
+    __syncthreads();
+  }
+  constexpr int kOwn = 4;  // slots of a thread at a time
+  for (int64_t j0 = s0; j0 < s1; j0 += kOwn * kPickThreads) {
+    bool sure[kOwn], tie[kOwn];
+    float wj[kOwn];
+    uint64_t mine = 0, total;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      const int64_t j = j0 + tid * kOwn + e;
+      kinds((int)min(j, (int64_t)s1), sure[e], tie[e]);
+      mine += ((uint64_t)sure[e] << 32) | (uint64_t)tie[e];
+      wj[e] = out != nullptr && j < s1 ? weight_at((int)j) : 0.f;
+    }
+    // (ends with barriers: the step's weights are read before any is written)
+    const uint64_t sum = before + scan(mine, sums, total) - mine;
+    uint32_t s = (uint32_t)(sum >> 32), t = (uint32_t)sum;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      if (sure[e] || (tie[e] && t < left)) {
+        const uint32_t to = s + min(t, left);
+        RA_BOUNDS(P.t.status, to < (uint32_t)P.keep, 118);
+        kept[to] = (int32_t)(j0 + tid * kOwn + e);
+        if (out != nullptr) out[to] = wj[e];
       }
+      s += sure[e], t += tie[e];
     }
-    uint64_t total;  // (ends with barriers: the chunk's weights are read before any is written)
-    const uint64_t sum = scan(((uint64_t)sure << 32) | (uint64_t)tie, sums, total);
-    const uint32_t s = sure_before + (uint32_t)(sum >> 32) - (sure ? 1u : 0u);
-    const uint32_t t = ties_before + (uint32_t)sum - (tie ? 1u : 0u);
-    if (sure || (tie && t < left)) {
-      const uint32_t to = s + min(t, left);
-      RA_BOUNDS(P.t.status, to < (uint32_t)P.keep, 118);
-      kept[to] = (int32_t)j;
-      if (out != nullptr) out[to] = wj;
-    }
-    sure_before += (uint32_t)(total >> 32);
-    ties_before += (uint32_t)total;
+    before += total;
   }
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kPiece = 64;                        // bytes of a row that a CTA moves
-constexpr int kPassRows = kMoveThreads / (kPiece / 16);
-constexpr int kUnroll = 4;                        // rows of a thread under way, twice
+constexpr int kUnroll = 8;      // rows of a thread under way, twice
+constexpr int kBlock = 2048;    // rows whose places are looked up at a time: four steps or more
 
-struct MoveRow {
-  int64_t from, to;  // byte offsets; from < 0: nothing
-};
-__device__ __forceinline__ MoveRow move_row(const PagedEvictParams& P, int row_bytes, int b, int head, int which,
-                                            const int32_t* kept, int m, int j) {
-  if (j >= m) return {-1, 0};
-  const int s = __ldg(kept + j);
-  const int pr = P.t.page_rows;
-  const int from_page = paged_page(P.t, b, s / pr);
-  const int to_page = __ldg(P.new_table + b * P.new_width + j / pr);
-  if (to_page < 0 || to_page >= P.t.pages) {
-    atomicOr(P.t.status, kPagedStatusRange);
-    return {-1, 0};
-  }
-  if (from_page < 0) return {-1, 0};
-  const int64_t from = paged_row(P.t, from_page, which, head, s % pr), to = paged_row(P.t, to_page, which, head, j % pr);
-  if (from == to) return {-1, 0};
-  RA_BOUNDS(P.t.status, s >= j && from >= 0 && to >= 0, 119);
-  return {from * row_bytes, to * row_bytes};
-}
+static_assert(kBlock >= 4 * (kMoveThreads / 4) * kUnroll, "a step's places are written two barriers before they are read");
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedEvictParams P, int row_bytes) {
-  const int pieces = row_bytes / kPiece;
-  const int which = (int)blockIdx.x / pieces, piece = (int)blockIdx.x % pieces;
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedEvictParams P, int row_bytes, int pieces, int runs) {
+  __shared__ int2 places[2][kBlock];  // rows of the cache: from, to (from < 0: nothing to move)
+  const int piece_bytes = row_bytes / pieces, lanes = piece_bytes / 16, pass = kMoveThreads / lanes;
+  const int run = (int)blockIdx.x % runs, part = (int)blockIdx.x / runs;
+  const int which = part / pieces, piece = part % pieces;
   const int head = (int)blockIdx.y, b = (int)blockIdx.z;
   const int m = __ldg(P.new_length + b);
+  if (m == 0) return;
+  // The pages are the same, or none of them is: the first entry tells.
+  const bool in_place = __ldg(P.new_table + b * P.new_width) == __ldg(P.t.page_table + b * P.t.width);
+  if (in_place && run > 0) return;
+  const int r0 = in_place ? 0 : (int)((int64_t)m * run / runs), r1 = in_place ? m : (int)((int64_t)m * (run + 1) / runs);
   const int32_t* kept = P.kept + ((int64_t)b * P.t.heads_kv + head) * P.keep;
-  uint8_t* cache = static_cast<uint8_t*>(P.t.cache) + piece * kPiece + (threadIdx.x & 3) * 16;
-  const int r0 = threadIdx.x >> 2;
-  constexpr int kStep = kPassRows * kUnroll;
-  uint4 x[2][kUnroll];
-  int64_t to[2][kUnroll];
-  auto load = [&](int j0, uint4 (&v)[kUnroll], int64_t (&t)[kUnroll]) {
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const MoveRow r = move_row(P, row_bytes, b, head, which, kept, m, j0 + i * kPassRows + r0);
-      t[i] = r.from < 0 ? -1 : r.to;
-      if (r.from >= 0) v[i] = __ldcg(reinterpret_cast<const uint4*>(cache + r.from));
+  const int pr = P.t.page_rows;
+  auto look_up = [&](int block) {
+    for (int i = threadIdx.x; i < kBlock; i += kMoveThreads) {
+      const int j = r0 + block * kBlock + i;
+      int2 at = make_int2(-1, 0);
+      if (j < r1) {
+        const int s = __ldg(kept + j);
+        const int from_page = paged_page(P.t, b, s / pr), to_page = __ldg(P.new_table + b * P.new_width + j / pr);
+        if (to_page < 0 || to_page >= P.t.pages) {
+          atomicOr(P.t.status, kPagedStatusRange);
+        } else if (from_page >= 0) {
+          at = make_int2((int)paged_row(P.t, from_page, which, head, s % pr), (int)paged_row(P.t, to_page, which, head, j % pr));
+          if (at.x == at.y) at.x = -1;
+          RA_BOUNDS(P.t.status, s >= j && at.y >= 0, 119);
+        }
+      }
+      places[block & 1][i] = at;
     }
   };
-  auto store = [&](const uint4 (&v)[kUnroll], const int64_t (&t)[kUnroll]) {
+  uint8_t* cache = static_cast<uint8_t*>(P.t.cache) + piece * piece_bytes + (threadIdx.x % lanes) * 16;
+  const int sub = threadIdx.x / lanes, step = pass * kUnroll;
+  const int steps = (r1 - r0 + step - 1) / step, per_block = kBlock / step;
+  uint4 x[2][kUnroll];
+  auto place = [&](int s, int i) { return places[(s / per_block) & 1][s % per_block * step + i * pass + sub]; };
+  auto load = [&](int s, uint4 (&v)[kUnroll]) {
+    if (s >= steps) return;
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i)
-      if (t[i] >= 0) *reinterpret_cast<uint4*>(cache + t[i]) = v[i];
+    for (int i = 0; i < kUnroll; ++i) {
+      const int from = place(s, i).x;
+      if (from >= 0) v[i] = __ldcg(reinterpret_cast<const uint4*>(cache + (int64_t)from * row_bytes));
+    }
   };
-  load(0, x[0], to[0]);
-  for (int j0 = 0; j0 < m; j0 += 2 * kStep) {
-    load(j0 + kStep, x[1], to[1]);
-    __syncthreads();  // all rows up to here are read: their places may be written
-    store(x[0], to[0]);
-    load(j0 + 2 * kStep, x[0], to[0]);
+  auto store = [&](int s, const uint4 (&v)[kUnroll]) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int2 at = place(s, i);
+      if (at.x >= 0) *reinterpret_cast<uint4*>(cache + (int64_t)at.y * row_bytes) = v[i];
+    }
+  };
+  // Step s is stored once step s + 1 is read and all threads have read step s.
+  auto turn = [&](int s, const uint4 (&now)[kUnroll], uint4 (&next)[kUnroll]) {
+    load(s + 1, next);
     __syncthreads();
-    store(x[1], to[1]);
+    store(s, now);
+    // (all threads have stored the block before this one; the next one is read two barriers on)
+    if (s % per_block == 0) look_up(s / per_block + 1);
+  };
+  look_up(0);
+  __syncthreads();
+  load(0, x[0]);
+  for (int s = 0; s < steps; s += 2) {
+    turn(s, x[0], x[1]);
+    if (s + 1 < steps) turn(s + 1, x[1], x[0]);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, cudaStream_t stream) {
-  const int known = (int)std::min<int64_t>(prm.weight_width, kMaxKnown);
+cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, int sm_count, cudaStream_t stream) {
+  const int known = (int)std::min<int64_t>(prm.weight_width + 4, kMaxKnown);
   static std::atomic<int> ready[kMaxDevices];
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -225,13 +281,32 @@ cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, cudaStrea
     if (e != cudaSuccess) return e;
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
-  const dim3 grid((unsigned)prm.t.heads_kv, (unsigned)prm.t.batch);
-  pick_kernel<<<grid, kPickThreads, known * 4, stream>>>(prm, known);
-  e = cudaGetLastError();
+  // A cluster where a sequence may be long and the heads are few (they are one wave then).
+  const int64_t heads = (int64_t)prm.t.heads_kv * prm.t.batch;
+  int ctas = 1;
+  while (ctas < kMaxCluster && prm.weight_width > 4096 * ctas && 2 * ctas * heads <= sm_count) ctas *= 2;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3((unsigned)(prm.t.heads_kv * ctas), (unsigned)prm.t.batch);
+  config.blockDim = dim3(kPickThreads);
+  config.dynamicSmemBytes = (size_t)std::min<int64_t>(known, prm.weight_width / ctas + 8) * 4;
+  config.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  e = cudaLaunchKernelEx(&config, pick_kernel, prm, (int)(config.dynamicSmemBytes / 4));
   if (e != cudaSuccess) return e;
   const int row_bytes = prm.d * (dtype == RA_DTYPE_BF16 ? 2 : 4);
-  const dim3 moves((unsigned)(2 * row_bytes / kPiece), (unsigned)prm.t.heads_kv, (unsigned)prm.t.batch);
-  move_kernel<<<moves, kMoveThreads, 0, stream>>>(prm, row_bytes);
+  // Pieces of 64 bytes at least, as many as fill the GPU twice (in place they are all there is);
+  // runs of rows until it is filled eight times.
+  int pieces = 1;
+  while (row_bytes / pieces > 64 && 2 * pieces * heads < 2 * sm_count) pieces *= 2;
+  const int64_t most = (prm.keep + 255) / 256;
+  const int runs = (int)std::max<int64_t>(1, std::min(most, (int64_t)sm_count * 8 / (2 * pieces * heads)));
+  const dim3 moves((unsigned)(2 * pieces * runs), (unsigned)prm.t.heads_kv, (unsigned)prm.t.batch);
+  move_kernel<<<moves, kMoveThreads, 0, stream>>>(prm, row_bytes, pieces, runs);
   return cudaGetLastError();
 }
 

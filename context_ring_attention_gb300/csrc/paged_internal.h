@@ -23,7 +23,10 @@ struct PagedTable {
   int64_t width;
   int32_t pages, page_rows, batch, heads_kv, tokens;
   uint32_t* status;
+  int32_t few;  // sequences of a launch: kAllRows, or those with up to / more than kFewRows query rows a head
 };
+enum : int32_t { kAllRows = 0, kFewOnly = 1, kManyOnly = 2 };
+constexpr int kFewRows = 16;
 
 struct PagedStrides {  // elements
   int64_t token, head;
@@ -133,7 +136,7 @@ cudaError_t launch_paged_weigh_rows(int dtype, int head_dim, const PagedWeighPar
                                     cudaStream_t stream);
 cudaError_t launch_paged_weigh_chunk(int head_dim, const PagedWeighChunkParams& prm, int grid, cudaStream_t stream,
                                      const char** why);
-cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, cudaStream_t stream);
+cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, int sm_count, cudaStream_t stream);
 
 constexpr int kMaxChunkSequences = 2048;  // of a call of the chunk kernels (shared memory)
 constexpr int kMaxRounds = 8;
@@ -164,6 +167,11 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedTable& t, int b) {
     return {0, 0, 0};
   }
   return {a, e - a, n};
+}
+
+// Whether a launch takes a sequence.
+__device__ __forceinline__ bool paged_mine(const PagedTable& t, const PagedSeq& q, int group) {
+  return t.few == kAllRows || (q.count * group <= kFewRows) == (t.few == kFewOnly);
 }
 
 // Page of a sequence's entry; -1, and a report, where the table names none.

@@ -35,7 +35,7 @@ __device__ void paged_prefix(const PagedTable& t, int group, int window, int sin
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int b = warp; b < t.batch; b += kWarps) {
     const PagedSeq q = paged_seq(t, b);
-    const int tiles = (q.count * group + kR - 1) / kR;
+    const int tiles = paged_mine(t, q, group) ? (q.count * group + kR - 1) / kR : 0;
     int64_t sum = 0;
     for (int i = lane; i < tiles; i += 32) sum += paged_units<kR, kB>(q, group, window, sinks, i);
 #pragma unroll

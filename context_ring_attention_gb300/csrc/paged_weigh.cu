@@ -52,12 +52,16 @@ __device__ __forceinline__ void copies_wait() {
 
 // Sums of the sequences' blocks of kB slots (as paged_prefix, of lengths).
 template <int kB>
-__device__ void slot_prefix(const PagedTable& t, int64_t* prefix) {
+__device__ void slot_prefix(const PagedTable& t, int group, int64_t* prefix) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
     int64_t before = 0;
     for (int b0 = 0; b0 < t.batch; b0 += 32) {
-      int64_t x = b0 + lane < t.batch ? (paged_seq(t, b0 + lane).length + kB - 1) / kB : 0;
+      int64_t x = 0;
+      if (b0 + lane < t.batch) {
+        const PagedSeq q = paged_seq(t, b0 + lane);
+        if (paged_mine(t, q, group)) x = (q.length + kB - 1) / kB;
+      }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -110,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
   extern __shared__ __align__(128) uint8_t smem_bytes[];
   uint8_t* smem = smem_bytes;
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + kWarps * kStages * kStageBytes);
-  slot_prefix<kRowsBlock>(P.t, prefix);
+  slot_prefix<kRowsBlock>(P.t, P.group, prefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
   const int quad = lane >> 2, two = (lane & 3) * 2;
   const __nv_bfloat16* cache = static_cast<const __nv_bfloat16*>(P.t.cache);
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
 template <int D>
 __global__ void __launch_bounds__(kThreads) weigh_f32_kernel(const PagedWeighParams P) {
   extern __shared__ int64_t prefix[];
-  slot_prefix<kChunk>(P.t, prefix);
+  slot_prefix<kChunk>(P.t, P.group, prefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
   const int64_t chunks = prefix[P.t.batch];
   const float* cache = static_cast<const float*>(P.t.cache);

@@ -138,7 +138,8 @@ __device__ void copy_unseen(const PagedWeighChunkParams& P) {
     int lo = 0, hi = 0;
     if (b0 + lane < P.t.batch) {
       const PagedSeq q = paged_seq(P.t, b0 + lane);
-      if (q.count == 0) hi = q.length;
+      if (!paged_mine(P.t, q, P.group)) hi = 0;
+      else if (q.count == 0) hi = q.length;
       else if (P.window > 0) lo = P.sinks, hi = q.slot0() - P.window + 1;
       if (hi > P.weight_width) {
         atomicOr(P.t.status, kPagedStatusRange);
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   copy_unseen(P);
   paged_sums<kWarps>(P.t.batch, prefix, [&](int b) {
     const PagedSeq q = paged_seq(P.t, b);
-    return warp_total((q.length + kPair - 1) / kPair, [&](int i) { return tiles_of(P, q, per_tile, i).n; });
+    return warp_total(paged_mine(P.t, q, P.group) ? (q.length + kPair - 1) / kPair : 0, [&](int i) { return tiles_of(P, q, per_tile, i).n; });
   });
   Shares sh;
   sh.per_head = prefix[P.t.batch];
@@ -590,7 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(kTile) paged_weigh_extra_kernel(const PagedWeighChunkParams P) {
   extern __shared__ int64_t prefix[];
   const int per_tile = kTile / P.group;
-  paged_sums<kTile / 32>(P.t.batch, prefix, [&](int b) { return (int64_t)((paged_seq(P.t, b).count + per_tile - 1) / per_tile); });
+  paged_sums<kTile / 32>(P.t.batch, prefix, [&](int b) {
+    const PagedSeq q = paged_seq(P.t, b);
+    return paged_mine(P.t, q, P.group) ? (int64_t)((q.count + per_tile - 1) / per_tile) : 0;
+  });
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int b = threadIdx.x; b < P.t.batch; b += kTile) P.extra_at[b] = (int32_t)min(prefix[b], (int64_t)P.tiles - 1);
   const int head = (int)blockIdx.y, row = threadIdx.x, tok = row / P.group;

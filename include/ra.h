@@ -807,8 +807,9 @@ ra_status ra_paged_weigh_scratch_size(ra_paged_t kv, int64_t batch, int64_t toke
  * length: [batch] int32.  weight_in: [batch, Hkv, weight_width] float32, weight (may be weight_in
  * or NULL) receives the weights of the slots that stay; other entries stay as they were.
  * new_table: [batch, new_width] int32, the pages that the sequences have afterwards: page_table
- * itself (in place), an array with the same entries, or pages that no sequence of the call has
- * (the old pages then keep what they hold, for others that share them).
+ * itself (in place; no page of it may be another sequence's), an array with the same entries, or
+ * pages that no sequence of the call has (the old pages then keep what they hold, for others that
+ * share them).
  * kept: [batch, Hkv, keep] int32, -1 behind the last; new_length: [batch] int32 (not length).
  * A sequence whose length is beyond the page table or weight_width, or whose slots do not fit in
  * new_width pages, is left as it is, with new_length 0, and reported.
