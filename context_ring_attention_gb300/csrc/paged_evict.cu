@@ -28,7 +28,7 @@ namespace cg = cooperative_groups;
 constexpr int kPickThreads = 1024;
 constexpr int kBins = 2048;       // 11 bits a pass
 constexpr int kMaxKnown = 49152;  // weights that a CTA keeps in shared memory
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 4;
 
 // Whole numbers in the order of the weights: NaN lowest, then -inf .. +inf, -0 as +0.
 __device__ __forceinline__ uint32_t rank_of(float w) {
@@ -193,22 +193,30 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictPara
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kUnroll = 8;      // rows of a thread under way, twice
+constexpr int kUnroll = 4;      // rows of a thread under way, twice
 constexpr int kBlock = 2048;    // rows whose places are looked up at a time: four steps or more
 
 static_assert(kBlock >= 4 * (kMoveThreads / 4) * kUnroll, "a step's places are written two barriers before they are read");
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedEvictParams P, int row_bytes, int pieces, int runs) {
   __shared__ int2 places[2][kBlock];  // rows of the cache: from, to (from < 0: nothing to move)
-  const int piece_bytes = row_bytes / pieces, lanes = piece_bytes / 16, pass = kMoveThreads / lanes;
-  const int run = (int)blockIdx.x % runs, part = (int)blockIdx.x / runs;
-  const int which = part / pieces, piece = part % pieces;
   const int head = (int)blockIdx.y, b = (int)blockIdx.z;
   const int m = __ldg(P.new_length + b);
   if (m == 0) return;
   // The pages are the same, or none of them is: the first entry tells.
   const bool in_place = __ldg(P.new_table + b * P.new_width) == __ldg(P.t.page_table + b * P.t.width);
-  if (in_place && run > 0) return;
+  // In place: CTA 2 * piece + which has a piece of every row.  Else: CTA 2 * run + which a run of rows.
+  const int which = (int)blockIdx.x & 1;
+  int piece = 0, run = (int)blockIdx.x >> 1;
+  if (in_place) {
+    if (run >= pieces) return;
+    piece = run;
+    run = 0;
+  } else {
+    runs *= pieces;
+    pieces = 1;
+  }
+  const int piece_bytes = row_bytes / pieces, lanes = piece_bytes / 16, pass = kMoveThreads / lanes;
   const int r0 = in_place ? 0 : (int)((int64_t)m * run / runs), r1 = in_place ? m : (int)((int64_t)m * (run + 1) / runs);
   const int32_t* kept = P.kept + ((int64_t)b * P.t.heads_kv + head) * P.keep;
   const int pr = P.t.page_rows;
@@ -300,11 +308,12 @@ cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, int sm_co
   if (e != cudaSuccess) return e;
   const int row_bytes = prm.d * (dtype == RA_DTYPE_BF16 ? 2 : 4);
   // Pieces of 64 bytes at least, as many as fill the GPU twice (in place they are all there is);
-  // runs of rows until it is filled eight times.
+  // runs of rows until there are six CTAs an SM (two to sixteen are within 4%; below 128 rows a
+  // run is too short for its start).
   int pieces = 1;
   while (row_bytes / pieces > 64 && 2 * pieces * heads < 2 * sm_count) pieces *= 2;
-  const int64_t most = (prm.keep + 255) / 256;
-  const int runs = (int)std::max<int64_t>(1, std::min(most, (int64_t)sm_count * 8 / (2 * pieces * heads)));
+  const int64_t most = (prm.keep + 127) / 128;
+  const int runs = (int)std::max<int64_t>(1, std::min(most, (int64_t)sm_count * 6 / (2 * pieces * heads)));
   const dim3 moves((unsigned)(2 * pieces * runs), (unsigned)prm.t.heads_kv, (unsigned)prm.t.batch);
   move_kernel<<<moves, kMoveThreads, 0, stream>>>(prm, row_bytes, pieces, runs);
   return cudaGetLastError();
