@@ -134,7 +134,7 @@ int row_slots(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width
   int64_t blocks = width * pb.page_rows / ra::kRowsBlock;
   if (pb.window > 0 && pb.window < kMaxPositions && pb.sinks < kMaxPositions)
     blocks = std::min(blocks, (pb.window + ra::kRowsTile + pb.sinks) / ra::kRowsBlock + 3);
-  const int64_t shares = tiles * blocks / 16;  // (tiles below 2^30, blocks up to 2^26)
+  const int64_t shares = tiles * blocks / (pb.dtype == RA_DTYPE_BF16 ? 16 : 4);  // as the kernels cut them (tiles below 2^30, blocks up to 2^26)
   const int64_t sms = kv->sm_count > 0 ? kv->sm_count : 148;
   return (int)std::max<int64_t>(1, std::min({shares, 2 * sms / pb.heads_kv, (int64_t)kMaxSlots}));
 }

@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* prefix = reinterpret_cast<int64_t*>(sgen + S::kOffPrefix);
   const int per_tile = kTile / P.group;
 
+  next_may_come();
   // Shares that cut no item leave nothing to join.
   for (int s = (int)blockIdx.x + threadIdx.x * gridDim.x; s < P.rounds * (int)gridDim.x; s += kThreads * gridDim.x)
     P.joins[s] = {0, 0, 0, 0};
@@ -733,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // beginning of the shares up to the last.  A thread has 4 channels of a row.
 template <int D>
 __global__ void __launch_bounds__(256) paged_chunk_join_kernel(const PagedChunkParams P, int shares) {
+  after_previous();
   for (int s = (int)blockIdx.x; s < shares; s += (int)gridDim.x) {
     const PagedJoin rec = P.joins[s];
     if (rec.tokens == 0) continue;
@@ -787,10 +789,8 @@ cudaError_t launch(const PagedChunkParams& prm, int grid, cudaStream_t stream, c
   if (e != cudaSuccess) return e;
   paged_chunk_kernel<D><<<grid, kThreads, Smem<D>::kFixed + (prm.t.batch + 1) * 8, stream>>>(tq, tkv, prm);
   e = cudaGetLastError();
-  if (e == cudaSuccess) {
-    paged_chunk_join_kernel<D><<<dim3((unsigned)grid, 8), 256, 0, stream>>>(prm, grid * prm.rounds);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess)
+    e = launch_behind(paged_chunk_join_kernel<D>, dim3((unsigned)grid, 8), 256, 0, stream, prm, grid * (int)prm.rounds);
   if (e != cudaSuccess) *why = "launch failed";
   return e;
 }

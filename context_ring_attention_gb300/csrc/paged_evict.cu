@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictPara
   __shared__ uint64_t sums[32];
   __shared__ uint32_t found[2];
   __shared__ uint64_t own_count;  // of this CTA's slots: sure << 32 | ties
+  next_may_come();
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int head = (int)blockIdx.x / ctas, b = (int)blockIdx.y, tid = threadIdx.x;
@@ -201,7 +202,8 @@ static_assert(kBlock >= 4 * (kMoveThreads / 4) * kUnroll, "a step's places are w
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedEvictParams P, int row_bytes, int pieces, int runs) {
   __shared__ int2 places[2][kBlock];  // rows of the cache: from, to (from < 0: nothing to move)
   const int head = (int)blockIdx.y, b = (int)blockIdx.z;
-  const int m = __ldg(P.new_length + b);
+  after_previous();
+  const int m = P.new_length[b];
   if (m == 0) return;
   // The pages are the same, or none of them is: the first entry tells.
   const bool in_place = __ldg(P.new_table + b * P.new_width) == __ldg(P.t.page_table + b * P.t.width);
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedEvictPara
       const int j = r0 + block * kBlock + i;
       int2 at = make_int2(-1, 0);
       if (j < r1) {
-        const int s = __ldg(kept + j);
+        const int s = kept[j];
         const int from_page = paged_page(P.t, b, s / pr), to_page = __ldg(P.new_table + b * P.new_width + j / pr);
         if (to_page < 0 || to_page >= P.t.pages) {
           atomicOr(P.t.status, kPagedStatusRange);
@@ -315,8 +317,7 @@ cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, int sm_co
   const int64_t most = (prm.keep + 127) / 128;
   const int runs = (int)std::max<int64_t>(1, std::min(most, (int64_t)sm_count * 6 / (2 * pieces * heads)));
   const dim3 moves((unsigned)(2 * pieces * runs), (unsigned)prm.t.heads_kv, (unsigned)prm.t.batch);
-  move_kernel<<<moves, kMoveThreads, 0, stream>>>(prm, row_bytes, pieces, runs);
-  return cudaGetLastError();
+  return launch_behind(move_kernel, moves, kMoveThreads, 0, stream, prm, row_bytes, pieces, runs);
 }
 
 }  // namespace ra

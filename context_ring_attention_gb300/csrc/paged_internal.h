@@ -152,6 +152,26 @@ constexpr int kRowsTile = 16;   // query rows of an item of the row kernels
 constexpr int kRowsBlock = 16;  // keys of a block
 
 #ifdef __CUDACC__
+// A kernel of a call behind another one's: its CTAs come to the SMs while the other kernel ends,
+// and wait there (after_previous) until all of it is done and can be read.  The other kernel lets
+// them come by next_may_come.
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = dim3((unsigned)threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, args...);
+}
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_may_come() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A sequence of the batch.  Offsets that do not rise within 0..tokens, or a length that is
 // negative, smaller than the new tokens' count or beyond the page table: reported, and the
 // sequence has no tokens and no keys.

@@ -27,7 +27,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;   // blocks of a warp's ring
-constexpr int kMinUnits = 16;  // of a share: four blocks a warp
+// Blocks of a share at least: bf16 four a warp; float32, whose 32 keys at a time take 3 us, two
+// times that (3 sequences of 300 tokens: 41 us with 16 blocks).
+template <typename T>
+constexpr int kMinUnits = sizeof(T) == 2 ? 16 : 4;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -63,9 +66,10 @@ struct Walk {
   PagedSeq seq;
 };
 // Where this CTA's share begins; false where it has none.
+template <typename T>
 __device__ __forceinline__ bool walk_begin(const PagedAttendParams& P, const int64_t* prefix, Walk& w) {
   w.all = prefix[P.t.batch];
-  w.slots = (int)max((int64_t)1, min((int64_t)P.slots, w.all / kMinUnits));
+  w.slots = (int)max((int64_t)1, min((int64_t)P.slots, w.all / kMinUnits<T>));
   const int c = (int)blockIdx.x;
   if (w.all == 0 || c >= w.slots) return false;
   w.x = w.all * c / w.slots;
@@ -121,10 +125,11 @@ __global__ void __launch_bounds__(kThreads) rows_bf16_kernel(const PagedAttendPa
   extern __shared__ __align__(128) uint8_t smem[];
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + G::kRing);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
+  next_may_come();
   if (P.joins != nullptr && threadIdx.x == 0) P.joins[(int64_t)head * P.slots + blockIdx.x] = make_int4(0, 0, 0, 0);
   paged_prefix<kRowsTile, kRowsBlock, kWarps>(P.t, P.group, P.window, P.sinks, prefix);
   Walk w;
-  if (!walk_begin(P, prefix, w)) return;
+  if (!walk_begin<__nv_bfloat16>(P, prefix, w)) return;
 
   const uint32_t ring = ptx::smem_addr(smem) + warp * kStages * 2 * G::kBlockBytes;
   const __nv_bfloat16* cache = static_cast<const __nv_bfloat16*>(P.t.cache);
@@ -341,10 +346,11 @@ __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendPar
   float* qs = reinterpret_cast<float*>(smem + 2 * G::kStage);
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + G::kBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
+  next_may_come();
   if (P.joins != nullptr && threadIdx.x == 0) P.joins[(int64_t)head * P.slots + blockIdx.x] = make_int4(0, 0, 0, 0);
   paged_prefix<kRowsTile, kRowsBlock, kWarps>(P.t, P.group, P.window, P.sinks, prefix);
   Walk w;
-  if (!walk_begin(P, prefix, w)) return;
+  if (!walk_begin<float>(P, prefix, w)) return;
   const float* cache = static_cast<const float*>(P.t.cache);
   constexpr int kPer = kRowsTile / kWarps, kCh = D / 32;
 
@@ -483,6 +489,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kRowsTile * D / 4) rows_join_kernel(const PagedAttendParams P) {
   const int head = (int)blockIdx.y;
   const int64_t me = (int64_t)head * P.slots + blockIdx.x;
+  after_previous();
   const int4 rec = P.joins[me];
   const int r = threadIdx.x / (D / 4), ch = threadIdx.x % (D / 4);
   if (r >= rec.y) return;
@@ -546,8 +553,7 @@ cudaError_t launch(const PagedAttendParams& prm, cudaStream_t stream) {
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || prm.slots == 1) return e;
-  rows_join_kernel<T, D><<<grid, kRowsTile * D / 4, 0, stream>>>(prm);
-  return cudaGetLastError();
+  return launch_behind(rows_join_kernel<T, D>, grid, kRowsTile * D / 4, 0, stream, prm);
 }
 
 }  // namespace

@@ -203,7 +203,7 @@ __device__ void run_records(const PagedWeighChunkParams& P, const Ctl& c, Record
         r.length = q.length;
         r.t0 = t.t0 + u0;
         r.n = u1 - u0;
-        r.extra = __ldg(P.extra_at + b);
+        r.extra = __ldcg(P.extra_at + b);
         if (cut && u0 == 0) P.joins[s] = {head, b, i * kPair, (int)(((item_x + t.n) * sh.count - 1) / sh.all)};
         ptx::mbar_arrive(c.bar(kItemFull + (int)slot));
       }
@@ -492,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* prefix = reinterpret_cast<int64_t*>(sgen + S::kOffPrefix);
   const int per_tile = kTile / P.group;
 
+  next_may_come();
   if (threadIdx.x == 0) P.joins[blockIdx.x] = {0, 0, 0, -1};  // nothing to join
   copy_unseen(P);
   paged_sums<kWarps>(P.t.batch, prefix, [&](int b) {
@@ -502,7 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   sh.per_head = prefix[P.t.batch];
   sh.all = sh.per_head * P.t.heads_kv;
   sh.count = (int)max((int64_t)1, min((int64_t)gridDim.x, sh.all / kMinUnits));
-  if (sh.all == 0 || (int)blockIdx.x >= sh.count) return;
+  if (sh.all == 0 || (int)blockIdx.x >= sh.count) {
+    after_previous();  // (every CTA: this kernel's end then tells that the other one's has come)
+    return;
+  }
 
   for (uint32_t at = threadIdx.x * 16; at < kStages * kExtra; at += kThreads * 16)
     ptx::st_shared_v4(sbase + S::kOffExtra + at, 0u, 0u, 0u, 0u);
@@ -550,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
 
+  after_previous();  // (the extra channels)
   ProducerState ps{0u, 0u};
   if (warp < 4) {
     if (warp == 0) {
@@ -590,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // leaves nothing of their weights.  A thread has a row; the tiles of the sequences follow each other.
 __global__ void __launch_bounds__(kTile) paged_weigh_extra_kernel(const PagedWeighChunkParams P) {
   extern __shared__ int64_t prefix[];
+  next_may_come();
   const int per_tile = kTile / P.group;
   paged_sums<kTile / 32>(P.t.batch, prefix, [&](int b) {
     const PagedSeq q = paged_seq(P.t, b);
@@ -620,6 +626,7 @@ __global__ void __launch_bounds__(kTile) paged_weigh_extra_kernel(const PagedWei
 // The item that share x begins and does not end: its first part there, the others at the
 // beginning of the shares up to the last.
 __global__ void __launch_bounds__(kPair) paged_weigh_join_kernel(const PagedWeighChunkParams P) {
+  after_previous();
   const PagedWeighJoin rec = P.joins[blockIdx.x];
   if (rec.last < 0) return;
   const PagedSeq q = paged_seq(P.t, rec.b);
@@ -652,12 +659,9 @@ cudaError_t launch(const PagedWeighChunkParams& prm, int grid, cudaStream_t stre
     *why = "launch failed";
     return e;
   }
-  paged_weigh_chunk_kernel<D><<<grid, kThreads, Smem<D>::kFixed + (prm.t.batch + 1) * 8, stream>>>(tq, tkv, prm);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) {
-    paged_weigh_join_kernel<<<grid, kPair, 0, stream>>>(prm);
-    e = cudaGetLastError();
-  }
+  e = launch_behind(paged_weigh_chunk_kernel<D>, dim3((unsigned)grid), kThreads,
+                    (size_t)Smem<D>::kFixed + (prm.t.batch + 1) * 8, stream, tq, tkv, prm);
+  if (e == cudaSuccess) e = launch_behind(paged_weigh_join_kernel, dim3((unsigned)grid), kPair, 0, stream, prm);
   if (e != cudaSuccess) *why = "launch failed";
   return e;
 }

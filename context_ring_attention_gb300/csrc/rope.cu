@@ -25,7 +25,8 @@
 namespace ra {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kAtOnce = 4;  // heads
 
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams P) {
@@ -54,22 +55,35 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams P) {
   const T* k = static_cast<const T*>(P.k) + b * P.ks.batch + i * P.ks.row;
   T* ko = static_cast<T*>(P.k_out) + b * P.kos.batch + i * P.kos.row;
   const int heads = P.heads_q + P.heads_kv;
-#pragma unroll 2
-  for (int h = blockIdx.y; h < heads; h += gridDim.y) {
-    const bool key = h >= P.heads_q;
-    const T* src = key ? k + (h - P.heads_q) * P.ks.head : q + h * P.qs.head;
-    T* dst = key ? ko + (h - P.heads_q) * P.kos.head : qo + h * P.qos.head;
+  // kWide: the loads of a few heads before their stores.
+  constexpr int kHeads = kWide ? kAtOnce : 1;
+  for (int h0 = blockIdx.y * kHeads; h0 < heads; h0 += gridDim.y * kHeads) {
+    const T* src[kHeads];
+    T* dst[kHeads];
+#pragma unroll
+    for (int e = 0; e < kHeads; ++e) {
+      const int h = min(h0 + e, heads - 1);
+      const bool key = h >= P.heads_q;
+      src[e] = key ? k + (h - P.heads_q) * P.ks.head : q + h * P.qs.head;
+      dst[e] = key ? ko + (h - P.heads_q) * P.kos.head : qo + h * P.qos.head;
+    }
     if constexpr (kWide) {
-      RopeUnit<T> u;
-      u.load(src, at.first, at.second);
-      if (at.pair >= 0) u.turn(c, s, P.t.interleaved);
-      u.store(dst, at.first, at.second);
+      RopeUnit<T> u[kHeads];
+#pragma unroll
+      for (int e = 0; e < kHeads; ++e)
+        if (h0 + e < heads) u[e].load(src[e], at.first, at.second);
+#pragma unroll
+      for (int e = 0; e < kHeads; ++e) {
+        if (h0 + e >= heads) break;
+        if (at.pair >= 0) u[e].turn(c, s, P.t.interleaved);
+        u[e].store(dst[e], at.first, at.second);
+      }
     } else if (at.pair >= 0) {
-      const float x1 = rope_load(src + at.first), x2 = rope_load(src + at.second);
-      rope_store(dst + at.first, x1 * c[0] - x2 * s[0]);
-      rope_store(dst + at.second, x1 * s[0] + x2 * c[0]);
+      const float x1 = rope_load(src[0] + at.first), x2 = rope_load(src[0] + at.second);
+      rope_store(dst[0] + at.first, x1 * c[0] - x2 * s[0]);
+      rope_store(dst[0] + at.second, x1 * s[0] + x2 * c[0]);
     } else {
-      dst[at.first] = src[at.first];
+      dst[0][at.first] = src[0][at.first];
     }
   }
 }

@@ -258,7 +258,7 @@ def test_out_of_range_tables_are_reported_and_skipped(dtype, counts):
         ra.ra_paged_sync_status(t.kv)  # cleared
 
     n, w = t.tokens, t.ref.width * 32
-    for offset, length in (([0, 5, 3, n], lengths), ([-1, 0, 0, 0], lengths), ([0, 0, 0, n + 1], lengths), ([5, 2, 2, 2], lengths),
+    for offset, length in (([0, 5, 3, 3], lengths), ([-1, 0, 0, 0], lengths), ([0, 0, 0, n + 1], lengths), ([5, 2, 2, 2], lengths),
                            (t.first, [counts[0] - 1, 60, 33]), (t.first, [w + 1, 60, 33]), (t.first, [-1, 60, 33]),
                            (t.first, [2 ** 31 - 1, 60, 33]), ([0, -2 ** 31, 2 ** 31 - 1, n], lengths)):
         off, ln = _i32(offset), _i32(length)
