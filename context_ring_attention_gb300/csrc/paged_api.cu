@@ -39,7 +39,7 @@ ra_status ok() {
 }
 
 constexpr int64_t kMaxPositions = int64_t(1) << 30;  // of a sequence: slot arithmetic stays in 32 bits
-constexpr int kMaxSlots = 1024;                      // CTAs of a key/value head
+constexpr int kMaxSlots = 512;                       // CTAs of a key/value head (the join's shared memory)
 // Of a sequence in the chunk kernels, so that an item, 2^18 tiles at most, ends well within their wait budget.
 constexpr int64_t kMaxChunkSlots = int64_t(1) << 25, kMaxChunkTiles = int64_t(1) << 18;
 
@@ -127,16 +127,16 @@ ra_status launched(ra_paged_s* kv, cudaError_t e, const char* what, cudaStream_t
 }
 
 // CTAs per key/value head of the row kernels: as many as the GPU holds at once (two an SM), and
-// no more than the largest number of shares that these sizes can make.
+// no more than the largest number of shares or items that these sizes can make.
 int row_slots(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width) {
   const ra_paged_problem& pb = kv->prob;
   const int64_t tiles = tokens * (pb.heads_q / pb.heads_kv) / ra::kRowsTile + std::min(batch, tokens);
   int64_t blocks = width * pb.page_rows / ra::kRowsBlock;
   if (pb.window > 0 && pb.window < kMaxPositions && pb.sinks < kMaxPositions)
     blocks = std::min(blocks, (pb.window + ra::kRowsTile + pb.sinks) / ra::kRowsBlock + 3);
-  const int64_t shares = tiles * blocks / (pb.dtype == RA_DTYPE_BF16 ? 16 : 4);  // as the kernels cut them (tiles below 2^30, blocks up to 2^26)
+  const int64_t shares = tiles * blocks / (pb.dtype == RA_DTYPE_BF16 ? 8 : 4);  // as the kernels cut them (tiles below 2^30, blocks up to 2^26)
   const int64_t sms = kv->sm_count > 0 ? kv->sm_count : 148;
-  return (int)std::max<int64_t>(1, std::min({shares, 2 * sms / pb.heads_kv, (int64_t)kMaxSlots}));
+  return (int)std::max<int64_t>(1, std::min({std::max(shares, tiles), 2 * sms / pb.heads_kv, (int64_t)kMaxSlots}));
 }
 
 // Shares of a CTA of the chunk kernel at most: where more than one item reads a sequence's keys,

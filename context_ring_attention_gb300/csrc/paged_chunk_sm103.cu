@@ -142,7 +142,9 @@ __device__ Shares shares_of(const PagedChunkParams& P, int per_item, int64_t* pr
   Shares s;
   s.per_head = prefix[P.t.batch];
   s.all = s.per_head * P.t.heads_kv;
-  const int64_t rounds = max((int64_t)1, min((int64_t)P.rounds, again * P.t.heads_kv * P.row_bytes * 2 / kRoundBytes));
+  // (rounds of 32 tiles a share at least: below that the parts cost more than the reads)
+  const int64_t rounds = max((int64_t)1, min(min((int64_t)P.rounds, s.all / (32 * (int64_t)gridDim.x)),
+                                             again * P.t.heads_kv * P.row_bytes * 2 / kRoundBytes));
   s.count = (int)max((int64_t)1, min(rounds * gridDim.x, s.all / kMinUnits));
   return s;
 }
@@ -730,46 +732,74 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- cut items --
-// The item that share s begins and does not end: its first part there, the others at the
-// beginning of the shares up to the last.  A thread has 4 channels of a row.
+// The items that shares begin and do not end: an item's first part is there, the others at the
+// beginning of the shares up to the last.  A CTA has 32 rows (its lanes): the warps bring the
+// parts' statistics side by side, then add columns of 4 channels, a few parts under way.
+constexpr int kJoinWarps = 16;
 template <int D>
-__global__ void __launch_bounds__(256) paged_chunk_join_kernel(const PagedChunkParams P, int shares) {
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_chunk_join_kernel(const PagedChunkParams P, int shares) {
+  __shared__ float tops[kJoinWarps][32];
+  __shared__ float2 sums[kJoinWarps][32];
   after_previous();
+  const int per_tile = kTile / P.group;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = (int)blockIdx.y >> 2, in_tile = ((int)blockIdx.y & 3) * 32 + lane;  // this lane's row of both tiles
+  const int token = in_tile / P.group;
   for (int s = (int)blockIdx.x; s < shares; s += (int)gridDim.x) {
     const PagedJoin rec = P.joins[s];
     if (rec.tokens == 0) continue;
-    const int per_tile = kTile / P.group;
     const int count = rec.last - s + 1;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // A warp has 32 rows of one column group, so that reads are whole lines.
-    for (int id = blockIdx.y * 8 + warp; id < (2 * kTile / 32) * (D / 4); id += gridDim.y * 8) {
-      const int q = id % (D / 4), r = id / (D / 4) * 32 + lane;  // column group; row over both tiles
-      const int g = r >> 7, in_tile = r & 127;
-      const int token = in_tile / P.group;
-      if (token >= per_tile || g * per_tile + token >= rec.tokens) continue;
-      auto row_of = [&](int i) { return ((i == 0 ? 2 * s + 1 : 2 * (s + i)) * 2 + g) * kTile + in_tile; };
-      float m = -INFINITY;
-      for (int i = 0; i < count; ++i) m = fmaxf(m, P.part_ml[row_of(i)].x);
-      const float ref = m == -INFINITY ? 0.f : m;
-      float l = 0.f, fix = 0.f;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+    const bool live = token < per_tile && g * per_tile + token < rec.tokens;
+    if (__syncthreads_or(live) == 0) continue;
+    auto row_of = [&](int i) { return ((i == 0 ? 2 * s + 1 : 2 * (s + i)) * 2 + g) * kTile + in_tile; };
+    float m = -INFINITY;
+    for (int i = warp; i < count; i += kJoinWarps)
+      if (live) m = fmaxf(m, P.part_ml[row_of(i)].x);
+    tops[warp][lane] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) m = fmaxf(m, tops[i][lane]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float2 lf = make_float2(0.f, 0.f);  // the sum, its correction
+    for (int i = warp; i < count; i += kJoinWarps)
+      if (live) {
+        const float4 ml = P.part_ml[row_of(i)];
+        const float f = exp2f(ml.x - ref);
+        lf.x = fmaf(ml.y, f, lf.x);
+        lf.y = fmaf(ml.z, f, lf.y);
+      }
+    sums[warp][lane] = lf;
+    __syncthreads();
+    lf = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) lf.x += sums[i][lane].x, lf.y += sums[i][lane].y;
+    const float l = lf.x, inv = l == 0.f ? 0.f : 1.0f / (l + lf.y);
+    const int at = rec.token + g * per_tile + token, head = rec.head * P.group + in_tile - token * P.group;
+    constexpr int kCols = D / 4 / kJoinWarps;  // column groups of a warp
+    float4 x[kCols];
+#pragma unroll
+    for (int q = 0; q < kCols; ++q) x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+#pragma unroll 4
       for (int i = 0; i < count; ++i) {
         const int row = row_of(i);
-        const float4 ml = P.part_ml[row];
-        const float f = exp2f(ml.x - ref);
-        const float4 y = reinterpret_cast<const float4*>(P.part_o)[((int64_t)(row >> 7) * (D / 4) + q) * kTile + in_tile];
-        l = fmaf(ml.y, f, l);
-        fix = fmaf(ml.z, f, fix);
-        x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+        const float f = exp2f(P.part_ml[row].x - ref);
+#pragma unroll
+        for (int q = 0; q < kCols; ++q) {
+          const float4 y =
+              reinterpret_cast<const float4*>(P.part_o)[((int64_t)(row >> 7) * (D / 4) + warp * kCols + q) * kTile + in_tile];
+          x[q].x = fmaf(y.x, f, x[q].x), x[q].y = fmaf(y.y, f, x[q].y);
+          x[q].z = fmaf(y.z, f, x[q].z), x[q].w = fmaf(y.w, f, x[q].w);
+        }
       }
-      const float inv = l == 0.f ? 0.f : 1.0f / (l + fix);
-      const int at = rec.token + g * per_tile + token, head = rec.head * P.group + in_tile - token * P.group;
-      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.o) + at * P.os.token + head * P.os.head + q * 4);
-      *dst = make_uint2(ptx::pack_bf16x2(x.x * inv, x.y * inv), ptx::pack_bf16x2(x.z * inv, x.w * inv));
-      if (q == 0 && P.lse != nullptr)
+      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.o) + at * P.os.token + head * P.os.head + warp * kCols * 4);
+#pragma unroll
+      for (int q = 0; q < kCols; ++q)
+        dst[q] = make_uint2(ptx::pack_bf16x2(x[q].x * inv, x[q].y * inv), ptx::pack_bf16x2(x[q].z * inv, x[q].w * inv));
+      if (warp == 0 && P.lse != nullptr)
         P.lse[(int64_t)at * P.heads_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
+    __syncthreads();
   }
 }
 
@@ -790,7 +820,7 @@ cudaError_t launch(const PagedChunkParams& prm, int grid, cudaStream_t stream, c
   paged_chunk_kernel<D><<<grid, kThreads, Smem<D>::kFixed + (prm.t.batch + 1) * 8, stream>>>(tq, tkv, prm);
   e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = launch_behind(paged_chunk_join_kernel<D>, dim3((unsigned)grid, 8), 256, 0, stream, prm, grid * (int)prm.rounds);
+    e = launch_behind(paged_chunk_join_kernel<D>, dim3((unsigned)grid, 8), kJoinWarps * 32, 0, stream, prm, grid * (int)prm.rounds);
   if (e != cudaSuccess) *why = "launch failed";
   return e;
 }

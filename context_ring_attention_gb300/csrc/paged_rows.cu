@@ -27,10 +27,11 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;   // blocks of a warp's ring
-// Blocks of a share at least: bf16 four a warp; float32, whose 32 keys at a time take 3 us, two
-// times that (3 sequences of 300 tokens: 41 us with 16 blocks).
+// Blocks of a share at least: bf16 two a warp (512 tokens of one sequence 13 us, with four 14.5,
+// as one item 16.5); float32, whose 32 keys at a time take 3 us, two times that (3 sequences of
+// 300 tokens: 41 us with 16 blocks).
 template <typename T>
-constexpr int kMinUnits = sizeof(T) == 2 ? 16 : 4;
+constexpr int kMinUnits = sizeof(T) == 2 ? 8 : 4;
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -57,27 +58,58 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// A CTA's walk over its share: items and the units [u0, u1) of each.
+// A CTA's walk over its share: items and the units [u0, u1) of each.  Where no item is long and
+// there are CTAs for all of them, shares are whole items instead (a unit is an item).
 struct Walk {
   int64_t x, x1, all;
   int slots;
+  bool whole;
   int b, tile;
   int64_t item_x;  // the item's first unit
   PagedSeq seq;
 };
-// Where this CTA's share begins; false where it has none.
+constexpr int kWholeUnits = 16;  // blocks of the longest item in that form
+// Where this CTA's share begins; false where it has none.  Every thread of the CTA calls it.
 template <typename T>
-__device__ __forceinline__ bool walk_begin(const PagedAttendParams& P, const int64_t* prefix, Walk& w) {
+__device__ __forceinline__ bool walk_begin(const PagedAttendParams& P, int64_t* prefix, Walk& w) {
+  __shared__ int longest;
+  if (threadIdx.x == 0) longest = 0;
+  paged_prefix<kRowsTile, kRowsBlock, kWarps>(P.t, P.group, P.window, P.sinks, prefix);
   w.all = prefix[P.t.batch];
-  w.slots = (int)max((int64_t)1, min((int64_t)P.slots, w.all / kMinUnits<T>));
   const int c = (int)blockIdx.x;
-  if (w.all == 0 || c >= w.slots) return false;
+  if (w.all == 0) return false;
+  // (a sequence of one item, as in a decoding step, is as long as it)
+  int most = 0;
+  for (int b = threadIdx.x; b < P.t.batch; b += kThreads) most = max(most, (int)min(prefix[b + 1] - prefix[b], (int64_t)1 << 30));
+  if (most > 0) atomicMax(&longest, most);
+  __syncthreads();
+  w.whole = longest <= kWholeUnits && P.t.batch <= P.slots;
+  if (w.whole) {
+    __syncthreads();  // (all have read the units)
+    for (int b = threadIdx.x; b < P.t.batch; b += kThreads) {
+      const PagedSeq q = paged_seq(P.t, b);
+      prefix[b + 1] = paged_mine(P.t, q, P.group) ? (q.count * P.group + kRowsTile - 1) / kRowsTile : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) paged_scan(P.t.batch, prefix);
+    __syncthreads();
+    w.all = prefix[P.t.batch];
+    w.slots = (int)min((int64_t)P.slots, w.all);
+  } else {
+    w.slots = (int)max((int64_t)1, min((int64_t)P.slots, w.all / kMinUnits<T>));
+  }
+  if (c >= w.slots) return false;
   w.x = w.all * c / w.slots;
   w.x1 = w.all * (c + 1) / w.slots;
   w.b = paged_find(prefix, P.t.batch, w.x);
   w.seq = paged_seq(P.t, w.b);
-  w.tile = paged_find_item<kRowsTile, kRowsBlock>(w.seq, P.group, P.window, P.sinks, w.x - prefix[w.b], w.item_x);
-  w.item_x += prefix[w.b];
+  if (w.whole) {
+    w.tile = (int)(w.x - prefix[w.b]);
+    w.item_x = w.x;
+  } else {
+    w.tile = paged_find_item<kRowsTile, kRowsBlock>(w.seq, P.group, P.window, P.sinks, w.x - prefix[w.b], w.item_x);
+    w.item_x += prefix[w.b];
+  }
   return true;
 }
 // To the item at x (the share's current item is done).
@@ -127,7 +159,6 @@ __global__ void __launch_bounds__(kThreads) rows_bf16_kernel(const PagedAttendPa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
   next_may_come();
   if (P.joins != nullptr && threadIdx.x == 0) P.joins[(int64_t)head * P.slots + blockIdx.x] = make_int4(0, 0, 0, 0);
-  paged_prefix<kRowsTile, kRowsBlock, kWarps>(P.t, P.group, P.window, P.sinks, prefix);
   Walk w;
   if (!walk_begin<__nv_bfloat16>(P, prefix, w)) return;
 
@@ -142,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) rows_bf16_kernel(const PagedAttendPa
     const PagedSpan span = paged_span(P.window, P.sinks, it.s0, it.s1);
     const PagedBlocks<kRowsBlock> blocks(span);
     const int n = max(1, blocks.n);
-    const int u0 = (int)(w.x - w.item_x), u1 = (int)min((int64_t)n, w.x1 - w.item_x);
+    const int u0 = w.whole ? 0 : (int)(w.x - w.item_x), u1 = w.whole ? n : (int)min((int64_t)n, w.x1 - w.item_x);
     const int n_live = min(u1, blocks.n);
     const int mine = n_live > u0 + warp ? (n_live - u0 - warp + kWarps - 1) / kWarps : 0;  // blocks of this warp
 
@@ -322,7 +353,7 @@ __global__ void __launch_bounds__(kThreads) rows_bf16_kernel(const PagedAttendPa
       }
     }
     __syncthreads();  // the ring is free for the next item
-    w.x = w.item_x + u1;
+    w.x = w.item_x + (w.whole ? 1 : u1);
     if (w.x >= w.x1) return;
   }
 }
@@ -348,7 +379,6 @@ __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendPar
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
   next_may_come();
   if (P.joins != nullptr && threadIdx.x == 0) P.joins[(int64_t)head * P.slots + blockIdx.x] = make_int4(0, 0, 0, 0);
-  paged_prefix<kRowsTile, kRowsBlock, kWarps>(P.t, P.group, P.window, P.sinks, prefix);
   Walk w;
   if (!walk_begin<float>(P, prefix, w)) return;
   const float* cache = static_cast<const float*>(P.t.cache);
@@ -359,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendPar
     const PagedSpan span = paged_span(P.window, P.sinks, it.s0, it.s1);
     const PagedBlocks<kRowsBlock> blocks(span);
     const int n = max(1, blocks.n);
-    const int u0 = (int)(w.x - w.item_x), u1 = (int)min((int64_t)n, w.x1 - w.item_x);
+    const int u0 = w.whole ? 0 : (int)(w.x - w.item_x), u1 = w.whole ? n : (int)min((int64_t)n, w.x1 - w.item_x);
     const int n_live = min(u1, blocks.n);
     const int steps = n_live > u0 ? (n_live - u0 + 1) / 2 : 0;
     RA_BOUNDS(P.t.status, it.row0 >= 0 && it.rows > 0 && w.seq.token0 + w.seq.count <= P.t.tokens && u0 >= 0 && u0 < u1 && u1 <= n, 117);
@@ -477,38 +507,54 @@ __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendPar
       }
     }
     __syncthreads();
-    w.x = w.item_x + u1;
+    w.x = w.item_x + (w.whole ? 1 : u1);
     if (w.x >= w.x1) return;
   }
 }
 
 // ---------------------------------------------------------------- cut items --
 // The item that slot x's share begins and does not end: its first part there, the others at the
-// beginning of the slots up to the last.  A thread has 4 channels of a row.
+// beginning of the slots up to the last.  A warp brings the statistics of a row's parts at once,
+// then a thread adds 4 channels of a row, eight parts under way.
 template <typename T, int D>
-__global__ void __launch_bounds__(kRowsTile * D / 4) rows_join_kernel(const PagedAttendParams P) {
+__global__ void __launch_bounds__(kRowsTile * 32) rows_join_kernel(const PagedAttendParams P) {
+  extern __shared__ float factors[];  // [parts, kRowsTile]
+  __shared__ float2 totals[kRowsTile];
   const int head = (int)blockIdx.y;
   const int64_t me = (int64_t)head * P.slots + blockIdx.x;
   after_previous();
   const int4 rec = P.joins[me];
+  if (rec.y == 0) return;
+  const int count = rec.z - (int)blockIdx.x + 1;
+  auto part = [&](int i, int r) { return (i == 0 ? me * 2 + 1 : (me + i) * 2) * kRowsTile + r; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  {
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < count; i += 32) m = fmaxf(m, P.part_ml[part(i, warp)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int i = lane; i < count; i += 32) {
+      const float2 ml = P.part_ml[part(i, warp)];
+      const float f = exp2f(ml.x - ref);
+      factors[i * kRowsTile + warp] = f;
+      l = fmaf(ml.y, f, l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) totals[warp] = make_float2(m, l);
+  }
+  __syncthreads();
   const int r = threadIdx.x / (D / 4), ch = threadIdx.x % (D / 4);
   if (r >= rec.y) return;
-  const int count = rec.z - (int)blockIdx.x + 1;
-  auto part = [&](int i) { return (i == 0 ? me * 2 + 1 : (me + i) * 2) * kRowsTile + r; };
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i < count; ++i) m = fmaxf(m, P.part_ml[part(i)].x);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < count; ++i) {
-    const float2 ml = P.part_ml[part(i)];
-    const float f = exp2f(ml.x - ref);
-    const float4 y = *reinterpret_cast<const float4*>(P.part_o + part(i) * D + ch * 4);
-    l = fmaf(ml.y, f, l);
+    const float f = factors[i * kRowsTile + r];
+    const float4 y = *reinterpret_cast<const float4*>(P.part_o + part(i, r) * D + ch * 4);
     x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
   }
+  const float m = totals[r].x, l = totals[r].y;
   const int row = rec.x + r;
   const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
   T* dst = row_of<T>(P.os, P.o, P.group, head, row) + ch * 4;
@@ -553,7 +599,7 @@ cudaError_t launch(const PagedAttendParams& prm, cudaStream_t stream) {
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || prm.slots == 1) return e;
-  return launch_behind(rows_join_kernel<T, D>, grid, kRowsTile * D / 4, 0, stream, prm);
+  return launch_behind(rows_join_kernel<T, D>, grid, kRowsTile * 32, (size_t)prm.slots * kRowsTile * 4, stream, prm);
 }
 
 }  // namespace

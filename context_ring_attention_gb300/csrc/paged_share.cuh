@@ -28,35 +28,51 @@ __device__ __forceinline__ int paged_units(const PagedSeq& q, int group, int win
   return max(1, PagedBlocks<kB>(paged_span(window, sinks, it.s0, it.s1)).n);
 }
 
+// prefix[1 ..] from the sequences' own numbers to their sums (a whole warp calls it).
+__device__ __forceinline__ void paged_scan(int batch, int64_t* prefix) {
+  const int lane = threadIdx.x & 31;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < batch; b0 += 32) {
+    int64_t x = b0 + lane < batch ? prefix[b0 + lane + 1] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (b0 + lane < batch) prefix[b0 + lane + 1] = before + x;
+    before += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) prefix[0] = 0;
+}
+
 // Sums of the sequences' units: prefix[b] of the sequences before b, prefix[batch] of all.
 // Every thread of the CTA calls it; it ends with a barrier.
 template <int kR, int kB, int kWarps>
 __device__ void paged_prefix(const PagedTable& t, int group, int window, int sinks, int64_t* prefix) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int b = warp; b < t.batch; b += kWarps) {
-    const PagedSeq q = paged_seq(t, b);
+  for (int b0 = warp * 32; b0 < t.batch; b0 += kWarps * 32) {
+    // A lane has a sequence of one or two items (a decoding step's) for itself; the others' items
+    // are shared out among the lanes.
+    PagedSeq q{0, 0, 0};
+    if (b0 + lane < t.batch) q = paged_seq(t, b0 + lane);
     const int tiles = paged_mine(t, q, group) ? (q.count * group + kR - 1) / kR : 0;
     int64_t sum = 0;
-    for (int i = lane; i < tiles; i += 32) sum += paged_units<kR, kB>(q, group, window, sinks, i);
+    if (tiles <= 2)
+      for (int i = 0; i < tiles; ++i) sum += paged_units<kR, kB>(q, group, window, sinks, i);
+    for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
+      const int src = __ffs(many) - 1;
+      const PagedSeq o{0, __shfl_sync(0xffffffffu, q.count, src), __shfl_sync(0xffffffffu, q.length, src)};
+      const int n = __shfl_sync(0xffffffffu, tiles, src);
+      int64_t all = 0;
+      for (int i = lane; i < n; i += 32) all += paged_units<kR, kB>(o, group, window, sinks, i);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) prefix[b + 1] = sum;
+      for (int e = 16; e > 0; e >>= 1) all += __shfl_xor_sync(0xffffffffu, all, e);
+      if (lane == src) sum = all;
+    }
+    if (b0 + lane < t.batch) prefix[b0 + lane + 1] = sum;
   }
   __syncthreads();
-  if (warp == 0) {
-    int64_t before = 0;
-    for (int b0 = 0; b0 < t.batch; b0 += 32) {
-      int64_t x = b0 + lane < t.batch ? prefix[b0 + lane + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (b0 + lane < t.batch) prefix[b0 + lane + 1] = before + x;
-      before += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) prefix[0] = 0;
-  }
+  if (warp == 0) paged_scan(t.batch, prefix);
   __syncthreads();
 }
 

@@ -69,20 +69,7 @@ __device__ __forceinline__ void paged_sums(int batch, int64_t* prefix, Own own) 
     if (lane == 0) prefix[b + 1] = sum;
   }
   __syncthreads();
-  if (warp == 0) {
-    int64_t before = 0;
-    for (int b0 = 0; b0 < batch; b0 += 32) {
-      int64_t x = b0 + lane < batch ? prefix[b0 + lane + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (b0 + lane < batch) prefix[b0 + lane + 1] = before + x;
-      before += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) prefix[0] = 0;
-  }
+  if (warp == 0) paged_scan(batch, prefix);
   __syncthreads();
 }
 // Sum of units(i) over i < n, the whole warp's.

@@ -105,16 +105,17 @@ struct Rows {
   }
 };
 
-constexpr int kStages = 4;  // blocks of a warp's ring
+constexpr int kStages = 2;  // steps of a warp's ring: three leave room for 8 warps an SM, not 12 (1M tokens 389 us, 336)
+constexpr int kStepKeys = 32;  // two blocks of 16 (one at a time: 1M tokens 416 us)
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighParams P) {
-  constexpr int kRowBytes = D * 2, kChunks = D / 8, kBlockBytes = kRowsBlock * kRowBytes;
-  constexpr int kStageBytes = kBlockBytes + kRowsBlock * 4;  // keys, and what they had before
+  constexpr int kRowBytes = D * 2, kChunks = D / 8, kBlockBytes = kStepKeys * kRowBytes;
+  constexpr int kStageBytes = kBlockBytes + kStepKeys * 4;  // keys, and what they had before
   extern __shared__ __align__(128) uint8_t smem_bytes[];
   uint8_t* smem = smem_bytes;
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + kWarps * kStages * kStageBytes);
-  slot_prefix<kRowsBlock>(P.t, P.group, prefix);
+  slot_prefix<kStepKeys>(P.t, P.group, prefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
   const int quad = lane >> 2, two = (lane & 3) * 2;
   const __nv_bfloat16* cache = static_cast<const __nv_bfloat16*>(P.t.cache);
@@ -131,8 +132,8 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
   while (prefix[b_first + 1] <= x0) ++b_first;
 
   // Block i of the run into the ring; a lane knows sequence, slot and page of one of the next 32.
-  int known_b = b_first, known_j = 0, known_page = -1;
-  uint32_t bad = 0u;  // stages whose page is none
+  int known_b = b_first, known_j = 0, known_page[2] = {-1, -1};
+  uint32_t bad = 0u;  // blocks of the stages whose page is none
   auto load = [&](int i) {
     if ((i & 31) == 0 && i < n) {
       int b = __shfl_sync(0xffffffffu, known_b, 31);  // (the last block known so far)
@@ -140,25 +141,34 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
       const int64_t x = min(x0 + i + lane, x0 + n - 1);
       while (prefix[b + 1] <= x) ++b;
       known_b = b;
-      known_j = (int)(x - prefix[b]) * kRowsBlock;
+      known_j = (int)(x - prefix[b]) * kStepKeys;
       const Rows<__nv_bfloat16> rows{P, paged_seq(P.t, b), head};
-      // (of a block the first slot or the last one is seen, or none)
-      const bool look = rows.seen(known_j) || rows.seen(min(known_j + kRowsBlock, rows.seq.length) - 1);
-      known_page = look ? paged_page(P.t, b, known_j / P.t.page_rows) : -2;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // a page of either block
+        const int j = known_j + e * kRowsBlock;
+        // (of a block the first slot or the last one is seen, or none)
+        const bool look = j < rows.seq.length && (rows.seen(j) || rows.seen(min(j + kRowsBlock, rows.seq.length) - 1));
+        known_page[e] = look ? paged_page(P.t, b, j / P.t.page_rows) : -2;
+      }
     }
     if (i < n) {
       const int b = __shfl_sync(0xffffffffu, known_b, i & 31), j0 = __shfl_sync(0xffffffffu, known_j, i & 31);
-      const int page = __shfl_sync(0xffffffffu, known_page, i & 31), s = i % kStages;
-      bad = page == -1 ? bad | (1u << s) : bad & ~(1u << s);
-      const int64_t row0 = paged_row(P.t, max(page, 0), 0, head, j0 % P.t.page_rows);
-      RA_BOUNDS(P.t.status, row0 >= 0 && row0 + kRowsBlock <= (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 115);
+      const int s = i % kStages;
       const uint32_t dst = ring + s * kStageBytes;
 #pragma unroll
-      for (int x = 0; x < kChunks / 2; ++x) {
-        const int id = lane + 32 * x, r = id / kChunks, ch = id % kChunks;
-        copy16(dst + r * kRowBytes + ((ch ^ (r & 7)) * 16), cache + (row0 + r) * D + ch * 8, page >= 0);
+      for (int e = 0; e < 2; ++e) {
+        const int page = __shfl_sync(0xffffffffu, known_page[e], i & 31), j = j0 + e * kRowsBlock;
+        const uint32_t bit = 1u << (2 * s + e);
+        bad = page == -1 ? bad | bit : bad & ~bit;
+        const int64_t row0 = paged_row(P.t, max(page, 0), 0, head, j % P.t.page_rows);
+        RA_BOUNDS(P.t.status, row0 >= 0 && row0 + kRowsBlock <= (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 115);
+#pragma unroll
+        for (int x = 0; x < kChunks / 2; ++x) {
+          const int id = lane + 32 * x, r = id / kChunks, ch = id % kChunks;
+          copy16(dst + (e * kRowsBlock + r) * kRowBytes + ((ch ^ (r & 7)) * 16), cache + (row0 + r) * D + ch * 8, page >= 0);
+        }
       }
-      if (lane < kRowsBlock) {
+      {
         const int j = j0 + lane;
         const bool had = P.weight_in != nullptr && j < P.weight_width && j < paged_seq(P.t, b).slot0();
         const int64_t at = ((int64_t)b * P.t.heads_kv + head) * P.weight_width + j;
@@ -185,12 +195,12 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
       rows.seq = paged_seq(P.t, b);
       held = -1;
     }
-    const int j0 = (int)(x0 + i - prefix[b]) * kRowsBlock;
+    const int j0 = (int)(x0 + i - prefix[b]) * kStepKeys;
     const int rows_n = rows.seq.count * P.group;
     int tile0, tile1;
-    rows.tiles(j0, kRowsBlock, tile0, tile1);
+    rows.tiles(j0, kStepKeys, tile0, tile1);
     const uint32_t kb = ring + st * kStageBytes;
-    float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // keys two, two + 1 of each 8
+    float sum[4][2] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};  // keys two, two + 1 of each 8
     for (int t = tile0; t < tile1; ++t) {
       if (t != held) {
         // The rows as the first operand: rows quad and quad + 8, channels two.. and two + 8..
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
           const int r = t * 16 + quad + 8 * e;
           const bool live = r < rows_n;
           slot[e] = live ? rows.seq.slot0() + r / P.group : -1;
-          lse2[e] = live ? rows.lse_of(r) * kLog2e : 0.f;
+          lse2[e] = live ? rows.lse_of(r) * kLog2e : INFINITY;  // (rows of no token: no weight)
           const __nv_bfloat16* src = live ? rows.row_ptr(r) : nullptr;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
@@ -209,41 +219,57 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
               q[kk][e + 2 * f] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + f * 8 + two)) : 0u;
         }
       }
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float s[4][4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[c][e] = 0.f;
       const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t r[4];
-        ldmatrix4(r, kb + kr * kRowBytes + (((2 * kk + kc) ^ (kr & 7)) * 16));
-        mma16816(s[0], q[kk], r[0], r[1]);
-        mma16816(s[1], q[kk], r[2], r[3]);
-      }
+      for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+        for (int e = 0; e < 2; ++e) {
+          uint32_t r[4];
+          ldmatrix4(r, kb + (e * kRowsBlock + kr) * kRowBytes + (((2 * kk + kc) ^ (kr & 7)) * 16));
+          mma16816(s[2 * e], q[kk], r[0], r[1]);
+          mma16816(s[2 * e + 1], q[kk], r[2], r[3]);
+        }
+      // Keys that every row of the tile sees need no mask.
+      const int s0 = rows.seq.slot0() + t * 16 / P.group;
+      const int s1 = rows.seq.slot0() + (min(t * 16 + 16, rows_n) - 1) / P.group;
+      const bool whole = j0 + kStepKeys - 1 <= s0 && (P.window == 0 || j0 > s1 - P.window || j0 + kStepKeys <= P.sinks);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool sees = paged_sees(P.window, P.sinks, slot[e >> 1], j0 + 8 * c + two + (e & 1));
-          const float p = ptx::ex2_approx(fmaf(s[c][e], P.scale_log2, -lse2[e >> 1]));
-          sum[c][e & 1] += sees ? p : 0.f;
+          float p = ptx::ex2_approx(fmaf(s[c][e], P.scale_log2, -lse2[e >> 1]));
+          if (!whole && !paged_sees(P.window, P.sinks, slot[e >> 1], j0 + 8 * c + two + (e & 1))) p = 0.f;
+          sum[c][e & 1] += p;
         }
     }
     // Down the columns; then lane l has slot j0 + l.
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) sum[c][e] += __shfl_xor_sync(0xffffffffu, sum[c][e], o);
-    const int from = (lane & 7) >> 1;
-    const float a0 = __shfl_sync(0xffffffffu, sum[0][0], from), a1 = __shfl_sync(0xffffffffu, sum[0][1], from);
-    const float c0 = __shfl_sync(0xffffffffu, sum[1][0], from), c1 = __shfl_sync(0xffffffffu, sum[1][1], from);
+    // (lanes 4 n + i hold the keys 8 c + 2 i, + 1 in sum[c])
+    float mine = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = __shfl_sync(0xffffffffu, sum[c][e], (lane & 7) >> 1);
+        if ((lane >> 3) == c && (lane & 1) == e) mine = x;
+      }
     const int j = j0 + lane;
-    if (lane < kRowsBlock && j < rows.seq.length && !(((bad >> st) & 1u) && rows.seen(j))) {
+    if (j < rows.seq.length && !(((bad >> (2 * st + (lane >> 4))) & 1u) && rows.seen(j))) {
       if (j < P.weight_width) {
         const float had = *reinterpret_cast<const float*>(smem + (kb - ptx::smem_addr(smem)) + kBlockBytes + lane * 4);
         const int64_t at = ((int64_t)b * P.t.heads_kv + head) * P.weight_width + j;
         RA_BOUNDS(P.t.status, j >= 0 && at < (int64_t)P.t.batch * P.t.heads_kv * P.weight_width, 112);
-        P.weight[at] = had + (lane < 8 ? ((lane & 1) ? a1 : a0) : ((lane & 1) ? c1 : c0));
+        P.weight[at] = had + mine;
       } else {
         atomicOr(P.t.status, kPagedStatusRange);
       }
@@ -314,7 +340,7 @@ unsigned slots_of(const PagedWeighParams& prm, int sm_count, int per_sm, int own
 
 template <int D>
 cudaError_t launch_bf16(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
-  constexpr int kRing = kWarps * kStages * (kRowsBlock * D * 2 + kRowsBlock * 4);
+  constexpr int kRing = kWarps * kStages * (kStepKeys * D * 2 + kStepKeys * 4);
   static std::atomic<int> ready[kMaxDevices];
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -325,7 +351,7 @@ cudaError_t launch_bf16(const PagedWeighParams& prm, int sm_count, cudaStream_t 
     if (e != cudaSuccess) return e;
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
-  const dim3 grid(slots_of(prm, sm_count, 3, kWarps * kRowsBlock), (unsigned)prm.t.heads_kv);
+  const dim3 grid(slots_of(prm, sm_count, 3, kWarps * kStepKeys), (unsigned)prm.t.heads_kv);
   weigh_bf16_kernel<D><<<grid, kThreads, kRing + (prm.t.batch + 1) * 8, stream>>>(prm);
   return cudaGetLastError();
 }

@@ -597,10 +597,13 @@ __global__ void __launch_bounds__(kTile) paged_weigh_extra_kernel(const PagedWei
   extern __shared__ int64_t prefix[];
   next_may_come();
   const int per_tile = kTile / P.group;
-  paged_sums<kTile / 32>(P.t.batch, prefix, [&](int b) {
+  for (int b = threadIdx.x; b < P.t.batch; b += kTile) {
     const PagedSeq q = paged_seq(P.t, b);
-    return paged_mine(P.t, q, P.group) ? (int64_t)((q.count + per_tile - 1) / per_tile) : 0;
-  });
+    prefix[b + 1] = paged_mine(P.t, q, P.group) ? (q.count + per_tile - 1) / per_tile : 0;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) paged_scan(P.t.batch, prefix);
+  __syncthreads();
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int b = threadIdx.x; b < P.t.batch; b += kTile) P.extra_at[b] = (int32_t)min(prefix[b], (int64_t)P.tiles - 1);
   const int head = (int)blockIdx.y, row = threadIdx.x, tok = row / P.group;
