@@ -127,8 +127,9 @@ ra_status launched(ra_paged_s* kv, cudaError_t e, const char* what, cudaStream_t
 }
 
 // CTAs per key/value head of the row kernels: as many as the GPU holds at once (two an SM), and
-// no more than the largest number of shares or items that these sizes can make.
-int row_slots(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width) {
+// no more than the largest number of shares or items that these sizes can make.  Beside a chunk
+// kernel three times as many: it leaves them only some of the SMs, and more as it ends.
+int row_slots(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width, bool beside) {
   const ra_paged_problem& pb = kv->prob;
   const int64_t tiles = tokens * (pb.heads_q / pb.heads_kv) / ra::kRowsTile + std::min(batch, tokens);
   int64_t blocks = width * pb.page_rows / ra::kRowsBlock;
@@ -136,7 +137,7 @@ int row_slots(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width
     blocks = std::min(blocks, (pb.window + ra::kRowsTile + pb.sinks) / ra::kRowsBlock + 3);
   const int64_t shares = tiles * blocks / (pb.dtype == RA_DTYPE_BF16 ? 8 : 4);  // as the kernels cut them (tiles below 2^30, blocks up to 2^26)
   const int64_t sms = kv->sm_count > 0 ? kv->sm_count : 148;
-  return (int)std::max<int64_t>(1, std::min({std::max(shares, tiles), 2 * sms / pb.heads_kv, (int64_t)kMaxSlots}));
+  return (int)std::max<int64_t>(1, std::min({std::max(shares, tiles), (beside ? 6 : 2) * sms / pb.heads_kv, (int64_t)kMaxSlots}));
 }
 
 // Shares of a CTA of the chunk kernel at most: where more than one item reads a sequence's keys,
@@ -308,7 +309,7 @@ ra_status ra_paged_attend_scratch_size(ra_paged_t kv, int64_t batch, int64_t tok
   const Route route = route_of(kv, batch, tokens, table_width);
   *bytes = 0;
   if (route.chunks) *bytes += chunk_scratch(kv, (int64_t)chunk_grid(kv) * chunk_rounds(kv, batch, tokens, table_width));
-  if (route.rows) *bytes += rows_scratch(kv, row_slots(kv, batch, tokens, table_width));
+  if (route.rows) *bytes += rows_scratch(kv, row_slots(kv, batch, tokens, table_width, route.chunks));
   return ok();
 }
 
@@ -329,7 +330,7 @@ ra_status ra_paged_attend(ra_paged_t kv, const void* cache, int64_t batch, int64
   if ((tokens > 1 && prm.qs.token == 0) || (pb.heads_q > 1 && prm.qs.head == 0))
     return fail(RA_ERR_INVALID_ARG, "q: rows lie in one place");
   const Route route = route_of(kv, batch, tokens, table_width);
-  const int slots = route.rows ? row_slots(kv, batch, tokens, table_width) : 1;
+  const int slots = route.rows ? row_slots(kv, batch, tokens, table_width, route.chunks) : 1;
   const bool parts = route.chunks || slots > 1;
   if (parts && scratch == nullptr)
     return fail(RA_ERR_INVALID_ARG, "null scratch (ra_paged_attend_scratch_size bytes are needed)");
@@ -339,8 +340,9 @@ ra_status ra_paged_attend(ra_paged_t kv, const void* cache, int64_t batch, int64
   s = check_call(kv, batch, tokens, table_width, t16, 4, t4, 4, st);
   if (s != RA_OK) return s;
   prm.t = table_of(kv, cache, batch, tokens, page_table, table_width, offset, length);
+  const int grid = chunk_grid(kv);
+  ra::PagedChunkParams c{};
   if (route.chunks) {
-    ra::PagedChunkParams c{};
     c.t = prm.t;
     c.t.few = route.rows ? ra::kManyOnly : ra::kAllRows;
     c.heads_q = pb.heads_q;
@@ -356,34 +358,39 @@ ra_status ra_paged_attend(ra_paged_t kv, const void* cache, int64_t batch, int64
     c.qs = prm.qs;
     c.os = prm.os;
     c.lse = lse;
-    const int grid = chunk_grid(kv);
-    const int64_t shares = (int64_t)grid * c.rounds, rows = shares * 2 * 2 * 128;
+    const int64_t shares = (int64_t)grid * c.rounds, n = shares * 2 * 2 * 128;
     c.part_o = scratch;
-    c.part_ml = reinterpret_cast<float4*>(scratch + rows * pb.head_dim);
-    c.joins = reinterpret_cast<ra::PagedJoin*>(c.part_ml + rows);
-    const char* why = "";
-    const cudaError_t e = ra::launch_paged_chunk(pb.head_dim, c, grid, st, &why);
-    if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache attention: %s (%s)", why, cudaGetErrorString(e));
-    if (!route.rows) return launched(kv, e, "cache attention", st);
-    prm.t.few = ra::kFewOnly;
+    c.part_ml = reinterpret_cast<float4*>(scratch + n * pb.head_dim);
+    c.joins = reinterpret_cast<ra::PagedJoin*>(c.part_ml + n);
     scratch += chunk_scratch(kv, shares) / 4;
   }
-  prm.heads_q = pb.heads_q;
-  prm.group = pb.heads_q / pb.heads_kv;
-  prm.slots = slots;
-  prm.window = (int32_t)std::min(pb.window, kMaxPositions);
-  prm.sinks = pb.window > 0 ? (int32_t)std::min(pb.sinks, kMaxPositions) : 0;
-  prm.scale_log2 = pb.scale * 1.4426950408889634f;
-  prm.q = q;
-  prm.o = o;
-  prm.lse = lse;
-  if (slots > 1) {
-    const int64_t n = (int64_t)pb.heads_kv * slots * 2;
-    prm.part_o = scratch;
-    prm.part_ml = reinterpret_cast<float2*>(scratch + n * ra::kRowsTile * pb.head_dim);
-    prm.joins = reinterpret_cast<int4*>(prm.part_ml + n * ra::kRowsTile);
+  if (route.rows) {
+    if (route.chunks) prm.t.few = ra::kFewOnly;
+    prm.beside = route.chunks;
+    prm.heads_q = pb.heads_q;
+    prm.group = pb.heads_q / pb.heads_kv;
+    prm.slots = slots;
+    prm.window = (int32_t)std::min(pb.window, kMaxPositions);
+    prm.sinks = pb.window > 0 ? (int32_t)std::min(pb.sinks, kMaxPositions) : 0;
+    prm.scale_log2 = pb.scale * 1.4426950408889634f;
+    prm.q = q;
+    prm.o = o;
+    prm.lse = lse;
+    if (slots > 1) {
+      const int64_t n = (int64_t)pb.heads_kv * slots * 2;
+      prm.part_o = scratch;
+      prm.part_ml = reinterpret_cast<float2*>(scratch + n * ra::kRowsTile * pb.head_dim);
+      prm.joins = reinterpret_cast<int4*>(prm.part_ml + n * ra::kRowsTile);
+    }
   }
-  return launched(kv, ra::launch_paged_rows(pb.dtype, pb.head_dim, prm, st), "cache attention launch", st);
+  const char* why = "";
+  cudaError_t e = cudaSuccess;
+  if (route.chunks) e = ra::launch_paged_chunk(pb.head_dim, c, grid, st, &why);
+  if (e == cudaSuccess && route.rows) e = ra::launch_paged_rows(pb.dtype, pb.head_dim, prm, route.chunks, st);
+  if (e == cudaSuccess && route.chunks) e = ra::launch_paged_chunk_join(pb.head_dim, c, grid, st);
+  if (e == cudaSuccess && route.rows) e = ra::launch_paged_rows_join(pb.dtype, pb.head_dim, prm, st);
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache attention launch: %s %s", cudaGetErrorString(e), why);
+  return launched(kv, e, "cache attention launch", st);
 }
 
 ra_status ra_paged_weigh_scratch_size(ra_paged_t kv, int64_t batch, int64_t tokens, int64_t table_width, int64_t* bytes) {

@@ -121,31 +121,65 @@ __device__ __forceinline__ int item_units(const PagedChunkParams& P, const Paged
 
 struct Shares {
   int64_t all, per_head;  // units of all heads, of one
-  int count;              // shares
+  int ctas, count;        // CTAs that take shares, shares
   __device__ __forceinline__ int64_t begin(int s) const { return all * s / count; }
 };
+
+// CTAs of this kernel's, where the row kernel reads other sequences' keys beside it: the two then
+// end together.  A key tile takes a CTA 1.45 us; the reads take the time of their bytes at 6.6 TB/s
+// if five eighths of the SMs are left to them, and longer in proportion if fewer are.  (One chunk of
+// 512 tokens and 31 single ones under a window of 8192: one kernel after the other 226 us.)
+__device__ __forceinline__ int ctas_beside(int64_t units, double bytes, int sms) {
+  const float work = 1.45f * (float)units, reads = (float)(bytes / 6.6e6);  // us
+  const float few = 0.375f * (float)sms, need = 0.625f * (float)sms;
+  const float n = work <= few * reads ? 1.1f * work / reads + 1.f : (float)sms * work / (need * reads + work);
+  return max(1, min(sms, (int)ceilf(n)));
+}
 
 // Prefix sums of the sequences' units (one head), and the number of shares: as many as CTAs, times
 // the rounds.  Every thread calls it; it ends with a barrier.
 __device__ Shares shares_of(const PagedChunkParams& P, int per_item, int64_t* prefix, int64_t* scratch) {
-  int64_t again = 0;  // slots that more than one item reads
-  paged_sums<kWarps>(P.t.batch, prefix, [&](int b) {
-    const PagedSeq q = paged_seq(P.t, b);
-    const int items = paged_mine(P.t, q, P.group) ? (q.count + per_item - 1) / per_item : 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t again = 0, others = 0;  // slots that more than one item reads; that other kernels' sequences read
+  for (int b0 = warp * 32; b0 < P.t.batch; b0 += kWarps * 32) {
+    PagedSeq q{0, 0, 0};
+    if (b0 + lane < P.t.batch) q = paged_seq(P.t, b0 + lane);
+    const bool mine = paged_mine(P.t, q, P.group);
+    const int items = mine ? (q.count + per_item - 1) / per_item : 0;
+    if (!mine && q.count > 0) {
+      const PagedSpan sp = paged_span(P.window, P.sinks, q.slot0(), q.length - 1);
+      others += sp.sink + sp.hi - sp.lo;
+    }
     if (items > 1) again += q.length;
-    return warp_total(items, [&](int i) { return item_units(P, q, per_item, i); });
-  });
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = again;
+    int64_t sum = 0;
+    for (uint32_t some = __ballot_sync(0xffffffffu, items > 0); some; some &= some - 1) {
+      const int src = __ffs(some) - 1;
+      const PagedSeq o{0, __shfl_sync(0xffffffffu, q.count, src), __shfl_sync(0xffffffffu, q.length, src)};
+      const int64_t all = warp_total(__shfl_sync(0xffffffffu, items, src), [&](int i) { return item_units(P, o, per_item, i); });
+      if (lane == src) sum = all;
+    }
+    if (b0 + lane < P.t.batch) prefix[b0 + lane + 1] = sum;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    again += __shfl_xor_sync(0xffffffffu, again, o);
+    others += __shfl_xor_sync(0xffffffffu, others, o);
+  }
+  if (lane == 0) scratch[warp] = again, scratch[kWarps + warp] = others;
   __syncthreads();
-  again = 0;
-  for (int i = 0; i < kWarps; ++i) again += scratch[i];
+  if (warp == 0) paged_scan(P.t.batch, prefix);
+  __syncthreads();
+  again = others = 0;
+  for (int i = 0; i < kWarps; ++i) again += scratch[i], others += scratch[kWarps + i];
   Shares s;
   s.per_head = prefix[P.t.batch];
   s.all = s.per_head * P.t.heads_kv;
+  s.ctas = (int)gridDim.x;
+  if (others > 0) s.ctas = ctas_beside(s.all, (double)others * P.t.heads_kv * P.row_bytes * 2, s.ctas);
   // (rounds of 32 tiles a share at least: below that the parts cost more than the reads)
-  const int64_t rounds = max((int64_t)1, min(min((int64_t)P.rounds, s.all / (32 * (int64_t)gridDim.x)),
+  const int64_t rounds = max((int64_t)1, min(min((int64_t)P.rounds, s.all / (32 * (int64_t)s.ctas)),
                                              again * P.t.heads_kv * P.row_bytes * 2 / kRoundBytes));
-  s.count = (int)max((int64_t)1, min(rounds * gridDim.x, s.all / kMinUnits));
+  s.count = (int)max((int64_t)1, min(rounds * s.ctas, s.all / kMinUnits));
   return s;
 }
 
@@ -154,7 +188,8 @@ __device__ void run_records(const PagedChunkParams& P, const Ctl& c, Record* rec
                             int per_tile, int lane) {
   const int per_item = 2 * per_tile;
   uint32_t u = 0;
-  for (int s = (int)blockIdx.x; s < sh.count; s += (int)gridDim.x) {
+  for (int s = (int)blockIdx.x; s < sh.count; s += sh.ctas) {
+    if (lane == 0) P.joins[s] = {0, 0, 0, 0};  // nothing to join, so far
     int64_t x = sh.begin(s);
     const int64_t x1 = sh.begin(s + 1);
     int b = -1, head = 0, i = 0;
@@ -248,28 +283,36 @@ __device__ void run_producer(const PagedChunkParams& P, const Ctl& c, uint32_t s
   const int piece = P.piece, pieces = kTile / piece;
   const int rows_all = P.t.pages * 2 * P.t.heads_kv * P.t.page_rows;  // the first row that reads as zeros
   const uint32_t q_bytes = (uint32_t)(per_tile * P.group * D * 2);
+  const uint64_t keep = ptx::l2_policy_evict_last();  // the items of a sequence read the same keys and values
   uint32_t tile = 0;
   for (uint32_t u = 0;; ++u) {
     const Record* r = next_record(c, recs, u, kStatusTimeoutProducer);
     if (r == nullptr) return;
-    // Lane p brings piece p: its page's row of keys, or the row of zeros.
-    auto row_at = [&](int k, uint32_t& bad) {
-      const int j = r->at(k) * kTile + lane * piece;
-      bool want = lane < pieces && ((j < r->span.hi && j + piece > r->span.lo) || j < r->span.sink);
-      int y = rows_all;
-      if (want) {
-        const int page = paged_page(P.t, r->b, j / P.t.page_rows);
-        if (page >= 0) y = (int)paged_row(P.t, page, 0, r->head, j % P.t.page_rows);
-      }
-      bad = __ballot_sync(0xffffffffu, want && y == rows_all);
-      return y;
+    // The pages of the next 32 pieces, a lane each, read a group of tiles ahead (under load a read
+    // takes longer than a tile).
+    const int group = 32 / pieces, end = r->k0 + r->n;  // tiles of a group
+    bool want;
+    auto read = [&](int k) {
+      k += lane / pieces;
+      const int j = k < end ? r->at(k) * kTile + lane % pieces * piece : 0;
+      want = k < end && ((j < r->span.hi && j + piece > r->span.lo) || j < r->span.sink);  // somebody sees it
+      return want ? __ldg(P.t.page_table + r->b * P.t.width + j / P.t.page_rows) : -1;
     };
-    uint32_t bad;
-    int y = row_at(r->k0, bad);
-    for (int k = r->k0; k < r->k0 + r->n; ++k, ++tile) {
-      const int y_now = y;
-      const uint32_t bad_now = bad;
-      if (k + 1 < r->k0 + r->n) y = row_at(k + 1, bad);
+    int page_next = read(r->k0), rows = 0;
+    uint32_t bad = 0u;
+    for (int k = r->k0; k < end; ++k, ++tile) {
+      const int at = (k - r->k0) % group;
+      if (at == 0) {
+        // A lane's row of keys, or the row of zeros.
+        const int mine = k + lane / pieces, j = mine < end ? r->at(mine) * kTile + lane % pieces * piece : 0;
+        const bool there = page_next >= 0 && page_next < P.t.pages;
+        if (want && !there) atomicOr(P.t.status, kPagedStatusRange);
+        bad = __ballot_sync(0xffffffffu, want && !there);
+        rows = there ? (int)paged_row(P.t, page_next, 0, r->head, j % P.t.page_rows) : rows_all;
+        page_next = read(k + group);
+      }
+      const int y_now = __shfl_sync(0xffffffffu, rows, at * pieces + lane % pieces);
+      const uint32_t bad_now = (bad >> (at * pieces)) & ((1u << pieces) - 1u);
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         const uint32_t s = st.kv_issued % kStages, use = st.kv_issued / kStages;
@@ -282,8 +325,8 @@ __device__ void run_producer(const PagedChunkParams& P, const Ctl& c, uint32_t s
         ptx::mbar_arrive_expect_tx_warp(c.bar(kKVFull + (int)s), S::kTileBytes);
         __syncwarp();
         if (lane < pieces) {
-          ptx::tma_load_2d(dst, tkv, c.bar(kKVFull + (int)s), 0, row);
-          if (D == 128) ptx::tma_load_2d(dst + S::kHalf, tkv, c.bar(kKVFull + (int)s), 64, row);
+          tma_load_2d_hint(dst, tkv, c.bar(kKVFull + (int)s), 0, row, keep);
+          if (D == 128) tma_load_2d_hint(dst + S::kHalf, tkv, c.bar(kKVFull + (int)s), 64, row, keep);
         }
         __syncwarp();
         ++st.kv_issued;
@@ -651,11 +694,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per_tile = kTile / P.group;
 
   next_may_come();
-  // Shares that cut no item leave nothing to join.
-  for (int s = (int)blockIdx.x + threadIdx.x * gridDim.x; s < P.rounds * (int)gridDim.x; s += kThreads * gridDim.x)
-    P.joins[s] = {0, 0, 0, 0};
   const Shares sh = shares_of(P, 2 * per_tile, prefix, reinterpret_cast<int64_t*>(sgen + S::kOffOut));
-  if (sh.all == 0 || (int)blockIdx.x >= sh.count) return;
+  // Shares that there are none of leave nothing to join.
+  for (int s = (int)blockIdx.x + threadIdx.x * gridDim.x; s < P.rounds * (int)gridDim.x; s += kThreads * gridDim.x)
+    if (sh.all == 0 || s >= sh.count) P.joins[s] = {0, 0, 0, 0};
+  if (sh.all == 0 || (int)blockIdx.x >= min(sh.ctas, sh.count)) return;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kItemSlots; ++s) {
@@ -745,61 +788,96 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_chunk_join_kernel(const
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = (int)blockIdx.y >> 2, in_tile = ((int)blockIdx.y & 3) * 32 + lane;  // this lane's row of both tiles
   const int token = in_tile / P.group;
-  for (int s = (int)blockIdx.x; s < shares; s += (int)gridDim.x) {
-    const PagedJoin rec = P.joins[s];
+  PagedJoin recs[kMaxRounds];  // (all at once: most shares have nothing to join)
+#pragma unroll
+  for (int i = 0; i < kMaxRounds; ++i) {
+    const int s = (int)blockIdx.x + i * (int)gridDim.x;
+    recs[i] = s < shares ? P.joins[s] : PagedJoin{0, 0, 0, 0};
+  }
+#pragma unroll 1
+  for (int k = 0; k < kMaxRounds; ++k) {
+    const int s = (int)blockIdx.x + k * (int)gridDim.x;
+    PagedJoin rec = recs[0];
+#pragma unroll
+    for (int i = 1; i < kMaxRounds; ++i)
+      if (i == k) rec = recs[i];
     if (rec.tokens == 0) continue;
     const int count = rec.last - s + 1;
     const bool live = token < per_tile && g * per_tile + token < rec.tokens;
-    if (__syncthreads_or(live) == 0) continue;
     auto row_of = [&](int i) { return ((i == 0 ? 2 * s + 1 : 2 * (s + i)) * 2 + g) * kTile + in_tile; };
-    float m = -INFINITY;
-    for (int i = warp; i < count; i += kJoinWarps)
-      if (live) m = fmaxf(m, P.part_ml[row_of(i)].x);
-    tops[warp][lane] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) m = fmaxf(m, tops[i][lane]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float2 lf = make_float2(0.f, 0.f);  // the sum, its correction
-    for (int i = warp; i < count; i += kJoinWarps)
-      if (live) {
-        const float4 ml = P.part_ml[row_of(i)];
-        const float f = exp2f(ml.x - ref);
-        lf.x = fmaf(ml.y, f, lf.x);
-        lf.y = fmaf(ml.z, f, lf.y);
-      }
-    sums[warp][lane] = lf;
-    __syncthreads();
-    lf = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) lf.x += sums[i][lane].x, lf.y += sums[i][lane].y;
-    const float l = lf.x, inv = l == 0.f ? 0.f : 1.0f / (l + lf.y);
     const int at = rec.token + g * per_tile + token, head = rec.head * P.group + in_tile - token * P.group;
     constexpr int kCols = D / 4 / kJoinWarps;  // column groups of a warp
+    const float4* parts = reinterpret_cast<const float4*>(P.part_o) + (int64_t)(warp * kCols) * kTile + in_tile;
+    auto part = [&](int i, int q) { return parts[(int64_t)(row_of(i) >> 7) * (D / 4) * kTile + q * kTile]; };
+    float m = -INFINITY;
+    float2 lf = make_float2(0.f, 0.f);  // the sum, its correction
     float4 x[kCols];
 #pragma unroll
     for (int q = 0; q < kCols; ++q) x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-#pragma unroll 4
-      for (int i = 0; i < count; ++i) {
-        const int row = row_of(i);
-        const float f = exp2f(P.part_ml[row].x - ref);
+    auto add = [&](float4& a, const float4& y, float f) {
+      a.x = fmaf(y.x, f, a.x), a.y = fmaf(y.y, f, a.y), a.z = fmaf(y.z, f, a.z), a.w = fmaf(y.w, f, a.w);
+    };
+    constexpr int kFew = 4;
+    if (count <= kFew) {  // the usual case: everything is read at once
+      float4 ml[kFew], y[kFew][kCols];
 #pragma unroll
-        for (int q = 0; q < kCols; ++q) {
-          const float4 y =
-              reinterpret_cast<const float4*>(P.part_o)[((int64_t)(row >> 7) * (D / 4) + warp * kCols + q) * kTile + in_tile];
-          x[q].x = fmaf(y.x, f, x[q].x), x[q].y = fmaf(y.y, f, x[q].y);
-          x[q].z = fmaf(y.z, f, x[q].z), x[q].w = fmaf(y.w, f, x[q].w);
+      for (int i = 0; i < kFew; ++i)
+        if (live && i < count) {
+          ml[i] = P.part_ml[row_of(i)];
+#pragma unroll
+          for (int q = 0; q < kCols; ++q) y[i][q] = part(i, q);
+        }
+#pragma unroll
+      for (int i = 0; i < kFew; ++i)
+        if (live && i < count) m = fmaxf(m, ml[i].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i)
+        if (live && i < count) {
+          const float f = exp2f(ml[i].x - ref);
+          lf.x = fmaf(ml[i].y, f, lf.x);
+          lf.y = fmaf(ml[i].z, f, lf.y);
+#pragma unroll
+          for (int q = 0; q < kCols; ++q) add(x[q], y[i][q], f);
+        }
+    } else {
+      for (int i = warp; i < count; i += kJoinWarps)
+        if (live) m = fmaxf(m, P.part_ml[row_of(i)].x);
+      tops[warp][lane] = m;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kJoinWarps; ++i) m = fmaxf(m, tops[i][lane]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      for (int i = warp; i < count; i += kJoinWarps)
+        if (live) {
+          const float4 ml = P.part_ml[row_of(i)];
+          const float f = exp2f(ml.x - ref);
+          lf.x = fmaf(ml.y, f, lf.x);
+          lf.y = fmaf(ml.z, f, lf.y);
+        }
+      sums[warp][lane] = lf;
+      __syncthreads();
+      lf = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kJoinWarps; ++i) lf.x += sums[i][lane].x, lf.y += sums[i][lane].y;
+      if (live) {
+#pragma unroll 4
+        for (int i = 0; i < count; ++i) {
+          const float f = exp2f(P.part_ml[row_of(i)].x - ref);
+#pragma unroll
+          for (int q = 0; q < kCols; ++q) add(x[q], part(i, q), f);
         }
       }
-      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.o) + at * P.os.token + head * P.os.head + warp * kCols * 4);
-#pragma unroll
-      for (int q = 0; q < kCols; ++q)
-        dst[q] = make_uint2(ptx::pack_bf16x2(x[q].x * inv, x[q].y * inv), ptx::pack_bf16x2(x[q].z * inv, x[q].w * inv));
-      if (warp == 0 && P.lse != nullptr)
-        P.lse[(int64_t)at * P.heads_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      __syncthreads();  // (the shared memory is free for the next item)
     }
-    __syncthreads();
+    if (!live) continue;
+    const float l = lf.x, inv = l == 0.f ? 0.f : 1.0f / (l + lf.y);
+    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.o) + at * P.os.token + head * P.os.head + warp * kCols * 4);
+#pragma unroll
+    for (int q = 0; q < kCols; ++q)
+      dst[q] = make_uint2(ptx::pack_bf16x2(x[q].x * inv, x[q].y * inv), ptx::pack_bf16x2(x[q].z * inv, x[q].w * inv));
+    if (warp == 0 && P.lse != nullptr)
+      P.lse[(int64_t)at * P.heads_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -819,8 +897,6 @@ cudaError_t launch(const PagedChunkParams& prm, int grid, cudaStream_t stream, c
   if (e != cudaSuccess) return e;
   paged_chunk_kernel<D><<<grid, kThreads, Smem<D>::kFixed + (prm.t.batch + 1) * 8, stream>>>(tq, tkv, prm);
   e = cudaGetLastError();
-  if (e == cudaSuccess)
-    e = launch_behind(paged_chunk_join_kernel<D>, dim3((unsigned)grid, 8), kJoinWarps * 32, 0, stream, prm, grid * (int)prm.rounds);
   if (e != cudaSuccess) *why = "launch failed";
   return e;
 }
@@ -829,6 +905,13 @@ cudaError_t launch(const PagedChunkParams& prm, int grid, cudaStream_t stream, c
 
 cudaError_t launch_paged_chunk(int head_dim, const PagedChunkParams& prm, int grid, cudaStream_t stream, const char** why) {
   return head_dim == 128 ? launch<128>(prm, grid, stream, why) : launch<64>(prm, grid, stream, why);
+}
+
+cudaError_t launch_paged_chunk_join(int head_dim, const PagedChunkParams& prm, int grid, cudaStream_t stream) {
+  const dim3 blocks((unsigned)grid, 8);
+  const int shares = grid * prm.rounds;
+  return head_dim == 128 ? launch_behind(paged_chunk_join_kernel<128>, blocks, kJoinWarps * 32, 0, stream, prm, shares)
+                         : launch_behind(paged_chunk_join_kernel<64>, blocks, kJoinWarps * 32, 0, stream, prm, shares);
 }
 
 }  // namespace ra

@@ -52,6 +52,7 @@ struct PagedAttendParams {
   void* o;
   PagedStrides qs, os;
   float* lse;        // [tokens, heads_q] or nullptr
+  int32_t beside;    // a chunk kernel may still run: this one ends after it
   float* part_o;     // [head, slot, 2, kRowsTile, d]
   float2* part_ml;   // [head, slot, 2, kRowsTile]: running maximum (log2 units) and sum
   int4* joins;       // [head, slot]: first query row, rows, last slot of an item cut here (rows 0: none)
@@ -130,8 +131,11 @@ struct PagedEvictParams {
 };
 
 cudaError_t launch_paged_append(int dtype, const PagedAppendParams& prm, int sm_count, cudaStream_t stream);
-cudaError_t launch_paged_rows(int dtype, int head_dim, const PagedAttendParams& prm, cudaStream_t stream);
+// beside: the kernel starts while the chunk kernel before it in the stream runs.
+cudaError_t launch_paged_rows(int dtype, int head_dim, const PagedAttendParams& prm, bool beside, cudaStream_t stream);
+cudaError_t launch_paged_rows_join(int dtype, int head_dim, const PagedAttendParams& prm, cudaStream_t stream);
 cudaError_t launch_paged_chunk(int head_dim, const PagedChunkParams& prm, int grid, cudaStream_t stream, const char** why);
+cudaError_t launch_paged_chunk_join(int head_dim, const PagedChunkParams& prm, int grid, cudaStream_t stream);
 cudaError_t launch_paged_weigh_rows(int dtype, int head_dim, const PagedWeighParams& prm, int sm_count,
                                     cudaStream_t stream);
 cudaError_t launch_paged_weigh_chunk(int head_dim, const PagedWeighChunkParams& prm, int grid, cudaStream_t stream,

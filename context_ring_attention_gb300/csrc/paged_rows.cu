@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "paged_share.cuh"
 #include "sm100_ptx.cuh"
@@ -51,6 +52,12 @@ __device__ __forceinline__ void ldmatrix4t(uint32_t (&r)[4], uint32_t addr) {
 // 16 bytes from global to shared memory, asynchronously; zeros where !live.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+// The same, with an L2 policy.
+__device__ __forceinline__ void copy16_hint(uint32_t dst, const void* src, bool live, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0),
+               "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
@@ -133,6 +140,12 @@ __device__ __forceinline__ int64_t part_at(const PagedAttendParams& P, const Wal
   return me * 2 + 1;
 }
 
+// Where this kernel runs beside a chunk kernel: its end, that of one CTA of it, has to come after
+// the other's, so that what waits for this one finds both done.
+__device__ __forceinline__ void end_after_others(const PagedAttendParams& P) {
+  if (P.beside && blockIdx.x == 0 && blockIdx.y == 0) after_previous();
+}
+
 // Where row `row` (over the tokens' groups) of this head lies.
 template <typename T>
 __device__ __forceinline__ T* row_of(const PagedStrides& s, const void* base, int group, int head, int row) {
@@ -160,10 +173,12 @@ __global__ void __launch_bounds__(kThreads) rows_bf16_kernel(const PagedAttendPa
   next_may_come();
   if (P.joins != nullptr && threadIdx.x == 0) P.joins[(int64_t)head * P.slots + blockIdx.x] = make_int4(0, 0, 0, 0);
   Walk w;
-  if (!walk_begin<__nv_bfloat16>(P, prefix, w)) return;
+  if (!walk_begin<__nv_bfloat16>(P, prefix, w)) return end_after_others(P);
 
   const uint32_t ring = ptx::smem_addr(smem) + warp * kStages * 2 * G::kBlockBytes;
-  const __nv_bfloat16* cache = static_cast<const __nv_bfloat16*>(P.t.cache);
+  const uint8_t* lane_src = static_cast<const uint8_t*>(P.t.cache) + lane / G::kChunks * G::kRowBytes + lane % G::kChunks * 16;
+  const int64_t to_v = (int64_t)P.t.heads_kv * P.t.page_rows * G::kRowBytes;  // from a key's row to its value's
+  const uint64_t once = ptx::l2_policy_evict_first();  // (a chunk kernel beside this one keeps its keys in the L2)
   const int quad = lane >> 2, two = (lane & 3) * 2;
   float* sums = reinterpret_cast<float*>(smem);
   float2* stats = reinterpret_cast<float2*>(sums + kWarps * kRowsTile * G::kJoinRow);
@@ -200,43 +215,59 @@ __global__ void __launch_bounds__(kThreads) rows_bf16_kernel(const PagedAttendPa
       for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    // Block i of this warp into its ring; a lane keeps the page of one of the next 32.
-    int pages = -1;
-    uint32_t bad = 0u;  // stages whose page is none
+    // Block i of this warp into its ring, and its first slot.  A lane knows one of the next 32
+    // blocks: what it takes to find them is done once for all.
+    int known_j = 0, known_row = -1;  // first slot; row of the cache (-1: the page is none)
+    bool known_full = false;          // some token sees every slot of the block
+    uint32_t bad = 0u;                // stages whose page is none
     auto load = [&](int i) {
-      if ((i & 31) == 0) {
+      if ((i & 31) == 0 && i < mine) {
         const int k = u0 + warp + (i + lane) * kWarps;
-        pages = i + lane < mine ? paged_page(P.t, w.b, blocks.at(k) * kRowsBlock / P.t.page_rows) : -1;
-      }
-      if (i < mine) {
-        const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-        const int j0 = blocks.at(u0 + warp + i * kWarps) * kRowsBlock, s = i % kStages;
-        bad = page < 0 ? bad | (1u << s) : bad & ~(1u << s);
-        const int64_t row0 = paged_row(P.t, max(page, 0), 0, head, j0 % P.t.page_rows);
-        RA_BOUNDS(P.t.status, row0 >= 0 && row0 + kRowsBlock <= (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 111);
-        const int64_t to_v = (int64_t)P.t.heads_kv * P.t.page_rows * D;
-        const uint32_t dst = ring + s * 2 * G::kBlockBytes;
-#pragma unroll
-        for (int x = 0; x < G::kChunks / 2; ++x) {
-          const int id = lane + 32 * x, r = id / G::kChunks, ch = id % G::kChunks;
-          const bool live = page >= 0 && span.holds(j0 + r);
-          const __nv_bfloat16* src = cache + (row0 + r) * D + ch * 8;
-          const uint32_t to = dst + r * G::kRowBytes + ((ch ^ (r & 7)) * 16);
-          copy16(to, src, live);
-          copy16(to + G::kBlockBytes, src + to_v, live);
+        known_row = -1;
+        if (i + lane < mine) {
+          known_j = blocks.at(k) * kRowsBlock;
+          const int page = paged_page(P.t, w.b, known_j / P.t.page_rows);
+          if (page >= 0) known_row = (int)paged_row(P.t, page, 0, head, known_j % P.t.page_rows);
+          known_full = page >= 0 && ((known_j >= span.lo && known_j + kRowsBlock <= span.hi) || known_j + kRowsBlock <= span.sink);
         }
       }
-      copies_commit();
-    };
+      const int j0 = __shfl_sync(0xffffffffu, known_j, i & 31);
+      if (i < mine) {
+        const int row0 = __shfl_sync(0xffffffffu, known_row, i & 31), s = i % kStages;
+        const bool full = __shfl_sync(0xffffffffu, known_full, i & 31);
+        bad = row0 < 0 ? bad | (1u << s) : bad & ~(1u << s);
+        RA_BOUNDS(P.t.status, row0 >= -1 && row0 + kRowsBlock <= (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 111);
+        const uint8_t* src = lane_src + (int64_t)max(row0, 0) * G::kRowBytes;
+        const uint32_t dst = ring + s * 2 * G::kBlockBytes;
+        auto copies = [&](auto whole) {
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) load(i);
+          for (int x = 0; x < G::kChunks / 2; ++x) {
+            constexpr int kStep = 32 / G::kChunks;  // rows
+            const int r = x * kStep + lane / G::kChunks, ch = lane % G::kChunks;
+            const bool live = decltype(whole)::value || (row0 >= 0 && span.holds(j0 + r));
+            const uint32_t to = dst + r * G::kRowBytes + ((ch ^ (r & 7)) * 16);
+            copy16_hint(to, src + x * kStep * G::kRowBytes, live, once);
+            copy16_hint(to + G::kBlockBytes, src + to_v + x * kStep * G::kRowBytes, live, once);
+          }
+        };
+        if (full) copies(std::true_type());
+        else copies(std::false_type());
+      }
+      copies_commit();
+      return j0;
+    };
+    int ahead[kStages - 1];  // first slots of the blocks under way
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) ahead[i] = load(i);
     for (int i = 0; i < mine; ++i) {
       copies_wait<kStages - 2>();
       __syncwarp();
-      load(i + kStages - 1);
+      const int j0 = ahead[0];
+#pragma unroll
+      for (int e = 0; e + 1 < kStages - 1; ++e) ahead[e] = ahead[e + 1];
+      ahead[kStages - 2] = load(i + kStages - 1);
       const int st = i % kStages;
       const uint32_t kb = ring + st * 2 * G::kBlockBytes, vb = kb + G::kBlockBytes;
-      const int j0 = blocks.at(u0 + warp + i * kWarps) * kRowsBlock;
       // Scores: rows x 16 keys, as two products of 8 keys.
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       const int kr = (lane & 7) + ((lane >> 4) << 3);  // key of this lane's address; its half of 16 channels:
@@ -354,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) rows_bf16_kernel(const PagedAttendPa
     }
     __syncthreads();  // the ring is free for the next item
     w.x = w.item_x + (w.whole ? 1 : u1);
-    if (w.x >= w.x1) return;
+    if (w.x >= w.x1) return end_after_others(P);
   }
 }
 
@@ -584,30 +615,41 @@ cudaError_t raise_smem(Kernel kernel, std::atomic<int>* ready, int bytes) {
 }
 
 template <typename T, int D>
-cudaError_t launch(const PagedAttendParams& prm, cudaStream_t stream) {
+cudaError_t launch(const PagedAttendParams& prm, bool beside, cudaStream_t stream) {
   const dim3 grid((unsigned)prm.slots, (unsigned)prm.t.heads_kv);
   const int prefix = (prm.t.batch + 1) * 8, most = (kMaxSequences + 1) * 8;
   static std::atomic<int> ready[kMaxDevices];
   if constexpr (sizeof(T) == 2) {
     const cudaError_t e = raise_smem(rows_bf16_kernel<D>, ready, Bf16<D>::kRing + most);
     if (e != cudaSuccess) return e;
+    if (beside) return launch_behind(rows_bf16_kernel<D>, grid, kThreads, Bf16<D>::kRing + prefix, stream, prm);
     rows_bf16_kernel<D><<<grid, kThreads, Bf16<D>::kRing + prefix, stream>>>(prm);
   } else {
     const cudaError_t e = raise_smem(rows_f32_kernel<D>, ready, F32<D>::kBytes + most);
     if (e != cudaSuccess) return e;
     rows_f32_kernel<D><<<grid, kThreads, F32<D>::kBytes + prefix, stream>>>(prm);
   }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || prm.slots == 1) return e;
+  return cudaGetLastError();
+}
+template <typename T, int D>
+cudaError_t launch_join(const PagedAttendParams& prm, cudaStream_t stream) {
+  if (prm.slots == 1) return cudaSuccess;
+  const dim3 grid((unsigned)prm.slots, (unsigned)prm.t.heads_kv);
   return launch_behind(rows_join_kernel<T, D>, grid, kRowsTile * 32, (size_t)prm.slots * kRowsTile * 4, stream, prm);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_rows(int dtype, int head_dim, const PagedAttendParams& prm, cudaStream_t stream) {
+cudaError_t launch_paged_rows(int dtype, int head_dim, const PagedAttendParams& prm, bool beside, cudaStream_t stream) {
   if (dtype == RA_DTYPE_BF16)
-    return head_dim == 128 ? launch<__nv_bfloat16, 128>(prm, stream) : launch<__nv_bfloat16, 64>(prm, stream);
-  return head_dim == 128 ? launch<float, 128>(prm, stream) : launch<float, 64>(prm, stream);
+    return head_dim == 128 ? launch<__nv_bfloat16, 128>(prm, beside, stream) : launch<__nv_bfloat16, 64>(prm, beside, stream);
+  return head_dim == 128 ? launch<float, 128>(prm, beside, stream) : launch<float, 64>(prm, beside, stream);
+}
+
+cudaError_t launch_paged_rows_join(int dtype, int head_dim, const PagedAttendParams& prm, cudaStream_t stream) {
+  if (dtype == RA_DTYPE_BF16)
+    return head_dim == 128 ? launch_join<__nv_bfloat16, 128>(prm, stream) : launch_join<__nv_bfloat16, 64>(prm, stream);
+  return head_dim == 128 ? launch_join<float, 128>(prm, stream) : launch_join<float, 64>(prm, stream);
 }
 
 }  // namespace ra

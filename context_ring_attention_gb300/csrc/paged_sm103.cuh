@@ -59,6 +59,16 @@ __device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// As ptx::tma_load_2d, with an L2 policy.
+__device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+
 // Prefix sums over a batch, of what `own(b)` says of a sequence (a whole warp calls it and agrees):
 // prefix[b] of the sequences before b.  Every thread of the CTA calls it; it ends with a barrier.
 template <int kWarps, typename Own>

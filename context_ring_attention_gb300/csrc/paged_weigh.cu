@@ -118,7 +118,6 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
   slot_prefix<kStepKeys>(P.t, P.group, prefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
   const int quad = lane >> 2, two = (lane & 3) * 2;
-  const __nv_bfloat16* cache = static_cast<const __nv_bfloat16*>(P.t.cache);
   const int64_t all = prefix[P.t.batch], me = (int64_t)blockIdx.x * kWarps + warp, runs = (int64_t)gridDim.x * kWarps;
   const int64_t x0 = all * me / runs;
   const int n = (int)(all * (me + 1) / runs - x0);
@@ -131,12 +130,14 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
   }
   while (prefix[b_first + 1] <= x0) ++b_first;
 
-  // Block i of the run into the ring; a lane knows sequence, slot and page of one of the next 32.
-  int known_b = b_first, known_j = 0, known_page[2] = {-1, -1};
+  // Step i of the run into the ring; a lane knows one of the next 32: what it takes to find them is
+  // done once for all.
+  int known_b = b_first, known_j = 0, known_row[2] = {-2, -2};  // rows of the cache; -1: the page is none, -2: nobody sees it
+  const uint8_t* lane_src = static_cast<const uint8_t*>(P.t.cache) + lane / kChunks * kRowBytes + lane % kChunks * 16;
   uint32_t bad = 0u;  // blocks of the stages whose page is none
   auto load = [&](int i) {
     if ((i & 31) == 0 && i < n) {
-      int b = __shfl_sync(0xffffffffu, known_b, 31);  // (the last block known so far)
+      int b = __shfl_sync(0xffffffffu, known_b, 31);  // (the last step known so far)
       if (i == 0) b = b_first;
       const int64_t x = min(x0 + i + lane, x0 + n - 1);
       while (prefix[b + 1] <= x) ++b;
@@ -144,11 +145,14 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
       known_j = (int)(x - prefix[b]) * kStepKeys;
       const Rows<__nv_bfloat16> rows{P, paged_seq(P.t, b), head};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {  // a page of either block
+      for (int e = 0; e < 2; ++e) {
         const int j = known_j + e * kRowsBlock;
+        known_row[e] = -2;
         // (of a block the first slot or the last one is seen, or none)
-        const bool look = j < rows.seq.length && (rows.seen(j) || rows.seen(min(j + kRowsBlock, rows.seq.length) - 1));
-        known_page[e] = look ? paged_page(P.t, b, j / P.t.page_rows) : -2;
+        if (j < rows.seq.length && (rows.seen(j) || rows.seen(min(j + kRowsBlock, rows.seq.length) - 1))) {
+          const int page = paged_page(P.t, b, j / P.t.page_rows);
+          known_row[e] = page < 0 ? -1 : (int)paged_row(P.t, page, 0, head, j % P.t.page_rows);
+        }
       }
     }
     if (i < n) {
@@ -157,15 +161,16 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
       const uint32_t dst = ring + s * kStageBytes;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int page = __shfl_sync(0xffffffffu, known_page[e], i & 31), j = j0 + e * kRowsBlock;
+        const int row0 = __shfl_sync(0xffffffffu, known_row[e], i & 31);
         const uint32_t bit = 1u << (2 * s + e);
-        bad = page == -1 ? bad | bit : bad & ~bit;
-        const int64_t row0 = paged_row(P.t, max(page, 0), 0, head, j % P.t.page_rows);
-        RA_BOUNDS(P.t.status, row0 >= 0 && row0 + kRowsBlock <= (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 115);
+        bad = row0 == -1 ? bad | bit : bad & ~bit;
+        RA_BOUNDS(P.t.status, row0 >= -2 && row0 + kRowsBlock <= (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 115);
+        const uint8_t* src = lane_src + (int64_t)max(row0, 0) * kRowBytes;
 #pragma unroll
         for (int x = 0; x < kChunks / 2; ++x) {
-          const int id = lane + 32 * x, r = id / kChunks, ch = id % kChunks;
-          copy16(dst + (e * kRowsBlock + r) * kRowBytes + ((ch ^ (r & 7)) * 16), cache + (row0 + r) * D + ch * 8, page >= 0);
+          constexpr int kStep = 32 / kChunks;  // rows
+          const int r = x * kStep + lane / kChunks, ch = lane % kChunks;
+          copy16(dst + (e * kRowsBlock + r) * kRowBytes + ((ch ^ (r & 7)) * 16), src + x * kStep * kRowBytes, row0 >= 0);
         }
       }
       {
