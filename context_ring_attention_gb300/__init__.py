@@ -881,7 +881,21 @@ def ra_rope_destroy(rope):
     rope.close()
 
 
-_I64x2, _I64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+_ARRAYS = {}  # strides -> the host array that the library takes
+
+
+def _array(*strides):
+    a = _ARRAYS.get(strides)
+    if a is None:
+        if len(_ARRAYS) > 4096:
+            _ARRAYS.clear()
+        a = _ARRAYS[strides] = (ctypes.c_int64 * len(strides))(*strides)
+    return a
+
+
+def _new_like(t):
+    """A contiguous tensor of t's shape and type."""
+    return _TORCH.empty_like(t, memory_format=_TORCH.contiguous_format)
 
 
 def _bad_rows(name, shape, dtype, device):
@@ -896,7 +910,7 @@ def _rows4(name, t, shape, dtype, device):
     a, b, c, e = t.stride()
     if e != 1 and shape[3] > 1:
         raise _bad_rows(name, shape, dtype, device)
-    return _I64x3(a if shape[0] > 1 else 0, b if shape[1] > 1 else 0, c if shape[2] > 1 else 0)
+    return _array(a if shape[0] > 1 else 0, b if shape[1] > 1 else 0, c if shape[2] > 1 else 0)
 
 
 def _rows3(name, t, shape, dtype, device):
@@ -906,7 +920,7 @@ def _rows3(name, t, shape, dtype, device):
     a, b, e = t.stride()
     if e != 1 and shape[2] > 1:
         raise _bad_rows(name, shape, dtype, device)
-    return _I64x2(a if shape[0] > 1 else 0, b if shape[1] > 1 else 0)
+    return _array(a if shape[0] > 1 else 0, b if shape[1] > 1 else 0)
 
 
 def _rope_call(call, rope, q, k, layout, n_shards, position, q_out, k_out, stream):
@@ -922,8 +936,8 @@ def _rope_call(call, rope, q, k, layout, n_shards, position, q_out, k_out, strea
         _need_like("position", position, (B, S), torch.int32, device)
     if q_out is None:
         with _alloc_on(stream):
-            q_out = torch.empty(shape, dtype=dtype, device=device)
-        qos = _I64x3(Hq * S * d, S * d, d)
+            q_out = _new_like(q)
+        qos = _array(Hq * S * d, S * d, d)
     else:
         qos = _rows4("q_out", q_out, shape, dtype, device)
     if k is None:
@@ -937,8 +951,8 @@ def _rope_call(call, rope, q, k, layout, n_shards, position, q_out, k_out, strea
     ks = _rows4("k", k, shape, dtype, device)
     if k_out is None:
         with _alloc_on(stream):
-            k_out = torch.empty(shape, dtype=dtype, device=device)
-        kos = _I64x3(Hk * S * d, S * d, d)
+            k_out = _new_like(k)
+        kos = _array(Hk * S * d, S * d, d)
     else:
         kos = _rows4("k_out", k_out, shape, dtype, device)
     _check(call(rope.handle, B, S, Hq, Hk, _layout(layout), int(n_shards), _ptr(position), q.data_ptr(), qs, k.data_ptr(), ks,
@@ -1049,7 +1063,7 @@ def ra_paged_append(kv, cache, k, v, page_table, offset, length, rope=None, posi
         qs = _rows3("q", q, shape, dtype, device)
         if q_out is None:
             with _alloc_on(stream):
-                q_out = torch.empty(shape, dtype=dtype, device=device)
+                q_out = _new_like(q)
         qos = _rows3("q_out", q_out, shape, dtype, device)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -1089,7 +1103,7 @@ def ra_paged_attend(kv, cache, q, page_table, offset, length, o=None, lse=None, 
         _need_like("lse", lse, (T, pb["heads_q"]), torch.float32, device)
     with _alloc_on(stream):
         if o is None:
-            o = torch.empty(shape, dtype=dtype, device=device)
+            o = _new_like(q)
         if lse is None:
             lse = torch.empty(shape[:2], dtype=torch.float32, device=device)
         if scratch is None and need:

@@ -126,11 +126,11 @@ struct Shares {
 };
 
 // CTAs of this kernel's, where the row kernel reads other sequences' keys beside it: the two then
-// end together.  A key tile takes a CTA 1.45 us; the reads take the time of their bytes at 6.6 TB/s
+// end together.  A key tile takes a CTA 1.4 us, beside the reads 1.7; the reads take the time of their bytes at 6.6 TB/s
 // if five eighths of the SMs are left to them, and longer in proportion if fewer are.  (One chunk of
 // 512 tokens and 31 single ones under a window of 8192: one kernel after the other 226 us.)
 __device__ __forceinline__ int ctas_beside(int64_t units, double bytes, int sms) {
-  const float work = 1.45f * (float)units, reads = (float)(bytes / 6.6e6);  // us
+  const float work = 1.7f * (float)units, reads = (float)(bytes / 6.6e6);  // us
   const float few = 0.375f * (float)sms, need = 0.625f * (float)sms;
   const float n = work <= few * reads ? 1.1f * work / reads + 1.f : (float)sms * work / (need * reads + work);
   return max(1, min(sms, (int)ceilf(n)));

@@ -257,8 +257,9 @@ def test_buffers_are_made_on_the_calls_stream(monkeypatch, name):
     monkeypatch.setattr(ra, "_on_current_device", lambda *a: None)
     for size in ("ra_paged_attend_scratch_size", "ra_paged_weigh_scratch_size"):
         monkeypatch.setattr(ra, size, lambda *a: 4096)
-    real = torch.empty
-    monkeypatch.setattr(torch, "empty", lambda *a, **kw: (made.append(bool(inside)), real(*a, **kw))[1])
+    for fn in ("empty", "empty_like"):
+        real = getattr(torch, fn)
+        monkeypatch.setattr(torch, fn, lambda *a, real=real, **kw: (made.append(bool(inside)), real(*a, **kw))[1])
     _binding_calls(kv, rope, t, stream)[name]()
     assert made and all(made)
 
