@@ -403,16 +403,18 @@ __device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, uint32_t 
       }
     }
     float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    // Query tiles [full0, full1) are seen by every key of the warp that is asked for, in every row:
+    // told once an item, as the sums are bound by the instructions of a tile.
+    int full0, full1;
+    {
+      const int top = __reduce_max_sync(0xffffffffu, mine ? j : 0);
+      const bool edge = mine && P.window > 0 && j >= P.sinks;
+      const int low = __reduce_min_sync(0xffffffffu, edge ? j : INT32_MAX);
+      full0 = top > slot0 ? (top - slot0 + per_tile - 1) / per_tile : 0;
+      full1 = count / per_tile;
+      if (low != INT32_MAX) full1 = (int)min((int64_t)full1, max((int64_t)0, (int64_t)low + P.window - slot0) / per_tile);
+    }
     for (int t = 0; t < n; ++t, ++tile) {
-      const int first = slot0 + (t0 + t) * per_tile;  // slot of the tile's first token
-      const int tokens = min(per_tile, count - (t0 + t) * per_tile);
-      // rows [c_lo, c_hi) see the key (keys that nobody asks for: all)
-      int c_lo = 0, c_hi = tokens * P.group;
-      if (mine) {
-        c_lo = clamped(j - first) * P.group;
-        if (P.window > 0 && j >= P.sinks) c_hi = min(c_hi, clamped((int64_t)j + P.window - first) * P.group);
-      }
-      const bool full = c_lo <= 0 && c_hi >= per_tile * P.group;
       const bool ok = wait_bar(c, c.bar(kSFull + g), tile & 1u, kStatusTimeoutSoftmax);
       if (!__all_sync(0xffffffffu, ok)) return;
       ptx::tc_fence_after();
@@ -423,6 +425,16 @@ __device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, uint32_t 
       if (lane == 0) ptx::mbar_arrive(c.bar(kSEmpty + g));  // (a warp's 32 arrivals would come one after the other)
       const float* s = reinterpret_cast<const float*>(raw);
       auto sums = [&](auto edge) {
+        int c_lo = 0, c_hi = 0;
+        if (decltype(edge)::value) {
+          // rows [c_lo, c_hi) see the key (keys that nobody asks for: all)
+          const int first = slot0 + (t0 + t) * per_tile;  // slot of the tile's first token
+          c_hi = min(per_tile, count - (t0 + t) * per_tile) * P.group;
+          if (mine) {
+            c_lo = clamped(j - first) * P.group;
+            if (P.window > 0 && j >= P.sinks) c_hi = min(c_hi, clamped((int64_t)j + P.window - first) * P.group);
+          }
+        }
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t bits = ~0u;
@@ -450,7 +462,7 @@ __device__ void run_sums(const PagedWeighChunkParams& P, const Ctl& c, uint32_t 
           }
         }
       };
-      if (__all_sync(0xffffffffu, full)) sums(std::false_type());
+      if (t0 + t >= full0 && t0 + t < full1) sums(std::false_type());
       else sums(std::true_type());
     }
     const float2 a = ptx::add2(ptx::add2(acc[0], acc[1]), ptx::add2(acc[2], acc[3]));
