@@ -37,7 +37,8 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
   return (x & 0x80000000u) ? ~x : x | 0x80000000u;
 }
 
-// Inclusive sums over the CTA's threads; all of them in `total`.  sums: 32 places.
+// Inclusive sums over the CTA's threads; all of them in `total`.  sums: 32 places that the scan
+// before did not have.  One barrier.
 __device__ __forceinline__ uint64_t scan(uint64_t x, uint64_t* sums, uint64_t& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -47,27 +48,22 @@ __device__ __forceinline__ uint64_t scan(uint64_t x, uint64_t* sums, uint64_t& t
   }
   if (lane == 31) sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    uint64_t s = sums[lane];
+  uint64_t s = sums[lane];  // (every warp adds the warps up for itself)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    sums[lane] = s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
   }
-  __syncthreads();
-  total = sums[31];
-  if (warp > 0) x += sums[warp - 1];
-  __syncthreads();
-  return x;
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const uint64_t before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+  return warp > 0 ? x + before : x;
 }
 
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictParams P, int known) {
   extern __shared__ __align__(16) float weights[];  // [known]
-  __shared__ uint32_t bins[kBins];
-  __shared__ uint64_t sums[32];
-  __shared__ uint32_t found[2];
+  __shared__ uint32_t bins[3][kBins];  // of each pass
+  __shared__ uint64_t sums[2][32];
+  __shared__ uint32_t found[3][2];
   __shared__ uint64_t own_count;  // of this CTA's slots: sure << 32 | ties
   next_may_come();
   cg::cluster_group cluster = cg::this_cluster();
@@ -97,6 +93,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictPara
   int s0 = (int)((int64_t)n * rank / ctas) & ~3, s1 = rank + 1 == ctas ? n : (int)((int64_t)n * (rank + 1) / ctas) & ~3;
   const bool in_smem = (n + ctas - 1) / ctas + 4 <= known;
   if (!in_smem && out == w) s0 = rank == 0 ? 0 : n, s1 = n;
+  for (int i = tid; i < 3 * kBins; i += kPickThreads) (&bins[0][0])[i] = 0u;
   if (in_smem)
     for (int j = s0 + tid; j < s1; j += kPickThreads) weights[j - s0] = w[j];
   auto weight_at = [&](int j) { return in_smem ? weights[j - s0] : w[j]; };
@@ -105,35 +102,35 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictPara
 
   // The lowest rank that stays, and how many slots of that very rank do.
   uint32_t prefix = 0u, left = (uint32_t)places;
+  __syncthreads();
   if (places > 0) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-      for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0u;
-      __syncthreads();
       for (int j = max(s0, lo) + tid; j < min(s1, hi); j += kPickThreads) {
         const uint32_t r = rank_of(weight_at(j));
-        if (pass == 0 || (r >> (shift + width)) == prefix) atomicAdd(&bins[(r >> shift) & ((1u << width) - 1u)], 1u);
+        if (pass == 0 || (r >> (shift + width)) == prefix) atomicAdd(&bins[pass][(r >> shift) & ((1u << width) - 1u)], 1u);
       }
-      cluster.sync();
+      if (ctas > 1) cluster.sync();
+      else __syncthreads();
       // From the highest bin down: the one in which `left` slots are reached.
       const int top = kBins - 1 - 2 * tid;
       uint32_t a = 0u, c = 0u;
       for (int i = 0; i < ctas; ++i) {
-        const uint32_t* other = cluster.map_shared_rank(bins, i);
-        a += other[top], c += other[top - 1];
+        const uint2 two = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&bins[pass][0], i) + top - 1);
+        a += two.y, c += two.x;
       }
       uint64_t total;
-      const uint64_t sum = scan((uint64_t)a + c, sums, total);
+      const uint64_t sum = scan((uint64_t)a + c, sums[pass & 1], total);
       const uint64_t before = sum - a - c;
       if (before < left && sum >= left) {
         const bool second = before + a < left;
-        found[0] = (uint32_t)(second ? top - 1 : top);
-        found[1] = (uint32_t)(left - before - (second ? a : 0u));
+        found[pass][0] = (uint32_t)(second ? top - 1 : top);
+        found[pass][1] = (uint32_t)(left - before - (second ? a : 0u));
       }
-      cluster.sync();  // (nobody reads these bins any more)
-      prefix = (prefix << width) | found[0];
-      left = found[1];
+      __syncthreads();
+      prefix = (prefix << width) | found[pass][0];
+      left = found[pass][1];
     }
   }
   // Slots that stay for certain, and those of the lowest rank, of which the first `left` do.
@@ -148,47 +145,53 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictPara
       tie = r == prefix;
     }
   };
-  uint64_t before = 0;
-  if (ctas > 1) {  // those of the CTAs before this one
-    uint64_t mine = 0, total;
-    for (int j = s0 + tid; j < s1; j += kPickThreads) {
-      bool sure, tie;
-      kinds(j, sure, tie);
-      mine += ((uint64_t)sure << 32) | (uint64_t)tie;
+  auto emit = [&](int j, bool sure, bool tie, float wj, uint32_t& s, uint32_t& t) {
+    if (sure || (tie && t < left)) {
+      const uint32_t to = s + min(t, left);
+      RA_BOUNDS(P.t.status, to < (uint32_t)P.keep, 118);
+      kept[to] = j;
+      if (out != nullptr) out[to] = wj;
     }
-    scan(mine, sums, total);
+    s += sure, t += tie;
+  };
+  // A thread has a run of slots, of an odd number so that a warp's reads fall into different banks.
+  const int own = ((s1 - s0 + kPickThreads - 1) / kPickThreads) | 1;
+  const int j0 = (int)min((int64_t)s0 + (int64_t)own * tid, (int64_t)s1), j1 = min(j0 + own, s1);
+  uint64_t mine = 0, total;
+  for (int j = j0; j < j1; ++j) {
+    bool sure, tie;
+    kinds(j, sure, tie);
+    mine += ((uint64_t)sure << 32) | (uint64_t)tie;
+  }
+  uint64_t before = scan(mine, sums[1], total) - mine;
+  if (ctas > 1) {  // those of the CTAs before this one
     if (tid == 0) own_count = total;
     cluster.sync();
     for (int i = 0; i < rank; ++i) before += *cluster.map_shared_rank(&own_count, i);
     cluster.sync();  // (no CTA leaves while another reads its count)
-  } else {
-    __syncthreads();
   }
-  constexpr int kOwn = 4;  // slots of a thread at a time
-  for (int64_t j0 = s0; j0 < s1; j0 += kOwn * kPickThreads) {
-    bool sure[kOwn], tie[kOwn];
-    float wj[kOwn];
-    uint64_t mine = 0, total;
-#pragma unroll
-    for (int e = 0; e < kOwn; ++e) {
-      const int64_t j = j0 + tid * kOwn + e;
-      kinds((int)min(j, (int64_t)s1), sure[e], tie[e]);
-      mine += ((uint64_t)sure[e] << 32) | (uint64_t)tie[e];
-      wj[e] = out != nullptr && j < s1 ? weight_at((int)j) : 0.f;
+  if (in_smem || out != w) {
+    uint32_t s = (uint32_t)(before >> 32), t = (uint32_t)before;
+    for (int j = j0; j < j1; ++j) {
+      bool sure, tie;
+      kinds(j, sure, tie);
+      emit(j, sure, tie, out != nullptr ? weight_at(j) : 0.f, s, t);
     }
-    // (ends with barriers: the step's weights are read before any is written)
-    const uint64_t sum = before + scan(mine, sums, total) - mine;
+    return;
+  }
+  // In place, more weights than shared memory holds (one CTA has them all): in order, a step's
+  // weights read before any is written.
+  before = 0;
+  for (int64_t step = s0; step < s1; step += kPickThreads) {
+    const int j = (int)min(step + tid, (int64_t)s1);
+    bool sure, tie;
+    kinds(j, sure, tie);
+    const float wj = j < s1 ? weight_at(j) : 0.f;
+    const uint64_t one = ((uint64_t)sure << 32) | (uint64_t)tie;
+    __syncthreads();  // (the scan before has been read)
+    const uint64_t sum = before + scan(one, sums[0], total) - one;
     uint32_t s = (uint32_t)(sum >> 32), t = (uint32_t)sum;
-#pragma unroll
-    for (int e = 0; e < kOwn; ++e) {
-      if (sure[e] || (tie[e] && t < left)) {
-        const uint32_t to = s + min(t, left);
-        RA_BOUNDS(P.t.status, to < (uint32_t)P.keep, 118);
-        kept[to] = (int32_t)(j0 + tid * kOwn + e);
-        if (out != nullptr) out[to] = wj[e];
-      }
-      s += sure[e], t += tie[e];
-    }
+    emit(j, sure, tie, wj, s, t);
     before += total;
   }
 }
