@@ -431,21 +431,30 @@ __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendPar
           ? __ldg(reinterpret_cast<const float4*>(row_of<const float>(P.qs, P.q, P.group, head, row0 + r)) + ch)
           : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    // Slot of key i of a step; -1 past the share's end.
-    auto slot_of = [&](int step, int i) {
-      const int k = u0 + 2 * step + (i >> 4);
-      return k < n_live ? blocks.at(k) * kRowsBlock + (i & 15) : -1;
+    // Slot and row of the cache of this lane's key of a step; row -1: past the share's end, a slot
+    // that no token sees, or a page that is none.  Read a step ahead.
+    auto find = [&](int step, int& j, int& row) {
+      const int k = u0 + 2 * step + (lane >> 4);
+      j = k < n_live ? blocks.at(k) * kRowsBlock + (lane & 15) : 0;
+      row = -1;
+      if (k < n_live && span.holds(j)) {
+        const int page = paged_page(P.t, w.b, j / P.t.page_rows);
+        if (page >= 0) row = (int)paged_row(P.t, page, 0, head, j % P.t.page_rows);
+      }
+      RA_BOUNDS(P.t.status, row >= -1 && row < (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 125);
     };
-    auto load = [&](int step) {
+    auto load = [&](int step, int row) {
       if (step < steps) {
-        float* dst = reinterpret_cast<float*>(smem + (step & 1) * G::kStage);
-        for (int id = threadIdx.x; id < G::kKeys * (D / 4); id += kThreads) {
-          const int i = id / (D / 4), ch = id % (D / 4), j = slot_of(step, i);
-          const int page = j >= 0 && span.holds(j) ? paged_page(P.t, w.b, j / P.t.page_rows) : -1;
-          const float* src = cache + paged_row(P.t, max(page, 0), 0, head, max(j, 0) % P.t.page_rows) * D + ch * 4;
-          const uint32_t to = ptx::smem_addr(dst + i * G::kRow + ch * 4);
-          copy16(to, src, page >= 0);
-          copy16(to + G::kKeys * G::kRow * 4, src + (int64_t)P.t.heads_kv * P.t.page_rows * D, page >= 0);
+        const uint32_t dst = ptx::smem_addr(smem + (step & 1) * G::kStage);
+        constexpr int kCh4 = D / 4;  // 16-byte pieces of a row
+#pragma unroll
+        for (int x = 0; x < G::kKeys * kCh4 / kThreads; ++x) {
+          const int id = threadIdx.x + x * kThreads, i = id / kCh4, ch = id % kCh4;
+          const int from = __shfl_sync(0xffffffffu, row, i);
+          const float* src = cache + (int64_t)max(from, 0) * D + ch * 4;
+          const uint32_t to = dst + (i * G::kRow + ch * 4) * 4;
+          copy16(to, src, from >= 0);
+          copy16(to + G::kKeys * G::kRow * 4, src + (int64_t)P.t.heads_kv * P.t.page_rows * D, from >= 0);
         }
       }
       copies_commit();
@@ -454,16 +463,21 @@ __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendPar
     float m[kPer], l[kPer], acc[kPer][kCh];
 #pragma unroll
     for (int r = 0; r < kPer; ++r) {
-      const int row = warp * kPer + r;
-      slot[r] = row < it.rows ? w.seq.slot0() + (it.row0 + row) / P.group : -1;
+      const int own = warp * kPer + r;
+      slot[r] = own < it.rows ? w.seq.slot0() + (it.row0 + own) / P.group : -1;
       m[r] = -INFINITY;
       l[r] = 0.f;
 #pragma unroll
       for (int c = 0; c < kCh; ++c) acc[r][c] = 0.f;
     }
-    load(0);
+    int j, row, j_next, row_next;
+    find(0, j, row);
+    load(0, row);
+    find(1, j_next, row_next);
     for (int step = 0; step < steps; ++step) {
-      load(step + 1);
+      load(step + 1, row_next);
+      int j_after, row_after;
+      find(step + 2, j_after, row_after);
       copies_wait<1>();
       __syncthreads();
       const float* ks = reinterpret_cast<const float*>(smem + (step & 1) * G::kStage);
@@ -480,12 +494,10 @@ __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendPar
           s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
         }
       }
-      const int j = slot_of(step, lane);
-      const bool there = j >= 0 && span.holds(j) && paged_page(P.t, w.b, j / P.t.page_rows) >= 0;
       float p[kPer];
 #pragma unroll
       for (int r = 0; r < kPer; ++r) {
-        const float x = there && paged_sees(P.window, P.sinks, slot[r], j) ? s[r] : -INFINITY;
+        const float x = row >= 0 && paged_sees(P.window, P.sinks, slot[r], j) ? s[r] : -INFINITY;
         float mx = x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -510,6 +522,8 @@ __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendPar
           for (int c = 0; c < kCh; ++c) acc[r][c] = fmaf(pr, v[c], acc[r][c]);
         }
       }
+      j = j_next, row = row_next;
+      j_next = j_after, row_next = row_after;
       __syncthreads();
     }
     copies_wait<0>();
