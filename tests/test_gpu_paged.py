@@ -182,13 +182,42 @@ def test_page_sizes(page_rows, counts, lengths):
 
 @gpu
 @pytest.mark.parametrize("counts,lengths,hq,hk", [([1500], [1500], 4, 1), ([1000, 600, 1], [4000, 700, 3000], 8, 2),
-                                                  ([257], [2000], 5, 1), ([300] * 6, [300, 600, 2000, 301, 900, 5000], 2, 2)])
+                                                  ([257], [2000], 5, 1), ([300] * 6, [300, 600, 2000, 301, 900, 5000], 2, 2),
+                                                  ([9], [500], 72, 1), ([7, 3], [300, 200], 128, 1), ([5], [200], 160, 1)])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (300, 40)])
 def test_chunks(counts, lengths, hq, hk, d, window, sinks):
     """Prompts without and with a prefix, chunks that fill several tiles."""
     t = Batch(np.random.default_rng(hq + d), counts, lengths, hq, hk, d, "bf16", 64, window=window, sinks=sinks)
     t.check_attend(*t.attend())
+
+
+@gpu
+@pytest.mark.parametrize("counts", [[1, 2], [150, 1]])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_cache_beyond_4_gb(dtype, counts):
+    """The same sequences on pages at the end of a pool of 6 GB: every call's results bit for bit."""
+    rng = np.random.default_rng(2)
+    t = Batch(rng, counts, [700, 300], 4, 2, 128, dtype, 64)
+    far = int(6e9 / (2 * 2 * 64 * 128 * DT[dtype].itemsize))
+    kv = ra.ra_paged_plan(far, 64, 4, 2, 128, dtype=dtype)
+    cache = torch.empty(ra.ra_paged_cache_shape(kv), dtype=DT[dtype], device="cuda")
+    cache[far - t.ref.pages:] = t.cache
+    table = t.table + (far - t.ref.pages)
+    rope = ra.ra_rope_plan(128, dtype=dtype)
+    k, v, q = t.random(t.tokens, 2).cuda(), t.random(t.tokens, 2).cuda(), t.q.cuda()
+    out = []
+    for plan, c, tab in ((t.kv, t.cache, t.table), (kv, cache, table)):
+        turned = ra.ra_paged_append(plan, c, k, v, tab, t.offset, t.length, rope=rope, q=q)
+        o, lse = ra.ra_paged_attend(plan, c, turned, tab, t.offset, t.length)
+        w = torch.zeros((2, 2, 700), device="cuda")
+        ra.ra_paged_weigh(plan, c, turned, lse, tab, t.offset, t.length, w)
+        weighed = w.clone()
+        kept, n = ra.ra_paged_evict(plan, c, tab, t.length, w, 250, first=1, recent=20)
+        ra.ra_paged_sync_status(plan)
+        out.append((turned, o, lse, weighed, kept, n, c[-t.ref.pages:]))
+    for a, e in zip(*out):
+        assert _same_bits(a, e) if a.is_floating_point() else torch.equal(a, e)
 
 
 @gpu
