@@ -8,12 +8,13 @@
 // sequences are laid in a row and shared out among the warps in equal runs; a warp streams its
 // run through a ring of its own (cp.async, 16 bytes a lane) and scores the keys against 16 query
 // rows at a time by m16n8k16, the rows of a sequence of up to 16 staying in registers.
-// float32: a warp has 32 keys, one a lane.
+// float32: a CTA has 128 keys in shared memory, a lane one of them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "paged_share.cuh"
 #include "sm100_ptx.cuh"
@@ -283,9 +284,24 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
   }
 }
 
+// A CTA has 128 keys in shared memory, a lane one of them; the query rows come 16 at a time and
+// are read by all lanes at once, so that a key's value enters as many products as there are rows.
+template <int D>
+struct F32 {
+  static constexpr int kRow = D + 4;  // floats; 8 lanes' 16-byte reads of a column fall into different banks
+  static constexpr int kKeyBytes = kChunk * kRow * 4;
+  static constexpr int kBytes = kKeyBytes + 16 * D * 4 + 2 * 16 * 4;
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) weigh_f32_kernel(const PagedWeighParams P) {
-  extern __shared__ int64_t prefix[];
+  using G = F32<D>;
+  extern __shared__ __align__(128) uint8_t smem_bytes[];
+  float* keys = reinterpret_cast<float*>(smem_bytes);
+  float* qs = reinterpret_cast<float*>(smem_bytes + G::kKeyBytes);
+  float* lse2 = qs + 16 * D;
+  int* slots = reinterpret_cast<int*>(lse2 + 16);
+  int64_t* prefix = reinterpret_cast<int64_t*>(smem_bytes + G::kBytes);
   slot_prefix<kChunk>(P.t, P.group, prefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
   const int64_t chunks = prefix[P.t.batch];
@@ -294,37 +310,65 @@ __global__ void __launch_bounds__(kThreads) weigh_f32_kernel(const PagedWeighPar
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     while (prefix[b + 1] <= c) ++b;
     const Rows<float> rows{P, paged_seq(P.t, b), head};
-    const int j0 = (int)(c - prefix[b]) * kChunk + warp * kKeys, j = j0 + lane;
-    if (j0 >= rows.seq.length) continue;
-    const int rows_n = rows.seq.count * P.group;
-    int tile0, tile1;
-    rows.tiles(j0, kKeys, tile0, tile1);
+    const int first = (int)(c - prefix[b]) * kChunk, j = first + warp * kKeys + lane;
     const bool look = j < rows.seq.length && rows.seen(j);
     const int page = look ? paged_page(P.t, b, j / P.t.page_rows) : -1;
-    const float4* k = reinterpret_cast<const float4*>(cache + paged_row(P.t, max(page, 0), 0, head, j % P.t.page_rows) * D);
+    const int row = page >= 0 ? (int)paged_row(P.t, page, 0, head, j % P.t.page_rows) : -1;
+    RA_BOUNDS(P.t.status, row >= -1 && row < (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 114);
+    __syncthreads();  // (the keys of the chunk before are done with)
+    // A warp brings its own keys: rows known to the lanes, 16 bytes a lane.
+    constexpr int kPieces = D / 4;
+#pragma unroll 8
+    for (int x = 0; x < kKeys * kPieces / 32; ++x) {
+      const int id = lane + 32 * x, i = id / kPieces, ch = id % kPieces;
+      const int from = __shfl_sync(0xffffffffu, row, i);
+      copy16(ptx::smem_addr(keys + (warp * kKeys + i) * G::kRow + ch * 4), cache + (int64_t)max(from, 0) * D + ch * 4, from >= 0);
+    }
+    copies_commit();
+    const int rows_n = rows.seq.count * P.group;
+    int tile0, tile1;
+    rows.tiles(first, kChunk, tile0, tile1);
     float sum = 0.f;
-    for (int r0 = tile0 * 16; r0 < min(rows_n, tile1 * 16); r0 += 4) {
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      const float4* q[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = reinterpret_cast<const float4*>(rows.row_ptr(min(r0 + i, rows_n - 1)));
-#pragma unroll 4
-      for (int c4 = 0; c4 < D / 4; ++c4) {
-        const float4 kk = page >= 0 ? __ldg(k + c4) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 qq = __ldg(q[i] + c4);
-          s[i] = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, fmaf(qq.z, kk.z, fmaf(qq.w, kk.w, s[i]))));
-        }
+    for (int t = tile0; t < tile1; ++t) {
+      const int n = min(16, rows_n - t * 16);
+      __syncthreads();  // (the rows before are done with)
+      for (int id = threadIdx.x; id < n * kPieces; id += kThreads)
+        reinterpret_cast<float4*>(qs)[id] = __ldg(reinterpret_cast<const float4*>(rows.row_ptr(t * 16 + id / kPieces)) + id % kPieces);
+      if (threadIdx.x < n) {
+        lse2[threadIdx.x] = rows.lse_of(t * 16 + threadIdx.x) * kLog2e;
+        slots[threadIdx.x] = rows.seq.slot0() + (t * 16 + (int)threadIdx.x) / P.group;
       }
+      copies_wait<0>();
+      __syncthreads();
+      const float* k = keys + (warp * kKeys + lane) * G::kRow;
+      auto add = [&](auto most, int r0) {  // rows r0 .. r0 + most
+        constexpr int kN = decltype(most)::value;
+        float s[kN];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (r0 + i >= rows_n) break;
-        const bool sees = paged_sees(P.window, P.sinks, rows.seq.slot0() + (r0 + i) / P.group, j);
-        const float p = exp2f(fmaf(s[i], P.scale_log2, -rows.lse_of(r0 + i) * kLog2e));
-        sum += sees ? p : 0.f;
+        for (int i = 0; i < kN; ++i) s[i] = 0.f;
+#pragma unroll 4
+        for (int x = 0; x < kPieces; ++x) {
+          const float4 kk = *reinterpret_cast<const float4*>(k + x * 4);
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const float4 q = *reinterpret_cast<const float4*>(qs + (r0 + i) * D + x * 4);
+            s[i] = fmaf(q.x, kk.x, fmaf(q.y, kk.y, fmaf(q.z, kk.z, fmaf(q.w, kk.w, s[i]))));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          if (r0 + i >= n) break;
+          const float p = exp2f(fmaf(s[i], P.scale_log2, -lse2[r0 + i]));
+          sum += paged_sees(P.window, P.sinks, slots[r0 + i], j) ? p : 0.f;
+        }
+      };
+      if (n > 8) {
+        add(std::integral_constant<int, 16>(), 0);
+      } else {
+        for (int r0 = 0; r0 < n; r0 += 4) add(std::integral_constant<int, 4>(), r0);
       }
     }
+    copies_wait<0>();
     if (j < rows.seq.length && (page >= 0 || !look)) {
       if (j < P.weight_width) {
         const int64_t at = ((int64_t)b * P.t.heads_kv + head) * P.weight_width + j;
@@ -343,28 +387,31 @@ unsigned slots_of(const PagedWeighParams& prm, int sm_count, int per_sm, int own
   return (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)sm_count * per_sm / prm.t.heads_kv));
 }
 
-template <int D>
-cudaError_t launch_bf16(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
-  constexpr int kRing = kWarps * kStages * (kStepKeys * D * 2 + kStepKeys * 4);
-  static std::atomic<int> ready[kMaxDevices];
+template <typename Kernel>
+cudaError_t launch(Kernel kernel, std::atomic<int>* ready, const PagedWeighParams& prm, unsigned slots, int bytes,
+                   cudaStream_t stream) {
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool cached = dev >= 0 && dev < kMaxDevices;
   if (!cached || !ready[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(weigh_bf16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + (kMaxSequences + 1) * 8);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes + (kMaxSequences + 1) * 8);
     if (e != cudaSuccess) return e;
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
-  const dim3 grid(slots_of(prm, sm_count, 3, kWarps * kStepKeys), (unsigned)prm.t.heads_kv);
-  weigh_bf16_kernel<D><<<grid, kThreads, kRing + (prm.t.batch + 1) * 8, stream>>>(prm);
+  kernel<<<dim3(slots, (unsigned)prm.t.heads_kv), kThreads, bytes + (prm.t.batch + 1) * 8, stream>>>(prm);
   return cudaGetLastError();
 }
 template <int D>
+cudaError_t launch_bf16(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
+  static std::atomic<int> ready[kMaxDevices];
+  return launch(weigh_bf16_kernel<D>, ready, prm, slots_of(prm, sm_count, 3, kWarps * kStepKeys),
+                kWarps * kStages * (kStepKeys * D * 2 + kStepKeys * 4), stream);
+}
+template <int D>
 cudaError_t launch_f32(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
-  const dim3 grid(slots_of(prm, sm_count, 4, kChunk), (unsigned)prm.t.heads_kv);
-  weigh_f32_kernel<D><<<grid, kThreads, (prm.t.batch + 1) * 8, stream>>>(prm);
-  return cudaGetLastError();
+  static std::atomic<int> ready[kMaxDevices];
+  return launch(weigh_f32_kernel<D>, ready, prm, slots_of(prm, sm_count, D == 64 ? 5 : 2, kChunk), F32<D>::kBytes, stream);
 }
 
 }  // namespace
