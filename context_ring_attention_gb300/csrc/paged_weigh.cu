@@ -8,7 +8,7 @@
 // sequences are laid in a row and shared out among the warps in equal runs; a warp streams its
 // run through a ring of its own (cp.async, 16 bytes a lane) and scores the keys against 16 query
 // rows at a time by m16n8k16, the rows of a sequence of up to 16 staying in registers.
-// float32: a CTA has 128 keys in shared memory, a lane one of them.
+// float32: keys in shared memory, a lane one of them, 16 query rows at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,8 +24,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kKeys = 32;                  // of a warp
-constexpr int kChunk = kWarps * kKeys;     // of a CTA at a time
+constexpr int kKeys = 32;  // float32: a lane each
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -284,63 +283,75 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
   }
 }
 
-// A CTA has 128 keys in shared memory, a lane one of them; the query rows come 16 at a time and
-// are read by all lanes at once, so that a key's value enters as many products as there are rows.
-template <int D>
+// A lane has a key, in shared memory; a warp has a tile of 16 query rows in shared memory of its
+// own, where all lanes read a row's value at once: a key's value enters as many products as there
+// are rows.  kFew: each warp has 32 keys and goes through all tiles.  Otherwise the CTA has 32
+// keys and its warps take the tiles in turn; their sums are added in order.
+template <int D, bool kFew>
 struct F32 {
+  static constexpr int kOwn = kFew ? kWarps * kKeys : kKeys;  // keys of the CTA
   static constexpr int kRow = D + 4;  // floats; 8 lanes' 16-byte reads of a column fall into different banks
-  static constexpr int kKeyBytes = kChunk * kRow * 4;
-  static constexpr int kBytes = kKeyBytes + 16 * D * 4 + 2 * 16 * 4;
+  static constexpr int kKeyBytes = kOwn * kRow * 4;
+  static constexpr int kWarpBytes = 16 * D * 4 + 2 * 16 * 4;
+  static constexpr int kBytes = kKeyBytes + kWarps * kWarpBytes + (kFew ? 0 : kWarps * kKeys * 4);
 };
 
-template <int D>
+template <int D, bool kFew>
 __global__ void __launch_bounds__(kThreads) weigh_f32_kernel(const PagedWeighParams P) {
-  using G = F32<D>;
+  using G = F32<D, kFew>;
   extern __shared__ __align__(128) uint8_t smem_bytes[];
-  float* keys = reinterpret_cast<float*>(smem_bytes);
-  float* qs = reinterpret_cast<float*>(smem_bytes + G::kKeyBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
+  float* keys = reinterpret_cast<float*>(smem_bytes) + (kFew ? warp * kKeys * G::kRow : 0);
+  float* qs = reinterpret_cast<float*>(smem_bytes + G::kKeyBytes + warp * G::kWarpBytes);
   float* lse2 = qs + 16 * D;
   int* slots = reinterpret_cast<int*>(lse2 + 16);
+  float* sums = reinterpret_cast<float*>(smem_bytes + G::kKeyBytes + kWarps * G::kWarpBytes);
   int64_t* prefix = reinterpret_cast<int64_t*>(smem_bytes + G::kBytes);
-  slot_prefix<kChunk>(P.t, P.group, prefix);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
+  slot_prefix<G::kOwn>(P.t, P.group, prefix);
   const int64_t chunks = prefix[P.t.batch];
   const float* cache = static_cast<const float*>(P.t.cache);
   int b = 0;
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     while (prefix[b + 1] <= c) ++b;
     const Rows<float> rows{P, paged_seq(P.t, b), head};
-    const int first = (int)(c - prefix[b]) * kChunk, j = first + warp * kKeys + lane;
+    const int first = (int)(c - prefix[b]) * G::kOwn + (kFew ? warp * kKeys : 0), j = first + lane;
     const bool look = j < rows.seq.length && rows.seen(j);
     const int page = look ? paged_page(P.t, b, j / P.t.page_rows) : -1;
     const int row = page >= 0 ? (int)paged_row(P.t, page, 0, head, j % P.t.page_rows) : -1;
     RA_BOUNDS(P.t.status, row >= -1 && row < (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 114);
-    __syncthreads();  // (the keys of the chunk before are done with)
-    // A warp brings its own keys: rows known to the lanes, 16 bytes a lane.
-    constexpr int kPieces = D / 4;
+    // Keys and sums of the chunk before are done with.
+    if constexpr (kFew) __syncwarp(); else __syncthreads();
+    constexpr int kPieces = D / 4, kBring = kFew ? 32 : kThreads;
 #pragma unroll 8
-    for (int x = 0; x < kKeys * kPieces / 32; ++x) {
-      const int id = lane + 32 * x, i = id / kPieces, ch = id % kPieces;
+    for (int x = 0; x < kKeys * kPieces / kBring; ++x) {
+      const int id = (kFew ? lane : (int)threadIdx.x) + x * kBring, i = id / kPieces, ch = id % kPieces;
       const int from = __shfl_sync(0xffffffffu, row, i);
-      copy16(ptx::smem_addr(keys + (warp * kKeys + i) * G::kRow + ch * 4), cache + (int64_t)max(from, 0) * D + ch * 4, from >= 0);
+      copy16(ptx::smem_addr(keys + i * G::kRow + ch * 4), cache + (int64_t)max(from, 0) * D + ch * 4, from >= 0);
     }
     copies_commit();
     const int rows_n = rows.seq.count * P.group;
     int tile0, tile1;
-    rows.tiles(first, kChunk, tile0, tile1);
+    rows.tiles(first, kKeys, tile0, tile1);
     float sum = 0.f;
-    for (int t = tile0; t < tile1; ++t) {
-      const int n = min(16, rows_n - t * 16);
-      __syncthreads();  // (the rows before are done with)
-      for (int id = threadIdx.x; id < n * kPieces; id += kThreads)
-        reinterpret_cast<float4*>(qs)[id] = __ldg(reinterpret_cast<const float4*>(rows.row_ptr(t * 16 + id / kPieces)) + id % kPieces);
-      if (threadIdx.x < n) {
-        lse2[threadIdx.x] = rows.lse_of(t * 16 + threadIdx.x) * kLog2e;
-        slots[threadIdx.x] = rows.seq.slot0() + (t * 16 + (int)threadIdx.x) / P.group;
-      }
+    bool there = false;  // the keys are
+    auto await = [&] {
+      if (there) return;
       copies_wait<0>();
-      __syncthreads();
-      const float* k = keys + (warp * kKeys + lane) * G::kRow;
+      if constexpr (kFew) __syncwarp(); else __syncthreads();
+      there = true;
+    };
+    for (int t = tile0 + (kFew ? 0 : warp); t < tile1; t += kFew ? 1 : kWarps) {
+      const int n = min(16, rows_n - t * 16);
+      __syncwarp();
+      for (int id = lane; id < n * kPieces; id += 32)
+        reinterpret_cast<float4*>(qs)[id] = __ldg(reinterpret_cast<const float4*>(rows.row_ptr(t * 16 + id / kPieces)) + id % kPieces);
+      if (lane < n) {
+        lse2[lane] = rows.lse_of(t * 16 + lane) * kLog2e;
+        slots[lane] = rows.seq.slot0() + (t * 16 + lane) / P.group;
+      }
+      __syncwarp();
+      await();
+      const float* k = keys + lane * G::kRow;
       auto add = [&](auto most, int r0) {  // rows r0 .. r0 + most
         constexpr int kN = decltype(most)::value;
         float s[kN];
@@ -368,11 +379,20 @@ __global__ void __launch_bounds__(kThreads) weigh_f32_kernel(const PagedWeighPar
         for (int r0 = 0; r0 < n; r0 += 4) add(std::integral_constant<int, 4>(), r0);
       }
     }
-    copies_wait<0>();
-    if (j < rows.seq.length && (page >= 0 || !look)) {
+    await();
+    if constexpr (!kFew) {
+      sums[warp * kKeys + lane] = sum;
+      __syncthreads();
+    }
+    if ((kFew || warp == 0) && j < rows.seq.length && (page >= 0 || !look)) {
       if (j < P.weight_width) {
         const int64_t at = ((int64_t)b * P.t.heads_kv + head) * P.weight_width + j;
         RA_BOUNDS(P.t.status, at < (int64_t)P.t.batch * P.t.heads_kv * P.weight_width, 113);
+        if constexpr (!kFew) {
+          sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) sum += sums[i * kKeys + lane];
+        }
         P.weight[at] = (P.weight_in != nullptr && j < rows.seq.slot0() ? P.weight_in[at] : 0.f) + sum;
       } else {
         atomicOr(P.t.status, kPagedStatusRange);
@@ -408,10 +428,21 @@ cudaError_t launch_bf16(const PagedWeighParams& prm, int sm_count, cudaStream_t 
   return launch(weigh_bf16_kernel<D>, ready, prm, slots_of(prm, sm_count, 3, kWarps * kStepKeys),
                 kWarps * kStages * (kStepKeys * D * 2 + kStepKeys * 4), stream);
 }
+template <int D, bool kFew>
+cudaError_t launch_f32(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
+  using G = F32<D, kFew>;
+  static std::atomic<int> ready[kMaxDevices];
+  constexpr int kPerSm = kFew ? (D == 64 ? 4 : 2) : (D == 64 ? 8 : 4);
+  return launch(weigh_f32_kernel<D, kFew>, ready, prm, slots_of(prm, sm_count, kPerSm, G::kOwn), G::kBytes, stream);
+}
 template <int D>
 cudaError_t launch_f32(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
-  static std::atomic<int> ready[kMaxDevices];
-  return launch(weigh_f32_kernel<D>, ready, prm, slots_of(prm, sm_count, D == 64 ? 5 : 2, kChunk), F32<D>::kBytes, stream);
+  // By the mean rows of a sequence and head.  16 sequences of 4k, D 128, few and not: 4 rows 54
+  // and 65 us, 16 rows 102 and 132, 32 rows 170 and 158, 64 rows 310 and 231 (D 64: 26 and 47,
+  // 47 and 88, 78 and 108, 138 and 147).  400 tokens of a head over 700 slots 164 and 57: too few
+  // CTAs have work in the first form.
+  const bool few = (int64_t)prm.t.tokens * prm.group <= 32 * (int64_t)prm.t.batch;
+  return few ? launch_f32<D, true>(prm, sm_count, stream) : launch_f32<D, false>(prm, sm_count, stream);
 }
 
 }  // namespace
