@@ -603,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------ extra channels --
-// -LSE / scale of every query tile's rows as three bf16 terms; of rows of no token a number that
-// leaves nothing of their weights.  A thread has a row; the tiles of the sequences follow each other.
+// -LSE / scale of every query tile's rows as three bf16 terms; of rows of no token -inf, which
+// leaves nothing of their weights at any scale.  A thread has a row; the tiles of the sequences follow each other.
 __global__ void __launch_bounds__(kTile) paged_weigh_extra_kernel(const PagedWeighChunkParams P) {
   extern __shared__ int64_t prefix[];
   next_may_come();
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kTile) paged_weigh_extra_kernel(const PagedWei
     const int b = paged_find(prefix, P.t.batch, i);
     const PagedSeq q = paged_seq(P.t, b);
     const int token = (i - (int)prefix[b]) * per_tile + tok;
-    float x = -1e30f;
+    float x = -INFINITY;
     if (tok < per_tile && token < q.count)
       x = inv * __ldg(P.lse + (int64_t)(q.token0 + token) * P.heads_q + head * P.group + row - tok * P.group);
     const uint32_t hi = ptx::pack_bf16x2(x, 0.f) & 0xffffu;

@@ -706,7 +706,7 @@ typedef struct {
   int32_t dtype;      /* ra_dtype of the cache, Q, K, V and O                       */
   int64_t window;     /* as ra_plan_window's, counted in slots; 0: the whole prefix */
   int64_t sinks;      /* as ra_plan_window's                                        */
-  float scale;        /* score scale; 0 selects 1/sqrt(head_dim)                    */
+  float scale;        /* score scale, 2^-100..2^100; 0 selects 1/sqrt(head_dim)     */
 } ra_paged_problem;
 
 typedef struct ra_paged_s* ra_paged_t;

@@ -38,11 +38,12 @@ def _same_bits(a, b):
 class Batch:
     """A packed batch over a cache: `lead` and `tail` tokens of no sequence around it."""
 
-    def __init__(self, rng, counts, lengths, hq, hk, d, dtype, page_rows, lead=0, tail=0, window=0, sinks=0, **kw):
+    def __init__(self, rng, counts, lengths, hq, hk, d, dtype, page_rows, lead=0, tail=0, window=0, sinks=0, scale=None, **kw):
         self.rng, self.counts, self.lengths = rng, list(counts), list(lengths)
-        self.hq, self.hk, self.d, self.dtype, self.window, self.sinks = hq, hk, d, dtype, window, sinks
+        self.hq, self.hk, self.d, self.dtype, self.window, self.sinks, self.scale = hq, hk, d, dtype, window, sinks, scale
         self.ref = paged_ref.Cache(rng, lengths, page_rows, hk, d, dtype, **kw)
-        self.kv = ra.ra_paged_plan(self.ref.pages, page_rows, hq, hk, d, dtype=dtype, window=window, sinks=sinks)
+        self.kv = ra.ra_paged_plan(self.ref.pages, page_rows, hq, hk, d, dtype=dtype, window=window, sinks=sinks,
+                                   scale=scale)
         self.cache, self.table = self.ref.data.cuda(), _i32(self.ref.table)
         self.first = np.concatenate([[lead], lead + np.cumsum(counts)])
         self.tokens = int(self.first[-1]) + tail
@@ -71,7 +72,7 @@ class Batch:
             seen = paged_ref.sees(self.slots(b), j, self.window, self.sinks).any(0)
             j = j[seen]
             ow, lw, ob, lb = paged_ref.attend(self.ref.rows(b, j, 0), self.ref.rows(b, j, 1), self.q[self.rows(b)], self.slots(b), j,
-                                              self.window, self.sinks, U[self.dtype])
+                                              self.window, self.sinks, U[self.dtype], self.scale)
             assert_within(lse[self.rows(b)], lw, lb, f"LSE of sequence {b}")
             assert_within(o[self.rows(b)], ow, ob, f"O of sequence {b}")
 
@@ -86,7 +87,8 @@ class Batch:
                 seen = paged_ref.sees(self.slots(b), j, self.window, self.sinks).any(0)
                 js = j[seen]
                 want[:, js], bound[:, js] = paged_ref.weigh(self.ref.rows(b, js, 0), self.q[self.rows(b)],
-                                                            lse[self.rows(b)].cpu(), self.slots(b), js, self.window, self.sinks)
+                                                            lse[self.rows(b)].cpu(), self.slots(b), js, self.window, self.sinks,
+                                                            self.scale)
             want[:, :old] += before[b, :, :old].double()
             assert_within(weight[b, :, :n], want, bound + U["f32"] * want.abs() + 1e-37, f"weights of sequence {b}")
 
@@ -499,6 +501,21 @@ def test_weights(dtype, d, hq, hk, counts, lengths):
         total = fresh[b, :, :n].double().sum(-1).cpu()
         want = counts[b] * hq / hk
         assert (total - want).abs().max() <= want * (2.0 ** -14 * 40) + 1e-9
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -7, 0.3, 3.0])
+@pytest.mark.parametrize("counts,lengths,hq,hk", [([1, 2], [700, 90], 6, 2), ([150, 90], [700, 90], 6, 2), ([150, 1], [700, 90], 4, 1)])
+def test_scales(dtype, scale, counts, lengths, hq, hk):
+    """Scales from the smallest one, at which all weights are alike, groups that leave rows of a query tile empty."""
+    t = Batch(np.random.default_rng(3), counts, lengths, hq, hk, 128, dtype, 32, scale=scale)
+    o, lse = t.attend()
+    t.check_attend(o, lse)
+    before = torch.rand((2, hk, 700))
+    weight = before.cuda()
+    ra.ra_paged_weigh(t.kv, t.cache, t.q.cuda(), lse, t.table, t.offset, t.length, weight, weight_in=weight)
+    t.check_weigh(weight.cpu(), before, lse)
 
 
 @gpu

@@ -55,7 +55,7 @@ def test_unsupported_rotation_and_amplitude():
     (dict(heads_q=3), "RA_ERR_INVALID_ARG"), (dict(heads_kv=0), "RA_ERR_INVALID_ARG"),
     (dict(window=-1), "RA_ERR_INVALID_ARG"), (dict(sinks=-1), "RA_ERR_INVALID_ARG"),
     (dict(scale=float("inf")), "RA_ERR_INVALID_ARG"), (dict(scale=-1.0), "RA_ERR_INVALID_ARG"),
-    (dict(scale=float("nan")), "RA_ERR_INVALID_ARG"), (dict(dtype=7), "RA_ERR_INVALID_ARG"),
+    (dict(scale=float("nan")), "RA_ERR_INVALID_ARG"), (dict(scale=2.0 ** -101), "RA_ERR_INVALID_ARG"), (dict(dtype=7), "RA_ERR_INVALID_ARG"),
     (dict(head_dim=0), "RA_ERR_INVALID_ARG"), (dict(head_dim=96), "RA_ERR_UNSUPPORTED"),
     (dict(head_dim=256), "RA_ERR_UNSUPPORTED"), (dict(heads_q=65536, heads_kv=65536), "RA_ERR_UNSUPPORTED"),
     (dict(pages=1 << 24, page_rows=64), "RA_ERR_UNSUPPORTED")])
