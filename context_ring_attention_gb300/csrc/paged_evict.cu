@@ -8,10 +8,15 @@
 // the slots in order with a scan.  Counts are whole numbers: their order does not matter.
 //
 // The second moves rows, bound by HBM: the kept rows are read and written once.  Into other pages
-// the CTAs take runs of rows.  In place a row's new one is never behind its old one, so that a CTA
-// that has read all rows up to some place may write up to it: a CTA walks the whole list in
-// order, for a piece of every row of a head's keys or values, reading a step ahead.  Where each
-// row lies is looked up for many rows at once, before their turn.
+// the CTAs take runs of rows.  In place a row's new one is never behind its old one, so that whoever
+// has read all rows up to some place may write up to it: a cluster walks the whole list in order,
+// its CTAs some rows of each step, for a piece of every row of a head's keys or values, reading a
+// step ahead.  Where each row lies is looked up for many rows at once, before their turn.
+//
+// Measured (8 heads, D 128, bf16): 16 sequences of 4352 slots to 4096 (543 MB) into other pages 107
+// us, in place 108; the choice alone takes 15.  33001 slots to 8192 (69 MB) into other pages 33 us,
+// of which the choice 20: bound by the latency of its three passes, barriers and the scan (one CTA a
+// head: 51); in place 41.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -198,11 +203,13 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const PagedEvictPara
 
 constexpr int kMoveThreads = 256;
 constexpr int kUnroll = 4;      // rows of a thread under way, twice
+constexpr int kMaxTeam = 8;
 constexpr int kBlock = 2048;    // rows whose places are looked up at a time: four steps or more
 
 static_assert(kBlock >= 4 * (kMoveThreads / 4) * kUnroll, "a step's places are written two barriers before they are read");
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedEvictParams P, int row_bytes, int pieces, int runs) {
+// team: CTAs of a cluster.
+__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const PagedEvictParams P, int row_bytes, int pieces, int team) {
   __shared__ int2 places[2][kBlock];  // rows of the cache: from, to (from < 0: nothing to move)
   const int head = (int)blockIdx.y, b = (int)blockIdx.z;
   after_previous();
@@ -210,24 +217,22 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedEvictPara
   if (m == 0) return;
   // The pages are the same, or none of them is: the first entry tells.
   const bool in_place = __ldg(P.new_table + b * P.new_width) == __ldg(P.t.page_table + b * P.t.width);
-  // In place: CTA 2 * piece + which has a piece of every row.  Else: CTA 2 * run + which a run of rows.
-  const int which = (int)blockIdx.x & 1;
-  int piece = 0, run = (int)blockIdx.x >> 1;
-  if (in_place) {
-    if (run >= pieces) return;
-    piece = run;
-    run = 0;
-  } else {
-    runs *= pieces;
-    pieces = 1;
-  }
+  // In place: cluster 2 * piece + which has a piece of every row, its CTAs a step of rows in turn.
+  // Else: CTA 2 * run + which a run of rows.
+  const int unit = in_place ? (int)blockIdx.x / team : (int)blockIdx.x, which = unit & 1, part = unit >> 1;
+  const int rank = in_place ? (int)blockIdx.x % team : 0;
+  if (!in_place) pieces = team = 1;
+  else if (part >= pieces) return;  // (a whole cluster)
+  const int piece = in_place ? part : 0, runs = in_place ? 1 : (int)gridDim.x >> 1, run = in_place ? 0 : part;
   const int piece_bytes = row_bytes / pieces, lanes = piece_bytes / 16, pass = kMoveThreads / lanes;
-  const int r0 = in_place ? 0 : (int)((int64_t)m * run / runs), r1 = in_place ? m : (int)((int64_t)m * (run + 1) / runs);
+  const int r0 = (int)((int64_t)m * run / runs), r1 = (int)((int64_t)m * (run + 1) / runs);
+  const int sub = threadIdx.x / lanes, step = pass * kUnroll;  // rows of this CTA a step: a power of two
+  const int bits = __ffs(step) - 1;
   const int32_t* kept = P.kept + ((int64_t)b * P.t.heads_kv + head) * P.keep;
   const int pr = P.t.page_rows;
   auto look_up = [&](int block) {
     for (int i = threadIdx.x; i < kBlock; i += kMoveThreads) {
-      const int j = r0 + block * kBlock + i;
+      const int k = block * kBlock + i, j = r0 + ((((k >> bits) * team + rank) << bits) | (k & (step - 1)));
       int2 at = make_int2(-1, 0);
       if (j < r1) {
         const int s = kept[j];
@@ -244,10 +249,9 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedEvictPara
     }
   };
   uint8_t* cache = static_cast<uint8_t*>(P.t.cache) + piece * piece_bytes + (threadIdx.x % lanes) * 16;
-  const int sub = threadIdx.x / lanes, step = pass * kUnroll;
-  const int steps = (r1 - r0 + step - 1) / step, per_block = kBlock / step;
+  const int steps = (r1 - r0 + step * team - 1) / (step * team), per_block = kBlock >> bits;  // (a power of two)
   uint4 x[2][kUnroll];
-  auto place = [&](int s, int i) { return places[(s / per_block) & 1][s % per_block * step + i * pass + sub]; };
+  auto place = [&](int s, int i) { return places[(s << bits) / kBlock & 1][((s & (per_block - 1)) << bits) + i * pass + sub]; };
   auto load = [&](int s, uint4 (&v)[kUnroll]) {
     if (s >= steps) return;
 #pragma unroll
@@ -263,13 +267,14 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const PagedEvictPara
       if (at.x >= 0) *reinterpret_cast<uint4*>(cache + (int64_t)at.y * row_bytes) = v[i];
     }
   };
-  // Step s is stored once step s + 1 is read and all threads have read step s.
+  // Step s is stored once step s + 1 is read and all threads, of the whole cluster, have read step s.
   auto turn = [&](int s, const uint4 (&now)[kUnroll], uint4 (&next)[kUnroll]) {
     load(s + 1, next);
-    __syncthreads();
+    if (team > 1) cg::this_cluster().sync();
+    else __syncthreads();
     store(s, now);
     // (all threads have stored the block before this one; the next one is read two barriers on)
-    if (s % per_block == 0) look_up(s / per_block + 1);
+    if ((s & (per_block - 1)) == 0) look_up((s << bits) / kBlock + 1);
   };
   look_up(0);
   __syncthreads();
@@ -312,15 +317,30 @@ cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, int sm_co
   e = cudaLaunchKernelEx(&config, pick_kernel, prm, (int)(config.dynamicSmemBytes / 4));
   if (e != cudaSuccess) return e;
   const int row_bytes = prm.d * (dtype == RA_DTYPE_BF16 ? 2 : 4);
-  // Pieces of 64 bytes at least, as many as fill the GPU twice (in place they are all there is);
-  // runs of rows until there are six CTAs an SM (two to sixteen are within 4%; below 128 rows a
+  // Pieces of 64 bytes at least, as many as fill the GPU twice; runs of rows until there are six CTAs an SM (two to sixteen are within 4%; below 128 rows a
   // run is too short for its start).
   int pieces = 1;
   while (row_bytes / pieces > 64 && 2 * pieces * heads < 2 * sm_count) pieces *= 2;
   const int64_t most = (prm.keep + 127) / 128;
   const int runs = (int)std::max<int64_t>(1, std::min(most, (int64_t)sm_count * 6 / (2 * pieces * heads)));
-  const dim3 moves((unsigned)(2 * pieces * runs), (unsigned)prm.t.heads_kv, (unsigned)prm.t.batch);
-  return launch_behind(move_kernel, moves, kMoveThreads, 0, stream, prm, row_bytes, pieces, runs);
+  // In place, clusters where the pieces leave the GPU idle (one sequence of 33001 slots to 8192:
+  // clusters of 1, 2, 4, 8 CTAs 82, 65, 51, 41 us; to 32768: 247, 179, 123, 88).
+  const int step = kMoveThreads * 16 * pieces / row_bytes * kUnroll;
+  int team = 1;
+  while (team < kMaxTeam && (int64_t)team * step < prm.keep && 2 * 2 * team * pieces * heads <= 4 * sm_count) team *= 2;
+  cudaLaunchConfig_t move{};
+  move.gridDim = dim3((unsigned)(2 * pieces * ((runs + team - 1) / team * team)), (unsigned)prm.t.heads_kv, (unsigned)prm.t.batch);
+  move.blockDim = dim3(kMoveThreads);
+  move.stream = stream;
+  cudaLaunchAttribute how[2]{};
+  how[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_behind
+  how[0].val.programmaticStreamSerializationAllowed = 1;
+  how[1].id = cudaLaunchAttributeClusterDimension;
+  how[1].val.clusterDim.x = (unsigned)team;
+  how[1].val.clusterDim.y = how[1].val.clusterDim.z = 1;
+  move.attrs = how;
+  move.numAttrs = 2;
+  return cudaLaunchKernelEx(&move, move_kernel, prm, row_bytes, pieces, team);
 }
 
 }  // namespace ra

@@ -10,9 +10,14 @@
 // warp-level tensor instruction m16n8k16 with the query rows as its 16 rows: for so few rows
 // the 5th-generation one would spend its 128 rows on padding, and the products are far from
 // the bound.  Each warp takes every fourth block of its CTA's share through a ring of its own
-// (cp.async, 16 bytes a lane, rows swizzled for ldmatrix); rows that no query sees arrive as zeros, so that what a page holds
-// there does not matter.  The warps' sums are joined in shared memory, the parts of an item
-// that several CTAs share by a second kernel, both in a fixed order.
+// (cp.async, 16 bytes a lane, rows swizzled for ldmatrix); rows that no query sees arrive as
+// zeros, so that what a page holds there does not matter.  The warps' sums are joined in shared
+// memory, the parts of an item that several CTAs share by a second kernel, both in a fixed order.
+//
+// Measured (32 query and 8 key/value heads, D 128, bf16): one token of 16 sequences up to 32k
+// (1.27 GB) 190 us, 6.7 TB/s; one token over 1M 598 us, 7.2 TB/s.  float32 has no such instruction
+// to its precision: bound by the CUDA cores' reads of shared memory, one token of 16 sequences of
+// 4k (0.34 GB) 149 us, 2.1 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -391,7 +396,8 @@ __global__ void __launch_bounds__(kThreads) rows_bf16_kernel(const PagedAttendPa
 
 // --------------------------------------------------------------------- float32 --
 // A CTA meets 32 keys (two blocks) at a time; a warp has 4 of the 16 rows, a lane scores one
-// key against them, and then holds D / 32 channels of their outputs.
+// key against them, and then holds D / 32 channels of their outputs.  Which slot and row of the
+// cache a step's keys are is read two steps ahead (3 sequences of 300 tokens: 27 -> 23 us).
 template <int D>
 struct F32 {
   static constexpr int kRow = D + 4;  // floats; 8 lanes' 16-byte reads of a column fall into different banks

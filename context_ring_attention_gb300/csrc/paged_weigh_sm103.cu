@@ -5,19 +5,24 @@
 // that see any of them: 128 / group tokens with the rows of all heads of the group.  The scores
 // are made with the keys in the rows (S^T = K Q^T), so that a thread has one key and sums
 // e^(score - LSE) over the columns in its registers: no exchange between threads, no product
-// after it, and the keys stay in shared memory while the queries stream by.  The LSE of a query
-// tile's rows lies in shared memory, negated and in log2 units; rows of no token have -inf there.
+// after it.  The keys lie in tensor memory, as the first operand, while the queries stream by.
+//
+// The LSE enters by the product too: the queries have 16 channels more, -LSE / scale in three
+// bf16 terms (2^-24 of it) and zeros, the keys 1, 1, 1 and zeros; a first kernel makes them.  What a
+// thread has left to do for a score is one multiplication, the exponential and the sum.
 //
 // Shares: all items laid in a row, each as long as its query tiles, cut into one share per CTA.
-// An item that is cut leaves a sum per key and part, which a second kernel adds in order.
+// An item that is cut leaves a sum per key and part, which a last kernel adds in order.
 //
-// Bound by the tensor cores and the exponentials alike: a pair of tiles of 128 x 128 scores is
-// 512 cycles of either (d = 128).
+// Bound by the tensor cores and the exponentials alike (69% and 64% of the cycles busy, 55% of the
+// issue slots).  Measured: 1000 tokens of 32 and 8 heads, D 128, over 32k 186 us (2.6e11 operations,
+// 1.42 PFLOP/s); with the extra channels made by a warp of this kernel 250, with every tile asked
+// whether it needs a mask 189, with the warp-level instruction 3.5 ms.
 //
 // Roles (one CTA per SM, 20 warps): warp 0 TMA producer, warp 1 tcgen05 issuer, warp 2 the
-// items' records, warps 4-19 sums: four for each key tile and half of the
-// columns (two threads per key, whose sums meet in shared memory at an item's end).  With one
-// thread per key, two warps per scheduler, neither unit was busy half of the time.
+// items' records, warps 4-19 sums: four for each key tile and half of the columns (two threads
+// per key, whose sums meet in shared memory at an item's end).  With one thread per key, two
+// warps per scheduler, neither unit was busy half of the time.
 // TMEM: scores of the two key tiles 0-127 and 128-255, the keys 256-319 and 320-383, their extra
 // channels 384-391.
 //
