@@ -408,7 +408,7 @@ struct F32 {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendParams P) {
+__global__ void __launch_bounds__(kThreads, 2) rows_f32_kernel(const PagedAttendParams P) {
   using G = F32<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   float* qs = reinterpret_cast<float*>(smem + 2 * G::kStage);
@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendPar
   Walk w;
   if (!walk_begin<float>(P, prefix, w)) return;
   const float* cache = static_cast<const float*>(P.t.cache);
-  constexpr int kPer = kRowsTile / kWarps, kCh = D / 32;
+  constexpr int kPer = kRowsTile / kWarps, kCh = D / 32, kFew = 4;
+  static_assert(kFew == kWarps && kWarps * 8 == G::kKeys, "a warp for 8 keys, and for a row in the end");
 
   for (;; walk_next(P, prefix, w)) {
     const PagedItem it = paged_item<kRowsTile>(w.seq, P.group, w.tile);
@@ -465,96 +466,193 @@ __global__ void __launch_bounds__(kThreads) rows_f32_kernel(const PagedAttendPar
       }
       copies_commit();
     };
-    int slot[kPer];
-    float m[kPer], l[kPer], acc[kPer][kCh];
-#pragma unroll
-    for (int r = 0; r < kPer; ++r) {
-      const int own = warp * kPer + r;
-      slot[r] = own < it.rows ? w.seq.slot0() + (it.row0 + own) / P.group : -1;
-      m[r] = -INFINITY;
-      l[r] = 0.f;
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) acc[r][c] = 0.f;
-    }
     int j, row, j_next, row_next;
     find(0, j, row);
     load(0, row);
     find(1, j_next, row_next);
-    for (int step = 0; step < steps; ++step) {
-      load(step + 1, row_next);
-      int j_after, row_after;
-      find(step + 2, j_after, row_after);
-      copies_wait<1>();
-      __syncthreads();
-      const float* ks = reinterpret_cast<const float*>(smem + (step & 1) * G::kStage);
-      const float* vs = ks + G::kKeys * G::kRow;
-      float s[kPer];
-#pragma unroll
-      for (int r = 0; r < kPer; ++r) s[r] = 0.f;
-#pragma unroll 8
-      for (int c = 0; c < D / 4; ++c) {
-        const float4 k4 = *reinterpret_cast<const float4*>(ks + lane * G::kRow + c * 4);
-#pragma unroll
-        for (int r = 0; r < kPer; ++r) {
-          const float4 q4 = *reinterpret_cast<const float4*>(qs + (warp * kPer + r) * D + c * 4);
-          s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
-        }
-      }
-      float p[kPer];
-#pragma unroll
-      for (int r = 0; r < kPer; ++r) {
-        const float x = row >= 0 && paged_sees(P.window, P.sinks, slot[r], j) ? s[r] : -INFINITY;
-        float mx = x;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float m_new = fmaxf(m[r], mx * P.scale_log2);
-        const float ref = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = exp2f(m[r] - ref);
-        m[r] = m_new;
-        p[r] = exp2f(fmaf(x, P.scale_log2, -ref));
-        l[r] = l[r] * alpha + p[r];
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) acc[r][c] *= alpha;
-      }
-#pragma unroll 4
-      for (int i = 0; i < G::kKeys; ++i) {
-        float v[kCh];
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) v[c] = vs[i * G::kRow + lane + 32 * c];
-#pragma unroll
-        for (int r = 0; r < kPer; ++r) {
-          const float pr = __shfl_sync(0xffffffffu, p[r], i);
-#pragma unroll
-          for (int c = 0; c < kCh; ++c) acc[r][c] = fmaf(pr, v[c], acc[r][c]);
-        }
-      }
-      j = j_next, row = row_next;
-      j_next = j_after, row_next = row_after;
-      __syncthreads();
-    }
-    copies_wait<0>();
     const bool cut = u0 > 0 || u1 < n;
     const int64_t part = cut ? part_at(P, w, it, u0, n) : 0;
-#pragma unroll
-    for (int r = 0; r < kPer; ++r) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-      const int at = warp * kPer + r;
+    // Row `at` of the item, of which this lane has the channels lane, lane + 32 ..
+    auto put = [&](int at, float m, float l, const float (&acc)[kCh]) {
       if (cut) {
 #pragma unroll
-        for (int c = 0; c < kCh; ++c) P.part_o[(part * kRowsTile + at) * D + lane + 32 * c] = acc[r][c];
-        if (lane == 0) P.part_ml[part * kRowsTile + at] = make_float2(m[r], l[r]);
+        for (int c = 0; c < kCh; ++c) P.part_o[(part * kRowsTile + at) * D + lane + 32 * c] = acc[c];
+        if (lane == 0) P.part_ml[part * kRowsTile + at] = make_float2(m, l);
       } else if (at < it.rows) {
         const int row = row0 + at;
-        const float inv = l[r] > 0.f ? 1.0f / l[r] : (l[r] == 0.f ? 0.f : l[r]);
+        const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
         float* dst = row_of<float>(P.os, P.o, P.group, head, row);
 #pragma unroll
-        for (int c = 0; c < kCh; ++c) dst[lane + 32 * c] = acc[r][c] * inv;
+        for (int c = 0; c < kCh; ++c) dst[lane + 32 * c] = acc[c] * inv;
         if (lane == 0 && P.lse != nullptr) {
           const int token = row / P.group;
           P.lse[(int64_t)token * P.heads_q + head * P.group + row - token * P.group] =
-              l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+              l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
+      }
+    };
+    if (it.rows <= kFew) {
+      int order = lane >> 2;  // keys 4 apart beside each other: 4 lanes' pieces of them fall into different banks
+      order = (order >> 1) + 4 * (order & 1);
+      const int key = warp * 8 + order, r = lane & 3, slot = r < it.rows ? w.seq.slot0() + (it.row0 + r) / P.group : -1;
+      float m = -INFINITY, l = 0.f, acc[kFew][kCh];  // m, l: of row r
+#pragma unroll
+      for (int e = 0; e < kFew; ++e)
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) acc[e][c] = 0.f;
+      for (int step = 0; step < steps; ++step) {
+        load(step + 1, row_next);
+        int j_after, row_after;
+        find(step + 2, j_after, row_after);
+        copies_wait<1>();
+        __syncthreads();
+        const float* ks = reinterpret_cast<const float*>(smem + (step & 1) * G::kStage);
+        const float* vs = ks + G::kKeys * G::kRow;
+        float s[kFew] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {  // a fourth of the channels each
+          const float4 k4 = *reinterpret_cast<const float4*>(ks + key * G::kRow + c * 16 + r * 4);
+#pragma unroll
+          for (int e = 0; e < kFew; ++e) {
+            const float4 q4 = *reinterpret_cast<const float4*>(qs + e * D + c * 16 + r * 4);
+            s[e] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[e]))));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kFew; ++e) {
+          s[e] += __shfl_xor_sync(0xffffffffu, s[e], 1);
+          s[e] += __shfl_xor_sync(0xffffffffu, s[e], 2);
+        }
+        const int j_key = __shfl_sync(0xffffffffu, j, key), row_key = __shfl_sync(0xffffffffu, row, key);
+        const float own = r < 2 ? (r == 0 ? s[0] : s[1]) : (r == 2 ? s[2] : s[3]);
+        const float x = row_key >= 0 && paged_sees(P.window, P.sinks, slot, j_key) ? own : -INFINITY;
+        float mx = x;
+#pragma unroll
+        for (int o = 16; o > 2; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float m_new = fmaxf(m, mx * P.scale_log2);
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = exp2f(m - ref), p = exp2f(fmaf(x, P.scale_log2, -ref));
+        m = m_new;
+        l = l * alpha + p;
+        if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll
+          for (int e = 0; e < kFew; ++e) {
+            const float f = __shfl_sync(0xffffffffu, alpha, e);
+#pragma unroll
+            for (int c = 0; c < kCh; ++c) acc[e][c] *= f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v[kCh];
+#pragma unroll
+          for (int c = 0; c < kCh; ++c) v[c] = vs[(warp * 8 + (i >> 1) + 4 * (i & 1)) * G::kRow + lane + 32 * c];
+#pragma unroll
+          for (int e = 0; e < kFew; ++e) {
+            const float pr = __shfl_sync(0xffffffffu, p, i * 4 + e);
+#pragma unroll
+            for (int c = 0; c < kCh; ++c) acc[e][c] = fmaf(pr, v[c], acc[e][c]);
+          }
+        }
+        j = j_next, row = row_next;
+        j_next = j_after, row_next = row_after;
+        __syncthreads();
+      }
+      copies_wait<0>();
+      // The warps' sums side by side, then a row each joined by a warp.
+      float* sums = reinterpret_cast<float*>(smem);
+      float2* stats = reinterpret_cast<float2*>(sums + kWarps * kFew * D);
+#pragma unroll
+      for (int o = 16; o > 2; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      __syncthreads();
+      if (lane < kFew) stats[warp * kFew + lane] = make_float2(m, l);
+#pragma unroll
+      for (int e = 0; e < kFew; ++e)
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) sums[(warp * kFew + e) * D + lane + 32 * c] = acc[e][c];
+      __syncthreads();
+      float top = -INFINITY, all = 0.f, out[kCh] = {};
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) top = fmaxf(top, stats[v * kFew + warp].x);
+      const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float2 ml = stats[v * kFew + warp];
+        const float f = exp2f(ml.x - base);
+        all = fmaf(ml.y, f, all);
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) out[c] = fmaf(sums[(v * kFew + warp) * D + lane + 32 * c], f, out[c]);
+      }
+      put(warp, top, all, out);
+    } else {
+      int slot[kPer];
+      float m[kPer], l[kPer], acc[kPer][kCh];
+#pragma unroll
+      for (int r = 0; r < kPer; ++r) {
+        const int own = warp * kPer + r;
+        slot[r] = own < it.rows ? w.seq.slot0() + (it.row0 + own) / P.group : -1;
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) acc[r][c] = 0.f;
+      }
+      for (int step = 0; step < steps; ++step) {
+        load(step + 1, row_next);
+        int j_after, row_after;
+        find(step + 2, j_after, row_after);
+        copies_wait<1>();
+        __syncthreads();
+        const float* ks = reinterpret_cast<const float*>(smem + (step & 1) * G::kStage);
+        const float* vs = ks + G::kKeys * G::kRow;
+        float s[kPer];
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) s[r] = 0.f;
+#pragma unroll 8
+        for (int c = 0; c < D / 4; ++c) {
+          const float4 k4 = *reinterpret_cast<const float4*>(ks + lane * G::kRow + c * 4);
+#pragma unroll
+          for (int r = 0; r < kPer; ++r) {
+            const float4 q4 = *reinterpret_cast<const float4*>(qs + (warp * kPer + r) * D + c * 4);
+            s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
+          }
+        }
+        float p[kPer];
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) {
+          const float x = row >= 0 && paged_sees(P.window, P.sinks, slot[r], j) ? s[r] : -INFINITY;
+          float mx = x;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const float m_new = fmaxf(m[r], mx * P.scale_log2);
+          const float ref = m_new == -INFINITY ? 0.f : m_new;
+          const float alpha = exp2f(m[r] - ref);
+          m[r] = m_new;
+          p[r] = exp2f(fmaf(x, P.scale_log2, -ref));
+          l[r] = l[r] * alpha + p[r];
+#pragma unroll
+          for (int c = 0; c < kCh; ++c) acc[r][c] *= alpha;
+        }
+#pragma unroll 4
+        for (int i = 0; i < G::kKeys; ++i) {
+          float v[kCh];
+#pragma unroll
+          for (int c = 0; c < kCh; ++c) v[c] = vs[i * G::kRow + lane + 32 * c];
+#pragma unroll
+          for (int r = 0; r < kPer; ++r) {
+            const float pr = __shfl_sync(0xffffffffu, p[r], i);
+#pragma unroll
+            for (int c = 0; c < kCh; ++c) acc[r][c] = fmaf(pr, v[c], acc[r][c]);
+          }
+        }
+        j = j_next, row = row_next;
+        j_next = j_after, row_next = row_after;
+        __syncthreads();
+      }
+#pragma unroll
+      for (int r = 0; r < kPer; ++r) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+        put(warp * kPer + r, m[r], l[r], acc[r]);
       }
     }
     __syncthreads();
