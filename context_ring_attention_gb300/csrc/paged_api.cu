@@ -128,8 +128,8 @@ ra_status launched(ra_paged_s* kv, cudaError_t e, const char* what, cudaStream_t
   return s != RA_OK ? s : ok();
 }
 
-// CTAs per key/value head of the row kernels: as many as the GPU holds at once (two an SM), and
-// no more than the largest number of shares or items that these sizes can make.  Beside a chunk
+// CTAs per key/value head of the row kernels: as many as the GPU holds at once (two an SM, float32
+// of 64 channels four: one token of 16 sequences of 4k 56 us with two, 46 with four), and no more than the largest number of shares or items that these sizes can make.  Beside a chunk
 // kernel three times as many: it leaves them only some of the SMs, and more as it ends.
 int row_slots(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width, bool beside) {
   const ra_paged_problem& pb = kv->prob;
@@ -139,7 +139,8 @@ int row_slots(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t width
     blocks = std::min(blocks, (pb.window + ra::kRowsTile + pb.sinks) / ra::kRowsBlock + 3);
   const int64_t shares = tiles * blocks / (pb.dtype == RA_DTYPE_BF16 ? 8 : 4);  // as the kernels cut them (tiles below 2^30, blocks up to 2^26)
   const int64_t sms = kv->sm_count > 0 ? kv->sm_count : 148;
-  return (int)std::max<int64_t>(1, std::min({std::max(shares, tiles), (beside ? 6 : 2) * sms / pb.heads_kv, (int64_t)kMaxSlots}));
+  const int64_t per_sm = beside ? 6 : pb.dtype == RA_DTYPE_F32 && pb.head_dim == 64 ? 4 : 2;
+  return (int)std::max<int64_t>(1, std::min({std::max(shares, tiles), per_sm * sms / pb.heads_kv, (int64_t)kMaxSlots}));
 }
 
 // Shares of a CTA of the chunk kernel at most: where more than one item reads a sequence's keys,

@@ -317,8 +317,8 @@ cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, int sm_co
   e = cudaLaunchKernelEx(&config, pick_kernel, prm, (int)(config.dynamicSmemBytes / 4));
   if (e != cudaSuccess) return e;
   const int row_bytes = prm.d * (dtype == RA_DTYPE_BF16 ? 2 : 4);
-  // Pieces of 64 bytes at least, as many as fill the GPU twice; runs of rows until there are six CTAs an SM (two to sixteen are within 4%; below 128 rows a
-  // run is too short for its start).
+  // Pieces of 64 bytes at least, as many as fill the GPU twice; runs of rows until there are six
+  // CTAs an SM (two to sixteen are within 4%; below 128 rows a run is too short for its start).
   int pieces = 1;
   while (row_bytes / pieces > 64 && 2 * pieces * heads < 2 * sm_count) pieces *= 2;
   const int64_t most = (prm.keep + 127) / 128;

@@ -16,8 +16,9 @@
 //
 // Measured (32 query and 8 key/value heads, D 128, bf16): one token of 16 sequences up to 32k
 // (1.27 GB) 190 us, 6.7 TB/s; one token over 1M 598 us, 7.2 TB/s.  float32 has no such instruction
-// to its precision: bound by the CUDA cores' reads of shared memory, one token of 16 sequences of
-// 4k (0.34 GB) 149 us, 2.1 TB/s.
+// to its precision: few rows are bound by the latency of a step of 32 keys, one token of 16
+// sequences of 4k (0.32 GB) 78 us, 4.1 TB/s; many by the reads of shared memory, 500 tokens of 16
+// heads over 4k 773 us, 20 TFLOP/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -395,8 +396,11 @@ __global__ void __launch_bounds__(kThreads) rows_bf16_kernel(const PagedAttendPa
 }
 
 // --------------------------------------------------------------------- float32 --
-// A CTA meets 32 keys (two blocks) at a time; a warp has 4 of the 16 rows, a lane scores one
-// key against them, and then holds D / 32 channels of their outputs.  Which slot and row of the
+// A CTA meets 32 keys (two blocks) at a time.  Items of more than 4 rows: a warp has 4 of the 16
+// rows, a lane scores one key against them, and then holds D / 32 channels of their outputs.  Items
+// of up to 4 (a token of a group of 4): a warp has 8 of the keys and all rows, 4 lanes share a key,
+// and the warps' sums are joined at the end; with the other form, three warps without rows, one
+// token of 16 sequences of 4k took 149 us, of 64k 230 (now 118).  Which slot and row of the
 // cache a step's keys are is read two steps ahead (3 sequences of 300 tokens: 27 -> 23 us).
 template <int D>
 struct F32 {
@@ -408,7 +412,7 @@ struct F32 {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) rows_f32_kernel(const PagedAttendParams P) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) rows_f32_kernel(const PagedAttendParams P) {
   using G = F32<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   float* qs = reinterpret_cast<float*>(smem + 2 * G::kStage);
