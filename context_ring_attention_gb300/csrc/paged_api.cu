@@ -149,7 +149,7 @@ int chunk_rounds(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t wi
   const ra_paged_problem& pb = kv->prob;
   if (tokens <= 2 * (128 / (pb.heads_q / pb.heads_kv))) return 1;
   const int64_t bytes = std::min(batch, tokens) * width * pb.page_rows * pb.heads_kv * 4 / 1024 * pb.head_dim;  // KiB
-  return (int)std::max<int64_t>(1, std::min<int64_t>(ra::kMaxRounds, bytes / (64 << 10)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(ra::kMaxRounds, bytes / (ra::kRoundBytes >> 10)));
 }
 
 // Which kernels a call takes.  A sequence with up to 16 query rows a head belongs to the row

@@ -52,7 +52,6 @@ constexpr int kStages = 3;      // K/V ring
 constexpr int kItemSlots = 4;   // items under way from the record warp to the others
 constexpr int kNotes = 8;       // key tiles' notes from the producer: no role is that far apart
 constexpr int kMinUnits = 2;    // key tiles of a share
-constexpr int64_t kRoundBytes = int64_t(64) << 20;  // of keys and values that a round walks, about half the L2
 constexpr uint32_t kStageRow = 144;  // 128 bytes of an output row, and 16 so that the lanes'
                                      // 16-byte writes fall into different banks
 
@@ -180,8 +179,10 @@ __device__ Shares shares_of(const PagedChunkParams& P, int per_item, int64_t* pr
   s.all = s.per_head * P.t.heads_kv;
   s.ctas = (int)gridDim.x;
   if (others > 0) s.ctas = ctas_beside(s.all, (double)others * P.t.heads_kv * P.row_bytes * 2, s.ctas);
-  // (rounds of 32 tiles a share at least: below that the parts cost more than the reads)
-  const int64_t rounds = max((int64_t)1, min(min((int64_t)P.rounds, s.all / (32 * (int64_t)s.ctas)),
+  // (Rounds of 100 tiles a share at least: below that the parts cost more than the reads.  256 tokens
+  // over 128k with 32 tiles 545 us, 64 459, 100 429; 512 over 64k 487, 402, 423.  2048 tokens over 32k
+  // and 128k without rounds 693 and 3188 us, of 64 MB 656 and 2756, of 44 MB 653 and 2734.)
+  const int64_t rounds = max((int64_t)1, min(min((int64_t)P.rounds, s.all / (100 * (int64_t)s.ctas)),
                                              again * P.t.heads_kv * P.row_bytes * 2 / kRoundBytes));
   s.count = (int)max((int64_t)1, min(rounds * s.ctas, s.all / kMinUnits));
   return s;

@@ -144,6 +144,7 @@ cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, int sm_co
 
 constexpr int kMaxChunkSequences = 2048;  // of a call of the chunk kernels (shared memory)
 constexpr int kMaxRounds = 8;
+constexpr int64_t kRoundBytes = int64_t(44) << 20;  // of keys and values that a round walks, a third of the L2
 
 // Tensor maps of the chunk kernels (paged_maps.cu): rows of d bf16 in boxes of 64 channels by
 // `box` rows; a packed tensor [tokens, heads, d] in boxes of 64 channels, `group` heads and
