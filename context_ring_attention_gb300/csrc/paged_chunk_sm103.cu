@@ -24,8 +24,8 @@
 // TMEM: S0 cols 0-127 (P0 in 64-127), S1 128-255 (P1 in 192-255), O0 256-383, O1 384-511.
 //
 // Bound by the tensor cores (71% of the elapsed cycles busy) with the softmax between their
-// products.  Measured: 2048 tokens of 32 and 8 heads, D 128, over 32k 650 us (1.06e12 operations,
-// 1.64 PFLOP/s), the join with it; with the warp-level instruction 7.5 ms.
+// products.  Measured: 2048 tokens of 32 and 8 heads, D 128, over 32k 654 us (1.06e12 operations,
+// 1.63 PFLOP/s), the join with it; with the warp-level instruction 7.5 ms.
 //
 // Every mbarrier wait is bounded (~1 s).  On expiry the CTA raises an abort flag, records the
 // role in the handle's status word, drains its own in-flight TMA loads and MMAs (bounded
