@@ -473,6 +473,66 @@ def test_another_stream(counts):
     ra.ra_paged_sync_status(t.kv, side)
 
 
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("keep", [40, 1200])
+def test_a_captured_step_under_a_budget(dtype, keep):
+    """A decoding step with its eviction in place, captured and replayed on another stream, against
+    the same calls one by one: every output, the cache and the weights, bit for bit."""
+    b, hq, hk, d, pr, steps = 2, 4, 2, 64, 16, 12
+    rng = np.random.default_rng(keep)
+    lengths = [keep - 5, keep]
+    rows = lambda h: torch.from_numpy(rng.normal(size=(steps, b, h, d))).to(DT[dtype]).cuda()
+    q, k, v = rows(hq), rows(hk), rows(hk)
+    width = -(-(keep + 1) // pr)
+    rope = ra.ra_rope_plan(d, dtype=dtype)
+    runs = []
+    start = torch.from_numpy(rng.normal(size=(b * width, 2, hk, pr, d))).to(DT[dtype]).cuda()
+    heavy = torch.from_numpy(rng.exponential(size=(b, hk, keep + 1))).float().cuda()
+    for captured in (False, True):
+        kv = ra.ra_paged_plan(b * width, pr, hq, hk, d, dtype=dtype)
+        cache, weight = start.clone(), heavy.clone()
+        table, offset = _i32(np.arange(b * width).reshape(b, width)[:, ::-1].copy()), _i32([0, 1, 2])
+        length, position = _i32(lengths), _i32([5000, 70000])
+        x = [torch.zeros_like(t[0]) for t in (q, k, v)]
+        kept, left = torch.zeros((b, hk, keep), dtype=torch.int32, device="cuda"), _i32([0, 0])
+        out = {}
+
+        def step():
+            length.add_(1)
+            turned = ra.ra_paged_append(kv, cache, x[1], x[2], table, offset, length, rope=rope, position=position, q=x[0])
+            out["o"], out["lse"] = ra.ra_paged_attend(kv, cache, turned, table, offset, length)
+            ra.ra_paged_weigh(kv, cache, turned, out["lse"], table, offset, length, weight, weight_in=weight)
+            ra.ra_paged_evict(kv, cache, table, length, weight, keep, first=2, recent=7, kept=kept, new_length=left)
+            length.copy_(left)
+            position.add_(1)
+
+        if captured:
+            torch.cuda.synchronize()
+            graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+            with torch.cuda.graph(graph):
+                step()
+        seen = []
+        for i in range(steps):
+            for t, new in zip(x, (q, k, v)):
+                t.copy_(new[i])
+            if captured:
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    graph.replay()
+                torch.cuda.current_stream().wait_stream(side)
+            else:
+                step()
+            seen.append([out["o"].clone(), out["lse"].clone(), kept.clone(), length.clone()])
+        ra.ra_paged_sync_status(kv)
+        seen.append([cache, weight])
+        runs.append(seen)
+    assert list(runs[0][-2][3].cpu()) == [keep, keep]
+    for one, two in zip(*runs):
+        for x, y in zip(one, two):
+            assert _same_bits(x, y) if x.dtype != torch.int32 else torch.equal(x, y)
+
+
 # ----------------------------------------------------------------------- weights --
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
