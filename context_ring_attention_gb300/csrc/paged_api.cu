@@ -51,7 +51,7 @@ ra_status validate(const ra_paged_problem* p) {
   if (p->heads_q % p->heads_kv) return fail(RA_ERR_INVALID_ARG, "heads_q %% heads_kv != 0");
   if (p->dtype != RA_DTYPE_F32 && p->dtype != RA_DTYPE_BF16) return fail(RA_ERR_INVALID_ARG, "unknown dtype %d", p->dtype);
   if (p->window < 0 || p->sinks < 0) return fail(RA_ERR_INVALID_ARG, "window and sinks must be >= 0");
-  // (LSE / scale and scores stay finite)
+  // (LSE / scale and the scores stay finite)
   if (!(p->scale == 0.f || (p->scale >= 0x1p-100f && p->scale <= 0x1p100f)))
     return fail(RA_ERR_INVALID_ARG, "scale must be 0 or in 2^-100..2^100");
   if (p->head_dim != 64 && p->head_dim != 128)

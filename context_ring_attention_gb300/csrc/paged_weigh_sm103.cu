@@ -16,8 +16,11 @@
 //
 // Bound by the tensor cores and the exponentials alike (69% and 64% of the cycles busy, 55% of the
 // issue slots).  Measured: 1000 tokens of 32 and 8 heads, D 128, over 32k 186 us (2.6e11 operations,
-// 1.42 PFLOP/s); with the extra channels made by a warp of this kernel 250, with every tile asked
-// whether it needs a mask 189, with the warp-level instruction 3.5 ms.
+// 1.42 PFLOP/s), 4000 tokens 641 us (1.61).  With the LSE subtracted by the warps that sum, from
+// shared memory, 219 (the product is shorter by its ninth part, the sums longer); with the second
+// half of a warp's scores read behind the first's exponentials 192 (the products wait for it); with the
+// extra channels made by a warp of this kernel 250, with every tile asked whether it needs a mask
+// 189, with the warp-level instruction 3.5 ms.
 //
 // Roles (one CTA per SM, 20 warps): warp 0 TMA producer, warp 1 tcgen05 issuer, warp 2 the
 // items' records, warps 4-19 sums: four for each key tile and half of the columns (two threads
