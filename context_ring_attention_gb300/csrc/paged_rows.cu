@@ -18,7 +18,8 @@
 // (1.27 GB) 190 us, 6.7 TB/s; one token over 1M 598 us, 7.2 TB/s.  float32 has no such instruction
 // to its precision: few rows are bound by the latency of a step of 32 keys, one token of 16
 // sequences of 4k (0.32 GB) 78 us, 4.1 TB/s; many by the reads of shared memory, 500 tokens of 16
-// heads over 4k 773 us, 20 TFLOP/s.
+// heads over 4k 715 us, 22 TFLOP/s (a step's weights handed on by shuffles, not through shared
+// memory: 773).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -408,8 +409,24 @@ struct F32 {
   static constexpr int kKeys = 2 * kRowsBlock;
   static constexpr int kStage = 2 * kKeys * kRow * 4;
   static constexpr int kQ = kRowsTile * D * 4;
-  static constexpr int kBytes = 2 * kStage + kQ;
+  static constexpr int kP = kWarps * kKeys * 16;  // a step's weights of 4 rows
+  static constexpr int kBytes = 2 * kStage + kQ + kP;
 };
+// D / 32 channels that follow each other.
+__device__ __forceinline__ void load_channels(float (&x)[4], const float* p) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void load_channels(float (&x)[2], const float* p) {
+  const float2 v = *reinterpret_cast<const float2*>(p);
+  x[0] = v.x, x[1] = v.y;
+}
+__device__ __forceinline__ void store_channels(float* p, const float (&x)[4], float f) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+}
+__device__ __forceinline__ void store_channels(float* p, const float (&x)[2], float f) {
+  *reinterpret_cast<float2*>(p) = make_float2(x[0] * f, x[1] * f);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) rows_f32_kernel(const PagedAttendParams P) {
@@ -418,13 +435,14 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) rows_f32_kernel(con
   float* qs = reinterpret_cast<float*>(smem + 2 * G::kStage);
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + G::kBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
+  float4* ps = reinterpret_cast<float4*>(smem + 2 * G::kStage + G::kQ) + warp * G::kKeys;  // of this warp's keys
   next_may_come();
   if (P.joins != nullptr && threadIdx.x == 0) P.joins[(int64_t)head * P.slots + blockIdx.x] = make_int4(0, 0, 0, 0);
   Walk w;
   if (!walk_begin<float>(P, prefix, w)) return;
   const float* cache = static_cast<const float*>(P.t.cache);
   constexpr int kPer = kRowsTile / kWarps, kCh = D / 32, kFew = 4;
-  static_assert(kFew == kWarps && kWarps * 8 == G::kKeys, "a warp for 8 keys, and for a row in the end");
+  static_assert(kPer == 4 && kFew == kWarps && kWarps * 8 == G::kKeys, "4 rows a float4; a warp for 8 keys, and for a row in the end");
 
   for (;; walk_next(P, prefix, w)) {
     const PagedItem it = paged_item<kRowsTile>(w.seq, P.group, w.tile);
@@ -476,18 +494,15 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) rows_f32_kernel(con
     find(1, j_next, row_next);
     const bool cut = u0 > 0 || u1 < n;
     const int64_t part = cut ? part_at(P, w, it, u0, n) : 0;
-    // Row `at` of the item, of which this lane has the channels lane, lane + 32 ..
+    // Row `at` of the item, of which this lane has kCh channels.
     auto put = [&](int at, float m, float l, const float (&acc)[kCh]) {
       if (cut) {
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) P.part_o[(part * kRowsTile + at) * D + lane + 32 * c] = acc[c];
+        store_channels(P.part_o + (part * kRowsTile + at) * D + lane * kCh, acc, 1.0f);
         if (lane == 0) P.part_ml[part * kRowsTile + at] = make_float2(m, l);
       } else if (at < it.rows) {
         const int row = row0 + at;
         const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
-        float* dst = row_of<float>(P.os, P.o, P.group, head, row);
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) dst[lane + 32 * c] = acc[c] * inv;
+        store_channels(row_of<float>(P.os, P.o, P.group, head, row) + lane * kCh, acc, inv);
         if (lane == 0 && P.lse != nullptr) {
           const int token = row / P.group;
           P.lse[(int64_t)token * P.heads_q + head * P.group + row - token * P.group] =
@@ -546,16 +561,19 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) rows_f32_kernel(con
             for (int c = 0; c < kCh; ++c) acc[e][c] *= f;
           }
         }
+        reinterpret_cast<float*>(ps)[order * 4 + r] = p;
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float v[kCh];
+          load_channels(v, vs + (warp * 8 + i) * G::kRow + lane * kCh);
+          const float4 p4 = ps[i];
 #pragma unroll
-          for (int c = 0; c < kCh; ++c) v[c] = vs[(warp * 8 + (i >> 1) + 4 * (i & 1)) * G::kRow + lane + 32 * c];
-#pragma unroll
-          for (int e = 0; e < kFew; ++e) {
-            const float pr = __shfl_sync(0xffffffffu, p, i * 4 + e);
-#pragma unroll
-            for (int c = 0; c < kCh; ++c) acc[e][c] = fmaf(pr, v[c], acc[e][c]);
+          for (int c = 0; c < kCh; ++c) {
+            acc[0][c] = fmaf(p4.x, v[c], acc[0][c]);
+            acc[1][c] = fmaf(p4.y, v[c], acc[1][c]);
+            acc[2][c] = fmaf(p4.z, v[c], acc[2][c]);
+            acc[3][c] = fmaf(p4.w, v[c], acc[3][c]);
           }
         }
         j = j_next, row = row_next;
@@ -571,9 +589,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) rows_f32_kernel(con
       __syncthreads();
       if (lane < kFew) stats[warp * kFew + lane] = make_float2(m, l);
 #pragma unroll
-      for (int e = 0; e < kFew; ++e)
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) sums[(warp * kFew + e) * D + lane + 32 * c] = acc[e][c];
+      for (int e = 0; e < kFew; ++e) store_channels(sums + (warp * kFew + e) * D + lane * kCh, acc[e], 1.0f);
       __syncthreads();
       float top = -INFINITY, all = 0.f, out[kCh] = {};
 #pragma unroll
@@ -584,8 +600,10 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) rows_f32_kernel(con
         const float2 ml = stats[v * kFew + warp];
         const float f = exp2f(ml.x - base);
         all = fmaf(ml.y, f, all);
+        float x[kCh];
+        load_channels(x, sums + (v * kFew + warp) * D + lane * kCh);
 #pragma unroll
-        for (int c = 0; c < kCh; ++c) out[c] = fmaf(sums[(v * kFew + warp) * D + lane + 32 * c], f, out[c]);
+        for (int c = 0; c < kCh; ++c) out[c] = fmaf(x[c], f, out[c]);
       }
       put(warp, top, all, out);
     } else {
@@ -636,16 +654,19 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) rows_f32_kernel(con
 #pragma unroll
           for (int c = 0; c < kCh; ++c) acc[r][c] *= alpha;
         }
-#pragma unroll 4
+        ps[lane] = make_float4(p[0], p[1], p[2], p[3]);
+        __syncwarp();
+#pragma unroll 8
         for (int i = 0; i < G::kKeys; ++i) {
           float v[kCh];
+          load_channels(v, vs + i * G::kRow + lane * kCh);
+          const float4 p4 = ps[i];
 #pragma unroll
-          for (int c = 0; c < kCh; ++c) v[c] = vs[i * G::kRow + lane + 32 * c];
-#pragma unroll
-          for (int r = 0; r < kPer; ++r) {
-            const float pr = __shfl_sync(0xffffffffu, p[r], i);
-#pragma unroll
-            for (int c = 0; c < kCh; ++c) acc[r][c] = fmaf(pr, v[c], acc[r][c]);
+          for (int c = 0; c < kCh; ++c) {
+            acc[0][c] = fmaf(p4.x, v[c], acc[0][c]);
+            acc[1][c] = fmaf(p4.y, v[c], acc[1][c]);
+            acc[2][c] = fmaf(p4.z, v[c], acc[2][c]);
+            acc[3][c] = fmaf(p4.w, v[c], acc[3][c]);
           }
         }
         j = j_next, row = row_next;
