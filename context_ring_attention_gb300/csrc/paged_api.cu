@@ -431,8 +431,9 @@ ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_
   s = check_call(kv, batch, tokens, table_width, t16, 3, t4, 6, st);
   if (s != RA_OK) return s;
   prm.t = table_of(kv, cache, batch, tokens, page_table, table_width, offset, length);
+  ra::PagedWeighChunkParams c{};
+  const int grid = chunk_grid(kv);
   if (route.chunks) {
-    ra::PagedWeighChunkParams c{};
     c.t = prm.t;
     c.t.few = route.rows ? ra::kManyOnly : ra::kAllRows;
     c.heads_q = pb.heads_q;
@@ -448,17 +449,13 @@ ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_
     c.weight_in = weight_in;
     c.weight = weight;
     c.weight_width = weight_width;
-    const int grid = chunk_grid(kv);
     c.tiles = (int32_t)weigh_tiles(kv, batch, tokens);
     c.extra = reinterpret_cast<uint4*>(scratch);
     c.parts = scratch + (int64_t)pb.heads_kv * c.tiles * 128 * 4;
     c.joins = reinterpret_cast<ra::PagedWeighJoin*>(c.parts + (int64_t)grid * 2 * 256);
     c.extra_at = reinterpret_cast<int32_t*>(c.joins + grid);
-    const char* why = "";
-    const cudaError_t e = ra::launch_paged_weigh_chunk(pb.head_dim, c, grid, st, &why);
-    if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache weights: %s (%s)", why, cudaGetErrorString(e));
-    if (!route.rows) return launched(kv, e, "cache weights", st);
     prm.t.few = ra::kFewOnly;
+    prm.beside = 1;
   }
   prm.heads_q = pb.heads_q;
   prm.group = pb.heads_q / pb.heads_kv;
@@ -470,7 +467,13 @@ ra_status ra_paged_weigh(ra_paged_t kv, const void* cache, int64_t batch, int64_
   prm.weight_in = weight_in;
   prm.weight = weight;
   prm.weight_width = weight_width;
-  return launched(kv, ra::launch_paged_weigh_rows(pb.dtype, pb.head_dim, prm, kv->sm_count, st), "cache weights launch", st);
+  const char* why = "";
+  cudaError_t e = cudaSuccess;
+  if (route.chunks) e = ra::launch_paged_weigh_chunk(pb.head_dim, c, grid, st, &why);
+  if (e == cudaSuccess && route.rows) e = ra::launch_paged_weigh_rows(pb.dtype, pb.head_dim, prm, kv->sm_count, st);
+  if (e == cudaSuccess && route.chunks) e = ra::launch_paged_weigh_join(c, grid, st);
+  if (e != cudaSuccess) return fail(RA_ERR_CUDA, "cache weights launch: %s %s", cudaGetErrorString(e), why);
+  return launched(kv, e, "cache weights launch", st);
 }
 
 ra_status ra_paged_evict(ra_paged_t kv, void* cache, int64_t batch, const int32_t* page_table, int64_t table_width,

@@ -91,6 +91,7 @@ struct PagedWeighParams {
   const float* weight_in;  // [batch, heads_kv, weight_width] or nullptr
   float* weight;
   int64_t weight_width;
+  int32_t beside;          // as in PagedAttendParams (bf16)
 };
 
 // An item that share x of the chunk kernel begins and does not end (last < 0: none).
@@ -140,6 +141,7 @@ cudaError_t launch_paged_weigh_rows(int dtype, int head_dim, const PagedWeighPar
                                     cudaStream_t stream);
 cudaError_t launch_paged_weigh_chunk(int head_dim, const PagedWeighChunkParams& prm, int grid, cudaStream_t stream,
                                      const char** why);
+cudaError_t launch_paged_weigh_join(const PagedWeighChunkParams& prm, int grid, cudaStream_t stream);
 cudaError_t launch_paged_evict(int dtype, const PagedEvictParams& prm, int sm_count, cudaStream_t stream);
 
 constexpr int kMaxChunkSequences = 2048;  // of a call of the chunk kernels (shared memory)

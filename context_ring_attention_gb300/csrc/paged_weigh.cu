@@ -120,13 +120,18 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
   extern __shared__ __align__(128) uint8_t smem_bytes[];
   uint8_t* smem = smem_bytes;
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + kWarps * kStages * kStageBytes);
+  next_may_come();
+  // Where this kernel runs beside a chunk kernel: its end, that of one CTA of it, comes after the other's.
+  auto end_after_others = [&] {
+    if (P.beside && blockIdx.x == 0 && blockIdx.y == 0) after_previous();
+  };
   slot_prefix<kStepKeys>(P.t, P.group, prefix);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
   const int quad = lane >> 2, two = (lane & 3) * 2;
   const int64_t all = prefix[P.t.batch], me = (int64_t)blockIdx.x * kWarps + warp, runs = (int64_t)gridDim.x * kWarps;
   const int64_t x0 = all * me / runs;
   const int n = (int)(all * (me + 1) / runs - x0);
-  if (n <= 0) return;
+  if (n <= 0) return end_after_others();
   const uint32_t ring = ptx::smem_addr(smem) + warp * kStages * kStageBytes;
   int b_first = 0;  // sequence of the run's first block
   for (int end = P.t.batch; end - b_first > 1;) {
@@ -286,6 +291,7 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
     }
     __syncwarp();
   }
+  end_after_others();
 }
 
 // A lane has a key, in shared memory; a warp has a tile of 16 query rows in shared memory of its
@@ -424,7 +430,10 @@ cudaError_t launch(Kernel kernel, std::atomic<int>* ready, const PagedWeighParam
     if (e != cudaSuccess) return e;
     if (cached) ready[dev].store(1, std::memory_order_release);
   }
-  kernel<<<dim3(slots, (unsigned)prm.t.heads_kv), kThreads, bytes + (prm.t.batch + 1) * 8, stream>>>(prm);
+  const dim3 grid(slots, (unsigned)prm.t.heads_kv);
+  const int all = bytes + (prm.t.batch + 1) * 8;
+  if (prm.beside) return launch_behind(kernel, grid, kThreads, all, stream, prm);
+  kernel<<<grid, kThreads, all, stream>>>(prm);
   return cudaGetLastError();
 }
 template <int D>

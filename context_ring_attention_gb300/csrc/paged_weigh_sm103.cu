@@ -684,12 +684,15 @@ cudaError_t launch(const PagedWeighChunkParams& prm, int grid, cudaStream_t stre
   }
   e = launch_behind(paged_weigh_chunk_kernel<D>, dim3((unsigned)grid), kThreads,
                     (size_t)Smem<D>::kFixed + (prm.t.batch + 1) * 8, stream, tq, tkv, prm);
-  if (e == cudaSuccess) e = launch_behind(paged_weigh_join_kernel, dim3((unsigned)grid), kPair, 0, stream, prm);
   if (e != cudaSuccess) *why = "launch failed";
   return e;
 }
 
 }  // namespace
+
+cudaError_t launch_paged_weigh_join(const PagedWeighChunkParams& prm, int grid, cudaStream_t stream) {
+  return launch_behind(paged_weigh_join_kernel, dim3((unsigned)grid), kPair, 0, stream, prm);
+}
 
 cudaError_t launch_paged_weigh_chunk(int head_dim, const PagedWeighChunkParams& prm, int grid, cudaStream_t stream,
                                      const char** why) {
