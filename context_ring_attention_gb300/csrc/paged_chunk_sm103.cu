@@ -24,8 +24,8 @@
 // TMEM: S0 cols 0-127 (P0 in 64-127), S1 128-255 (P1 in 192-255), O0 256-383, O1 384-511.
 //
 // Bound by the tensor cores (71% of the elapsed cycles busy) with the softmax between their
-// products.  Measured: 2048 tokens of 32 and 8 heads, D 128, over 32k 654 us (1.06e12 operations,
-// 1.63 PFLOP/s), the join with it; with the warp-level instruction 7.5 ms.
+// products.  Measured: 2048 tokens of 32 and 8 heads, D 128, over 32k 651 us (1.06e12 operations,
+// 1.64 PFLOP/s), the join with it; with the warp-level instruction 7.5 ms.
 //
 // Every mbarrier wait is bounded (~1 s).  On expiry the CTA raises an abort flag, records the
 // role in the handle's status word, drains its own in-flight TMA loads and MMAs (bounded
@@ -783,14 +783,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- cut items --
 // The items that shares begin and do not end: an item's first part is there, the others at the
-// beginning of the shares up to the last.  A CTA has 32 rows (its lanes): the warps bring the
-// parts' statistics side by side, then add columns of 4 channels, a few parts under way.
-constexpr int kJoinWarps = 16;
-constexpr int kJoinCtas = 2;  // for a share's 8 times 32 rows (8: 512 tokens and 31 single ones 190 us, 4: 189, 2: 188, 1: 193)
+// beginning of the shares up to the last.  A warp has 32 rows, a lane each, and kJoinCols columns of
+// 4 channels of them, and folds the parts in order, kJoinParts at a time, with the running maximum.
+// Small CTAs, many for a share: an item may be cut into a part for every CTA of the GPU, and then
+// there are few such items (20 tokens over 60k of one head 43 us, with 8 CTAs of 16 warps a share 60,
+// with 2 139; with 8 parts at a time 41, but 2048 tokens over 32k 656 us instead of 651).
+constexpr int kJoinWarps = 4, kJoinCols = 2, kJoinParts = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_chunk_join_kernel(const PagedChunkParams P, int shares) {
-  __shared__ float tops[kJoinWarps][32];
-  __shared__ float2 sums[kJoinWarps][32];
   after_previous();
   const int per_tile = kTile / P.group;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -798,91 +798,64 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_chunk_join_kernel(const
   static_assert(kMaxRounds <= 32, "a lane each");
   PagedJoin own{0, 0, 0, 0};
   if (lane < kMaxRounds && (int)blockIdx.x + lane * (int)gridDim.x < shares) own = P.joins[blockIdx.x + lane * gridDim.x];
-  const uint32_t any = __ballot_sync(0xffffffffu, own.tokens != 0);
-  for (int y = (int)blockIdx.y; any && y < 8; y += (int)gridDim.y) {
-    const int g = y >> 2, in_tile = (y & 3) * 32 + lane;  // this lane's row of both tiles
-    const int token = in_tile / P.group;
-    for (uint32_t some = any; some; some &= some - 1) {
-      const int k = __ffs(some) - 1, s = (int)blockIdx.x + k * (int)gridDim.x;
-      const PagedJoin rec{__shfl_sync(0xffffffffu, own.head, k), __shfl_sync(0xffffffffu, own.token, k),
-                          __shfl_sync(0xffffffffu, own.tokens, k), __shfl_sync(0xffffffffu, own.last, k)};
-      const int count = rec.last - s + 1;
-      const bool live = token < per_tile && g * per_tile + token < rec.tokens;
-      auto row_of = [&](int i) { return ((i == 0 ? 2 * s + 1 : 2 * (s + i)) * 2 + g) * kTile + in_tile; };
-      const int at = rec.token + g * per_tile + token, head = rec.head * P.group + in_tile - token * P.group;
-      constexpr int kCols = D / 4 / kJoinWarps;  // column groups of a warp
-      const float4* parts = reinterpret_cast<const float4*>(P.part_o) + (int64_t)(warp * kCols) * kTile + in_tile;
-      auto part = [&](int i, int q) { return parts[(int64_t)(row_of(i) >> 7) * (D / 4) * kTile + q * kTile]; };
-      float m = -INFINITY;
-      float2 lf = make_float2(0.f, 0.f);  // the sum, its correction
-      float4 x[kCols];
+  const int g = (int)blockIdx.y >> 2, in_tile = ((int)blockIdx.y & 3) * 32 + lane;  // this lane's row of both tiles
+  const int token = in_tile / P.group;
+  const int col = ((int)blockIdx.z * kJoinWarps + warp) * kJoinCols;
+  for (uint32_t some = __ballot_sync(0xffffffffu, own.tokens != 0); some; some &= some - 1) {
+    const int k = __ffs(some) - 1, s = (int)blockIdx.x + k * (int)gridDim.x;
+    const PagedJoin rec{__shfl_sync(0xffffffffu, own.head, k), __shfl_sync(0xffffffffu, own.token, k),
+                        __shfl_sync(0xffffffffu, own.tokens, k), __shfl_sync(0xffffffffu, own.last, k)};
+    if (token >= per_tile || g * per_tile + token >= rec.tokens) continue;
+    const int count = rec.last - s + 1;
+    auto tile_of = [&](int i) { return (i == 0 ? 2 * s + 1 : 2 * (s + i)) * 2 + g; };
+    const int at = rec.token + g * per_tile + token, head = rec.head * P.group + in_tile - token * P.group;
+    const float4* parts = reinterpret_cast<const float4*>(P.part_o) + (int64_t)col * kTile + in_tile;
+    float m = -INFINITY;
+    float2 lf = make_float2(0.f, 0.f);  // the sum, its correction
+    float4 x[kJoinCols];
 #pragma unroll
-      for (int q = 0; q < kCols; ++q) x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](float4& a, const float4& y, float f) {
-        a.x = fmaf(y.x, f, a.x), a.y = fmaf(y.y, f, a.y), a.z = fmaf(y.z, f, a.z), a.w = fmaf(y.w, f, a.w);
-      };
-      constexpr int kFew = 4;
-      if (count <= kFew) {  // the usual case: everything is read at once
-        float4 ml[kFew], y[kFew][kCols];
+    for (int q = 0; q < kJoinCols; ++q) x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < count; i0 += kJoinParts) {
+      float4 ml[kJoinParts], y[kJoinParts][kJoinCols];
 #pragma unroll
-        for (int i = 0; i < kFew; ++i)
-          if (live && i < count) {
-            ml[i] = P.part_ml[row_of(i)];
+      for (int i = 0; i < kJoinParts; ++i) {
+        ml[i].x = -INFINITY;
+        if (i0 + i < count) {
+          const int tile = tile_of(i0 + i);
+          ml[i] = P.part_ml[tile * kTile + in_tile];
 #pragma unroll
-            for (int q = 0; q < kCols; ++q) y[i][q] = part(i, q);
-          }
-#pragma unroll
-        for (int i = 0; i < kFew; ++i)
-          if (live && i < count) m = fmaxf(m, ml[i].x);
-        const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int i = 0; i < kFew; ++i)
-          if (live && i < count) {
-            const float f = exp2f(ml[i].x - ref);
-            lf.x = fmaf(ml[i].y, f, lf.x);
-            lf.y = fmaf(ml[i].z, f, lf.y);
-#pragma unroll
-            for (int q = 0; q < kCols; ++q) add(x[q], y[i][q], f);
-          }
-      } else {
-        for (int i = warp; i < count; i += kJoinWarps)
-          if (live) m = fmaxf(m, P.part_ml[row_of(i)].x);
-        tops[warp][lane] = m;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) m = fmaxf(m, tops[i][lane]);
-        const float ref = m == -INFINITY ? 0.f : m;
-        for (int i = warp; i < count; i += kJoinWarps)
-          if (live) {
-            const float4 ml = P.part_ml[row_of(i)];
-            const float f = exp2f(ml.x - ref);
-            lf.x = fmaf(ml.y, f, lf.x);
-            lf.y = fmaf(ml.z, f, lf.y);
-          }
-        sums[warp][lane] = lf;
-        __syncthreads();
-        lf = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) lf.x += sums[i][lane].x, lf.y += sums[i][lane].y;
-        if (live) {
-#pragma unroll 4
-          for (int i = 0; i < count; ++i) {
-            const float f = exp2f(P.part_ml[row_of(i)].x - ref);
-#pragma unroll
-            for (int q = 0; q < kCols; ++q) add(x[q], part(i, q), f);
-          }
+          for (int q = 0; q < kJoinCols; ++q) y[i][q] = parts[((int64_t)tile * (D / 4) + q) * kTile];
         }
-        __syncthreads();  // (the shared memory is free for the next item)
       }
-      if (!live) continue;
-      const float l = lf.x, inv = l == 0.f ? 0.f : 1.0f / (l + lf.y);
-      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.o) + at * P.os.token + head * P.os.head + warp * kCols * 4);
+      float top = m;
 #pragma unroll
-      for (int q = 0; q < kCols; ++q)
-        dst[q] = make_uint2(ptx::pack_bf16x2(x[q].x * inv, x[q].y * inv), ptx::pack_bf16x2(x[q].z * inv, x[q].w * inv));
-      if (warp == 0 && P.lse != nullptr)
-        P.lse[(int64_t)at * P.heads_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      for (int i = 0; i < kJoinParts; ++i) top = fmaxf(top, ml[i].x);
+      const float ref = top == -INFINITY ? 0.f : top, alpha = exp2f(m - ref);
+      m = top;
+      lf.x *= alpha;
+      lf.y *= alpha;
+#pragma unroll
+      for (int q = 0; q < kJoinCols; ++q) x[q].x *= alpha, x[q].y *= alpha, x[q].z *= alpha, x[q].w *= alpha;
+#pragma unroll
+      for (int i = 0; i < kJoinParts; ++i) {
+        if (i0 + i >= count) break;
+        const float f = exp2f(ml[i].x - ref);
+        lf.x = fmaf(ml[i].y, f, lf.x);
+        lf.y = fmaf(ml[i].z, f, lf.y);
+#pragma unroll
+        for (int q = 0; q < kJoinCols; ++q) {
+          x[q].x = fmaf(y[i][q].x, f, x[q].x), x[q].y = fmaf(y[i][q].y, f, x[q].y);
+          x[q].z = fmaf(y[i][q].z, f, x[q].z), x[q].w = fmaf(y[i][q].w, f, x[q].w);
+        }
+      }
     }
+    const float l = lf.x, inv = l == 0.f ? 0.f : 1.0f / (l + lf.y);
+    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.o) + at * P.os.token + head * P.os.head + col * 4);
+#pragma unroll
+    for (int q = 0; q < kJoinCols; ++q)
+      dst[q] = make_uint2(ptx::pack_bf16x2(x[q].x * inv, x[q].y * inv), ptx::pack_bf16x2(x[q].z * inv, x[q].w * inv));
+    if (col == 0 && P.lse != nullptr)
+      P.lse[(int64_t)at * P.heads_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -913,7 +886,7 @@ cudaError_t launch_paged_chunk(int head_dim, const PagedChunkParams& prm, int gr
 }
 
 cudaError_t launch_paged_chunk_join(int head_dim, const PagedChunkParams& prm, int grid, cudaStream_t stream) {
-  const dim3 blocks((unsigned)grid, kJoinCtas);
+  const dim3 blocks((unsigned)grid, 8, (unsigned)(head_dim / 4 / (kJoinWarps * kJoinCols)));
   const int shares = grid * prm.rounds;
   return head_dim == 128 ? launch_behind(paged_chunk_join_kernel<128>, blocks, kJoinWarps * 32, 0, stream, prm, shares)
                          : launch_behind(paged_chunk_join_kernel<64>, blocks, kJoinWarps * 32, 0, stream, prm, shares);
