@@ -39,7 +39,7 @@ ra_status ok() {
 }
 
 constexpr int64_t kMaxPositions = int64_t(1) << 30;  // of a sequence: slot arithmetic stays in 32 bits
-constexpr int kMaxSlots = 512;                       // CTAs of a key/value head (the join's shared memory)
+constexpr int kMaxSlots = 512;                       // CTAs of a key/value head
 // Of a sequence in the chunk kernels, so that an item, 2^18 tiles at most, ends well within their wait budget.
 constexpr int64_t kMaxChunkSlots = int64_t(1) << 25, kMaxChunkTiles = int64_t(1) << 18;
 

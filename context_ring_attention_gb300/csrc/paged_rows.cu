@@ -688,47 +688,70 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) rows_f32_kernel(con
 
 // ---------------------------------------------------------------- cut items --
 // The item that slot x's share begins and does not end: its first part there, the others at the
-// beginning of the slots up to the last.  A warp brings the statistics of a row's parts at once,
-// then a thread adds 4 channels of a row, eight parts under way.
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowsTile * 32) rows_join_kernel(const PagedAttendParams P) {
-  extern __shared__ float factors[];  // [parts, kRowsTile]
-  __shared__ float2 totals[kRowsTile];
+// beginning of the slots up to the last.  A row has kJoinSplit warps, each of which folds its parts,
+// every kJoinSplit-th, with the running maximum, 8 at a time; the warps' sums are added in order.
+constexpr int kJoinParts = 8, kJoinThreads = 512;
+template <typename T, int D, int kJoinSplit>
+__global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const PagedAttendParams P) {
+  constexpr int kJoinRows = kJoinThreads / 32 / kJoinSplit;  // of a CTA
+  __shared__ float4 sums[kJoinRows * kJoinSplit][D / 4];
+  __shared__ float2 stats[kJoinRows * kJoinSplit];
   const int head = (int)blockIdx.y;
   const int64_t me = (int64_t)head * P.slots + blockIdx.x;
   after_previous();
   const int4 rec = P.joins[me];
-  if (rec.y == 0) return;
+  if (rec.y <= (int)blockIdx.z * kJoinRows) return;
   const int count = rec.z - (int)blockIdx.x + 1;
-  auto part = [&](int i, int r) { return (i == 0 ? me * 2 + 1 : (me + i) * 2) * kRowsTile + r; };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  {
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < count; i += 32) m = fmaxf(m, P.part_ml[part(i, warp)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    for (int i = lane; i < count; i += 32) {
-      const float2 ml = P.part_ml[part(i, warp)];
-      const float f = exp2f(ml.x - ref);
-      factors[i * kRowsTile + warp] = f;
-      l = fmaf(ml.y, f, l);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) totals[warp] = make_float2(m, l);
-  }
-  __syncthreads();
-  const int r = threadIdx.x / (D / 4), ch = threadIdx.x % (D / 4);
-  if (r >= rec.y) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = lane % (D / 4);
+  const int r = (int)blockIdx.z * kJoinRows + warp / kJoinSplit, first = warp % kJoinSplit;
+  auto part = [&](int i) { return (i == 0 ? me * 2 + 1 : (me + i) * 2) * kRowsTile + r; };
+  float m = -INFINITY, l = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = 0; i < count; ++i) {
-    const float f = factors[i * kRowsTile + r];
-    const float4 y = *reinterpret_cast<const float4*>(P.part_o + part(i, r) * D + ch * 4);
+  if (r < rec.y) {
+    for (int i0 = first; i0 < count; i0 += kJoinSplit * kJoinParts) {
+      float2 ml[kJoinParts];
+      float4 y[kJoinParts];
+#pragma unroll
+      for (int e = 0; e < kJoinParts; ++e) {
+        const int i = i0 + e * kJoinSplit;
+        ml[e] = make_float2(-INFINITY, 0.f);
+        y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < count) {
+          ml[e] = P.part_ml[part(i)];
+          y[e] = *reinterpret_cast<const float4*>(P.part_o + part(i) * D + ch * 4);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int e = 0; e < kJoinParts; ++e) top = fmaxf(top, ml[e].x);
+      const float ref = top == -INFINITY ? 0.f : top, alpha = exp2f(m - ref);
+      m = top;
+      l *= alpha;
+      x.x *= alpha, x.y *= alpha, x.z *= alpha, x.w *= alpha;
+#pragma unroll
+      for (int e = 0; e < kJoinParts; ++e) {
+        const float f = exp2f(ml[e].x - ref);
+        l = fmaf(ml[e].y, f, l);
+        x.x = fmaf(y[e].x, f, x.x), x.y = fmaf(y[e].y, f, x.y), x.z = fmaf(y[e].z, f, x.z), x.w = fmaf(y[e].w, f, x.w);
+      }
+    }
+  }
+  if (lane < D / 4) sums[warp][ch] = x;
+  if (lane == 0) stats[warp] = make_float2(m, l);
+  __syncthreads();
+  if (first != 0 || r >= rec.y || lane >= D / 4) return;
+  m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kJoinSplit; ++e) m = fmaxf(m, stats[warp + e].x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < kJoinSplit; ++e) {
+    const float f = exp2f(stats[warp + e].x - ref);
+    const float4 y = sums[warp + e][ch];
+    l = fmaf(stats[warp + e].y, f, l);
     x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
   }
-  const float m = totals[r].x, l = totals[r].y;
   const int row = rec.x + r;
   const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
   T* dst = row_of<T>(P.os, P.o, P.group, head, row) + ch * 4;
@@ -777,8 +800,12 @@ cudaError_t launch(const PagedAttendParams& prm, bool beside, cudaStream_t strea
 template <typename T, int D>
 cudaError_t launch_join(const PagedAttendParams& prm, cudaStream_t stream) {
   if (prm.slots == 1) return cudaSuccess;
+  // Of many shares a head an item may be cut into as many parts: one token over 60k of one head, 304
+  // parts, 27 us, with a warp a row 50.  With few shares more CTAs only cost their start: one of 512
+  // tokens and 31 single ones 195 us, with a warp a row 189.
   const dim3 grid((unsigned)prm.slots, (unsigned)prm.t.heads_kv);
-  return launch_behind(rows_join_kernel<T, D>, grid, kRowsTile * 32, (size_t)prm.slots * kRowsTile * 4, stream, prm);
+  if (prm.slots <= 128) return launch_behind(rows_join_kernel<T, D, 1>, grid, kJoinThreads, 0, stream, prm);
+  return launch_behind(rows_join_kernel<T, D, 4>, dim3(grid.x, grid.y, 4), kJoinThreads, 0, stream, prm);
 }
 
 }  // namespace
