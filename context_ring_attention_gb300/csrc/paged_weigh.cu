@@ -296,27 +296,27 @@ __global__ void __launch_bounds__(kThreads) weigh_bf16_kernel(const PagedWeighPa
 
 // A lane has a key, in shared memory; a warp has a tile of 16 query rows in shared memory of its
 // own, where all lanes read a row's value at once: a key's value enters as many products as there
-// are rows.  kFew: each warp has 32 keys and goes through all tiles.  Otherwise the CTA has 32
-// keys and its warps take the tiles in turn; their sums are added in order.
-template <int D, bool kFew>
+// are rows.  kFew: each of the CTA's kTeam warps has 32 keys and goes through all tiles.  Otherwise
+// the CTA has 32 keys and its warps take the tiles in turn; their sums are added in order.
+template <int D, bool kFew, int kTeam>
 struct F32 {
-  static constexpr int kOwn = kFew ? kWarps * kKeys : kKeys;  // keys of the CTA
+  static constexpr int kOwn = kFew ? kTeam * kKeys : kKeys;  // keys of the CTA
   static constexpr int kRow = D + 4;  // floats; 8 lanes' 16-byte reads of a column fall into different banks
   static constexpr int kKeyBytes = kOwn * kRow * 4;
   static constexpr int kWarpBytes = 16 * D * 4 + 2 * 16 * 4;
-  static constexpr int kBytes = kKeyBytes + kWarps * kWarpBytes + (kFew ? 0 : kWarps * kKeys * 4);
+  static constexpr int kBytes = kKeyBytes + kTeam * kWarpBytes + (kFew ? 0 : kTeam * kKeys * 4);
 };
 
-template <int D, bool kFew>
-__global__ void __launch_bounds__(kThreads) weigh_f32_kernel(const PagedWeighParams P) {
-  using G = F32<D, kFew>;
+template <int D, bool kFew, int kTeam>
+__global__ void __launch_bounds__(kTeam * 32) weigh_f32_kernel(const PagedWeighParams P) {
+  using G = F32<D, kFew, kTeam>;
   extern __shared__ __align__(128) uint8_t smem_bytes[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = (int)blockIdx.y;
   float* keys = reinterpret_cast<float*>(smem_bytes) + (kFew ? warp * kKeys * G::kRow : 0);
   float* qs = reinterpret_cast<float*>(smem_bytes + G::kKeyBytes + warp * G::kWarpBytes);
   float* lse2 = qs + 16 * D;
   int* slots = reinterpret_cast<int*>(lse2 + 16);
-  float* sums = reinterpret_cast<float*>(smem_bytes + G::kKeyBytes + kWarps * G::kWarpBytes);
+  float* sums = reinterpret_cast<float*>(smem_bytes + G::kKeyBytes + kTeam * G::kWarpBytes);
   int64_t* prefix = reinterpret_cast<int64_t*>(smem_bytes + G::kBytes);
   slot_prefix<G::kOwn>(P.t, P.group, prefix);
   const int64_t chunks = prefix[P.t.batch];
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) weigh_f32_kernel(const PagedWeighPar
     RA_BOUNDS(P.t.status, row >= -1 && row < (int64_t)P.t.pages * 2 * P.t.heads_kv * P.t.page_rows, 114);
     // Keys and sums of the chunk before are done with.
     if constexpr (kFew) __syncwarp(); else __syncthreads();
-    constexpr int kPieces = D / 4, kBring = kFew ? 32 : kThreads;
+    constexpr int kPieces = D / 4, kBring = kFew ? 32 : kTeam * 32;
 #pragma unroll 8
     for (int x = 0; x < kKeys * kPieces / kBring; ++x) {
       const int id = (kFew ? lane : (int)threadIdx.x) + x * kBring, i = id / kPieces, ch = id % kPieces;
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads) weigh_f32_kernel(const PagedWeighPar
       if constexpr (kFew) __syncwarp(); else __syncthreads();
       there = true;
     };
-    for (int t = tile0 + (kFew ? 0 : warp); t < tile1; t += kFew ? 1 : kWarps) {
+    for (int t = tile0 + (kFew ? 0 : warp); t < tile1; t += kFew ? 1 : kTeam) {
       const int n = min(16, rows_n - t * 16);
       __syncwarp();
       for (int id = lane; id < n * kPieces; id += 32)
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads) weigh_f32_kernel(const PagedWeighPar
         if constexpr (!kFew) {
           sum = 0.f;
 #pragma unroll
-          for (int i = 0; i < kWarps; ++i) sum += sums[i * kKeys + lane];
+          for (int i = 0; i < kTeam; ++i) sum += sums[i * kKeys + lane];
         }
         P.weight[at] = (P.weight_in != nullptr && j < rows.seq.slot0() ? P.weight_in[at] : 0.f) + sum;
       } else {
@@ -419,8 +419,8 @@ unsigned slots_of(const PagedWeighParams& prm, int sm_count, int per_sm, int own
 }
 
 template <typename Kernel>
-cudaError_t launch(Kernel kernel, std::atomic<int>* ready, const PagedWeighParams& prm, unsigned slots, int bytes,
-                   cudaStream_t stream) {
+cudaError_t launch(Kernel kernel, std::atomic<int>* ready, const PagedWeighParams& prm, unsigned slots, int threads,
+                   int bytes, cudaStream_t stream) {
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -432,31 +432,37 @@ cudaError_t launch(Kernel kernel, std::atomic<int>* ready, const PagedWeighParam
   }
   const dim3 grid(slots, (unsigned)prm.t.heads_kv);
   const int all = bytes + (prm.t.batch + 1) * 8;
-  if (prm.beside) return launch_behind(kernel, grid, kThreads, all, stream, prm);
-  kernel<<<grid, kThreads, all, stream>>>(prm);
+  if (prm.beside) return launch_behind(kernel, grid, threads, all, stream, prm);
+  kernel<<<grid, threads, all, stream>>>(prm);
   return cudaGetLastError();
 }
 template <int D>
 cudaError_t launch_bf16(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
   static std::atomic<int> ready[kMaxDevices];
-  return launch(weigh_bf16_kernel<D>, ready, prm, slots_of(prm, sm_count, 3, kWarps * kStepKeys),
+  return launch(weigh_bf16_kernel<D>, ready, prm, slots_of(prm, sm_count, 3, kWarps * kStepKeys), kThreads,
                 kWarps * kStages * (kStepKeys * D * 2 + kStepKeys * 4), stream);
 }
-template <int D, bool kFew>
+template <int D, bool kFew, int kTeam>
 cudaError_t launch_f32(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
-  using G = F32<D, kFew>;
+  using G = F32<D, kFew, kTeam>;
   static std::atomic<int> ready[kMaxDevices];
-  constexpr int kPerSm = kFew ? (D == 64 ? 4 : 2) : (D == 64 ? 8 : 4);
-  return launch(weigh_f32_kernel<D, kFew>, ready, prm, slots_of(prm, sm_count, kPerSm, G::kOwn), G::kBytes, stream);
+  constexpr int kPerSm = kTeam == 16 ? 1 : (kFew ? 4 : 8) / (D / 64);
+  return launch(weigh_f32_kernel<D, kFew, kTeam>, ready, prm, slots_of(prm, sm_count, kPerSm, G::kOwn), kTeam * 32, G::kBytes,
+                stream);
 }
 template <int D>
 cudaError_t launch_f32(const PagedWeighParams& prm, int sm_count, cudaStream_t stream) {
   // By the mean rows of a sequence and head.  16 sequences of 4k, D 128, few and not: 4 rows 54
   // and 65 us, 16 rows 102 and 132, 32 rows 170 and 158, 64 rows 310 and 231 (D 64: 26 and 47,
-  // 47 and 88, 78 and 108, 138 and 147).  400 tokens of a head over 700 slots 164 and 57: too few
-  // CTAs have work in the first form.
-  const bool few = (int64_t)prm.t.tokens * prm.group <= 32 * (int64_t)prm.t.batch;
-  return few ? launch_f32<D, true>(prm, sm_count, stream) : launch_f32<D, false>(prm, sm_count, stream);
+  // 47 and 88, 78 and 108, 138 and 147).
+  const int64_t rows = (int64_t)prm.t.tokens * prm.group;
+  if (rows <= 32 * (int64_t)prm.t.batch) return launch_f32<D, true, kWarps>(prm, sm_count, stream);
+  // Many rows and few keys: more warps of a CTA.  400 tokens of 8 heads over 700 slots of one 162 us
+  // (with 4 warps 302), 2048 tokens of one head 105 (195); but 500 tokens over 4k of 8 heads, D 64, 205
+  // (172), and 64 rows of a sequence 404 (231).
+  const int64_t ctas = (int64_t)prm.t.batch * ((prm.t.width * prm.t.page_rows + kKeys - 1) / kKeys) * prm.t.heads_kv;
+  if (rows >= 256 * (int64_t)prm.t.batch && ctas < 4 * (int64_t)sm_count) return launch_f32<D, false, 16>(prm, sm_count, stream);
+  return launch_f32<D, false, kWarps>(prm, sm_count, stream);
 }
 
 }  // namespace

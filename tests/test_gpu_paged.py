@@ -805,7 +805,8 @@ def paged_outputs():
     for n, (dtype, d, counts, lengths, hq, hk, window, sinks) in enumerate([
             ("bf16", 128, [1], [1900], 4, 1, 0, 0), ("bf16", 64, [3, 0, 33], [70, 5, 33], 6, 2, 20, 3),
             ("f32", 128, [9, 1, 1], [300, 16, 1], 3, 3, 0, 0), ("bf16", 128, [300, 1, 5], [2300, 1801, 40], 16, 2, 1500, 20),
-            ("bf16", 64, [700, 129], [700, 2000], 4, 2, 0, 0), ("f32", 64, [1, 40], [1700, 40], 4, 2, 0, 0)]):
+            ("bf16", 64, [700, 129], [700, 2000], 4, 2, 0, 0), ("f32", 64, [1, 40], [1700, 40], 4, 2, 0, 0),
+            ("f32", 128, [300], [613], 4, 1, 0, 0), ("bf16", 128, [20], [9000], 8, 1, 0, 0)]):
         t = Batch(rng, counts, lengths, hq, hk, d, dtype, 48, window=window, sinks=sinks)
         rope = ra.ra_rope_plan(d, d // 2, dtype=dtype)
         k, v = t.random(t.tokens, hk).cuda(), t.random(t.tokens, hk).cuda()
