@@ -153,7 +153,8 @@ double speed_of(const ra_rope_problem& p, int j) {
     case RA_ROPE_RAMP: {
       auto index = [&](double t) { return rot * std::log((double)p.original / (two_pi * t)) / (2.0 * std::log(p.base)); };
       const double lo = std::max(std::floor(index(p.high)), 0.0), hi = std::min(std::ceil(index(p.low)), rot - 1.0);
-      const double part = std::min(1.0, std::max(0.0, (j - lo) / (hi != lo ? hi - lo : 0.001)));
+      // (lo may lie behind hi: every pair turns more than `high` times, or none turns `low` times)
+      const double part = std::min(1.0, std::max(0.0, (j - lo) / std::max(hi - lo, 0.001)));
       return (1.0 - part) * w + part * w / p.factor;
     }
     default:
