@@ -25,21 +25,30 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const PagedAppendParam
   constexpr int kPairs = kWide ? RopeUnit<T>::kPairs : 1;
   __shared__ int32_t offsets[kKnown];
   const bool known = P.t.batch <= kKnown;
-  if (known) {
-    for (int b = threadIdx.x; b < P.t.batch; b += kThreads) offsets[b] = P.t.offset[b];
-    __syncthreads();
+  bool falls = false;  // the offsets do somewhere: they are no order to search by
+  for (int b = threadIdx.x; b < P.t.batch; b += kThreads) {
+    const int a = __ldg(P.t.offset + b);
+    falls |= __ldg(P.t.offset + b + 1) < a;
+    if (known) offsets[b] = a;
   }
+  falls = __syncthreads_or(falls);
   if (blockIdx.x == 0 && blockIdx.y == 0)  // the sequences that no token is found in are checked too
     for (int b = threadIdx.x; b < P.t.batch; b += kThreads) paged_seq(P.t, b);
   const int units = rope_units<T>(P.rope, kWide, P.d);
   const int64_t n = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (n / units >= P.t.tokens) return;
   const int token = (int)(n / units), unit = (int)(n - (int64_t)token * units);
-  // the last sequence that begins at the token or before it
   int b = 0;
-  for (int end = P.t.batch; end - b > 1;) {
-    const int mid = (b + end) >> 1;
-    ((known ? offsets[mid] : __ldg(P.t.offset + mid)) <= token ? b : end) = mid;
+  if (!falls) {  // the last sequence that begins at the token or before it
+    for (int end = P.t.batch; end - b > 1;) {
+      const int mid = (b + end) >> 1;
+      ((known ? offsets[mid] : __ldg(P.t.offset + mid)) <= token ? b : end) = mid;
+    }
+  } else {  // the first one that has the token
+    auto has = [&](int b) {
+      return __ldg(P.t.offset + b) <= token && token < __ldg(P.t.offset + b + 1) && paged_seq(P.t, b).count > 0;
+    };
+    while (b + 1 < P.t.batch && !has(b)) ++b;
   }
   const PagedSeq seq = paged_seq(P.t, b);
   const int i = token - seq.token0;

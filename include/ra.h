@@ -695,6 +695,8 @@ ra_status ra_rope_bwd(ra_rope_t rope, int64_t batch, int64_t seq, int32_t heads_
  * new tokens or beyond its page table, and page indices outside the pool are found by the
  * kernels: such sequences are left out (their rows stay as they were), the slots of such pages
  * are not written, not moved and not attended to, and ra_paged_sync_status reports them.
+ * (Offsets that fall can name a token twice: ra_paged_append writes it for the first of its
+ * sequences, and what the other calls leave for it is that of either.)
  * Entries of the page table for slots that no token of the call sees are not read.
  */
 typedef struct {
