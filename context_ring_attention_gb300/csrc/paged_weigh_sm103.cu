@@ -149,10 +149,7 @@ __device__ void copy_unseen(const PagedWeighChunkParams& P) {
       if (!paged_mine(P.t, q, P.group)) hi = 0;
       else if (q.count == 0) hi = q.length;
       else if (P.window > 0) lo = P.sinks, hi = q.slot0() - P.window + 1;
-      if (hi > P.weight_width) {
-        atomicOr(P.t.status, kPagedStatusRange);
-        hi = (int)P.weight_width;
-      }
+      hi = (int)min((int64_t)hi, P.weight_width);
     }
     for (uint32_t some = __ballot_sync(0xffffffffu, lo < hi); some; some &= some - 1) {
       const int src = __ffs(some) - 1, l = __shfl_sync(0xffffffffu, lo, src), h = __shfl_sync(0xffffffffu, hi, src);
@@ -170,10 +167,7 @@ __device__ void copy_unseen(const PagedWeighChunkParams& P) {
 
 // The weight of slot j, whose sum over the rows is known.
 __device__ __forceinline__ void put(const PagedWeighChunkParams& P, int b, int head, int j, int slot0, float sum) {
-  if (j >= P.weight_width) {
-    atomicOr(P.t.status, kPagedStatusRange);
-    return;
-  }
+  if (j >= P.weight_width) return;  // (reported, as every sequence of more slots is)
   const int64_t at = ((int64_t)b * P.t.heads_kv + head) * P.weight_width + j;
   RA_BOUNDS(P.t.status, j >= 0 && at < (int64_t)P.t.batch * P.t.heads_kv * P.weight_width, 130);
   P.weight[at] = (P.weight_in != nullptr && j < slot0 ? P.weight_in[at] : 0.f) + sum;
@@ -517,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   copy_unseen(P);
   paged_sums<kWarps>(P.t.batch, prefix, [&](int b) {
     const PagedSeq q = paged_seq(P.t, b);
-    return warp_total(paged_mine(P.t, q, P.group) ? (q.length + kPair - 1) / kPair : 0, [&](int i) { return tiles_of(P, q, per_tile, i).n; });
+    const bool mine = paged_mine(P.t, q, P.group);
+    if (mine && q.length > P.weight_width) atomicOr(P.t.status, kPagedStatusRange);
+    return warp_total(mine ? (q.length + kPair - 1) / kPair : 0, [&](int i) { return tiles_of(P, q, per_tile, i).n; });
   });
   Shares sh;
   sh.per_head = prefix[P.t.batch];

@@ -58,3 +58,23 @@ def test_appends_beside_offsets_that_fall(offset, good, many, rotated, dtype):
     assert _same_bits(t.cache, t.ref.data)
     if rotated:
         assert _same_bits(q_out, want_q)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("place", [False, True])
+@pytest.mark.parametrize("tokens,counts", [(40, [0]), (2, [0, 0]), (300, [0, 0, 0])])
+def test_weights_of_no_tokens(dtype, place, tokens, counts):
+    """Sequences without new tokens keep their weights, in place and in another tensor, and slots beyond the
+    weights are reported in both."""
+    b, n = len(counts), 90
+    t = Batch(np.random.default_rng(4), counts, [n] * b, 4, 2, 64, dtype, 16, tail=tokens)
+    q, lse = t.q.cuda(), torch.zeros((tokens, 4), device="cuda")
+    for width, fine in ((n, True), (n - 1, False)):
+        before = torch.rand((b, 2, width)).cuda()
+        weight = before.clone() if place else torch.zeros_like(before)
+        ra.ra_paged_weigh(t.kv, t.cache, q, lse, t.table, t.offset, t.length, weight, weight_in=weight if place else before)
+        if fine:
+            ra.ra_paged_sync_status(t.kv)
+        else:
+            _reported(t.kv)
+        assert _same_bits(weight, before)
