@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -123,7 +124,9 @@ ra_status validate(const ra_rope_problem* p) {
     return fail(RA_ERR_INVALID_ARG, "rotary_dim must be even, in 2..head_dim (got %d of %d)", p->rotary_dim, p->head_dim);
   if (p->interleaved != 0 && p->interleaved != 1) return fail(RA_ERR_INVALID_ARG, "interleaved must be 0 or 1");
   if (!(p->base > 1.0) || std::isinf(p->base)) return fail(RA_ERR_INVALID_ARG, "base must be finite and > 1");
-  if (!(p->amplitude >= 0.0) || std::isinf(p->amplitude)) return fail(RA_ERR_INVALID_ARG, "amplitude must be finite and >= 0");
+  // (it multiplies in float32)
+  if (p->amplitude != 0.0 && !(p->amplitude >= FLT_MIN && p->amplitude <= FLT_MAX))
+    return fail(RA_ERR_INVALID_ARG, "amplitude must be 0 or a normal float32 above 0");
   if (p->scaling < RA_ROPE_NONE || p->scaling > RA_ROPE_RAMP) return fail(RA_ERR_INVALID_ARG, "unknown scaling %d", p->scaling);
   if (p->scaling != RA_ROPE_NONE && (!(p->factor >= 1.0) || std::isinf(p->factor)))
     return fail(RA_ERR_INVALID_ARG, "factor must be finite and >= 1");

@@ -622,7 +622,7 @@ typedef struct {
   double factor;        /* >= 1 (scaling other than NONE)                       */
   int64_t original;     /* >= 1 (BANDS, RAMP)                                   */
   double low, high;     /* turns within `original` tokens, 0 < low < high (BANDS, RAMP) */
-  double amplitude;     /* A; 0 selects 1                                       */
+  double amplitude;     /* A, 2^-126 .. the largest float32; 0 selects 1        */
 } ra_rope_problem;
 
 typedef struct ra_rope_s* ra_rope_t;
@@ -632,8 +632,8 @@ typedef struct ra_rope_s* ra_rope_t;
  * handle owns a small device table and one event per stream it was used on (host-only without
  * a device, as ra_plan).  Release it with ra_rope_destroy, after the graphs that captured its
  * calls.  One host thread at a time may use a handle; its calls may overlap on the GPU.
- * Errors: RA_ERR_INVALID_ARG (null arguments, sizes, bad enum or factor), RA_ERR_UNSUPPORTED
- * (head_dim above 1024), RA_ERR_CUDA.
+ * Errors: RA_ERR_INVALID_ARG (null arguments, sizes, bad enum, factor or amplitude),
+ * RA_ERR_UNSUPPORTED (head_dim above 1024), RA_ERR_CUDA.
  */
 ra_status ra_rope_plan(const ra_rope_problem* prob, ra_rope_t* out);
 
