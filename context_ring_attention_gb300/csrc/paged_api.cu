@@ -155,9 +155,14 @@ int chunk_rounds(const ra_paged_s* kv, int64_t batch, int64_t tokens, int64_t wi
 // Which kernels a call takes.  A sequence with up to 16 query rows a head belongs to the row
 // kernels, which read its keys at the rate of HBM; one with more to the chunk kernels, whose query
 // tiles have 128 rows.  The counts are on the device: where a call may have sequences of both
-// kinds it launches both, each leaving out the other's sequences (a launch without work of its
-// own costs about 5 us).  A call whose largest sequence can have 128 rows at most (if every
-// sequence has a token) takes the row kernels alone.
+// kinds it launches both, each leaving out the other's sequences.  A batch whose largest sequence can
+// have 128 rows at most (if every sequence has a token) takes the row kernels alone, which walk a
+// sequence's keys once for 16 rows: the second kernel and its join cost 10 us, more than the walks where
+// the keys are few.  Attention and weights in us, 32 and 8 heads, D 128, row kernels alone and both:
+//   2 sequences of 20 rows over 1k 12 and 8, 23 and 13; over 8k 26 and 19, 34 and 19; over 32k 86 and 53, 77 and 41;
+//   2 of 64 rows over 1k 18 and 13, 24 and 14; over 8k 36 and 36, 35 and 20; over 32k 162 and 108, 77 and 45;
+//   5 of 20 rows over 1k 18 and 10, 27 and 14; over 8k 45 and 35, 61 and 30; over 32k 199 and 121, 140 and 80.
+// The rule does not see the keys' number, and is the wrong one over long prefixes.
 struct Route {
   bool rows, chunks;
 };

@@ -131,7 +131,9 @@ struct Shares {
 // CTAs of this kernel's, where the row kernel reads other sequences' keys beside it: the two then
 // end together.  A key tile takes a CTA 1.4 us, beside the reads 1.7; the reads take the time of their bytes at 6.6 TB/s
 // if five eighths of the SMs are left to them, and longer in proportion if fewer are.  (One chunk of
-// 512 tokens and 31 single ones under a window of 8192: one kernel after the other 226 us.)
+// 512 tokens and 31 single ones under a window of 8192: one kernel after the other 226 us.  With 1.7,
+// 1.2, 0.85 and 0.6 us a tile: 512 tokens, D 128, 186, 211, 261 and 345 us; D 64, whose tiles are half as long,
+// 119, 119, 118 and 155; 64 tokens, one query tile an item: D 128 176, 204, 243 and 282, D 64 100, 98, 117 and 142.)
 __device__ __forceinline__ int ctas_beside(int64_t units, double bytes, int sms) {
   const float work = 1.7f * (float)units, reads = (float)(bytes / 6.6e6);  // us
   const float few = 0.375f * (float)sms, need = 0.625f * (float)sms;

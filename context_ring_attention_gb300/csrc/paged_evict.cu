@@ -14,9 +14,9 @@
 // step ahead.  Where each row lies is looked up for many rows at once, before their turn.
 //
 // Measured (8 heads, D 128, bf16): 16 sequences of 4352 slots to 4096 (543 MB) into other pages 107
-// us, in place 108; the choice alone takes 15.  33001 slots to 8192 (69 MB) into other pages 33 us,
-// of which the choice 20: bound by the latency of its three passes, barriers and the scan (one CTA a
-// head: 51); in place 41.
+// us, in place 108; the choice alone takes 15.  33001 slots to 8192 (69 MB) into other pages 31 to 33
+// us, of which the choice 20: bound by the latency of its three passes, barriers and the scan; in place
+// 35 to 41.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -33,6 +33,8 @@ namespace cg = cooperative_groups;
 constexpr int kPickThreads = 1024;
 constexpr int kBins = 2048;       // 11 bits a pass
 constexpr int kMaxKnown = 49152;  // weights that a CTA keeps in shared memory
+// 33001 slots of 8 heads to 8192 with clusters of up to 1, 2, 4 and 8 CTAs a head 43, 34, 31 and 31 us, to
+// 32768 103, 81, 71 and 68; 100000 to 8192 403, 202, 42 and 37.
 constexpr int kMaxCluster = 4;
 
 // Whole numbers in the order of the weights: NaN lowest, then -inf .. +inf, -0 as +0.

@@ -13,6 +13,10 @@
 // (cp.async, 16 bytes a lane, rows swizzled for ldmatrix); rows that no query sees arrive as
 // zeros, so that what a page holds there does not matter.  The warps' sums are joined in shared
 // memory, the parts of an item that several CTAs share by a second kernel, both in a fixed order.
+// The weights are rounded to bf16 for the second product, whose operands are bf16; O is divided by
+// the sum of the exact ones.  (The chunk kernel, whose running maximum may be stale, corrects that sum by the
+// rounding of each tile's largest weight; here the largest weight of a warp's keys is 1
+// but for float32's rounding, which bf16 has.)  The exponentials are ex2.approx, off by 2^-22: nothing beside 2^-8.
 //
 // Measured (32 query and 8 key/value heads, D 128, bf16): one token of 16 sequences up to 32k
 // (1.27 GB) 190 us, 6.7 TB/s; one token over 1M 598 us, 7.2 TB/s.  float32 has no such instruction

@@ -6,9 +6,10 @@
 // the gradient goes back through the same with -sin.  Bound by HBM: every row is read and
 // written once.  A thread has the pairs of two 16-byte vectors of one position, computes their
 // angles once and takes the heads in turn, so that the angles cost nothing next to the rows.
-// Speeds are 64-bit fractions of a turn, so that an angle is exact to 2^-33 of a turn at any
-// position without 64-bit floating point (rope_internal.h).  Measured: 32768 positions of 32 and
-// 8 heads, d 128, strided queries and keys (671 MB) 106 us, 6.3 TB/s.
+// Speeds are 64-bit fractions of a turn, so that position times speed is brought within a turn,
+// to 2^-33 of it at any position, without 64-bit floating point; the speed's own error is that of
+// float64 (rope_internal.h).  Measured: 32768 positions of 32 and 8 heads, d 128, strided queries
+// and keys (671 MB) 106 us, 6.3 TB/s.
 //
 // Rows whose rotated part, length, address or strides do not divide into 16-byte vectors take
 // a thread per pair.

@@ -24,7 +24,9 @@ struct ra_rope_s {
 namespace ra {
 
 // Speeds as fractions of a full turn per position, in units of 2^-64 turns: position * speed,
-// wrapped to 64 bits, is the angle's fraction of a turn without error for any position.
+// wrapped to 64 bits, is that speed's angle within a turn without error for any position.  The
+// speeds are computed in float64, a few 2^-53 of themselves off, and so are the angles: 2^-24 of a
+// turn for the fastest pair at position 2^31, 2^-33 at 2^22.
 struct RopeTable {
   const uint64_t* speed;
   float amplitude;

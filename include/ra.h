@@ -601,8 +601,9 @@ ra_status ra_kv4_sync_status(ra_kv4_t kv, void* stream);
  *   RAMP    (1 - t_j) w_j + t_j w_j / factor, t_j = (j - j0) / (j1 - j0) held to 0..1, where j0 =
  *           max(floor(i(high)), 0), j1 = min(ceil(i(low)), rotary_dim - 1), j1 - j0 at least 0.001,
  *           and i(r) = rotary_dim * ln(original / 2 pi r) / (2 ln base).
- * Angles are taken modulo a turn exactly (64-bit fractions of a turn), products and sums in
- * float32, one rounding to the dtype.
+ * Speeds are float64, a few 2^-53 of themselves off; position * speed is taken modulo a turn in
+ * integers (64-bit fractions of a turn) and cut to 2^-33 of it; products and sums are float32, with
+ * one rounding to the dtype.
  */
 typedef enum {
   RA_ROPE_NONE = 0,
@@ -756,7 +757,12 @@ ra_status ra_paged_append(ra_paged_t kv, ra_rope_t rope, void* cache, int64_t ba
  * whose slots lie in pages out of range gets O = 0, LSE = -inf.
  * Slots that no token of the call sees may hold anything.  Values that some of them see must be
  * finite: they enter the products of the others with weight zero.
- * bf16: the softmax weights are rounded to bf16 for the second product; sums are fp32.
+ * bf16: the softmax weights are rounded to bf16 for the second product; sums are fp32.  A chunk's
+ * O is divided by the sum with the largest weight of every 128 slots as rounded, so that where one
+ * slot has nearly all the weight its rounding cancels; the LSE is that of the exact sum.
+ * bf16 chunks of calls of more than 2048 sequences, of tables of more than 2^25 slots
+ * (table_width * page_rows) or of more than 128 query heads a key/value head are read 16 query rows at a
+ * time, as float32 is, which takes them several times as long.
  * scratch: ra_paged_attend_scratch_size bytes (NULL when that is 0), not shared by calls that
  * may overlap.  o may not overlap an input.
  * Device pointers, 16-byte aligned (page_table, offset, length, lse: 4-byte).  Asynchronous on
